@@ -315,7 +315,7 @@ def _plain_tables(s):
     of = table[owner, (at // page).clamp(0, table.shape[1] - 1)]
     slots = torch.where(live, of * page + at % page, -1)
     counts = torch.where(served, held + need, held)
-    left = free - torch.where(served, upto, 0).amax()
+    left = free - torch.where(served & (need > 0), upto, 0).amax()
     return [table] + [x.to(torch.int32) for x in (starts, slots, counts, left)]
 
 
@@ -399,7 +399,7 @@ def _exact_tables(s):
             table[b][held + j] = s["stack"][free - 1 - (asked - need + j)] if served else -1
         counts.append(held + need if served else held)
         if served:
-            taken = max(taken, asked)
+            taken = asked if need else taken
             for i in range(n):
                 slots[begin + i] = table[b][(past + i) // page] * page + (past + i) % page
     return [torch.tensor(x, dtype=torch.int32, device="cuda") for x in (table, starts, slots, counts, [free - taken])]
