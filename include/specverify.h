@@ -62,7 +62,8 @@ typedef enum sv_status {
     SV_ERR_UNSUPPORTED = 3,  /* host: shape outside the kernels' range (see each call)    */
     SV_ERR_CUDA = 4,         /* host: a CUDA runtime call or launch failed                 */
     SV_ERR_TIMEOUT = 5,      /* device: a bounded wait inside a kernel gave up             */
-    SV_ERR_BAD_INPUT = 6     /* device: invalid per-sequence data (see conventions)       */
+    SV_ERR_BAD_INPUT = 6,    /* device: invalid per-sequence data (see conventions)       */
+    SV_ERR_NO_PAGES = 7      /* device: the pool has too few free pages for the sequence  */
 } sv_status;
 
 typedef enum sv_dtype { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
@@ -304,6 +305,104 @@ sv_status sv_compact_kv_paged(void *k_pages, void *v_pages, const int32_t *block
                               const int32_t *path_nodes, int path_stride,
                               const int32_t *accepted_len, int B, int Hkv, int D,
                               int32_t *seq_status, sv_stream_t stream);
+
+/*
+ * Page tables and slot maps of a paged KV cache, from request lengths.
+ * Source: the paged KV of "Chapitre 9", section "Ce que prépare le Chapitre
+ * 9"; "Chapitre 9" §9.1 (a step appends its candidates' rows to the cache).
+ *
+ * Sequence b holds page_counts[b] pages (the first entries of its table row)
+ * and its first prefix_lens[b] slots are filled; new_lens[b] rows are to be
+ * appended.  Free pages are a stack: free_pages[0 .. free_count).  With
+ * pages(x) = ceil(x / page_size):
+ *   valid_b: 0 <= prefix, 0 <= new, prefix + new <= max_pages * page_size,
+ *            pages(prefix) <= held <= max_pages, and b's rows end at or
+ *            before num_rows
+ *   need_b  = max(0, pages(prefix + new) - held) if valid, else 0
+ *   C_b     = need_0 + .. + need_b
+ *   served_b: valid, and need_b = 0 or C_b <= free_count (in sequence order;
+ *             a sequence that does not fit is not overtaken)
+ *   block_table[b, held + j] = free_pages[free_count - 1 - (C_{b-1} + j)], or
+ *            -1 where a valid sequence is not served, for j < need_b; other
+ *            entries are left as they are
+ *   row_starts[b] = max(0, new_0) + .. + max(0, new_{b-1}), b = 0..B (at most INT32_MAX)
+ *   slot_map[row_starts[b] + i] = p * page_size + (prefix + i) % page_size,
+ *            p = block_table[b, (prefix + i) / page_size]; -1 for the rows of a
+ *            sequence that is not served, on a page id outside [0, num_pages),
+ *            and for the rows from row_starts[B] on
+ *   new_page_counts[b] = held + need_b if served, else held
+ *   new_free_count  = free_count - C_b of the last served b with need_b > 0
+ *   seq_status[b] = SV_OK; SV_ERR_NO_PAGES (valid, not served);
+ *            SV_ERR_BAD_INPUT (not valid, a page id out of range among the
+ *            pages its new rows fall into, or free_count outside
+ *            [0, num_pages], in which case no sequence gets a page)
+ *
+ *   prefix_lens, new_lens, page_counts int32 [B]; free_pages int32 [num_pages];
+ *   free_count, new_free_count int32 [1]; block_table int32 [B, max_pages];
+ *   row_starts int32 [B + 1]; slot_map int32 [num_rows]; new_page_counts
+ *   int32 [B]; seq_status int32 [B] or NULL.  No output may alias an input.
+ * Supported: B <= 4096, max_pages * page_size < 2^30, B * max_pages < 2^31,
+ * num_pages * page_size < 2^31, num_rows < 2^30.
+ */
+sv_status sv_build_block_tables(const int32_t *prefix_lens, const int32_t *new_lens,
+                                const int32_t *page_counts, const int32_t *free_pages,
+                                const int32_t *free_count, int B, int page_size, int max_pages,
+                                int num_pages, int num_rows, int32_t *block_table,
+                                int32_t *row_starts, int32_t *slot_map, int32_t *new_page_counts,
+                                int32_t *new_free_count, int32_t *seq_status, sv_stream_t stream);
+
+/*
+ * Pages given back to the pool when sequences shrink (rejected candidates) or
+ * end (keep_lens[b] = 0).
+ * Source: "Parallel Decoding" glossary, "Limites du parallel decoding" (the
+ * cache is enlarged for the branches); "Chapitre 9" §9.1 (the accepted prefix
+ * is kept and the rest discarded).
+ *
+ *   back_b = page_counts[b] - pages(keep_lens[b]); R_b = back_0 + .. + back_b
+ *   free_pages[free_count + R_{b-1} + j] = block_table[b, pages(keep) + j], j < back_b
+ *   new_page_counts[b] = pages(keep_lens[b]); new_free_count = free_count + R_b
+ *            of the last sequence served
+ * A sequence with keep_lens < 0, page_counts > max_pages or fewer pages than it
+ * is to keep gives nothing back (back_b = 0), and neither does one whose pages
+ * the stack has no room for (free_count + R_b > num_pages: some page is held
+ * twice) nor, when free_count is outside [0, num_pages], any: seq_status[b] =
+ * SV_ERR_BAD_INPUT, its count unchanged.  The table's entries stay as they are.
+ *
+ *   Arrays as sv_build_block_tables; keep_lens int32 [B]; free_pages is
+ *   written in place.  No other output may alias an input.
+ * Supported: as sv_build_block_tables.
+ */
+sv_status sv_release_pages(const int32_t *keep_lens, const int32_t *page_counts,
+                           const int32_t *block_table, int32_t *free_pages,
+                           const int32_t *free_count, int B, int page_size, int max_pages,
+                           int num_pages, int32_t *new_page_counts, int32_t *new_free_count,
+                           int32_t *seq_status, sv_stream_t stream);
+
+/*
+ * New K/V rows written to a paged cache through a slot map.
+ * Source: as sv_build_block_tables.
+ *
+ *   k_pages[s / page_size, h, s % page_size, :] = k_new[r, h, :] with
+ *   s = slot_map[r], for every row r and KV head h; v likewise.  Rows of
+ *   dtype SV_F32 are rounded to the nearest bf16 (ties to even).
+ * A row with s = -1 is padding and skipped; one with s outside
+ * [-1, num_pages * page_size) is skipped and row_status[r] = SV_ERR_BAD_INPUT.
+ * Two rows must not name one slot (sv_build_block_tables names none twice
+ * unless a page is in two tables).
+ *
+ *   k_new, v_new  `dtype` [num_rows, Hkv, D], rows k_stride / v_stride
+ *                 elements apart (>= Hkv * D, a multiple of 16 bytes: parts
+ *                 of a fused projection's rows)
+ *   slot_map      int32 [num_rows]; row_status int32 [num_rows] or NULL
+ *   k_pages, v_pages  bf16 [num_pages, Hkv, page_size, D]
+ * Supported: D % 8 == 0, D <= 256, num_pages * Hkv * page_size < 2^31,
+ * num_rows < 2^30.
+ */
+sv_status sv_append_kv_paged(const void *k_new, const void *v_new, sv_dtype dtype,
+                             long long k_stride, long long v_stride, const int32_t *slot_map,
+                             int num_rows, int Hkv, int D, int page_size, int num_pages,
+                             void *k_pages, void *v_pages, int32_t *row_status,
+                             sv_stream_t stream);
 
 /*
  * The fused verification step on a chain: sv_tree_attention with the causal

@@ -23,6 +23,7 @@ SV_ERR_UNSUPPORTED = 3
 SV_ERR_CUDA = 4
 SV_ERR_TIMEOUT = 5
 SV_ERR_BAD_INPUT = 6
+SV_ERR_NO_PAGES = 7
 
 SV_F32 = 0
 SV_BF16 = 1
@@ -37,7 +38,8 @@ SV_OP_VERIFY_STEP_TREE_GREEDY = 5
 EXPORTS = ("sv_workspace_size", "sv_tree_attention", "sv_verify_chain", "sv_verify_tree_greedy",
            "sv_compact_kv", "sv_status_string", "sv_version", "sv_verify_chain_noalloc",
            "sv_tree_attention_paged", "sv_compact_kv_paged", "sv_verify_tree_stochastic",
-           "sv_verify_step_chain", "sv_verify_step_tree_greedy")
+           "sv_verify_step_chain", "sv_verify_step_tree_greedy", "sv_build_block_tables",
+           "sv_release_pages", "sv_append_kv_paged")
 
 # Length of the fixed scratch array behind sv_verify_chain_noalloc.
 SV_NOALLOC_SCRATCH_BYTES = 4 << 20
@@ -94,7 +96,12 @@ def load(path: str) -> ctypes.CDLL:
                                        I, P, P, P, P, P, P, Z, P]
     L.sv_verify_step_tree_greedy.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, F, P, P, P, I, P,
                                              I, P, P, P, P, P, P, Z, P]
-    for fn in ("sv_tree_attention", "sv_verify_chain", "sv_verify_tree_greedy", "sv_compact_kv",
+    Q = ctypes.c_longlong
+    L.sv_build_block_tables.argtypes = [P, P, P, P, P, I, I, I, I, I, P, P, P, P, P, P, P]
+    L.sv_release_pages.argtypes = [P, P, P, P, P, I, I, I, I, P, P, P, P]
+    L.sv_append_kv_paged.argtypes = [P, P, I, Q, Q, P, I, I, I, I, I, P, P, P, P]
+    for fn in ("sv_build_block_tables", "sv_release_pages", "sv_append_kv_paged",
+               "sv_tree_attention", "sv_verify_chain", "sv_verify_tree_greedy", "sv_compact_kv",
                "sv_verify_chain_noalloc", "sv_tree_attention_paged", "sv_compact_kv_paged",
                "sv_verify_tree_stochastic", "sv_verify_step_chain", "sv_verify_step_tree_greedy"):
         getattr(L, fn).restype = I
@@ -534,6 +541,183 @@ def sv_compact_kv_paged(k_pages, v_pages, block_table, prefix_lens, accepted_len
                                    _stream(stream))
     _check("sv_compact_kv_paged", rc)
     return new_kv_lens
+
+
+class _Launch:
+    """The device and stream of one call: every tensor on the first one's
+    device, that device current while the call allocates and launches, its
+    current stream (or the given one) the launch stream, on which outputs the
+    call allocates are first used."""
+
+    def __init__(self, device, stream):
+        self.device, self.given = device, stream
+        self.contexts = ()
+        if device.type == "cuda":
+            if device.index != torch.cuda.current_device():
+                self.contexts += (torch.cuda.device(device),)
+            if stream is not None:
+                self.contexts += (torch.cuda.stream(stream),)
+
+    def __enter__(self):
+        for c in self.contexts:
+            c.__enter__()
+        s = torch.cuda.current_stream(self.device) if self.given is None else self.given
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
+
+
+def _arr(t, name, dtype, shape, device):
+    """A contiguous array of the call's sizes on the call's device; its pointer."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device or not _on_device(t) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor on {device}")
+    return t.data_ptr()
+
+
+def _opt_arr(t, name, dtype, shape, device):
+    return None if t is None else _arr(t, name, dtype, shape, device)
+
+
+def _rows(t, name, heads, device):
+    """Rows [num_rows, heads, D] that may lie apart (parts of a wider row): the
+    pointer and the elements between rows."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a tensor of 3 dims")
+    n, h, d = t.shape
+    if heads is not None and h != heads:
+        raise ValueError(f"{name} must have {heads} heads, got {h}")
+    sr, sh, sd = t.stride()
+    if n == 1:
+        sr = h * d  # the stride of a dimension of one says nothing
+    if (t.device != device or not _on_device(t) or (d > 1 and sd != 1) or (h > 1 and sh != d)
+            or sr < h * d):
+        raise ValueError(f"{name} must be a CUDA tensor on {device} with its last two dims dense")
+    return t.data_ptr(), sr
+
+
+def _need_int(v, name):
+    if isinstance(v, bool) or not isinstance(v, int):
+        raise TypeError(f"{name} must be an int, got {type(v).__name__}")
+    return v
+
+
+def sv_build_block_tables(prefix_lens, new_lens, page_counts, block_table, free_pages, free_count,
+                          page_size, num_rows, row_starts=None, slot_map=None,
+                          new_page_counts=None, new_free_count=None, seq_status=None, stream=None):
+    """prefix_lens, new_lens, page_counts [B] int32; block_table [B,max_pages]
+    int32 (the new pages' entries written in place); free_pages [num_pages]
+    int32, free_count [1] int32 (a stack); num_rows: rows of the packed batch.
+    Returns (row_starts [B+1], slot_map [num_rows], new_page_counts [B],
+    new_free_count [1]), int32."""
+    i32 = torch.int32
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a tensor of 2 dims")
+    dev = block_table.device
+    B, max_pages = block_table.shape
+    _need_int(page_size, "page_size")
+    _need_int(num_rows, "num_rows")
+    if num_rows <= 0:
+        raise ValueError(f"num_rows must be positive, got {num_rows}")
+    if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
+        raise ValueError("free_pages must be a tensor of 1 dim")
+    num_pages = free_pages.shape[0]
+    p_tab = _arr(block_table, "block_table", i32, (B, max_pages), dev)
+    p_pre = _arr(prefix_lens, "prefix_lens", i32, (B,), dev)
+    p_new = _arr(new_lens, "new_lens", i32, (B,), dev)
+    p_cnt = _arr(page_counts, "page_counts", i32, (B,), dev)
+    p_stk = _arr(free_pages, "free_pages", i32, (num_pages,), dev)
+    p_fc = _arr(free_count, "free_count", i32, (1,), dev)
+    p_st = _opt_arr(seq_status, "seq_status", i32, (B,), dev)
+    with _Launch(dev, stream) as s:
+        if row_starts is None:
+            row_starts = torch.empty(B + 1, dtype=i32, device=dev)
+        if slot_map is None:
+            slot_map = torch.empty(num_rows, dtype=i32, device=dev)
+        if new_page_counts is None:
+            new_page_counts = torch.empty(B, dtype=i32, device=dev)
+        if new_free_count is None:
+            new_free_count = torch.empty(1, dtype=i32, device=dev)
+        rc = lib().sv_build_block_tables(
+            p_pre, p_new, p_cnt, p_stk, p_fc, B, page_size, max_pages, num_pages, num_rows, p_tab,
+            _arr(row_starts, "row_starts", i32, (B + 1,), dev),
+            _arr(slot_map, "slot_map", i32, (num_rows,), dev),
+            _arr(new_page_counts, "new_page_counts", i32, (B,), dev),
+            _arr(new_free_count, "new_free_count", i32, (1,), dev), p_st, s)
+    _check("sv_build_block_tables", rc)
+    return row_starts, slot_map, new_page_counts, new_free_count
+
+
+def sv_release_pages(keep_lens, page_counts, block_table, free_pages, free_count, page_size,
+                     new_page_counts=None, new_free_count=None, seq_status=None, stream=None):
+    """keep_lens, page_counts [B] int32; block_table [B,max_pages] int32;
+    free_pages [num_pages] int32 (the pages given back written in place),
+    free_count [1] int32.  Returns (new_page_counts [B], new_free_count [1]), int32."""
+    i32 = torch.int32
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a tensor of 2 dims")
+    dev = block_table.device
+    B, max_pages = block_table.shape
+    _need_int(page_size, "page_size")
+    if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
+        raise ValueError("free_pages must be a tensor of 1 dim")
+    num_pages = free_pages.shape[0]
+    p_tab = _arr(block_table, "block_table", i32, (B, max_pages), dev)
+    p_keep = _arr(keep_lens, "keep_lens", i32, (B,), dev)
+    p_cnt = _arr(page_counts, "page_counts", i32, (B,), dev)
+    p_stk = _arr(free_pages, "free_pages", i32, (num_pages,), dev)
+    p_fc = _arr(free_count, "free_count", i32, (1,), dev)
+    p_st = _opt_arr(seq_status, "seq_status", i32, (B,), dev)
+    with _Launch(dev, stream) as s:
+        if new_page_counts is None:
+            new_page_counts = torch.empty(B, dtype=i32, device=dev)
+        if new_free_count is None:
+            new_free_count = torch.empty(1, dtype=i32, device=dev)
+        rc = lib().sv_release_pages(
+            p_keep, p_cnt, p_tab, p_stk, p_fc, B, page_size, max_pages, num_pages,
+            _arr(new_page_counts, "new_page_counts", i32, (B,), dev),
+            _arr(new_free_count, "new_free_count", i32, (1,), dev), p_st, s)
+    _check("sv_release_pages", rc)
+    return new_page_counts, new_free_count
+
+
+def _pages(k_pages, v_pages):
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+        raise ValueError("k_pages must be a tensor of 4 dims")
+    dev = k_pages.device
+    return (_arr(k_pages, "k_pages", torch.bfloat16, k_pages.shape, dev),
+            _arr(v_pages, "v_pages", torch.bfloat16, k_pages.shape, dev), dev)
+
+
+def sv_append_kv_paged(k_new, v_new, slot_map, k_pages, v_pages, row_status=None, stream=None):
+    """k_new, v_new [num_rows,Hkv,D] bf16 or f32 (rows may lie apart: parts of a
+    fused projection); slot_map [num_rows] int32 (-1: padding).  Writes the
+    rows into k_pages/v_pages [num_pages,Hkv,page_size,D] bf16, in place."""
+    p_k, p_v, dev = _pages(k_pages, v_pages)
+    num_pages, Hkv, page_size, D = k_pages.shape
+    p_kn, k_stride = _rows(k_new, "k_new", Hkv, dev)
+    p_vn, v_stride = _rows(v_new, "v_new", Hkv, dev)
+    num_rows = k_new.shape[0]
+    if k_new.shape[2] != D or v_new.shape != k_new.shape:
+        raise ValueError(f"k_new and v_new must have shape [num_rows, {Hkv}, {D}]")
+    if k_new.dtype != v_new.dtype:
+        raise TypeError("k_new and v_new must have one dtype")
+    if k_new.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"k_new must be bfloat16 or float32, got {k_new.dtype}")
+    dt = SV_BF16 if k_new.dtype == torch.bfloat16 else SV_F32
+    p_slot = _arr(slot_map, "slot_map", torch.int32, (num_rows,), dev)
+    p_st = _opt_arr(row_status, "row_status", torch.int32, (num_rows,), dev)
+    with _Launch(dev, stream) as s:
+        rc = lib().sv_append_kv_paged(p_kn, p_vn, dt, k_stride, v_stride, p_slot, num_rows, Hkv, D,
+                                      page_size, num_pages, p_k, p_v, p_st, s)
+    _check("sv_append_kv_paged", rc)
 
 
 def sv_verify_chain_noalloc(target_logits, draft_logits, draft_tokens, u_accept, u_sample,

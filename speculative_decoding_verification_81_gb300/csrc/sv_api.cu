@@ -27,6 +27,7 @@ const char *sv_status_string(sv_status s) {
         case SV_ERR_CUDA: return "SV_ERR_CUDA: a CUDA runtime call failed";
         case SV_ERR_TIMEOUT: return "SV_ERR_TIMEOUT: a bounded wait in a kernel gave up";
         case SV_ERR_BAD_INPUT: return "SV_ERR_BAD_INPUT: invalid per-sequence input";
+        case SV_ERR_NO_PAGES: return "SV_ERR_NO_PAGES: too few free pages";
     }
     return "unknown sv_status";
 }
@@ -227,6 +228,72 @@ sv_status sv_compact_kv_paged(void *k_pages, void *v_pages, const int32_t *block
                       page_size};
     a.num_pages = num_pages;
     return sv::launch_compact_kv(a, as_stream(stream));
+}
+
+static bool page_tables_ok(int B, int page_size, int max_pages, int num_pages) {
+    return B <= 4096 && (long long)max_pages * page_size < (1LL << 30) &&
+           (long long)B * max_pages < (1LL << 31) && (long long)num_pages * page_size < (1LL << 31);
+}
+
+sv_status sv_build_block_tables(const int32_t *prefix_lens, const int32_t *new_lens,
+                                const int32_t *page_counts, const int32_t *free_pages,
+                                const int32_t *free_count, int B, int page_size, int max_pages,
+                                int num_pages, int num_rows, int32_t *block_table,
+                                int32_t *row_starts, int32_t *slot_map, int32_t *new_page_counts,
+                                int32_t *new_free_count, int32_t *seq_status, sv_stream_t stream) {
+    if (!prefix_lens || !new_lens || !page_counts || !free_pages || !free_count || !block_table ||
+        !row_starts || !slot_map || !new_page_counts || !new_free_count)
+        return SV_ERR_INVALID_ARG;
+    if (B <= 0 || page_size <= 0 || max_pages <= 0 || num_pages <= 0 || num_rows <= 0)
+        return SV_ERR_INVALID_ARG;
+    // the CTAs read the old counts while one of them writes the new ones
+    if (new_page_counts == page_counts || new_free_count == free_count) return SV_ERR_INVALID_ARG;
+    if (!page_tables_ok(B, page_size, max_pages, num_pages) || num_rows >= (1 << 30))
+        return SV_ERR_UNSUPPORTED;
+    sv::BuildTablesArgs a{prefix_lens, new_lens,    page_counts, free_pages,      free_count,
+                          B,           page_size,   max_pages,   num_pages,       num_rows,
+                          block_table, row_starts,  slot_map,    new_page_counts, new_free_count,
+                          seq_status};
+    return sv::launch_build_tables(a, as_stream(stream));
+}
+
+sv_status sv_release_pages(const int32_t *keep_lens, const int32_t *page_counts,
+                           const int32_t *block_table, int32_t *free_pages,
+                           const int32_t *free_count, int B, int page_size, int max_pages,
+                           int num_pages, int32_t *new_page_counts, int32_t *new_free_count,
+                           int32_t *seq_status, sv_stream_t stream) {
+    if (!keep_lens || !page_counts || !block_table || !free_pages || !free_count ||
+        !new_page_counts || !new_free_count)
+        return SV_ERR_INVALID_ARG;
+    if (B <= 0 || page_size <= 0 || max_pages <= 0 || num_pages <= 0) return SV_ERR_INVALID_ARG;
+    if (new_page_counts == page_counts || new_free_count == free_count) return SV_ERR_INVALID_ARG;
+    if (!page_tables_ok(B, page_size, max_pages, num_pages)) return SV_ERR_UNSUPPORTED;
+    sv::ReleasePagesArgs a{keep_lens, page_counts, block_table, free_pages,
+                           free_count, B,          page_size,   max_pages,
+                           num_pages, new_page_counts, new_free_count, seq_status};
+    return sv::launch_release_pages(a, as_stream(stream));
+}
+
+sv_status sv_append_kv_paged(const void *k_new, const void *v_new, sv_dtype dtype,
+                             long long k_stride, long long v_stride, const int32_t *slot_map,
+                             int num_rows, int Hkv, int D, int page_size, int num_pages,
+                             void *k_pages, void *v_pages, int32_t *row_status,
+                             sv_stream_t stream) {
+    if (!k_new || !v_new || !slot_map || !k_pages || !v_pages) return SV_ERR_INVALID_ARG;
+    if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_INVALID_ARG;
+    if (num_rows <= 0 || Hkv <= 0 || D <= 0 || page_size <= 0 || num_pages <= 0)
+        return SV_ERR_INVALID_ARG;
+    if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pages) || !aligned16(v_pages))
+        return SV_ERR_INVALID_ARG;
+    const long long per16 = dtype == SV_F32 ? 4 : 8, row = (long long)Hkv * D;
+    if (k_stride < row || v_stride < row || k_stride % per16 != 0 || v_stride % per16 != 0)
+        return SV_ERR_INVALID_ARG;
+    if (D % 8 != 0 || D > 256 || num_rows >= (1 << 30) ||
+        (long long)num_pages * Hkv * page_size >= (1LL << 31))
+        return SV_ERR_UNSUPPORTED;
+    sv::AppendArgs a{k_new, v_new, k_stride,  v_stride,  slot_map, num_rows,
+                     Hkv,   D,     page_size, num_pages, k_pages,  v_pages, row_status};
+    return sv::launch_append_kv(a, dtype, as_stream(stream));
 }
 
 }  // extern "C"

@@ -221,6 +221,51 @@ sv_status launch_compact_kv(const CompactArgs &args, cudaStream_t stream);
 
 int device_sm_count();
 
+// ---------------------------------------------------------------- paged cache bookkeeping (sv_pages.cu)
+
+struct BuildTablesArgs {
+    const int32_t *prefix_lens;
+    const int32_t *new_lens;
+    const int32_t *page_counts;
+    const int32_t *free_pages;
+    const int32_t *free_count;
+    int B, page_size, max_pages, num_pages, num_rows;
+    int32_t *block_table;
+    int32_t *row_starts;
+    int32_t *slot_map;
+    int32_t *new_page_counts;
+    int32_t *new_free_count;
+    int32_t *seq_status;
+};
+
+struct ReleasePagesArgs {
+    const int32_t *keep_lens;
+    const int32_t *page_counts;
+    const int32_t *block_table;
+    int32_t *free_pages;
+    const int32_t *free_count;
+    int B, page_size, max_pages, num_pages;
+    int32_t *new_page_counts;
+    int32_t *new_free_count;
+    int32_t *seq_status;
+};
+
+struct AppendArgs {
+    const void *k_new;
+    const void *v_new;
+    long long k_stride, v_stride;  // elements between rows
+    const int32_t *slot_map;
+    int num_rows, Hkv, D, page_size, num_pages;
+    void *k_pages;
+    void *v_pages;
+    int32_t *row_status;
+    int rows_per_cta;  // set at launch
+};
+
+sv_status launch_build_tables(const BuildTablesArgs &args, cudaStream_t stream);
+sv_status launch_release_pages(const ReleasePagesArgs &args, cudaStream_t stream);
+sv_status launch_append_kv(const AppendArgs &args, int dtype, cudaStream_t stream);
+
 // Workspace of a fused step: attention, vocabulary pass, then (trees) the
 // compaction counters, each 256-byte aligned; 0 if the attention shape is unsupported.
 size_t step_workspace_size(bool chain, int B, int T_or_N, int V, int dtype, int Hq, int Hkv,

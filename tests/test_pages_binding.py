@@ -1,0 +1,202 @@
+"""The page-table, page-release and row-append calls without a GPU: what the
+library refuses on the host, and what the binding refuses before it calls it."""
+import ctypes
+import types
+
+import pytest
+import torch
+
+import speculative_decoding_verification_81_gb300 as sv
+from speculative_decoding_verification_81_gb300 import api
+from speculative_decoding_verification_81_gb300 import build as svbuild
+
+FAKE, OTHER = ctypes.c_void_p(0x10000), ctypes.c_void_p(0x20000)  # never dereferenced
+MISALIGNED = ctypes.c_void_p(0x10004)
+STREAM = types.SimpleNamespace(cuda_stream=0)
+
+
+@pytest.fixture(scope="module")
+def L():
+    svbuild.build()
+    return sv.lib()
+
+
+def test_build_block_tables_host_validation(L):
+    def call(**kw):
+        a = dict(pre=FAKE, new=FAKE, cnt=FAKE, stk=FAKE, fc=FAKE, B=2, ps=0, mp=8, np=64, rows=20,
+                 tab=FAKE, rs=FAKE, sm=FAKE, nc=OTHER, nf=OTHER)
+        a.update(kw)
+        return L.sv_build_block_tables(a["pre"], a["new"], a["cnt"], a["stk"], a["fc"], a["B"], a["ps"],
+                                       a["mp"], a["np"], a["rows"], a["tab"], a["rs"], a["sm"], a["nc"],
+                                       a["nf"], None, None)
+    for name in ("pre", "new", "cnt", "stk", "fc", "tab", "rs", "sm", "nc", "nf"):
+        assert call(ps=16, **{name: None}) == sv.SV_ERR_INVALID_ARG, name
+    assert call() == sv.SV_ERR_INVALID_ARG                      # page_size 0
+    for name in ("B", "mp", "np", "rows"):
+        assert call(ps=16, **{name: 0}) == sv.SV_ERR_INVALID_ARG, name
+    assert call(ps=16, nc=FAKE) == sv.SV_ERR_INVALID_ARG        # new counts over the old ones
+    assert call(ps=16, nf=FAKE) == sv.SV_ERR_INVALID_ARG
+    assert call(ps=16, B=4097) == sv.SV_ERR_UNSUPPORTED
+    assert call(ps=1 << 28) == sv.SV_ERR_UNSUPPORTED            # max_pages * page_size
+    assert call(ps=1 << 20, np=1 << 12) == sv.SV_ERR_UNSUPPORTED  # num_pages * page_size
+    assert call(ps=16, rows=1 << 30) == sv.SV_ERR_UNSUPPORTED
+
+
+def test_release_pages_host_validation(L):
+    def call(**kw):
+        a = dict(keep=FAKE, cnt=FAKE, tab=FAKE, stk=FAKE, fc=FAKE, B=2, ps=0, mp=8, np=64, nc=OTHER, nf=OTHER)
+        a.update(kw)
+        return L.sv_release_pages(a["keep"], a["cnt"], a["tab"], a["stk"], a["fc"], a["B"], a["ps"], a["mp"],
+                                  a["np"], a["nc"], a["nf"], None, None)
+    for name in ("keep", "cnt", "tab", "stk", "fc", "nc", "nf"):
+        assert call(ps=16, **{name: None}) == sv.SV_ERR_INVALID_ARG, name
+    assert call() == sv.SV_ERR_INVALID_ARG
+    assert call(ps=16, nc=FAKE) == sv.SV_ERR_INVALID_ARG
+    assert call(ps=16, nf=FAKE) == sv.SV_ERR_INVALID_ARG
+    assert call(ps=16, B=5000) == sv.SV_ERR_UNSUPPORTED
+
+
+def test_append_host_validation(L):
+    def call(**kw):
+        a = dict(k=FAKE, v=FAKE, dt=sv.SV_BF16, ks=1024, vs=1024, sm=FAKE, rows=4, Hkv=8, D=128, ps=16, np=8,
+                 kp=FAKE, vp=FAKE)
+        a.update(kw)
+        return L.sv_append_kv_paged(a["k"], a["v"], a["dt"], a["ks"], a["vs"], a["sm"], a["rows"], a["Hkv"],
+                                    a["D"], a["ps"], a["np"], a["kp"], a["vp"], None, None)
+    for name in ("k", "v", "sm", "kp", "vp"):
+        assert call(**{name: None}) == sv.SV_ERR_INVALID_ARG, name
+    for name in ("k", "v", "kp", "vp"):
+        assert call(**{name: MISALIGNED}) == sv.SV_ERR_INVALID_ARG, name
+    for name in ("rows", "Hkv", "D", "ps", "np"):
+        assert call(**{name: 0}) == sv.SV_ERR_INVALID_ARG, name
+    assert call(dt=5) == sv.SV_ERR_INVALID_ARG
+    assert call(ks=1016) == sv.SV_ERR_INVALID_ARG               # rows would overlap
+    assert call(vs=1028) == sv.SV_ERR_INVALID_ARG               # rows off their 16-byte boundaries
+    assert call(dt=sv.SV_F32, vs=1026) == sv.SV_ERR_INVALID_ARG
+    assert call(D=100, ks=1024, vs=1024) == sv.SV_ERR_UNSUPPORTED
+    assert call(D=512, ks=4096, vs=4096) == sv.SV_ERR_UNSUPPORTED
+    assert call(np=1 << 24) == sv.SV_ERR_UNSUPPORTED
+
+
+class Recorder:
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        if name.startswith("__"):
+            raise AttributeError(name)
+
+        def fn(*args):
+            self.calls.append((name, args))
+            return 0
+        return fn
+
+
+@pytest.fixture
+def rec(monkeypatch):
+    r = Recorder()
+    monkeypatch.setattr(api, "_lib", r)
+    monkeypatch.setattr(api, "_on_device", lambda t: True)
+    return r
+
+
+def _i32(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+def _refused(rec, fn, **kw):
+    n = len(rec.calls)
+    with pytest.raises((ValueError, TypeError)):
+        fn(**kw)
+    assert len(rec.calls) == n
+
+
+def _build_kw():
+    return dict(prefix_lens=_i32(3), new_lens=_i32(3), page_counts=_i32(3), block_table=_i32(3, 5),
+                free_pages=_i32(20), free_count=_i32(1), page_size=16, num_rows=11, row_starts=_i32(4),
+                slot_map=_i32(11), new_page_counts=_i32(3), new_free_count=_i32(1), seq_status=_i32(3),
+                stream=STREAM)
+
+
+def test_build_marshalling(rec):
+    kw = _build_kw()
+    got = api.sv_build_block_tables(**kw)
+    name, a = rec.calls[-1]
+    assert name == "sv_build_block_tables"
+    assert a[5:10] == (3, 16, 5, 20, 11)     # B, page_size, max_pages, num_pages, num_rows
+    order = ("prefix_lens", "new_lens", "page_counts", "free_pages", "free_count")
+    assert list(a[:5]) == [kw[n].data_ptr() for n in order]
+    assert list(a[10:16]) == [kw[n].data_ptr() for n in ("block_table", "row_starts", "slot_map",
+                                                         "new_page_counts", "new_free_count", "seq_status")]
+    assert [g is kw[n] for g, n in zip(got, ("row_starts", "slot_map", "new_page_counts", "new_free_count"))]
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("prefix_lens", _i32(4)), ("new_lens", _i32(2)), ("page_counts", _i32(1)), ("free_count", _i32(2)),
+    ("block_table", _i32(15)), ("free_pages", _i32(4, 5)), ("row_starts", _i32(3)), ("slot_map", _i32(12)),
+    ("new_page_counts", _i32(4)), ("new_free_count", _i32(0)), ("seq_status", _i32(4)), ("page_size", 16.0),
+    ("num_rows", -1), ("num_rows", True), ("prefix_lens", torch.zeros(3, dtype=torch.int64)),
+    ("new_lens", [1, 2, 3]), ("page_counts", _i32(6)[::2]),
+])
+def test_build_refuses(rec, name, bad):
+    kw = _build_kw()
+    kw[name] = bad
+    _refused(rec, api.sv_build_block_tables, **kw)
+
+
+def _release_kw():
+    return dict(keep_lens=_i32(3), page_counts=_i32(3), block_table=_i32(3, 5), free_pages=_i32(20),
+                free_count=_i32(1), page_size=16, new_page_counts=_i32(3), new_free_count=_i32(1),
+                seq_status=_i32(3), stream=STREAM)
+
+
+def test_release_marshalling(rec):
+    kw = _release_kw()
+    api.sv_release_pages(**kw)
+    name, a = rec.calls[-1]
+    assert name == "sv_release_pages" and a[5:9] == (3, 16, 5, 20)
+    assert list(a[:5]) == [kw[n].data_ptr() for n in ("keep_lens", "page_counts", "block_table", "free_pages",
+                                                      "free_count")]
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("keep_lens", _i32(2)), ("page_counts", _i32(4)), ("block_table", _i32(2, 5)), ("free_pages", _i32(2, 2)),
+    ("free_count", _i32(3)), ("new_page_counts", _i32(2)), ("new_free_count", _i32(2)), ("seq_status", _i32(1)),
+    ("page_size", None),
+])
+def test_release_refuses(rec, name, bad):
+    kw = _release_kw()
+    kw[name] = bad
+    _refused(rec, api.sv_release_pages, **kw)
+
+
+def _append_kw(dtype=torch.bfloat16):
+    qkv = torch.zeros((6, 9, 8), dtype=dtype)
+    return dict(k_new=qkv[:, 5:7], v_new=qkv[:, 7:9], slot_map=_i32(6),
+                k_pages=torch.zeros((4, 2, 16, 8), dtype=torch.bfloat16),
+                v_pages=torch.zeros((4, 2, 16, 8), dtype=torch.bfloat16), row_status=_i32(6), stream=STREAM)
+
+
+@pytest.mark.parametrize("dtype,code", [(torch.bfloat16, sv.SV_BF16), (torch.float32, sv.SV_F32)])
+def test_append_marshalling(rec, dtype, code):
+    kw = _append_kw(dtype)
+    api.sv_append_kv_paged(**kw)
+    name, a = rec.calls[-1]
+    assert name == "sv_append_kv_paged"
+    assert a[2:5] == (code, 72, 72) and a[6:11] == (6, 2, 8, 16, 4)  # rows, Hkv, D, page_size, num_pages
+    assert a[0] == kw["k_new"].data_ptr() and a[1] == kw["v_new"].data_ptr()
+
+
+def test_append_refuses(rec):
+    bf = torch.bfloat16
+    for name, bad in (("k_new", torch.zeros((6, 3, 8), dtype=bf)), ("v_new", torch.zeros((5, 2, 8), dtype=bf)),
+                      ("k_new", torch.zeros((6, 2, 8), dtype=torch.float16)),
+                      ("v_new", torch.zeros((6, 2, 8), dtype=torch.float32)),
+                      ("k_new", torch.zeros((6, 2, 16), dtype=bf)[:, :, ::2]),
+                      ("k_new", torch.zeros((2, 6, 8), dtype=bf).transpose(0, 1)),
+                      ("slot_map", _i32(7)), ("slot_map", torch.zeros(6)), ("row_status", _i32(5)),
+                      ("v_pages", torch.zeros((4, 2, 8, 8), dtype=bf)),
+                      ("k_pages", torch.zeros((4, 2, 16, 8)))):
+        kw = _append_kw()
+        kw[name] = bad
+        _refused(rec, api.sv_append_kv_paged, **kw)
