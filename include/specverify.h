@@ -74,7 +74,8 @@ typedef enum sv_op {
     SV_OP_VERIFY_TREE_GREEDY = 2,
     SV_OP_VERIFY_TREE_STOCHASTIC = 3,
     SV_OP_VERIFY_STEP_CHAIN = 4,
-    SV_OP_VERIFY_STEP_TREE_GREEDY = 5
+    SV_OP_VERIFY_STEP_TREE_GREEDY = 5,
+    SV_OP_CHUNK_ATTENTION = 6
 } sv_op;
 
 /*
@@ -87,6 +88,7 @@ typedef enum sv_op {
  *   SV_OP_VERIFY_TREE_STOCHASTIC:  B, T, V, dtype
  *   SV_OP_VERIFY_STEP_CHAIN:       B, N (as T_or_N), V, dtype, Hq, Hkv, D
  *   SV_OP_VERIFY_STEP_TREE_GREEDY: B, T, V, dtype, Hq, Hkv, D
+ *   SV_OP_CHUNK_ATTENTION:         Hq, Hkv, D (B and T_or_N too are ignored)
  * Returns 0 for invalid arguments and for shapes the call refuses as
  * SV_ERR_UNSUPPORTED.
  */
@@ -403,6 +405,57 @@ sv_status sv_append_kv_paged(const void *k_new, const void *v_new, sv_dtype dtyp
                              int num_rows, int Hkv, int D, int page_size, int num_pages,
                              void *k_pages, void *v_pages, int32_t *row_status,
                              sv_stream_t stream);
+
+/*
+ * Attention of chunks of new tokens over a paged KV cache: prompts (whole or
+ * in chunks of any length) and single tokens, packed row after row in one call.
+ * Source: the paged KV of "Chapitre 9", section "Ce que prépare le Chapitre
+ * 9"; "Chapitre 9" §9.1 (the prefix's K/V is reused; new positions attend to
+ * it and to each other causally in one pass).
+ *
+ * Sequence b's rows are row_starts[b] .. row_starts[b + 1] - 1 (none, one or
+ * many); the i-th of them is at position p = prefix_lens[b] + i, its own K/V row
+ * already in the cache (sv_append_kv_paged).  For query head h (KV head
+ * h / (Hq/Hkv)):
+ *   out[r,h,:] = sum_j softmax_j(scale * q[r,h,:] . k_j) v_j
+ *   lse[r,h]   = log sum_j exp(scale * q[r,h,:] . k_j)          (natural log)
+ * over the logical slots j <= p, and j > p - window when window > 0.
+ *
+ *   q            bf16 [num_rows, Hq, D], rows q_stride elements apart
+ *                (>= Hq * D, a multiple of 8: part of a fused projection)
+ *   k_pages, v_pages, block_table  as sv_tree_attention_paged.  A slot that no
+ *                row of its sequence sees may hold anything, and a table entry
+ *                for a page without a seen slot is never read (pages behind
+ *                a window may be gone); a slot that some row sees holds finite
+ *                values
+ *   prefix_lens  int32 [B]; row_starts int32 [B + 1].  A sequence with
+ *                prefix < 0, rows outside [0, num_rows) or in descending order,
+ *                or prefix + rows > max_pages * page_size is skipped
+ *                (SV_ERR_BAD_INPUT); one with a page id outside [0, num_pages)
+ *                among the pages its rows see is reported so, its rows
+ *                unspecified.  Rows of no sequence, and of a skipped one, are
+ *                left as they were.  Sequences' rows must not overlap
+ *   window       >= 0; 0: no limit
+ *   out          bf16 [num_rows, Hq, D]; must not overlap q
+ *   lse          f32 [num_rows, Hq] or NULL
+ *   seq_status   int32 [B] or NULL
+ *   workspace    >= sv_workspace_size(SV_OP_CHUNK_ATTENTION, 0, 0, 0, dtype,
+ *                Hq, Hkv, D) bytes, of which the first 64 KiB zero-filled
+ *                before its first use
+ * P is rounded to bf16 for the second product, as in sv_tree_attention; sums,
+ * maxima and O are f32.  The result does not depend on how the SMs
+ * interleave: cut work is merged in a fixed order.
+ * Supported: D = 64 or 128, Hq % Hkv == 0, Hq/Hkv <= 128, B <= 4096, page_size
+ * a power of two >= 8 or a multiple of 128, num_rows < 2^30,
+ * max_pages * page_size < 2^30, num_pages * Hkv * page_size < 2^31.
+ */
+sv_status sv_chunk_attention_paged(const void *q, long long q_stride, const void *k_pages,
+                                   const void *v_pages, const int32_t *block_table, int max_pages,
+                                   int num_pages, int page_size, const int32_t *prefix_lens,
+                                   const int32_t *row_starts, int B, int num_rows, int Hq, int Hkv,
+                                   int D, float scale, int window, void *out, float *lse,
+                                   int32_t *seq_status, void *workspace, size_t workspace_bytes,
+                                   sv_stream_t stream);
 
 /*
  * The fused verification step on a chain: sv_tree_attention with the causal

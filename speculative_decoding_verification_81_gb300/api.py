@@ -34,12 +34,13 @@ SV_OP_VERIFY_TREE_GREEDY = 2
 SV_OP_VERIFY_TREE_STOCHASTIC = 3
 SV_OP_VERIFY_STEP_CHAIN = 4
 SV_OP_VERIFY_STEP_TREE_GREEDY = 5
+SV_OP_CHUNK_ATTENTION = 6
 
 EXPORTS = ("sv_workspace_size", "sv_tree_attention", "sv_verify_chain", "sv_verify_tree_greedy",
            "sv_compact_kv", "sv_status_string", "sv_version", "sv_verify_chain_noalloc",
            "sv_tree_attention_paged", "sv_compact_kv_paged", "sv_verify_tree_stochastic",
            "sv_verify_step_chain", "sv_verify_step_tree_greedy", "sv_build_block_tables",
-           "sv_release_pages", "sv_append_kv_paged")
+           "sv_release_pages", "sv_append_kv_paged", "sv_chunk_attention_paged")
 
 # Length of the fixed scratch array behind sv_verify_chain_noalloc.
 SV_NOALLOC_SCRATCH_BYTES = 4 << 20
@@ -100,7 +101,10 @@ def load(path: str) -> ctypes.CDLL:
     L.sv_build_block_tables.argtypes = [P, P, P, P, P, I, I, I, I, I, P, P, P, P, P, P, P]
     L.sv_release_pages.argtypes = [P, P, P, P, P, I, I, I, I, P, P, P, P]
     L.sv_append_kv_paged.argtypes = [P, P, I, Q, Q, P, I, I, I, I, I, P, P, P, P]
+    L.sv_chunk_attention_paged.argtypes = [P, Q, P, P, P, I, I, I, P, P, I, I, I, I, I, F, I, P, P, P,
+                                           P, Z, P]
     for fn in ("sv_build_block_tables", "sv_release_pages", "sv_append_kv_paged",
+               "sv_chunk_attention_paged",
                "sv_tree_attention", "sv_verify_chain", "sv_verify_tree_greedy", "sv_compact_kv",
                "sv_verify_chain_noalloc", "sv_tree_attention_paged", "sv_compact_kv_paged",
                "sv_verify_tree_stochastic", "sv_verify_step_chain", "sv_verify_step_tree_greedy"):
@@ -718,6 +722,72 @@ def sv_append_kv_paged(k_new, v_new, slot_map, k_pages, v_pages, row_status=None
         rc = lib().sv_append_kv_paged(p_kn, p_vn, dt, k_stride, v_stride, p_slot, num_rows, Hkv, D,
                                       page_size, num_pages, p_k, p_v, p_st, s)
     _check("sv_append_kv_paged", rc)
+
+
+_WS_ZEROED = 1 << 16  # bytes at a chunk attention workspace's start that must begin as zeros
+_chunk_ws: dict = {}
+
+
+def _chunk_workspace(Hq, Hkv, D, device, stream):
+    """A workspace for one call on `stream`: kept for the stream's later calls,
+    which run after it, or, in a capture, the graph's own (zeroed by it), so
+    that two graphs never share one."""
+    capturing = device.type == "cuda" and torch.cuda.is_current_stream_capturing()
+    key = (D, device.index, stream)
+    ws = None if capturing else _chunk_ws.get(key)
+    if ws is None:
+        n = sv_workspace_size(SV_OP_CHUNK_ATTENTION, 0, 0, Hq=Hq, Hkv=Hkv, D=D)
+        if n == 0:
+            raise SpecVerifyError("sv_workspace_size", SV_ERR_UNSUPPORTED)
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        ws[:_WS_ZEROED].zero_()
+        if not capturing:
+            _chunk_ws[key] = ws
+    return ws
+
+
+def sv_chunk_attention_paged(q, k_pages, v_pages, block_table, prefix_lens, row_starts, scale=None,
+                             window=0, out=None, lse=None, return_lse=False, seq_status=None,
+                             ws=None, stream=None):
+    """q [num_rows,Hq,D] bf16 (rows may lie apart: part of a fused projection);
+    k_pages/v_pages [num_pages,Hkv,page_size,D] bf16; block_table
+    [B,max_pages], prefix_lens [B], row_starts [B+1] int32; window: slots a
+    row sees at most (0: all before it).  Returns out [num_rows,Hq,D] bf16, or
+    (out, lse [num_rows,Hq] f32) with return_lse or a given lse."""
+    bf16, i32 = torch.bfloat16, torch.int32
+    p_k, p_v, dev = _pages(k_pages, v_pages)
+    num_pages, Hkv, page_size, D = k_pages.shape
+    p_q, q_stride = _rows(q, "q", None, dev)
+    num_rows, Hq, dq = q.shape
+    if q.dtype != bf16:
+        raise TypeError(f"q must be {bf16}, got {q.dtype}")
+    if dq != D:
+        raise ValueError(f"q must have shape [num_rows, Hq, {D}], got {tuple(q.shape)}")
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a tensor of 2 dims")
+    B, max_pages = block_table.shape
+    p_tab = _arr(block_table, "block_table", i32, (B, max_pages), dev)
+    p_pre = _arr(prefix_lens, "prefix_lens", i32, (B,), dev)
+    p_row = _arr(row_starts, "row_starts", i32, (B + 1,), dev)
+    p_st = _opt_arr(seq_status, "seq_status", i32, (B,), dev)
+    _need_int(window, "window")
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    with _Launch(dev, stream) as s:
+        if out is None:
+            out = torch.empty((num_rows, Hq, D), dtype=bf16, device=dev)
+        if lse is None and return_lse:
+            lse = torch.empty((num_rows, Hq), dtype=torch.float32, device=dev)
+        if ws is None:
+            ws = _chunk_workspace(Hq, Hkv, D, dev, s)
+        rc = lib().sv_chunk_attention_paged(
+            p_q, q_stride, p_k, p_v, p_tab, max_pages, num_pages, page_size, p_pre, p_row, B,
+            num_rows, Hq, Hkv, D, float(scale), window,
+            _arr(out, "out", bf16, (num_rows, Hq, D), dev),
+            _opt_arr(lse, "lse", torch.float32, (num_rows, Hq), dev), p_st,
+            _arr(ws, "ws", torch.uint8, ws.shape, dev), ws.numel(), s)
+    _check("sv_chunk_attention_paged", rc)
+    return out if lse is None else (out, lse)
 
 
 def sv_verify_chain_noalloc(target_logits, draft_logits, draft_tokens, u_accept, u_sample,

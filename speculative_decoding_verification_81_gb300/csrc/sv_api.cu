@@ -34,8 +34,14 @@ const char *sv_status_string(sv_status s) {
 
 size_t sv_workspace_size(sv_op op, int B, int T_or_N, int V, sv_dtype dtype, int Hq, int Hkv,
                          int D) {
+    if (op == SV_OP_CHUNK_ATTENTION) {
+        if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
+        sv::ChunkPlan pl;
+        return sv::plan_chunk(Hq, Hkv, D, &pl) == SV_OK ? pl.bytes : 0;
+    }
     if (B <= 0 || T_or_N <= 0) return 0;
     switch (op) {
+        case SV_OP_CHUNK_ATTENTION: break;  // (above)
         case SV_OP_TREE_ATTENTION: {
             if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
             sv::AttnPlan pl;
@@ -294,6 +300,38 @@ sv_status sv_append_kv_paged(const void *k_new, const void *v_new, sv_dtype dtyp
     sv::AppendArgs a{k_new, v_new, k_stride,  v_stride,  slot_map, num_rows,
                      Hkv,   D,     page_size, num_pages, k_pages,  v_pages, row_status};
     return sv::launch_append_kv(a, dtype, as_stream(stream));
+}
+
+sv_status sv_chunk_attention_paged(const void *q, long long q_stride, const void *k_pages,
+                                   const void *v_pages, const int32_t *block_table, int max_pages,
+                                   int num_pages, int page_size, const int32_t *prefix_lens,
+                                   const int32_t *row_starts, int B, int num_rows, int Hq, int Hkv,
+                                   int D, float scale, int window, void *out, float *lse,
+                                   int32_t *seq_status, void *workspace, size_t workspace_bytes,
+                                   sv_stream_t stream) {
+    if (!q || !k_pages || !v_pages || !block_table || !prefix_lens || !row_starts || !out)
+        return SV_ERR_INVALID_ARG;
+    if (B <= 0 || num_rows <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || max_pages <= 0 || num_pages <= 0 ||
+        window < 0)
+        return SV_ERR_INVALID_ARG;
+    if (!valid_page_size(page_size)) return SV_ERR_INVALID_ARG;
+    if (Hq % Hkv != 0 || !(scale > 0.f) || !std::isfinite(scale)) return SV_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out))
+        return SV_ERR_INVALID_ARG;
+    if (q_stride < (long long)Hq * D || q_stride % 8 != 0) return SV_ERR_INVALID_ARG;
+    if (B > 4096 || num_rows >= (1 << 30) || (long long)Hq * D >= (1LL << 30) || q_stride >= (1LL << 38) ||
+        (long long)max_pages * page_size >= (1LL << 30) || (long long)B * max_pages >= (1LL << 31) ||
+        (long long)num_pages * Hkv * page_size >= (1LL << 31))
+        return SV_ERR_UNSUPPORTED;
+    sv::ChunkPlan pl;
+    const sv_status st = sv::plan_chunk(Hq, Hkv, D, &pl);
+    if (st != SV_OK) return st;
+    if (!workspace || workspace_bytes < pl.bytes || !aligned16(workspace)) return SV_ERR_WORKSPACE;
+    sv::ChunkArgs a{q,         q_stride,    k_pages,    v_pages, block_table, max_pages,
+                    num_pages, page_size,   prefix_lens, row_starts, B,       num_rows,
+                    Hq,        Hkv,         D,          scale,   window,      out,
+                    lse,       seq_status};
+    return sv::launch_chunk_attention(a, pl, workspace, as_stream(stream));
 }
 
 }  // extern "C"

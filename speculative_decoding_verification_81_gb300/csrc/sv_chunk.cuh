@@ -1,0 +1,81 @@
+// sv_chunk.cuh -- geometry, parameters and shared-memory layout of the chunk
+// attention kernel (sv_chunk_tc.cu) and its host side (sv_chunk.cu).
+#pragma once
+
+#include "sv_chunk_list.h"
+#include "sv_device.cuh"
+#include "sv_internal.h"
+
+namespace sv {
+namespace chunk {
+
+constexpr int kBK = kTileSlots;          // slots of a K/V tile
+constexpr int kRows = 128;               // rows of a Q tile (the MMA's M)
+constexpr int kBox = kBK * 64 * 2;       // 128 rows of 64 dims: 16 KB
+constexpr int kThreads = 32 * 12;
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;  // 256 x 208 + 128 x 88 = 384 x 168
+constexpr int kLaunchRegs = 168;
+constexpr int kItems = 4;                // items published ahead
+constexpr int kMinUnits = 4;             // units a CTA takes at least
+constexpr int kNone = INT32_MIN;
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units the maximum grows before O is rescaled
+
+// Tensor-memory columns: S (then P) of streams 0 and 1, O of streams 0 and 1.
+constexpr uint32_t kCols = 512, kColS = 0, kColO = 256;
+
+template <int D>
+constexpr int kTileBytes = kBK * D * 2;
+template <int D>
+constexpr int kStagesOf = D == 128 ? 5 : 8;  // K and V tiles in flight
+
+struct Params {
+    uint16_t *out;
+    float *lse;                    // or null
+    const int32_t *block_table;
+    const int32_t *prefix_lens;
+    const int32_t *row_starts;
+    int32_t *seq_status;           // or null
+    Shape shape;                   // tpt = 128 / G tokens of a Q tile
+    int B, Hq, Hkv, G;
+    int max_pages, num_pages, page_size;
+    float scale_log2;
+    float *part_o;   // [grid][2][Q tile][D / 4][128] float4: a cut item's unnormalised O
+    float *part_ml;  // [grid][2][Q tile][128] float2: (max in log2 units, sum)
+    int *counters;   // [grid][Q tile][quarter]: CTAs arrived at a cut item (0 between calls)
+};
+
+// A run of K/V tiles of one item.
+struct Item {
+    int b;             // sequence; -1: the end of the list
+    int h;             // KV head
+    int row0, ntok;    // first row, tokens (1 .. 2 tpt)
+    int pos0;          // position of the first token
+    int kt0, n;        // first K/V tile and number of tiles of this run
+    int single;        // the sequence's only item: its K/V is read once
+    int c_first, nc;   // CTAs that share the item's tiles: c_first .. c_first + nc - 1
+    int ci;            // this CTA's index among them
+};
+
+struct Shared {
+    uint64_t full[8], empty[8];        // K/V ring
+    uint64_t q_full[2], q_empty[2];    // Q tiles
+    uint64_t s_full[2], p_full[2];     // per stream: S ready; P ready
+    uint64_t o_full[2], o_empty[2];    // per stream: O complete; O read
+    uint64_t x_full[2];                // per stream: its share of a one-tile item posted
+    uint64_t item_full[kItems], item_empty[kItems];
+    uint64_t fin;
+    float2 xml[2][kRows];              // a stream's (m, sum) of a one-tile item
+    Item items[kItems];
+    long long warp_units[kThreads / 32];
+    long long U, ub_start;
+    int nctas, b_start;
+    uint32_t tmem;
+    int abort_flag;
+};
+
+const void *kernel_fn(int D);
+int smem_bytes(int D);
+
+}  // namespace chunk
+}  // namespace sv

@@ -1,0 +1,132 @@
+// sv_chunk_list.h -- the work list of the chunk attention as arithmetic on
+// host or device: items of a sequence, their units, and the cut of the list
+// into the CTAs' ranges.
+//
+// An item is up to 2 tpt consecutive rows of one sequence and one KV head; its
+// units are kItemCost and one for each 128-slot K/V tile that its rows see.
+// The list runs over sequences, then KV heads, then items; CTA c of nctas
+// takes units floor(U c / nctas) .. floor(U (c + 1) / nctas) - 1 of the U.
+#pragma once
+
+#include <stdint.h>
+
+#ifdef __CUDACC__
+#define SV_HD __host__ __device__ __forceinline__
+#else
+#define SV_HD inline
+#endif
+
+namespace sv {
+namespace chunk {
+
+constexpr int kTileSlots = 128;
+constexpr int kItemCost = 1;  // an item's start and end, in K/V tiles
+
+// Sum of floor((a i + c) / m) for i = 0 .. n - 1 (m > 0): the quotients' whole
+// parts in closed form, the rest by exchanging the roles of slope and
+// modulus, as Euclid's algorithm does.
+SV_HD long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t c) {
+    long long s = 0;
+    while (n > 0) {
+        if (a >= m) {
+            s += (long long)n * (n - 1) / 2 * (a / m);
+            a %= m;
+        }
+        if (c >= m) {
+            s += (long long)n * (c / m);
+            c %= m;
+        }
+        const unsigned long long y = (unsigned long long)a * n + c;
+        if (y < m) break;  // (with a = 0 always)
+        n = (uint32_t)(y / m);
+        c = (uint32_t)(y % m);
+        const uint32_t t = m;
+        m = a;
+        a = t;
+    }
+    return s;
+}
+
+struct Shape {
+    int tpt;     // tokens of a Q tile
+    int window;  // slots a row sees at most, 0: all
+    int num_rows, S_max;
+};
+
+struct Seq {
+    int L, n;   // filled slots, new rows (0: none, or refused)
+    int row0;   // its first row
+    int items;  // items per KV head
+};
+
+// The lengths of a sequence whose rows are r0 .. r1 - 1 after L slots.
+SV_HD bool lengths_ok(const Shape &p, int L, int r0, int r1) {
+    return L >= 0 && r0 >= 0 && r1 >= r0 && r1 <= p.num_rows && (long long)L + r1 - r0 <= p.S_max;
+}
+
+SV_HD Seq seq_of(const Shape &p, int L, int r0, int r1) {
+    Seq s;
+    s.L = L;
+    s.row0 = r0;
+    s.n = lengths_ok(p, L, r0, r1) ? r1 - r0 : 0;
+    s.items = s.n == 0 ? 0 : (s.n - 1) / (2 * p.tpt) + 1;
+    return s;
+}
+
+// The first tile that the row at position pos sees.
+SV_HD int first_tile(const Shape &p, int pos) {
+    return p.window > 0 && pos >= p.window ? (pos - p.window + 1) / kTileSlots : 0;
+}
+
+// K/V tiles of item i.
+SV_HD int item_tiles(const Shape &p, const Seq &s, int i) {
+    const int t0 = i * 2 * p.tpt, t1 = s.n - t0 < 2 * p.tpt ? s.n : t0 + 2 * p.tpt;
+    return (s.L + t1 + kTileSlots - 1) / kTileSlots - first_tile(p, s.L + t0);
+}
+
+// Units of items 0 .. i - 1 of one KV head.
+SV_HD long long units_before(const Shape &p, const Seq &s, int i) {
+    if (i <= 0) return 0;
+    long long u = (long long)i * kItemCost;
+    if (i == s.items) u += item_tiles(p, s, --i);  // the last item may be short
+    if (i > 0) {
+        const uint32_t tok = 2 * p.tpt;
+        u += floor_sum(i, kTileSlots, tok, s.L + tok + kTileSlots - 1);
+        if (p.window > 0) {
+            // first tiles: floor((L + k tok - window + 1) / 128), from the first k at which that is >= 0
+            const long long c = (long long)s.L - p.window + 1;
+            const long long k0 = c >= 0 ? 0 : (-c + tok - 1) / tok;
+            if (k0 < i) u -= floor_sum((uint32_t)(i - k0), kTileSlots, tok, (uint32_t)(c + k0 * tok));
+        }
+    }
+    return u;
+}
+
+SV_HD long long cta_begin(long long U, int nctas, int c) { return U * c / nctas; }
+
+// The CTA whose range holds unit u.
+SV_HD int cta_of(long long U, int nctas, long long u) { return (int)(((u + 1) * nctas - 1) / U); }
+
+// What of an item of n tiles whose units start at ui falls into units
+// u0 .. u1 - 1 of CTA `cta`: tiles a .. z - 1 (none if a >= z), shared with
+// CTAs c_first .. c_first + nc - 1.
+struct Cut {
+    int a, z, c_first, nc;
+};
+
+SV_HD Cut cut_item(long long ui, int n, long long u0, long long u1, long long U, int nctas, int cta) {
+    const long long t = ui + kItemCost;  // the unit of the first tile
+    Cut c;
+    c.a = u0 <= t ? 0 : u0 - t < n ? (int)(u0 - t) : n;
+    c.z = u1 >= t + n ? n : u1 > t ? (int)(u1 - t) : 0;
+    c.c_first = cta;
+    c.nc = 1;
+    if (c.a < c.z && (c.a > 0 || c.z < n)) {
+        c.c_first = cta_of(U, nctas, t);
+        c.nc = cta_of(U, nctas, t + n - 1) - c.c_first + 1;
+    }
+    return c;
+}
+
+}  // namespace chunk
+}  // namespace sv

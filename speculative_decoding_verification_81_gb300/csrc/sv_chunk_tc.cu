@@ -1,0 +1,773 @@
+// sv_chunk_tc.cu -- attention of chunks of new tokens over a paged KV cache
+// (prompt chunks of any length, mixed with single tokens) on the
+// 5th-generation tensor cores.
+//
+// Source: the paged KV of "Chapitre 9", section "Ce que prépare le Chapitre
+// 9"; "Chapitre 9" §9.1 (the prefix's K/V is reused, the new positions attend
+// to it and causally to each other in one pass).
+//
+// Row i of sequence b sits at position p = L_b + i and sees the slots
+// max(0, p - window + 1) .. p.  An item is a run of consecutive rows of one
+// sequence and one KV head: the G = Hq/Hkv heads of a token share K/V, so a
+// Q tile holds tpt = 128 / G tokens (128 MMA rows), and an item one or two
+// tiles.  For each 128-slot tile of K/V an item runs one step a Q tile:
+//     S = Q K^T (128 x 128, f32 in tensor memory)
+//     P = 2^(scale * log2 e * S - m), written over S as bf16
+//     O += P V (f32 in tensor memory)
+// with a running row maximum m that moves only when it grows by more than
+// 2^8 (O is then rescaled) and the row sums of the f32 P.
+//
+// Two streams of steps alternate, so that the tensor core works on one
+// stream's products while the softmax warps of the other turn S into P: the
+// steps of a CTA are one list, step g belongs to stream g & 1 (its own S/P
+// and O columns and its own four softmax warps).  An item of two Q tiles puts
+// a tile on each stream and both read every K/V tile; an item of one Q tile
+// (single tokens, short chunks) gives the streams its K/V tiles in turn, and
+// their (O, m, sum) are merged at the end.
+//
+// The work list is every (sequence, KV head, item, K/V tile).  A persistent
+// grid takes equal contiguous ranges of it (an item counts kItemCost tiles
+// more than it has, for its start and end), so the load is even whatever the
+// lengths; an item cut by a range's end leaves partials in the workspace,
+// merged by the warp that arrives last, in index order.
+//
+// Warps: 0-3 and 4-7 softmax of streams 0 and 1 (one thread a row); 8 loads K
+// and V tiles by TMA through the page table; 9 issues the products; 10 walks
+// the work list, publishes the items and loads Q; 11 checks the page table
+// and writes seq_status.  Every wait is bounded.
+#include <type_traits>
+
+#include "sv_chunk.cuh"
+
+namespace sv {
+namespace chunk {
+
+// ---------------------------------------------------------------- small pieces
+
+__device__ __forceinline__ uint32_t sw128(int row, int c) {
+    return (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4));
+}
+
+// 16 bytes from 8 floats.
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
+
+// This warp's O rows (D columns at TMEM address o) times a.
+template <int D>
+__device__ __noinline__ void rescale_o(uint32_t o, float a) {
+#pragma unroll
+    for (int h = 0; h < D / 32; ++h) {
+        uint32_t ov[32];
+        tc::tmem_ld32(o + 32 * h, ov);
+        tc::wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * a);
+        tc::tmem_st32(o + 32 * h, ov);
+    }
+    tc::wait_st();
+}
+
+// V rows [z0, z1) of a tile zeroed by the 128 threads of a stream, visible to
+// the tensor core: slots that no row sees may hold anything, and 0 * NaN
+// would reach every row.
+template <int D>
+__device__ __noinline__ void zero_v_rows(uint8_t *st, int z0, int z1, int t) {
+    constexpr int kW = D / 8;  // 16-byte words of a row
+    for (int i = t; i < (z1 - z0) * kW; i += 128) {
+        const int row = z0 + i / kW, c = i % kW;
+        *reinterpret_cast<uint4 *>(st + (c >> 3) * kBox + sw128(row, c & 7)) = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+// A split item's rows of one warp: partial O (chunk-major, so that a warp's
+// lanes, one row each, use consecutive 16 bytes) and (m, sum).
+template <int D>
+__device__ __forceinline__ float4 *part_o(const Params &p, int cta, int slot, int qt) {
+    return reinterpret_cast<float4 *>(p.part_o) + ((size_t)(cta * 2 + slot) * 2 + qt) * (D / 4) * kRows;
+}
+__device__ __forceinline__ float2 *part_ml(const Params &p, int cta, int slot, int qt) {
+    return reinterpret_cast<float2 *>(p.part_ml) + ((size_t)(cta * 2 + slot) * 2 + qt) * kRows;
+}
+
+// The nc partials of this warp's rows (row0 .. row0 + nv - 1 of Q tile qt;
+// out_off and lse_off: lane r's row in `out` and `lse`) merged in index order
+// and written out.
+template <int D>
+__device__ __noinline__ void merge_parts(const Params &p, const Item it, int qt, int row0, int nv,
+                                         int lane, long long out_off, long long lse_off) {
+    float M = kNegInf, l = 0.f;
+    if (lane < nv) {
+#pragma unroll 4
+        for (int i = 0; i < it.nc; ++i)
+            M = fmaxf(M, __ldcg(part_ml(p, it.c_first + i, i == 0, qt) + row0 + lane).x);
+#pragma unroll 4
+        for (int i = 0; i < it.nc; ++i) {
+            const float2 ml = __ldcg(part_ml(p, it.c_first + i, i == 0, qt) + row0 + lane);
+            l += ml.x == kNegInf ? 0.f : ml.y * ex2_approx(ml.x - M);
+        }
+        if (p.lse) p.lse[lse_off] = l > 0.f ? M * kLn2 + logf(l) : kNegInf;
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int total = nv * (D / 8);
+    for (int idx0 = 0; idx0 < total; idx0 += 32) {
+        const int idx = idx0 + lane;
+        const int c8 = idx / nv, r = idx - c8 * nv;
+        const float Mr = __shfl_sync(0xffffffffu, M, r);
+        const float ir = __shfl_sync(0xffffffffu, inv, r);
+        const long long off = __shfl_sync(0xffffffffu, out_off, r);
+        if (idx >= total) continue;
+        float acc[8] = {};
+#pragma unroll 4
+        for (int i = 0; i < it.nc; ++i) {
+            const float2 ml = __ldcg(part_ml(p, it.c_first + i, i == 0, qt) + row0 + r);
+            const float4 *src = part_o<D>(p, it.c_first + i, i == 0, qt) + row0 + r;
+            const float4 x = __ldcg(src + (size_t)(2 * c8) * kRows);
+            const float4 y = __ldcg(src + (size_t)(2 * c8 + 1) * kRows);
+            // a partial without a visible slot has no O: select, never multiply, it
+            if (ml.x != kNegInf) {
+                const float w = ex2_approx(ml.x - Mr) * ir;
+                acc[0] = __fmaf_rn(x.x, w, acc[0]);
+                acc[1] = __fmaf_rn(x.y, w, acc[1]);
+                acc[2] = __fmaf_rn(x.z, w, acc[2]);
+                acc[3] = __fmaf_rn(x.w, w, acc[3]);
+                acc[4] = __fmaf_rn(y.x, w, acc[4]);
+                acc[5] = __fmaf_rn(y.y, w, acc[5]);
+                acc[6] = __fmaf_rn(y.z, w, acc[6]);
+                acc[7] = __fmaf_rn(y.w, w, acc[7]);
+            }
+        }
+        *reinterpret_cast<uint4 *>(p.out + off + 8 * c8) = pack8(acc);
+    }
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_attention_kernel(const __grid_constant__ CUtensorMap tmk,
+                           const __grid_constant__ CUtensorMap tmv,
+                           const __grid_constant__ CUtensorMap tmq,
+                           const __grid_constant__ CUtensorMap tmq1, const Params p) {
+    constexpr int kStages = kStagesOf<D>;
+    constexpr int kTile = kTileBytes<D>;
+    constexpr int kHalves = D / 64;
+    extern __shared__ __align__(1024) uint8_t smem[];  // (the swizzle's atoms are 1024 bytes)
+    const uint32_t base_u32 = smem_u32(smem);
+    uint8_t *qbuf = smem + kStages * kTile;
+    const uint32_t q_u32 = base_u32 + kStages * kTile;
+    Shared *sh = reinterpret_cast<Shared *>(qbuf + 2 * kTile);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sh->full[i], 1);
+            mbar_init(&sh->empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh->q_full[i], 1);
+            mbar_init(&sh->q_empty[i], 1);
+            mbar_init(&sh->s_full[i], 1);
+            mbar_init(&sh->p_full[i], 4);
+            mbar_init(&sh->o_full[i], 1);
+            mbar_init(&sh->o_empty[i], 4);
+            mbar_init(&sh->x_full[i], 4);
+        }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&sh->item_full[i], 1);
+            mbar_init(&sh->item_empty[i], 10);  // softmax warps, K/V loader, issuer
+        }
+        mbar_init(&sh->fin, 1);
+        sh->abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (tid == 32 * 8) {
+        prefetch_tensormap(&tmk);
+        prefetch_tensormap(&tmv);
+        prefetch_tensormap(&tmq);
+        prefetch_tensormap(&tmq1);
+    }
+    if (warp == 9) tc::tmem_alloc(&sh->tmem, kCols);
+
+    griddep_wait();
+    griddep_launch_dependents();
+    if ((base_u32 & 1023u) != 0) {  // (never seen: nothing else takes shared memory here)
+        if (p.seq_status)
+            for (int b = tid; b < p.B; b += kThreads) p.seq_status[b] = SV_ERR_CUDA;
+        __syncthreads();
+        if (warp == 9) tc::tmem_dealloc(sh->tmem, kCols);
+        return;
+    }
+
+    // ---- every CTA: units of all sequences, its own range, the sequence it starts in
+    {
+        const int per = (p.B + kThreads - 1) / kThreads;
+        const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+        long long mine = 0;
+        for (int b = b0; b < b1; ++b) {
+            const Seq s = seq_of(p.shape, p.prefix_lens[b], p.row_starts[b], p.row_starts[b + 1]);
+            mine += units_before(p.shape, s, s.items) * p.Hkv;
+        }
+        long long x = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, off);
+            if (lane >= off) x += y;
+        }
+        if (lane == 31) sh->warp_units[warp] = x;
+        tc::fence_before();  // (the tensor memory's address, below)
+        __syncthreads();
+        tc::fence_after();
+        long long before = x - mine, U = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            const long long v = sh->warp_units[w];
+            if (w < warp) before += v;
+            U += v;
+        }
+        const long long want = U / kMinUnits > 0 ? U / kMinUnits : 1;
+        const int nctas = (int)(want < (long long)gridDim.x ? want : (long long)gridDim.x);
+        const long long u0 = blockIdx.x < nctas ? cta_begin(U, nctas, blockIdx.x) : U;
+        if (tid == 0) {
+            sh->U = U;
+            sh->nctas = nctas;
+            if (u0 >= U) sh->b_start = p.B;
+        }
+        if (u0 >= before && u0 < before + mine) {  // exactly one thread, when the CTA has work
+            int b = b0;
+            long long ub = before;
+            for (; b < b1; ++b) {
+                const Seq s = seq_of(p.shape, p.prefix_lens[b], p.row_starts[b], p.row_starts[b + 1]);
+                const long long u = units_before(p.shape, s, s.items) * p.Hkv;
+                if (u0 < ub + u) break;
+                ub += u;
+            }
+            sh->b_start = b;
+            sh->ub_start = ub;
+        }
+        __syncthreads();
+    }
+    const uint32_t tbase = sh->tmem;
+    volatile int *abort_flag = &sh->abort_flag;
+    auto fail = [&](int b) {
+        *abort_flag = 1;
+        if (p.seq_status) p.seq_status[b] = SV_ERR_TIMEOUT;
+    };
+
+    if (warp < 8) {
+        // ===================== softmax: stream s, one thread a row
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        const int s = warp >> 2, quarter = warp & 3;
+        const int r = quarter * 32 + lane;  // the row in its Q tile
+        const int t = r / p.G, g = r - t * p.G;
+        const uint32_t tl = tbase + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t sbuf = tl + kColS + s * kBK;
+        const float sc = p.scale_log2;
+        uint32_t s_ph = 0, o_ph = 0, x_ph = 0;
+        uint32_t gstep = 0;       // steps of the CTA before this item
+        uint32_t ring = 0;        // K/V ring position of the item's first tile
+        bool ok = true;
+        for (uint32_t k = 0;; ++k) {
+            const int slot = k % kItems;
+            if (!warp_wait_bounded(&sh->item_full[slot], (k / kItems) & 1)) {
+                fail(0);
+                break;
+            }
+            const Item it = sh->items[slot];
+            if (it.b < 0) break;
+            const bool two = it.ntok > p.shape.tpt;
+            const int a = (s ^ (int)gstep) & 1;         // this stream's first step of the item
+            const int qt = two ? a : 0;                 // its Q tile
+            const int ntok = min(p.shape.tpt, it.ntok - qt * p.shape.tpt);
+            const int pos0 = it.pos0 + qt * p.shape.tpt;      // position of the tile's first token
+            const int rows = ntok * p.G;                // valid rows of the tile
+            const bool active = quarter * 32 < rows;    // the warp has valid rows
+            const int pos = pos0 + t;                   // this row's position
+            const int see_hi = pos + 1, see_lo = p.shape.window > 0 ? pos - p.shape.window + 1 : 0;
+            // tiles all of whose slots every row of the warp sees
+            const int w_hi = pos0 + (quarter * 32) / p.G + 1;
+            const int w_lo = p.shape.window > 0 ? pos0 + min(quarter * 32 + 31, rows - 1) / p.G - p.shape.window + 1 : 0;
+            const int item_lo = p.shape.window > 0 ? max(0, it.pos0 - p.shape.window + 1) : 0;
+            const int item_hi = it.pos0 + it.ntok;
+            float m = kNegInf, l = 0.f;
+            const int first = two ? 0 : a, stride = two ? 1 : 2;
+            const uint32_t o_cols = tl + kColO + s * 128;
+            for (int j = first; j < it.n; j += stride) {
+                const int kb = (it.kt0 + j) * kBK;
+                if (!(ok = warp_wait_bounded(&sh->s_full[s], s_ph))) break;
+                s_ph ^= 1;
+                tc::fence_after();
+                if (active) {
+                    float sv[kBK];
+                    {
+                        uint32_t ra[32], rb[32], rc[32], rd[32];
+                        tc::tmem_ld32(sbuf, ra);
+                        tc::tmem_ld32(sbuf + 32, rb);
+                        tc::tmem_ld32(sbuf + 64, rc);
+                        tc::tmem_ld32(sbuf + 96, rd);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            sv[i] = __uint_as_float(ra[i]);
+                            sv[32 + i] = __uint_as_float(rb[i]);
+                            sv[64 + i] = __uint_as_float(rc[i]);
+                            sv[96 + i] = __uint_as_float(rd[i]);
+                        }
+                    }
+                    if (kb + kBK > w_hi || kb < w_lo) {
+                        const int hi = see_hi - kb, lo = see_lo - kb;
+#pragma unroll
+                        for (int i = 0; i < kBK; ++i)
+                            if (i >= hi || i < lo) sv[i] = kNegInf;
+                    }
+                    float mq[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+                    for (int i = 0; i < kBK; i += 8) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) mq[e] = fmaxf(fmaxf(mq[e], sv[i + e]), sv[i + 4 + e]);
+                    }
+                    const float c = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * sc;
+                    const bool up = c > m + kRescaleThreshold;
+                    const bool any_up = __any_sync(0xffffffffu, up);
+                    const float f = up ? ex2_approx(m - c) : 1.f;
+                    if (up) {
+                        m = c;
+                        l *= f;
+                    }
+                    const float nb = m == kNegInf ? 0.f : -m;
+                    const float2 nb2 = make_float2(nb, nb), sc2 = make_float2(sc, sc);
+                    float2 ls0 = make_float2(0.f, 0.f), ls1 = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float2 x = __ffma2_rn(make_float2(sv[64 * h + 2 * i], sv[64 * h + 2 * i + 1]), sc2, nb2);
+                            const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                            if (i & 1) ls1 = __fadd2_rn(ls1, e);
+                            else ls0 = __fadd2_rn(ls0, e);
+                            pk[i] = pack_bf16x2(e.x, e.y);
+                        }
+                        tc::tmem_st32(sbuf + 32 * h, pk);
+                    }
+                    l += (ls0.x + ls0.y) + (ls1.x + ls1.y);
+                    // (the wait for S covers this stream's earlier PV products: issued before it)
+                    if (any_up && j != first) rescale_o<D>(o_cols, f);
+                    tc::wait_st();
+                }
+                if (kb + kBK > item_hi || kb < item_lo) {
+                    const uint32_t pv = ring + 2 * j + 1;
+                    if (!(ok = warp_wait_bounded(&sh->full[pv % kStages], (pv / kStages) & 1))) break;
+                    uint8_t *st = smem + (pv % kStages) * kTile;
+                    if (kb + kBK > item_hi) zero_v_rows<D>(st, max(0, item_hi - kb), kBK, tid & 127);
+                    if (kb < item_lo) zero_v_rows<D>(st, 0, min(kBK, item_lo - kb), tid & 127);
+                    tc::fence_proxy_async_smem();
+                }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->p_full[s]);
+            }
+            if (!ok) {
+                fail(it.b);
+                break;
+            }
+            const int steps = two ? it.n : (it.n - a + 1) / 2;
+            if (steps > 0) {  // the stream's last PV product of the item
+                if (!(ok = warp_wait_bounded(&sh->o_full[s], o_ph))) {
+                    fail(it.b);
+                    break;
+                }
+                o_ph ^= 1;
+                tc::fence_after();
+            }
+            if (!two && a == 1) {
+                // one Q tile: the other stream finishes the item
+                if (steps > 0) {
+                    sh->xml[s][r] = make_float2(m, l);
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh->x_full[s]);
+                }
+            } else {
+                const bool pair = !two && it.n > 1;  // the other stream holds a share
+                float m2 = kNegInf, l2 = 0.f;
+                if (pair) {
+                    if (!(ok = warp_wait_bounded(&sh->x_full[s ^ 1], x_ph))) {
+                        fail(it.b);
+                        break;
+                    }
+                    x_ph ^= 1;
+                    tc::fence_after();
+                    m2 = sh->xml[s ^ 1][r].x;
+                    l2 = sh->xml[s ^ 1][r].y;
+                }
+                const bool valid = r < rows;
+                const long long row = (long long)it.row0 + qt * p.shape.tpt + t;
+                const long long head = (long long)it.h * p.G + g;
+                const long long out_off = (row * p.Hq + head) * D, lse_off = row * p.Hq + head;
+                const float M = fmaxf(m, m2);
+                const float w1 = m == kNegInf ? 0.f : ex2_approx(m - M);
+                const float w2 = m2 == kNegInf ? 0.f : ex2_approx(m2 - M);
+                const float lt = l * w1 + l2 * w2;
+                const bool whole = it.nc == 1;
+                const float inv = whole ? (lt > 0.f ? 1.f / lt : 0.f) : 1.f;
+                const float f1 = w1 * inv, f2 = w2 * inv;
+                const int pslot = it.ci == 0 ? 1 : 0;
+                if (active) {
+                    if (valid && whole && p.lse) p.lse[lse_off] = lt > 0.f ? M * kLn2 + logf(lt) : kNegInf;
+                    if (valid && !whole)
+                        __stcg(part_ml(p, blockIdx.x, pslot, qt) + r, make_float2(M, lt));
+#pragma unroll
+                    for (int h = 0; h < D / 32; ++h) {
+                        uint32_t ov[32];
+                        float acc[32];
+                        __syncwarp();
+                        tc::tmem_ld32(o_cols + 32 * h, ov);
+                        tc::wait_ld();
+                        // a share without a visible slot weighs nothing, whatever its O holds
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) acc[i] = w1 != 0.f ? __uint_as_float(ov[i]) * f1 : 0.f;
+                        if (pair) {
+                            tc::tmem_ld32(tl + kColO + (s ^ 1) * 128 + 32 * h, ov);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                acc[i] = w2 != 0.f ? __fmaf_rn(__uint_as_float(ov[i]), f2, acc[i]) : acc[i];
+                        }
+                        if (!valid) continue;
+                        if (whole) {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                float e[8];
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) e[i] = acc[8 * c + i];
+                                *reinterpret_cast<uint4 *>(p.out + out_off + 32 * h + 8 * c) = pack8(e);
+                            }
+                        } else {
+                            float4 *po = part_o<D>(p, blockIdx.x, pslot, qt) + r;
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+                                __stcg(po + (size_t)(8 * h + c) * kRows,
+                                       make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]));
+                        }
+                    }
+                }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) {  // O may start over
+                    mbar_arrive(&sh->o_empty[s]);
+                    if (pair) mbar_arrive(&sh->o_empty[s ^ 1]);
+                }
+                if (!whole && active) {
+                    int *ctr = p.counters + (it.c_first * 2 + qt) * 4 + quarter;
+                    int last = 0;
+                    if (lane == 0) {
+                        __threadfence();
+                        last = atomicAdd(ctr, 1) == it.nc - 1;
+                        __threadfence();
+                        if (last) *ctr = 0;  // all have arrived: ready for the next call
+                    }
+                    if (__shfl_sync(0xffffffffu, last, 0))
+                        merge_parts<D>(p, it, qt, quarter * 32, min(32, rows - quarter * 32), lane, out_off, lse_off);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->item_empty[slot]);
+            gstep += two ? 2 * it.n : it.n;
+            ring += 2 * it.n;
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == 8) {
+            // ===================== K and V tiles: lane (half, page of the tile)
+            const int ps = p.page_size;
+            const int sub = ps < kBK ? ps : kBK;          // rows of a box
+            const int npg = kBK / sub;                    // boxes a tile and half
+            const int pg_l = lane & 15, half = lane >> 4;
+            const bool lane_on = pg_l < npg && half < kHalves;
+            const uint64_t once = l2_policy_evict_first();
+            uint32_t pos = 0;
+            bool ok = true;
+            for (uint32_t k = 0; ok; ++k) {
+                const int slot = k % kItems;
+                if (!warp_wait_bounded(&sh->item_full[slot], (k / kItems) & 1)) {
+                    fail(0);
+                    break;
+                }
+                const Item it = sh->items[slot];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->item_empty[slot]);
+                if (it.b < 0) break;
+                const int lo = p.shape.window > 0 ? max(0, it.pos0 - p.shape.window + 1) : 0, hi = it.pos0 + it.ntok;
+                const int32_t *trow = p.block_table + (size_t)it.b * p.max_pages;
+                // row of this lane's box of tile j in the caches; kNone: no slot of it is seen.  A page id
+                // out of range (reported by the check) reads zeros.
+                auto box_row = [&](int j) -> int {
+                    const int s0 = (it.kt0 + j) * kBK + pg_l * sub;
+                    if (!lane_on || s0 >= hi || s0 + sub <= lo) return kNone;
+                    const int pg = trow[s0 / ps];
+                    return pg >= 0 && pg < p.num_pages ? (pg * p.Hkv + it.h) * ps + s0 % ps : -kBK;
+                };
+                int y = box_row(0);
+                for (int j = 0; j < it.n && ok; ++j) {
+                    const int y_next = j + 1 < it.n ? box_row(j + 1) : kNone;
+                    const int boxes = __popc(__ballot_sync(0xffffffffu, y != kNone));
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv, ++pos) {
+                        const int st = pos % kStages;
+                        if (!warp_wait_bounded(&sh->empty[st], ((pos / kStages) & 1) ^ 1)) {
+                            fail(it.b);
+                            ok = false;
+                            break;
+                        }
+                        if (__shfl_sync(0xffffffffu, *abort_flag, 0)) {
+                            ok = false;
+                            break;
+                        }
+                        if (lane == 0) mbar_arrive_expect_tx(&sh->full[st], (uint32_t)(boxes * sub * 128));
+                        __syncwarp();
+                        if (y != kNone) {
+                            uint8_t *dst = smem + st * kTile + half * kBox + pg_l * sub * 128;
+                            if (it.single) tma_load_2d_hint(dst, kv ? &tmv : &tmk, half * 64, y, &sh->full[st], once);
+                            else tma_load_2d(dst, kv ? &tmv : &tmk, half * 64, y, &sh->full[st]);
+                        }
+                    }
+                    y = y_next;
+                }
+            }
+            // every copy issued must land before the CTA may exit
+            for (uint32_t q = pos > (uint32_t)kStages ? pos - kStages : 0; q < pos; ++q)
+                warp_wait_bounded(&sh->full[q % kStages], (q / kStages) & 1);
+        } else if (warp == 9) {
+            // ===================== the products, issued by one lane in step order
+            if (lane == 0) {
+                constexpr uint32_t idS = tc::idesc_bf16(kRows, kBK, false);
+                constexpr uint32_t idPV = tc::idesc_bf16(kRows, D, true);
+                struct Pending {
+                    uint32_t ring;  // its V tile
+                    bool live, first, last, frees;
+                } pend[2] = {};
+                uint32_t p_ph[2] = {0, 0}, o_ph[2] = {1, 1};
+                uint32_t g = 0, ring = 0, qpos = 0;
+                bool ok = true;
+                int b_now = 0;
+                auto issue_pv = [&](int s) -> bool {
+                    const Pending q = pend[s];
+                    pend[s].live = false;
+                    if (!mbar_wait_bounded(&sh->p_full[s], p_ph[s])) return false;
+                    p_ph[s] ^= 1;
+                    const int st = q.ring % kStages;
+                    if (!mbar_wait_bounded(&sh->full[st], (q.ring / kStages) & 1)) return false;
+                    if (q.first) {
+                        if (!mbar_wait_bounded(&sh->o_empty[s], o_ph[s])) return false;
+                        o_ph[s] ^= 1;
+                    }
+                    tc::fence_after();
+                    // V rows 16kk.. start 2048 bytes apart (descriptor units of 16 bytes)
+                    const uint64_t dv = tc::smem_desc(base_u32 + st * kTile, kBox, 1024);
+                    const uint32_t pcol = tbase + kColS + s * kBK;
+#pragma unroll
+                    for (int kk = 0; kk < kBK / 16; ++kk)
+                        tc::mma_bf16_ts(tbase + kColO + s * 128, pcol + kk * 8, dv + (uint64_t)(kk * (2048 >> 4)),
+                                        idPV, (kk > 0 || !q.first) ? 1u : 0u);
+                    if (q.frees) tc::commit(&sh->empty[st]);
+                    if (q.last) tc::commit(&sh->o_full[s]);
+                    return true;
+                };
+                for (uint32_t k = 0; ok; ++k) {
+                    const int slot = k % kItems;
+                    if (!(ok = mbar_wait_bounded(&sh->item_full[slot], (k / kItems) & 1))) break;
+                    const Item it = sh->items[slot];
+                    mbar_arrive(&sh->item_empty[slot]);
+                    if (it.b < 0) break;
+                    b_now = it.b;
+                    const bool two = it.ntok > p.shape.tpt;
+                    const int steps = two ? 2 * it.n : it.n;
+                    for (int i = 0; i < steps; ++i, ++g) {
+                        const int s = g & 1;
+                        if (pend[s].live && !(ok = issue_pv(s))) break;
+                        const int j = two ? i >> 1 : i, qt = two ? i & 1 : 0;
+                        const uint32_t qp = qpos + qt, rk = ring + 2 * j;
+                        if (j == 0) ok = mbar_wait_bounded(&sh->q_full[qp & 1], (qp >> 1) & 1);
+                        const int st = rk % kStages;
+                        if (ok) ok = mbar_wait_bounded(&sh->full[st], (rk / kStages) & 1);
+                        if (!ok || *abort_flag) {
+                            ok = false;
+                            break;
+                        }
+                        tc::fence_after();
+                        const uint64_t dk = tc::smem_desc(base_u32 + st * kTile, 16, 1024);
+                        const uint64_t dq = tc::smem_desc(q_u32 + (qp & 1) * kTile, 16, 1024);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint64_t o = (uint64_t)((kk >> 2) * (kBox >> 4) + (kk & 3) * 2);
+                            tc::mma_bf16(tbase + kColS + s * kBK, dq + o, dk + o, idS, kk > 0 ? 1u : 0u);
+                        }
+                        tc::commit(&sh->s_full[s]);
+                        const bool frees = !two || qt == 1;  // the tile's last reader
+                        if (frees) tc::commit(&sh->empty[st]);
+                        if (j == it.n - 1) tc::commit(&sh->q_empty[qp & 1]);
+                        pend[s].ring = rk + 1;
+                        pend[s].live = true;
+                        pend[s].first = two ? j == 0 : i < 2;
+                        pend[s].last = two ? j == it.n - 1 : i >= steps - 2;
+                        pend[s].frees = frees;
+                    }
+                    ring += 2 * it.n;
+                    qpos += two ? 2 : 1;
+                }
+                if (ok && pend[g & 1].live) ok = issue_pv(g & 1);
+                if (ok && pend[(g & 1) ^ 1].live) ok = issue_pv((g & 1) ^ 1);
+                if (!ok) fail(b_now);
+                // every product issued is complete before the tensor memory is given back
+                tc::commit(&sh->fin);
+                mbar_wait_bounded(&sh->fin, 0);
+            }
+            __syncwarp();
+        } else if (warp == 10) {
+            // ===================== the work list: items of this CTA's units, and their Q tiles
+            const long long U = sh->U;
+            const int nctas = sh->nctas;
+            const bool has = (int)blockIdx.x < nctas && sh->b_start < p.B;
+            const long long u0 = has ? cta_begin(U, nctas, blockIdx.x) : 0;
+            const long long u1 = has ? cta_begin(U, nctas, blockIdx.x + 1) : 0;
+            uint32_t k = 0, qpos = 0;
+            bool ok = true;
+            int b = has ? sh->b_start : p.B;
+            long long ub = has ? sh->ub_start : 0;  // first unit of sequence b
+            int pre = 0, r0 = 0, r1 = 0, cached = -1;  // lane: lengths of sequence cached + lane
+            while (ok && b < p.B && ub < u1) {
+                if (cached < 0 || b >= cached + 32) {
+                    cached = b;
+                    const int bl = min(b + lane, p.B - 1);
+                    pre = p.prefix_lens[bl];
+                    r0 = p.row_starts[bl];
+                    r1 = p.row_starts[bl + 1];
+                }
+                const Seq sq = seq_of(p.shape, __shfl_sync(0xffffffffu, pre, b - cached), __shfl_sync(0xffffffffu, r0, b - cached),
+                                      __shfl_sync(0xffffffffu, r1, b - cached));
+                if (sq.items == 0) {
+                    ++b;
+                    continue;
+                }
+                const long long per_head = units_before(p.shape, sq, sq.items);
+                int h = 0, i = 0;
+                long long ui = ub;  // first unit of item (h, i)
+                if (u0 > ub) {      // the range starts inside this sequence
+                    h = (int)((u0 - ub) / per_head);
+                    const long long v = (u0 - ub) - (long long)h * per_head;
+                    // the last item whose first unit is at most v: 32 candidates at a time
+                    int lo = 0, span = sq.items;
+                    while (span > 1) {
+                        const int step = (span + 31) / 32;
+                        const int cand = lo + lane * step;
+                        const bool below = lane * step < span && units_before(p.shape, sq, cand) <= v;
+                        const int hit = 31 - __clz(__ballot_sync(0xffffffffu, below));  // (lane 0 always)
+                        lo += hit * step;
+                        span = min(step, span - hit * step);
+                    }
+                    i = lo;
+                    ui = ub + (long long)h * per_head + units_before(p.shape, sq, i);
+                }
+                for (; ok && h < p.Hkv && ui < u1; ++h, i = 0)
+                    for (; ok && i < sq.items && ui < u1; ++i) {
+                        const int n = item_tiles(p.shape, sq, i);
+                        const Cut c = cut_item(ui, n, u0, u1, U, nctas, blockIdx.x);
+                        ui += n + kItemCost;
+                        if (c.a >= c.z) continue;  // only its cost falls into the range
+                        Item it;
+                        it.b = b;
+                        it.h = h;
+                        it.row0 = sq.row0 + i * 2 * p.shape.tpt;
+                        it.ntok = min(2 * p.shape.tpt, sq.n - i * 2 * p.shape.tpt);
+                        it.pos0 = sq.L + i * 2 * p.shape.tpt;
+                        it.kt0 = first_tile(p.shape, it.pos0) + c.a;
+                        it.n = c.z - c.a;
+                        it.single = sq.items == 1;
+                        it.c_first = c.c_first;
+                        it.nc = c.nc;
+                        it.ci = blockIdx.x - c.c_first;
+                        const int slot = k % kItems;
+                        if (!warp_wait_bounded(&sh->item_empty[slot], ((k / kItems) & 1) ^ 1) ||
+                            __shfl_sync(0xffffffffu, *abort_flag, 0)) {
+                            ok = false;
+                            break;
+                        }
+                        if (lane == 0) {
+                            sh->items[slot] = it;
+                            mbar_arrive(&sh->item_full[slot]);
+                        }
+                        ++k;
+                        const int tiles = it.ntok > p.shape.tpt ? 2 : 1;
+                        for (int q = 0; q < tiles; ++q, ++qpos) {
+                            const int qb = qpos & 1;
+                            if (!warp_wait_bounded(&sh->q_empty[qb], ((qpos >> 1) & 1) ^ 1)) {
+                                ok = false;
+                                break;
+                            }
+                            if (lane == 0) {
+                                // a single token needs one token's box, the rest of the tile may hold anything
+                                const bool one = it.ntok - q * p.shape.tpt == 1;
+                                const CUtensorMap *map = one ? &tmq1 : &tmq;
+                                uint8_t *qd = qbuf + qb * kTile;
+                                mbar_arrive_expect_tx(&sh->q_full[qb],
+                                                      (uint32_t)(kHalves * 128 * p.G * (one ? 1 : p.shape.tpt)));
+                                for (int hf = 0; hf < kHalves; ++hf)
+                                    tma_load_3d(qd + hf * kBox, map, hf * 64, h * p.G, it.row0 + q * p.shape.tpt,
+                                                &sh->q_full[qb]);
+                            }
+                            __syncwarp();
+                        }
+                        if (!ok) break;
+                    }
+                ub += per_head * p.Hkv;
+                ++b;
+            }
+            if (!ok) fail(b < p.B ? b : 0);
+            // the end of the list
+            const int slot = k % kItems;
+            if (warp_wait_bounded(&sh->item_empty[slot], ((k / kItems) & 1) ^ 1) && lane == 0) {
+                sh->items[slot].b = -1;
+                mbar_arrive(&sh->item_full[slot]);
+            }
+            for (uint32_t q = qpos > 2 ? qpos - 2 : 0; q < qpos; ++q)
+                warp_wait_bounded(&sh->q_full[q & 1], (q >> 1) & 1);
+        } else if (p.seq_status) {
+            // ===================== seq_status: lengths, and the ids of the pages that rows see
+            for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+                const int L = p.prefix_lens[b], r0 = p.row_starts[b], r1 = p.row_starts[b + 1];
+                const Seq s = seq_of(p.shape, L, r0, r1);
+                bool bad = !lengths_ok(p.shape, L, r0, r1);
+                if (s.n > 0) {
+                    const int lo = p.shape.window > 0 ? max(0, L - p.shape.window + 1) : 0;
+                    const int32_t *trow = p.block_table + (size_t)b * p.max_pages;
+                    for (int j = lo / p.page_size + lane; j <= (L + s.n - 1) / p.page_size; j += 32) {
+                        const int pg = trow[j];
+                        if (pg < 0 || pg >= p.num_pages) bad = true;
+                    }
+                }
+                bad = __any_sync(0xffffffffu, bad);
+                if (lane == 0 && !*abort_flag) p.seq_status[b] = bad ? SV_ERR_BAD_INPUT : SV_OK;
+            }
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc::fence_after();
+        tc::tmem_dealloc(tbase, kCols);
+    }
+}
+
+const void *kernel_fn(int D) {
+    return D == 128 ? reinterpret_cast<const void *>(&chunk_attention_kernel<128>)
+                    : reinterpret_cast<const void *>(&chunk_attention_kernel<64>);
+}
+
+static_assert((kStagesOf<128> + 2) * kTileBytes<128> + sizeof(Shared) <= 227 * 1024, "shared memory");
+
+int smem_bytes(int D) { return (D == 128 ? (kStagesOf<128> + 2) * kTileBytes<128> : (kStagesOf<64> + 2) * kTileBytes<64>) + (int)sizeof(Shared); }
+
+}  // namespace chunk
+}  // namespace sv

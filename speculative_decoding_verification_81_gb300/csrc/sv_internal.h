@@ -262,6 +262,34 @@ struct AppendArgs {
     int rows_per_cta;  // set at launch
 };
 
+// ---------------------------------------------------------------- chunk attention (sv_chunk.cu)
+
+struct ChunkPlan {
+    int grid;
+    size_t off_counters, off_part_ml, off_part_o, bytes;
+};
+
+struct ChunkArgs {
+    const void *q;
+    long long q_stride;  // elements between rows
+    const void *k_pages;
+    const void *v_pages;
+    const int32_t *block_table;
+    int max_pages, num_pages, page_size;
+    const int32_t *prefix_lens;
+    const int32_t *row_starts;
+    int B, num_rows, Hq, Hkv, D;
+    float scale;
+    int window;
+    void *out;
+    float *lse;
+    int32_t *seq_status;
+};
+
+sv_status plan_chunk(int Hq, int Hkv, int D, ChunkPlan *plan);
+sv_status launch_chunk_attention(const ChunkArgs &args, const ChunkPlan &plan, void *ws,
+                                 cudaStream_t stream);
+
 sv_status launch_build_tables(const BuildTablesArgs &args, cudaStream_t stream);
 sv_status launch_release_pages(const ReleasePagesArgs &args, cudaStream_t stream);
 sv_status launch_append_kv(const AppendArgs &args, int dtype, cudaStream_t stream);
