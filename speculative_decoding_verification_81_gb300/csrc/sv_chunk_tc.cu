@@ -48,6 +48,47 @@ __device__ __forceinline__ uint32_t sw128(int row, int c) {
     return (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4));
 }
 
+// 1 in one lane of the (converged) warp, 0 in the others.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+
+// A value that is the same in every lane, as one the compiler knows to be.
+__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
+
+// The products and the commit of tc::, run by a whole warp and issued by its
+// lane with leader = 1.
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t leader, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(leader)
+        : "memory");
+}
+
 // 16 bytes from 8 floats.
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
@@ -540,91 +581,97 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t q = pos > (uint32_t)kStages ? pos - kStages : 0; q < pos; ++q)
                 warp_wait_bounded(&sh->full[q % kStages], (q / kStages) & 1);
         } else if (warp == 9) {
-            // ===================== the products, issued by one lane in step order
-            if (lane == 0) {
-                constexpr uint32_t idS = tc::idesc_bf16(kRows, kBK, false);
-                constexpr uint32_t idPV = tc::idesc_bf16(kRows, D, true);
-                struct Pending {
-                    uint32_t ring;  // its V tile
-                    bool live, first, last, frees;
-                } pend[2] = {};
-                uint32_t p_ph[2] = {0, 0}, o_ph[2] = {1, 1};
-                uint32_t g = 0, ring = 0, qpos = 0;
-                bool ok = true;
-                int b_now = 0;
-                auto issue_pv = [&](int s) -> bool {
-                    const Pending q = pend[s];
-                    pend[s].live = false;
-                    if (!mbar_wait_bounded(&sh->p_full[s], p_ph[s])) return false;
-                    p_ph[s] ^= 1;
-                    const int st = q.ring % kStages;
-                    if (!mbar_wait_bounded(&sh->full[st], (q.ring / kStages) & 1)) return false;
-                    if (q.first) {
-                        if (!mbar_wait_bounded(&sh->o_empty[s], o_ph[s])) return false;
-                        o_ph[s] ^= 1;
-                    }
-                    tc::fence_after();
-                    // V rows 16kk.. start 2048 bytes apart (descriptor units of 16 bytes)
-                    const uint64_t dv = tc::smem_desc(base_u32 + st * kTile, kBox, 1024);
-                    const uint32_t pcol = tbase + kColS + s * kBK;
-#pragma unroll
-                    for (int kk = 0; kk < kBK / 16; ++kk)
-                        tc::mma_bf16_ts(tbase + kColO + s * 128, pcol + kk * 8, dv + (uint64_t)(kk * (2048 >> 4)),
-                                        idPV, (kk > 0 || !q.first) ? 1u : 0u);
-                    if (q.frees) tc::commit(&sh->empty[st]);
-                    if (q.last) tc::commit(&sh->o_full[s]);
-                    return true;
-                };
-                for (uint32_t k = 0; ok; ++k) {
-                    const int slot = k % kItems;
-                    if (!(ok = mbar_wait_bounded(&sh->item_full[slot], (k / kItems) & 1))) break;
-                    const Item it = sh->items[slot];
-                    mbar_arrive(&sh->item_empty[slot]);
-                    if (it.b < 0) break;
-                    b_now = it.b;
-                    const bool two = it.ntok > p.shape.tpt;
-                    const int steps = two ? 2 * it.n : it.n;
-                    for (int i = 0; i < steps; ++i, ++g) {
-                        const int s = g & 1;
-                        if (pend[s].live && !(ok = issue_pv(s))) break;
-                        const int j = two ? i >> 1 : i, qt = two ? i & 1 : 0;
-                        const uint32_t qp = qpos + qt, rk = ring + 2 * j;
-                        if (j == 0) ok = mbar_wait_bounded(&sh->q_full[qp & 1], (qp >> 1) & 1);
-                        const int st = rk % kStages;
-                        if (ok) ok = mbar_wait_bounded(&sh->full[st], (rk / kStages) & 1);
-                        if (!ok || *abort_flag) {
-                            ok = false;
-                            break;
-                        }
-                        tc::fence_after();
-                        const uint64_t dk = tc::smem_desc(base_u32 + st * kTile, 16, 1024);
-                        const uint64_t dq = tc::smem_desc(q_u32 + (qp & 1) * kTile, 16, 1024);
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint64_t o = (uint64_t)((kk >> 2) * (kBox >> 4) + (kk & 3) * 2);
-                            tc::mma_bf16(tbase + kColS + s * kBK, dq + o, dk + o, idS, kk > 0 ? 1u : 0u);
-                        }
-                        tc::commit(&sh->s_full[s]);
-                        const bool frees = !two || qt == 1;  // the tile's last reader
-                        if (frees) tc::commit(&sh->empty[st]);
-                        if (j == it.n - 1) tc::commit(&sh->q_empty[qp & 1]);
-                        pend[s].ring = rk + 1;
-                        pend[s].live = true;
-                        pend[s].first = two ? j == 0 : i < 2;
-                        pend[s].last = two ? j == it.n - 1 : i >= steps - 2;
-                        pend[s].frees = frees;
-                    }
-                    ring += 2 * it.n;
-                    qpos += two ? 2 : 1;
+            // ===================== the products, in step order.  The whole warp runs the
+            // loop with values that are the same in every lane (the item's by a
+            // warp-wide maximum, the waits' by a vote), and one elected lane's
+            // predicate issues: a loop that only lane 0 ran made the compiler move
+            // every operand of every product to the uniform registers anew, and the
+            // issue, ~88 cycles a product against the tensor core's 64, set the pace
+            // (a chunk of 4096 rows after 28672 slots: 1924 us).
+            constexpr uint32_t idS = tc::idesc_bf16(kRows, kBK, false);
+            constexpr uint32_t idPV = tc::idesc_bf16(kRows, D, true);
+            const uint32_t leader = elect_one();
+            const uint64_t desc_k = tc::smem_desc(base_u32, 16, 1024), desc_v = tc::smem_desc(base_u32, kBox, 1024);
+            const uint64_t desc_q = tc::smem_desc(q_u32, 16, 1024);
+            // a step whose PV product is still to be issued: its V tile's stage, and flags
+            constexpr uint32_t kLive = 16, kPhase = 32, kFirst = 64, kLast = 128, kFrees = 256;
+            uint32_t before2 = 0, before1 = 0;  // steps g - 2 and g - 1
+            uint32_t p_ph = 0, o_ph = 3;        // a bit a stream
+            uint32_t g = 0, qpos = 0;
+            uint32_t st = 0, st_ph = 0;         // ring stage of the K tile at hand
+            bool ok = true;
+            int b_now = 0;
+            auto issue_pv = [&](uint32_t s, uint32_t q) -> bool {
+                if (!warp_wait_bounded(&sh->p_full[s], (p_ph >> s) & 1)) return false;
+                p_ph ^= 1u << s;
+                const uint32_t vs = q & 15;
+                if (!warp_wait_bounded(&sh->full[vs], q & kPhase ? 1 : 0)) return false;
+                if (q & kFirst) {
+                    if (!warp_wait_bounded(&sh->o_empty[s], (o_ph >> s) & 1)) return false;
+                    o_ph ^= 1u << s;
                 }
-                if (ok && pend[g & 1].live) ok = issue_pv(g & 1);
-                if (ok && pend[(g & 1) ^ 1].live) ok = issue_pv((g & 1) ^ 1);
-                if (!ok) fail(b_now);
-                // every product issued is complete before the tensor memory is given back
-                tc::commit(&sh->fin);
-                mbar_wait_bounded(&sh->fin, 0);
+                tc::fence_after();
+                // V rows 16kk.. start 2048 bytes apart (descriptor units of 16 bytes)
+                const uint64_t dv = desc_v + (uint64_t)(vs * (kTile >> 4));
+                const uint32_t pcol = tbase + kColS + s * kBK, ocol = tbase + kColO + s * 128;
+#pragma unroll
+                for (int kk = 0; kk < kBK / 16; ++kk)
+                    mma_ts(leader, ocol, pcol + kk * 8, dv + (uint64_t)(kk * (2048 >> 4)), idPV,
+                           kk > 0 ? 1u : (q & kFirst ? 0u : 1u));
+                if (q & kFrees) commit(leader, &sh->empty[vs]);
+                if (q & kLast) commit(leader, &sh->o_full[s]);
+                return true;
+            };
+            for (uint32_t k = 0; ok; ++k) {
+                const int slot = k % kItems;
+                if (!(ok = warp_wait_bounded(&sh->item_full[slot], (k / kItems) & 1))) break;
+                const int b = uniform(sh->items[slot].b), n = uniform(sh->items[slot].n);
+                const bool two = uniform(sh->items[slot].ntok) > p.shape.tpt;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->item_empty[slot]);
+                if (b < 0) break;
+                b_now = b;
+                const int steps = two ? 2 * n : n;
+                for (int i = 0; i < steps; ++i, ++g) {
+                    const uint32_t s = g & 1;
+                    if (before2 && !(ok = issue_pv(s, before2))) break;
+                    const bool second = two && (i & 1);  // of an item of two Q tiles: the second tile's step
+                    const uint32_t qp = qpos + (second ? 1 : 0);
+                    if (i == 0 || (two && i == 1)) ok = warp_wait_bounded(&sh->q_full[qp & 1], (qp >> 1) & 1);
+                    if (ok && !second) ok = warp_wait_bounded(&sh->full[st], st_ph);
+                    if (!ok) break;
+                    tc::fence_after();
+                    const uint64_t dk = desc_k + (uint64_t)(st * (kTile >> 4));
+                    const uint64_t dq = desc_q + (uint64_t)((qp & 1) * (kTile >> 4));
+                    const uint32_t scol = tbase + kColS + s * kBK;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t o = (uint64_t)((kk >> 2) * (kBox >> 4) + (kk & 3) * 2);
+                        mma_ss(leader, scol, dq + o, dk + o, idS, kk > 0 ? 1u : 0u);
+                    }
+                    commit(leader, &sh->s_full[s]);
+                    const bool frees = !two || second;  // the tile's last reader
+                    if (frees) commit(leader, &sh->empty[st]);
+                    const bool last_tile = i >= steps - (two ? 2 : 1);
+                    if (last_tile) commit(leader, &sh->q_empty[qp & 1]);
+                    const uint32_t vs = st + 1 == kStages ? 0 : st + 1;
+                    const uint32_t v_ph = st + 1 == kStages ? st_ph ^ 1 : st_ph;
+                    before2 = before1;
+                    before1 = vs | kLive | (v_ph ? kPhase : 0u) | (i < 2 ? kFirst : 0u) |
+                              (i >= steps - 2 ? kLast : 0u) | (frees ? kFrees : 0u);
+                    if (frees) {  // on to the next tile: K and V took a stage each
+                        st = vs + 1 == kStages ? 0 : vs + 1;
+                        st_ph = vs + 1 == kStages ? v_ph ^ 1 : v_ph;
+                    }
+                }
+                qpos += two ? 2 : 1;
             }
-            __syncwarp();
+            if (ok && before2) ok = issue_pv(g & 1, before2);
+            if (ok && before1) ok = issue_pv((g & 1) ^ 1, before1);
+            if (!ok && lane == 0) fail(b_now);
+            // every product issued is complete before the tensor memory is given back
+            commit(leader, &sh->fin);
+            warp_wait_bounded(&sh->fin, 0);
         } else if (warp == 10) {
             // ===================== the work list: items of this CTA's units, and their Q tiles
             const long long U = sh->U;
