@@ -16,7 +16,7 @@ constexpr int kThreads = 32 * 12;
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;  // 256 x 208 + 128 x 88 = 384 x 168
 constexpr int kLaunchRegs = 168;
 constexpr int kItems = 4;                // items published ahead
-constexpr int kMinUnits = 4;             // units a CTA takes at least
+constexpr int kWarpPlanB = 32;           // sequences up to which one warp plans alone
 constexpr int kNone = INT32_MIN;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units the maximum grows before O is rescaled
@@ -27,7 +27,7 @@ constexpr uint32_t kCols = 512, kColS = 0, kColO = 256;
 template <int D>
 constexpr int kTileBytes = kBK * D * 2;
 template <int D>
-constexpr int kStagesOf = D == 128 ? 5 : 8;  // K and V tiles in flight
+constexpr int kStagesOf = D == 128 ? 5 : 12;  // K and V tiles in flight
 
 struct Params {
     uint16_t *out;
@@ -58,7 +58,7 @@ struct Item {
 };
 
 struct Shared {
-    uint64_t full[8], empty[8];        // K/V ring
+    uint64_t full[12], empty[12];      // K/V ring
     uint64_t q_full[2], q_empty[2];    // Q tiles
     uint64_t s_full[2], p_full[2];     // per stream: S ready; P ready
     uint64_t o_full[2], o_empty[2];    // per stream: O complete; O read
@@ -68,6 +68,7 @@ struct Shared {
     float2 xml[2][kRows];              // a stream's (m, sum) of a one-tile item
     Item items[kItems];
     long long warp_units[kThreads / 32];
+    int warp_items[kThreads / 32], warp_most[kThreads / 32];
     long long U, ub_start;
     int nctas, b_start;
     uint32_t tmem;

@@ -31,10 +31,10 @@
 // lengths; an item cut by a range's end leaves partials in the workspace,
 // merged by the warp that arrives last, in index order.
 //
-// Warps: 0-3 and 4-7 softmax of streams 0 and 1 (one thread a row); 8 loads K
-// and V tiles by TMA through the page table; 9 issues the products; 10 walks
-// the work list, publishes the items and loads Q; 11 checks the page table
-// and writes seq_status.  Every wait is bounded.
+// Warps: 0-3 and 4-7 softmax of streams 0 and 1 (one thread a row); 8 and 11
+// load K and V tiles by TMA through the page table; 9 issues the products; 10
+// walks the work list, publishes the items, loads Q and at the end checks the
+// page table and writes seq_status.  Every wait is bounded.
 #include <type_traits>
 
 #include "sv_chunk.cuh"
@@ -46,6 +46,26 @@ namespace chunk {
 
 __device__ __forceinline__ uint32_t sw128(int row, int c) {
     return (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4));
+}
+
+// A sequence's items and units, of one KV head.
+struct Units {
+    int items, most;  // most: units of its largest item
+    long long per_head;
+};
+
+__device__ __forceinline__ Units units_of(const Params &p, int L, int r0, int r1) {
+    const Seq s = seq_of(p.shape, L, r0, r1);
+    Units u{s.items, 0, 0};
+    if (s.items == 1) {
+        u.most = item_tiles(p.shape, s, 0) + kItemCost;
+        u.per_head = u.most;
+    } else if (s.items > 1) {
+        // (the last item sees the most slots; a window may leave the one before it a tile more)
+        u.most = max(item_tiles(p.shape, s, s.items - 1), item_tiles(p.shape, s, s.items - 2)) + kItemCost;
+        u.per_head = units_before(p.shape, s, s.items);
+    }
+    return u;
 }
 
 // 1 in one lane of the (converged) warp, 0 in the others.
@@ -132,54 +152,56 @@ __device__ __forceinline__ float2 *part_ml(const Params &p, int cta, int slot, i
     return reinterpret_cast<float2 *>(p.part_ml) + ((size_t)(cta * 2 + slot) * 2 + qt) * kRows;
 }
 
-// The nc partials of this warp's rows (row0 .. row0 + nv - 1 of Q tile qt;
-// out_off and lse_off: lane r's row in `out` and `lse`) merged in index order
-// and written out.
+// The nc partials of this warp's rows (row0 .. row0 + nv - 1 of Q tile qt)
+// merged in index order and written out.  A lane takes 8 columns of a row at
+// a time and passes over the parts once with a running maximum; kept out of
+// line and short, since a call runs it once or twice and its instructions
+// come from L2.  out_off and lse_off: lane r's row in `out` and `lse`.
 template <int D>
-__device__ __noinline__ void merge_parts(const Params &p, const Item it, int qt, int row0, int nv,
-                                         int lane, long long out_off, long long lse_off) {
-    float M = kNegInf, l = 0.f;
-    if (lane < nv) {
-#pragma unroll 4
-        for (int i = 0; i < it.nc; ++i)
-            M = fmaxf(M, __ldcg(part_ml(p, it.c_first + i, i == 0, qt) + row0 + lane).x);
-#pragma unroll 4
-        for (int i = 0; i < it.nc; ++i) {
-            const float2 ml = __ldcg(part_ml(p, it.c_first + i, i == 0, qt) + row0 + lane);
-            l += ml.x == kNegInf ? 0.f : ml.y * ex2_approx(ml.x - M);
-        }
-        if (p.lse) p.lse[lse_off] = l > 0.f ? M * kLn2 + logf(l) : kNegInf;
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+__device__ __noinline__ void merge_parts(const float4 *part_o, const float2 *part_ml, uint16_t *out, float *lse,
+                                         int nc, int nv, int lane, long long out_off, long long lse_off) {
+    // from part to part: the first is in its CTA's slot 1, the others in their CTAs' slot 0
+    constexpr size_t kO = (size_t)2 * (D / 4) * kRows, kMl = 2 * kRows;  // a slot (two Q tiles)
     const int total = nv * (D / 8);
+#pragma unroll 1
     for (int idx0 = 0; idx0 < total; idx0 += 32) {
-        const int idx = idx0 + lane;
+        const int idx = min(idx0 + lane, total - 1);
         const int c8 = idx / nv, r = idx - c8 * nv;
-        const float Mr = __shfl_sync(0xffffffffu, M, r);
-        const float ir = __shfl_sync(0xffffffffu, inv, r);
         const long long off = __shfl_sync(0xffffffffu, out_off, r);
-        if (idx >= total) continue;
+        const long long loff = __shfl_sync(0xffffffffu, lse_off, r);
         float acc[8] = {};
-#pragma unroll 4
-        for (int i = 0; i < it.nc; ++i) {
-            const float2 ml = __ldcg(part_ml(p, it.c_first + i, i == 0, qt) + row0 + r);
-            const float4 *src = part_o<D>(p, it.c_first + i, i == 0, qt) + row0 + r;
-            const float4 x = __ldcg(src + (size_t)(2 * c8) * kRows);
-            const float4 y = __ldcg(src + (size_t)(2 * c8 + 1) * kRows);
-            // a partial without a visible slot has no O: select, never multiply, it
-            if (ml.x != kNegInf) {
-                const float w = ex2_approx(ml.x - Mr) * ir;
-                acc[0] = __fmaf_rn(x.x, w, acc[0]);
-                acc[1] = __fmaf_rn(x.y, w, acc[1]);
-                acc[2] = __fmaf_rn(x.z, w, acc[2]);
-                acc[3] = __fmaf_rn(x.w, w, acc[3]);
-                acc[4] = __fmaf_rn(y.x, w, acc[4]);
-                acc[5] = __fmaf_rn(y.y, w, acc[5]);
-                acc[6] = __fmaf_rn(y.z, w, acc[6]);
-                acc[7] = __fmaf_rn(y.w, w, acc[7]);
+        float M = kNegInf, l = 0.f;
+#pragma unroll 1
+        for (int i0 = 0; i0 < nc; i0 += 4) {
+            float2 ml[4];
+            float4 x[4], y[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = min(i0 + u, nc - 1), slot = 2 * i + (i == 0 ? 1 : 0);
+                ml[u] = __ldcg(part_ml + slot * kMl + r);
+                x[u] = __ldcg(part_o + slot * kO + (size_t)(2 * c8) * kRows + r);
+                y[u] = __ldcg(part_o + slot * kO + (size_t)(2 * c8 + 1) * kRows + r);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                // (a part without a visible slot has no O: select, never multiply, it)
+                if (i0 + u >= nc || ml[u].x == kNegInf) continue;
+                const float Mn = fmaxf(M, ml[u].x);
+                const float f = M == kNegInf ? 0.f : ex2_approx(M - Mn), w = ex2_approx(ml[u].x - Mn);
+                M = Mn;
+                l = l * f + ml[u].y * w;
+                const float o[8] = {x[u].x, x[u].y, x[u].z, x[u].w, y[u].x, y[u].y, y[u].z, y[u].w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] = __fmaf_rn(o[e], w, acc[e] * f);
             }
         }
-        *reinterpret_cast<uint4 *>(p.out + off + 8 * c8) = pack8(acc);
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] *= inv;
+        if (idx0 + lane < total) {
+            *reinterpret_cast<uint4 *>(out + off + 8 * c8) = pack8(acc);
+            if (lse && c8 == 0) lse[loff] = l > 0.f ? M * kLn2 + logf(l) : kNegInf;
+        }
     }
 }
 
@@ -218,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&sh->item_full[i], 1);
-            mbar_init(&sh->item_empty[i], 10);  // softmax warps, K/V loader, issuer
+            mbar_init(&sh->item_empty[i], 11);  // softmax warps, loaders, issuer
         }
         mbar_init(&sh->fin, 1);
         sh->abort_flag = 0;
@@ -242,14 +264,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
 
-    // ---- every CTA: units of all sequences, its own range, the sequence it starts in
-    {
+    tc::fence_before();  // (the barriers and the tensor memory's address)
+    __syncthreads();
+    tc::fence_after();
+    // ---- many sequences: every CTA sums the units of all, finds its own range
+    // and the sequence it starts in (up to 32, the walking warp does it alone)
+    if (p.B > kWarpPlanB) {
         const int per = (p.B + kThreads - 1) / kThreads;
         const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
         long long mine = 0;
+        int items = 0, most = 0;
         for (int b = b0; b < b1; ++b) {
-            const Seq s = seq_of(p.shape, p.prefix_lens[b], p.row_starts[b], p.row_starts[b + 1]);
-            mine += units_before(p.shape, s, s.items) * p.Hkv;
+            const Units u = units_of(p, p.prefix_lens[b], p.row_starts[b], p.row_starts[b + 1]);
+            mine += u.per_head * p.Hkv;
+            items += u.items * p.Hkv;
+            most = max(most, u.most);
         }
         long long x = mine;
 #pragma unroll
@@ -257,19 +286,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             const long long y = __shfl_up_sync(0xffffffffu, x, off);
             if (lane >= off) x += y;
         }
-        if (lane == 31) sh->warp_units[warp] = x;
-        tc::fence_before();  // (the tensor memory's address, below)
+        items = __reduce_add_sync(0xffffffffu, items);
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 31) {
+            sh->warp_units[warp] = x;
+            sh->warp_items[warp] = items;
+            sh->warp_most[warp] = most;
+        }
         __syncthreads();
-        tc::fence_after();
-        long long before = x - mine, U = 0;
+        long long before = x - mine, U = 0, all_items = 0;
         for (int w = 0; w < kThreads / 32; ++w) {
             const long long v = sh->warp_units[w];
             if (w < warp) before += v;
             U += v;
+            all_items += sh->warp_items[w];
+            most = max(most, sh->warp_most[w]);
         }
-        const long long want = U / kMinUnits > 0 ? U / kMinUnits : 1;
-        const int nctas = (int)(want < (long long)gridDim.x ? want : (long long)gridDim.x);
-        const long long u0 = blockIdx.x < nctas ? cta_begin(U, nctas, blockIdx.x) : U;
+        const int nctas = ctas_for(U, all_items, most, gridDim.x);
+        const long long u0 = (int)blockIdx.x < nctas ? cta_begin(U, nctas, blockIdx.x) : U;
         if (tid == 0) {
             sh->U = U;
             sh->nctas = nctas;
@@ -279,10 +313,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             int b = b0;
             long long ub = before;
             for (; b < b1; ++b) {
-                const Seq s = seq_of(p.shape, p.prefix_lens[b], p.row_starts[b], p.row_starts[b + 1]);
-                const long long u = units_before(p.shape, s, s.items) * p.Hkv;
-                if (u0 < ub + u) break;
-                ub += u;
+                const Units u = units_of(p, p.prefix_lens[b], p.row_starts[b], p.row_starts[b + 1]);
+                if (u0 < ub + u.per_head * p.Hkv) break;
+                ub += u.per_head * p.Hkv;
             }
             sh->b_start = b;
             sh->ub_start = ub;
@@ -459,8 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (valid && whole && p.lse) p.lse[lse_off] = lt > 0.f ? M * kLn2 + logf(lt) : kNegInf;
                     if (valid && !whole)
                         __stcg(part_ml(p, blockIdx.x, pslot, qt) + r, make_float2(M, lt));
-#pragma unroll
-                    for (int h = 0; h < D / 32; ++h) {
+#pragma unroll 1
+                    for (int h = 0; h < D / 32; ++h) {  // (short code: most of its time is instruction fetch)
                         uint32_t ov[32];
                         float acc[32];
                         __syncwarp();
@@ -510,7 +543,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (last) *ctr = 0;  // all have arrived: ready for the next call
                     }
                     if (__shfl_sync(0xffffffffu, last, 0))
-                        merge_parts<D>(p, it, qt, quarter * 32, min(32, rows - quarter * 32), lane, out_off, lse_off);
+                        merge_parts<D>(part_o<D>(p, it.c_first, 0, qt) + quarter * 32,
+                                       part_ml(p, it.c_first, 0, qt) + quarter * 32, p.out, p.lse, it.nc,
+                                       min(32, rows - quarter * 32), lane, out_off, lse_off);
                 }
             }
             __syncwarp();
@@ -520,15 +555,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (warp == 8) {
-            // ===================== K and V tiles: lane (half, page of the tile)
+        if (warp == 8 || warp == 11) {
+            // ===================== K tiles (warp 8: the even ring positions) and V tiles
+            // (warp 11: the odd ones): lane (half, page of the tile)
+            const int kv = warp == 11;
+            const CUtensorMap *map = kv ? &tmv : &tmk;
             const int ps = p.page_size;
             const int sub = ps < kBK ? ps : kBK;          // rows of a box
             const int npg = kBK / sub;                    // boxes a tile and half
             const int pg_l = lane & 15, half = lane >> 4;
             const bool lane_on = pg_l < npg && half < kHalves;
             const uint64_t once = l2_policy_evict_first();
-            uint32_t pos = 0;
+            uint32_t pos = kv;
             bool ok = true;
             for (uint32_t k = 0; ok; ++k) {
                 const int slot = k % kItems;
@@ -554,32 +592,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < it.n && ok; ++j) {
                     const int y_next = j + 1 < it.n ? box_row(j + 1) : kNone;
                     const int boxes = __popc(__ballot_sync(0xffffffffu, y != kNone));
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv, ++pos) {
-                        const int st = pos % kStages;
-                        if (!warp_wait_bounded(&sh->empty[st], ((pos / kStages) & 1) ^ 1)) {
-                            fail(it.b);
-                            ok = false;
-                            break;
-                        }
-                        if (__shfl_sync(0xffffffffu, *abort_flag, 0)) {
-                            ok = false;
-                            break;
-                        }
-                        if (lane == 0) mbar_arrive_expect_tx(&sh->full[st], (uint32_t)(boxes * sub * 128));
-                        __syncwarp();
-                        if (y != kNone) {
-                            uint8_t *dst = smem + st * kTile + half * kBox + pg_l * sub * 128;
-                            if (it.single) tma_load_2d_hint(dst, kv ? &tmv : &tmk, half * 64, y, &sh->full[st], once);
-                            else tma_load_2d(dst, kv ? &tmv : &tmk, half * 64, y, &sh->full[st]);
-                        }
+                    const int st = pos % kStages;
+                    if (!warp_wait_bounded(&sh->empty[st], ((pos / kStages) & 1) ^ 1)) {
+                        fail(it.b);
+                        ok = false;
+                        break;
                     }
+                    if (__shfl_sync(0xffffffffu, *abort_flag, 0)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(&sh->full[st], (uint32_t)(boxes * sub * 128));
+                    __syncwarp();  // the expected bytes are set before any box lands
+                    if (y != kNone) {
+                        uint8_t *dst = smem + st * kTile + half * kBox + pg_l * sub * 128;
+                        if (it.single) tma_load_2d_hint(dst, map, half * 64, y, &sh->full[st], once);
+                        else tma_load_2d(dst, map, half * 64, y, &sh->full[st]);
+                    }
+                    pos += 2;
                     y = y_next;
                 }
             }
-            // every copy issued must land before the CTA may exit
-            for (uint32_t q = pos > (uint32_t)kStages ? pos - kStages : 0; q < pos; ++q)
-                warp_wait_bounded(&sh->full[q % kStages], (q / kStages) & 1);
+            // every copy issued must land before the CTA may exit: the products have
+            // waited for all of them, unless a wait gave up
+            if (__shfl_sync(0xffffffffu, *abort_flag, 0))
+                for (uint32_t q = pos > kStages ? pos - kStages : kv; q < pos; ++q)
+                    if ((q & 1) == (uint32_t)kv) warp_wait_bounded(&sh->full[q % kStages], (q / kStages) & 1);
         } else if (warp == 9) {
             // ===================== the products, in step order.  The whole warp runs the
             // loop with values that are the same in every lane (the item's by a
@@ -674,35 +712,60 @@ __global__ void __launch_bounds__(kThreads, 1)
             warp_wait_bounded(&sh->fin, 0);
         } else if (warp == 10) {
             // ===================== the work list: items of this CTA's units, and their Q tiles
-            const long long U = sh->U;
-            const int nctas = sh->nctas;
-            const bool has = (int)blockIdx.x < nctas && sh->b_start < p.B;
-            const long long u0 = has ? cta_begin(U, nctas, blockIdx.x) : 0;
-            const long long u1 = has ? cta_begin(U, nctas, blockIdx.x + 1) : 0;
+            long long U, u0, u1, ub;  // ub: first unit of sequence b
+            int nctas, b;
+            int pre = 0, r0 = 0, r1 = 0;       // lane: lengths of sequence cached + lane
+            Units un{0, 0, 0};                 // and its units
+            int cached = -1;
+            auto load = [&](int first) {
+                cached = first;
+                un = Units{0, 0, 0};
+                if (first + lane < p.B) {
+                    pre = p.prefix_lens[first + lane];
+                    r0 = p.row_starts[first + lane];
+                    r1 = p.row_starts[first + lane + 1];
+                    un = units_of(p, pre, r0, r1);
+                }
+            };
+            if (p.B > kWarpPlanB) {
+                U = sh->U;
+                nctas = sh->nctas;
+                b = (int)blockIdx.x < nctas ? sh->b_start : p.B;
+                ub = sh->ub_start;
+            } else {
+                load(0);
+                const long long mine = un.per_head * p.Hkv;
+                long long x = mine;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const long long y = __shfl_up_sync(0xffffffffu, x, off);
+                    if (lane >= off) x += y;
+                }
+                U = __shfl_sync(0xffffffffu, x, 31);
+                nctas = ctas_for(U, (long long)__reduce_add_sync(0xffffffffu, un.items) * p.Hkv,
+                                 __reduce_max_sync(0xffffffffu, un.most), gridDim.x);
+                const long long first = (int)blockIdx.x < nctas ? cta_begin(U, nctas, blockIdx.x) : U;
+                const uint32_t here = __ballot_sync(0xffffffffu, first < x);  // (x only grows)
+                b = here ? __ffs(here) - 1 : p.B;
+                ub = __shfl_sync(0xffffffffu, x - mine, b & 31);
+            }
+            u0 = b < p.B ? cta_begin(U, nctas, blockIdx.x) : 0;
+            u1 = b < p.B ? cta_begin(U, nctas, blockIdx.x + 1) : 0;
             uint32_t k = 0, qpos = 0;
             bool ok = true;
-            int b = has ? sh->b_start : p.B;
-            long long ub = has ? sh->ub_start : 0;  // first unit of sequence b
-            int pre = 0, r0 = 0, r1 = 0, cached = -1;  // lane: lengths of sequence cached + lane
             while (ok && b < p.B && ub < u1) {
-                if (cached < 0 || b >= cached + 32) {
-                    cached = b;
-                    const int bl = min(b + lane, p.B - 1);
-                    pre = p.prefix_lens[bl];
-                    r0 = p.row_starts[bl];
-                    r1 = p.row_starts[bl + 1];
-                }
-                const Seq sq = seq_of(p.shape, __shfl_sync(0xffffffffu, pre, b - cached), __shfl_sync(0xffffffffu, r0, b - cached),
-                                      __shfl_sync(0xffffffffu, r1, b - cached));
+                if (cached < 0 || b >= cached + 32) load(b);
+                const Seq sq = seq_of(p.shape, __shfl_sync(0xffffffffu, pre, b - cached),
+                                      __shfl_sync(0xffffffffu, r0, b - cached), __shfl_sync(0xffffffffu, r1, b - cached));
+                const long long per_head = __shfl_sync(0xffffffffu, un.per_head, b - cached);
                 if (sq.items == 0) {
                     ++b;
                     continue;
                 }
-                const long long per_head = units_before(p.shape, sq, sq.items);
                 int h = 0, i = 0;
                 long long ui = ub;  // first unit of item (h, i)
                 if (u0 > ub) {      // the range starts inside this sequence
-                    h = (int)((u0 - ub) / per_head);
+                    h = (int)quot(u0 - ub, per_head);
                     const long long v = (u0 - ub) - (long long)h * per_head;
                     // the last item whose first unit is at most v: 32 candidates at a time
                     int lo = 0, span = sq.items;
@@ -778,25 +841,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sh->items[slot].b = -1;
                 mbar_arrive(&sh->item_full[slot]);
             }
-            for (uint32_t q = qpos > 2 ? qpos - 2 : 0; q < qpos; ++q)
-                warp_wait_bounded(&sh->q_full[q & 1], (q >> 1) & 1);
-        } else if (p.seq_status) {
-            // ===================== seq_status: lengths, and the ids of the pages that rows see
-            for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-                const int L = p.prefix_lens[b], r0 = p.row_starts[b], r1 = p.row_starts[b + 1];
-                const Seq s = seq_of(p.shape, L, r0, r1);
-                bool bad = !lengths_ok(p.shape, L, r0, r1);
+            // seq_status: lengths, and the ids of the pages that rows see
+            for (int sb = p.seq_status ? (int)blockIdx.x : p.B; sb < p.B; sb += gridDim.x) {
+                const int L = p.prefix_lens[sb], first = p.row_starts[sb], end = p.row_starts[sb + 1];
+                const Seq s = seq_of(p.shape, L, first, end);
+                bool bad = !lengths_ok(p.shape, L, first, end);
                 if (s.n > 0) {
                     const int lo = p.shape.window > 0 ? max(0, L - p.shape.window + 1) : 0;
-                    const int32_t *trow = p.block_table + (size_t)b * p.max_pages;
+                    const int32_t *trow = p.block_table + (size_t)sb * p.max_pages;
                     for (int j = lo / p.page_size + lane; j <= (L + s.n - 1) / p.page_size; j += 32) {
                         const int pg = trow[j];
                         if (pg < 0 || pg >= p.num_pages) bad = true;
                     }
                 }
                 bad = __any_sync(0xffffffffu, bad);
-                if (lane == 0 && !*abort_flag) p.seq_status[b] = bad ? SV_ERR_BAD_INPUT : SV_OK;
+                if (lane == 0 && !*abort_flag) p.seq_status[sb] = bad ? SV_ERR_BAD_INPUT : SV_OK;
             }
+            for (uint32_t q = qpos > 2 ? qpos - 2 : 0; q < qpos; ++q)
+                warp_wait_bounded(&sh->q_full[q & 1], (q >> 1) & 1);
         }
     }
     tc::fence_before();
