@@ -68,6 +68,29 @@ __device__ __forceinline__ Units units_of(const Params &p, int L, int r0, int r1
     return u;
 }
 
+// Wait for the phase of `bar` with the given parity, by a whole warp with one
+// verdict for its lanes; false after kWaitCycles.  The first probe may suspend
+// and nearly always suffices; the counting is out of line, so that the loops
+// around the waits stay short.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity) {
+    const long long t0 = clock64();
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (__all_sync(0xffffffffu, ok != 0)) return true;
+        if (__any_sync(0xffffffffu, clock64() - t0 > kWaitCycles)) return false;
+    }
+}
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_long(smem_u32(bar), parity);
+}
+
 // 1 in one lane of the (converged) warp, 0 in the others.
 __device__ __forceinline__ uint32_t elect_one() {
     uint32_t r;
@@ -107,6 +130,28 @@ __device__ __forceinline__ void commit(uint32_t leader, uint64_t *bar) {
         "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
         "r"(leader)
         : "memory");
+}
+
+// Stream s's S = Q K^T, from the descriptors of its Q tile and the K tile.
+template <int D>
+__device__ __forceinline__ void s_products(uint32_t leader, uint32_t tbase, uint32_t s, uint64_t dq, uint64_t dk) {
+    constexpr uint32_t idesc = tc::idesc_bf16(kRows, kBK, false);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+        const uint64_t o = (uint64_t)((kk >> 2) * (kBox >> 4) + (kk & 3) * 2);
+        mma_ss(leader, tbase + kColS + s * kBK, dq + o, dk + o, idesc, kk > 0 ? 1u : 0u);
+    }
+}
+// Stream s's O += P V (O = P V where accumulate is 0); V rows 16kk.. start
+// 2048 bytes apart (descriptor units of 16 bytes).
+template <int D>
+__device__ __forceinline__ void pv_products(uint32_t leader, uint32_t tbase, uint32_t s, uint64_t dv,
+                                            uint32_t accumulate) {
+    constexpr uint32_t idesc = tc::idesc_bf16(kRows, D, true);
+#pragma unroll
+    for (int kk = 0; kk < kBK / 16; ++kk)
+        mma_ts(leader, tbase + kColO + s * 128, tbase + kColS + s * kBK + kk * 8,
+               dv + (uint64_t)(kk * (2048 >> 4)), idesc, kk > 0 ? 1u : accumulate);
 }
 
 // 16 bytes from 8 floats.
@@ -570,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (uint32_t k = 0; ok; ++k) {
                 const int slot = k % kItems;
-                if (!warp_wait_bounded(&sh->item_full[slot], (k / kItems) & 1)) {
+                if (!wait(&sh->item_full[slot], (k / kItems) & 1)) {
                     fail(0);
                     break;
                 }
@@ -593,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int y_next = j + 1 < it.n ? box_row(j + 1) : kNone;
                     const int boxes = __popc(__ballot_sync(0xffffffffu, y != kNone));
                     const int st = pos % kStages;
-                    if (!warp_wait_bounded(&sh->empty[st], ((pos / kStages) & 1) ^ 1)) {
+                    if (!wait(&sh->empty[st], ((pos / kStages) & 1) ^ 1)) {
                         fail(it.b);
                         ok = false;
                         break;
@@ -617,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // waited for all of them, unless a wait gave up
             if (__shfl_sync(0xffffffffu, *abort_flag, 0))
                 for (uint32_t q = pos > kStages ? pos - kStages : kv; q < pos; ++q)
-                    if ((q & 1) == (uint32_t)kv) warp_wait_bounded(&sh->full[q % kStages], (q / kStages) & 1);
+                    if ((q & 1) == (uint32_t)kv) wait(&sh->full[q % kStages], (q / kStages) & 1);
         } else if (warp == 9) {
             // ===================== the products, in step order.  The whole warp runs the
             // loop with values that are the same in every lane (the item's by a
@@ -626,8 +671,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             // every operand of every product to the uniform registers anew, and the
             // issue, ~88 cycles a product against the tensor core's 64, set the pace
             // (a chunk of 4096 rows after 28672 slots: 1924 us).
-            constexpr uint32_t idS = tc::idesc_bf16(kRows, kBK, false);
-            constexpr uint32_t idPV = tc::idesc_bf16(kRows, D, true);
             const uint32_t leader = elect_one();
             const uint64_t desc_k = tc::smem_desc(base_u32, 16, 1024), desc_v = tc::smem_desc(base_u32, kBox, 1024);
             const uint64_t desc_q = tc::smem_desc(q_u32, 16, 1024);
@@ -640,29 +683,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             int b_now = 0;
             auto issue_pv = [&](uint32_t s, uint32_t q) -> bool {
-                if (!warp_wait_bounded(&sh->p_full[s], (p_ph >> s) & 1)) return false;
+                if (!wait(&sh->p_full[s], (p_ph >> s) & 1)) return false;
                 p_ph ^= 1u << s;
-                const uint32_t vs = q & 15;
-                if (!warp_wait_bounded(&sh->full[vs], q & kPhase ? 1 : 0)) return false;
+                if (!wait(&sh->full[q & 15], q & kPhase ? 1 : 0)) return false;
                 if (q & kFirst) {
-                    if (!warp_wait_bounded(&sh->o_empty[s], (o_ph >> s) & 1)) return false;
+                    if (!wait(&sh->o_empty[s], (o_ph >> s) & 1)) return false;
                     o_ph ^= 1u << s;
                 }
+                const uint32_t vs = q & 15;
                 tc::fence_after();
-                // V rows 16kk.. start 2048 bytes apart (descriptor units of 16 bytes)
-                const uint64_t dv = desc_v + (uint64_t)(vs * (kTile >> 4));
-                const uint32_t pcol = tbase + kColS + s * kBK, ocol = tbase + kColO + s * 128;
-#pragma unroll
-                for (int kk = 0; kk < kBK / 16; ++kk)
-                    mma_ts(leader, ocol, pcol + kk * 8, dv + (uint64_t)(kk * (2048 >> 4)), idPV,
-                           kk > 0 ? 1u : (q & kFirst ? 0u : 1u));
+                pv_products<D>(leader, tbase, s, desc_v + (uint64_t)(vs * (kTile >> 4)), q & kFirst ? 0u : 1u);
                 if (q & kFrees) commit(leader, &sh->empty[vs]);
                 if (q & kLast) commit(leader, &sh->o_full[s]);
                 return true;
             };
             for (uint32_t k = 0; ok; ++k) {
                 const int slot = k % kItems;
-                if (!(ok = warp_wait_bounded(&sh->item_full[slot], (k / kItems) & 1))) break;
+                if (!(ok = wait(&sh->item_full[slot], (k / kItems) & 1))) break;
                 const int b = uniform(sh->items[slot].b), n = uniform(sh->items[slot].n);
                 const bool two = uniform(sh->items[slot].ntok) > p.shape.tpt;
                 __syncwarp();
@@ -671,22 +708,58 @@ __global__ void __launch_bounds__(kThreads, 1)
                 b_now = b;
                 const int steps = two ? 2 * n : n;
                 for (int i = 0; i < steps; ++i, ++g) {
+                    if (two && i == 4 && n > 2) {
+                        // An item of two Q tiles from its third K/V tile on: both
+                        // streams' steps of a tile, without the generic step's
+                        // bookkeeping (its instructions, fetched anew each time beside
+                        // the softmax warps' code, held the products up).
+                        const uint32_t sa = g & 1, sb = sa ^ 1;
+                        uint32_t vs = before1 & 15, v_ph = before1 & kPhase ? 1 : 0;  // V of the tile before
+                        const uint64_t qa = desc_q + (uint64_t)((qpos & 1) * (kTile >> 4));
+                        const uint64_t qb = desc_q + (uint64_t)(((qpos & 1) ^ 1) * (kTile >> 4));
+#pragma unroll 1
+                        for (int j = 2; j < n; ++j) {
+                            const uint64_t dk = desc_k + (uint64_t)(st * (kTile >> 4));
+                            const uint64_t dv = desc_v + (uint64_t)(vs * (kTile >> 4));
+                            if (!(ok = wait(&sh->full[st], st_ph))) break;
+                            if (!(ok = wait(&sh->full[vs], v_ph))) break;
+                            if (!(ok = wait(&sh->p_full[sa], (p_ph >> sa) & 1))) break;
+                            tc::fence_after();
+                            pv_products<D>(leader, tbase, sa, dv, 1u);
+                            s_products<D>(leader, tbase, sa, qa, dk);
+                            commit(leader, &sh->s_full[sa]);
+                            if (!(ok = wait(&sh->p_full[sb], (p_ph >> sb) & 1))) break;
+                            tc::fence_after();
+                            pv_products<D>(leader, tbase, sb, dv, 1u);
+                            commit(leader, &sh->empty[vs]);
+                            s_products<D>(leader, tbase, sb, qb, dk);
+                            commit(leader, &sh->s_full[sb]);
+                            commit(leader, &sh->empty[st]);
+                            p_ph ^= 3u;
+                            vs = st + 1 == kStages ? 0 : st + 1;
+                            v_ph = st + 1 == kStages ? st_ph ^ 1 : st_ph;
+                            st = vs + 1 == kStages ? 0 : vs + 1;
+                            st_ph = vs + 1 == kStages ? v_ph ^ 1 : v_ph;
+                        }
+                        if (!ok) break;
+                        commit(leader, &sh->q_empty[0]);
+                        commit(leader, &sh->q_empty[1]);
+                        before2 = vs | kLive | (v_ph ? kPhase : 0u) | kLast;
+                        before1 = vs | kLive | (v_ph ? kPhase : 0u) | kLast | kFrees;
+                        g += steps - 4;
+                        break;
+                    }
                     const uint32_t s = g & 1;
-                    if (before2 && !(ok = issue_pv(s, before2))) break;
                     const bool second = two && (i & 1);  // of an item of two Q tiles: the second tile's step
                     const uint32_t qp = qpos + (second ? 1 : 0);
-                    if (i == 0 || (two && i == 1)) ok = warp_wait_bounded(&sh->q_full[qp & 1], (qp >> 1) & 1);
-                    if (ok && !second) ok = warp_wait_bounded(&sh->full[st], st_ph);
+                    if (before2 && !(ok = issue_pv(s, before2))) break;
+                    if (i == 0 || (two && i == 1)) ok = wait(&sh->q_full[qp & 1], (qp >> 1) & 1);
+                    if (ok && !second) ok = wait(&sh->full[st], st_ph);
                     if (!ok) break;
                     tc::fence_after();
                     const uint64_t dk = desc_k + (uint64_t)(st * (kTile >> 4));
                     const uint64_t dq = desc_q + (uint64_t)((qp & 1) * (kTile >> 4));
-                    const uint32_t scol = tbase + kColS + s * kBK;
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint64_t o = (uint64_t)((kk >> 2) * (kBox >> 4) + (kk & 3) * 2);
-                        mma_ss(leader, scol, dq + o, dk + o, idS, kk > 0 ? 1u : 0u);
-                    }
+                    s_products<D>(leader, tbase, s, dq, dk);
                     commit(leader, &sh->s_full[s]);
                     const bool frees = !two || second;  // the tile's last reader
                     if (frees) commit(leader, &sh->empty[st]);
@@ -709,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok && lane == 0) fail(b_now);
             // every product issued is complete before the tensor memory is given back
             commit(leader, &sh->fin);
-            warp_wait_bounded(&sh->fin, 0);
+            wait(&sh->fin, 0);
         } else if (warp == 10) {
             // ===================== the work list: items of this CTA's units, and their Q tiles
             long long U, u0, u1, ub;  // ub: first unit of sequence b
@@ -799,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         it.nc = c.nc;
                         it.ci = blockIdx.x - c.c_first;
                         const int slot = k % kItems;
-                        if (!warp_wait_bounded(&sh->item_empty[slot], ((k / kItems) & 1) ^ 1) ||
+                        if (!wait(&sh->item_empty[slot], ((k / kItems) & 1) ^ 1) ||
                             __shfl_sync(0xffffffffu, *abort_flag, 0)) {
                             ok = false;
                             break;
@@ -812,7 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int tiles = it.ntok > p.shape.tpt ? 2 : 1;
                         for (int q = 0; q < tiles; ++q, ++qpos) {
                             const int qb = qpos & 1;
-                            if (!warp_wait_bounded(&sh->q_empty[qb], ((qpos >> 1) & 1) ^ 1)) {
+                            if (!wait(&sh->q_empty[qb], ((qpos >> 1) & 1) ^ 1)) {
                                 ok = false;
                                 break;
                             }
@@ -837,7 +910,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) fail(b < p.B ? b : 0);
             // the end of the list
             const int slot = k % kItems;
-            if (warp_wait_bounded(&sh->item_empty[slot], ((k / kItems) & 1) ^ 1) && lane == 0) {
+            if (wait(&sh->item_empty[slot], ((k / kItems) & 1) ^ 1) && lane == 0) {
                 sh->items[slot].b = -1;
                 mbar_arrive(&sh->item_full[slot]);
             }
@@ -858,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0 && !*abort_flag) p.seq_status[sb] = bad ? SV_ERR_BAD_INPUT : SV_OK;
             }
             for (uint32_t q = qpos > 2 ? qpos - 2 : 0; q < qpos; ++q)
-                warp_wait_bounded(&sh->q_full[q & 1], (q >> 1) & 1);
+                wait(&sh->q_full[q & 1], (q >> 1) & 1);
         }
     }
     tc::fence_before();
