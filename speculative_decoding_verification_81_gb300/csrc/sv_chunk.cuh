@@ -13,7 +13,7 @@ constexpr int kBK = kTileSlots;          // slots of a K/V tile
 constexpr int kRows = 128;               // rows of a Q tile (the MMA's M)
 constexpr int kBox = kBK * 64 * 2;       // 128 rows of 64 dims: 16 KB
 constexpr int kThreads = 32 * 12;
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;  // 256 x 208 + 128 x 88 = 384 x 168
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;  // 256 x 200 + 128 x 104 = 384 x 168
 constexpr int kLaunchRegs = 168;
 constexpr int kItems = 4;                // items published ahead
 constexpr int kWarpPlanB = 32;           // sequences up to which one warp plans alone

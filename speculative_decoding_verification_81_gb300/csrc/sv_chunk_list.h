@@ -2,8 +2,11 @@
 // host or device: items of a sequence, their units, and the cut of the list
 // into the CTAs' ranges.
 //
-// An item is up to 2 tpt consecutive rows of one sequence and one KV head; its
-// units are kItemCost and one for each 128-slot K/V tile that its rows see.
+// An item is up to 2 tpt consecutive rows of one sequence and one KV head (one
+// or two Q tiles); its units are kItemCost and, for each 128-slot K/V tile that
+// its rows see, one a Q tile: a tile's time goes with the products and softmax
+// of its Q tiles, and single tokens, paced by the loads, take about as long a
+// tile as a half of a chunk's.
 // The list runs over sequences, then KV heads, then items; CTA c of nctas
 // takes units floor(U c / nctas) .. floor(U (c + 1) / nctas) - 1 of the U.
 #pragma once
@@ -20,7 +23,7 @@ namespace sv {
 namespace chunk {
 
 constexpr int kTileSlots = 128;
-constexpr int kItemCost = 1;  // an item's start and end, in K/V tiles
+constexpr int kItemCost = 4;  // units of an item's start and end
 
 // Sum of floor((a i + c) / m) for i = 0 .. n - 1 (m > 0): the quotients' whole
 // parts in closed form, the rest by exchanging the roles of slope and
@@ -84,6 +87,14 @@ SV_HD int item_tiles(const Shape &p, const Seq &s, int i) {
     return (s.L + t1 + kTileSlots - 1) / kTileSlots - first_tile(p, s.L + t0);
 }
 
+// Q tiles of item i.
+SV_HD int item_weight(const Shape &p, const Seq &s, int i) { return s.n - i * 2 * p.tpt > p.tpt ? 2 : 1; }
+
+// Units of item i.
+SV_HD int item_units(const Shape &p, const Seq &s, int i) {
+    return item_tiles(p, s, i) * item_weight(p, s, i) + kItemCost;
+}
+
 // Units of items 0 .. i - 1 of one KV head.
 #ifdef __CUDACC__
 __host__ __device__ __noinline__ static
@@ -92,24 +103,35 @@ inline
 #endif
 long long units_before(const Shape &p, const Seq &s, int i) {
     if (i <= 0) return 0;
-    long long u = (long long)i * kItemCost;
-    if (i == s.items) u += item_tiles(p, s, --i);  // the last item may be short
+    long long u = 0, tiles = 0;
+    if (i == s.items) u = item_units(p, s, --i);  // the last item may be short
     if (i > 0) {
         const uint32_t tok = 2 * p.tpt;
-        u += floor_sum(i, kTileSlots, tok, s.L + tok + kTileSlots - 1);
+        tiles = floor_sum(i, kTileSlots, tok, s.L + tok + kTileSlots - 1);
         if (p.window > 0) {
             // first tiles: floor((L + k tok - window + 1) / 128), from the first k at which that is >= 0
             const long long c = (long long)s.L - p.window + 1;
             const long long k0 = c >= 0 ? 0 : (-c + tok - 1) / tok;
-            if (k0 < i) u -= floor_sum((uint32_t)(i - k0), kTileSlots, tok, (uint32_t)(c + k0 * tok));
+            if (k0 < i) tiles -= floor_sum((uint32_t)(i - k0), kTileSlots, tok, (uint32_t)(c + k0 * tok));
         }
     }
-    return u;
+    return u + 2 * tiles + (long long)i * kItemCost;
 }
 
-// a / b of a >= 0, b > 0: in 32 bits where both fit, which takes a quarter of the time.
+// a / b of a >= 0, b > 0.  Numbers below 2^22, as a short call's are, divide in
+// floats: the quotient is off by less than one (two roundings of at most 2^-22
+// of it), which the remainder's sign puts right; about a fifth of the time.
 SV_HD long long quot(long long a, long long b) {
-    return ((unsigned long long)a | (unsigned long long)b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+    if (((unsigned long long)a | (unsigned long long)b) >> 22) return a / b;
+    const int x = (int)a, y = (int)b;
+#ifdef __CUDA_ARCH__
+    int q = (int)__fdividef((float)x, (float)y);
+#else
+    int q = (int)((float)x / (float)y);
+#endif
+    const int r = x - q * y;
+    q += r < 0 ? -1 : r >= y ? 1 : 0;
+    return q;
 }
 
 SV_HD long long cta_begin(long long U, int nctas, int c) { return quot(U * c, nctas); }
@@ -135,23 +157,25 @@ SV_HD int ctas_for(long long U, long long items, int most, int grid) {
     return (int)n;
 }
 
-// What of an item of n tiles whose units start at ui falls into units
-// u0 .. u1 - 1 of CTA `cta`: tiles a .. z - 1 (none if a >= z), shared with
-// CTAs c_first .. c_first + nc - 1.
+// What of an item of n tiles of w units each, its units starting at ui, falls
+// into units u0 .. u1 - 1 of CTA `cta`: tiles a .. z - 1 (none if a >= z; a
+// tile is the CTA's that has its first unit), shared with CTAs c_first ..
+// c_first + nc - 1 (ranges are no shorter than w: each of them has a tile).
 struct Cut {
     int a, z, c_first, nc;
 };
 
-SV_HD Cut cut_item(long long ui, int n, long long u0, long long u1, long long U, int nctas, int cta) {
-    const long long t = ui + kItemCost;  // the unit of the first tile
+SV_HD Cut cut_item(long long ui, int n, int w, long long u0, long long u1, long long U, int nctas, int cta) {
+    const long long t = ui + kItemCost;  // the first unit of the first tile
+    const long long a = u0 <= t ? 0 : (u0 - t + w - 1) >> (w - 1), z = u1 <= t ? 0 : (u1 - t + w - 1) >> (w - 1);
     Cut c;
-    c.a = u0 <= t ? 0 : u0 - t < n ? (int)(u0 - t) : n;
-    c.z = u1 >= t + n ? n : u1 > t ? (int)(u1 - t) : 0;
+    c.a = a < n ? (int)a : n;
+    c.z = z < n ? (int)z : n;
     c.c_first = cta;
     c.nc = 1;
     if (c.a < c.z && (c.a > 0 || c.z < n)) {
         c.c_first = cta_of(U, nctas, t);
-        c.nc = cta_of(U, nctas, t + n - 1) - c.c_first + 1;
+        c.nc = cta_of(U, nctas, t + (long long)w * (n - 1)) - c.c_first + 1;
     }
     return c;
 }

@@ -26,9 +26,8 @@
 // their (O, m, sum) are merged at the end.
 //
 // The work list is every (sequence, KV head, item, K/V tile).  A persistent
-// grid takes equal contiguous ranges of it (an item counts kItemCost tiles
-// more than it has, for its start and end), so the load is even whatever the
-// lengths; an item cut by a range's end leaves partials in the workspace,
+// grid takes equal contiguous ranges of it, a tile weighing one for each of the
+// item's Q tiles (sv_chunk_list.h), so the load is even whatever the lengths; an item cut by a range's end leaves partials in the workspace,
 // merged by the warp that arrives last, in index order.
 //
 // Warps: 0-3 and 4-7 softmax of streams 0 and 1 (one thread a row); 8 and 11
@@ -58,11 +57,11 @@ __device__ __forceinline__ Units units_of(const Params &p, int L, int r0, int r1
     const Seq s = seq_of(p.shape, L, r0, r1);
     Units u{s.items, 0, 0};
     if (s.items == 1) {
-        u.most = item_tiles(p.shape, s, 0) + kItemCost;
+        u.most = item_units(p.shape, s, 0);
         u.per_head = u.most;
     } else if (s.items > 1) {
         // (the last item sees the most slots; a window may leave the one before it a tile more)
-        u.most = max(item_tiles(p.shape, s, s.items - 1), item_tiles(p.shape, s, s.items - 2)) + kItemCost;
+        u.most = max(item_units(p.shape, s, s.items - 1), item_units(p.shape, s, s.items - 2));
         u.per_head = units_before(p.shape, s, s.items);
     }
     return u;
@@ -160,6 +159,42 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                       pack_bf16x2(f[6], f[7]));
 }
 
+// 32 columns of a warp's 32 rows (a lane's row: acc, to out + off) written as
+// bf16.  The lanes of a quad exchange 16-byte pieces first (a 4 x 4 transpose
+// in two rounds), so that a store covers 64 consecutive bytes of 8 rows: one
+// row a lane, its 32 separate lines took the load/store unit four times as
+// long (a step of 16 prompts of 512 rows 91 us, mostly this).  r4: the quad's
+// first row; rows from `rows` on are not written.
+__device__ __forceinline__ void store_quad(uint16_t *out, long long off, const float (&acc)[32], int r4, int rows,
+                                           int lane) {
+    uint32_t c[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) c[i][w] = pack_bf16x2(acc[8 * i + 2 * w], acc[8 * i + 2 * w + 1]);
+#pragma unroll
+    for (int b = 1; b <= 2; b <<= 1) {
+        const bool up = (lane & b) != 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & b) continue;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? c[i][w] : c[i | b][w], b);
+                if (up) c[i][w] = got;
+                else c[i | b][w] = got;
+            }
+        }
+    }
+    // now c[i] is piece lane & 3 of row r4 + i
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const long long o = __shfl_sync(0xffffffffu, off, (lane & ~3) + i);
+        if (r4 + i < rows)
+            *reinterpret_cast<uint4 *>(out + o + 8 * (lane & 3)) = make_uint4(c[i][0], c[i][1], c[i][2], c[i][3]);
+    }
+}
+
 // This warp's O rows (D columns at TMEM address o) times a.
 template <int D>
 __device__ __noinline__ void rescale_o(uint32_t o, float a) {
@@ -198,54 +233,70 @@ __device__ __forceinline__ float2 *part_ml(const Params &p, int cta, int slot, i
 }
 
 // The nc partials of this warp's rows (row0 .. row0 + nv - 1 of Q tile qt)
-// merged in index order and written out.  A lane takes 8 columns of a row at
-// a time and passes over the parts once with a running maximum; kept out of
-// line and short, since a call runs it once or twice and its instructions
-// come from L2.  out_off and lse_off: lane r's row in `out` and `lse`.
-template <int D>
+// merged in index order and written out.  A lane takes IDX groups of 8
+// columns at a time and passes over the parts once, PARTS of them in flight,
+// with a running maximum (IDX = 2, PARTS = 2 for the few parts of a chunk's
+// item, 1 and 8 for a single token spread over many CTAs: a round of loads
+// takes about a microsecond).  Out of line, since a call runs it once or
+// twice.  out_off and lse_off: lane r's row in `out` and `lse`.
+template <int D, int IDX, int PARTS>
 __device__ __noinline__ void merge_parts(const float4 *part_o, const float2 *part_ml, uint16_t *out, float *lse,
                                          int nc, int nv, int lane, long long out_off, long long lse_off) {
     // from part to part: the first is in its CTA's slot 1, the others in their CTAs' slot 0
     constexpr size_t kO = (size_t)2 * (D / 4) * kRows, kMl = 2 * kRows;  // a slot (two Q tiles)
     const int total = nv * (D / 8);
 #pragma unroll 1
-    for (int idx0 = 0; idx0 < total; idx0 += 32) {
-        const int idx = min(idx0 + lane, total - 1);
-        const int c8 = idx / nv, r = idx - c8 * nv;
-        const long long off = __shfl_sync(0xffffffffu, out_off, r);
-        const long long loff = __shfl_sync(0xffffffffu, lse_off, r);
-        float acc[8] = {};
-        float M = kNegInf, l = 0.f;
-#pragma unroll 1
-        for (int i0 = 0; i0 < nc; i0 += 4) {
-            float2 ml[4];
-            float4 x[4], y[4];
+    for (int idx0 = 0; idx0 < total; idx0 += 32 * IDX) {
+        int c8[IDX], r[IDX];
+        float acc[IDX][8] = {}, M[IDX], l[IDX];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int i = min(i0 + u, nc - 1), slot = 2 * i + (i == 0 ? 1 : 0);
-                ml[u] = __ldcg(part_ml + slot * kMl + r);
-                x[u] = __ldcg(part_o + slot * kO + (size_t)(2 * c8) * kRows + r);
-                y[u] = __ldcg(part_o + slot * kO + (size_t)(2 * c8 + 1) * kRows + r);
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                // (a part without a visible slot has no O: select, never multiply, it)
-                if (i0 + u >= nc || ml[u].x == kNegInf) continue;
-                const float Mn = fmaxf(M, ml[u].x);
-                const float f = M == kNegInf ? 0.f : ex2_approx(M - Mn), w = ex2_approx(ml[u].x - Mn);
-                M = Mn;
-                l = l * f + ml[u].y * w;
-                const float o[8] = {x[u].x, x[u].y, x[u].z, x[u].w, y[u].x, y[u].y, y[u].z, y[u].w};
-#pragma unroll
-                for (int e = 0; e < 8; ++e) acc[e] = __fmaf_rn(o[e], w, acc[e] * f);
-            }
+        for (int q = 0; q < IDX; ++q) {
+            const int idx = min(idx0 + 32 * q + lane, total - 1);
+            c8[q] = idx / nv;
+            r[q] = idx - c8[q] * nv;
+            M[q] = kNegInf;
+            l[q] = 0.f;
         }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll 1
+        for (int i0 = 0; i0 < nc; i0 += PARTS) {
+            float2 ml[IDX][PARTS];
+            float4 x[IDX][PARTS], y[IDX][PARTS];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] *= inv;
-        if (idx0 + lane < total) {
-            *reinterpret_cast<uint4 *>(out + off + 8 * c8) = pack8(acc);
-            if (lse && c8 == 0) lse[loff] = l > 0.f ? M * kLn2 + logf(l) : kNegInf;
+            for (int q = 0; q < IDX; ++q)
+#pragma unroll
+                for (int u = 0; u < PARTS; ++u) {
+                    const int i = min(i0 + u, nc - 1), slot = 2 * i + (i == 0 ? 1 : 0);
+                    ml[q][u] = __ldcg(part_ml + slot * kMl + r[q]);
+                    x[q][u] = __ldcg(part_o + slot * kO + (size_t)(2 * c8[q]) * kRows + r[q]);
+                    y[q][u] = __ldcg(part_o + slot * kO + (size_t)(2 * c8[q] + 1) * kRows + r[q]);
+                }
+#pragma unroll
+            for (int q = 0; q < IDX; ++q)
+#pragma unroll
+                for (int u = 0; u < PARTS; ++u) {
+                    // (a part without a visible slot has no O: select, never multiply, it)
+                    if (i0 + u >= nc || ml[q][u].x == kNegInf) continue;
+                    const float Mn = fmaxf(M[q], ml[q][u].x);
+                    const float f = M[q] == kNegInf ? 0.f : ex2_approx(M[q] - Mn), w = ex2_approx(ml[q][u].x - Mn);
+                    M[q] = Mn;
+                    l[q] = l[q] * f + ml[q][u].y * w;
+                    const float o[8] = {x[q][u].x, x[q][u].y, x[q][u].z, x[q][u].w,
+                                        y[q][u].x, y[q][u].y, y[q][u].z, y[q][u].w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) acc[q][e] = __fmaf_rn(o[e], w, acc[q][e] * f);
+                }
+        }
+#pragma unroll
+        for (int q = 0; q < IDX; ++q) {
+            const long long off = __shfl_sync(0xffffffffu, out_off, r[q]);
+            const long long loff = __shfl_sync(0xffffffffu, lse_off, r[q]);
+            const float inv = l[q] > 0.f ? 1.f / l[q] : 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[q][e] *= inv;
+            if (idx0 + 32 * q + lane < total) {
+                *reinterpret_cast<uint4 *>(out + off + 8 * c8[q]) = pack8(acc[q]);
+                if (lse && c8[q] == 0) lse[loff] = l[q] > 0.f ? M[q] * kLn2 + logf(l[q]) : kNegInf;
+            }
         }
     }
 }
@@ -380,6 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = warp >> 2, quarter = warp & 3;
         const int r = quarter * 32 + lane;  // the row in its Q tile
         const int t = r / p.G, g = r - t * p.G;
+        const int t_lo = (quarter * 32) / p.G, t_hi = (quarter * 32 + 31) / p.G;  // the warp's tokens
         const uint32_t tl = tbase + ((uint32_t)(quarter * 32) << 16);
         const uint32_t sbuf = tl + kColS + s * kBK;
         const float sc = p.scale_log2;
@@ -405,8 +457,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pos = pos0 + t;                   // this row's position
             const int see_hi = pos + 1, see_lo = p.shape.window > 0 ? pos - p.shape.window + 1 : 0;
             // tiles all of whose slots every row of the warp sees
-            const int w_hi = pos0 + (quarter * 32) / p.G + 1;
-            const int w_lo = p.shape.window > 0 ? pos0 + min(quarter * 32 + 31, rows - 1) / p.G - p.shape.window + 1 : 0;
+            const int w_hi = pos0 + t_lo + 1;
+            const int w_lo = p.shape.window > 0 ? pos0 + min(t_hi, ntok - 1) - p.shape.window + 1 : 0;
             const int item_lo = p.shape.window > 0 ? max(0, it.pos0 - p.shape.window + 1) : 0;
             const int item_hi = it.pos0 + it.ntok;
             float m = kNegInf, l = 0.f;
@@ -500,8 +552,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 o_ph ^= 1;
                 tc::fence_after();
             }
+            const bool pair = !two && it.n > 1;  // one Q tile, shared: its first stream finishes it
             if (!two && a == 1) {
-                // one Q tile: the other stream finishes the item
                 if (steps > 0) {
                     sh->xml[s][r] = make_float2(m, l);
                     tc::fence_before();
@@ -509,7 +561,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) mbar_arrive(&sh->x_full[s]);
                 }
             } else {
-                const bool pair = !two && it.n > 1;  // the other stream holds a share
                 float m2 = kNegInf, l2 = 0.f;
                 if (pair) {
                     if (!(ok = warp_wait_bounded(&sh->x_full[s ^ 1], x_ph))) {
@@ -540,10 +591,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int h = 0; h < D / 32; ++h) {  // (short code: most of its time is instruction fetch)
                         uint32_t ov[32];
-                        float acc[32];
                         __syncwarp();
                         tc::tmem_ld32(o_cols + 32 * h, ov);
                         tc::wait_ld();
+                        float acc[32];
                         // a share without a visible slot weighs nothing, whatever its O holds
 #pragma unroll
                         for (int i = 0; i < 32; ++i) acc[i] = w1 != 0.f ? __uint_as_float(ov[i]) * f1 : 0.f;
@@ -554,8 +605,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int i = 0; i < 32; ++i)
                                 acc[i] = w2 != 0.f ? __fmaf_rn(__uint_as_float(ov[i]), f2, acc[i]) : acc[i];
                         }
-                        if (!valid) continue;
-                        if (whole) {
+                        if (whole && rows > 8) {
+                            store_quad(p.out, out_off + 32 * h, acc, r & ~3, rows, lane);
+                        } else if (whole) {
+                            if (!valid) continue;
 #pragma unroll
                             for (int c = 0; c < 4; ++c) {
                                 float e[8];
@@ -563,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 for (int i = 0; i < 8; ++i) e[i] = acc[8 * c + i];
                                 *reinterpret_cast<uint4 *>(p.out + out_off + 32 * h + 8 * c) = pack8(e);
                             }
-                        } else {
+                        } else if (valid) {
                             float4 *po = part_o<D>(p, blockIdx.x, pslot, qt) + r;
 #pragma unroll
                             for (int c = 0; c < 8; ++c)
@@ -588,9 +641,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (last) *ctr = 0;  // all have arrived: ready for the next call
                     }
                     if (__shfl_sync(0xffffffffu, last, 0))
-                        merge_parts<D>(part_o<D>(p, it.c_first, 0, qt) + quarter * 32,
-                                       part_ml(p, it.c_first, 0, qt) + quarter * 32, p.out, p.lse, it.nc,
-                                       min(32, rows - quarter * 32), lane, out_off, lse_off);
+                    {
+                        const float4 *po = part_o<D>(p, it.c_first, 0, qt) + quarter * 32;
+                        const float2 *pm = part_ml(p, it.c_first, 0, qt) + quarter * 32;
+                        const int nv = min(32, rows - quarter * 32);
+                        // (not through a pointer to either: with an indirect call in it
+                        // the kernel is built without its register split)
+                        if (it.nc > 4) merge_parts<D, 1, 8>(po, pm, p.out, p.lse, it.nc, nv, lane, out_off, lse_off);
+                        else merge_parts<D, 2, 2>(po, pm, p.out, p.lse, it.nc, nv, lane, out_off, lse_off);
+                    }
                 }
             }
             __syncwarp();
@@ -777,8 +836,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 qpos += two ? 2 : 1;
             }
-            if (ok && before2) ok = issue_pv(g & 1, before2);
-            if (ok && before1) ok = issue_pv((g & 1) ^ 1, before1);
+                if (ok && before2) ok = issue_pv(g & 1, before2);
+                if (ok && before1) ok = issue_pv((g & 1) ^ 1, before1);
             if (!ok && lane == 0) fail(b_now);
             // every product issued is complete before the tensor memory is given back
             commit(leader, &sh->fin);
@@ -856,8 +915,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (; ok && h < p.Hkv && ui < u1; ++h, i = 0)
                     for (; ok && i < sq.items && ui < u1; ++i) {
                         const int n = item_tiles(p.shape, sq, i);
-                        const Cut c = cut_item(ui, n, u0, u1, U, nctas, blockIdx.x);
-                        ui += n + kItemCost;
+                        const int w = item_weight(p.shape, sq, i);
+                        const Cut c = cut_item(ui, n, w, u0, u1, U, nctas, blockIdx.x);
+                        ui += n * w + kItemCost;
                         if (c.a >= c.z) continue;  // only its cost falls into the range
                         Item it;
                         it.b = b;

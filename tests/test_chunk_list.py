@@ -23,8 +23,9 @@ extern "C" long long c_before(int tpt, int window, int L, int n, int i) {
     return units_before(p, seq_of(p, L, 5, 5 + n), i);
 }
 extern "C" int c_valid(int L, int r0, int r1, int rows, int smax) { return seq_of({32, 0, rows, smax}, L, r0, r1).n; }
-extern "C" void c_cut(long long ui, int n, long long U, int nctas, int cta, int *out) {
-    const Cut c = cut_item(ui, n, cta_begin(U, nctas, cta), cta_begin(U, nctas, cta + 1), U, nctas, cta);
+extern "C" int c_ctas(long long U, long long items, int most, int grid) { return ctas_for(U, items, most, grid); }
+extern "C" void c_cut(long long ui, int n, int w, long long U, int nctas, int cta, int *out) {
+    const Cut c = cut_item(ui, n, w, cta_begin(U, nctas, cta), cta_begin(U, nctas, cta + 1), U, nctas, cta);
     out[0] = c.a; out[1] = c.z; out[2] = c.c_first; out[3] = c.nc;
 }
 """
@@ -41,8 +42,9 @@ def C(tmp_path_factory):
     L = ctypes.CDLL(str(d / "shim.so"))
     L.c_floor_sum.argtypes = [ctypes.c_uint32] * 4
     L.c_floor_sum.restype = L.c_before.restype = ctypes.c_longlong
-    L.c_cut.argtypes = [ctypes.c_longlong, ctypes.c_int, ctypes.c_longlong, ctypes.c_int, ctypes.c_int,
-                        ctypes.c_void_p]
+    L.c_cut.argtypes = [ctypes.c_longlong, ctypes.c_int, ctypes.c_int, ctypes.c_longlong, ctypes.c_int,
+                        ctypes.c_int, ctypes.c_void_p]
+    L.c_ctas.argtypes = [ctypes.c_longlong, ctypes.c_longlong, ctypes.c_int, ctypes.c_int]
     return L
 
 
@@ -50,6 +52,10 @@ def tiles(tpt, window, L, n, i):
     t0, t1 = i * 2 * tpt, min((i + 1) * 2 * tpt, n)
     lo = max(0, L + t0 - window + 1) if window else 0
     return (L + t1 - 1) // 128 - lo // 128 + 1
+
+
+def weight(tpt, n, i):
+    return 2 if n - i * 2 * tpt > tpt else 1  # Q tiles
 
 
 def test_floor_sum(C):
@@ -73,7 +79,7 @@ def test_units_closed_form(C):
         for i in range(items):
             assert C.c_before(tpt, window, L, n, i) == total, (tpt, window, L, n, i)
             assert C.c_tiles(tpt, window, L, n, i) == tiles(tpt, window, L, n, i)
-            total += 1 + tiles(tpt, window, L, n, i)
+            total += 4 + weight(tpt, n, i) * tiles(tpt, window, L, n, i)
         assert C.c_before(tpt, window, L, n, items) == total
 
 
@@ -89,8 +95,8 @@ def test_refused_lengths_have_no_rows(C):
     assert C.c_valid(3, 2, 2, 5, 15) == 0     # no rows
 
 
-@pytest.mark.parametrize("sms,min_units", [(152, 4), (7, 1), (3, 4)])
-def test_ranges_cover_every_tile_once(C, sms, min_units):
+@pytest.mark.parametrize("sms", [152, 7, 3])
+def test_ranges_cover_every_tile_once(C, sms):
     rng = np.random.default_rng(3)
     out = (ctypes.c_int * 4)()
     for _ in range(25):
@@ -99,15 +105,16 @@ def test_ranges_cover_every_tile_once(C, sms, min_units):
         hkv = int(rng.integers(1, 5))
         seqs = [(int(rng.integers(0, 1200)), int(rng.choice([1, 1, int(rng.integers(1, 400))])))
                 for _ in range(int(rng.integers(1, 9)))]
-        units = [(1 + tiles(tpt, window, L, n, i)) for L, n in seqs for _ in range(hkv)
+        items = [(tiles(tpt, window, L, n, i), weight(tpt, n, i)) for L, n in seqs for _ in range(hkv)
                  for i in range(-(-n // (2 * tpt)))]
-        U = sum(units)
-        nctas = min(sms, max(1, U // min_units))
+        U = sum(4 + n * w for n, w in items)
+        nctas = C.c_ctas(U, len(items), max(4 + n * w for n, w in items), sms)
+        assert 1 <= nctas <= sms and (nctas == 1 or U // nctas >= 4)
         ui, slots = 0, set()
-        for u in units:
-            n, parts = u - 1, []
+        for n, w in items:
+            parts = []
             for cta in range(nctas):
-                C.c_cut(ui, n, U, nctas, cta, ctypes.addressof(out))
+                C.c_cut(ui, n, w, U, nctas, cta, ctypes.addressof(out))
                 a, z, first, nc = out
                 if a < z:
                     parts.append((cta, a, z, first, nc))
@@ -117,4 +124,4 @@ def test_ranges_cover_every_tile_once(C, sms, min_units):
                 if nc > 1:  # a CTA's partial slots are its own: the item it begins, or the one it continues
                     assert (cta, k == 0) not in slots
                     slots.add((cta, k == 0))
-            ui += u
+            ui += 4 + n * w
