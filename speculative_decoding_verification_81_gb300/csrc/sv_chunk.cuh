@@ -69,8 +69,6 @@ struct Shared {
     Item items[kItems];
     long long warp_units[kThreads / 32];
     int warp_items[kThreads / 32], warp_most[kThreads / 32];
-    long long U, ub_start;
-    int nctas, b_start;
     uint32_t tmem;
     int abort_flag;
 };

@@ -15,8 +15,12 @@
 
 #ifdef __CUDACC__
 #define SV_HD __host__ __device__ __forceinline__
+// out of line on the device: the walking warp's instructions share the
+// instruction caches with the loops that set the pace
+#define SV_HD_CALL __host__ __device__ __noinline__ static
 #else
 #define SV_HD inline
+#define SV_HD_CALL inline
 #endif
 
 namespace sv {
@@ -96,12 +100,7 @@ SV_HD int item_units(const Shape &p, const Seq &s, int i) {
 }
 
 // Units of items 0 .. i - 1 of one KV head.
-#ifdef __CUDACC__
-__host__ __device__ __noinline__ static
-#else
-inline
-#endif
-long long units_before(const Shape &p, const Seq &s, int i) {
+SV_HD_CALL long long units_before(const Shape &p, const Seq &s, int i) {
     if (i <= 0) return 0;
     long long u = 0, tiles = 0;
     if (i == s.items) u = item_units(p, s, --i);  // the last item may be short
@@ -146,37 +145,34 @@ SV_HD int cta_of(long long U, int nctas, long long u) { return (int)quot((u + 1)
 constexpr int kMinUnits = 4;
 
 SV_HD int ctas_for(long long U, long long items, int most, int grid) {
-    const long long want = quot(U, kMinUnits) > 0 ? quot(U, kMinUnits) : 1;
-    long long n = want < grid ? want : grid;
-    if (items > 0 && items <= grid && items * most == U) {
-        const long long parts = n / items > 0 ? n / items : 1;  // CTAs an item
-        // a cut item costs its merge, about as long as four tiles
-        const long long even = quot(most + parts - 1, parts) + (parts > 1 ? 4 : 0), flat = quot(U + n - 1, n) + 4;
-        if (even <= flat) n = items * parts;
+    const long long want = U / kMinUnits > 0 ? U / kMinUnits : 1;
+    int n = want < grid ? (int)want : grid;
+    if (items > 0 && items <= n && items * most == U && most < (1 << 20)) {
+        const int k = (int)items, parts = n / k;  // CTAs an item
+        // a cut item costs its merge, about as long as four units
+        const int even = (most + parts - 1) / parts + (parts > 1 ? 4 : 0), flat = (k * most + n - 1) / n + 4;
+        if (even <= flat) n = k * parts;
     }
-    return (int)n;
+    return n;
 }
 
 // What of an item of n tiles of w units each, its units starting at ui, falls
-// into units u0 .. u1 - 1 of CTA `cta`: tiles a .. z - 1 (none if a >= z; a
-// tile is the CTA's that has its first unit), shared with CTAs c_first ..
-// c_first + nc - 1 (ranges are no shorter than w: each of them has a tile).
+// into a CTA's units u0 .. u1 - 1: tiles a .. z - 1 (none if a >= z; a tile is
+// the CTA's that has its first unit).  A cut item is shared by the CTAs of
+// its first and last tile's first units and all between them (a range is no
+// shorter than w, so that each of them has a tile).
 struct Cut {
-    int a, z, c_first, nc;
+    int a, z;
 };
 
-SV_HD Cut cut_item(long long ui, int n, int w, long long u0, long long u1, long long U, int nctas, int cta) {
+SV_HD long long tile_unit(long long ui, int w, int tile) { return ui + kItemCost + (long long)w * tile; }
+
+SV_HD Cut cut_item(long long ui, int n, int w, long long u0, long long u1) {
     const long long t = ui + kItemCost;  // the first unit of the first tile
     const long long a = u0 <= t ? 0 : (u0 - t + w - 1) >> (w - 1), z = u1 <= t ? 0 : (u1 - t + w - 1) >> (w - 1);
     Cut c;
     c.a = a < n ? (int)a : n;
     c.z = z < n ? (int)z : n;
-    c.c_first = cta;
-    c.nc = 1;
-    if (c.a < c.z && (c.a > 0 || c.z < n)) {
-        c.c_first = cta_of(U, nctas, t);
-        c.nc = cta_of(U, nctas, t + (long long)w * (n - 1)) - c.c_first + 1;
-    }
     return c;
 }
 

@@ -47,6 +47,16 @@ __device__ __forceinline__ uint32_t sw128(int row, int c) {
     return (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4));
 }
 
+// Inclusive prefix sum over the warp.
+__device__ __forceinline__ long long warp_scan(long long x, int lane) {
+#pragma unroll 1
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+    }
+    return x;
+}
+
 // A sequence's items and units, of one KV head.
 struct Units {
     int items, most;  // most: units of its largest item
@@ -321,10 +331,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
+#pragma unroll 1
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sh->full[i], 1);
             mbar_init(&sh->empty[i], 1);
         }
+#pragma unroll 1
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh->q_full[i], 1);
             mbar_init(&sh->q_empty[i], 1);
@@ -334,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh->o_empty[i], 4);
             mbar_init(&sh->x_full[i], 4);
         }
+#pragma unroll 1
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&sh->item_full[i], 1);
             mbar_init(&sh->item_empty[i], 11);  // softmax warps, loaders, issuer
@@ -354,6 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_launch_dependents();
     if ((base_u32 & 1023u) != 0) {  // (never seen: nothing else takes shared memory here)
         if (p.seq_status)
+#pragma unroll 1
             for (int b = tid; b < p.B; b += kThreads) p.seq_status[b] = SV_ERR_CUDA;
         __syncthreads();
         if (warp == 9) tc::tmem_dealloc(sh->tmem, kCols);
@@ -363,25 +377,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_before();  // (the barriers and the tensor memory's address)
     __syncthreads();
     tc::fence_after();
-    // ---- many sequences: every CTA sums the units of all, finds its own range
-    // and the sequence it starts in (up to 32, the walking warp does it alone)
+    // ---- many sequences: the units before each thread's share of them, for the
+    // walking warp (up to 32 sequences it sums alone), in the still idle Q tiles
+    long long *before = reinterpret_cast<long long *>(qbuf);
+    const int per = (p.B + kThreads - 1) / kThreads;
     if (p.B > kWarpPlanB) {
-        const int per = (p.B + kThreads - 1) / kThreads;
-        const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+        const int b1 = min((tid + 1) * per, p.B);
         long long mine = 0;
         int items = 0, most = 0;
-        for (int b = b0; b < b1; ++b) {
+#pragma unroll 1
+        for (int b = tid * per; b < b1; ++b) {
             const Units u = units_of(p, p.prefix_lens[b], p.row_starts[b], p.row_starts[b + 1]);
             mine += u.per_head * p.Hkv;
             items += u.items * p.Hkv;
             most = max(most, u.most);
         }
-        long long x = mine;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, x, off);
-            if (lane >= off) x += y;
-        }
+        const long long x = warp_scan(mine, lane);
         items = __reduce_add_sync(0xffffffffu, items);
         most = __reduce_max_sync(0xffffffffu, most);
         if (lane == 31) {
@@ -390,32 +401,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             sh->warp_most[warp] = most;
         }
         __syncthreads();
-        long long before = x - mine, U = 0, all_items = 0;
-        for (int w = 0; w < kThreads / 32; ++w) {
-            const long long v = sh->warp_units[w];
-            if (w < warp) before += v;
-            U += v;
-            all_items += sh->warp_items[w];
-            most = max(most, sh->warp_most[w]);
-        }
-        const int nctas = ctas_for(U, all_items, most, gridDim.x);
-        const long long u0 = (int)blockIdx.x < nctas ? cta_begin(U, nctas, blockIdx.x) : U;
-        if (tid == 0) {
-            sh->U = U;
-            sh->nctas = nctas;
-            if (u0 >= U) sh->b_start = p.B;
-        }
-        if (u0 >= before && u0 < before + mine) {  // exactly one thread, when the CTA has work
-            int b = b0;
-            long long ub = before;
-            for (; b < b1; ++b) {
-                const Units u = units_of(p, p.prefix_lens[b], p.row_starts[b], p.row_starts[b + 1]);
-                if (u0 < ub + u.per_head * p.Hkv) break;
-                ub += u.per_head * p.Hkv;
-            }
-            sh->b_start = b;
-            sh->ub_start = ub;
-        }
+        long long base = 0;
+#pragma unroll 1
+        for (int w = 0; w < warp; ++w) base += sh->warp_units[w];
+        before[tid] = base + x - mine;
+        tc::fence_proxy_async_smem();  // (a TMA copy writes there next)
         __syncthreads();
     }
     const uint32_t tbase = sh->tmem;
@@ -439,6 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t gstep = 0;       // steps of the CTA before this item
         uint32_t ring = 0;        // K/V ring position of the item's first tile
         bool ok = true;
+#pragma unroll 1
         for (uint32_t k = 0;; ++k) {
             const int slot = k % kItems;
             if (!warp_wait_bounded(&sh->item_full[slot], (k / kItems) & 1)) {
@@ -464,6 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = kNegInf, l = 0.f;
             const int first = two ? 0 : a, stride = two ? 1 : 2;
             const uint32_t o_cols = tl + kColO + s * 128;
+#pragma unroll 1
             for (int j = first; j < it.n; j += stride) {
                 const int kb = (it.kt0 + j) * kBK;
                 if (!(ok = warp_wait_bounded(&sh->s_full[s], s_ph))) break;
@@ -487,10 +479,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     if (kb + kBK > w_hi || kb < w_lo) {
+                        // bit i of word i / 32: slot kb + i is at least see_lo and below see_hi
                         const int hi = see_hi - kb, lo = see_lo - kb;
 #pragma unroll
-                        for (int i = 0; i < kBK; ++i)
-                            if (i >= hi || i < lo) sv[i] = kNegInf;
+                        for (int w = 0; w < kBK / 32; ++w) {
+                            const int h = hi - 32 * w, o = lo - 32 * w;
+                            const uint32_t below = h >= 32 ? ~0u : h <= 0 ? 0u : (1u << h) - 1u;
+                            const uint32_t under = o >= 32 ? ~0u : o <= 0 ? 0u : (1u << o) - 1u;
+                            const uint32_t sees = below & ~under;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!((sees >> i) & 1u)) sv[32 * w + i] = kNegInf;
+                        }
                     }
                     float mq[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
@@ -672,6 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t once = l2_policy_evict_first();
             uint32_t pos = kv;
             bool ok = true;
+#pragma unroll 1
             for (uint32_t k = 0; ok; ++k) {
                 const int slot = k % kItems;
                 if (!wait(&sh->item_full[slot], (k / kItems) & 1)) {
@@ -693,6 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return pg >= 0 && pg < p.num_pages ? (pg * p.Hkv + it.h) * ps + s0 % ps : -kBK;
                 };
                 int y = box_row(0);
+#pragma unroll 1
                 for (int j = 0; j < it.n && ok; ++j) {
                     const int y_next = j + 1 < it.n ? box_row(j + 1) : kNone;
                     const int boxes = __popc(__ballot_sync(0xffffffffu, y != kNone));
@@ -720,6 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // every copy issued must land before the CTA may exit: the products have
             // waited for all of them, unless a wait gave up
             if (__shfl_sync(0xffffffffu, *abort_flag, 0))
+#pragma unroll 1
                 for (uint32_t q = pos > kStages ? pos - kStages : kv; q < pos; ++q)
                     if ((q & 1) == (uint32_t)kv) wait(&sh->full[q % kStages], (q / kStages) & 1);
         } else if (warp == 9) {
@@ -756,18 +759,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (q & kLast) commit(leader, &sh->o_full[s]);
                 return true;
             };
+#pragma unroll 1
             for (uint32_t k = 0; ok; ++k) {
                 const int slot = k % kItems;
                 if (!(ok = wait(&sh->item_full[slot], (k / kItems) & 1))) break;
                 const int b = uniform(sh->items[slot].b), n = uniform(sh->items[slot].n);
                 const bool two = uniform(sh->items[slot].ntok) > p.shape.tpt;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh->item_empty[slot]);
-                if (b < 0) break;
-                b_now = b;
-                const int steps = two ? 2 * n : n;
+                if (b >= 0) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh->item_empty[slot]);
+                    b_now = b;
+                }
+                // (the end of the list: two steps without an S, for the last products)
+                const int steps = b < 0 ? 2 : two ? 2 * n : n;
+#pragma unroll 1
                 for (int i = 0; i < steps; ++i, ++g) {
-                    if (two && i == 4 && n > 2) {
+                    if (two && i == 4 && b >= 0) {  // (n > 2)
                         // An item of two Q tiles from its third K/V tile on: both
                         // streams' steps of a tile, without the generic step's
                         // bookkeeping (its instructions, fetched anew each time beside
@@ -812,6 +819,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool second = two && (i & 1);  // of an item of two Q tiles: the second tile's step
                     const uint32_t qp = qpos + (second ? 1 : 0);
                     if (before2 && !(ok = issue_pv(s, before2))) break;
+                    before2 = before1;
+                    before1 = 0;
+                    if (b < 0) continue;
                     if (i == 0 || (two && i == 1)) ok = wait(&sh->q_full[qp & 1], (qp >> 1) & 1);
                     if (ok && !second) ok = wait(&sh->full[st], st_ph);
                     if (!ok) break;
@@ -826,7 +836,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (last_tile) commit(leader, &sh->q_empty[qp & 1]);
                     const uint32_t vs = st + 1 == kStages ? 0 : st + 1;
                     const uint32_t v_ph = st + 1 == kStages ? st_ph ^ 1 : st_ph;
-                    before2 = before1;
                     before1 = vs | kLive | (v_ph ? kPhase : 0u) | (i < 2 ? kFirst : 0u) |
                               (i >= steps - 2 ? kLast : 0u) | (frees ? kFrees : 0u);
                     if (frees) {  // on to the next tile: K and V took a stage each
@@ -834,10 +843,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         st_ph = vs + 1 == kStages ? v_ph ^ 1 : v_ph;
                     }
                 }
+                if (b < 0) break;
                 qpos += two ? 2 : 1;
             }
-                if (ok && before2) ok = issue_pv(g & 1, before2);
-                if (ok && before1) ok = issue_pv((g & 1) ^ 1, before1);
             if (!ok && lane == 0) fail(b_now);
             // every product issued is complete before the tensor memory is given back
             commit(leader, &sh->fin);
@@ -859,38 +867,56 @@ __global__ void __launch_bounds__(kThreads, 1)
                     un = units_of(p, pre, r0, r1);
                 }
             };
+            long long items = 0, x = 0, mine = 0;
+            int most = 0;
             if (p.B > kWarpPlanB) {
-                U = sh->U;
-                nctas = sh->nctas;
-                b = (int)blockIdx.x < nctas ? sh->b_start : p.B;
-                ub = sh->ub_start;
+                U = 0;
+#pragma unroll 1
+                for (int w = 0; w < kThreads / 32; ++w) {
+                    U += sh->warp_units[w];
+                    items += sh->warp_items[w];
+                    most = max(most, sh->warp_most[w]);
+                }
             } else {
                 load(0);
-                const long long mine = un.per_head * p.Hkv;
-                long long x = mine;
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const long long y = __shfl_up_sync(0xffffffffu, x, off);
-                    if (lane >= off) x += y;
-                }
+                mine = un.per_head * p.Hkv;
+                x = warp_scan(mine, lane);
                 U = __shfl_sync(0xffffffffu, x, 31);
-                nctas = ctas_for(U, (long long)__reduce_add_sync(0xffffffffu, un.items) * p.Hkv,
-                                 __reduce_max_sync(0xffffffffu, un.most), gridDim.x);
-                const long long first = (int)blockIdx.x < nctas ? cta_begin(U, nctas, blockIdx.x) : U;
-                const uint32_t here = __ballot_sync(0xffffffffu, first < x);  // (x only grows)
-                b = here ? __ffs(here) - 1 : p.B;
-                ub = __shfl_sync(0xffffffffu, x - mine, b & 31);
+                items = (long long)__reduce_add_sync(0xffffffffu, un.items) * p.Hkv;
+                most = __reduce_max_sync(0xffffffffu, un.most);
             }
-            u0 = b < p.B ? cta_begin(U, nctas, blockIdx.x) : 0;
-            u1 = b < p.B ? cta_begin(U, nctas, blockIdx.x + 1) : 0;
+            nctas = ctas_for(U, items, most, gridDim.x);
+            const bool has = U > 0 && (int)blockIdx.x < nctas;
+            {
+                const long long edge = cta_begin(U, nctas, blockIdx.x + (lane & 1));  // (both ends at once)
+                u0 = __shfl_sync(0xffffffffu, edge, 0);
+                u1 = __shfl_sync(0xffffffffu, edge, 1);
+            }
+            if (!has) {
+                b = p.B;
+                ub = 0;
+            } else if (p.B > kWarpPlanB) {  // the last thread with at most u0 units before its sequences
+                int below = 0;
+#pragma unroll 1
+                for (int i = lane; i < kThreads; i += 32) below += before[i] <= u0;
+                const int at = __reduce_add_sync(0xffffffffu, below) - 1;
+                b = at * per;
+                ub = before[at];
+                __syncwarp();
+            } else {
+                b = __ffs(__ballot_sync(0xffffffffu, u0 < x)) - 1;  // (x only grows)
+                ub = __shfl_sync(0xffffffffu, x - mine, b);
+            }
             uint32_t k = 0, qpos = 0;
             bool ok = true;
+#pragma unroll 1
             while (ok && b < p.B && ub < u1) {
                 if (cached < 0 || b >= cached + 32) load(b);
                 const Seq sq = seq_of(p.shape, __shfl_sync(0xffffffffu, pre, b - cached),
                                       __shfl_sync(0xffffffffu, r0, b - cached), __shfl_sync(0xffffffffu, r1, b - cached));
                 const long long per_head = __shfl_sync(0xffffffffu, un.per_head, b - cached);
-                if (sq.items == 0) {
+                if (ub + per_head * p.Hkv <= u0 || sq.items == 0) {
+                    ub += per_head * p.Hkv;
                     ++b;
                     continue;
                 }
@@ -901,6 +927,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const long long v = (u0 - ub) - (long long)h * per_head;
                     // the last item whose first unit is at most v: 32 candidates at a time
                     int lo = 0, span = sq.items;
+#pragma unroll 1
                     while (span > 1) {
                         const int step = (span + 31) / 32;
                         const int cand = lo + lane * step;
@@ -912,11 +939,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     i = lo;
                     ui = ub + (long long)h * per_head + units_before(p.shape, sq, i);
                 }
+#pragma unroll 1
                 for (; ok && h < p.Hkv && ui < u1; ++h, i = 0)
+#pragma unroll 1
                     for (; ok && i < sq.items && ui < u1; ++i) {
                         const int n = item_tiles(p.shape, sq, i);
                         const int w = item_weight(p.shape, sq, i);
-                        const Cut c = cut_item(ui, n, w, u0, u1, U, nctas, blockIdx.x);
+                        const Cut c = cut_item(ui, n, w, u0, u1);
+                        const long long own = ui;
                         ui += n * w + kItemCost;
                         if (c.a >= c.z) continue;  // only its cost falls into the range
                         Item it;
@@ -928,9 +958,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         it.kt0 = first_tile(p.shape, it.pos0) + c.a;
                         it.n = c.z - c.a;
                         it.single = sq.items == 1;
-                        it.c_first = c.c_first;
-                        it.nc = c.nc;
-                        it.ci = blockIdx.x - c.c_first;
+                        it.c_first = blockIdx.x;
+                        it.nc = 1;
+                        if (it.n < n) {  // the CTAs of its first and its last tile
+                            const int cta = cta_of(U, nctas, tile_unit(own, w, lane & 1 ? n - 1 : 0));
+                            it.c_first = __shfl_sync(0xffffffffu, cta, 0);
+                            it.nc = __shfl_sync(0xffffffffu, cta, 1) - it.c_first + 1;
+                        }
+                        it.ci = blockIdx.x - it.c_first;
                         const int slot = k % kItems;
                         if (!wait(&sh->item_empty[slot], ((k / kItems) & 1) ^ 1) ||
                             __shfl_sync(0xffffffffu, *abort_flag, 0)) {
@@ -943,6 +978,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         ++k;
                         const int tiles = it.ntok > p.shape.tpt ? 2 : 1;
+#pragma unroll 1
                         for (int q = 0; q < tiles; ++q, ++qpos) {
                             const int qb = qpos & 1;
                             if (!wait(&sh->q_empty[qb], ((qpos >> 1) & 1) ^ 1)) {
@@ -956,6 +992,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 uint8_t *qd = qbuf + qb * kTile;
                                 mbar_arrive_expect_tx(&sh->q_full[qb],
                                                       (uint32_t)(kHalves * 128 * p.G * (one ? 1 : p.shape.tpt)));
+#pragma unroll 1
                                 for (int hf = 0; hf < kHalves; ++hf)
                                     tma_load_3d(qd + hf * kBox, map, hf * 64, h * p.G, it.row0 + q * p.shape.tpt,
                                                 &sh->q_full[qb]);
@@ -975,6 +1012,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&sh->item_full[slot]);
             }
             // seq_status: lengths, and the ids of the pages that rows see
+#pragma unroll 1
             for (int sb = p.seq_status ? (int)blockIdx.x : p.B; sb < p.B; sb += gridDim.x) {
                 const int L = p.prefix_lens[sb], first = p.row_starts[sb], end = p.row_starts[sb + 1];
                 const Seq s = seq_of(p.shape, L, first, end);
@@ -982,6 +1020,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (s.n > 0) {
                     const int lo = p.shape.window > 0 ? max(0, L - p.shape.window + 1) : 0;
                     const int32_t *trow = p.block_table + (size_t)sb * p.max_pages;
+#pragma unroll 1
                     for (int j = lo / p.page_size + lane; j <= (L + s.n - 1) / p.page_size; j += 32) {
                         const int pg = trow[j];
                         if (pg < 0 || pg >= p.num_pages) bad = true;
@@ -990,6 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bad = __any_sync(0xffffffffu, bad);
                 if (lane == 0 && !*abort_flag) p.seq_status[sb] = bad ? SV_ERR_BAD_INPUT : SV_OK;
             }
+#pragma unroll 1
             for (uint32_t q = qpos > 2 ? qpos - 2 : 0; q < qpos; ++q)
                 wait(&sh->q_full[q & 1], (q >> 1) & 1);
         }

@@ -25,8 +25,10 @@ extern "C" long long c_before(int tpt, int window, int L, int n, int i) {
 extern "C" int c_valid(int L, int r0, int r1, int rows, int smax) { return seq_of({32, 0, rows, smax}, L, r0, r1).n; }
 extern "C" int c_ctas(long long U, long long items, int most, int grid) { return ctas_for(U, items, most, grid); }
 extern "C" void c_cut(long long ui, int n, int w, long long U, int nctas, int cta, int *out) {
-    const Cut c = cut_item(ui, n, w, cta_begin(U, nctas, cta), cta_begin(U, nctas, cta + 1), U, nctas, cta);
-    out[0] = c.a; out[1] = c.z; out[2] = c.c_first; out[3] = c.nc;
+    const Cut c = cut_item(ui, n, w, cta_begin(U, nctas, cta), cta_begin(U, nctas, cta + 1));
+    out[0] = c.a; out[1] = c.z;
+    out[2] = cta_of(U, nctas, tile_unit(ui, w, 0));
+    out[3] = cta_of(U, nctas, tile_unit(ui, w, n - 1)) - out[2] + 1;
 }
 """
 
