@@ -110,45 +110,22 @@ __device__ __forceinline__ uint32_t elect_one() {
 // A value that is the same in every lane, as one the compiler knows to be.
 __device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
 
-// The products and the commit of tc::, run by a whole warp and issued by its
-// lane with leader = 1.
-__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
-        : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
-        : "memory");
-}
+// The commit of tc::, run by a whole warp and issued by its lane with leader = 1.
 __device__ __forceinline__ void commit(uint32_t leader, uint64_t *bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
-        "r"(leader)
-        : "memory");
+    if (leader) tc::commit(bar);
 }
 
-// Stream s's S = Q K^T, from the descriptors of its Q tile and the K tile.
+// Stream s's S = Q K^T, from the descriptors of its Q tile and the K tile; by a
+// whole warp, issued by its lane with leader = 1 (as the next).
 template <int D>
 __device__ __forceinline__ void s_products(uint32_t leader, uint32_t tbase, uint32_t s, uint64_t dq, uint64_t dk) {
     constexpr uint32_t idesc = tc::idesc_bf16(kRows, kBK, false);
+    if (leader) {
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-        const uint64_t o = (uint64_t)((kk >> 2) * (kBox >> 4) + (kk & 3) * 2);
-        mma_ss(leader, tbase + kColS + s * kBK, dq + o, dk + o, idesc, kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t o = (uint64_t)((kk >> 2) * (kBox >> 4) + (kk & 3) * 2);
+            tc::mma_bf16(tbase + kColS + s * kBK, dq + o, dk + o, idesc, kk > 0 ? 1u : 0u);
+        }
     }
 }
 // Stream s's O += P V (O = P V where accumulate is 0); V rows 16kk.. start
@@ -157,10 +134,12 @@ template <int D>
 __device__ __forceinline__ void pv_products(uint32_t leader, uint32_t tbase, uint32_t s, uint64_t dv,
                                             uint32_t accumulate) {
     constexpr uint32_t idesc = tc::idesc_bf16(kRows, D, true);
+    if (leader) {
 #pragma unroll
-    for (int kk = 0; kk < kBK / 16; ++kk)
-        mma_ts(leader, tbase + kColO + s * 128, tbase + kColS + s * kBK + kk * 8,
-               dv + (uint64_t)(kk * (2048 >> 4)), idesc, kk > 0 ? 1u : accumulate);
+        for (int kk = 0; kk < kBK / 16; ++kk)
+            tc::mma_bf16_ts(tbase + kColO + s * 128, tbase + kColS + s * kBK + kk * 8,
+                            dv + (uint64_t)(kk * (2048 >> 4)), idesc, kk > 0 ? 1u : accumulate);
+    }
 }
 
 // 16 bytes from 8 floats.
@@ -169,39 +148,18 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                       pack_bf16x2(f[6], f[7]));
 }
 
-// 32 columns of a warp's 32 rows (a lane's row: acc, to out + off) written as
-// bf16.  The lanes of a quad exchange 16-byte pieces first (a 4 x 4 transpose
-// in two rounds), so that a store covers 64 consecutive bytes of 8 rows: one
-// row a lane, its 32 separate lines took the load/store unit four times as
-// long (a step of 16 prompts of 512 rows 91 us, mostly this).  r4: the quad's
-// first row; rows from `rows` on are not written.
-__device__ __forceinline__ void store_quad(uint16_t *out, long long off, const float (&acc)[32], int r4, int rows,
-                                           int lane) {
-    uint32_t c[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int w = 0; w < 4; ++w) c[i][w] = pack_bf16x2(acc[8 * i + 2 * w], acc[8 * i + 2 * w + 1]);
-#pragma unroll
-    for (int b = 1; b <= 2; b <<= 1) {
-        const bool up = (lane & b) != 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (i & b) continue;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? c[i][w] : c[i | b][w], b);
-                if (up) c[i][w] = got;
-                else c[i | b][w] = got;
-            }
-        }
-    }
-    // now c[i] is piece lane & 3 of row r4 + i
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const long long o = __shfl_sync(0xffffffffu, off, (lane & ~3) + i);
-        if (r4 + i < rows)
-            *reinterpret_cast<uint4 *>(out + o + 8 * (lane & 3)) = make_uint4(c[i][0], c[i][1], c[i][2], c[i][3]);
+// 32 bytes of a row: in one store where the output is 32-byte aligned, a whole
+// sector each lane (two stores of 16 bytes cost the load/store unit twice the
+// time with a row a lane; exchanging pieces between lanes first, so that a
+// store covers 64 bytes of 8 rows, costs more instructions than it saves).
+__device__ __forceinline__ void store32(uint16_t *to, const uint32_t (&x)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(x[0]), "r"(x[1]),
+                     "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(to)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<uint4 *>(to)[1] = make_uint4(x[4], x[5], x[6], x[7]);
     }
 }
 
@@ -328,7 +286,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t q_u32 = base_u32 + kStages * kTile;
     Shared *sh = reinterpret_cast<Shared *>(qbuf + 2 * kTile);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (the warp's number as the compiler knows to be the same in all its lanes)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
     if (tid == 0) {
 #pragma unroll 1
@@ -425,6 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tl = tbase + ((uint32_t)(quarter * 32) << 16);
         const uint32_t sbuf = tl + kColS + s * kBK;
         const float sc = p.scale_log2;
+        const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
         uint32_t s_ph = 0, o_ph = 0, x_ph = 0;
         uint32_t gstep = 0;       // steps of the CTA before this item
         uint32_t ring = 0;        // K/V ring position of the item's first tile
@@ -595,26 +555,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc::tmem_ld32(o_cols + 32 * h, ov);
                         tc::wait_ld();
                         float acc[32];
-                        // a share without a visible slot weighs nothing, whatever its O holds
+                        // (a share that no row of its tiles sees has O = 0 and f = 0)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) acc[i] = w1 != 0.f ? __uint_as_float(ov[i]) * f1 : 0.f;
+                        for (int i = 0; i < 32; ++i) acc[i] = __uint_as_float(ov[i]) * f1;
                         if (pair) {
                             tc::tmem_ld32(tl + kColO + (s ^ 1) * 128 + 32 * h, ov);
                             tc::wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                acc[i] = w2 != 0.f ? __fmaf_rn(__uint_as_float(ov[i]), f2, acc[i]) : acc[i];
+                            for (int i = 0; i < 32; ++i) acc[i] = __fmaf_rn(__uint_as_float(ov[i]), f2, acc[i]);
                         }
-                        if (whole && rows > 8) {
-                            store_quad(p.out, out_off + 32 * h, acc, r & ~3, rows, lane);
-                        } else if (whole) {
+                        if (whole) {
                             if (!valid) continue;
+                            uint16_t *to = p.out + out_off + 32 * h;
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                float e[8];
+                            for (int c = 0; c < 2; ++c) {
+                                uint32_t x[8];
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) e[i] = acc[8 * c + i];
-                                *reinterpret_cast<uint4 *>(p.out + out_off + 32 * h + 8 * c) = pack8(e);
+                                for (int i = 0; i < 8; ++i) x[i] = pack_bf16x2(acc[16 * c + 2 * i], acc[16 * c + 2 * i + 1]);
+                                store32(to + 16 * c, x, wide);
                             }
                         } else if (valid) {
                             float4 *po = part_o<D>(p, blockIdx.x, pslot, qt) + r;
@@ -728,8 +686,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == 9) {
             // ===================== the products, in step order.  The whole warp runs the
             // loop with values that are the same in every lane (the item's by a
-            // warp-wide maximum, the waits' by a vote), and one elected lane's
-            // predicate issues: a loop that only lane 0 ran made the compiler move
+            // warp-wide maximum, the waits' by a vote), and one elected lane
+            // issues: a loop that only lane 0 ran made the compiler move
             // every operand of every product to the uniform registers anew, and the
             // issue, ~88 cycles a product against the tensor core's 64, set the pace
             // (a chunk of 4096 rows after 28672 slots: 1924 us).
