@@ -64,6 +64,7 @@ def lib() -> ctypes.CDLL:
                               "run __graft_entry__.build() or python -m "
                               "speculative_decoding_verification_81_gb300.build")
         _lib = load(_build.LIB_PATH)
+        _bind_to(_lib)
     return _lib
 
 
@@ -72,7 +73,29 @@ def use_library(path: str) -> ctypes.CDLL:
     the same sources, e.g. the phase-stamped one of the ``phases`` tool)."""
     global _lib
     _lib = load(path)
+    _bind_to(_lib)
     return _lib
+
+
+_bind = None   # the marshalling extension, and the library it calls
+_bound = None
+
+
+def _bind_to(L):
+    global _bind, _bound
+    if os.path.exists(_build.BIND_PATH):
+        from . import _sv_bind
+        names = ("sv_build_block_tables", "sv_release_pages", "sv_append_kv_paged", "sv_chunk_attention_paged")
+        _sv_bind.use(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names))
+        _bind, _bound = _sv_bind, L
+
+
+def _native():
+    """The extension that marshals the plain form of the paged-cache calls, when
+    it is built and calls the library in use.  Its functions return None, having
+    launched nothing, for every call they do not take: the checks below then
+    name what is wrong with it, or make it."""
+    return _bind if lib() is _bound else None
 
 
 def load(path: str) -> ctypes.CDLL:
@@ -621,6 +644,11 @@ def sv_build_block_tables(prefix_lens, new_lens, page_counts, block_table, free_
     int32, free_count [1] int32 (a stack); num_rows: rows of the packed batch.
     Returns (row_starts [B+1], slot_map [num_rows], new_page_counts [B],
     new_free_count [1]), int32."""
+    if row_starts is slot_map is new_page_counts is new_free_count is stream is None and (native := _native()) is not None:
+        r = native.build_block_tables(prefix_lens, new_lens, page_counts, block_table, free_pages, free_count,
+                                      page_size, num_rows, seq_status)
+        if r is not None:
+            return r
     i32 = torch.int32
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be a tensor of 2 dims")
@@ -664,6 +692,11 @@ def sv_release_pages(keep_lens, page_counts, block_table, free_pages, free_count
     """keep_lens, page_counts [B] int32; block_table [B,max_pages] int32;
     free_pages [num_pages] int32 (the pages given back written in place),
     free_count [1] int32.  Returns (new_page_counts [B], new_free_count [1]), int32."""
+    if new_page_counts is new_free_count is stream is None and (native := _native()) is not None:
+        r = native.release_pages(keep_lens, page_counts, block_table, free_pages, free_count, page_size,
+                                 seq_status)
+        if r is not None:
+            return r
     i32 = torch.int32
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be a tensor of 2 dims")
@@ -704,6 +737,10 @@ def sv_append_kv_paged(k_new, v_new, slot_map, k_pages, v_pages, row_status=None
     """k_new, v_new [num_rows,Hkv,D] bf16 or f32 (rows may lie apart: parts of a
     fused projection); slot_map [num_rows] int32 (-1: padding).  Writes the
     rows into k_pages/v_pages [num_pages,Hkv,page_size,D] bf16, in place."""
+    if stream is None and (native := _native()) is not None:
+        r = native.append_kv_paged(k_new, v_new, slot_map, k_pages, v_pages, row_status)
+        if r is not None:
+            return
     p_k, p_v, dev = _pages(k_pages, v_pages)
     num_pages, Hkv, page_size, D = k_pages.shape
     p_kn, k_stride = _rows(k_new, "k_new", Hkv, dev)
@@ -754,6 +791,13 @@ def sv_chunk_attention_paged(q, k_pages, v_pages, block_table, prefix_lens, row_
     [B,max_pages], prefix_lens [B], row_starts [B+1] int32; window: slots a
     row sees at most (0: all before it).  Returns out [num_rows,Hq,D] bf16, or
     (out, lse [num_rows,Hq] f32) with return_lse or a given lse."""
+    if scale is None and isinstance(q, torch.Tensor) and q.dim() == 3:
+        scale = 1.0 / math.sqrt(q.shape[2] or 1)
+    if out is lse is ws is stream is None and (native := _native()) is not None:
+        r = native.chunk_attention_paged(q, k_pages, v_pages, block_table, prefix_lens, row_starts, scale, window,
+                                         return_lse, seq_status, _chunk_ws)
+        if r is not None:
+            return r
     bf16, i32 = torch.bfloat16, torch.int32
     p_k, p_v, dev = _pages(k_pages, v_pages)
     num_pages, Hkv, page_size, D = k_pages.shape
@@ -771,8 +815,6 @@ def sv_chunk_attention_paged(q, k_pages, v_pages, block_table, prefix_lens, row_
     p_row = _arr(row_starts, "row_starts", i32, (B + 1,), dev)
     p_st = _opt_arr(seq_status, "seq_status", i32, (B,), dev)
     _need_int(window, "window")
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
     with _Launch(dev, stream) as s:
         if out is None:
             out = torch.empty((num_rows, Hq, D), dtype=bf16, device=dev)

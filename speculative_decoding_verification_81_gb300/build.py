@@ -1,4 +1,5 @@
-"""Build libspecverify.so in place (nvcc, sm_103a only, one -gencode).
+"""Build libspecverify.so in place (nvcc, sm_103a only, one -gencode), and
+``_sv_bind.so``, the extension that marshals the paged-cache calls (g++).
 
 The translation units compile in parallel into ``_build/`` beside the
 package and link into ``libspecverify.so`` next to this file.  A rebuild
@@ -16,6 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(HERE, "libspecverify.so")
+BIND_PATH = os.path.join(HERE, "_sv_bind.so")
+BIND_SOURCE = os.path.join(CSRC, "sv_bind.cpp")
 
 SOURCES = ["sv_api.cu", "sv_attention.cu", "sv_attention_tc.cu", "sv_vocab.cu", "sv_compact.cu",
            "sv_noalloc.cu", "sv_step.cu", "sv_pages.cu",
@@ -41,10 +44,47 @@ def up_to_date(lib_path: str = LIB_PATH) -> bool:
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
+def _start_bind():
+    """g++ at work on the extension (torch's and Python's headers): the process
+    and the file it writes."""
+    import sysconfig
+
+    import torch
+    troot = os.path.join(os.path.dirname(torch.__file__))
+    inc = [os.path.join(troot, "include"), os.path.join(troot, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"],
+           os.path.join(os.path.dirname(os.path.dirname(_nvcc())) or "/usr/local/cuda", "include")]
+    tmp = BIND_PATH + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", *[f"-isystem{i}" for i in inc], BIND_SOURCE, "-o", tmp,
+           f"-L{os.path.join(troot, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT), tmp
+
+
+def bind_up_to_date() -> bool:
+    if not os.path.exists(BIND_PATH):
+        return False
+    t = os.path.getmtime(BIND_PATH)
+    return all(os.path.getmtime(p) <= t for p in [BIND_SOURCE, *glob.glob(os.path.join(INCLUDE, "*.h"))])
+
+
 def build(force: bool = False, verbose: bool = False, defines=(), lib_path: str = LIB_PATH,
           build_dir: str = BUILD_DIR) -> str:
     """Compile the library; `defines` (e.g. SV_PHASE_STAMPS) go to every
     translation unit, for a diagnostic build at another `lib_path`."""
+    bind = None
+    if lib_path == LIB_PATH and (force or not bind_up_to_date()):
+        bind = _start_bind()
+    try:
+        return _build_lib(force, verbose, defines, lib_path, build_dir)
+    finally:
+        if bind is not None:
+            out, _ = bind[0].communicate()
+            if bind[0].returncode != 0:
+                raise RuntimeError(f"g++ failed for {BIND_SOURCE}:\n{out.decode(errors='replace')}")
+            os.replace(bind[1], BIND_PATH)
+
+
+def _build_lib(force, verbose, defines, lib_path, build_dir) -> str:
     if not force and up_to_date(lib_path):
         return lib_path
     os.makedirs(build_dir, exist_ok=True)
