@@ -16,7 +16,7 @@ constexpr int kThreads = 32 * 12;
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;  // 256 x 200 + 128 x 104 = 384 x 168
 constexpr int kLaunchRegs = 168;
 constexpr int kItems = 4;                // items published ahead
-constexpr int kWarpPlanB = 32;           // sequences up to which one warp plans alone
+constexpr int kWarpPlanB = 128;          // sequences up to which one warp plans alone
 constexpr int kNone = INT32_MIN;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units the maximum grows before O is rescaled

@@ -201,71 +201,103 @@ __device__ __forceinline__ float2 *part_ml(const Params &p, int cta, int slot, i
 }
 
 // The nc partials of this warp's rows (row0 .. row0 + nv - 1 of Q tile qt)
-// merged in index order and written out.  A lane takes IDX groups of 8
-// columns at a time and passes over the parts once, PARTS of them in flight,
-// with a running maximum (IDX = 2, PARTS = 2 for the few parts of a chunk's
-// item, 1 and 8 for a single token spread over many CTAs: a round of loads
+// merged in index order and written out, for few rows: a lane takes 8 columns
+// of a row and passes over the parts once, eight in flight, with a running
+// maximum (a single token spread over many CTAs has many; a round of loads
 // takes about a microsecond).  Out of line, since a call runs it once or
 // twice.  out_off and lse_off: lane r's row in `out` and `lse`.
-template <int D, int IDX, int PARTS>
-__device__ __noinline__ void merge_parts(const float4 *part_o, const float2 *part_ml, uint16_t *out, float *lse,
-                                         int nc, int nv, int lane, long long out_off, long long lse_off) {
+template <int D>
+__device__ __noinline__ void merge_few(const float4 *part_o, const float2 *part_ml, uint16_t *out, float *lse,
+                                       int nc, int nv, int lane, long long out_off, long long lse_off) {
     // from part to part: the first is in its CTA's slot 1, the others in their CTAs' slot 0
     constexpr size_t kO = (size_t)2 * (D / 4) * kRows, kMl = 2 * kRows;  // a slot (two Q tiles)
+    constexpr int kParts = 8;
     const int total = nv * (D / 8);
 #pragma unroll 1
-    for (int idx0 = 0; idx0 < total; idx0 += 32 * IDX) {
-        int c8[IDX], r[IDX];
-        float acc[IDX][8] = {}, M[IDX], l[IDX];
-#pragma unroll
-        for (int q = 0; q < IDX; ++q) {
-            const int idx = min(idx0 + 32 * q + lane, total - 1);
-            c8[q] = idx / nv;
-            r[q] = idx - c8[q] * nv;
-            M[q] = kNegInf;
-            l[q] = 0.f;
-        }
+    for (int idx0 = 0; idx0 < total; idx0 += 32) {
+        const int idx = min(idx0 + lane, total - 1), c8 = idx / nv, r = idx - c8 * nv;
+        float acc[8] = {}, M = kNegInf, l = 0.f;
 #pragma unroll 1
-        for (int i0 = 0; i0 < nc; i0 += PARTS) {
-            float2 ml[IDX][PARTS];
-            float4 x[IDX][PARTS], y[IDX][PARTS];
+        for (int i0 = 0; i0 < nc; i0 += kParts) {
+            float2 ml[kParts];
+            float4 x[kParts], y[kParts];
 #pragma unroll
-            for (int q = 0; q < IDX; ++q)
+            for (int u = 0; u < kParts; ++u) {
+                const int i = min(i0 + u, nc - 1), slot = 2 * i + (i == 0 ? 1 : 0);
+                ml[u] = __ldcg(part_ml + slot * kMl + r);
+                x[u] = __ldcg(part_o + slot * kO + (size_t)(2 * c8) * kRows + r);
+                y[u] = __ldcg(part_o + slot * kO + (size_t)(2 * c8 + 1) * kRows + r);
+            }
 #pragma unroll
-                for (int u = 0; u < PARTS; ++u) {
-                    const int i = min(i0 + u, nc - 1), slot = 2 * i + (i == 0 ? 1 : 0);
-                    ml[q][u] = __ldcg(part_ml + slot * kMl + r[q]);
-                    x[q][u] = __ldcg(part_o + slot * kO + (size_t)(2 * c8[q]) * kRows + r[q]);
-                    y[q][u] = __ldcg(part_o + slot * kO + (size_t)(2 * c8[q] + 1) * kRows + r[q]);
-                }
+            for (int u = 0; u < kParts; ++u) {
+                // (a part without a visible slot weighs nothing)
+                if (i0 + u >= nc || ml[u].x == kNegInf) continue;
+                const float Mn = fmaxf(M, ml[u].x);
+                const float f = M == kNegInf ? 0.f : ex2_approx(M - Mn), w = ex2_approx(ml[u].x - Mn);
+                M = Mn;
+                l = l * f + ml[u].y * w;
+                const float o[8] = {x[u].x, x[u].y, x[u].z, x[u].w, y[u].x, y[u].y, y[u].z, y[u].w};
 #pragma unroll
-            for (int q = 0; q < IDX; ++q)
-#pragma unroll
-                for (int u = 0; u < PARTS; ++u) {
-                    // (a part without a visible slot has no O: select, never multiply, it)
-                    if (i0 + u >= nc || ml[q][u].x == kNegInf) continue;
-                    const float Mn = fmaxf(M[q], ml[q][u].x);
-                    const float f = M[q] == kNegInf ? 0.f : ex2_approx(M[q] - Mn), w = ex2_approx(ml[q][u].x - Mn);
-                    M[q] = Mn;
-                    l[q] = l[q] * f + ml[q][u].y * w;
-                    const float o[8] = {x[q][u].x, x[q][u].y, x[q][u].z, x[q][u].w,
-                                        y[q][u].x, y[q][u].y, y[q][u].z, y[q][u].w};
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) acc[q][e] = __fmaf_rn(o[e], w, acc[q][e] * f);
-                }
-        }
-#pragma unroll
-        for (int q = 0; q < IDX; ++q) {
-            const long long off = __shfl_sync(0xffffffffu, out_off, r[q]);
-            const long long loff = __shfl_sync(0xffffffffu, lse_off, r[q]);
-            const float inv = l[q] > 0.f ? 1.f / l[q] : 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc[q][e] *= inv;
-            if (idx0 + 32 * q + lane < total) {
-                *reinterpret_cast<uint4 *>(out + off + 8 * c8[q]) = pack8(acc[q]);
-                if (lse && c8[q] == 0) lse[loff] = l[q] > 0.f ? M[q] * kLn2 + logf(l[q]) : kNegInf;
+                for (int e = 0; e < 8; ++e) acc[e] = __fmaf_rn(o[e], w, acc[e] * f);
             }
         }
+        const long long off = __shfl_sync(0xffffffffu, out_off, r);
+        const long long loff = __shfl_sync(0xffffffffu, lse_off, r);
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] *= inv;
+        if (idx0 + lane < total) {
+            *reinterpret_cast<uint4 *>(out + off + 8 * c8) = pack8(acc);
+            if (lse && c8 == 0) lse[loff] = l > 0.f ? M * kLn2 + logf(l) : kNegInf;
+        }
+    }
+}
+
+// The same for many rows (nv of 16 or more): a lane takes its row, 32 columns
+// and two parts at a time.
+template <int D>
+__device__ __noinline__ void merge_rows(const float4 *part_o, const float2 *part_ml, uint16_t *out, float *lse, int nc,
+                                        int nv, int lane, bool wide) {
+    constexpr size_t kO = (size_t)2 * (D / 4) * kRows, kMl = 2 * kRows;
+    if (lane >= nv) return;
+#pragma unroll 1
+    for (int h = 0; h < D / 32; ++h) {
+        float acc[32] = {}, M = kNegInf, l = 0.f;
+#pragma unroll 1
+        for (int i0 = 0; i0 < nc; i0 += 2) {
+            float2 ml[2];
+            float4 o[2][8];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int i = min(i0 + u, nc - 1), slot = 2 * i + (i == 0 ? 1 : 0);
+                ml[u] = __ldcg(part_ml + slot * kMl + lane);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) o[u][c] = __ldcg(part_o + slot * kO + (size_t)(8 * h + c) * kRows + lane);
+            }
+            // (a part without a visible slot weighs nothing; M stays at -inf before the first that has one)
+            if (i0 + 1 >= nc) ml[1].x = kNegInf;
+            const float Mn = fmaxf(M, fmaxf(ml[0].x, ml[1].x));
+            const float base = Mn == kNegInf ? 0.f : Mn;
+            const float f = ex2_approx(M - base), w0 = ex2_approx(ml[0].x - base), w1 = ex2_approx(ml[1].x - base);
+            M = Mn;
+            l = l * f + ml[0].y * w0 + (w1 != 0.f ? ml[1].y * w1 : 0.f);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const float a[4] = {o[0][c].x, o[0][c].y, o[0][c].z, o[0][c].w};
+                const float b[4] = {o[1][c].x, o[1][c].y, o[1][c].z, o[1][c].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[4 * c + e] = __fmaf_rn(b[e], w1, __fmaf_rn(a[e], w0, acc[4 * c + e] * f));
+            }
+        }
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            uint32_t x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = pack_bf16x2(acc[16 * c + 2 * i] * inv, acc[16 * c + 2 * i + 1] * inv);
+            store32(out + 32 * h + 16 * c, x, wide);
+        }
+        if (lse && h == 0) *lse = l > 0.f ? M * kLn2 + logf(l) : kNegInf;
     }
 }
 
@@ -337,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc::fence_after();
     // ---- many sequences: the units before each thread's share of them, for the
-    // walking warp (up to 32 sequences it sums alone), in the still idle Q tiles
+    // walking warp (up to kWarpPlanB sequences it sums alone), in the still idle Q tiles
     long long *before = reinterpret_cast<long long *>(qbuf);
     const int per = (p.B + kThreads - 1) / kThreads;
     if (p.B > kWarpPlanB) {
@@ -605,8 +637,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int nv = min(32, rows - quarter * 32);
                         // (not through a pointer to either: with an indirect call in it
                         // the kernel is built without its register split)
-                        if (it.nc > 4) merge_parts<D, 1, 8>(po, pm, p.out, p.lse, it.nc, nv, lane, out_off, lse_off);
-                        else merge_parts<D, 2, 2>(po, pm, p.out, p.lse, it.nc, nv, lane, out_off, lse_off);
+                        if (nv >= 16) merge_rows<D>(po, pm, p.out + out_off, p.lse ? p.lse + lse_off : nullptr, it.nc, nv, lane, wide);
+                        else merge_few<D>(po, pm, p.out, p.lse, it.nc, nv, lane, out_off, lse_off);
                     }
                 }
             }
@@ -625,6 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int ps = p.page_size;
             const int sub = ps < kBK ? ps : kBK;          // rows of a box
             const int npg = kBK / sub;                    // boxes a tile and half
+            const int tpp = ps < kBK ? 1 : ps / kBK;      // tiles a page (of 128 slots or more)
             const int pg_l = lane & 15, half = lane >> 4;
             const bool lane_on = pg_l < npg && half < kHalves;
             const uint64_t once = l2_policy_evict_first();
@@ -646,10 +679,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // row of this lane's box of tile j in the caches; kNone: no slot of it is seen.  A page id
                 // out of range (reported by the check) reads zeros.
                 auto box_row = [&](int j) -> int {
-                    const int s0 = (it.kt0 + j) * kBK + pg_l * sub;
+                    const int tile = it.kt0 + j, s0 = tile * kBK + pg_l * sub;
                     if (!lane_on || s0 >= hi || s0 + sub <= lo) return kNone;
-                    const int pg = trow[s0 / ps];
-                    return pg >= 0 && pg < p.num_pages ? (pg * p.Hkv + it.h) * ps + s0 % ps : -kBK;
+                    const int page = tpp == 1 ? tile * npg + pg_l : tile / tpp;
+                    const int pg = trow[page];
+                    if (pg < 0 || pg >= p.num_pages) return -kBK;
+                    return (pg * p.Hkv + it.h) * ps + (tpp == 1 ? 0 : (tile - page * tpp) * kBK);
                 };
                 int y = box_row(0);
 #pragma unroll 1
@@ -827,6 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             long long items = 0, x = 0, mine = 0;
             int most = 0;
+            const int few = (p.B + 31) / 32;
             if (p.B > kWarpPlanB) {
                 U = 0;
 #pragma unroll 1
@@ -835,13 +871,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     items += sh->warp_items[w];
                     most = max(most, sh->warp_most[w]);
                 }
-            } else {
-                load(0);
-                mine = un.per_head * p.Hkv;
+            } else {  // a lane sums a few consecutive sequences (their lengths share cache lines)
+                int some = 0;
+#pragma unroll 1
+                for (int i = lane * few; i < min((lane + 1) * few, p.B); ++i) {
+                    const Units v = units_of(p, p.prefix_lens[i], p.row_starts[i], p.row_starts[i + 1]);
+                    mine += v.per_head * p.Hkv;
+                    some += v.items;
+                    most = max(most, v.most);
+                }
                 x = warp_scan(mine, lane);
                 U = __shfl_sync(0xffffffffu, x, 31);
-                items = (long long)__reduce_add_sync(0xffffffffu, un.items) * p.Hkv;
-                most = __reduce_max_sync(0xffffffffu, un.most);
+                items = (long long)__reduce_add_sync(0xffffffffu, some) * p.Hkv;
+                most = __reduce_max_sync(0xffffffffu, most);
             }
             nctas = ctas_for(U, items, most, gridDim.x);
             const bool has = U > 0 && (int)blockIdx.x < nctas;
@@ -862,8 +904,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ub = before[at];
                 __syncwarp();
             } else {
-                b = __ffs(__ballot_sync(0xffffffffu, u0 < x)) - 1;  // (x only grows)
-                ub = __shfl_sync(0xffffffffu, x - mine, b);
+                const int at = __ffs(__ballot_sync(0xffffffffu, u0 < x)) - 1;  // (x only grows)
+                ub = __shfl_sync(0xffffffffu, x - mine, at);
+                b = at * few;
             }
             uint32_t k = 0, qpos = 0;
             bool ok = true;
@@ -883,6 +926,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (u0 > ub) {      // the range starts inside this sequence
                     h = (int)quot(u0 - ub, per_head);
                     const long long v = (u0 - ub) - (long long)h * per_head;
+                    ui = ub + (long long)h * per_head;
                     // the last item whose first unit is at most v: 32 candidates at a time
                     int lo = 0, span = sq.items;
 #pragma unroll 1
@@ -894,8 +938,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         lo += hit * step;
                         span = min(step, span - hit * step);
                     }
-                    i = lo;
-                    ui = ub + (long long)h * per_head + units_before(p.shape, sq, i);
+                    if (lo > 0) {
+                        i = lo;
+                        ui += units_before(p.shape, sq, i);
+                    }
                 }
 #pragma unroll 1
                 for (; ok && h < p.Hkv && ui < u1; ++h, i = 0)

@@ -21,8 +21,8 @@ namespace sv {
 constexpr int kPT = 512;              // threads of the table kernels
 constexpr int kPagesMaxB = 4096;
 constexpr int kPerThread = kPagesMaxB / kPT;
-constexpr int kRowsPerCta = 2048;     // slot-map rows (or pages pushed) a CTA is launched for
-constexpr int kSeqsPerCta = 64;       // sequences whose entries and counts a CTA writes
+constexpr int kRowsPerCta = 512;      // slot-map rows (or pages pushed) a CTA is launched for
+constexpr int kSeqsPerCta = 16;       // sequences whose entries and counts a CTA writes
 
 // Exclusive prefix sum of one value per thread over the CTA; total in *sum.
 __device__ __forceinline__ long long block_scan(long long v, long long *warp_sums, long long *sum) {
@@ -280,7 +280,7 @@ sv_status launch_release_pages(const ReleasePagesArgs &a, cudaStream_t st) {
 // ---------------------------------------------------------------- new rows
 
 constexpr int kAT = 256;
-constexpr int kAUnroll = 4;
+constexpr int kAUnroll = 2;
 
 // One 16-byte piece of a bf16 row from 8 source elements.
 template <bool F32>
