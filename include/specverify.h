@@ -368,7 +368,9 @@ sv_status sv_build_block_tables(const int32_t *prefix_lens, const int32_t *new_l
  * is to keep gives nothing back (back_b = 0), and neither does one whose pages
  * the stack has no room for (free_count + R_b > num_pages: some page is held
  * twice) nor, when free_count is outside [0, num_pages], any: seq_status[b] =
- * SV_ERR_BAD_INPUT, its count unchanged.  The table's entries stay as they are.
+ * SV_ERR_BAD_INPUT, its count unchanged.  The table's entries stay as they
+ * are, and their ids move unchecked: sv_build_block_tables reports one that is
+ * out of range when it hands it out.
  *
  *   Arrays as sv_build_block_tables; keep_lens int32 [B]; free_pages is
  *   written in place.  No other output may alias an input.

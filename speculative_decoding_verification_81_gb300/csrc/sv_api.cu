@@ -318,7 +318,7 @@ sv_status sv_chunk_attention_paged(const void *q, long long q_stride, const void
     if (Hq % Hkv != 0 || !(scale > 0.f) || !std::isfinite(scale)) return SV_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out))
         return SV_ERR_INVALID_ARG;
-    if (q_stride < (long long)Hq * D || q_stride % 8 != 0) return SV_ERR_INVALID_ARG;
+    if (q_stride < (long long)Hq * D || q_stride % 8 != 0 || out == q) return SV_ERR_INVALID_ARG;
     if (B > 4096 || num_rows >= (1 << 30) || (long long)Hq * D >= (1LL << 30) || q_stride >= (1LL << 38) ||
         (long long)max_pages * page_size >= (1LL << 30) || (long long)B * max_pages >= (1LL << 31) ||
         (long long)num_pages * Hkv * page_size >= (1LL << 31))

@@ -121,7 +121,9 @@ sv_status launch_chunk_attention(const ChunkArgs &a, const ChunkPlan &pl, void *
     p.Hq = a.Hq;
     p.Hkv = a.Hkv;
     p.G = G;
-    p.shape = chunk::Shape{tpt, a.window, a.num_rows, a.max_pages * a.page_size};
+    const int S_max = a.max_pages * a.page_size;
+    // (a window as long as the table hides nothing)
+    p.shape = chunk::Shape{tpt, a.window < S_max ? a.window : 0, a.num_rows, S_max};
     p.max_pages = a.max_pages;
     p.num_pages = a.num_pages;
     p.page_size = a.page_size;

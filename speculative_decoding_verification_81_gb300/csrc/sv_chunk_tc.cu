@@ -27,15 +27,26 @@
 //
 // The work list is every (sequence, KV head, item, K/V tile).  A persistent
 // grid takes equal contiguous ranges of it, a tile weighing one for each of the
-// item's Q tiles (sv_chunk_list.h), so the load is even whatever the lengths; an item cut by a range's end leaves partials in the workspace,
-// merged by the warp that arrives last, in index order.
+// item's Q tiles (sv_chunk_list.h), so the load is even whatever the lengths;
+// an item cut by a range's end leaves partials in the workspace, merged by the
+// warp that arrives last, in index order.
 //
 // Warps: 0-3 and 4-7 softmax of streams 0 and 1 (one thread a row); 8 and 11
 // load K and V tiles by TMA through the page table; 9 issues the products; 10
 // walks the work list, publishes the items, loads Q and at the end checks the
 // page table and writes seq_status.  Every wait is bounded.
-#include <type_traits>
-
+//
+// What bounds it (32 query over 8 KV heads of 128, one GB300): long chunks the
+// tensor core -- 4096 rows after 28672 slots 1.31-1.38 ms, 1.5-1.57 PFLOP/s;
+// large batches of single tokens HBM -- 128 after 4096 slots 316-321 us, 6.8
+// TB/s.  In between, a step's chain: S product, softmax of one row a thread
+// (about 1400 cycles a tile), PV product; and for short items the instructions
+// themselves: the roles' code is fetched through one instruction cache, and
+// every shortening of it (loops kept rolled, rare parts out of line) gained
+// several per cent.  Tried without gain: P released in two halves; the softmax
+// in two or four rounds of columns read twice from tensor memory; with D = 64,
+// P in columns of its own so that the next S is made during the softmax;
+// products of 64 rows for few rows; the two streams finishing items in turn.
 #include "sv_chunk.cuh"
 
 namespace sv {
@@ -624,12 +635,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!whole && active) {
                     int *ctr = p.counters + (it.c_first * 2 + qt) * 4 + quarter;
                     int last = 0;
-                    if (lane == 0) {
-                        __threadfence();
-                        last = atomicAdd(ctr, 1) == it.nc - 1;
-                        __threadfence();
+                    if (lane == 0) {  // (its release covers the warp's partials, written before the barrier above)
+                        int before_me;
+                        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before_me) : "l"(ctr) : "memory");
+                        last = before_me == it.nc - 1;
                         if (last) *ctr = 0;  // all have arrived: ready for the next call
                     }
+                    __syncwarp();
                     if (__shfl_sync(0xffffffffu, last, 0))
                     {
                         const float4 *po = part_o<D>(p, it.c_first, 0, qt) + quarter * 32;

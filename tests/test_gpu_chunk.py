@@ -169,6 +169,67 @@ def test_repeats_bit_for_bit():
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def test_rows_of_others_do_not_matter():
+    """NaN and infinity in the query rows of no sequence, and in a neighbour's
+    rows, reach no other row: rows share products but not sums."""
+    c = Case([(300, 5), (40, 70), (7, 1), (1000, 1)], hq=8, hkv=2, seed=20, spare_rows=9)
+    want = c.want()
+    q = c.q.clone()
+    q[77:] = NAN
+    q[5:75] = float("inf")  # the second sequence's
+    c.q = q
+    out, lse = c.run()
+    o, e, ob, eb = want
+    for rows in (slice(0, 5), slice(75, 77)):
+        assert ((out.double() - o).abs() <= ob)[rows].all() and ((lse.double() - e).abs() <= eb)[rows].all()
+
+
+def test_pages_shared_by_sequences():
+    """A prefix's pages in the tables of several sequences, one of them twice."""
+    c = Case([(64, 20), (64, 1), (64, 3)], hq=8, hkv=2, seed=21)
+    c.table[1:, :4] = c.table[0, :4]
+    c.table[2, 3] = c.table[2, 2]
+    c.check()
+
+
+@pytest.mark.parametrize("window", [10 ** 6, 2 ** 31 - 1])
+def test_a_window_longer_than_the_table_hides_nothing(window):
+    c = Case([(700, 40), (5, 1)], hq=4, hkv=2, seed=22)
+    want = c.run()
+    c.window = window
+    got = c.run()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_alignments_and_strides():
+    """An output 16 bytes off a 32-byte boundary, and rows of q a little apart."""
+    c = Case([(300, 70), (90, 1), (64, 17)], hq=4, hkv=2, d=64, seed=23)
+    want = c.run()
+    rows, hq, d = c.q.shape
+    buf = torch.zeros(rows * hq * d + 16, dtype=torch.bfloat16, device="cuda")
+    off = 8 if buf.data_ptr() % 32 == 0 else 0
+    out = buf[off:off + rows * hq * d].view(rows, hq, d)
+    wide = torch.full((rows, hq * d + 8), NAN, dtype=torch.bfloat16, device="cuda")
+    wide[:, :hq * d] = c.q.reshape(rows, -1)
+    c.q = wide.as_strided((rows, hq, d), (hq * d + 8, d, 1))
+    got = c.run(out=out)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    with pytest.raises(sv.SpecVerifyError):  # rows 2 bytes off their 16-byte boundary
+        c.q = wide.as_strided((rows, hq, d), (hq * d + 1, d, 1))
+        c.run()
+    with pytest.raises(sv.SpecVerifyError):  # written over its own queries
+        c.q = out
+        c.run(out=out)
+
+
+@pytest.mark.parametrize("lens,kw", [
+    ([(30, 2100)], dict(hq=128, hkv=1, d=64)),                 # 1050 items a head: two rounds of the search
+    ([(int(x), 1) for x in np.random.default_rng(24).integers(0, 40, 4096)], dict(hq=1, hkv=1, d=64, page_size=8)),
+])
+def test_many_items(lens, kw):
+    Case(lens, seed=24, **kw).check()
+
+
 def test_offsets_past_32_bits():
     """A pool of more than 2^32 elements, the sequence's pages at its end."""
     hkv, ps, d = 8, 16, 128

@@ -179,6 +179,22 @@ def test_append_rows(rows, hkv, d, page_size, wide, strided, seed):
     np.testing.assert_array_equal(host(st), np.where(bad, sv.SV_ERR_BAD_INPUT, sv.SV_OK))
 
 
+def test_append_past_32_bits():
+    """Slots at the end of a pool of more than 2^32 elements."""
+    hkv, ps, d = 8, 16, 128
+    num_pages = (1 << 25) // (hkv * ps) + 3
+    k = torch.empty((num_pages, hkv, ps, d), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    k[-2:], v[-2:] = 0, 0
+    rows = torch.randn((5, hkv, d), device="cuda").to(torch.bfloat16)
+    slots = [num_pages * ps - 1, (num_pages - 1) * ps, num_pages * ps - 5, (num_pages - 2) * ps + 3, -1]
+    sv.sv_append_kv_paged(rows, rows * 2, i32(slots), k, v)
+    torch.cuda.synchronize()
+    for r, s in enumerate(slots[:4]):
+        assert torch.equal(k[s // ps, :, s % ps], rows[r]) and torch.equal(v[s // ps, :, s % ps], rows[r] * 2)
+    assert (k[-2:] != 0).any(-1).sum() == 4 * hkv
+
+
 def test_tables_across_steps_keep_every_page_once():
     """Build, shorten and give back over many steps: the pages in the tables
     and on the stack are always the whole pool, each once."""
