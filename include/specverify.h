@@ -392,7 +392,7 @@ sv_status sv_release_pages(const int32_t *keep_lens, const int32_t *page_counts,
  * A row with s = -1 is padding and skipped; one with s outside
  * [-1, num_pages * page_size) is skipped and row_status[r] = SV_ERR_BAD_INPUT.
  * Two rows must not name one slot (sv_build_block_tables names none twice
- * unless a page is in two tables).
+ * unless a page is in two tables), and the new rows must not overlap the pages.
  *
  *   k_new, v_new  `dtype` [num_rows, Hkv, D], rows k_stride / v_stride
  *                 elements apart (>= Hkv * D, a multiple of 16 bytes: parts

@@ -1,7 +1,8 @@
 """libspecverify: the target model's verification step of speculative
 decoding on one GB300 (sm_103a) -- tree/chain verification attention,
 full-vocabulary stochastic (chain and tree) and greedy (tree) acceptance, KV
-compaction, and the fused step that runs them side by side -- as hand-written
+compaction, the fused step that runs them side by side, and the paged cache
+around it (page tables, new rows, attention of prompt chunks) -- as hand-written
 CUDA kernels behind a C ABI (include/specverify.h), with this thin Python
 binding on top.
 """

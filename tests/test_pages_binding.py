@@ -1,5 +1,6 @@
-"""The page-table, page-release and row-append calls without a GPU: what the
-library refuses on the host, and what the binding refuses before it calls it."""
+"""The paged-cache calls (tables, pages back, new rows, attention of chunks)
+without a GPU: what the library refuses on the host, and what the binding
+refuses before it calls it."""
 import ctypes
 import types
 
@@ -76,6 +77,39 @@ def test_append_host_validation(L):
     assert call(D=100, ks=1024, vs=1024) == sv.SV_ERR_UNSUPPORTED
     assert call(D=512, ks=4096, vs=4096) == sv.SV_ERR_UNSUPPORTED
     assert call(np=1 << 24) == sv.SV_ERR_UNSUPPORTED
+
+
+def test_chunk_attention_host_validation(L):
+    def call(**kw):
+        a = dict(q=FAKE, qs=4096, k=FAKE, v=FAKE, bt=FAKE, mp=8, np=64, ps=16, pl=FAKE, rs=FAKE, B=2, rows=9, Hq=32,
+                 Hkv=8, D=128, scale=0.088, win=0, out=OTHER)
+        a.update(kw)
+        return L.sv_chunk_attention_paged(a["q"], a["qs"], a["k"], a["v"], a["bt"], a["mp"], a["np"], a["ps"], a["pl"],
+                                          a["rs"], a["B"], a["rows"], a["Hq"], a["Hkv"], a["D"], a["scale"], a["win"],
+                                          a["out"], None, None, None, 0, None)
+    for name in ("q", "k", "v", "bt", "pl", "rs", "out"):
+        assert call(**{name: None}) == sv.SV_ERR_INVALID_ARG, name
+    for name in ("mp", "np", "ps", "B", "rows", "Hq", "Hkv", "D"):
+        assert call(**{name: 0}) == sv.SV_ERR_INVALID_ARG, name
+    for name in ("q", "k", "v", "out"):
+        assert call(**{name: MISALIGNED}) == sv.SV_ERR_INVALID_ARG, name
+    assert call(out=FAKE) == sv.SV_ERR_INVALID_ARG                 # written over its own queries
+    assert call(qs=4088) == sv.SV_ERR_INVALID_ARG                  # rows would overlap
+    assert call(qs=4100) == sv.SV_ERR_INVALID_ARG                  # rows off their 16-byte boundaries
+    assert call(ps=24) == sv.SV_ERR_INVALID_ARG                    # neither a power of two nor a multiple of 128
+    assert call(ps=4) == sv.SV_ERR_INVALID_ARG
+    assert call(Hq=30) == sv.SV_ERR_INVALID_ARG                    # Hq % Hkv
+    assert call(win=-1) == sv.SV_ERR_INVALID_ARG
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        assert call(scale=scale) == sv.SV_ERR_INVALID_ARG, scale
+    assert call(D=96) == sv.SV_ERR_UNSUPPORTED
+    assert call(Hq=1032, Hkv=8, qs=1032 * 128) == sv.SV_ERR_UNSUPPORTED   # 129 heads a group
+    assert call(B=4097) == sv.SV_ERR_UNSUPPORTED
+    assert call(mp=1 << 26) == sv.SV_ERR_UNSUPPORTED               # max_pages * page_size
+    assert call(np=1 << 24) == sv.SV_ERR_UNSUPPORTED               # rows of the cache
+    assert call(rows=1 << 30) == sv.SV_ERR_UNSUPPORTED
+    for kw in (dict(Hq=30, Hkv=8, D=128), dict(Hq=32, Hkv=8, D=96), dict(Hq=256, Hkv=1, D=64), dict(Hq=0, Hkv=1, D=64)):
+        assert sv.sv_workspace_size(sv.SV_OP_CHUNK_ATTENTION, 0, 0, **kw) == 0
 
 
 class Recorder:
@@ -200,3 +234,44 @@ def test_append_refuses(rec):
         kw = _append_kw()
         kw[name] = bad
         _refused(rec, api.sv_append_kv_paged, **kw)
+
+
+def _chunk_kw():
+    qkv = torch.zeros((6, 8, 64), dtype=torch.bfloat16)
+    pages = torch.zeros((9, 2, 16, 64), dtype=torch.bfloat16)
+    return dict(q=qkv[:, :4], k_pages=pages, v_pages=pages.clone(), block_table=_i32(3, 5), prefix_lens=_i32(3),
+                row_starts=_i32(4), window=7, out=torch.zeros((6, 4, 64), dtype=torch.bfloat16),
+                lse=torch.zeros((6, 4)), seq_status=_i32(3), ws=torch.zeros(256, dtype=torch.uint8), stream=STREAM)
+
+
+def test_chunk_attention_marshalling(rec):
+    kw = _chunk_kw()
+    out, lse = api.sv_chunk_attention_paged(**kw)
+    name, a = rec.calls[-1]
+    assert name == "sv_chunk_attention_paged" and out is kw["out"] and lse is kw["lse"]
+    assert a[1] == 512 and a[5:8] == (5, 9, 16)            # row stride; max_pages, num_pages, page_size
+    assert a[10:15] == (3, 6, 4, 2, 64)                    # B, num_rows, Hq, Hkv, D
+    assert a[15] == pytest.approx(64 ** -0.5) and a[16] == 7
+    order = ((0, "q"), (2, "k_pages"), (3, "v_pages"), (4, "block_table"), (8, "prefix_lens"), (9, "row_starts"),
+             (17, "out"), (18, "lse"), (19, "seq_status"), (20, "ws"))
+    assert all(a[i] == kw[n].data_ptr() for i, n in order) and a[21] == 256
+    del kw["lse"]
+    assert api.sv_chunk_attention_paged(**kw) is kw["out"]
+    assert rec.calls[-1][1][18] is None
+    out, lse = api.sv_chunk_attention_paged(**kw, return_lse=True)
+    assert lse.shape == (6, 4) and lse.dtype == torch.float32
+
+
+def test_chunk_attention_refuses(rec):
+    bf = torch.bfloat16
+    for name, bad in (("q", torch.zeros((6, 4, 128), dtype=bf)), ("q", torch.zeros((6, 4, 64))), ("q", None),
+                      ("q", torch.zeros((4, 6, 64), dtype=bf).transpose(0, 1)), ("k_pages", torch.zeros((9, 2, 16), dtype=bf)),
+                      ("v_pages", torch.zeros((9, 2, 8, 64), dtype=bf)), ("block_table", _i32(4, 5)),
+                      ("block_table", _i32(15)), ("block_table", torch.zeros((3, 5), dtype=torch.int64)),
+                      ("prefix_lens", _i32(4)), ("row_starts", _i32(3)), ("window", 2.0), ("window", None),
+                      ("out", torch.zeros((6, 4, 32), dtype=bf)), ("lse", torch.zeros((4, 6))),
+                      ("lse", torch.zeros((6, 4), dtype=torch.float64)), ("seq_status", _i32(2)),
+                      ("ws", torch.zeros(8))):
+        kw = _chunk_kw()
+        kw[name] = bad
+        _refused(rec, api.sv_chunk_attention_paged, **kw)
