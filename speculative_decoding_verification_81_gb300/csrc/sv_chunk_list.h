@@ -29,24 +29,34 @@ namespace chunk {
 constexpr int kTileSlots = 128;
 constexpr int kItemCost = 4;  // units of an item's start and end
 
-// Sum of floor((a i + c) / m) for i = 0 .. n - 1 (m > 0): the quotients' whole
-// parts in closed form, the rest by exchanging the roles of slope and
-// modulus, as Euclid's algorithm does.
-SV_HD long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t c) {
-    long long s = 0;
-    while (n > 0) {
-        if (a >= m) {
-            s += (long long)n * (n - 1) / 2 * (a / m);
-            a %= m;
+// Sum of floor((a i + c) / 128) for i = 0 .. n - 1: the quotients' whole parts in
+// closed form, the rest by exchanging the roles of slope and modulus, as
+// Euclid's algorithm does.  The first round divides by shifts and, with slopes
+// that are powers of two, is the last but one; the others divide in 32 bits
+// where they can.
+SV_HD long long floor_sum(uint32_t n, uint32_t a, uint32_t c) {
+    static_assert(kTileSlots == 128, "the shifts");
+    if (n == 0) return 0;
+    long long s = (long long)n * (n - 1) / 2 * (a >> 7) + (long long)n * (c >> 7);
+    unsigned long long y = (unsigned long long)(a & 127) * n + (c & 127);
+    n = (uint32_t)(y >> 7);
+    c = (uint32_t)y & 127;
+    uint32_t m = a & 127;
+    a = 128;
+    while (n > 0) {  // (m > 0: with m = 0 the sum above is all of it)
+        s += (long long)n * (n - 1) / 2 * (a / m);
+        a %= m;
+        s += (long long)n * (c / m);
+        c %= m;
+        y = (unsigned long long)a * n + c;
+        if (y < m) break;
+        if (y >> 32) {
+            n = (uint32_t)(y / m);
+            c = (uint32_t)(y % m);
+        } else {
+            n = (uint32_t)y / m;
+            c = (uint32_t)y - n * m;
         }
-        if (c >= m) {
-            s += (long long)n * (c / m);
-            c %= m;
-        }
-        const unsigned long long y = (unsigned long long)a * n + c;
-        if (y < m) break;  // (with a = 0 always)
-        n = (uint32_t)(y / m);
-        c = (uint32_t)(y % m);
         const uint32_t t = m;
         m = a;
         a = t;
@@ -106,12 +116,12 @@ SV_HD_CALL long long units_before(const Shape &p, const Seq &s, int i) {
     if (i == s.items) u = item_units(p, s, --i);  // the last item may be short
     if (i > 0) {
         const uint32_t tok = 2 * p.tpt;
-        tiles = floor_sum(i, kTileSlots, tok, s.L + tok + kTileSlots - 1);
+        tiles = floor_sum(i, tok, s.L + tok + kTileSlots - 1);
         if (p.window > 0) {
             // first tiles: floor((L + k tok - window + 1) / 128), from the first k at which that is >= 0
             const long long c = (long long)s.L - p.window + 1;
             const long long k0 = c >= 0 ? 0 : (-c + tok - 1) / tok;
-            if (k0 < i) tiles -= floor_sum((uint32_t)(i - k0), kTileSlots, tok, (uint32_t)(c + k0 * tok));
+            if (k0 < i) tiles -= floor_sum((uint32_t)(i - k0), tok, (uint32_t)(c + k0 * tok));
         }
     }
     return u + 2 * tiles + (long long)i * kItemCost;

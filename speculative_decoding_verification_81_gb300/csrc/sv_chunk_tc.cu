@@ -940,20 +940,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const long long v = (u0 - ub) - (long long)h * per_head;
                     ui = ub + (long long)h * per_head;
                     // the last item whose first unit is at most v: 32 candidates at a time
-                    int lo = 0, span = sq.items;
+                    int span = sq.items;
+                    long long at = 0;
 #pragma unroll 1
                     while (span > 1) {
                         const int step = (span + 31) / 32;
-                        const int cand = lo + lane * step;
-                        const bool below = lane * step < span && units_before(p.shape, sq, cand) <= v;
-                        const int hit = 31 - __clz(__ballot_sync(0xffffffffu, below));  // (lane 0 always)
-                        lo += hit * step;
+                        const bool in = lane * step < span;
+                        const long long u = in ? units_before(p.shape, sq, i + lane * step) : 0;
+                        const int hit = 31 - __clz(__ballot_sync(0xffffffffu, in && u <= v));  // (lane 0 always)
+                        at = __shfl_sync(0xffffffffu, u, hit);
+                        i += hit * step;
                         span = min(step, span - hit * step);
                     }
-                    if (lo > 0) {
-                        i = lo;
-                        ui += units_before(p.shape, sq, i);
-                    }
+                    ui += at;
                 }
 #pragma unroll 1
                 for (; ok && h < p.Hkv && ui < u1; ++h, i = 0)

@@ -12,7 +12,7 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 SRC = r"""
 #include "sv_chunk_list.h"
 using namespace sv::chunk;
-extern "C" long long c_floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t c) { return floor_sum(n, m, a, c); }
+extern "C" long long c_floor_sum(uint32_t n, uint32_t a, uint32_t c) { return floor_sum(n, a, c); }
 extern "C" int c_items(int tpt, int window, int L, int n) { return seq_of({tpt, window, 1 << 29, 1 << 29}, L, 5, 5 + n).items; }
 extern "C" int c_tiles(int tpt, int window, int L, int n, int i) {
     const Shape p{tpt, window, 1 << 29, 1 << 29};
@@ -42,7 +42,7 @@ def C(tmp_path_factory):
                            "-fno-sanitize-recover", "-static-libubsan", f"-I{inc}", str(d / "shim.cpp"),
                            "-o", str(d / "shim.so")])
     L = ctypes.CDLL(str(d / "shim.so"))
-    L.c_floor_sum.argtypes = [ctypes.c_uint32] * 4
+    L.c_floor_sum.argtypes = [ctypes.c_uint32] * 3
     L.c_floor_sum.restype = L.c_before.restype = ctypes.c_longlong
     L.c_cut.argtypes = [ctypes.c_longlong, ctypes.c_int, ctypes.c_int, ctypes.c_longlong, ctypes.c_int,
                         ctypes.c_int, ctypes.c_void_p]
@@ -62,11 +62,23 @@ def weight(tpt, n, i):
 
 def test_floor_sum(C):
     rng = np.random.default_rng(1)
-    for _ in range(300):
-        n, m, a, c = (int(rng.integers(lo, hi)) for lo, hi in ((0, 200), (1, 300), (0, 600), (0, 2000)))
-        assert C.c_floor_sum(n, m, a, c) == sum((a * i + c) // m for i in range(n)), (n, m, a, c)
-    n, a, c = 1 << 22, 256, (1 << 30) - 1  # the largest lengths
-    assert C.c_floor_sum(n, 128, a, c) == sum((a * i + c) // 128 for i in range(n))
+    for _ in range(500):
+        n, a, c = (int(rng.integers(lo, hi)) for lo, hi in ((0, 300), (0, 600), (0, 5000)))
+        assert C.c_floor_sum(n, a, c) == sum((a * i + c) // 128 for i in range(n)), (n, a, c)
+    for n, a, c in ((1 << 22, 256, (1 << 30) - 1), (1 << 22, 254, (1 << 30) - 1), (1 << 22, 250, 12345)):
+        assert C.c_floor_sum(n, a, c) == sum((a * i + c) // 128 for i in range(n))  # the largest lengths
+    # items of two tokens up to the longest sequence: in closed form, i // 64 for c = 0
+    n = 1 << 29
+    q, r = divmod(n, 64)
+    assert C.c_floor_sum(n, 2, 0) == 64 * q * (q - 1) // 2 + q * r
+    # slope 127: floor(127 i / 128) = i - ceil(i / 128)
+    assert C.c_floor_sum(n, 127, 0) == n * (n - 1) // 2 - _ceil_sum(n)
+
+
+def _ceil_sum(n):
+    """Sum of ceil(i / 128) for i < n."""
+    q, r = divmod(n - 1, 128)
+    return 128 * q * (q + 1) // 2 + (q + 1) * r
 
 
 def test_units_closed_form(C):
