@@ -4,9 +4,10 @@
 //
 // An item is up to 2 tpt consecutive rows of one sequence and one KV head (one
 // or two Q tiles); its units are kItemCost and, for each 128-slot K/V tile that
-// its rows see, one a Q tile: a tile's time goes with the products and softmax
-// of its Q tiles, and single tokens, paced by the loads, take about as long a
-// tile as a half of a chunk's.
+// its rows see, kOne or kTwo: a tile of two Q tiles takes about 1.6 times as
+// long as one of one, whose loads set its pace, and an item's start and end
+// about as long as two to three tiles (48 tokens beside 2 chunks: 112 us at 1
+// to 2 and 4, 106 us at these).
 // The list runs over sequences, then KV heads, then items; CTA c of nctas
 // takes units floor(U c / nctas) .. floor(U (c + 1) / nctas) - 1 of the U.
 #pragma once
@@ -27,7 +28,8 @@ namespace sv {
 namespace chunk {
 
 constexpr int kTileSlots = 128;
-constexpr int kItemCost = 4;  // units of an item's start and end
+constexpr int kOne = 2, kTwo = 3;  // units of a K/V tile for an item of one and of two Q tiles
+constexpr int kItemCost = 8;       // units of an item's start and end
 
 // Sum of floor((a i + c) / 128) for i = 0 .. n - 1: the quotients' whole parts in
 // closed form, the rest by exchanging the roles of slope and modulus, as
@@ -101,8 +103,8 @@ SV_HD int item_tiles(const Shape &p, const Seq &s, int i) {
     return (s.L + t1 + kTileSlots - 1) / kTileSlots - first_tile(p, s.L + t0);
 }
 
-// Q tiles of item i.
-SV_HD int item_weight(const Shape &p, const Seq &s, int i) { return s.n - i * 2 * p.tpt > p.tpt ? 2 : 1; }
+// Units of a K/V tile of item i.
+SV_HD int item_weight(const Shape &p, const Seq &s, int i) { return s.n - i * 2 * p.tpt > p.tpt ? kTwo : kOne; }
 
 // Units of item i.
 SV_HD int item_units(const Shape &p, const Seq &s, int i) {
@@ -124,7 +126,7 @@ SV_HD_CALL long long units_before(const Shape &p, const Seq &s, int i) {
             if (k0 < i) tiles -= floor_sum((uint32_t)(i - k0), tok, (uint32_t)(c + k0 * tok));
         }
     }
-    return u + 2 * tiles + (long long)i * kItemCost;
+    return u + kTwo * tiles + (long long)i * kItemCost;
 }
 
 // a / b of a >= 0, b > 0.  Numbers below 2^22, as a short call's are, divide in
@@ -152,15 +154,15 @@ SV_HD int cta_of(long long U, int nctas, long long u) { return (int)quot((u + 1)
 // items are few and all alike (their number `items`, the largest and so each
 // of `most` units), a multiple of their number, so that ranges end where
 // items do.
-constexpr int kMinUnits = 4;
+constexpr int kMinUnits = 8;
 
 SV_HD int ctas_for(long long U, long long items, int most, int grid) {
     const long long want = U / kMinUnits > 0 ? U / kMinUnits : 1;
     int n = want < grid ? (int)want : grid;
     if (items > 0 && items <= n && items * most == U && most < (1 << 20)) {
         const int k = (int)items, parts = n / k;  // CTAs an item
-        // a cut item costs its merge, about as long as four units
-        const int even = (most + parts - 1) / parts + (parts > 1 ? 4 : 0), flat = (k * most + n - 1) / n + 4;
+        // a cut item costs its merge, about as long as four tiles
+        const int even = (most + parts - 1) / parts + (parts > 1 ? 4 * kOne : 0), flat = (k * most + n - 1) / n + 4 * kOne;
         if (even <= flat) n = k * parts;
     }
     return n;
@@ -177,12 +179,19 @@ struct Cut {
 
 SV_HD long long tile_unit(long long ui, int w, int tile) { return ui + kItemCost + (long long)w * tile; }
 
+// Tiles of an item (n of w units) whose first unit is before unit d of its tiles'.
+SV_HD int tiles_before(long long d, int n, int w) {
+    if (d <= 0) return 0;
+    if (d >= (long long)w * n) return n;
+    const int x = (int)d + w - 1;
+    return w == kOne ? x / kOne : x / kTwo;
+}
+
 SV_HD Cut cut_item(long long ui, int n, int w, long long u0, long long u1) {
     const long long t = ui + kItemCost;  // the first unit of the first tile
-    const long long a = u0 <= t ? 0 : (u0 - t + w - 1) >> (w - 1), z = u1 <= t ? 0 : (u1 - t + w - 1) >> (w - 1);
     Cut c;
-    c.a = a < n ? (int)a : n;
-    c.z = z < n ? (int)z : n;
+    c.a = tiles_before(u0 - t, n, w);
+    c.z = tiles_before(u1 - t, n, w);
     return c;
 }
 

@@ -26,8 +26,8 @@
 // their (O, m, sum) are merged at the end.
 //
 // The work list is every (sequence, KV head, item, K/V tile).  A persistent
-// grid takes equal contiguous ranges of it, a tile weighing one for each of the
-// item's Q tiles (sv_chunk_list.h), so the load is even whatever the lengths;
+// grid takes equal contiguous ranges of it, weighed by what tiles and items take
+// (sv_chunk_list.h), so the load is even whatever the lengths;
 // an item cut by a range's end leaves partials in the workspace, merged by the
 // warp that arrives last, in index order.
 //

@@ -9,6 +9,7 @@ import numpy as np
 import pytest
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+COST = 8  # units of an item's start and end
 SRC = r"""
 #include "sv_chunk_list.h"
 using namespace sv::chunk;
@@ -57,7 +58,7 @@ def tiles(tpt, window, L, n, i):
 
 
 def weight(tpt, n, i):
-    return 2 if n - i * 2 * tpt > tpt else 1  # Q tiles
+    return 3 if n - i * 2 * tpt > tpt else 2  # two Q tiles or one
 
 
 def test_floor_sum(C):
@@ -93,7 +94,7 @@ def test_units_closed_form(C):
         for i in range(items):
             assert C.c_before(tpt, window, L, n, i) == total, (tpt, window, L, n, i)
             assert C.c_tiles(tpt, window, L, n, i) == tiles(tpt, window, L, n, i)
-            total += 4 + weight(tpt, n, i) * tiles(tpt, window, L, n, i)
+            total += COST + weight(tpt, n, i) * tiles(tpt, window, L, n, i)
         assert C.c_before(tpt, window, L, n, items) == total
 
 
@@ -121,9 +122,9 @@ def test_ranges_cover_every_tile_once(C, sms):
                 for _ in range(int(rng.integers(1, 9)))]
         items = [(tiles(tpt, window, L, n, i), weight(tpt, n, i)) for L, n in seqs for _ in range(hkv)
                  for i in range(-(-n // (2 * tpt)))]
-        U = sum(4 + n * w for n, w in items)
-        nctas = C.c_ctas(U, len(items), max(4 + n * w for n, w in items), sms)
-        assert 1 <= nctas <= sms and (nctas == 1 or U // nctas >= 4)
+        U = sum(COST + n * w for n, w in items)
+        nctas = C.c_ctas(U, len(items), max(COST + n * w for n, w in items), sms)
+        assert 1 <= nctas <= sms and (nctas == 1 or U // nctas >= 8)
         ui, slots = 0, set()
         for n, w in items:
             parts = []
@@ -138,4 +139,4 @@ def test_ranges_cover_every_tile_once(C, sms):
                 if nc > 1:  # a CTA's partial slots are its own: the item it begins, or the one it continues
                     assert (cta, k == 0) not in slots
                     slots.add((cta, k == 0))
-            ui += 4 + n * w
+            ui += COST + n * w
