@@ -37,9 +37,9 @@
 // page table and writes seq_status.  Every wait is bounded.
 //
 // What bounds it (32 query over 8 KV heads of 128, one GB300): long chunks the
-// tensor core -- 4096 rows after 28672 slots 1.31-1.38 ms, 1.5-1.57 PFLOP/s;
-// large batches of single tokens HBM -- 128 after 4096 slots 316-321 us, 6.8
-// TB/s.  In between, a step's chain: S product, softmax of one row a thread
+// tensor core and the power cap -- 4096 rows after 28672 slots 1.19 ms (1.73
+// PFLOP/s) after a pause, 1.31-1.38 ms back to back; large batches of single
+// tokens HBM -- 128 after 4096 slots 316-321 us, 6.8 TB/s.  In between, a step's chain: S product, softmax of one row a thread
 // (about 1400 cycles a tile), PV product; and for short items the instructions
 // themselves: the roles' code is fetched through one instruction cache, and
 // every shortening of it (loops kept rolled, rare parts out of line) gained
