@@ -376,6 +376,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
 
+    // up to 32 sequences: the walking warp's lengths, on their way while the CTA meets
+    int pre = 0, r0 = 0, r1 = 0;
+    if (warp == 10 && p.B <= 32 && lane < p.B) {
+        pre = p.prefix_lens[lane];
+        r0 = p.row_starts[lane];
+        r1 = p.row_starts[lane + 1];
+    }
     tc::fence_before();  // (the barriers and the tensor memory's address)
     __syncthreads();
     tc::fence_after();
@@ -859,8 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ===================== the work list: items of this CTA's units, and their Q tiles
             long long U, u0, u1, ub;  // ub: first unit of sequence b
             int nctas, b;
-            int pre = 0, r0 = 0, r1 = 0;       // lane: lengths of sequence cached + lane
-            Units un{0, 0, 0};                 // and its units
+            Units un{0, 0, 0};        // lane: units of sequence cached + lane (pre, r0, r1: its lengths)
             int cached = -1;
             auto load = [&](int first) {
                 cached = first;
@@ -883,14 +889,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     items += sh->warp_items[w];
                     most = max(most, sh->warp_most[w]);
                 }
-            } else {  // a lane sums a few consecutive sequences (their lengths share cache lines)
+            } else {
                 int some = 0;
+                if (p.B <= 32) {
+                    cached = 0;
+                    un = units_of(p, pre, r0, r1);  // (no rows past the last sequence)
+                    mine = un.per_head * p.Hkv;
+                    some = un.items;
+                    most = un.most;
+                } else {  // a lane sums a few consecutive sequences (their lengths share cache lines)
 #pragma unroll 1
-                for (int i = lane * few; i < min((lane + 1) * few, p.B); ++i) {
-                    const Units v = units_of(p, p.prefix_lens[i], p.row_starts[i], p.row_starts[i + 1]);
-                    mine += v.per_head * p.Hkv;
-                    some += v.items;
-                    most = max(most, v.most);
+                    for (int i = lane * few; i < min((lane + 1) * few, p.B); ++i) {
+                        const Units v = units_of(p, p.prefix_lens[i], p.row_starts[i], p.row_starts[i + 1]);
+                        mine += v.per_head * p.Hkv;
+                        some += v.items;
+                        most = max(most, v.most);
+                    }
                 }
                 x = warp_scan(mine, lane);
                 U = __shfl_sync(0xffffffffu, x, 31);
