@@ -275,3 +275,44 @@ def test_chunk_attention_refuses(rec):
         kw = _chunk_kw()
         kw[name] = bad
         _refused(rec, api.sv_chunk_attention_paged, **kw)
+
+
+def test_arrays_on_other_devices_are_refused(rec):
+    for fn, kw, name in ((api.sv_build_block_tables, _build_kw(), "new_lens"),
+                         (api.sv_release_pages, _release_kw(), "free_pages"),
+                         (api.sv_append_kv_paged, _append_kw(), "slot_map"),
+                         (api.sv_append_kv_paged, _append_kw(), "k_new"),
+                         (api.sv_chunk_attention_paged, _chunk_kw(), "row_starts"),
+                         (api.sv_chunk_attention_paged, _chunk_kw(), "q"),
+                         (api.sv_chunk_attention_paged, _chunk_kw(), "ws")):
+        kw[name] = kw[name].to("meta")
+        _refused(rec, fn, **kw)
+
+
+@pytest.mark.parametrize("current,given", [(1, False), (0, False), (0, True), (1, True)])
+def test_launch_makes_the_tensors_device_and_the_stream_current(monkeypatch, current, given):
+    """The call's device and the given stream are current while it allocates
+    and launches, and what was current before is again afterwards."""
+    log = []
+
+    class Context:
+        def __init__(self, what):
+            self.what = what
+
+        def __enter__(self):
+            log.append(("enter", self.what))
+
+        def __exit__(self, *exc):
+            log.append(("exit", self.what))
+
+    stream = types.SimpleNamespace(cuda_stream=77)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: Context(d.index))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: Context(s))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: types.SimpleNamespace(cuda_stream=100 + d.index))
+    with api._Launch(torch.device("cuda", 1), stream if given else None) as handle:
+        assert handle == (77 if given else 101)
+        inside = list(log)
+    want = ([1] if current != 1 else []) + ([stream] if given else [])
+    assert inside == [("enter", w) for w in want]
+    assert log[len(inside):] == [("exit", w) for w in reversed(want)]
