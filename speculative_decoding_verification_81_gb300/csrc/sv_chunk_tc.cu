@@ -649,8 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (last) *ctr = 0;  // all have arrived: ready for the next call
                     }
                     __syncwarp();
-                    if (__shfl_sync(0xffffffffu, last, 0))
-                    {
+                    if (__shfl_sync(0xffffffffu, last, 0)) {
                         const float4 *po = part_o<D>(p, it.c_first, 0, qt) + quarter * 32;
                         const float2 *pm = part_ml(p, it.c_first, 0, qt) + quarter * 32;
                         const int nv = min(32, rows - quarter * 32);

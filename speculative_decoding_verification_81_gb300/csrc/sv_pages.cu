@@ -83,15 +83,21 @@ __global__ void __launch_bounds__(kPT) build_tables_kernel(BuildTablesArgs a) {
     const bool pool_ok = nfree >= 0 && nfree <= a.num_pages;
     const long long room = (long long)a.max_pages * a.page_size;
 
-    int n[kPerThread];
+    int n[kPerThread], len[kPerThread], cnt[kPerThread];
     long long rows = 0, total_rows, total_need;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {  // every load on its way before the first is used
+        const bool in = b0 + i < b1;
+        n[i] = in ? a.new_lens[b0 + i] : 0;
+        len[i] = in ? a.prefix_lens[b0 + i] : 0;
+        cnt[i] = in ? a.page_counts[b0 + i] : 0;
+    }
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
         const int b = b0 + i;
         if (b >= b1) break;
-        n[i] = a.new_lens[b];
-        prefix[b] = a.prefix_lens[b];
-        held[b] = a.page_counts[b];
+        prefix[b] = len[i];
+        held[b] = cnt[i];
         rows += max(n[i], 0);
     }
     long long row = block_scan(rows, warp_sums, &total_rows);
@@ -102,7 +108,7 @@ __global__ void __launch_bounds__(kPT) build_tables_kernel(BuildTablesArgs a) {
         if (b >= b1) break;
         starts[b] = (int)min(row, (long long)INT32_MAX);
         row += max(n[i], 0);
-        const int L = prefix[b], h = held[b];
+        const int L = len[i], h = cnt[i];
         const bool valid = L >= 0 && n[i] >= 0 && (long long)L + n[i] <= room && h >= 0 &&
                            h <= a.max_pages && h >= pages_of(L, a.page_size) && row <= a.num_rows;
         need[b] = valid ? max(pages_of(L + n[i], a.page_size) - h, 0) : -1;
@@ -139,6 +145,26 @@ __global__ void __launch_bounds__(kPT) build_tables_kernel(BuildTablesArgs a) {
         }
     }
 
+    // The page of row r of the slot map (-1: none) and its offset there.
+    auto page_of = [&](int r, int &off) -> int {
+        off = 0;
+        if (r >= starts[a.B]) return -1;
+        const int b = last_at_most(starts, a.B, r);
+        if (need[b] < 0 || (held[b] & kServed) == 0) return -1;
+        const int at = prefix[b] + r - starts[b];
+        const int j = at / a.page_size, h = held[b] & ~kServed;
+        off = at - j * a.page_size;
+        return j < h ? a.block_table[(size_t)b * a.max_pages + j] : a.free_pages[nfree - 1 - (taken[b] + j - h)];
+    };
+    auto put_slot = [&](int r, int pg, int off) {
+        a.slot_map[r] = pg >= 0 && pg < a.num_pages ? pg * a.page_size + off : -1;
+    };
+    // this CTA's rows of the slot map: the first one's page is on its way while
+    // the sequences are written
+    const int row0 = blockIdx.x * kPT + threadIdx.x;
+    int off0 = 0;
+    const int pg0 = row0 < a.num_rows ? page_of(row0, off0) : -1;
+
     // this CTA's sequences: table entries, counts, first rows, status; a warp each
     const int lane = threadIdx.x & 31;
     const int gwarp = (int)(blockIdx.x * (kPT / 32) + (threadIdx.x >> 5));
@@ -173,20 +199,11 @@ __global__ void __launch_bounds__(kPT) build_tables_kernel(BuildTablesArgs a) {
         }
     }
 
-    // this CTA's rows of the slot map
-    for (int r = blockIdx.x * kPT + threadIdx.x; r < a.num_rows; r += gridDim.x * kPT) {
-        int slot = -1;
-        if (r < starts[a.B]) {
-            const int b = last_at_most(starts, a.B, r);
-            if (need[b] >= 0 && (held[b] & kServed) != 0) {
-                const int at = prefix[b] + r - starts[b];
-                const int j = at / a.page_size, h = held[b] & ~kServed;
-                const int pg = j < h ? a.block_table[(size_t)b * a.max_pages + j]
-                                     : a.free_pages[nfree - 1 - (taken[b] + j - h)];
-                if (pg >= 0 && pg < a.num_pages) slot = pg * a.page_size + at % a.page_size;
-            }
-        }
-        a.slot_map[r] = slot;
+    if (row0 < a.num_rows) put_slot(row0, pg0, off0);
+    for (int r = row0 + (int)gridDim.x * kPT; r < a.num_rows; r += (int)gridDim.x * kPT) {
+        int off;
+        const int pg = page_of(r, off);
+        put_slot(r, pg, off);
     }
 }
 
@@ -205,16 +222,20 @@ __global__ void __launch_bounds__(kPT) release_pages_kernel(ReleasePagesArgs a) 
     const int nfree = *a.free_count;
     const bool pool_ok = nfree >= 0 && nfree <= a.num_pages;
 
-    int held[kPerThread], back[kPerThread];
+    int held[kPerThread], back[kPerThread], keep[kPerThread];
     long long sum = 0, total;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+        const bool in = b0 + i < b1;
+        keep[i] = in ? a.keep_lens[b0 + i] : 0;
+        held[i] = in ? a.page_counts[b0 + i] : 0;
+    }
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
         const int b = b0 + i;
         if (b >= b1) break;
-        const int keep = a.keep_lens[b];
-        held[i] = a.page_counts[b];
-        const int k = keep >= 0 ? pages_of(keep, a.page_size) : 0;
-        const bool valid = keep >= 0 && held[i] >= k && held[i] <= a.max_pages;
+        const int k = keep[i] >= 0 ? pages_of(keep[i], a.page_size) : 0;
+        const bool valid = keep[i] >= 0 && held[i] >= k && held[i] <= a.max_pages;
         back[i] = valid ? held[i] - k : -1;
         kept[b] = k;
         sum += max(back[i], 0);
