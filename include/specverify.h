@@ -399,8 +399,8 @@ sv_status sv_release_pages(const int32_t *keep_lens, const int32_t *page_counts,
  *                 of a fused projection's rows)
  *   slot_map      int32 [num_rows]; row_status int32 [num_rows] or NULL
  *   k_pages, v_pages  bf16 [num_pages, Hkv, page_size, D]
- * Supported: D % 8 == 0, D <= 256, num_pages * Hkv * page_size < 2^31,
- * num_rows < 2^30.
+ * Supported: D % 8 == 0, D <= 256, Hkv * D < 2^30, num_rows < 2^30,
+ * num_pages * Hkv * page_size < 2^31.
  */
 sv_status sv_append_kv_paged(const void *k_new, const void *v_new, sv_dtype dtype,
                              long long k_stride, long long v_stride, const int32_t *slot_map,

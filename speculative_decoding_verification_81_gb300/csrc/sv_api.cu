@@ -294,7 +294,7 @@ sv_status sv_append_kv_paged(const void *k_new, const void *v_new, sv_dtype dtyp
     const long long per16 = dtype == SV_F32 ? 4 : 8, row = (long long)Hkv * D;
     if (k_stride < row || v_stride < row || k_stride % per16 != 0 || v_stride % per16 != 0)
         return SV_ERR_INVALID_ARG;
-    if (D % 8 != 0 || D > 256 || num_rows >= (1 << 30) ||
+    if (D % 8 != 0 || D > 256 || row >= (1LL << 30) || num_rows >= (1 << 30) ||
         (long long)num_pages * Hkv * page_size >= (1LL << 31))
         return SV_ERR_UNSUPPORTED;
     sv::AppendArgs a{k_new, v_new, k_stride,  v_stride,  slot_map, num_rows,

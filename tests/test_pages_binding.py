@@ -79,6 +79,12 @@ def test_append_host_validation(L):
     assert call(np=1 << 24) == sv.SV_ERR_UNSUPPORTED
 
 
+def test_append_rows_past_the_kernels_indexes(L):
+    # 2^23 heads of 256: 2^31 elements a row
+    assert L.sv_append_kv_paged(FAKE, FAKE, sv.SV_BF16, 1 << 31, 1 << 31, FAKE, 1, 1 << 23, 256, 1, 1, FAKE, FAKE,
+                                None, None) == sv.SV_ERR_UNSUPPORTED
+
+
 def test_chunk_attention_host_validation(L):
     def call(**kw):
         a = dict(q=FAKE, qs=4096, k=FAKE, v=FAKE, bt=FAKE, mp=8, np=64, ps=16, pl=FAKE, rs=FAKE, B=2, rows=9, Hq=32,
