@@ -272,8 +272,9 @@ __global__ void __launch_bounds__(kPT) release_pages_kernel(ReleasePagesArgs a) 
 static sv_status table_launch(const void *fn, int B, int words, long long work, cudaStream_t st,
                               void **args) {
     const size_t smem = (size_t)words * sizeof(int);
-    if (smem > 40 * 1024 &&
-        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    // one limit for every call: another thread's cannot lower it before this launch
+    if (smem > 40 * 1024 && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (5 * kPagesMaxB + 1) * (int)sizeof(int)) != cudaSuccess)
         return SV_ERR_CUDA;
     const int sms = device_sm_count();
     if (sms <= 0) return SV_ERR_CUDA;

@@ -243,3 +243,32 @@ def test_tables_captured_and_on_another_stream():
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         np.testing.assert_array_equal(host(a), host(b))
+
+
+def test_tables_from_two_threads_at_once():
+    """Calls whose shared memory is past the default limit by different amounts, from two host threads."""
+    import threading
+    failed = []
+
+    def calls(B):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                past = torch.arange(B, dtype=torch.int32, device="cuda") % 5
+                new, held = torch.ones_like(past), (past + 3) // 4
+                table = torch.zeros(B, 2, dtype=torch.int32, device="cuda")
+                stack = torch.arange(B, dtype=torch.int32, device="cuda")
+                free = torch.tensor([B], dtype=torch.int32, device="cuda")
+            for _ in range(200):
+                r = sv.sv_build_block_tables(past, new, held, table, stack, free, 4, B, stream=stream)
+            stream.synchronize()
+            need = ((torch.arange(B) % 5 + 4) // 4 - (torch.arange(B) % 5 + 3) // 4).sum().item()
+            assert host(r[3])[0] == B - need
+        except Exception as e:
+            failed.append(e)
+    threads = [threading.Thread(target=calls, args=(B,)) for B in (4096, 2100)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
