@@ -446,7 +446,9 @@ sv_status sv_append_kv_paged(const void *k_new, const void *v_new, sv_dtype dtyp
  *                before its first use
  * P is rounded to bf16 for the second product, as in sv_tree_attention; sums,
  * maxima and O are f32.  The result does not depend on how the SMs
- * interleave: cut work is merged in a fixed order.
+ * interleave: cut work is merged in a fixed order.  (num_rows, B, the heads, the
+ * window and the table's width choose between two kernels, which differ by
+ * roundings.)
  * Supported: D = 64 or 128, Hq % Hkv == 0, Hq/Hkv <= 128, B <= 4096, page_size
  * a power of two >= 8 or a multiple of 128, num_rows < 2^30,
  * max_pages * page_size < 2^30, num_pages * Hkv * page_size < 2^31.

@@ -22,7 +22,7 @@ BIND_SOURCE = os.path.join(CSRC, "sv_bind.cpp")
 
 SOURCES = ["sv_api.cu", "sv_attention.cu", "sv_attention_tc.cu", "sv_vocab.cu", "sv_compact.cu",
            "sv_noalloc.cu", "sv_step.cu", "sv_pages.cu",
-           "sv_chunk.cu", "sv_chunk_tc.cu"]
+           "sv_chunk.cu", "sv_chunk_tc.cu", "sv_chunk_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", f"-I{INCLUDE}"]
 

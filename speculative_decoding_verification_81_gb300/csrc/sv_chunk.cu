@@ -101,14 +101,7 @@ sv_status plan_chunk(int Hq, int Hkv, int D, ChunkPlan *plan) {
 }
 
 sv_status launch_chunk_attention(const ChunkArgs &a, const ChunkPlan &pl, void *ws, cudaStream_t st) {
-    const long long rows = (long long)a.num_pages * a.Hkv * a.page_size;
-    const int box_rows = a.page_size < chunk::kBK ? a.page_size : chunk::kBK;
     const int G = a.Hq / a.Hkv, tpt = chunk::kRows / G;
-    CUtensorMap tmk, tmv, tmq, tmq1;
-    if (!cache_map(&tmk, a.k_pages, rows, a.D, box_rows) || !cache_map(&tmv, a.v_pages, rows, a.D, box_rows) ||
-        !q_map(&tmq, a.q, a.num_rows, a.Hq, a.D, a.q_stride, G, tpt) ||
-        !q_map(&tmq1, a.q, a.num_rows, a.Hq, a.D, a.q_stride, G, 1))
-        return SV_ERR_CUDA;
     char *base = static_cast<char *>(ws);
     chunk::Params p{};
     p.out = static_cast<uint16_t *>(a.out);
@@ -131,6 +124,14 @@ sv_status launch_chunk_attention(const ChunkArgs &a, const ChunkPlan &pl, void *
     p.part_o = reinterpret_cast<float *>(base + pl.off_part_o);
     p.part_ml = reinterpret_cast<float *>(base + pl.off_part_ml);
     p.counters = reinterpret_cast<int *>(base + pl.off_counters);
+    if (const int cluster = chunk::few_cluster(a)) return chunk::launch_few(a, p, cluster, st);
+    const long long rows = (long long)a.num_pages * a.Hkv * a.page_size;
+    const int box_rows = a.page_size < chunk::kBK ? a.page_size : chunk::kBK;
+    CUtensorMap tmk, tmv, tmq, tmq1;
+    if (!cache_map(&tmk, a.k_pages, rows, a.D, box_rows) || !cache_map(&tmv, a.v_pages, rows, a.D, box_rows) ||
+        !q_map(&tmq, a.q, a.num_rows, a.Hq, a.D, a.q_stride, G, tpt) ||
+        !q_map(&tmq1, a.q, a.num_rows, a.Hq, a.D, a.q_stride, G, 1))
+        return SV_ERR_CUDA;
     void *args[] = {&tmk, &tmv, &tmq, &tmq1, &p};
     return launch_pdl(chunk::kernel_fn(a.D), dim3(pl.grid), dim3(chunk::kThreads), chunk::smem_bytes(a.D), st,
                       args) == cudaSuccess

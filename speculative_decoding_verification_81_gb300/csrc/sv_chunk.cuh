@@ -73,6 +73,18 @@ struct Shared {
     int abort_flag;
 };
 
+// The form for a few rows over short tables (sv_chunk_few.cu).
+struct FewParams {
+    Params c;  // (of which the workspace's parts are unused)
+    const uint16_t *q, *k, *v;
+    long long q_stride;  // elements between rows of q
+    int cluster;         // CTAs of a row and KV head
+};
+
+// CTAs a row and KV head in that form, 0 where the call does not take it.
+int few_cluster(const ChunkArgs &args);
+sv_status launch_few(const ChunkArgs &args, const Params &params, int cluster, cudaStream_t stream);
+
 const void *kernel_fn(int D);
 int smem_bytes(int D);
 

@@ -1,0 +1,443 @@
+// sv_chunk_few.cu -- the chunk attention's form for few rows: one request or a
+// handful generating, the last tokens of a prompt.
+//
+// Row r of sequence b is at position p = L_b + r - (b's first row) and sees
+// the slots max(0, p - window + 1) .. p.  A cluster of C CTAs takes one row
+// and one KV head, whose G = Hq/Hkv <= 8 query heads share K/V: its warps take
+// units of 16 consecutive slots in turn,
+//     S = scale log2 e K Q^T   (16 slots x 8 heads)
+//     P = 2^(S - m), rounded to bf16; l += sum of the f32 P
+//     O^T += V^T P             (D dims x 8 heads)
+// with a head's running maximum m that moves only when it grows by more than
+// 2^8, the sums in registers; then the CTA's warps meet in its shared memory and
+// the CTAs in that of the one which owns a slice of the row's values, always in
+// the same order.
+//
+// Why a second form: such a call costs the chain of latencies between its start
+// and its last store.  The other form (sv_chunk_tc.cu) passes a tile of 128
+// slots through tensor memory and three warps and merges cut items through L2;
+// 128-row products have no use here, where 8 rows are all that share a slot.
+// The warp's own products of 16 x 8 take K from shared memory as it lies there
+// (which of its dims a column is does not matter as long as Q's are taken alike)
+// and V with two slots' words exchanged, so nothing is transposed but P, a
+// register.  Each half unit's K and V are one copy each (a page holds whole
+// halves), all units of a warp or two of them on their way at once.
+//
+// Measured with K/V from HBM (32 query over 8 KV heads of 128, this form against
+// the other): one token after 511 slots 5.1 us against 10.1, after 2047 7.1
+// against 13.7, after 8191 14.0 against 18.4; 4 tokens after 2047 10.8 against
+// 17.1; 16 rows of a chunk after 900 12.4 against 14.3.  What bounds it: two
+// dependent loads before the first K/V (lengths and pages at once, on the guess
+// that sequence r has row r: 5.4 us without), the copies' latency, the cluster's
+// barrier; from about 256 slots a CTA on, what one SM draws from HBM, 60 GB/s
+// (43 with loads of 16 bytes a lane, whether to registers or shared memory).
+// Tried before: the products by f32 pairs on the ordinary cores (one token after
+// 511 slots the same, after 8191 15.7 us from L2 against 12.5); 4 warps a CTA
+// (5.0 us, but 17.3 after 8191).
+#include <mutex>
+
+#include "sv_chunk.cuh"
+
+namespace sv {
+namespace chunk {
+
+namespace {
+
+constexpr int kFewWarps = 8, kFewThreads = 32 * kFewWarps;
+constexpr int kUnit = 16, kHalf = 8;               // slots of a unit; a page holds whole halves
+constexpr int kFewSlots = 2048;                    // slots a CTA takes at most (32 units a warp hold twice that)
+static_assert(kFewSlots <= 32 * kFewWarps * kUnit, "a lane a unit");
+constexpr int kFewCluster = 16;
+constexpr int kGMax = 8;
+template <int D>
+constexpr int kUnitBytes = kUnit * D * 4;  // K and V
+template <int D>
+constexpr int kFewDepth = 128 * 1024 / (kFewWarps * kUnitBytes<D>);  // units of a warp on their way
+template <int D>
+constexpr int kRingBytes = kFewWarps * kFewDepth<D> * kUnitBytes<D>;
+
+__device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
+    uint4 x;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                 : "r"(a)
+                 : "memory");
+    return x;
+}
+
+// D (16 x 8, f32) += A (16 x 16) B (16 x 8) of bf16, the warp's fragments: with
+// g = lane / 4 and t = lane % 4, a[0..3] hold A at rows g, g + 8, g, g + 8 and
+// columns 2t, 2t + 1 (the last two 8 further), b[0..1] B at rows 2t, 2t + 1 and 8
+// further, column g, and d[0..3] D at (g, 2t), (g, 2t + 1), (g + 8, 2t), (g + 8, 2t + 1).
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The transpose of an 8 x 8 matrix of 16 bits, lane (g, t) with row g, columns 2t and 2t + 1.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t word(const uint4 &x, int i) {
+    return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
+}
+
+}  // namespace
+
+template <int D>
+__global__ void __launch_bounds__(kFewThreads, 1) chunk_few_kernel(const FewParams p) {
+    constexpr int kK = D / 32;  // 16-byte pieces of a K (or Q) row a lane: piece 4 i + t
+    constexpr int kV = D / 64;  // of a V row: piece 8 i + g
+    constexpr int kDepth = kFewDepth<D>;
+    // [warp][unit][K, V][slot][D]; a warp's O [8][D] takes the place of its first unit when it has read its last
+    extern __shared__ __align__(16) uint8_t ring[];
+    auto warp_o = [&](int w) { return reinterpret_cast<float *>(ring + w * kDepth * kUnitBytes<D>); };
+    __shared__ uint64_t full[kFewWarps][kDepth];
+    __shared__ float2 warp_ml[kFewWarps][kGMax];
+    __shared__ __align__(16) float part[kGMax * D];  // [CTA of the cluster][this CTA's slice]
+    __shared__ float2 ml[kFewCluster][kGMax];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int G = p.c.G, C = p.cluster, rank = (int)cluster_ctarank(), pair = (int)blockIdx.x / C;
+    const int row = pair / p.c.Hkv, h = pair - row * p.c.Hkv;
+    const Shape &shape = p.c.shape;
+    if (lane < kDepth) mbar_init(&full[warp][lane], 1);
+    fence_mbar_init();
+    __syncwarp();
+    cluster_arrive_relaxed();  // (waited for before the first store to another CTA)
+    griddep_wait();
+    griddep_launch_dependents();
+
+    // the lengths, a lane a sequence; query head g of the row; and this warp's pages (a lane a
+    // unit), on the guess that sequence `row` has one row, so that their load need not wait
+    int L = 0, r0 = 0, r1 = 0;
+    if (lane < p.c.B) {
+        L = p.c.prefix_lens[lane];
+        r0 = p.c.row_starts[lane];
+        r1 = p.c.row_starts[lane + 1];
+    }
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    uint4 q[kK];
+#pragma unroll
+    for (int i = 0; i < kK; ++i)
+        q[i] = g < G ? ldg_stream(p.q + (size_t)row * p.q_stride + (size_t)(h * G + g) * D + (4 * i + t) * 8) : none;
+    const int step = C * kFewWarps, guess = min(row, p.c.B - 1);
+    int pages[2] = {-1, -1};
+    auto load_pages = [&](int b, int first, int lo, int pos) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int slot = (first + lane * step) * kUnit + x * kHalf;
+            if (slot + kHalf > lo && slot <= pos)
+                pages[x] = p.c.block_table[(size_t)b * p.c.max_pages + slot / p.c.page_size];
+        }
+    };
+    if (shape.window == 0) load_pages(guess, rank * kFewWarps + warp, 0, shape.S_max - 1);
+    const bool ok = lane < p.c.B && lengths_ok(shape, L, r0, r1);
+    const uint32_t mine = __ballot_sync(0xffffffffu, ok && r0 <= row && row < r1);
+    bool lost = false;
+    if (mine != 0) {
+        const int b = __ffs(mine) - 1;
+        const int pos = __shfl_sync(0xffffffffu, L, b) + row - __shfl_sync(0xffffffffu, r0, b);
+        const int lo = shape.window > 0 ? max(0, pos - shape.window + 1) : 0;
+        // this warp's units, and the cache row of each half's first slot (-1: nothing to read)
+        const int first = lo / kUnit + rank * kFewWarps + warp, last = pos / kUnit;
+        const int n = first <= last ? (last - first) / step + 1 : 0;
+        if (shape.window != 0 || b != guess) load_pages(b, first, lo, pos);
+        int at[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int slot = (first + lane * step) * kUnit + x * kHalf;
+            const bool on = lane < n && slot + kHalf > lo && slot <= pos && pages[x] >= 0 && pages[x] < p.c.num_pages;
+            at[x] = on ? (pages[x] * p.c.Hkv + h) * p.c.page_size + slot % p.c.page_size : -1;
+        }
+        uint8_t *const units = ring + warp * kDepth * kUnitBytes<D>;
+        auto fetch = [&](int i, int st) {
+            const int a0 = __shfl_sync(0xffffffffu, at[0], i), a1 = __shfl_sync(0xffffffffu, at[1], i);
+            if (lane == 0) {
+                constexpr uint32_t kB = kHalf * D * 2;
+                uint8_t *to = units + st * kUnitBytes<D>;
+                mbar_arrive_expect_tx(&full[warp][st], ((a0 >= 0) + (a1 >= 0)) * 2 * kB);
+                if (a0 >= 0) {
+                    bulk_load(to, p.k + (size_t)a0 * D, kB, &full[warp][st]);
+                    bulk_load(to + 2 * kB, p.v + (size_t)a0 * D, kB, &full[warp][st]);
+                }
+                if (a1 >= 0) {
+                    bulk_load(to + kB, p.k + (size_t)a1 * D, kB, &full[warp][st]);
+                    bulk_load(to + 3 * kB, p.v + (size_t)a1 * D, kB, &full[warp][st]);
+                }
+            }
+        };
+#pragma unroll 1
+        for (int i = 0; i < kDepth; ++i)
+            if (i < n) fetch(i, i);
+        int st = 0, ph = 0;
+        float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};  // heads 2t and 2t + 1 (l: this lane's slots)
+        float o[4 * kV][4];  // [4 c + r]: dims 64 c + 8 g + 2 r and the next, heads 2t and 2t + 1 each
+#pragma unroll
+        for (int i = 0; i < 4 * kV; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            if (!warp_wait_bounded(&full[warp][st], ph)) {
+                lost = true;
+                for (int k = i + 1; k < min(n, i + kDepth); ++k) {  // its own copies still on their way
+                    if (++st == kDepth) st = 0, ph ^= 1;
+                    warp_wait_bounded(&full[warp][st], ph);
+                }
+                break;
+            }
+            const uint32_t here = smem_u32(units) + (uint32_t)(st * kUnitBytes<D>);
+            const int slot0 = (first + i * step) * kUnit;
+            const bool whole = slot0 >= lo && slot0 + kUnit - 1 <= pos;
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < kK; ++c) {
+                const uint32_t at_k = here + g * (D * 2) + (4 * c + t) * 16;
+                const uint4 k0 = ld_shared16(at_k), k1 = ld_shared16(at_k + kHalf * D * 2);
+                mma16(s, k0.x, k1.x, k0.y, k1.y, q[c].x, q[c].y);
+                mma16(s, k0.z, k1.z, k0.w, k1.w, q[c].z, q[c].w);
+            }
+            const int slot = (first + i * step) * kUnit + g;
+            const bool see0 = slot >= lo && slot <= pos, see1 = slot + 8 >= lo && slot + 8 <= pos;
+            float f[2], e[2][2];
+            bool moved = false;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float s0 = see0 ? s[j] * p.c.scale_log2 : kNegInf;
+                const float s1 = see1 ? s[2 + j] * p.c.scale_log2 : kNegInf;
+                float c = fmaxf(s0, s1);
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, off));
+                const bool up = c > m[j] + kRescaleThreshold;
+                f[j] = up ? ex2_approx(m[j] - c) : 1.f;
+                if (up) m[j] = c;
+                moved = moved || up;
+                const float base = m[j] == kNegInf ? 0.f : m[j];
+                e[0][j] = ex2_approx(s0 - base);
+                e[1][j] = ex2_approx(s1 - base);
+                l[j] = l[j] * f[j] + (e[0][j] + e[1][j]);
+            }
+            if (__any_sync(0xffffffffu, moved) && i > 0) {
+#pragma unroll
+                for (int x = 0; x < 4 * kV; ++x)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) o[x][y] *= f[y & 1];
+            }
+            const uint32_t p0 = transposed(pack_bf16x2(e[0][0], e[0][1]));
+            const uint32_t p1 = transposed(pack_bf16x2(e[1][0], e[1][1]));
+#pragma unroll
+            for (int c = 0; c < kV; ++c) {
+                uint4 v[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const int sl = 2 * t + (y & 1) + (y >> 1) * 8;
+                    v[y] = ld_shared16(here + kUnitBytes<D> / 2 + sl * (D * 2) + (8 * c + g) * 16);
+                    if (!whole && (slot0 + sl < lo || slot0 + sl > pos)) v[y] = none;
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const uint32_t a = word(v[0], r), a1 = word(v[1], r), b0 = word(v[2], r), b1 = word(v[3], r);
+                    // even dims as rows g, odd ones as rows g + 8; two slots a word
+                    mma16(o[4 * c + r], __byte_perm(a, a1, 0x5410), __byte_perm(a, a1, 0x7632),
+                          __byte_perm(b0, b1, 0x5410), __byte_perm(b0, b1, 0x7632), p0, p1);
+                }
+            }
+            __syncwarp();
+            if (i + kDepth < n) fetch(i + kDepth, st);
+            if (++st == kDepth) st = 0, ph ^= 1;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) l[j] += __shfl_xor_sync(0xffffffffu, l[j], off);
+            if (lane < 4) warp_ml[warp][2 * t + j] = make_float2(m[j], l[j]);
+            if (2 * t + j < G) {
+#pragma unroll
+                for (int c = 0; c < kV; ++c) {
+                    float4 *to = reinterpret_cast<float4 *>(warp_o(warp) + (2 * t + j) * D + c * 64 + g * 8);
+                    to[0] = make_float4(o[4 * c][j], o[4 * c][2 + j], o[4 * c + 1][j], o[4 * c + 1][2 + j]);
+                    to[1] = make_float4(o[4 * c + 2][j], o[4 * c + 2][2 + j], o[4 * c + 3][j], o[4 * c + 3][2 + j]);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    cluster_wait();
+    const int pairs = G * D / 2, slice = pairs / C;  // pairs of values: a multiple of 32
+    if (mine != 0) {
+        // the CTA's sums, each to the CTA that owns it
+        for (int x = tid; x < pairs; x += kFewThreads) {
+            const int hd = 2 * x / D;
+            float M = kNegInf;
+            float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kFewWarps; ++i) M = fmaxf(M, warp_ml[i][hd].x);
+#pragma unroll
+            for (int i = 0; i < kFewWarps; ++i) {
+                const float mi = warp_ml[i][hd].x, w = mi == kNegInf ? 0.f : ex2_approx(mi - M);
+                const float2 v = reinterpret_cast<const float2 *>(warp_o(i))[x];
+                acc.x = __fmaf_rn(v.x, w, acc.x);
+                acc.y = __fmaf_rn(v.y, w, acc.y);
+            }
+            const int owner = x / slice;
+            st_cluster_f2(cluster_map(smem_u32(&part[2 * (rank * slice + x - owner * slice)]), (uint32_t)owner), acc);
+        }
+        if (tid < kGMax * C) {
+            const int hd = tid % kGMax, dst = tid / kGMax;
+            float M = kNegInf, sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < kFewWarps; ++i) M = fmaxf(M, warp_ml[i][hd].x);
+#pragma unroll
+            for (int i = 0; i < kFewWarps; ++i) {
+                const float2 x = warp_ml[i][hd];
+                if (x.x != kNegInf) sum = __fmaf_rn(x.y, ex2_approx(x.x - M), sum);
+            }
+            st_cluster_f2(cluster_map(smem_u32(&ml[rank][hd]), (uint32_t)dst), make_float2(M, sum));
+        }
+    }
+    // seq_status: lengths, and the ids of the pages that rows see; a warp a sequence
+    for (int sb = p.c.seq_status ? (int)blockIdx.x * kFewWarps + warp : p.c.B; sb < p.c.B;
+         sb += (int)gridDim.x * kFewWarps) {
+        const int n = __shfl_sync(0xffffffffu, r1 - r0, sb), Ls = __shfl_sync(0xffffffffu, L, sb);
+        bool bad = !__shfl_sync(0xffffffffu, (int)ok, sb);
+        if (!bad && n > 0) {
+            const int lo = shape.window > 0 ? max(0, Ls - shape.window + 1) : 0;
+            const int32_t *trow = p.c.block_table + (size_t)sb * p.c.max_pages;
+            for (int j = lo / p.c.page_size + lane; j <= (Ls + n - 1) / p.c.page_size; j += 32) {
+                const int pg = trow[j];
+                if (pg < 0 || pg >= p.c.num_pages) bad = true;
+            }
+        }
+        bad = __any_sync(0xffffffffu, bad);
+        if (lane == 0) p.c.seq_status[sb] = bad ? SV_ERR_BAD_INPUT : SV_OK;
+    }
+    __syncwarp();
+    cluster_sync();
+    if (mine == 0) return;
+    if (lost && lane == 0 && p.c.seq_status) p.c.seq_status[__ffs(mine) - 1] = SV_ERR_TIMEOUT;
+    // the cluster's sums of this CTA's slice
+    for (int x = tid; x < slice; x += kFewThreads) {
+        const int at = rank * slice + x, hd = 2 * at / D, dim = 2 * at - hd * D;
+        float M = kNegInf, sum = 0.f;
+        float2 acc = make_float2(0.f, 0.f);
+#pragma unroll 4
+        for (int c = 0; c < C; ++c) M = fmaxf(M, ml[c][hd].x);
+#pragma unroll 4
+        for (int c = 0; c < C; ++c) {
+            const float2 y = ml[c][hd], v = reinterpret_cast<const float2 *>(part)[c * slice + x];
+            const float w = y.x == kNegInf ? 0.f : ex2_approx(y.x - M);
+            sum = __fmaf_rn(y.y, w, sum);
+            acc.x = __fmaf_rn(v.x, w, acc.x);
+            acc.y = __fmaf_rn(v.y, w, acc.y);
+        }
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const long long head = (long long)row * p.c.Hq + h * G + hd;
+        reinterpret_cast<uint32_t *>(p.c.out)[(head * D + dim) / 2] = pack_bf16x2(acc.x * inv, acc.y * inv);
+        if (p.c.lse && dim == 0) p.c.lse[head] = sum > 0.f ? M * kLn2 + logf(sum) : kNegInf;
+    }
+}
+
+namespace {
+
+int few_smem(int D) { return D == 128 ? kRingBytes<128> : kRingBytes<64>; }
+
+const void *few_fn(int D) {
+    return D == 128 ? reinterpret_cast<const void *>(&chunk_few_kernel<128>)
+                    : reinterpret_cast<const void *>(&chunk_few_kernel<64>);
+}
+
+// Clusters of `size` CTAs that the device holds at once, asked for once a device.
+int few_capacity(int D, int size) {
+    const void *fn = few_fn(D);
+    struct Entry {
+        int dev;
+        const void *fn;
+        int size, n;
+    };
+    static std::mutex mu;
+    static Entry cache[64];
+    static int ncache = 0;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < ncache; ++i)
+        if (cache[i].dev == dev && cache[i].fn == fn && cache[i].size == size) return cache[i].n;
+    int n = 0;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, few_smem(D)) == cudaSuccess &&
+        (size <= 8 || cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess)) {
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)size;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)size);
+        cfg.blockDim = dim3(kFewThreads);
+        cfg.dynamicSmemBytes = (size_t)few_smem(D);
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) n = 0;
+    }
+    cudaGetLastError();  // (a refused query leaves no error behind)
+    if (ncache < 64) cache[ncache++] = Entry{dev, fn, size, n};
+    return n;
+}
+
+}  // namespace
+
+// The smallest cluster whose warps have a unit each at most (one token after 511
+// slots: 4 CTAs 5.1 us, 8 5.3, 2 6.4), or the largest of which the rows and
+// KV heads all find room at once.  A CTA then takes up to 2048 slots of a single
+// row (after 16383 slots 22.8 us against 25.1 for the other form); of several
+// rows 1024, since theirs may be uneven, which the other form's list evens out
+// (8 tokens after 2047: 16.2 us against 22.9, with a single long one about as long
+// as there).  Lengths are on the device: the table's width stands for them.
+int few_cluster(const ChunkArgs &a) {
+    if (a.Hq / a.Hkv > kGMax || a.B > 32) return 0;
+    const long long pairs = (long long)a.num_rows * a.Hkv, table = (long long)a.max_pages * a.page_size;
+    // (a window's first and last unit are seen in part)
+    const long long slots = a.window > 0 && a.window + 2LL * kUnit < table ? a.window + 2LL * kUnit : table;
+    int best = 0;
+    for (int C = 1; C <= kFewCluster && few_capacity(a.D, C) >= pairs; C *= 2) {
+        best = C;
+        if (slots <= (long long)C * kFewWarps * kUnit) break;
+    }
+    return slots <= (long long)best * (a.num_rows == 1 ? kFewSlots : kFewSlots / 2) ? best : 0;
+}
+
+sv_status launch_few(const ChunkArgs &a, const Params &c, int cluster, cudaStream_t st) {
+    FewParams p{};
+    p.c = c;
+    p.q = static_cast<const uint16_t *>(a.q);
+    p.k = static_cast<const uint16_t *>(a.k_pages);
+    p.v = static_cast<const uint16_t *>(a.v_pages);
+    p.q_stride = a.q_stride;
+    p.cluster = cluster;
+    void *args[] = {&p};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.num_rows * a.Hkv * cluster));
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = (size_t)few_smem(a.D);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelExC(&cfg, few_fn(a.D), args) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+}  // namespace chunk
+}  // namespace sv
