@@ -33,7 +33,8 @@
 // (43 with loads of 16 bytes a lane, whether to registers or shared memory).
 // Tried before: the products by f32 pairs on the ordinary cores (one token after
 // 511 slots the same, after 8191 15.7 us from L2 against 12.5); 4 warps a CTA
-// (5.0 us, but 17.3 after 8191).
+// (5.0 us, but 17.3 after 8191); rows a little apart in shared memory, a copy
+// each, for reads without bank conflicts (5.6 and 16.9: 32 copies a unit for 4).
 #include <mutex>
 
 #include "sv_chunk.cuh"
