@@ -355,41 +355,47 @@ const void *few_fn(int D) {
                     : reinterpret_cast<const void *>(&chunk_few_kernel<64>);
 }
 
-// Clusters of `size` CTAs that the device holds at once, asked for once a device.
-int few_capacity(int D, int size) {
-    const void *fn = few_fn(D);
+// Clusters of 2^i CTAs that the current device holds at once, asked for once a
+// device; zeros where the kernel does not run.
+struct Capacity {
+    int n[5];
+};
+static_assert(kFewCluster == 1 << 4, "sizes of clusters");
+
+Capacity few_capacity(int D) {
     struct Entry {
-        int dev;
-        const void *fn;
-        int size, n;
+        int dev, D;
+        Capacity c;
     };
     static std::mutex mu;
     static Entry cache[64];
     static int ncache = 0;
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    Capacity c{};
+    if (cudaGetDevice(&dev) != cudaSuccess) return c;
     std::lock_guard<std::mutex> lock(mu);
     for (int i = 0; i < ncache; ++i)
-        if (cache[i].dev == dev && cache[i].fn == fn && cache[i].size == size) return cache[i].n;
-    int n = 0;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, few_smem(D)) == cudaSuccess &&
-        (size <= 8 || cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess)) {
+        if (cache[i].dev == dev && cache[i].D == D) return cache[i].c;
+    const void *fn = few_fn(D);
+    const bool smem_ok = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, few_smem(D)) == cudaSuccess;
+    const bool large_ok = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+    for (int i = 0; smem_ok && i < (large_ok ? 5 : 4); ++i) {
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = (unsigned)size;
+        attr[0].val.clusterDim.x = 1u << i;
         attr[0].val.clusterDim.y = 1;
         attr[0].val.clusterDim.z = 1;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)size);
+        cfg.gridDim = dim3(1u << i);
         cfg.blockDim = dim3(kFewThreads);
         cfg.dynamicSmemBytes = (size_t)few_smem(D);
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) n = 0;
+        if (cudaOccupancyMaxActiveClusters(&c.n[i], fn, &cfg) != cudaSuccess) c.n[i] = 0;
     }
     cudaGetLastError();  // (a refused query leaves no error behind)
-    if (ncache < 64) cache[ncache++] = Entry{dev, fn, size, n};
-    return n;
+    if (ncache < 64) cache[ncache++] = Entry{dev, D, c};
+    return c;
 }
 
 }  // namespace
@@ -406,10 +412,11 @@ int few_cluster(const ChunkArgs &a) {
     const long long pairs = (long long)a.num_rows * a.Hkv, table = (long long)a.max_pages * a.page_size;
     // (a window's first and last unit are seen in part)
     const long long slots = a.window > 0 && a.window + 2LL * kUnit < table ? a.window + 2LL * kUnit : table;
+    const Capacity room = few_capacity(a.D);
     int best = 0;
-    for (int C = 1; C <= kFewCluster && few_capacity(a.D, C) >= pairs; C *= 2) {
-        best = C;
-        if (slots <= (long long)C * kFewWarps * kUnit) break;
+    for (int i = 0; i < 5 && room.n[i] >= pairs; ++i) {
+        best = 1 << i;
+        if (slots <= (long long)best * kFewWarps * kUnit) break;
     }
     return slots <= (long long)best * (a.num_rows == 1 ? kFewSlots : kFewSlots / 2) ? best : 0;
 }
