@@ -643,7 +643,7 @@ def sv_build_block_tables(prefix_lens, new_lens, page_counts, block_table, free_
     int32 (the new pages' entries written in place); free_pages [num_pages]
     int32, free_count [1] int32 (a stack); num_rows: rows of the packed batch.
     Returns (row_starts [B+1], slot_map [num_rows], new_page_counts [B],
-    new_free_count [1]), int32 (the three short ones may share one allocation)."""
+    new_free_count [1]), int32 (they may share one allocation)."""
     if row_starts is slot_map is new_page_counts is new_free_count is stream is None and (native := _native()) is not None:
         r = native.build_block_tables(prefix_lens, new_lens, page_counts, block_table, free_pages, free_count,
                                       page_size, num_rows, seq_status)

@@ -74,6 +74,8 @@ at::Tensor part(const at::Tensor &buffer, int64_t at, int64_t n) {
     return t;
 }
 
+constexpr int64_t kShared = 2048;  // ints of a slot map that shares the others' allocation
+
 // A small non-negative int, -1 if the object is another thing.
 int64_t small_int(PyObject *o) {
     if (!PyLong_CheckExact(o)) return -1;
@@ -107,7 +109,10 @@ PyObject *build(PyObject *, PyObject *const *a, Py_ssize_t na) {
     if (bad || !array(tab, at::kInt, dev, {B, mp}) || !i32(stk, dev, np) || !i32(pre, dev, B) || !i32(nw, dev, B) ||
         !i32(cnt, dev, B) || !i32(fc, dev, 1))
         return none();
-    at::Tensor slots = empty({rows}, at::kInt, dev), buffer = empty({2 * B + 2}, at::kInt, dev);
+    // a short slot map too lies with the others (a long one would keep them all alive, or they it)
+    const bool with = rows <= kShared;
+    at::Tensor buffer = empty({2 * B + 2 + (with ? rows : 0)}, at::kInt, dev);
+    at::Tensor slots = with ? part(buffer, 2 * B + 2, rows) : empty({rows}, at::kInt, dev);
     at::Tensor starts = part(buffer, 0, B + 1), counts = part(buffer, B + 1, B), left = part(buffer, 2 * B + 1, 1);
     if (f_build(ip(*pre), ip(*nw), ip(*cnt), ip(*stk), ip(*fc), (int)B, (int)ps, (int)mp, (int)np, (int)rows, ip(*tab),
                 ip(starts), ip(slots), ip(counts), ip(left), st, stream_of(dev)) != SV_OK)
