@@ -13,6 +13,8 @@
 // every CTA repeats the prefix sums over the sequences in shared memory (two
 // loads and two block scans) rather than wait for a first kernel's result,
 // then takes its share of the rows and pages.
+#include <mutex>
+
 #include "sv_device.cuh"
 #include "sv_internal.h"
 
@@ -269,13 +271,32 @@ __global__ void __launch_bounds__(kPT) release_pages_kernel(ReleasePagesArgs a) 
     }
 }
 
+// Room in shared memory for the largest call, asked for once a device and
+// kernel (one limit for every call, so that no thread's lowers another's).
+static bool large_smem(const void *fn) {
+    struct Entry {
+        int dev;
+        const void *fn;
+    };
+    static std::mutex mu;
+    static Entry done[64];
+    static int ndone = 0;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < ndone; ++i)
+        if (done[i].dev == dev && done[i].fn == fn) return true;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (5 * kPagesMaxB + 1) * (int)sizeof(int)) !=
+        cudaSuccess)
+        return false;
+    if (ndone < 64) done[ndone++] = Entry{dev, fn};
+    return true;
+}
+
 static sv_status table_launch(const void *fn, int B, int words, long long work, cudaStream_t st,
                               void **args) {
     const size_t smem = (size_t)words * sizeof(int);
-    // one limit for every call: another thread's cannot lower it before this launch
-    if (smem > 40 * 1024 && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (5 * kPagesMaxB + 1) * (int)sizeof(int)) != cudaSuccess)
-        return SV_ERR_CUDA;
+    if (smem > 40 * 1024 && !large_smem(fn)) return SV_ERR_CUDA;
     const int sms = device_sm_count();
     if (sms <= 0) return SV_ERR_CUDA;
     long long grid = (work + kRowsPerCta - 1) / kRowsPerCta;
