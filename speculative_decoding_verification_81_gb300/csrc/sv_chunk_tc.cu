@@ -468,7 +468,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int j = first; j < it.n; j += stride) {
                 const int kb = (it.kt0 + j) * kBK;
-                if (!(ok = warp_wait_bounded(&sh->s_full[s], s_ph))) break;
+                // (one probe and a vote nearly always suffice; the slow part in line, since a call
+                // here costs the kernel its registers)
+                ok = __all_sync(0xffffffffu, mbar_try_wait(&sh->s_full[s], s_ph)) ||
+                     warp_wait_bounded(&sh->s_full[s], s_ph);
+                if (!ok) break;
                 s_ph ^= 1;
                 tc::fence_after();
                 if (active) {
