@@ -25,6 +25,8 @@ constexpr int kPagesMaxB = 4096;
 constexpr int kPerThread = kPagesMaxB / kPT;
 constexpr int kRowsPerCta = 512;      // slot-map rows (or pages pushed) a CTA is launched for
 constexpr int kSeqsPerCta = 16;       // sequences whose entries and counts a CTA writes
+constexpr int kAloneBytes = 116 << 10;  // shared memory that only one CTA an SM finds
+static_assert((5 * kPagesMaxB + 1) * 4 <= kAloneBytes, "the largest call");
 
 // Exclusive prefix sum of one value per thread over the CTA; total in *sum.
 __device__ __forceinline__ long long block_scan(long long v, long long *warp_sums, long long *sum) {
@@ -271,8 +273,8 @@ __global__ void __launch_bounds__(kPT) release_pages_kernel(ReleasePagesArgs a) 
     }
 }
 
-// Room in shared memory for the largest call, asked for once a device and
-// kernel (one limit for every call, so that no thread's lowers another's).
+// Room in shared memory for any call, asked for once a device and kernel
+// (one limit for every call, so that no thread's lowers another's).
 static bool large_smem(const void *fn) {
     struct Entry {
         int dev;
@@ -286,23 +288,26 @@ static bool large_smem(const void *fn) {
     std::lock_guard<std::mutex> lock(mu);
     for (int i = 0; i < ndone; ++i)
         if (done[i].dev == dev && done[i].fn == fn) return true;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (5 * kPagesMaxB + 1) * (int)sizeof(int)) !=
-        cudaSuccess)
-        return false;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kAloneBytes) != cudaSuccess) return false;
     if (ndone < 64) done[ndone++] = Entry{dev, fn};
     return true;
 }
 
 static sv_status table_launch(const void *fn, int B, int words, long long work, cudaStream_t st,
                               void **args) {
-    const size_t smem = (size_t)words * sizeof(int);
-    if (smem > 40 * 1024 && !large_smem(fn)) return SV_ERR_CUDA;
+    size_t smem = (size_t)words * sizeof(int);
     const int sms = device_sm_count();
     if (sms <= 0) return SV_ERR_CUDA;
     long long grid = (work + kRowsPerCta - 1) / kRowsPerCta;
     if (grid < (B + kSeqsPerCta - 1) / kSeqsPerCta) grid = (B + kSeqsPerCta - 1) / kSeqsPerCta;
     if (grid > sms) grid = sms;
     if (grid < 1) grid = 1;
+    // A grid that takes most SMs has them to itself: the next call's CTAs, launched
+    // early, otherwise met four together on the SMs that this one leaves free, and ran
+    // as much longer (tables for 2048 requests call after call 9.4 us, so 6.5; for
+    // 4096 11.9 or 17.5, so 11.9).
+    if (grid > sms / 2 && smem < kAloneBytes) smem = kAloneBytes;
+    if (smem > 40 * 1024 && !large_smem(fn)) return SV_ERR_CUDA;
     return launch_pdl(fn, dim3((unsigned)grid), dim3(kPT), smem, st, args) == cudaSuccess
                ? SV_OK
                : SV_ERR_CUDA;
