@@ -24,13 +24,14 @@
 // halves), all units of a warp or two of them on their way at once.
 //
 // Measured with K/V from HBM (32 query over 8 KV heads of 128, this form against
-// the other): one token after 511 slots 5.1 us against 10.1, after 2047 7.1
-// against 13.7, after 8191 14.0 against 18.4; 4 tokens after 2047 10.8 against
-// 17.1; 16 rows of a chunk after 900 12.4 against 14.3.  What bounds it: two
-// dependent loads before the first K/V (lengths and pages at once, on the guess
-// that sequence r has row r: 5.4 us without), the copies' latency, the cluster's
-// barrier; from about 256 slots a CTA on, what one SM draws from HBM, 60 GB/s
-// (43 with loads of 16 bytes a lane, whether to registers or shared memory).
+// the other): one token after 511 slots 5.0 us against 10.1, after 2047 6.8
+// against 13.7, after 8191 13.7 against 18.4; 4 tokens after 2047 10.1 against
+// 17.1; 16 rows of a chunk after 900 12.0 against 14.3.  What bounds it: the
+// loads before the first K/V (lengths and pages at once, on the guess that
+// sequence r has row r: 0.3 us less), the copies' latency, the CTAs' meeting
+// (shares sent with their bytes counted at the receiver: 0.1 to 0.3 us less than a
+// barrier of the cluster); from about 256 slots a CTA on, what one SM draws from
+// HBM, 60 GB/s (43 with loads of 16 bytes a lane, to registers or shared memory).
 // Tried before: the products by f32 pairs on the ordinary cores (one token after
 // 511 slots the same, after 8191 15.7 us from L2 against 12.5); 4 warps a CTA
 // (5.0 us, but 17.3 after 8191); rows a little apart in shared memory, a copy
@@ -86,6 +87,13 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     return y;
 }
 
+// Two floats to another CTA of the cluster; their bytes counted on its barrier.
+__device__ __forceinline__ void send_f2(uint32_t to, float2 v, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to), "f"(v.x),
+                 "f"(v.y), "r"(bar)
+                 : "memory");
+}
+
 __device__ __forceinline__ uint32_t word(const uint4 &x, int i) {
     return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
 }
@@ -100,7 +108,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) chunk_few_kernel(const FewPara
     // [warp][unit][K, V][slot][D]; a warp's O [8][D] takes the place of its first unit when it has read its last
     extern __shared__ __align__(16) uint8_t ring[];
     auto warp_o = [&](int w) { return reinterpret_cast<float *>(ring + w * kDepth * kUnitBytes<D>); };
-    __shared__ uint64_t full[kFewWarps][kDepth];
+    __shared__ uint64_t full[kFewWarps][kDepth], joined;
     __shared__ float2 warp_ml[kFewWarps][kGMax];
     __shared__ __align__(16) float part[kGMax * D];  // [CTA of the cluster][this CTA's slice]
     __shared__ float2 ml[kFewCluster][kGMax];
@@ -108,8 +116,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) chunk_few_kernel(const FewPara
     const int G = p.c.G, C = p.cluster, rank = (int)cluster_ctarank(), pair = (int)blockIdx.x / C;
     const int row = pair / p.c.Hkv, h = pair - row * p.c.Hkv;
     const Shape &shape = p.c.shape;
+    const int pairs = G * D / 2, slice = pairs / C;  // pairs of values: a multiple of 32
     if (lane < kDepth) mbar_init(&full[warp][lane], 1);
+    if (tid == 0) mbar_init(&joined, 1);
     fence_mbar_init();
+    if (tid == 0) mbar_arrive_expect_tx(&joined, (uint32_t)(C * (slice + kGMax) * sizeof(float2)));
     __syncwarp();
     cluster_arrive_relaxed();  // (waited for before the first store to another CTA)
     griddep_wait();
@@ -272,7 +283,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) chunk_few_kernel(const FewPara
     }
     __syncthreads();
     cluster_wait();
-    const int pairs = G * D / 2, slice = pairs / C;  // pairs of values: a multiple of 32
     if (mine != 0) {
         // the CTA's sums, each to the CTA that owns it
         for (int x = tid; x < pairs; x += kFewThreads) {
@@ -289,7 +299,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) chunk_few_kernel(const FewPara
                 acc.y = __fmaf_rn(v.y, w, acc.y);
             }
             const int owner = x / slice;
-            st_cluster_f2(cluster_map(smem_u32(&part[2 * (rank * slice + x - owner * slice)]), (uint32_t)owner), acc);
+            send_f2(cluster_map(smem_u32(&part[2 * (rank * slice + x - owner * slice)]), (uint32_t)owner), acc,
+                    cluster_map(smem_u32(&joined), (uint32_t)owner));
         }
         if (tid < kGMax * C) {
             const int hd = tid % kGMax, dst = tid / kGMax;
@@ -301,7 +312,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) chunk_few_kernel(const FewPara
                 const float2 x = warp_ml[i][hd];
                 if (x.x != kNegInf) sum = __fmaf_rn(x.y, ex2_approx(x.x - M), sum);
             }
-            st_cluster_f2(cluster_map(smem_u32(&ml[rank][hd]), (uint32_t)dst), make_float2(M, sum));
+            send_f2(cluster_map(smem_u32(&ml[rank][hd]), (uint32_t)dst), make_float2(M, sum),
+                    cluster_map(smem_u32(&joined), (uint32_t)dst));
         }
     }
     // seq_status: lengths, and the ids of the pages that rows see; a warp a sequence
@@ -321,8 +333,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) chunk_few_kernel(const FewPara
         if (lane == 0) p.c.seq_status[sb] = bad ? SV_ERR_BAD_INPUT : SV_OK;
     }
     __syncwarp();
-    cluster_sync();
     if (mine == 0) return;
+    if (!warp_wait_bounded(&joined, 0)) lost = true;
     if (lost && lane == 0 && p.c.seq_status) p.c.seq_status[__ffs(mine) - 1] = SV_ERR_TIMEOUT;
     // the cluster's sums of this CTA's slice
     for (int x = tid; x < slice; x += kFewThreads) {
@@ -401,7 +413,7 @@ Capacity few_capacity(int D) {
 }  // namespace
 
 // The smallest cluster whose warps have a unit each at most (one token after 511
-// slots: 4 CTAs 5.1 us, 8 5.3, 2 6.4), or the largest of which the rows and
+// slots: 4 CTAs 5.0 us, 8 5.2, 2 6.3), or the largest of which the rows and
 // KV heads all find room at once.  A CTA then takes up to 2048 slots of a single
 // row (after 16383 slots 22.8 us against 25.1 for the other form); of several
 // rows 1024, since theirs may be uneven, which the other form's list evens out
