@@ -47,7 +47,7 @@ namespace {
 
 constexpr int kFewWarps = 8, kFewThreads = 32 * kFewWarps;
 constexpr int kUnit = 16, kHalf = 8;               // slots of a unit; a page holds whole halves
-constexpr int kFewSlots = 2048;                    // slots a CTA takes at most (32 units a warp hold twice that)
+constexpr int kFewSlots = 2304;                    // slots a CTA takes at most: a power of two and spare pages
 static_assert(kFewSlots <= 32 * kFewWarps * kUnit, "a lane a unit");
 constexpr int kFewCluster = 16;
 constexpr int kGMax = 8;
@@ -414,11 +414,12 @@ Capacity few_capacity(int D) {
 
 // The smallest cluster whose warps have a unit each at most (one token after 511
 // slots: 4 CTAs 5.0 us, 8 5.2, 2 6.3), or the largest of which the rows and
-// KV heads all find room at once.  A CTA then takes up to 2048 slots of a single
-// row (after 16383 slots 22.8 us against 25.1 for the other form); of several
-// rows 1024, since theirs may be uneven, which the other form's list evens out
-// (8 tokens after 2047: 16.2 us against 22.9, with a single long one about as long
-// as there).  Lengths are on the device: the table's width stands for them.
+// KV heads all find room at once.  A CTA then takes up to 2304 slots of a single
+// row (after 16383 slots 22.6 us against 25.1 for the other form; they meet near
+// 2500 a CTA); of several rows half as many, since theirs may be uneven, which the
+// other form's list evens out (4 tokens after 4095: 15.5 us against 22.6; 8 after
+// 2047: 15.3 against 22.9, with a single long one about as long as there).
+// Lengths are on the device: the table's width stands for them.
 int few_cluster(const ChunkArgs &a) {
     if (a.Hq / a.Hkv > kGMax || a.B > 32) return 0;
     const long long pairs = (long long)a.num_rows * a.Hkv, table = (long long)a.max_pages * a.page_size;
