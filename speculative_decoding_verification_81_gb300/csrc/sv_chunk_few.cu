@@ -24,18 +24,19 @@
 // halves), all units of a warp or two of them on their way at once.
 //
 // Measured with K/V from HBM (32 query over 8 KV heads of 128, this form against
-// the other): one token after 511 slots 5.0 us against 10.1, after 2047 6.8
-// against 13.7, after 8191 13.7 against 18.4; 4 tokens after 2047 10.1 against
-// 17.1; 16 rows of a chunk after 900 12.0 against 14.3.  What bounds it: the
+// the other): one token after 511 slots 4.9 us against 10.1, after 2047 6.3
+// against 13.7, after 8191 12.2 against 18.4; 4 tokens after 2047 9.8 against
+// 17.1; 16 rows of a chunk after 900 11.7 against 14.3.  What bounds it: the
 // loads before the first K/V (lengths and pages at once, on the guess that
 // sequence r has row r: 0.3 us less), the copies' latency, the CTAs' meeting
 // (shares sent with their bytes counted at the receiver: 0.1 to 0.3 us less than a
 // barrier of the cluster); from about 256 slots a CTA on, what one SM draws from
-// HBM, 60 GB/s (43 with loads of 16 bytes a lane, to registers or shared memory).
-// Tried before: the products by f32 pairs on the ordinary cores (one token after
-// 511 slots the same, after 8191 15.7 us from L2 against 12.5); 4 warps a CTA
-// (5.0 us, but 17.3 after 8191); rows a little apart in shared memory, a copy
-// each, for reads without bank conflicts (5.6 and 16.9: 32 copies a unit for 4).
+// HBM and reads from shared memory, 67 GB/s (60 with bank conflicts in the reads of
+// K and V, 43 with loads of 16 bytes a lane in place of the copies).
+// Tried before: the products by f32 pairs on the ordinary cores (after 8191 slots
+// 15.7 us from L2 against 12.5); 4 warps a CTA (after 511 0.1 us less, after 8191
+// 3 us more); rows a little apart in shared memory, a copy each, against the bank
+// conflicts (after 511 0.3 us more, after 8191 3: 32 copies a unit for 4).
 #include <mutex>
 
 #include "sv_chunk.cuh"
@@ -94,8 +95,21 @@ __device__ __forceinline__ void send_f2(uint32_t to, float2 v, uint32_t bar) {
                  : "memory");
 }
 
-__device__ __forceinline__ uint32_t word(const uint4 &x, int i) {
-    return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
+__device__ __forceinline__ uint2 ld_shared8(uint32_t a) {
+    uint2 x;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(a) : "memory");
+    return x;
+}
+
+__device__ __forceinline__ void swap_if(bool yes, uint2 &a, uint2 &b) {
+    const uint2 x = a;
+    a = make_uint2(yes ? b.x : a.x, yes ? b.y : a.y);
+    b = make_uint2(yes ? x.x : b.x, yes ? x.y : b.y);
+}
+__device__ __forceinline__ void swap_if(bool yes, uint4 &a, uint4 &b) {
+    const uint4 x = a;
+    a = make_uint4(yes ? b.x : a.x, yes ? b.y : a.y, yes ? b.z : a.z, yes ? b.w : a.w);
+    b = make_uint4(yes ? x.x : b.x, yes ? x.y : b.y, yes ? x.z : b.z, yes ? x.w : b.w);
 }
 
 }  // namespace
@@ -103,7 +117,7 @@ __device__ __forceinline__ uint32_t word(const uint4 &x, int i) {
 template <int D>
 __global__ void __launch_bounds__(kFewThreads, 1) chunk_few_kernel(const FewParams p) {
     constexpr int kK = D / 32;  // 16-byte pieces of a K (or Q) row a lane: piece 4 i + t
-    constexpr int kV = D / 64;  // of a V row: piece 8 i + g
+    constexpr int kV = D / 32;  // 8-byte pieces of a V row a lane: piece kV g + i
     constexpr int kDepth = kFewDepth<D>;
     // [warp][unit][K, V][slot][D]; a warp's O [8][D] takes the place of its first unit when it has read its last
     extern __shared__ __align__(16) uint8_t ring[];
@@ -190,9 +204,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) chunk_few_kernel(const FewPara
             if (i < n) fetch(i, i);
         int st = 0, ph = 0;
         float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};  // heads 2t and 2t + 1 (l: this lane's slots)
-        float o[4 * kV][4];  // [4 c + r]: dims 64 c + 8 g + 2 r and the next, heads 2t and 2t + 1 each
+        float o[2 * kV][4];  // [i]: dims 4 kV g + 2 i and the next, heads 2t and 2t + 1 each
 #pragma unroll
-        for (int i = 0; i < 4 * kV; ++i)
+        for (int i = 0; i < 2 * kV; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 #pragma unroll 1
@@ -210,11 +224,18 @@ __global__ void __launch_bounds__(kFewThreads, 1) chunk_few_kernel(const FewPara
             const bool whole = slot0 >= lo && slot0 + kUnit - 1 <= pos;
             float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int c = 0; c < kK; ++c) {
-                const uint32_t at_k = here + g * (D * 2) + (4 * c + t) * 16;
-                const uint4 k0 = ld_shared16(at_k), k1 = ld_shared16(at_k + kHalf * D * 2);
-                mma16(s, k0.x, k1.x, k0.y, k1.y, q[c].x, q[c].y);
-                mma16(s, k0.z, k1.z, k0.w, k1.w, q[c].z, q[c].w);
+            for (int c = 0; c < kK; c += 2) {
+                // odd rows read the two pieces in the other order: eight lanes of a read (two
+                // rows, four pieces) then meet eight bank groups
+                const uint32_t at_k = here + g * (D * 2) + (4 * c + t) * 16, odd = g & 1 ? 64 : 0;
+                uint4 a0 = ld_shared16(at_k + odd), a1 = ld_shared16(at_k + (odd ^ 64));
+                uint4 b0 = ld_shared16(at_k + kHalf * D * 2 + odd), b1 = ld_shared16(at_k + kHalf * D * 2 + (odd ^ 64));
+                swap_if(odd != 0, a0, a1);
+                swap_if(odd != 0, b0, b1);
+                mma16(s, a0.x, b0.x, a0.y, b0.y, q[c].x, q[c].y);
+                mma16(s, a0.z, b0.z, a0.w, b0.w, q[c].z, q[c].w);
+                mma16(s, a1.x, b1.x, a1.y, b1.y, q[c + 1].x, q[c + 1].y);
+                mma16(s, a1.z, b1.z, a1.w, b1.w, q[c + 1].z, q[c + 1].w);
             }
             const int slot = (first + i * step) * kUnit + g;
             const bool see0 = slot >= lo && slot <= pos, see1 = slot + 8 >= lo && slot + 8 <= pos;
@@ -238,28 +259,39 @@ __global__ void __launch_bounds__(kFewThreads, 1) chunk_few_kernel(const FewPara
             }
             if (__any_sync(0xffffffffu, moved) && i > 0) {
 #pragma unroll
-                for (int x = 0; x < 4 * kV; ++x)
+                for (int x = 0; x < 2 * kV; ++x)
 #pragma unroll
                     for (int y = 0; y < 4; ++y) o[x][y] *= f[y & 1];
             }
             const uint32_t p0 = transposed(pack_bf16x2(e[0][0], e[0][1]));
             const uint32_t p1 = transposed(pack_bf16x2(e[1][0], e[1][1]));
+            // a slot's pieces in an order by t, so that the four rows of a read meet other bank groups
+            // (sixteen lanes: four rows, four pieces each of a lane's kV), then put right
+            uint2 v[4][kV];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int sl = 2 * t + (y & 1) + (y >> 1) * 8;
+                const uint32_t at_v = here + kUnitBytes<D> / 2 + sl * (D * 2) + kV * g * 8;
+                const bool on = whole || (slot0 + sl >= lo && slot0 + sl <= pos);
+#pragma unroll
+                for (int c = 0; c < kV; ++c) {
+                    v[y][c] = ld_shared8(at_v + (c ^ (t & (kV - 1))) * 8);
+                    if (!on) v[y][c] = make_uint2(0, 0);
+                }
+                if constexpr (kV == 4) {
+                    swap_if(t & 2, v[y][0], v[y][2]);
+                    swap_if(t & 2, v[y][1], v[y][3]);
+                    swap_if(t & 1, v[y][2], v[y][3]);
+                }
+                swap_if(t & 1, v[y][0], v[y][1]);
+            }
 #pragma unroll
             for (int c = 0; c < kV; ++c) {
-                uint4 v[4];
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const int sl = 2 * t + (y & 1) + (y >> 1) * 8;
-                    v[y] = ld_shared16(here + kUnitBytes<D> / 2 + sl * (D * 2) + (8 * c + g) * 16);
-                    if (!whole && (slot0 + sl < lo || slot0 + sl > pos)) v[y] = none;
-                }
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const uint32_t a = word(v[0], r), a1 = word(v[1], r), b0 = word(v[2], r), b1 = word(v[3], r);
-                    // even dims as rows g, odd ones as rows g + 8; two slots a word
-                    mma16(o[4 * c + r], __byte_perm(a, a1, 0x5410), __byte_perm(a, a1, 0x7632),
-                          __byte_perm(b0, b1, 0x5410), __byte_perm(b0, b1, 0x7632), p0, p1);
-                }
+                // even dims as rows g, odd ones as rows g + 8; two slots a word
+                mma16(o[2 * c], __byte_perm(v[0][c].x, v[1][c].x, 0x5410), __byte_perm(v[0][c].x, v[1][c].x, 0x7632),
+                      __byte_perm(v[2][c].x, v[3][c].x, 0x5410), __byte_perm(v[2][c].x, v[3][c].x, 0x7632), p0, p1);
+                mma16(o[2 * c + 1], __byte_perm(v[0][c].y, v[1][c].y, 0x5410), __byte_perm(v[0][c].y, v[1][c].y, 0x7632),
+                      __byte_perm(v[2][c].y, v[3][c].y, 0x5410), __byte_perm(v[2][c].y, v[3][c].y, 0x7632), p0, p1);
             }
             __syncwarp();
             if (i + kDepth < n) fetch(i + kDepth, st);
@@ -274,9 +306,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) chunk_few_kernel(const FewPara
             if (2 * t + j < G) {
 #pragma unroll
                 for (int c = 0; c < kV; ++c) {
-                    float4 *to = reinterpret_cast<float4 *>(warp_o(warp) + (2 * t + j) * D + c * 64 + g * 8);
-                    to[0] = make_float4(o[4 * c][j], o[4 * c][2 + j], o[4 * c + 1][j], o[4 * c + 1][2 + j]);
-                    to[1] = make_float4(o[4 * c + 2][j], o[4 * c + 2][2 + j], o[4 * c + 3][j], o[4 * c + 3][2 + j]);
+                    *reinterpret_cast<float4 *>(warp_o(warp) + (2 * t + j) * D + 4 * (kV * g + c)) =
+                        make_float4(o[2 * c][j], o[2 * c][2 + j], o[2 * c + 1][j], o[2 * c + 1][2 + j]);
                 }
             }
         }
@@ -413,12 +444,12 @@ Capacity few_capacity(int D) {
 }  // namespace
 
 // The smallest cluster whose warps have a unit each at most (one token after 511
-// slots: 4 CTAs 5.0 us, 8 5.2, 2 6.3), or the largest of which the rows and
+// slots: 4 CTAs 4.9 us, 8 5.1, 2 6.2), or the largest of which the rows and
 // KV heads all find room at once.  A CTA then takes up to 2304 slots of a single
-// row (after 16383 slots 22.6 us against 25.1 for the other form; they meet near
-// 2500 a CTA); of several rows half as many, since theirs may be uneven, which the
-// other form's list evens out (4 tokens after 4095: 15.5 us against 22.6; 8 after
-// 2047: 15.3 against 22.9, with a single long one about as long as there).
+// row (after 16383 slots 20.1 us against 25.1 for the other form; they meet near
+// 3000 a CTA); of several rows half as many, since theirs may be uneven, which the
+// other form's list evens out (4 tokens after 4095: 14.7 us against 22.6; 8 after
+// 2047: 14.7 against 22.9, with a single long one about as long as there).
 // Lengths are on the device: the table's width stands for them.
 int few_cluster(const ChunkArgs &a) {
     if (a.Hq / a.Hkv > kGMax || a.B > 32) return 0;
