@@ -48,8 +48,8 @@ namespace {
 
 constexpr int kFewWarps = 8, kFewThreads = 32 * kFewWarps;
 constexpr int kUnit = 16, kHalf = 8;               // slots of a unit; a page holds whole halves
-constexpr int kFewSlots = 2304;                    // slots a CTA takes at most: a power of two and spare pages
-static_assert(kFewSlots <= 32 * kFewWarps * kUnit, "a lane a unit");
+constexpr int kFewSlots = 32 * kFewWarps * kUnit;  // slots a CTA takes at most, of a single row: a lane a unit
+constexpr int kFewUneven = 1152;                   // and of several: a power of two and spare pages
 constexpr int kFewCluster = 16;
 constexpr int kGMax = 8;
 template <int D>
@@ -445,12 +445,13 @@ Capacity few_capacity(int D) {
 
 // The smallest cluster whose warps have a unit each at most (one token after 511
 // slots: 4 CTAs 4.9 us, 8 5.1, 2 6.2), or the largest of which the rows and
-// KV heads all find room at once.  A CTA then takes up to 2304 slots of a single
-// row (after 16383 slots 20.1 us against 25.1 for the other form; they meet near
-// 3000 a CTA); of several rows half as many, since theirs may be uneven, which the
-// other form's list evens out (4 tokens after 4095: 14.7 us against 22.6; 8 after
-// 2047: 14.7 against 22.9, with a single long one about as long as there).
-// Lengths are on the device: the table's width stands for them.
+// KV heads all find room at once.  A CTA then takes up to 4096 slots of a single
+// row (after 16383 slots 20.1 us against 25.1 for the other form, after 30000 32.7
+// against 34.9; 8 query heads over 1 KV head, after 30000: 18.4 against 41); of
+// several rows 1152, since theirs may be uneven, which the other form's list
+// evens out (8 tokens after 2047 each: 14.7 us against 22.9; one after 2047 among
+// short ones: as long here, 13.7 there).  Lengths are on the device: the table's
+// width stands for them.
 int few_cluster(const ChunkArgs &a) {
     if (a.Hq / a.Hkv > kGMax || a.B > 32) return 0;
     const long long pairs = (long long)a.num_rows * a.Hkv, table = (long long)a.max_pages * a.page_size;
@@ -462,7 +463,7 @@ int few_cluster(const ChunkArgs &a) {
         best = 1 << i;
         if (slots <= (long long)best * kFewWarps * kUnit) break;
     }
-    return slots <= (long long)best * (a.num_rows == 1 ? kFewSlots : kFewSlots / 2) ? best : 0;
+    return slots <= (long long)best * (a.num_rows == 1 ? kFewSlots : kFewUneven) ? best : 0;
 }
 
 sv_status launch_few(const ChunkArgs &a, const Params &c, int cluster, cudaStream_t st) {

@@ -37,6 +37,8 @@ def test_lengths(past):
     ([(1000, 1)], dict(hq=14, hkv=2, d=64)),                 # eight
     ([(32000, 1)], dict(hq=8, hkv=1, page_size=256)),        # sixteen, 15 units a warp
     ([(30000, 1)], dict(hq=6, hkv=2, d=64, page_size=8)),
+    ([(65400, 1)], dict(hq=2, hkv=1, d=64, page_size=64)),   # all 32 units of a warp
+    ([(32750, 1)], dict(hq=32, hkv=8, page_size=8)),
     ([(16000, 1)], dict(hq=32, hkv=8, page_size=384)),
     ([(880, 128)], dict(hq=8, hkv=1)),                       # 128 rows of one sequence, a CTA each
     ([(0, 16)], dict(hq=32, hkv=8)),
