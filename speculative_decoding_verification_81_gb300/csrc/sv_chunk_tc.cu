@@ -882,7 +882,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             long long items = 0, x = 0, mine = 0;
-            int most = 0;
+            int most = 0, some = 0;   // some: items of this lane's sequences, of one KV head
             const int few = (p.B + 31) / 32;
             if (p.B > kWarpPlanB) {
                 U = 0;
@@ -893,7 +893,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     most = max(most, sh->warp_most[w]);
                 }
             } else {
-                int some = 0;
                 if (p.B <= 32) {
                     cached = 0;
                     un = units_of(p, pre, r0, r1);  // (no rows past the last sequence)
@@ -915,6 +914,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 most = __reduce_max_sync(0xffffffffu, most);
             }
             nctas = ctas_for(U, items, most, gridDim.x);
+            // few items kept whole: units of each (0: its own)
+            const int each = p.B <= kWarpPlanB && whole_items(U, items, most, nctas, gridDim.x) ? most : 0;
+            if (each > 0) {
+                nctas = (int)items;
+                U = items * each;
+                mine = (long long)some * p.Hkv * each;
+                x = warp_scan(mine, lane);
+            }
             const bool has = U > 0 && (int)blockIdx.x < nctas;
             {
                 const long long edge = cta_begin(U, nctas, blockIdx.x + (lane & 1));  // (both ends at once)
@@ -944,7 +951,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (cached < 0 || b >= cached + 32) load(b);
                 const Seq sq = seq_of(p.shape, __shfl_sync(0xffffffffu, pre, b - cached),
                                       __shfl_sync(0xffffffffu, r0, b - cached), __shfl_sync(0xffffffffu, r1, b - cached));
-                const long long per_head = __shfl_sync(0xffffffffu, un.per_head, b - cached);
+                long long per_head = __shfl_sync(0xffffffffu, un.per_head, b - cached);
+                if (each > 0) per_head = (long long)sq.items * each;
                 if (ub + per_head * p.Hkv <= u0 || sq.items == 0) {
                     ub += per_head * p.Hkv;
                     ++b;
@@ -963,7 +971,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     while (span > 1) {
                         const int step = (span + 31) / 32;
                         const bool in = lane * step < span;
-                        const long long u = in ? units_before(p.shape, sq, i + lane * step) : 0;
+                        const long long u = !in ? 0 : each > 0 ? (long long)(i + lane * step) * each
+                                                               : units_before(p.shape, sq, i + lane * step);
                         const int hit = 31 - __clz(__ballot_sync(0xffffffffu, in && u <= v));  // (lane 0 always)
                         at = __shfl_sync(0xffffffffu, u, hit);
                         i += hit * step;
@@ -979,7 +988,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int w = item_weight(p.shape, sq, i);
                         const Cut c = cut_item(ui, n, w, u0, u1);
                         const long long own = ui;
-                        ui += n * w + kItemCost;
+                        ui += each > 0 ? each : n * w + kItemCost;
                         if (c.a >= c.z) continue;  // only its cost falls into the range
                         Item it;
                         it.b = b;

@@ -25,6 +25,7 @@ extern "C" long long c_before(int tpt, int window, int L, int n, int i) {
 }
 extern "C" int c_valid(int L, int r0, int r1, int rows, int smax) { return seq_of({32, 0, rows, smax}, L, r0, r1).n; }
 extern "C" int c_ctas(long long U, long long items, int most, int grid) { return ctas_for(U, items, most, grid); }
+extern "C" int c_whole(long long U, long long items, int most, int n, int grid) { return whole_items(U, items, most, n, grid); }
 extern "C" void c_cut(long long ui, int n, int w, long long U, int nctas, int cta, int *out) {
     const Cut c = cut_item(ui, n, w, cta_begin(U, nctas, cta), cta_begin(U, nctas, cta + 1));
     out[0] = c.a; out[1] = c.z;
@@ -47,6 +48,7 @@ def C(tmp_path_factory):
     L.c_floor_sum.restype = L.c_before.restype = ctypes.c_longlong
     L.c_cut.argtypes = [ctypes.c_longlong, ctypes.c_int, ctypes.c_int, ctypes.c_longlong, ctypes.c_int,
                         ctypes.c_int, ctypes.c_void_p]
+    L.c_whole.argtypes = [ctypes.c_longlong, ctypes.c_longlong, ctypes.c_int, ctypes.c_int, ctypes.c_int]
     L.c_ctas.argtypes = [ctypes.c_longlong, ctypes.c_longlong, ctypes.c_int, ctypes.c_int]
     return L
 
@@ -140,3 +142,26 @@ def test_ranges_cover_every_tile_once(C, sms):
                     assert (cta, k == 0) not in slots
                     slots.add((cta, k == 0))
             ui += COST + n * w
+
+
+def test_few_items_kept_whole(C):
+    """With every item as long as the largest, the CTAs' ranges hold an item each, uncut."""
+    rng = np.random.default_rng(8)
+    taken = 0
+    for _ in range(300):
+        items, grid = int(rng.integers(1, 200)), 152
+        n = [int(x) for x in rng.integers(1, rng.integers(2, 20), items)]
+        w = [int(x) for x in rng.integers(2, 4, items)]
+        units = [a * b + COST for a, b in zip(n, w)]
+        U, most = sum(units), max(units)
+        whole = C.c_whole(U, items, most, C.c_ctas(U, items, most, grid), grid)
+        if items > grid or len(set(units)) == 1:
+            assert not whole
+        if not whole:
+            continue
+        taken += 1
+        out = (ctypes.c_int * 4)()
+        for i in range(items):
+            C.c_cut(i * most, n[i], w[i], items * most, items, i, out)
+            assert list(out) == [0, n[i], i, 1]
+    assert taken > 50
