@@ -168,8 +168,18 @@ SV_HD int ctas_for(long long U, long long items, int most, int grid) {
     return n;
 }
 
+// Units that no item exceeds, of which `most` is the largest of the sequences'
+// last two each: without a window those see the most slots; with one, an item
+// anywhere may lie across a tile's end, and its tiles' number is bounded by
+// the slots that its rows see.
+SV_HD int units_bound(const Shape &p, int most) {
+    if (p.window == 0 || p.window >= (1 << 20)) return most;
+    const int b = kItemCost + kTwo * ((p.window + 2 * p.tpt - 3 + kTileSlots) / kTileSlots + 1);
+    return most > b ? most : b;
+}
+
 // Whether few items, not all alike, had better stay whole, a CTA each: every
-// item is then given as many units as the largest, so that the ranges of
+// item is then given `most` units, which none exceeds, so that the ranges of
 // `items` CTAs end where items do.  Ranges of n CTAs that end anywhere give
 // most CTAs parts of two items, whose starts and ends and merges they pay (7
 // prompts of 223 to 446, 12 query over 4 KV heads: 24.4 us, whole 17.5).

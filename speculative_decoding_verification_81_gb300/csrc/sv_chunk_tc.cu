@@ -915,7 +915,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             nctas = ctas_for(U, items, most, gridDim.x);
             // few items kept whole: units of each (0: its own)
-            const int each = p.B <= kWarpPlanB && whole_items(U, items, most, nctas, gridDim.x) ? most : 0;
+            const int bound = units_bound(p.shape, most);
+            const int each = p.B <= kWarpPlanB && p.shape.window < (1 << 20) &&
+                                     whole_items(U, items, bound, nctas, gridDim.x)
+                                 ? bound
+                                 : 0;
             if (each > 0) {
                 nctas = (int)items;
                 U = items * each;

@@ -25,6 +25,7 @@ extern "C" long long c_before(int tpt, int window, int L, int n, int i) {
 }
 extern "C" int c_valid(int L, int r0, int r1, int rows, int smax) { return seq_of({32, 0, rows, smax}, L, r0, r1).n; }
 extern "C" int c_ctas(long long U, long long items, int most, int grid) { return ctas_for(U, items, most, grid); }
+extern "C" int c_bound(int tpt, int window, int most) { return units_bound({tpt, window, 1 << 29, 1 << 29}, most); }
 extern "C" int c_whole(long long U, long long items, int most, int n, int grid) { return whole_items(U, items, most, n, grid); }
 extern "C" void c_cut(long long ui, int n, int w, long long U, int nctas, int cta, int *out) {
     const Cut c = cut_item(ui, n, w, cta_begin(U, nctas, cta), cta_begin(U, nctas, cta + 1));
@@ -165,3 +166,14 @@ def test_few_items_kept_whole(C):
             C.c_cut(i * most, n[i], w[i], items * most, items, i, out)
             assert list(out) == [0, n[i], i, 1]
     assert taken > 50
+
+
+def test_no_item_exceeds_the_bound(C):
+    """The largest of a sequence's last two items, and the bound with a window, against every item."""
+    rng = np.random.default_rng(9)
+    for k in range(400):
+        tpt, window = int(rng.choice([1, 2, 4, 16, 32, 128])), int(rng.choice([0, 0, 1, 2, 92, 128, 129, 1000]))
+        L, n = int(rng.integers(0, 1500)), int(rng.integers(1, 600))
+        items = C.c_items(tpt, window, L, n)
+        units = [tiles(tpt, window, L, n, i) * weight(tpt, n, i) + COST for i in range(items)]
+        assert max(units) <= C.c_bound(tpt, window, max(units[-2:])), (tpt, window, L, n)

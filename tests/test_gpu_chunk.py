@@ -371,3 +371,11 @@ def test_serving_steps_together():
         counts, free = sv.sv_release_pages(i32(past), counts, table, stack, free, ps, seq_status=st)
         assert (st == 0).all()
     assert po.pages(past, ps).tolist() == counts.tolist()
+
+
+@pytest.mark.parametrize("window", [0, 1, 92, 127, 128, 300])
+def test_few_items_of_unlike_lengths(window):
+    """Items enough for a CTA each, some of them across a tile's end in the middle of a sequence."""
+    Case([(0, 1), (5458, 1), (1690, 1), (128, 2), (129, 484)], hq=64, hkv=1, page_size=64, window=window, seed=30).check()
+    Case([(400, 300), (700, 170), (0, 90), (20, 3)], hq=12, hkv=4, window=window, seed=31).check()
+    Case([(30, 250)] + [(9, 0)] * 40 + [(5, 33), (100, 260)], hq=8, hkv=2, d=64, window=window, seed=32).check()
