@@ -425,6 +425,10 @@ sv_status sv_append_kv_paged(const void *k_new, const void *v_new, sv_dtype dtyp
  *
  *   q            bf16 [num_rows, Hq, D], rows q_stride elements apart
  *                (>= Hq * D, a multiple of 8: part of a fused projection)
+ *                A row and head whose scores are not all finite (NaN or an
+ *                infinity in q) has NaN in its own out and a value that is
+ *                not finite in its own lse (NaN for a NaN in q), and changes
+ *                no other
  *   k_pages, v_pages, block_table  as sv_tree_attention_paged.  A slot that no
  *                row of its sequence sees may hold anything, and a table entry
  *                for a page without a seen slot is never read (pages behind

@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) chunk_few_kernel(const FewPara
 #pragma unroll
             for (int i = 0; i < kFewWarps; ++i) {
                 const float2 x = warp_ml[i][hd];
-                if (x.x != kNegInf) sum = __fmaf_rn(x.y, ex2_approx(x.x - M), sum);
+                sum = __fmaf_rn(x.y, x.x == kNegInf ? 0.f : ex2_approx(x.x - M), sum);  // (a sum of NaN goes on)
             }
             send_f2(cluster_map(smem_u32(&ml[rank][hd]), (uint32_t)dst), make_float2(M, sum),
                     cluster_map(smem_u32(&joined), (uint32_t)dst));
@@ -382,10 +382,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) chunk_few_kernel(const FewPara
             acc.x = __fmaf_rn(v.x, w, acc.x);
             acc.y = __fmaf_rn(v.y, w, acc.y);
         }
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = 1.f / sum;  // (a row sees its own slot: 0 or NaN only where its scores are not finite)
         const long long head = (long long)row * p.c.Hq + h * G + hd;
         reinterpret_cast<uint32_t *>(p.c.out)[(head * D + dim) / 2] = pack_bf16x2(acc.x * inv, acc.y * inv);
-        if (p.c.lse && dim == 0) p.c.lse[head] = sum > 0.f ? M * kLn2 + logf(sum) : kNegInf;
+        if (p.c.lse && dim == 0) p.c.lse[head] = M * kLn2 + logf(sum);
     }
 }
 

@@ -241,8 +241,9 @@ __device__ __noinline__ void merge_few(const float4 *part_o, const float2 *part_
             }
 #pragma unroll
             for (int u = 0; u < kParts; ++u) {
-                // (a part without a visible slot weighs nothing)
-                if (i0 + u >= nc || ml[u].x == kNegInf) continue;
+                // (a part without a visible slot, its sum 0, weighs nothing; one whose scores are
+                // NaN has a maximum of -inf too, and its sum, NaN, goes on)
+                if (i0 + u >= nc || ml[u].y == 0.f) continue;
                 const float Mn = fmaxf(M, ml[u].x);
                 const float f = M == kNegInf ? 0.f : ex2_approx(M - Mn), w = ex2_approx(ml[u].x - Mn);
                 M = Mn;
@@ -254,12 +255,12 @@ __device__ __noinline__ void merge_few(const float4 *part_o, const float2 *part_
         }
         const long long off = __shfl_sync(0xffffffffu, out_off, r);
         const long long loff = __shfl_sync(0xffffffffu, lse_off, r);
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = 1.f / l;  // (a row sees its own slot: l is 0 or NaN where its scores are not finite)
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] *= inv;
         if (idx0 + lane < total) {
             *reinterpret_cast<uint4 *>(out + off + 8 * c8) = pack8(acc);
-            if (lse && c8 == 0) lse[loff] = l > 0.f ? M * kLn2 + logf(l) : kNegInf;
+            if (lse && c8 == 0) lse[loff] = M * kLn2 + logf(l);
         }
     }
 }
@@ -285,13 +286,14 @@ __device__ __noinline__ void merge_rows(const float4 *part_o, const float2 *part
 #pragma unroll
                 for (int c = 0; c < 8; ++c) o[u][c] = __ldcg(part_o + slot * kO + (size_t)(8 * h + c) * kRows + lane);
             }
-            // (a part without a visible slot weighs nothing; M stays at -inf before the first that has one)
-            if (i0 + 1 >= nc) ml[1].x = kNegInf;
+            // (a part without a visible slot weighs nothing; M stays at -inf before the first that has
+            // one; a sum of NaN goes on whatever its weight)
+            if (i0 + 1 >= nc) ml[1] = make_float2(kNegInf, 0.f);
             const float Mn = fmaxf(M, fmaxf(ml[0].x, ml[1].x));
             const float base = Mn == kNegInf ? 0.f : Mn;
             const float f = ex2_approx(M - base), w0 = ex2_approx(ml[0].x - base), w1 = ex2_approx(ml[1].x - base);
             M = Mn;
-            l = l * f + ml[0].y * w0 + (w1 != 0.f ? ml[1].y * w1 : 0.f);
+            l = l * f + ml[0].y * w0 + ml[1].y * w1;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
                 const float a[4] = {o[0][c].x, o[0][c].y, o[0][c].z, o[0][c].w};
@@ -300,7 +302,7 @@ __device__ __noinline__ void merge_rows(const float4 *part_o, const float2 *part
                 for (int e = 0; e < 4; ++e) acc[4 * c + e] = __fmaf_rn(b[e], w1, __fmaf_rn(a[e], w0, acc[4 * c + e] * f));
             }
         }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = 1.f / l;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             uint32_t x[8];
@@ -308,7 +310,7 @@ __device__ __noinline__ void merge_rows(const float4 *part_o, const float2 *part
             for (int i = 0; i < 8; ++i) x[i] = pack_bf16x2(acc[16 * c + 2 * i] * inv, acc[16 * c + 2 * i + 1] * inv);
             store32(out + 32 * h + 16 * c, x, wide);
         }
-        if (lse && h == 0) *lse = l > 0.f ? M * kLn2 + logf(l) : kNegInf;
+        if (lse && h == 0) *lse = M * kLn2 + logf(l);
     }
 }
 
@@ -595,11 +597,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float w2 = m2 == kNegInf ? 0.f : ex2_approx(m2 - M);
                 const float lt = l * w1 + l2 * w2;
                 const bool whole = it.nc == 1;
-                const float inv = whole ? (lt > 0.f ? 1.f / lt : 0.f) : 1.f;
+                const float inv = whole ? 1.f / lt : 1.f;  // (lt: 0 or NaN only where the row's scores are not finite)
                 const float f1 = w1 * inv, f2 = w2 * inv;
                 const int pslot = it.ci == 0 ? 1 : 0;
                 if (active) {
-                    if (valid && whole && p.lse) p.lse[lse_off] = lt > 0.f ? M * kLn2 + logf(lt) : kNegInf;
+                    if (valid && whole && p.lse) p.lse[lse_off] = M * kLn2 + logf(lt);
                     if (valid && !whole)
                         __stcg(part_ml(p, blockIdx.x, pslot, qt) + r, make_float2(M, lt));
 #pragma unroll 1
