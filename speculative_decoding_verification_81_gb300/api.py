@@ -633,7 +633,16 @@ def _rows(t, name, heads, device):
 def _need_int(v, name):
     if isinstance(v, bool) or not isinstance(v, int):
         raise TypeError(f"{name} must be an int, got {type(v).__name__}")
+    _fits32(**{name: v})
     return v
+
+
+def _fits32(**sizes):
+    """The library takes 32-bit sizes, and ctypes keeps the low 32 bits of a
+    longer one without a word: it would be another call."""
+    for name, v in sizes.items():
+        if not -(1 << 31) <= v < 1 << 31:
+            raise ValueError(f"{name} must fit in 32 bits, got {v}")
 
 
 def sv_build_block_tables(prefix_lens, new_lens, page_counts, block_table, free_pages, free_count,
@@ -661,6 +670,7 @@ def sv_build_block_tables(prefix_lens, new_lens, page_counts, block_table, free_
     if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
         raise ValueError("free_pages must be a tensor of 1 dim")
     num_pages = free_pages.shape[0]
+    _fits32(B=B, max_pages=max_pages, num_pages=num_pages)
     p_tab = _arr(block_table, "block_table", i32, (B, max_pages), dev)
     p_pre = _arr(prefix_lens, "prefix_lens", i32, (B,), dev)
     p_new = _arr(new_lens, "new_lens", i32, (B,), dev)
@@ -706,6 +716,7 @@ def sv_release_pages(keep_lens, page_counts, block_table, free_pages, free_count
     if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
         raise ValueError("free_pages must be a tensor of 1 dim")
     num_pages = free_pages.shape[0]
+    _fits32(B=B, max_pages=max_pages, num_pages=num_pages)
     p_tab = _arr(block_table, "block_table", i32, (B, max_pages), dev)
     p_keep = _arr(keep_lens, "keep_lens", i32, (B,), dev)
     p_cnt = _arr(page_counts, "page_counts", i32, (B,), dev)
@@ -746,6 +757,7 @@ def sv_append_kv_paged(k_new, v_new, slot_map, k_pages, v_pages, row_status=None
     p_kn, k_stride = _rows(k_new, "k_new", Hkv, dev)
     p_vn, v_stride = _rows(v_new, "v_new", Hkv, dev)
     num_rows = k_new.shape[0]
+    _fits32(num_rows=num_rows, num_pages=num_pages, Hkv=Hkv, page_size=page_size, D=D)
     if k_new.shape[2] != D or v_new.shape != k_new.shape:
         raise ValueError(f"k_new and v_new must have shape [num_rows, {Hkv}, {D}]")
     if k_new.dtype != v_new.dtype:
@@ -812,6 +824,7 @@ def sv_chunk_attention_paged(q, k_pages, v_pages, block_table, prefix_lens, row_
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be a tensor of 2 dims")
     B, max_pages = block_table.shape
+    _fits32(num_rows=num_rows, Hq=Hq, B=B, max_pages=max_pages, num_pages=num_pages, Hkv=Hkv, page_size=page_size, D=D)
     p_tab = _arr(block_table, "block_table", i32, (B, max_pages), dev)
     p_pre = _arr(prefix_lens, "prefix_lens", i32, (B,), dev)
     p_row = _arr(row_starts, "row_starts", i32, (B + 1,), dev)
