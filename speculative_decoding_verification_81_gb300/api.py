@@ -577,6 +577,9 @@ class _Launch:
     call allocates are first used."""
 
     def __init__(self, device, stream):
+        # (kernels launched on another device's stream would run there, on this device's addresses)
+        if stream is not None and getattr(stream, "device", device) != device:
+            raise ValueError(f"stream must be one of {device}, got one of {stream.device}")
         self.device, self.given = device, stream
         self.contexts = ()
         if device.type == "cuda":
