@@ -9,8 +9,11 @@ fallback.  If the library is missing the first call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
+import warnings
 
 import torch
 
@@ -81,13 +84,28 @@ _bind = None   # the marshalling extension, and the library it calls
 _bound = None
 
 
+def _load_bind(path):
+    """The extension at `path`; None, with a warning, when it does not import."""
+    name = f"{__package__}._sv_bind"
+    try:
+        loader = importlib.machinery.ExtensionFileLoader(name, path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_file_location(name, path, loader=loader))
+        loader.exec_module(module)
+        return module
+    except (ImportError, OSError) as e:
+        warnings.warn(f"the paged-cache calls go without their extension: {e}")
+        return None
+
+
 def _bind_to(L):
     global _bind, _bound
-    if os.path.exists(_build.BIND_PATH):
-        from . import _sv_bind
+    path = _build.bind_path()
+    if _bind is None and os.path.exists(path):
+        _bind = _load_bind(path)
+    if _bind is not None:
         names = ("sv_build_block_tables", "sv_release_pages", "sv_append_kv_paged", "sv_chunk_attention_paged")
-        _sv_bind.use(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names))
-        _bind, _bound = _sv_bind, L
+        _bind.use(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names))
+        _bound = L
 
 
 def _native():

@@ -1,15 +1,20 @@
 """Build libspecverify.so in place (nvcc, sm_103a only, one -gencode), and
-``_sv_bind.so``, the extension that marshals the paged-cache calls (g++).
+the extension that marshals the paged-cache calls (g++, against torch).
 
 The translation units compile in parallel into ``_build/`` beside the
 package and link into ``libspecverify.so`` next to this file.  A rebuild
-happens only when a source or header is newer than the library.
+happens only when a source or header is newer than the library.  The
+extension's file name carries the Python and torch that it was built for, so
+another one's is not found.  Where it cannot be built, a warning says why and
+the library is used without it: the binding's own marshalling takes every call.
 """
 from __future__ import annotations
 
 import glob
 import os
+import re
 import subprocess
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -17,7 +22,6 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(HERE, "libspecverify.so")
-BIND_PATH = os.path.join(HERE, "_sv_bind.so")
 BIND_SOURCE = os.path.join(CSRC, "sv_bind.cpp")
 
 SOURCES = ["sv_api.cu", "sv_attention.cu", "sv_attention_tc.cu", "sv_vocab.cu", "sv_compact.cu",
@@ -44,7 +48,16 @@ def up_to_date(lib_path: str = LIB_PATH) -> bool:
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
-def _start_bind():
+def bind_path() -> str:
+    """The extension's file for the running interpreter and its torch."""
+    import sysconfig
+
+    import torch
+    tag = f"{sysconfig.get_config_var('SOABI')}-torch-{torch.__version__}"
+    return os.path.join(HERE, f"_sv_bind.{re.sub('[^A-Za-z0-9-]', '_', tag)}.so")
+
+
+def _start_bind(path):
     """g++ at work on the extension (torch's and Python's headers): the process
     and the file it writes."""
     import sysconfig
@@ -54,17 +67,27 @@ def _start_bind():
     inc = [os.path.join(troot, "include"), os.path.join(troot, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"],
            os.path.join(os.path.dirname(os.path.dirname(_nvcc())) or "/usr/local/cuda", "include")]
-    tmp = BIND_PATH + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", *[f"-isystem{i}" for i in inc], BIND_SOURCE, "-o", tmp,
            f"-L{os.path.join(troot, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT), tmp
 
 
-def bind_up_to_date() -> bool:
-    if not os.path.exists(BIND_PATH):
+def bind_up_to_date(path: str) -> bool:
+    if not os.path.exists(path):
         return False
-    t = os.path.getmtime(BIND_PATH)
+    t = os.path.getmtime(path)
     return all(os.path.getmtime(p) <= t for p in [BIND_SOURCE, *glob.glob(os.path.join(INCLUDE, "*.h"))])
+
+
+def _finish_bind(path, proc, tmp) -> None:
+    out, _ = proc.communicate()
+    if proc.returncode == 0:
+        os.replace(tmp, path)
+        return
+    if os.path.exists(path):  # an older source's: it may call another interface
+        os.remove(path)
+    warnings.warn(f"the extension is left out, g++ failed for {BIND_SOURCE}:\n{out.decode(errors='replace')}")
 
 
 def build(force: bool = False, verbose: bool = False, defines=(), lib_path: str = LIB_PATH,
@@ -72,16 +95,18 @@ def build(force: bool = False, verbose: bool = False, defines=(), lib_path: str 
     """Compile the library; `defines` (e.g. SV_PHASE_STAMPS) go to every
     translation unit, for a diagnostic build at another `lib_path`."""
     bind = None
-    if lib_path == LIB_PATH and (force or not bind_up_to_date()):
-        bind = _start_bind()
+    if lib_path == LIB_PATH:
+        try:
+            path = bind_path()
+            if force or not bind_up_to_date(path):
+                bind = path, *_start_bind(path)
+        except (ImportError, OSError) as e:  # no torch, no g++
+            warnings.warn(f"the extension is left out: {e}")
     try:
         return _build_lib(force, verbose, defines, lib_path, build_dir)
     finally:
         if bind is not None:
-            out, _ = bind[0].communicate()
-            if bind[0].returncode != 0:
-                raise RuntimeError(f"g++ failed for {BIND_SOURCE}:\n{out.decode(errors='replace')}")
-            os.replace(bind[1], BIND_PATH)
+            _finish_bind(*bind)
 
 
 def _build_lib(force, verbose, defines, lib_path, build_dir) -> str:
