@@ -187,9 +187,11 @@ __global__ void __launch_bounds__(kPT) build_tables_kernel(BuildTablesArgs a) {
                 }
                 trow[h + j] = pg;
             }
-            // the held pages that the new rows fall into
+            // the held pages that the new rows fall into (without new rows none, not the one that the
+            // prefix ends in either)
             const int end = starts[b + 1] - starts[b] + prefix[b];
-            for (int j = prefix[b] / a.page_size + lane; j < min(h, pages_of(end, a.page_size)); j += 32) {
+            const int upto = end > prefix[b] ? min(h, pages_of(end, a.page_size)) : 0;
+            for (int j = prefix[b] / a.page_size + lane; j < upto; j += 32) {
                 const int pg = trow[j];
                 if (pg < 0 || pg >= a.num_pages) bad = true;
             }
