@@ -444,10 +444,12 @@ sv_status sv_append_kv_paged(const void *k_new, const void *v_new, sv_dtype dtyp
  *   window       >= 0; 0: no limit
  *   out          bf16 [num_rows, Hq, D]; must not overlap q
  *   lse          f32 [num_rows, Hq] or NULL
- *   seq_status   int32 [B] or NULL
+ *   seq_status   int32 [B] or NULL.  Where a wait in the kernel gave up, every
+ *                sequence of the call is SV_ERR_TIMEOUT, its rows unspecified
  *   workspace    >= sv_workspace_size(SV_OP_CHUNK_ATTENTION, 0, 0, 0, dtype,
  *                Hq, Hkv, D) bytes, of which the first 64 KiB zero-filled
- *                before its first use
+ *                before its first use (not again after SV_ERR_TIMEOUT: a call
+ *                finds its counters right whatever the one before left)
  * P is rounded to bf16 for the second product, as in sv_tree_attention; sums,
  * maxima and O are f32.  The result does not depend on how the SMs
  * interleave: cut work is merged in a fixed order.  (num_rows, B, the heads, the

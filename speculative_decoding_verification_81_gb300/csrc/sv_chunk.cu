@@ -88,9 +88,11 @@ sv_status plan_chunk(int Hq, int Hkv, int D, ChunkPlan *plan) {
     pl.grid = ready_sms(D);
     if (pl.grid <= 0) return SV_ERR_CUDA;
     const size_t tiles = (size_t)pl.grid * 2 * 2;
-    size_t off = 0;
+    static_assert(2 * sizeof(chunk::CallWords) <= chunk::kCallBytes, "the forms' words");
+    size_t off = chunk::kCallBytes;
     pl.off_counters = off;
-    off = align_up(off + sizeof(int) * (size_t)pl.grid * 2 * 4, 256);
+    off = align_up(off + sizeof(int) * (size_t)pl.grid * 2 * chunk::kCtaCounters, 256);
+    if (off > 64 * 1024 || pl.grid > chunk::kCallShares) return SV_ERR_UNSUPPORTED;  // (what starts as zeros; 1020 SMs)
     pl.off_part_ml = off;
     off = align_up(off + tiles * chunk::kRows * 2 * sizeof(float), 256);
     pl.off_part_o = off;
@@ -124,7 +126,11 @@ sv_status launch_chunk_attention(const ChunkArgs &a, const ChunkPlan &pl, void *
     p.part_o = reinterpret_cast<float *>(base + pl.off_part_o);
     p.part_ml = reinterpret_cast<float *>(base + pl.off_part_ml);
     p.counters = reinterpret_cast<int *>(base + pl.off_counters);
-    if (const int cluster = chunk::few_cluster(a)) return chunk::launch_few(a, p, cluster, st);
+    p.call = reinterpret_cast<chunk::CallWords *>(base);
+    if (const int cluster = chunk::few_cluster(a)) {
+        ++p.call;
+        return chunk::launch_few(a, p, cluster, st);
+    }
     const long long rows = (long long)a.num_pages * a.Hkv * a.page_size;
     const int box_rows = a.page_size < chunk::kBK ? a.page_size : chunk::kBK;
     CUtensorMap tmk, tmv, tmq, tmq1;

@@ -2,6 +2,7 @@
 // attention kernel (sv_chunk_tc.cu) and its host side (sv_chunk.cu).
 #pragma once
 
+#include "sv_chunk_call.h"
 #include "sv_chunk_list.h"
 #include "sv_device.cuh"
 #include "sv_internal.h"
@@ -42,8 +43,35 @@ struct Params {
     float scale_log2;
     float *part_o;   // [grid][2][Q tile][D / 4][128] float4: a cut item's unnormalised O
     float *part_ml;  // [grid][2][Q tile][128] float2: (max in log2 units, sum)
-    int *counters;   // [grid][Q tile][quarter]: CTAs arrived at a cut item (0 between calls)
+    int *counters;   // [2 sets][grid][Q tile][quarter]: CTAs arrived at a cut item (sv_chunk_call.h)
+    CallWords *call;  // the form's
 };
+
+// This CTA's share added to the workspace's word, by one thread: the call's number.
+__device__ __forceinline__ unsigned long long begin_call(CallWords *words) {
+    return call_number(atomicAdd(&words->shares, call_share((int)blockIdx.x, (int)gridDim.x)));
+}
+
+// The number of the call, whose share this CTA has added (and met since).
+__device__ __forceinline__ unsigned long long this_call(const CallWords *words) {
+    const unsigned long long shares = *reinterpret_cast<const volatile unsigned long long *>(&words->shares);
+    return call_number(shares - call_share((int)blockIdx.x, (int)gridDim.x));
+}
+
+// A wait of this CTA gave up: the whole call is reported, by one thread.
+__device__ __noinline__ inline void give_up(CallWords *words, int32_t *seq_status, int B) {
+    atomicExch(&words->gave_up, call_tag(this_call(words)));
+    __threadfence();
+    if (seq_status)
+#pragma unroll 1
+        for (int b = 0; b < B; ++b) seq_status[b] = SV_ERR_TIMEOUT;
+}
+
+// Whether a wait of the call has given up, asked by a thread that has written a status.
+__device__ __forceinline__ bool gave_up(const CallWords *words) {
+    __threadfence();
+    return *reinterpret_cast<const volatile unsigned long long *>(&words->gave_up) == call_tag(this_call(words));
+}
 
 // A run of K/V tiles of one item.
 struct Item {
@@ -55,6 +83,7 @@ struct Item {
     int single;        // the sequence's only item: its K/V is read once
     int c_first, nc;   // CTAs that share the item's tiles: c_first .. c_first + nc - 1
     int ci;            // this CTA's index among them
+    int counters;      // a cut item's arrival counters, from p.counters on
 };
 
 struct Shared {
@@ -75,7 +104,7 @@ struct Shared {
 
 // The form for a few rows over short tables (sv_chunk_few.cu).
 struct FewParams {
-    Params c;  // (of which the workspace's parts are unused)
+    Params c;  // (of which the workspace's parts but `call` are unused)
     const uint16_t *q, *k, *v;
     long long q_stride;  // elements between rows of q
     int cluster;         // CTAs of a row and KV head

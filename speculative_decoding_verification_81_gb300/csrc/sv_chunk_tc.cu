@@ -373,13 +373,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (p.seq_status)
 #pragma unroll 1
             for (int b = tid; b < p.B; b += kThreads) p.seq_status[b] = SV_ERR_CUDA;
+        if (tid == 0) {
+            const unsigned long long call = begin_call(p.call);
+            for (int i = 0; i < kCtaCounters; ++i) p.counters[counters_of(call + 1, gridDim.x, blockIdx.x) + i] = 0;
+        }
         __syncthreads();
         if (warp == 9) tc::tmem_dealloc(sh->tmem, kCols);
         return;
     }
 
-    // up to 32 sequences: the walking warp's lengths, on their way while the CTA meets
+    // up to 32 sequences: the walking warp's lengths, on their way while the CTA meets, and the
+    // call's number (lane 0; wanted for the first cut item and at the end)
     int pre = 0, r0 = 0, r1 = 0;
+    unsigned long long call = 0;
+    if (warp == 10 && lane == 0) call = begin_call(p.call);
     if (warp == 10 && p.B <= 32 && lane < p.B) {
         pre = p.prefix_lens[lane];
         r0 = p.row_starts[lane];
@@ -421,10 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const uint32_t tbase = sh->tmem;
     volatile int *abort_flag = &sh->abort_flag;
-    auto fail = [&](int b) {
-        *abort_flag = 1;
-        if (p.seq_status) p.seq_status[b] = SV_ERR_TIMEOUT;
-    };
+    auto fail = [&] { *abort_flag = 1; };  // (reported at the end, for the whole call)
 
     if (warp < 8) {
         // ===================== softmax: stream s, one thread a row
@@ -445,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t k = 0;; ++k) {
             const int slot = k % kItems;
             if (!warp_wait_bounded(&sh->item_full[slot], (k / kItems) & 1)) {
-                fail(0);
+                fail();
                 break;
             }
             const Item it = sh->items[slot];
@@ -556,13 +560,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(&sh->p_full[s]);
             }
             if (!ok) {
-                fail(it.b);
+                fail();
                 break;
             }
             const int steps = two ? it.n : (it.n - a + 1) / 2;
             if (steps > 0) {  // the stream's last PV product of the item
                 if (!(ok = warp_wait_bounded(&sh->o_full[s], o_ph))) {
-                    fail(it.b);
+                    fail();
                     break;
                 }
                 o_ph ^= 1;
@@ -580,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float m2 = kNegInf, l2 = 0.f;
                 if (pair) {
                     if (!(ok = warp_wait_bounded(&sh->x_full[s ^ 1], x_ph))) {
-                        fail(it.b);
+                        fail();
                         break;
                     }
                     x_ph ^= 1;
@@ -646,13 +650,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (pair) mbar_arrive(&sh->o_empty[s ^ 1]);
                 }
                 if (!whole && active) {
-                    int *ctr = p.counters + (it.c_first * 2 + qt) * 4 + quarter;
+                    int *ctr = p.counters + it.counters + qt * 4 + quarter;
                     int last = 0;
                     if (lane == 0) {  // (its release covers the warp's partials, written before the barrier above)
                         int before_me;
                         asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before_me) : "l"(ctr) : "memory");
                         last = before_me == it.nc - 1;
-                        if (last) *ctr = 0;  // all have arrived: ready for the next call
                     }
                     __syncwarp();
                     if (__shfl_sync(0xffffffffu, last, 0)) {
@@ -691,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t k = 0; ok; ++k) {
                 const int slot = k % kItems;
                 if (!wait(&sh->item_full[slot], (k / kItems) & 1)) {
-                    fail(0);
+                    fail();
                     break;
                 }
                 const Item it = sh->items[slot];
@@ -717,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int boxes = __popc(__ballot_sync(0xffffffffu, y != kNone));
                     const int st = pos % kStages;
                     if (!wait(&sh->empty[st], ((pos / kStages) & 1) ^ 1)) {
-                        fail(it.b);
+                        fail();
                         ok = false;
                         break;
                     }
@@ -760,7 +763,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t g = 0, qpos = 0;
             uint32_t st = 0, st_ph = 0;         // ring stage of the K tile at hand
             bool ok = true;
-            int b_now = 0;
             auto issue_pv = [&](uint32_t s, uint32_t q) -> bool {
                 if (!wait(&sh->p_full[s], (p_ph >> s) & 1)) return false;
                 p_ph ^= 1u << s;
@@ -785,7 +787,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (b >= 0) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh->item_empty[slot]);
-                    b_now = b;
                 }
                 // (the end of the list: two steps without an S, for the last products)
                 const int steps = b < 0 ? 2 : two ? 2 * n : n;
@@ -863,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (b < 0) break;
                 qpos += two ? 2 : 1;
             }
-            if (!ok && lane == 0) fail(b_now);
+            if (!ok && lane == 0) fail();
             // every product issued is complete before the tensor memory is given back
             commit(leader, &sh->fin);
             wait(&sh->fin, 0);
@@ -1007,10 +1008,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         it.single = sq.items == 1;
                         it.c_first = blockIdx.x;
                         it.nc = 1;
+                        it.counters = 0;
                         if (it.n < n) {  // the CTAs of its first and its last tile
                             const int cta = cta_of(U, nctas, tile_unit(own, w, lane & 1 ? n - 1 : 0));
                             it.c_first = __shfl_sync(0xffffffffu, cta, 0);
                             it.nc = __shfl_sync(0xffffffffu, cta, 1) - it.c_first + 1;
+                            it.counters = counters_of(call, gridDim.x, it.c_first);  // (lane 0's, which publishes it)
                         }
                         it.ci = blockIdx.x - it.c_first;
                         const int slot = k % kItems;
@@ -1051,7 +1054,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ub += per_head * p.Hkv;
                 ++b;
             }
-            if (!ok) fail(b < p.B ? b : 0);
+            if (!ok) fail();
             // the end of the list
             const int slot = k % kItems;
             if (wait(&sh->item_empty[slot], ((k / kItems) & 1) ^ 1) && lane == 0) {
@@ -1074,8 +1077,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 bad = __any_sync(0xffffffffu, bad);
-                if (lane == 0 && !*abort_flag) p.seq_status[sb] = bad ? SV_ERR_BAD_INPUT : SV_OK;
+                if (lane == 0) p.seq_status[sb] = bad ? SV_ERR_BAD_INPUT : SV_OK;
             }
+            if (lane == 0 && p.seq_status && (int)blockIdx.x < p.B && gave_up(p.call))
+#pragma unroll 1
+                for (int sb = blockIdx.x; sb < p.B; sb += gridDim.x) p.seq_status[sb] = SV_ERR_TIMEOUT;
+            // the next call's counters
+            call = __shfl_sync(0xffffffffu, call, 0);
+            if (lane < kCtaCounters) p.counters[counters_of(call + 1, gridDim.x, blockIdx.x) + lane] = 0;
 #pragma unroll 1
             for (uint32_t q = qpos > 2 ? qpos - 2 : 0; q < qpos; ++q)
                 wait(&sh->q_full[q & 1], (q >> 1) & 1);
@@ -1087,6 +1096,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_after();
         tc::tmem_dealloc(tbase, kCols);
     }
+    if (tid == 0 && *abort_flag) give_up(p.call, p.seq_status, p.B);
 }
 
 const void *kernel_fn(int D) {
