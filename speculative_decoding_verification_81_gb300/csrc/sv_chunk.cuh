@@ -52,7 +52,7 @@ __device__ __forceinline__ unsigned long long begin_call(CallWords *words) {
     return call_number(atomicAdd(&words->shares, call_share((int)blockIdx.x, (int)gridDim.x)));
 }
 
-// The number of the call, whose share this CTA has added (and met since).
+// The number of the call, whose share this thread has added, or another of the CTA before it met.
 __device__ __forceinline__ unsigned long long this_call(const CallWords *words) {
     const unsigned long long shares = *reinterpret_cast<const volatile unsigned long long *>(&words->shares);
     return call_number(shares - call_share((int)blockIdx.x, (int)gridDim.x));

@@ -140,7 +140,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) chunk_few_kernel(const FewPara
     griddep_wait();
     griddep_launch_dependents();
 
-    if (tid == 0) begin_call(p.c.call);
     // the lengths, a lane a sequence; query head g of the row; and this warp's pages (a lane a
     // unit), on the guess that sequence `row` has one row, so that their load need not wait
     int L = 0, r0 = 0, r1 = 0;
@@ -167,36 +166,27 @@ __global__ void __launch_bounds__(kFewThreads, 1) chunk_few_kernel(const FewPara
     if (shape.window == 0) load_pages(guess, rank * kFewWarps + warp, 0, shape.S_max - 1);
     const bool ok = lane < p.c.B && lengths_ok(shape, L, r0, r1);
     const uint32_t mine = __ballot_sync(0xffffffffu, ok && r0 <= row && row < r1);
-    // seq_status: lengths, and the ids of the pages that rows see; a warp a sequence, of each CTA
-    // the last warps first, which have no part in the end where a CTA's slice is short
+    // the sequences whose status this warp writes: one a warp, of each CTA the last warps first,
+    // which have no part in the end where a CTA's slice is short
     const int own = p.c.seq_status ? (kFewWarps - 1 - warp) * (int)gridDim.x + (int)blockIdx.x : p.c.B;
-    auto report = [&] {
-        for (int sb = own; sb < p.c.B; sb += (int)gridDim.x * kFewWarps) {
-            const int n = __shfl_sync(0xffffffffu, r1 - r0, sb), Ls = __shfl_sync(0xffffffffu, L, sb);
-            bool bad = !__shfl_sync(0xffffffffu, (int)ok, sb);
-            if (!bad && n > 0) {
-                const int lo = shape.window > 0 ? max(0, Ls - shape.window + 1) : 0;
-                const int32_t *trow = p.c.block_table + (size_t)sb * p.c.max_pages;
-                for (int j = lo / p.c.page_size + lane; j <= (Ls + n - 1) / p.c.page_size; j += 32) {
-                    const int pg = trow[j];
-                    if (pg < 0 || pg >= p.c.num_pages) bad = true;
-                }
-            }
-            bad = __any_sync(0xffffffffu, bad);
-            if (lane == 0) p.c.seq_status[sb] = bad ? SV_ERR_BAD_INPUT : SV_OK;
-        }
+    bool looked = own >= p.c.B;
+    auto look = [&] {  // (once, at any time after the report)
+        if (looked) return;
+        looked = true;
+        if (lane == 0 && gave_up(p.c.call))
+            for (int sb = own; sb < p.c.B; sb += (int)gridDim.x * kFewWarps) p.c.seq_status[sb] = SV_ERR_TIMEOUT;
         __syncwarp();
     };
     bool lost = false;
-    if (mine == 0) report();
-    if (mine != 0) {
-        const int b = __ffs(mine) - 1;
-        const int pos = __shfl_sync(0xffffffffu, L, b) + row - __shfl_sync(0xffffffffu, r0, b);
+    {  // (a row of no sequence has no units)
+        const int b = max(__ffs(mine) - 1, 0);
+        const int ahead = __shfl_sync(0xffffffffu, L, b), begin = __shfl_sync(0xffffffffu, r0, b);
+        const int pos = mine != 0 ? ahead + row - begin : 0;
         const int lo = shape.window > 0 ? max(0, pos - shape.window + 1) : 0;
         // this warp's units, and the cache row of each half's first slot (-1: nothing to read)
         const int first = lo / kUnit + rank * kFewWarps + warp, last = pos / kUnit;
-        const int n = first <= last ? (last - first) / step + 1 : 0;
-        if (shape.window != 0 || b != guess) load_pages(b, first, lo, pos);
+        const int n = mine != 0 && first <= last ? (last - first) / step + 1 : 0;
+        if (mine != 0 && (shape.window != 0 || b != guess)) load_pages(b, first, lo, pos);
         int at[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -224,7 +214,24 @@ __global__ void __launch_bounds__(kFewThreads, 1) chunk_few_kernel(const FewPara
 #pragma unroll 1
         for (int i = 0; i < kDepth; ++i)
             if (i < n) fetch(i, i);
-        report();  // while the copies are on their way
+        // while the copies are on their way, seq_status: lengths, and the ids of the pages that rows see
+        if (tid == kFewThreads - 32) begin_call(p.c.call);  // (the thread that may look for its call first)
+        for (int sb = own; sb < p.c.B; sb += (int)gridDim.x * kFewWarps) {
+            const int rows = __shfl_sync(0xffffffffu, r1 - r0, sb), Ls = __shfl_sync(0xffffffffu, L, sb);
+            bool bad = !__shfl_sync(0xffffffffu, (int)ok, sb);
+            if (!bad && rows > 0) {
+                const int from = shape.window > 0 ? max(0, Ls - shape.window + 1) : 0;
+                const int32_t *trow = p.c.block_table + (size_t)sb * p.c.max_pages;
+                for (int j = from / p.c.page_size + lane; j <= (Ls + rows - 1) / p.c.page_size; j += 32) {
+                    const int pg = trow[j];
+                    if (pg < 0 || pg >= p.c.num_pages) bad = true;
+                }
+            }
+            bad = __any_sync(0xffffffffu, bad);
+            if (lane == 0) p.c.seq_status[sb] = bad ? SV_ERR_BAD_INPUT : SV_OK;
+        }
+        __syncwarp();
+        if (n == 0 && warp == kFewWarps - 1) look();
         int st = 0, ph = 0;
         float m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};  // heads 2t and 2t + 1 (l: this lane's slots)
         float o[2 * kV][4];  // [i]: dims 4 kV g + 2 i and the next, heads 2t and 2t + 1 each
@@ -370,8 +377,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) chunk_few_kernel(const FewPara
                     cluster_map(smem_u32(&joined), (uint32_t)dst));
         }
     }
-    if (lane == 0 && own < p.c.B && gave_up(p.c.call))
-        for (int sb = own; sb < p.c.B; sb += (int)gridDim.x * kFewWarps) p.c.seq_status[sb] = SV_ERR_TIMEOUT;
+    look();
     __syncwarp();
     bool late = false;
     if (mine != 0) {
