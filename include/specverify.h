@@ -430,9 +430,9 @@ sv_status sv_append_kv_paged(const void *k_new, const void *v_new, sv_dtype dtyp
  *                not finite in its own lse (NaN for a NaN in q), and changes
  *                no other
  *   k_pages, v_pages, block_table  as sv_tree_attention_paged.  A slot that no
- *                row of its sequence sees may hold anything, and a table entry
- *                for a page without a seen slot is never read (pages behind
- *                a window may be gone); a slot that some row sees holds finite
+ *                row of its sequence sees may hold anything, and so may a table
+ *                entry for a page without a seen slot (pages behind a window
+ *                may be gone); a slot that some row sees holds finite
  *                values
  *   prefix_lens  int32 [B]; row_starts int32 [B + 1].  A sequence with
  *                prefix < 0, rows outside [0, num_rows) or in descending order,
@@ -444,7 +444,7 @@ sv_status sv_append_kv_paged(const void *k_new, const void *v_new, sv_dtype dtyp
  *   window       >= 0; 0: no limit
  *   out          bf16 [num_rows, Hq, D]; must not overlap q
  *   lse          f32 [num_rows, Hq] or NULL
- *   seq_status   int32 [B] or NULL.  Where a wait in the kernel gave up, every
+ *   seq_status   int32 [B] or NULL (nothing is reported then).  Where a wait in the kernel gave up, every
  *                sequence of the call is SV_ERR_TIMEOUT, its rows unspecified
  *   workspace    >= sv_workspace_size(SV_OP_CHUNK_ATTENTION, 0, 0, 0, dtype,
  *                Hq, Hkv, D) bytes, of which the first 64 KiB zero-filled

@@ -823,7 +823,7 @@ def sv_chunk_attention_paged(q, k_pages, v_pages, block_table, prefix_lens, row_
     k_pages/v_pages [num_pages,Hkv,page_size,D] bf16; block_table
     [B,max_pages], prefix_lens [B], row_starts [B+1] int32; window: slots a
     row sees at most (0: all before it).  Without ws the call keeps one a
-    stream.  Returns out [num_rows,Hq,D] bf16, or (out, lse [num_rows,Hq]
+    stream and D (40 MB at D = 128).  Returns out [num_rows,Hq,D] bf16, or (out, lse [num_rows,Hq]
     f32) with return_lse or a given lse."""
     if scale is None and isinstance(q, torch.Tensor) and q.dim() == 3:
         scale = 1.0 / math.sqrt(q.shape[2] or 1)

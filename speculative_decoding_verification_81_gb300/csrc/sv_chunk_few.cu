@@ -24,8 +24,8 @@
 // halves), all units of a warp or two of them on their way at once.
 //
 // Measured with K/V from HBM (32 query over 8 KV heads of 128, this form against
-// the other): one token after 511 slots 4.9 us against 10.1, after 2047 6.3
-// against 13.7, after 8191 12.2 against 18.4; 4 tokens after 2047 9.8 against
+// the other): one token after 511 slots 5.0 us against 10.1, after 2047 6.3
+// against 13.7, after 8191 12.4 against 18.4; 4 tokens after 2047 9.7 against
 // 17.1; 16 rows of a chunk after 900 11.7 against 14.3.  What bounds it: the
 // loads before the first K/V (lengths and pages at once, on the guess that
 // sequence r has row r: 0.3 us less), the copies' latency, the CTAs' meeting
@@ -49,7 +49,7 @@ namespace {
 constexpr int kFewWarps = 8, kFewThreads = 32 * kFewWarps;
 constexpr int kUnit = 16, kHalf = 8;               // slots of a unit; a page holds whole halves
 constexpr int kFewSlots = 32 * kFewWarps * kUnit;  // slots a CTA takes at most, of a single row: a lane a unit
-constexpr int kFewUneven = 1152;                   // and of several: a power of two and spare pages
+constexpr int kFewUneven = 1152;                   // and of several: 1024, and 128 for the pages that a table has to spare
 constexpr int kFewCluster = 16;
 constexpr int kGMax = 8;
 template <int D>
@@ -478,7 +478,8 @@ Capacity few_capacity(int D) {
 // several rows 1152, since theirs may be uneven, which the other form's list
 // evens out (8 tokens after 2047 each: 14.7 us against 22.9; one after 2047 among
 // short ones: as long here, 13.7 there).  Lengths are on the device: the table's
-// width stands for them.
+// width stands for them, so that short rows over a wider table take the other
+// form too (4 tokens after 511 slots 10.6 us for 5.4).
 int few_cluster(const ChunkArgs &a) {
     if (a.Hq / a.Hkv > kGMax || a.B > 32) return 0;
     const long long pairs = (long long)a.num_rows * a.Hkv, table = (long long)a.max_pages * a.page_size;

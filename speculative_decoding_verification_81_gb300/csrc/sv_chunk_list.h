@@ -33,7 +33,9 @@ constexpr int kItemCost = 8;       // units of an item's start and end
 
 // Sum of floor((a i + c) / 128) for i = 0 .. n - 1: the quotients' whole parts in
 // closed form, the rest by exchanging the roles of slope and modulus, as
-// Euclid's algorithm does.  The first round divides by shifts and, with slopes
+// Euclid's algorithm does: the published floor sum, lattice points below a
+// line (Graham, Knuth and Patashnik, Concrete Mathematics, section 3.5, has
+// the sum).  The first round divides by shifts and, with slopes
 // that are powers of two, is the last but one; the others divide in 32 bits
 // where they can.
 SV_HD long long floor_sum(uint32_t n, uint32_t a, uint32_t c) {
