@@ -444,8 +444,9 @@ sv_status sv_append_kv_paged(const void *k_new, const void *v_new, sv_dtype dtyp
  *   window       >= 0; 0: no limit
  *   out          bf16 [num_rows, Hq, D]; must not overlap q
  *   lse          f32 [num_rows, Hq] or NULL
- *   seq_status   int32 [B] or NULL (nothing is reported then).  Where a wait in the kernel gave up, every
- *                sequence of the call is SV_ERR_TIMEOUT, its rows unspecified
+ *   seq_status   int32 [B] or NULL (nothing is reported then).  Where a wait
+ *                in the kernel gave up, every sequence of the call is
+ *                SV_ERR_TIMEOUT, its rows unspecified
  *   workspace    >= sv_workspace_size(SV_OP_CHUNK_ATTENTION, 0, 0, 0, dtype,
  *                Hq, Hkv, D) bytes, of which the first 64 KiB zero-filled
  *                before its first use (not again after SV_ERR_TIMEOUT: a call

@@ -62,7 +62,7 @@ sv_stream_t stream_of(int dev) {
 // Memory for a call's outputs on the current device and stream, and a tensor of
 // `sizes` from element `at` of it on.  Straight from the allocator and as plain
 // tensors, without the dispatcher: pages of 8 requests back 4.3 -> 3.8 us a call
-// (4.7 on a box with a slower host).
+// (4.7 on a slower host).
 c10::Storage memory(int64_t bytes) {
     c10::Allocator *from = c10::cuda::CUDACachingAllocator::get();
     return c10::Storage(c10::Storage::use_byte_size_t(), (size_t)bytes, from->allocate((size_t)bytes), from, true);
