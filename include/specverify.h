@@ -75,7 +75,8 @@ typedef enum sv_op {
     SV_OP_VERIFY_TREE_STOCHASTIC = 3,
     SV_OP_VERIFY_STEP_CHAIN = 4,
     SV_OP_VERIFY_STEP_TREE_GREEDY = 5,
-    SV_OP_CHUNK_ATTENTION = 6
+    SV_OP_CHUNK_ATTENTION = 6,
+    SV_OP_RELEASE_SHARED_PAGES = 7
 } sv_op;
 
 /*
@@ -88,7 +89,9 @@ typedef enum sv_op {
  *   SV_OP_VERIFY_TREE_STOCHASTIC:  B, T, V, dtype
  *   SV_OP_VERIFY_STEP_CHAIN:       B, N (as T_or_N), V, dtype, Hq, Hkv, D
  *   SV_OP_VERIFY_STEP_TREE_GREEDY: B, T, V, dtype, Hq, Hkv, D
- *   SV_OP_CHUNK_ATTENTION:         Hq, Hkv, D (B and T_or_N too are ignored)
+ *   SV_OP_CHUNK_ATTENTION:         Hq, Hkv, D (B and T_or_N too are ignored); for
+ *                                  sv_chunk_attention_quant too
+ *   SV_OP_RELEASE_SHARED_PAGES:    num_pages (as T_or_N; the others are ignored)
  * Returns 0 for invalid arguments and for shapes the call refuses as
  * SV_ERR_UNSUPPORTED.
  */
@@ -467,6 +470,167 @@ sv_status sv_chunk_attention_paged(const void *q, long long q_stride, const void
                                    int D, float scale, int window, void *out, float *lse,
                                    int32_t *seq_status, void *workspace, size_t workspace_bytes,
                                    sv_stream_t stream);
+
+/*
+ * A cache held in 4 bits.  Source: the paged KV of "Chapitre 9", section "Ce
+ * que prépare le Chapitre 9" (the cache is what a server's memory goes to); the
+ * form of a row is this library's own.
+ *
+ * A row of a slot and KV head is D codes of 4 bits and two bf16 numbers, the
+ * step between codes and the row's minimum: x_d ~ minimum + step * c_d.
+ *   k_codes, v_codes    [num_pages, Hkv, page_size, D / 2] bytes: byte 4 w + b of
+ *                       a row has dims 8 w + n[2b] (low four bits) and
+ *                       8 w + n[2b + 1], n = 0, 2, 4, 6, 1, 3, 5, 7
+ *   k_params, v_params  bf16 [num_pages, Hkv, page_size, 2]: (step, minimum)
+ * page_size a power of two >= 8 or a multiple of 128, D = 64 or 128; pages, tables
+ * and slots as in the bf16 cache.
+ *
+ * sv_append_kv_quant is sv_append_kv_paged into such a cache.  A row's lowest
+ * and highest value lo and hi, in f32, each operation rounded to nearest:
+ *   step = bf16((hi - lo) * f32(1 / 15)), 0 where that is below 2^-126
+ *   minimum = bf16(lo)
+ *   c_d = 0 where step = 0, else round((x_d - minimum) * (1 / step)) (ties to
+ *         even), held to 0 .. 15
+ * A row of a head with a value that is not finite, or whose step or minimum is
+ * past bf16's range, becomes step 0, minimum NaN, codes 0: it reads as NaN.
+ *
+ *   k_new .. row_status, Supported  as sv_append_kv_paged, with D = 64 or 128
+ */
+sv_status sv_append_kv_quant(const void *k_new, const void *v_new, sv_dtype dtype,
+                             long long k_stride, long long v_stride, const int32_t *slot_map,
+                             int num_rows, int Hkv, int D, int page_size, int num_pages,
+                             void *k_codes, void *k_params, void *v_codes, void *v_params,
+                             int32_t *row_status, sv_stream_t stream);
+
+/*
+ * Attention of packed rows over a paged cache held in 4 bits: single tokens,
+ * chains, draft trees and parts of prompts in one call.
+ * Source: as sv_chunk_attention_paged; for trees as sv_tree_attention.
+ *
+ * sv_chunk_attention_paged over the values minimum + step * code, with one
+ * argument more:
+ *   parents  int32 [num_rows] or NULL.  With it a sequence's rows (at most 64)
+ *            are the nodes of a tree: its i-th row's parent is the sequence's
+ *            row parents[row_starts[b] + i], the first one's is -1, and
+ *            0 <= parent < i for the others.  A row then sees the slots below
+ *            prefix_lens[b] and those of the nodes on its path, its own too.  A
+ *            sequence whose parents are none such, or whose rows are more, is
+ *            reported as SV_ERR_BAD_INPUT, its rows unspecified.  Not with a window
+ * For few rows the codes themselves are multiplied and steps and minima applied
+ * to the f32 scores and to the weights before these are rounded to bf16;
+ * otherwise a value is rounded to bf16 before the products, to what a bf16 cache
+ * would hold of it.  The rest is as in that call.
+ * Supported: as sv_chunk_attention_paged.
+ */
+sv_status sv_chunk_attention_quant(const void *q, long long q_stride, const void *k_codes,
+                                   const void *k_params, const void *v_codes, const void *v_params,
+                                   const int32_t *block_table, int max_pages, int num_pages,
+                                   int page_size, const int32_t *prefix_lens,
+                                   const int32_t *row_starts, const int32_t *parents, int B,
+                                   int num_rows, int Hq, int Hkv, int D, float scale, int window,
+                                   void *out, float *lse, int32_t *seq_status, void *workspace,
+                                   size_t workspace_bytes, sv_stream_t stream);
+
+/*
+ * Compaction of the accepted path's rows in a paged cache held in 4 bits:
+ * sv_compact_kv_paged, its arguments and its errors, with a row's codes and
+ * parameters moved together.  No two sequences may hold the pages that the moved
+ * rows are in.  Supported: D = 64 or 128, limits as sv_compact_kv_paged.
+ */
+sv_status sv_compact_kv_quant(void *k_codes, void *k_params, void *v_codes, void *v_params,
+                              const int32_t *block_table, int max_pages, int num_pages,
+                              int page_size, const int32_t *prefix_lens, int32_t *new_kv_lens,
+                              const int32_t *path_nodes, int path_stride,
+                              const int32_t *accepted_len, int B, int Hkv, int D,
+                              int32_t *seq_status, sv_stream_t stream);
+
+/*
+ * Requests that share pages.  Source: the paged KV of "Chapitre 9", section
+ * "Ce que prépare le Chapitre 9" (a page table a sequence: two of them may name
+ * one page).
+ *
+ * shares[p] is the number of sequences that hold page p beside the first (a
+ * value below 0 counts as 0): zeros for a pool in which nothing is shared, as
+ * sv_build_block_tables hands pages out and sv_release_pages takes them back.
+ * Where pages are shared they are given back by sv_release_shared_pages.  A shared page is
+ * not to be written: a sequence appends behind its last full page, so that this
+ * needs no care unless it is cut to fewer slots than it shares.
+ *
+ * sv_fork_tables: fork f makes sequence t = targets[f], which holds no page, a
+ * holder of the first n = fork_lens[f] slots of sequence s = sources[f].  With
+ * full = n / page_size and part = n % page_size:
+ *   valid_f: s and t in [0, B), s != t, n >= 0, page_counts[t] = 0, f the first
+ *            fork that names t as its target, pages(n) <= page_counts[s] <= max_pages
+ *   C_f     = number of the valid forks up to and with f that have part > 0
+ *   served_f: valid, and part = 0 or C_f <= free_count (in order; a fork that does
+ *             not fit is not overtaken)
+ *   block_table[t, j] = block_table[s, j] and one more share of that page, j < full
+ *   block_table[t, full] = free_pages[free_count - C_f] if part > 0
+ *   copies[f] = (block_table[s, full], block_table[t, full], part), the copy that
+ *            sv_copy_pages is to make; (-1, -1, 0) if part = 0 or not served
+ *   new_page_counts[t] = pages(n); other sequences' counts as they were
+ *   new_free_count = free_count - C_f of the last served f with part > 0
+ *   fork_status[f] = SV_OK; SV_ERR_NO_PAGES (valid, not served); SV_ERR_BAD_INPUT
+ *            (not valid, a page id outside [0, num_pages) among those it names, or
+ *            free_count outside [0, num_pages], in which case no fork gets a page)
+ *
+ *   sources, targets, fork_lens int32 [F]; copies int32 [F, 3]; fork_status int32
+ *   [F] or NULL; page_counts, new_page_counts int32 [B]; shares, new_shares int32
+ *   [num_pages]; other arrays as sv_build_block_tables.  block_table is written
+ *   in place; no other output may alias an input.
+ * Supported: F <= 4096, B <= 4096, and as sv_build_block_tables.
+ */
+sv_status sv_fork_tables(const int32_t *sources, const int32_t *targets, const int32_t *fork_lens,
+                         const int32_t *page_counts, const int32_t *free_pages,
+                         const int32_t *free_count, const int32_t *shares, int F, int B,
+                         int page_size, int max_pages, int num_pages, int32_t *block_table,
+                         int32_t *copies, int32_t *new_page_counts, int32_t *new_free_count,
+                         int32_t *new_shares, int32_t *fork_status, sv_stream_t stream);
+
+/*
+ * Copies of pages: for copy f with (from, to, rows) = copies[f], in every plane
+ * and for every KV head, slots 0 .. rows - 1 of page `to` = those of page `from`.
+ * (-1, -1, any) is none.  A copy with a page outside [0, num_pages), from = to or
+ * rows outside [0, page_size] is skipped, copy_status[f] = SV_ERR_BAD_INPUT.  No
+ * page may be the target of two copies, or of one and the source of another.
+ *
+ *   copies     int32 [F, 3]; copy_status int32 [F] or NULL
+ *   planes     HOST array of num_planes device pointers to arrays [num_pages, Hkv,
+ *              page_size, row_bytes[i]] of bytes: K and V pages of any number of
+ *              layers, codes and parameters of pages held in 4 bits
+ *   row_bytes  HOST array
+ * Supported: num_planes <= 64, row_bytes a multiple of 4 up to 4096, F <= 2^20,
+ * num_pages * Hkv * page_size < 2^31.
+ */
+sv_status sv_copy_pages(const int32_t *copies, int F, void *const *planes, const int *row_bytes,
+                        int num_planes, int Hkv, int page_size, int num_pages,
+                        int32_t *copy_status, sv_stream_t stream);
+
+/*
+ * sv_release_pages where pages may be shared.  A page p with shares[p] > 0 of
+ * which the call's sequences give up k entries keeps max(0, shares[p] - k) holders
+ * beside the first and goes to the stack only where k > shares[p], in the place of
+ * the last of those entries; a page with shares[p] <= 0 goes there with its entry.
+ * The stack's order is that of the entries, by sequence.
+ *   new_shares[p] = what is left; 0 for a page that went to the stack
+ * A sequence with keep_lens < 0, page_counts > max_pages or fewer pages than it is
+ * to keep gives nothing back, and none that would does where free_count is outside
+ * [0, num_pages]: seq_status[b] = SV_ERR_BAD_INPUT, its count unchanged.  An entry
+ * outside [0, num_pages) goes nowhere and neither does a page for which the stack
+ * has no room (some page is free already): seq_status[b] = SV_ERR_BAD_INPUT.
+ *
+ *   Arrays as sv_release_pages and sv_fork_tables.
+ *   workspace  >= sv_workspace_size(SV_OP_RELEASE_SHARED_PAGES, 0, num_pages, ...)
+ *              bytes, of any contents
+ * Supported: as sv_build_block_tables.
+ */
+sv_status sv_release_shared_pages(const int32_t *keep_lens, const int32_t *page_counts,
+                                  const int32_t *block_table, int32_t *free_pages,
+                                  const int32_t *free_count, const int32_t *shares, int B,
+                                  int page_size, int max_pages, int num_pages,
+                                  int32_t *new_page_counts, int32_t *new_free_count,
+                                  int32_t *new_shares, int32_t *seq_status, void *workspace,
+                                  size_t workspace_bytes, sv_stream_t stream);
 
 /*
  * The fused verification step on a chain: sv_tree_attention with the causal

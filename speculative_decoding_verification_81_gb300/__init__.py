@@ -8,12 +8,14 @@ binding on top.
 """
 from .api import (SV_BF16, SV_ERR_BAD_INPUT, SV_ERR_CUDA, SV_ERR_INVALID_ARG, SV_ERR_NO_PAGES,
                   SV_ERR_TIMEOUT, SV_ERR_UNSUPPORTED, SV_ERR_WORKSPACE, SV_F32, SV_OK, SV_OP_CHUNK_ATTENTION,
+                  SV_OP_RELEASE_SHARED_PAGES,
                   SV_OP_TREE_ATTENTION,
                   SV_OP_VERIFY_CHAIN, SV_OP_VERIFY_STEP_CHAIN, SV_OP_VERIFY_STEP_TREE_GREEDY,
                   SV_OP_VERIFY_TREE_GREEDY, SV_OP_VERIFY_TREE_STOCHASTIC, SpecVerifyError, lib,
-                  status_string, sv_append_kv_paged, sv_build_block_tables,
-                  sv_chunk_attention_paged, sv_compact_kv,
-                  sv_compact_kv_paged, sv_release_pages, sv_tree_attention,
+                  status_string, sv_append_kv_paged, sv_append_kv_quant, sv_build_block_tables,
+                  sv_chunk_attention_paged, sv_chunk_attention_quant, sv_compact_kv,
+                  sv_compact_kv_paged, sv_compact_kv_quant, sv_copy_pages, sv_fork_tables, sv_release_pages,
+                  sv_release_shared_pages, sv_tree_attention,
                   sv_tree_attention_paged, sv_verify_chain, sv_verify_step_chain,
                   sv_verify_step_tree_greedy, sv_verify_tree_greedy, sv_verify_tree_stochastic,
                   sv_workspace_size, workspace)
@@ -29,5 +31,7 @@ __all__ = [
     "sv_verify_tree_stochastic", "sv_verify_step_chain", "sv_verify_step_tree_greedy",
     "SV_OP_CHUNK_ATTENTION", "sv_append_kv_paged", "sv_build_block_tables",
     "sv_chunk_attention_paged", "sv_release_pages",
+    "SV_OP_RELEASE_SHARED_PAGES", "sv_append_kv_quant", "sv_chunk_attention_quant", "sv_compact_kv_quant",
+    "sv_fork_tables", "sv_copy_pages", "sv_release_shared_pages",
     "sv_workspace_size", "workspace",
 ]

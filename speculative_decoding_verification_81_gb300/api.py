@@ -38,12 +38,15 @@ SV_OP_VERIFY_TREE_STOCHASTIC = 3
 SV_OP_VERIFY_STEP_CHAIN = 4
 SV_OP_VERIFY_STEP_TREE_GREEDY = 5
 SV_OP_CHUNK_ATTENTION = 6
+SV_OP_RELEASE_SHARED_PAGES = 7
 
 EXPORTS = ("sv_workspace_size", "sv_tree_attention", "sv_verify_chain", "sv_verify_tree_greedy",
            "sv_compact_kv", "sv_status_string", "sv_version", "sv_verify_chain_noalloc",
            "sv_tree_attention_paged", "sv_compact_kv_paged", "sv_verify_tree_stochastic",
            "sv_verify_step_chain", "sv_verify_step_tree_greedy", "sv_build_block_tables",
-           "sv_release_pages", "sv_append_kv_paged", "sv_chunk_attention_paged")
+           "sv_release_pages", "sv_append_kv_paged", "sv_chunk_attention_paged", "sv_append_kv_quant",
+           "sv_chunk_attention_quant", "sv_compact_kv_quant", "sv_fork_tables", "sv_copy_pages",
+           "sv_release_shared_pages")
 
 # Length of the fixed scratch array behind sv_verify_chain_noalloc.
 SV_NOALLOC_SCRATCH_BYTES = 4 << 20
@@ -144,8 +147,16 @@ def load(path: str) -> ctypes.CDLL:
     L.sv_append_kv_paged.argtypes = [P, P, I, Q, Q, P, I, I, I, I, I, P, P, P, P]
     L.sv_chunk_attention_paged.argtypes = [P, Q, P, P, P, I, I, I, P, P, I, I, I, I, I, F, I, P, P, P,
                                            P, Z, P]
+    L.sv_append_kv_quant.argtypes = [P, P, I, Q, Q, P, I, I, I, I, I, P, P, P, P, P, P]
+    L.sv_chunk_attention_quant.argtypes = [P, Q, P, P, P, P, P, I, I, I, P, P, P, I, I, I, I, I, F, I, P, P, P,
+                                           P, Z, P]
+    L.sv_compact_kv_quant.argtypes = [P, P, P, P, P, I, I, I, P, P, P, I, P, I, I, I, P, P]
+    L.sv_fork_tables.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, P, P, P, P, P, P, P]
+    L.sv_copy_pages.argtypes = [P, I, P, P, I, I, I, I, P, P]
+    L.sv_release_shared_pages.argtypes = [P, P, P, P, P, P, I, I, I, I, P, P, P, P, P, Z, P]
     for fn in ("sv_build_block_tables", "sv_release_pages", "sv_append_kv_paged",
-               "sv_chunk_attention_paged",
+               "sv_chunk_attention_paged", "sv_append_kv_quant", "sv_chunk_attention_quant",
+               "sv_compact_kv_quant", "sv_fork_tables", "sv_copy_pages", "sv_release_shared_pages",
                "sv_tree_attention", "sv_verify_chain", "sv_verify_tree_greedy", "sv_compact_kv",
                "sv_verify_chain_noalloc", "sv_tree_attention_paged", "sv_compact_kv_paged",
                "sv_verify_tree_stochastic", "sv_verify_step_chain", "sv_verify_step_tree_greedy"):
@@ -865,6 +876,225 @@ def sv_chunk_attention_paged(q, k_pages, v_pages, block_table, prefix_lens, row_
             _arr(ws, "ws", torch.uint8, ws.shape, dev), ws.numel(), s)
     _check("sv_chunk_attention_paged", rc)
     return out if lse is None else (out, lse)
+
+
+def _quant_pages(k_codes, k_params, v_codes, v_params):
+    """The four arrays of a cache held in 4 bits: their pointers, the device and
+    the sizes (num_pages, Hkv, page_size, D)."""
+    if not isinstance(k_codes, torch.Tensor) or k_codes.dim() != 4:
+        raise ValueError("k_codes must be a tensor of 4 dims")
+    dev, u8, bf16 = k_codes.device, torch.uint8, torch.bfloat16
+    num_pages, Hkv, page_size, half = k_codes.shape
+    _fits32(num_pages=num_pages, Hkv=Hkv, page_size=page_size, D=2 * half)
+    params = torch.Size((num_pages, Hkv, page_size, 2))
+    return (_arr(k_codes, "k_codes", u8, k_codes.shape, dev), _arr(k_params, "k_params", bf16, params, dev),
+            _arr(v_codes, "v_codes", u8, k_codes.shape, dev), _arr(v_params, "v_params", bf16, params, dev),
+            dev, num_pages, Hkv, page_size, 2 * half)
+
+
+def sv_append_kv_quant(k_new, v_new, slot_map, k_codes, k_params, v_codes, v_params, row_status=None, stream=None):
+    """k_new, v_new [num_rows,Hkv,D] bf16 or f32 (rows may lie apart: parts of a
+    fused projection); slot_map [num_rows] int32 (-1: padding).  Writes the
+    rows in 4 bits into k_codes/v_codes [num_pages,Hkv,page_size,D/2] uint8 and
+    k_params/v_params [num_pages,Hkv,page_size,2] bf16 (step, minimum), in place."""
+    p_k, p_kp, p_v, p_vp, dev, num_pages, Hkv, page_size, D = _quant_pages(k_codes, k_params, v_codes, v_params)
+    p_kn, k_stride = _rows(k_new, "k_new", Hkv, dev)
+    p_vn, v_stride = _rows(v_new, "v_new", Hkv, dev)
+    num_rows = k_new.shape[0]
+    _fits32(num_rows=num_rows)
+    if k_new.shape[2] != D or v_new.shape != k_new.shape:
+        raise ValueError(f"k_new and v_new must have shape [num_rows, {Hkv}, {D}]")
+    if k_new.dtype != v_new.dtype:
+        raise TypeError("k_new and v_new must have one dtype")
+    if k_new.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"k_new must be bfloat16 or float32, got {k_new.dtype}")
+    dt = SV_BF16 if k_new.dtype == torch.bfloat16 else SV_F32
+    p_slot = _arr(slot_map, "slot_map", torch.int32, (num_rows,), dev)
+    p_st = _opt_arr(row_status, "row_status", torch.int32, (num_rows,), dev)
+    with _Launch(dev, stream) as s:
+        rc = lib().sv_append_kv_quant(p_kn, p_vn, dt, k_stride, v_stride, p_slot, num_rows, Hkv, D, page_size,
+                                      num_pages, p_k, p_kp, p_v, p_vp, p_st, s)
+    _check("sv_append_kv_quant", rc)
+
+
+def sv_chunk_attention_quant(q, k_codes, k_params, v_codes, v_params, block_table, prefix_lens, row_starts,
+                             parents=None, scale=None, window=0, out=None, lse=None, return_lse=False,
+                             seq_status=None, ws=None, stream=None):
+    """sv_chunk_attention_paged over a cache held in 4 bits (arrays as
+    sv_append_kv_quant's).  parents [num_rows] int32: each sequence's rows (64 at
+    most) are the nodes of a tree, a row's parent by its number in the sequence, -1
+    for the first; None: every row sees the rows before it."""
+    bf16, i32 = torch.bfloat16, torch.int32
+    p_k, p_kp, p_v, p_vp, dev, num_pages, Hkv, page_size, D = _quant_pages(k_codes, k_params, v_codes, v_params)
+    p_q, q_stride = _rows(q, "q", None, dev)
+    num_rows, Hq, dq = q.shape
+    if q.dtype != bf16:
+        raise TypeError(f"q must be {bf16}, got {q.dtype}")
+    if dq != D:
+        raise ValueError(f"q must have shape [num_rows, Hq, {D}], got {tuple(q.shape)}")
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a tensor of 2 dims")
+    B, max_pages = block_table.shape
+    _fits32(num_rows=num_rows, Hq=Hq, B=B, max_pages=max_pages)
+    p_tab = _arr(block_table, "block_table", i32, (B, max_pages), dev)
+    p_pre = _arr(prefix_lens, "prefix_lens", i32, (B,), dev)
+    p_row = _arr(row_starts, "row_starts", i32, (B + 1,), dev)
+    p_par = _opt_arr(parents, "parents", i32, (num_rows,), dev)
+    p_st = _opt_arr(seq_status, "seq_status", i32, (B,), dev)
+    _need_int(window, "window")
+    if scale is None:
+        scale = 1.0 / math.sqrt(D or 1)
+    with _Launch(dev, stream) as s:
+        if out is None:
+            out = torch.empty((num_rows, Hq, D), dtype=bf16, device=dev)
+        if lse is None and return_lse:
+            lse = torch.empty((num_rows, Hq), dtype=torch.float32, device=dev)
+        if ws is None:
+            ws = _chunk_workspace(Hq, Hkv, D, dev, s)
+        rc = lib().sv_chunk_attention_quant(
+            p_q, q_stride, p_k, p_kp, p_v, p_vp, p_tab, max_pages, num_pages, page_size, p_pre, p_row, p_par, B,
+            num_rows, Hq, Hkv, D, float(scale), window, _arr(out, "out", bf16, (num_rows, Hq, D), dev),
+            _opt_arr(lse, "lse", torch.float32, (num_rows, Hq), dev), p_st,
+            _arr(ws, "ws", torch.uint8, ws.shape, dev), ws.numel(), s)
+    _check("sv_chunk_attention_quant", rc)
+    return out if lse is None else (out, lse)
+
+
+def sv_compact_kv_quant(k_codes, k_params, v_codes, v_params, block_table, prefix_lens, accepted_len,
+                        path_nodes=None, new_kv_lens=None, seq_status=None, stream=None):
+    """sv_compact_kv_paged in a cache held in 4 bits.  path_nodes [B,P] int32 or
+    None (chain).  Returns new_kv_lens [B] int32 (may be prefix_lens itself)."""
+    i32 = torch.int32
+    p_k, p_kp, p_v, p_vp, dev, num_pages, Hkv, page_size, D = _quant_pages(k_codes, k_params, v_codes, v_params)
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a tensor of 2 dims")
+    B, max_pages = block_table.shape
+    stride = 0
+    if path_nodes is not None:
+        if not isinstance(path_nodes, torch.Tensor) or path_nodes.dim() != 2:
+            raise ValueError("path_nodes must be a tensor of 2 dims")
+        stride = path_nodes.shape[1]
+    _fits32(B=B, max_pages=max_pages, path_stride=stride)
+    p_tab = _arr(block_table, "block_table", i32, (B, max_pages), dev)
+    p_pre = _arr(prefix_lens, "prefix_lens", i32, (B,), dev)
+    p_acc = _arr(accepted_len, "accepted_len", i32, (B,), dev)
+    p_path = _opt_arr(path_nodes, "path_nodes", i32, (B, stride), dev)
+    p_st = _opt_arr(seq_status, "seq_status", i32, (B,), dev)
+    with _Launch(dev, stream) as s:
+        if new_kv_lens is None:
+            new_kv_lens = torch.empty(B, dtype=i32, device=dev)
+        rc = lib().sv_compact_kv_quant(p_k, p_kp, p_v, p_vp, p_tab, max_pages, num_pages, page_size, p_pre,
+                                       _arr(new_kv_lens, "new_kv_lens", i32, (B,), dev), p_path, stride, p_acc, B,
+                                       Hkv, D, p_st, s)
+    _check("sv_compact_kv_quant", rc)
+    return new_kv_lens
+
+
+def _pool(block_table, free_pages, free_count, shares, page_size):
+    """The table and the pool of pages of a call: pointers, device and sizes."""
+    i32 = torch.int32
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a tensor of 2 dims")
+    dev = block_table.device
+    B, max_pages = block_table.shape
+    _need_int(page_size, "page_size")
+    if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
+        raise ValueError("free_pages must be a tensor of 1 dim")
+    num_pages = free_pages.shape[0]
+    _fits32(B=B, max_pages=max_pages, num_pages=num_pages)
+    return (_arr(block_table, "block_table", i32, (B, max_pages), dev),
+            _arr(free_pages, "free_pages", i32, (num_pages,), dev), _arr(free_count, "free_count", i32, (1,), dev),
+            _arr(shares, "shares", i32, (num_pages,), dev), dev, B, max_pages, num_pages)
+
+
+def _given(t, name, shape, device):
+    """An int32 output: the caller's, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=torch.int32, device=device)
+    _arr(t, name, torch.int32, shape, device)
+    return t
+
+
+def sv_fork_tables(sources, targets, fork_lens, page_counts, block_table, free_pages, free_count, shares, page_size,
+                   copies=None, new_page_counts=None, new_free_count=None, new_shares=None, fork_status=None,
+                   stream=None):
+    """sources, targets, fork_lens [F] int32: the first fork_lens slots of a
+    sequence for another one, which holds no page; page_counts [B], block_table
+    [B,max_pages] (the targets' entries written in place), free_pages, shares
+    [num_pages], free_count [1] int32.  Returns (copies [F,3] for sv_copy_pages,
+    new_page_counts [B], new_free_count [1], new_shares [num_pages]), int32."""
+    i32 = torch.int32
+    p_tab, p_stk, p_fc, p_sh, dev, B, max_pages, num_pages = _pool(block_table, free_pages, free_count, shares, page_size)
+    if not isinstance(sources, torch.Tensor) or sources.dim() != 1:
+        raise ValueError("sources must be a tensor of 1 dim")
+    F = sources.shape[0]
+    _fits32(F=F)
+    p_src = _arr(sources, "sources", i32, (F,), dev)
+    p_tgt = _arr(targets, "targets", i32, (F,), dev)
+    p_len = _arr(fork_lens, "fork_lens", i32, (F,), dev)
+    p_cnt = _arr(page_counts, "page_counts", i32, (B,), dev)
+    p_st = _opt_arr(fork_status, "fork_status", i32, (F,), dev)
+    with _Launch(dev, stream) as s:
+        copies = _given(copies, "copies", (F, 3), dev)
+        new_page_counts = _given(new_page_counts, "new_page_counts", (B,), dev)
+        new_free_count = _given(new_free_count, "new_free_count", (1,), dev)
+        new_shares = _given(new_shares, "new_shares", (num_pages,), dev)
+        rc = lib().sv_fork_tables(p_src, p_tgt, p_len, p_cnt, p_stk, p_fc, p_sh, F, B, page_size, max_pages, num_pages,
+                                  p_tab, copies.data_ptr(), new_page_counts.data_ptr(), new_free_count.data_ptr(),
+                                  new_shares.data_ptr(), p_st, s)
+    _check("sv_fork_tables", rc)
+    return copies, new_page_counts, new_free_count, new_shares
+
+
+def sv_copy_pages(copies, planes, copy_status=None, stream=None):
+    """copies [F,3] int32, rows (from, to, slots); planes: up to 64 tensors
+    [num_pages,Hkv,page_size,X] of any type (pages of K, V, codes, parameters, of
+    any number of layers).  The first slots of page `from` are written to page `to`."""
+    if not isinstance(planes, (list, tuple)) or not planes or not all(isinstance(t, torch.Tensor) for t in planes):
+        raise TypeError("planes must be a list of tensors")
+    if planes[0].dim() != 4:
+        raise ValueError("planes must have 4 dims")
+    dev, first = planes[0].device, planes[0].shape[:3]
+    for i, t in enumerate(planes):
+        if t.dim() != 4 or t.shape[:3] != first:
+            raise ValueError(f"planes[{i}] must have shape {tuple(first)} + (X,), got {tuple(t.shape)}")
+        _arr(t, f"planes[{i}]", t.dtype, t.shape, dev)
+    if not isinstance(copies, torch.Tensor) or copies.dim() != 2:
+        raise ValueError("copies must be a tensor of 2 dims")
+    F, n = copies.shape[0], len(planes)
+    num_pages, Hkv, page_size = first
+    row_bytes = [t.shape[3] * t.element_size() for t in planes]
+    _fits32(F=F, num_pages=num_pages, Hkv=Hkv, page_size=page_size, row_bytes=max(row_bytes))
+    p_c = _arr(copies, "copies", torch.int32, (F, 3), dev)
+    p_st = _opt_arr(copy_status, "copy_status", torch.int32, (F,), dev)
+    with _Launch(dev, stream) as s:
+        rc = lib().sv_copy_pages(p_c, F, (ctypes.c_void_p * n)(*(t.data_ptr() for t in planes)),
+                                 (ctypes.c_int * n)(*row_bytes), n, Hkv, page_size, num_pages, p_st, s)
+    _check("sv_copy_pages", rc)
+
+
+def sv_release_shared_pages(keep_lens, page_counts, block_table, free_pages, free_count, shares, page_size,
+                            new_page_counts=None, new_free_count=None, new_shares=None, seq_status=None, ws=None,
+                            stream=None):
+    """sv_release_pages where pages may be shared: a page goes to the stack (in
+    place) with its last holder.  Returns (new_page_counts [B], new_free_count
+    [1], new_shares [num_pages]), int32."""
+    i32 = torch.int32
+    p_tab, p_stk, p_fc, p_sh, dev, B, max_pages, num_pages = _pool(block_table, free_pages, free_count, shares, page_size)
+    p_keep = _arr(keep_lens, "keep_lens", i32, (B,), dev)
+    p_cnt = _arr(page_counts, "page_counts", i32, (B,), dev)
+    p_st = _opt_arr(seq_status, "seq_status", i32, (B,), dev)
+    with _Launch(dev, stream) as s:
+        new_page_counts = _given(new_page_counts, "new_page_counts", (B,), dev)
+        new_free_count = _given(new_free_count, "new_free_count", (1,), dev)
+        new_shares = _given(new_shares, "new_shares", (num_pages,), dev)
+        if ws is None:  # (any contents: no call needs another's)
+            ws = torch.empty(4 * num_pages, dtype=torch.uint8, device=dev)
+        rc = lib().sv_release_shared_pages(p_keep, p_cnt, p_tab, p_stk, p_fc, p_sh, B, page_size, max_pages, num_pages,
+                                           new_page_counts.data_ptr(), new_free_count.data_ptr(), new_shares.data_ptr(),
+                                           p_st, _arr(ws, "ws", torch.uint8, ws.shape, dev), ws.numel(), s)
+    _check("sv_release_shared_pages", rc)
+    return new_page_counts, new_free_count, new_shares
 
 
 def sv_verify_chain_noalloc(target_logits, draft_logits, draft_tokens, u_accept, u_sample,

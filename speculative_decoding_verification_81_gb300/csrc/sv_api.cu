@@ -37,11 +37,13 @@ size_t sv_workspace_size(sv_op op, int B, int T_or_N, int V, sv_dtype dtype, int
     if (op == SV_OP_CHUNK_ATTENTION) {
         if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
         sv::ChunkPlan pl;
-        return sv::plan_chunk(Hq, Hkv, D, &pl) == SV_OK ? pl.bytes : 0;
+        return sv::plan_chunk(Hq, Hkv, D, false, &pl) == SV_OK ? pl.bytes : 0;
     }
+    if (op == SV_OP_RELEASE_SHARED_PAGES) return T_or_N > 0 ? (size_t)T_or_N * sizeof(int) : 0;
     if (B <= 0 || T_or_N <= 0) return 0;
     switch (op) {
-        case SV_OP_CHUNK_ATTENTION: break;  // (above)
+        case SV_OP_CHUNK_ATTENTION:
+        case SV_OP_RELEASE_SHARED_PAGES: break;  // (above)
         case SV_OP_TREE_ATTENTION: {
             if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
             sv::AttnPlan pl;
@@ -302,13 +304,15 @@ sv_status sv_append_kv_paged(const void *k_new, const void *v_new, sv_dtype dtyp
     return sv::launch_append_kv(a, dtype, as_stream(stream));
 }
 
-sv_status sv_chunk_attention_paged(const void *q, long long q_stride, const void *k_pages,
-                                   const void *v_pages, const int32_t *block_table, int max_pages,
-                                   int num_pages, int page_size, const int32_t *prefix_lens,
-                                   const int32_t *row_starts, int B, int num_rows, int Hq, int Hkv,
-                                   int D, float scale, int window, void *out, float *lse,
-                                   int32_t *seq_status, void *workspace, size_t workspace_bytes,
-                                   sv_stream_t stream) {
+}  // extern "C"
+
+// The chunk attention over pages in bf16 or, with k_params, held in 4 bits.
+static sv_status chunk_attention(const void *q, long long q_stride, const void *k_pages, const void *v_pages,
+                                 const int32_t *block_table, int max_pages, int num_pages, int page_size,
+                                 const int32_t *prefix_lens, const int32_t *row_starts, int B, int num_rows, int Hq,
+                                 int Hkv, int D, float scale, int window, void *out, float *lse, int32_t *seq_status,
+                                 void *workspace, size_t workspace_bytes, sv_stream_t stream, const void *k_params,
+                                 const void *v_params, const int32_t *parents) {
     if (!q || !k_pages || !v_pages || !block_table || !prefix_lens || !row_starts || !out)
         return SV_ERR_INVALID_ARG;
     if (B <= 0 || num_rows <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || max_pages <= 0 || num_pages <= 0 ||
@@ -324,14 +328,148 @@ sv_status sv_chunk_attention_paged(const void *q, long long q_stride, const void
         (long long)num_pages * Hkv * page_size >= (1LL << 31))
         return SV_ERR_UNSUPPORTED;
     sv::ChunkPlan pl;
-    const sv_status st = sv::plan_chunk(Hq, Hkv, D, &pl);
+    const sv_status st = sv::plan_chunk(Hq, Hkv, D, k_params != nullptr, &pl);
     if (st != SV_OK) return st;
     if (!workspace || workspace_bytes < pl.bytes || !aligned16(workspace)) return SV_ERR_WORKSPACE;
     sv::ChunkArgs a{q,         q_stride,    k_pages,    v_pages, block_table, max_pages,
                     num_pages, page_size,   prefix_lens, row_starts, B,       num_rows,
                     Hq,        Hkv,         D,          scale,   window,      out,
-                    lse,       seq_status};
+                    lse,       seq_status,  k_params,   v_params, parents};
     return sv::launch_chunk_attention(a, pl, workspace, as_stream(stream));
+}
+
+extern "C" {
+
+sv_status sv_chunk_attention_paged(const void *q, long long q_stride, const void *k_pages,
+                                   const void *v_pages, const int32_t *block_table, int max_pages,
+                                   int num_pages, int page_size, const int32_t *prefix_lens,
+                                   const int32_t *row_starts, int B, int num_rows, int Hq, int Hkv,
+                                   int D, float scale, int window, void *out, float *lse,
+                                   int32_t *seq_status, void *workspace, size_t workspace_bytes,
+                                   sv_stream_t stream) {
+    return chunk_attention(q, q_stride, k_pages, v_pages, block_table, max_pages, num_pages, page_size, prefix_lens,
+                           row_starts, B, num_rows, Hq, Hkv, D, scale, window, out, lse, seq_status, workspace,
+                           workspace_bytes, stream, nullptr, nullptr, nullptr);
+}
+
+sv_status sv_chunk_attention_quant(const void *q, long long q_stride, const void *k_codes,
+                                   const void *k_params, const void *v_codes, const void *v_params,
+                                   const int32_t *block_table, int max_pages, int num_pages,
+                                   int page_size, const int32_t *prefix_lens,
+                                   const int32_t *row_starts, const int32_t *parents, int B,
+                                   int num_rows, int Hq, int Hkv, int D, float scale, int window,
+                                   void *out, float *lse, int32_t *seq_status, void *workspace,
+                                   size_t workspace_bytes, sv_stream_t stream) {
+    if (!k_params || !v_params || !aligned16(k_params) || !aligned16(v_params) || (parents && window > 0))
+        return SV_ERR_INVALID_ARG;
+    return chunk_attention(q, q_stride, k_codes, v_codes, block_table, max_pages, num_pages, page_size, prefix_lens,
+                           row_starts, B, num_rows, Hq, Hkv, D, scale, window, out, lse, seq_status, workspace,
+                           workspace_bytes, stream, k_params, v_params, parents);
+}
+
+sv_status sv_append_kv_quant(const void *k_new, const void *v_new, sv_dtype dtype,
+                             long long k_stride, long long v_stride, const int32_t *slot_map,
+                             int num_rows, int Hkv, int D, int page_size, int num_pages,
+                             void *k_codes, void *k_params, void *v_codes, void *v_params,
+                             int32_t *row_status, sv_stream_t stream) {
+    if (!k_new || !v_new || !slot_map || !k_codes || !k_params || !v_codes || !v_params) return SV_ERR_INVALID_ARG;
+    if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_INVALID_ARG;
+    if (num_rows <= 0 || Hkv <= 0 || D <= 0 || page_size <= 0 || num_pages <= 0) return SV_ERR_INVALID_ARG;
+    for (const void *p : {k_new, v_new, (const void *)k_codes, (const void *)k_params, (const void *)v_codes, (const void *)v_params})
+        if (!aligned16(p)) return SV_ERR_INVALID_ARG;
+    const long long per16 = dtype == SV_F32 ? 4 : 8, row = (long long)Hkv * D;
+    if (k_stride < row || v_stride < row || k_stride % per16 != 0 || v_stride % per16 != 0) return SV_ERR_INVALID_ARG;
+    if ((D != 64 && D != 128) || row >= (1LL << 30) || num_rows >= (1 << 30) || k_stride >= (1LL << 32) ||
+        v_stride >= (1LL << 32) || (long long)num_pages * Hkv * page_size >= (1LL << 31))
+        return SV_ERR_UNSUPPORTED;
+    sv::AppendQuantArgs a{k_new,     v_new,     k_stride, v_stride, slot_map, num_rows, Hkv,       D,
+                          page_size, num_pages, k_codes,  k_params, v_codes,  v_params, row_status};
+    return sv::launch_append_quant(a, dtype, as_stream(stream));
+}
+
+sv_status sv_compact_kv_quant(void *k_codes, void *k_params, void *v_codes, void *v_params,
+                              const int32_t *block_table, int max_pages, int num_pages,
+                              int page_size, const int32_t *prefix_lens, int32_t *new_kv_lens,
+                              const int32_t *path_nodes, int path_stride,
+                              const int32_t *accepted_len, int B, int Hkv, int D,
+                              int32_t *seq_status, sv_stream_t stream) {
+    if (!k_codes || !k_params || !v_codes || !v_params || !block_table || !prefix_lens || !new_kv_lens || !accepted_len)
+        return SV_ERR_INVALID_ARG;
+    if (B <= 0 || Hkv <= 0 || D <= 0 || max_pages <= 0 || num_pages <= 0 || page_size <= 0) return SV_ERR_INVALID_ARG;
+    if (path_nodes && path_stride <= 0) return SV_ERR_INVALID_ARG;
+    if (!aligned16(k_codes) || !aligned16(k_params) || !aligned16(v_codes) || !aligned16(v_params))
+        return SV_ERR_INVALID_ARG;
+    const long long S_max = (long long)max_pages * page_size;
+    if ((D != 64 && D != 128) || S_max >= (1LL << 30) || (long long)num_pages * Hkv * page_size >= (1LL << 31))
+        return SV_ERR_UNSUPPORTED;
+    sv::CompactQuantArgs a{k_codes,     k_params,    v_codes,    v_params,    block_table,  max_pages, num_pages,
+                           page_size,   prefix_lens, new_kv_lens, path_nodes, path_stride,  accepted_len, B,
+                           Hkv,         D,           (int)S_max, seq_status};
+    return sv::launch_compact_quant(a, as_stream(stream));
+}
+
+sv_status sv_fork_tables(const int32_t *sources, const int32_t *targets, const int32_t *fork_lens,
+                         const int32_t *page_counts, const int32_t *free_pages,
+                         const int32_t *free_count, const int32_t *shares, int F, int B,
+                         int page_size, int max_pages, int num_pages, int32_t *block_table,
+                         int32_t *copies, int32_t *new_page_counts, int32_t *new_free_count,
+                         int32_t *new_shares, int32_t *fork_status, sv_stream_t stream) {
+    if (!sources || !targets || !fork_lens || !page_counts || !free_pages || !free_count || !shares || !block_table ||
+        !copies || !new_page_counts || !new_free_count || !new_shares)
+        return SV_ERR_INVALID_ARG;
+    if (F <= 0 || B <= 0 || page_size <= 0 || max_pages <= 0 || num_pages <= 0) return SV_ERR_INVALID_ARG;
+    // the CTAs read the old counts while some of them write the new ones
+    if (new_page_counts == page_counts || new_free_count == free_count || new_shares == shares) return SV_ERR_INVALID_ARG;
+    if (F > 4096 || !page_tables_ok(B, page_size, max_pages, num_pages)) return SV_ERR_UNSUPPORTED;
+    sv::ForkArgs a{sources,   targets,   fork_lens,   page_counts, free_pages,      free_count,     shares,     F, B,
+                   page_size, max_pages, num_pages,   block_table, copies,          new_page_counts, new_free_count,
+                   new_shares, fork_status};
+    return sv::launch_fork_tables(a, as_stream(stream));
+}
+
+sv_status sv_copy_pages(const int32_t *copies, int F, void *const *planes, const int *row_bytes,
+                        int num_planes, int Hkv, int page_size, int num_pages,
+                        int32_t *copy_status, sv_stream_t stream) {
+    if (!copies || !planes || !row_bytes) return SV_ERR_INVALID_ARG;
+    if (F <= 0 || num_planes <= 0 || Hkv <= 0 || page_size <= 0 || num_pages <= 0) return SV_ERR_INVALID_ARG;
+    if (num_planes > sv::kMaxPlanes || F > (1 << 20) || (long long)num_pages * Hkv * page_size >= (1LL << 31))
+        return SV_ERR_UNSUPPORTED;
+    sv::CopyPagesArgs a{};
+    for (int i = 0; i < num_planes; ++i) {
+        if (!planes[i] || !aligned16(planes[i]) || row_bytes[i] <= 0 || row_bytes[i] % 4 != 0) return SV_ERR_INVALID_ARG;
+        if (row_bytes[i] > 4096) return SV_ERR_UNSUPPORTED;
+        a.planes[i] = planes[i];
+        a.row_bytes[i] = row_bytes[i];
+    }
+    a.copies = copies;
+    a.F = F;
+    a.num_planes = num_planes;
+    a.Hkv = Hkv;
+    a.page_size = page_size;
+    a.num_pages = num_pages;
+    a.copy_status = copy_status;
+    return sv::launch_copy_pages(a, as_stream(stream));
+}
+
+sv_status sv_release_shared_pages(const int32_t *keep_lens, const int32_t *page_counts,
+                                  const int32_t *block_table, int32_t *free_pages,
+                                  const int32_t *free_count, const int32_t *shares, int B,
+                                  int page_size, int max_pages, int num_pages,
+                                  int32_t *new_page_counts, int32_t *new_free_count,
+                                  int32_t *new_shares, int32_t *seq_status, void *workspace,
+                                  size_t workspace_bytes, sv_stream_t stream) {
+    if (!keep_lens || !page_counts || !block_table || !free_pages || !free_count || !shares || !new_page_counts ||
+        !new_free_count || !new_shares)
+        return SV_ERR_INVALID_ARG;
+    if (B <= 0 || page_size <= 0 || max_pages <= 0 || num_pages <= 0) return SV_ERR_INVALID_ARG;
+    if (new_page_counts == page_counts || new_free_count == free_count || new_shares == shares) return SV_ERR_INVALID_ARG;
+    if (!page_tables_ok(B, page_size, max_pages, num_pages)) return SV_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < (size_t)num_pages * sizeof(int) || reinterpret_cast<uintptr_t>(workspace) % sizeof(int) != 0)
+        return SV_ERR_WORKSPACE;
+    sv::ReleaseSharedArgs a{keep_lens, page_counts, block_table,     free_pages,     free_count, shares,     B,
+                            page_size, max_pages,   num_pages,       new_page_counts, new_free_count, new_shares, seq_status,
+                            static_cast<int *>(workspace)};
+    return sv::launch_release_shared(a, as_stream(stream));
 }
 
 }  // extern "C"

@@ -53,9 +53,10 @@ bool q_map(CUtensorMap *map, const void *q, int num_rows, int Hq, int D, long lo
 // SMs of the current device once the kernel is known to run on it as
 // planned, asked for once a device: the attribute calls cost more than a
 // launch.  0 when it cannot run.
-int ready_sms(int D) {
+int ready_sms(int D, bool quant) {
     struct Entry {
         int dev, D, sms;
+        bool quant;
     };
     static std::mutex mu;
     static Entry cache[64];
@@ -64,28 +65,30 @@ int ready_sms(int D) {
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
     std::lock_guard<std::mutex> lock(mu);
     for (int i = 0; i < ncache; ++i)
-        if (cache[i].dev == dev && cache[i].D == D) return cache[i].sms;
-    const void *fn = chunk::kernel_fn(D);
-    const int smem = chunk::smem_bytes(D);
+        if (cache[i].dev == dev && cache[i].D == D && cache[i].quant == quant) return cache[i].sms;
+    const void *fn = quant ? chunk::quant_kernel_fn(D) : chunk::kernel_fn(D);
+    const int smem = quant ? chunk::quant_smem_bytes(D) : chunk::smem_bytes(D);
+    const int threads = quant ? chunk::kThreadsOf<true> : chunk::kThreadsOf<false>;
+    const int regs = quant ? chunk::kLaunchRegsOf<true> : chunk::kLaunchRegsOf<false>;
     int max_optin = 0, sms = device_sm_count(), occ = 0;
     cudaFuncAttributes at;
     // the kernel hands its launch registers out again (setmaxnreg): it must
     // have been built with as many as that split adds up to
     if (cudaDeviceGetAttribute(&max_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
-        smem > max_optin || cudaFuncGetAttributes(&at, fn) != cudaSuccess || at.numRegs < chunk::kLaunchRegs ||
+        smem > max_optin || cudaFuncGetAttributes(&at, fn) != cudaSuccess || at.numRegs < regs ||
         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, fn, chunk::kThreads, smem) != cudaSuccess || occ < 1)
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, fn, threads, smem) != cudaSuccess || occ < 1)
         return 0;
-    if (ncache < 64) cache[ncache++] = Entry{dev, D, sms};
+    if (ncache < 64) cache[ncache++] = Entry{dev, D, sms, quant};
     return sms;
 }
 
 }  // namespace
 
-sv_status plan_chunk(int Hq, int Hkv, int D, ChunkPlan *plan) {
+sv_status plan_chunk(int Hq, int Hkv, int D, bool quant, ChunkPlan *plan) {
     if ((D != 64 && D != 128) || Hq / Hkv > chunk::kRows) return SV_ERR_UNSUPPORTED;
     ChunkPlan pl{};
-    pl.grid = ready_sms(D);
+    pl.grid = ready_sms(D, quant);
     if (pl.grid <= 0) return SV_ERR_CUDA;
     const size_t tiles = (size_t)pl.grid * 2 * 2;
     static_assert(2 * sizeof(chunk::CallWords) <= chunk::kCallBytes, "the forms' words");
@@ -105,7 +108,7 @@ sv_status plan_chunk(int Hq, int Hkv, int D, ChunkPlan *plan) {
 sv_status launch_chunk_attention(const ChunkArgs &a, const ChunkPlan &pl, void *ws, cudaStream_t st) {
     const int G = a.Hq / a.Hkv, tpt = chunk::kRows / G;
     char *base = static_cast<char *>(ws);
-    chunk::Params p{};
+    chunk::QuantParams p{};
     p.out = static_cast<uint16_t *>(a.out);
     p.lse = a.lse;
     p.block_table = a.block_table;
@@ -127,20 +130,29 @@ sv_status launch_chunk_attention(const ChunkArgs &a, const ChunkPlan &pl, void *
     p.part_ml = reinterpret_cast<float *>(base + pl.off_part_ml);
     p.counters = reinterpret_cast<int *>(base + pl.off_counters);
     p.call = reinterpret_cast<chunk::CallWords *>(base);
-    if (const int cluster = chunk::few_cluster(a)) {
+    if (a.k_params) {
+        p.k_codes = static_cast<const uint8_t *>(a.k_pages);
+        p.v_codes = static_cast<const uint8_t *>(a.v_pages);
+        p.k_params = static_cast<const uint32_t *>(a.k_params);
+        p.v_params = static_cast<const uint32_t *>(a.v_params);
+        p.parents = a.parents;
+    } else if (const int cluster = chunk::few_cluster(a)) {
         ++p.call;
         return chunk::launch_few(a, p, cluster, st);
     }
     const long long rows = (long long)a.num_pages * a.Hkv * a.page_size;
     const int box_rows = a.page_size < chunk::kBK ? a.page_size : chunk::kBK;
-    CUtensorMap tmk, tmv, tmq, tmq1;
-    if (!cache_map(&tmk, a.k_pages, rows, a.D, box_rows) || !cache_map(&tmv, a.v_pages, rows, a.D, box_rows) ||
-        !q_map(&tmq, a.q, a.num_rows, a.Hq, a.D, a.q_stride, G, tpt) ||
+    CUtensorMap tmk{}, tmv{}, tmq, tmq1;
+    const bool paged = a.k_params || (cache_map(&tmk, a.k_pages, rows, a.D, box_rows) && cache_map(&tmv, a.v_pages, rows, a.D, box_rows));
+    if (!paged || !q_map(&tmq, a.q, a.num_rows, a.Hq, a.D, a.q_stride, G, tpt) ||
         !q_map(&tmq1, a.q, a.num_rows, a.Hq, a.D, a.q_stride, G, 1))
         return SV_ERR_CUDA;
-    void *args[] = {&tmk, &tmv, &tmq, &tmq1, &p};
-    return launch_pdl(chunk::kernel_fn(a.D), dim3(pl.grid), dim3(chunk::kThreads), chunk::smem_bytes(a.D), st,
-                      args) == cudaSuccess
+    chunk::Params plain = p;
+    void *args[] = {&tmk, &tmv, &tmq, &tmq1, a.k_params ? static_cast<void *>(&p) : &plain};
+    const cudaError_t rc =
+        a.k_params ? launch_pdl(chunk::quant_kernel_fn(a.D), dim3(pl.grid), dim3(chunk::kThreadsOf<true>), chunk::quant_smem_bytes(a.D), st, args)
+                   : launch_pdl(chunk::kernel_fn(a.D), dim3(pl.grid), dim3(chunk::kThreadsOf<false>), chunk::smem_bytes(a.D), st, args);
+    return rc == cudaSuccess
                ? SV_OK
                : SV_ERR_CUDA;
 }

@@ -262,6 +262,88 @@ struct AppendArgs {
     int rows_per_cta;  // set at launch
 };
 
+// ---------------------------------------------------------------- a cache held in 4 bits (sv_quant.cu)
+
+struct AppendQuantArgs {
+    const void *k_new;
+    const void *v_new;
+    long long k_stride, v_stride;  // elements between rows
+    const int32_t *slot_map;
+    int num_rows, Hkv, D, page_size, num_pages;
+    void *k_codes;
+    void *k_params;
+    void *v_codes;
+    void *v_params;
+    int32_t *row_status;
+};
+
+struct CompactQuantArgs {
+    void *k_codes;
+    void *k_params;
+    void *v_codes;
+    void *v_params;
+    const int32_t *block_table;
+    int max_pages, num_pages, page_size;
+    const int32_t *prefix_lens;
+    int32_t *new_kv_lens;
+    const int32_t *path_nodes;
+    int path_stride;
+    const int32_t *accepted_len;
+    int B, Hkv, D, S_max;
+    int32_t *seq_status;
+};
+
+sv_status launch_append_quant(const AppendQuantArgs &args, int dtype, cudaStream_t stream);
+sv_status launch_compact_quant(const CompactQuantArgs &args, cudaStream_t stream);
+
+// ---------------------------------------------------------------- shared pages (sv_fork.cu)
+
+struct ForkArgs {
+    const int32_t *sources;
+    const int32_t *targets;
+    const int32_t *fork_lens;
+    const int32_t *page_counts;
+    const int32_t *free_pages;
+    const int32_t *free_count;
+    const int32_t *shares;
+    int F, B, page_size, max_pages, num_pages;
+    int32_t *block_table;
+    int32_t *copies;
+    int32_t *new_page_counts;
+    int32_t *new_free_count;
+    int32_t *new_shares;
+    int32_t *fork_status;
+};
+
+constexpr int kMaxPlanes = 64;  // arrays of a copy call
+
+struct CopyPagesArgs {
+    void *planes[kMaxPlanes];
+    int row_bytes[kMaxPlanes];
+    const int32_t *copies;
+    int F, num_planes, Hkv, page_size, num_pages;
+    int32_t *copy_status;
+};
+
+struct ReleaseSharedArgs {
+    const int32_t *keep_lens;
+    const int32_t *page_counts;
+    const int32_t *block_table;
+    int32_t *free_pages;
+    const int32_t *free_count;
+    const int32_t *shares;
+    int B, page_size, max_pages, num_pages;
+    int32_t *new_page_counts;
+    int32_t *new_free_count;
+    int32_t *new_shares;
+    int32_t *seq_status;
+    int *last;  // [num_pages], the workspace: a shared page's last entry
+};
+
+sv_status launch_fork_tables(const ForkArgs &args, cudaStream_t stream);
+sv_status launch_copy_pages(const CopyPagesArgs &args, cudaStream_t stream);
+sv_status launch_release_shared(const ReleaseSharedArgs &args, cudaStream_t stream);
+
 // ---------------------------------------------------------------- chunk attention (sv_chunk.cu)
 
 struct ChunkPlan {
@@ -284,9 +366,12 @@ struct ChunkArgs {
     void *out;
     float *lse;
     int32_t *seq_status;
+    const void *k_params;    // pages held in 4 bits: the pages' arrays are the codes, these the rows'
+    const void *v_params;    // steps and minima; null for bf16 pages
+    const int32_t *parents;  // or null; pages held in 4 bits only
 };
 
-sv_status plan_chunk(int Hq, int Hkv, int D, ChunkPlan *plan);
+sv_status plan_chunk(int Hq, int Hkv, int D, bool quant, ChunkPlan *plan);
 sv_status launch_chunk_attention(const ChunkArgs &args, const ChunkPlan &plan, void *ws,
                                  cudaStream_t stream);
 

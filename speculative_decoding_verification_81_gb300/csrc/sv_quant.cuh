@@ -1,0 +1,42 @@
+// sv_quant.cuh -- the 4-bit form of a K or V row.
+//
+// Codes c_d (0 .. 15) and two bf16 numbers: x_d ~ minimum + step * c_d.  One
+// step and minimum a row and head: K's fold into the scores (step * (q . c) +
+// minimum * sum(q)) and V's into the weights, so that a product with the codes
+// themselves, exact in bf16, is all that a matrix instruction has to do.
+//
+// Eight codes are a word, dims 0, 2, 4, 6, 1, 3, 5, 7 from its lowest four bits
+// up: the word shifted right by 4 i and masked has dims 2i and 2i + 1 in its two
+// halves, a pair of bf16 in order.
+#pragma once
+
+#include <stdint.h>
+
+namespace sv {
+namespace quant {
+
+constexpr float kFifteenth = 0.06666667014360428f;  // 1 / 15 in f32
+constexpr float kSmallestStep = 1.1754943508222875e-38f;  // 2^-126: below it 1 / step may not be finite
+constexpr uint32_t kNotFinite = 0x7fc00000u;        // step 0, minimum NaN: a row that has no encoding
+
+__device__ __forceinline__ uint32_t pack(const uint32_t (&c)[8]) {
+    return c[0] | c[2] << 4 | c[4] << 8 | c[6] << 12 | c[1] << 16 | c[3] << 20 | c[5] << 24 | c[7] << 28;
+}
+
+// A word's eight values in bf16, dims 0 .. 7 in order: each (minimum + step * code) rounded once.
+// step and base: the two parameters twice each.  Below 16 a code in the last bits of 128 is 128 +
+// code in bf16; what is taken off is exact.
+__device__ __forceinline__ uint4 expand(uint32_t w, uint32_t step, uint32_t base) {
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t x = (w >> (4 * i) & 0x000f000fu) | 0x43004300u;
+        uint32_t c;
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(x), "r"(0x43004300u));
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(v[i]) : "r"(c), "r"(step), "r"(base));
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+}  // namespace quant
+}  // namespace sv
