@@ -4,6 +4,7 @@
 #include <mutex>
 
 #include "sv_chunk.cuh"
+#include "sv_quant_rows.h"
 
 namespace sv {
 
@@ -91,10 +92,13 @@ sv_status plan_chunk(int Hq, int Hkv, int D, bool quant, ChunkPlan *plan) {
     pl.grid = ready_sms(D, quant);
     if (pl.grid <= 0) return SV_ERR_CUDA;
     const size_t tiles = (size_t)pl.grid * 2 * 2;
-    static_assert(2 * sizeof(chunk::CallWords) <= chunk::kCallBytes, "the forms' words");
+    static_assert(3 * sizeof(chunk::CallWords) <= chunk::kCallBytes, "the forms' words");
     size_t off = chunk::kCallBytes;
     pl.off_counters = off;
     off = align_up(off + sizeof(int) * (size_t)pl.grid * 2 * chunk::kCtaCounters, 256);
+    pl.off_rows = off;
+    off = align_up(off + sizeof(int) * 2 * chunk::kRowsMaxGrid, 256);
+    static_assert(chunk::kRowsCols * 2 <= chunk::kRows, "twice the CTAs of half the rows find room in the shares' places");
     if (off > 64 * 1024 || pl.grid > chunk::kCallShares) return SV_ERR_UNSUPPORTED;  // (what starts as zeros; 1020 SMs)
     pl.off_part_ml = off;
     off = align_up(off + tiles * chunk::kRows * 2 * sizeof(float), 256);
@@ -136,6 +140,10 @@ sv_status launch_chunk_attention(const ChunkArgs &a, const ChunkPlan &pl, void *
         p.k_params = static_cast<const uint32_t *>(a.k_params);
         p.v_params = static_cast<const uint32_t *>(a.v_params);
         p.parents = a.parents;
+        if (const int form = chunk::rows_form(a); form >= 0) {
+            p.call += 2;
+            return chunk::launch_rows(a, p, form, reinterpret_cast<int *>(base + pl.off_rows), st);
+        }
     } else if (const int cluster = chunk::few_cluster(a)) {
         ++p.call;
         return chunk::launch_few(a, p, cluster, st);

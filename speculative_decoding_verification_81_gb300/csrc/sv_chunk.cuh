@@ -2,6 +2,8 @@
 // attention kernel (sv_chunk_tc.cu) and its host side (sv_chunk.cu).
 #pragma once
 
+#include <stddef.h>
+
 #include "sv_chunk_call.h"
 #include "sv_chunk_list.h"
 #include "sv_device.cuh"
@@ -18,9 +20,9 @@ template <bool kQuant>
 constexpr int kThreadsOf = 32 * (kQuant ? 12 + kExpandWarps : 12);
 // bf16 pages: 256 x 200 + 128 x 104 = 384 x 168; in 4 bits: 256 x 176 + 256 x 80 = 512 x 128
 template <bool kQuant>
-constexpr int kSoftmaxRegsOf = kQuant ? 176 : 200;
+constexpr int kSoftmaxRegsOf = kQuant ? 160 : 200;
 template <bool kQuant>
-constexpr int kOtherRegsOf = kQuant ? 80 : 104;
+constexpr int kOtherRegsOf = kQuant ? 96 : 104;
 template <bool kQuant>
 constexpr int kLaunchRegsOf = kQuant ? 128 : 168;
 constexpr int kTreeNodes = 64;           // rows of a sequence that is a tree, at most
@@ -39,11 +41,18 @@ constexpr int kTileBytes = kBK * D * 2;
 template <int D, bool kQuant>
 constexpr int kStagesOf = kQuant ? (D == 128 ? 4 : 8) : D == 128 ? 5 : 12;
 template <int D>
-constexpr int kRawStages = D == 128 ? 3 : 12;
+constexpr int kRawStages = D == 128 ? 3 : 10;
 template <int D>
 constexpr int kRawTile = kBK * (D / 2 + 4);
+// Steps and middles of the tiles' slots in f32.  V's are read until its product is issued, as its
+// codes are; K's until its tile's softmax is done, two tiles after its codes' place may be taken.
+template <int D>
+constexpr int kKSlots = kStagesOf<D, true> / 2 + 2;
+template <int D>
+constexpr int kVSlots = kStagesOf<D, true> / 2;
+constexpr int kSlotBytes = kBK * 8;
 template <int D, bool kQuant>
-constexpr int kRawBytes = kQuant ? kRawStages<D> * kRawTile<D> : 0;
+constexpr int kRawBytes = kQuant ? kRawStages<D> * kRawTile<D> + (kKSlots<D> + kVSlots<D>) * kSlotBytes : 0;
 
 struct Params {
     uint16_t *out;
@@ -127,7 +136,7 @@ struct Shared {
     uint64_t x_full[2];                // per stream: its share of a one-tile item posted
     uint64_t item_full[kItems], item_empty[kItems];
     uint64_t fin;
-    float2 xml[2][kRows];              // a stream's (m, sum) of a one-tile item
+    alignas(16) float2 xml[2][kRows];              // a stream's (m, sum) of a one-tile item (in 4 bits: [kRows] float4)
     Item items[kItems];
     long long warp_units[16];          // (12 or 16 warps)
     int warp_items[16], warp_most[16];
@@ -138,6 +147,8 @@ struct Shared {
 struct QuantShared : Shared {
     uint64_t raw_full[12], raw_empty[12];
 };
+static_assert(sizeof(Shared::xml) == kRows * sizeof(float4), "the shares of a one-tile item");
+static_assert(offsetof(Shared, xml) % 16 == 0, "read and written by 16 bytes");
 template <bool kQuant>
 struct SharedType {
     using type = Shared;

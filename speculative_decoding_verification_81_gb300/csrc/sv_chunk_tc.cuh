@@ -147,6 +147,25 @@ __device__ __noinline__ void rescale_o(uint32_t o, float a) {
     tc::wait_st();
 }
 
+// This warp's P of the first 64 columns (packed at TMEM address s) times a.
+__device__ __noinline__ inline void rescale_p(uint32_t s, float a) {
+    uint32_t pv[32];
+    tc::wait_st();
+    tc::tmem_ld32(s, pv);
+    tc::wait_ld();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) pv[j] = pack_bf16x2(bf16_lo(pv[j]) * a, bf16_hi(pv[j]) * a);
+    tc::tmem_st32(s, pv);
+}
+
+// Of the slots at .. at + 31 a bit for each from lo on and below hi.
+__device__ __forceinline__ uint32_t visible(int at, int lo, int hi) {
+    const int h = hi - at, o = lo - at;
+    const uint32_t below = h >= 32 ? ~0u : h <= 0 ? 0u : (1u << h) - 1u;
+    const uint32_t under = o >= 32 ? ~0u : o <= 0 ? 0u : (1u << o) - 1u;
+    return below & ~under;
+}
+
 // V rows [z0, z1) of a tile zeroed by the 128 threads of a stream, visible to
 // the tensor core: slots that no row sees may hold anything, and 0 * NaN
 // would reach every row.
@@ -274,6 +293,26 @@ __device__ __noinline__ void merge_rows(const float4 *part_o, const float2 *part
 
 // ---------------------------------------------------------------- tiles held in 4 bits
 
+// The slots' steps and middles, behind the tiles as they lie in the pages: [K's and V's places][slot pairs].
+template <int D>
+__device__ __forceinline__ uint8_t *raw_slots(uint8_t *raw) {
+    return raw + kRawStages<D> * kRawTile<D>;
+}
+
+// Sum of a row of a Q tile.
+template <int D>
+__device__ __forceinline__ float row_sum(const uint8_t *tile, int r) {
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(tile + (c >> 3) * kBox + sw128(r, c & 7));
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum = __fadd2_rn(sum, make_float2(bf16_lo(w[i]), bf16_hi(w[i])));
+    }
+    return sum.x + sum.y;
+}
+
 // The tiles as they lie in the pages: K's (kv = 0: the even ring positions) or V's
 // by a warp, its lane a page of the tile; each one copy of codes and one of
 // parameters.
@@ -346,17 +385,18 @@ __device__ __forceinline__ void load_quant(const P &p, S *sh, uint8_t *raw, int 
             if ((q & 1) == (uint32_t)kv) wait(&sh->raw_full[q % kStages], (q / kStages) & 1);
 }
 
-// The tiles as the products read them: a thread a slot, its codes to bf16 values
-// (minimum + step * code, rounded once) in the swizzled tile; a slot that no row of
-// the item sees reads as zeros.
+// The tiles as the products read them: a thread a slot, its codes less 8 as bf16 in
+// the swizzled tile, its step and middle (minimum + 8 steps) beside it as f32, K's
+// times the scale; a slot that no row of the item sees has zeros.
 template <int D, class P, class S>
-__device__ __forceinline__ void expand_quant(const P &p, S *sh, uint8_t *smem, const uint8_t *raw, int w, int lane) {
+__device__ __forceinline__ void expand_quant(const P &p, S *sh, uint8_t *smem, uint8_t *raw, int w, int lane) {
     constexpr int kRow = D / 2, kPieces = D / 32, kStages = kStagesOf<D, true>, kRaw = kRawStages<D>;
     volatile int *abort_flag = &sh->abort_flag;
     auto fail = [&] { *abort_flag = 1; };
     const int r = 32 * w + lane;  // the slot in its tile
     const uint32_t raw_at = smem_u32(raw) + r * kRow, par_at = smem_u32(raw) + kBK * kRow + r * 4;
     const uint32_t out_at = smem_u32(smem) + r * 128;
+    float *slots = reinterpret_cast<float *>(raw_slots<D>(raw)) + (r >> 1) * 4 + (r & 1);
     uint32_t pos = 0;
     bool ok = true;
 #pragma unroll 1
@@ -402,7 +442,14 @@ __device__ __forceinline__ void expand_quant(const P &p, S *sh, uint8_t *smem, c
                 ok = false;
                 break;
             }
-            const uint32_t step = __byte_perm(par, par, 0x1010), base = __byte_perm(par, par, 0x3232);
+            {
+                const uint32_t tile = pos >> 1;
+                const float f = pos & 1 ? 1.f : p.scale_log2;
+                const float step = bf16_lo(par), mid = __fmaf_rn(8.f, step, bf16_hi(par));
+                float *to = slots + (pos & 1 ? kKSlots<D> + tile % kVSlots<D> : tile % kKSlots<D>) * (kSlotBytes / 4);
+                to[0] = step * f;  // (of two slots the steps, then the middles)
+                to[2] = mid * f;
+            }
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
                 const int piece = (i + (r >> (D == 128 ? 1 : 2))) & (kPieces - 1);
@@ -410,7 +457,7 @@ __device__ __forceinline__ void expand_quant(const P &p, S *sh, uint8_t *smem, c
                 const uint32_t to = out_at + st * kTileBytes<D> + (piece >> 1) * kBox;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    uint4 v = quant::expand(words[q], step, base);
+                    const uint4 v = quant::expand(seen ? words[q] : 0x88888888u);
                     const uint32_t chunk = (uint32_t)((piece & 1) * 4 + q) ^ (uint32_t)(r & 7);
                     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + chunk * 16), "r"(v.x), "r"(v.y),
                                  "r"(v.z), "r"(v.w)
@@ -437,6 +484,7 @@ __global__ void __launch_bounds__(kThreadsOf<kQuant>, 1)
     constexpr int kThreads = kThreadsOf<kQuant>;
     constexpr int kTile = kTileBytes<D>;
     constexpr int kHalves = D / 64;
+    constexpr int kKS = kKSlots<D>, kVS = kVSlots<D>;
     extern __shared__ __align__(1024) uint8_t smem[];  // (the swizzle's atoms are 1024 bytes)
     const uint32_t base_u32 = smem_u32(smem);
     uint8_t *qbuf = smem + kStages * kTile;
@@ -463,7 +511,7 @@ __global__ void __launch_bounds__(kThreadsOf<kQuant>, 1)
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh->q_full[i], 1);
-            mbar_init(&sh->q_empty[i], 1);
+            mbar_init(&sh->q_empty[i], kQuant ? 1 + 8 : 1);  // (in 4 bits the softmax warps read Q too)
             mbar_init(&sh->s_full[i], 1);
             mbar_init(&sh->p_full[i], 4);
             mbar_init(&sh->o_full[i], 1);
@@ -566,6 +614,7 @@ __global__ void __launch_bounds__(kThreadsOf<kQuant>, 1)
         uint32_t s_ph = 0, o_ph = 0, x_ph = 0;
         uint32_t gstep = 0;       // steps of the CTA before this item
         uint32_t ring = 0;        // K/V ring position of the item's first tile
+        uint32_t qpos = 0;        // Q tiles before this item
         bool ok = true;
 #pragma unroll 1
         for (uint32_t k = 0;; ++k) {
@@ -593,8 +642,10 @@ __global__ void __launch_bounds__(kThreadsOf<kQuant>, 1)
             // a tree: which of the sequence's own rows this one sees, and the slot of the first of them
             unsigned long long above = 0;
             int own0 = 0;
+            bool tree = false;
             if constexpr (kQuant) {
                 if (p.parents) {
+                    tree = true;
                     const int node0 = it.row0 - it.seq_row0, node = node0 + qt * p.shape.tpt + t;
                     const int nodes = min(node0 + it.ntok, kTreeNodes);  // (parents come before their children)
                     const int32_t *par = p.parents + it.seq_row0;
@@ -604,6 +655,22 @@ __global__ void __launch_bounds__(kThreadsOf<kQuant>, 1)
                 }
             }
             float m = kNegInf, l = 0.f;
+            float z = 0.f, qs = 0.f;  // in 4 bits: the sum of weight times V's middle; the sum of the row of Q
+            if constexpr (kQuant) {
+                const uint32_t qp = qpos + qt;
+                ok = warp_wait_bounded(&sh->q_full[qp & 1], (qp >> 1) & 1);
+                if (!ok) {
+                    fail();
+                    break;
+                }
+                if (active) qs = row_sum<D>(qbuf + (qp & 1) * kTile, r);
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sh->q_empty[qpos & 1]);
+                    if (two) mbar_arrive(&sh->q_empty[(qpos & 1) ^ 1]);
+                }
+                qpos += two ? 2 : 1;
+            }
             const int first = two ? 0 : a, stride = two ? 1 : 2;
             const uint32_t o_cols = tl + kColO + s * 128;
 #pragma unroll 1
@@ -616,7 +683,89 @@ __global__ void __launch_bounds__(kThreadsOf<kQuant>, 1)
                 if (!ok) break;
                 s_ph ^= 1;
                 tc::fence_after();
-                if (active) {
+                if (kQuant && active) {
+                    // in two halves of the columns (all of a row's scores beside what the codes need do
+                    // not fit a thread's registers)
+                    const uint32_t pv = ring + 2 * j + 1;
+                    ok = warp_wait_bounded(&sh->full[pv % kStages], (pv / kStages) & 1);  // (V's steps and middles)
+                    if (!ok) break;
+                    const uint8_t *slots = raw_slots<D>(raw);
+                    const float4 *ks = reinterpret_cast<const float4 *>(slots + (pv >> 1) % kKS * kSlotBytes);
+                    const float4 *vs = reinterpret_cast<const float4 *>(slots + (kKS + (pv >> 1) % kVS) * kSlotBytes);
+                    const float2 qs2 = make_float2(qs, qs);
+                    const bool masked = kb + kBK > w_hi || kb < w_lo;
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        float2 sv[32];
+                        {
+                            uint32_t ra[32], rb[32];
+                            tc::tmem_ld32(sbuf + 64 * h, ra);
+                            tc::tmem_ld32(sbuf + 64 * h + 32, rb);
+                            tc::wait_ld();
+                            // step * (q . (codes - 8)) + middle * sum(q), scaled
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                const uint32_t *r2 = i < 16 ? ra + 2 * i : rb + 2 * (i - 16);
+                                const float4 k4 = ks[32 * h + i];
+                                sv[i] = __ffma2_rn(make_float2(__uint_as_float(r2[0]), __uint_as_float(r2[1])),
+                                                   make_float2(k4.x, k4.y), __fmul2_rn(make_float2(k4.z, k4.w), qs2));
+                            }
+                        }
+                        if (masked) {
+#pragma unroll
+                            for (int w = 0; w < 2; ++w) {
+                                const int at = kb + 64 * h + 32 * w;
+                                uint32_t sees = visible(at, see_lo, see_hi);
+                                if (tree) {  // all of the slots before own0, and of those from it on the path's
+                                    const int x = at - own0;
+                                    sees = x <= -32 ? ~0u
+                                         : x < 0    ? ((1u << -x) - 1u) | (uint32_t)(above << -x)
+                                         : x < 64   ? (uint32_t)(above >> x)
+                                                    : 0u;
+                                }
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    if (!((sees >> (2 * i)) & 1u)) sv[16 * w + i].x = kNegInf;
+                                    if (!((sees >> (2 * i + 1)) & 1u)) sv[16 * w + i].y = kNegInf;
+                                }
+                            }
+                        }
+                        float mq[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) mq[i & 3] = fmaxf(fmaxf(mq[i & 3], sv[i].x), sv[i].y);
+                        const float c = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+                        const bool up = c > m + kRescaleThreshold;
+                        if (__any_sync(0xffffffffu, up)) {
+                            const float f = up ? ex2_approx(m - c) : 1.f;
+                            if (up) {
+                                m = c;
+                                l *= f;
+                                z *= f;
+                            }
+                            // (the wait for S covers this stream's earlier PV products: issued before it)
+                            if (j != first) rescale_o<D>(o_cols, f);
+                            if (h == 1) rescale_p(sbuf, f);
+                        }
+                        const float nb = m == kNegInf ? 0.f : -m;
+                        const float2 nb2 = make_float2(nb, nb);
+                        float2 ls = make_float2(0.f, 0.f), zs = make_float2(0.f, 0.f);
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float2 x = __fadd2_rn(sv[i], nb2);
+                            const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                            const float4 v4 = vs[32 * h + i];
+                            ls = __fadd2_rn(ls, e);
+                            zs = __ffma2_rn(e, make_float2(v4.z, v4.w), zs);
+                            const float2 w = __fmul2_rn(e, make_float2(v4.x, v4.y));
+                            pk[i] = pack_bf16x2(w.x, w.y);
+                        }
+                        l += ls.x + ls.y;
+                        z += zs.x + zs.y;
+                        tc::tmem_st32(sbuf + 32 * h, pk);
+                    }
+                    tc::wait_st();
+                } else if (active) {
                     float sv[kBK];
                     {
                         uint32_t ra[32], rb[32], rc[32], rd[32];
@@ -641,16 +790,7 @@ __global__ void __launch_bounds__(kThreadsOf<kQuant>, 1)
                             const int h = hi - 32 * w, o = lo - 32 * w;
                             const uint32_t below = h >= 32 ? ~0u : h <= 0 ? 0u : (1u << h) - 1u;
                             const uint32_t under = o >= 32 ? ~0u : o <= 0 ? 0u : (1u << o) - 1u;
-                            uint32_t sees = below & ~under;
-                            if constexpr (kQuant) {
-                                if (p.parents) {  // all of the slots before own0, and of those from it on the path's
-                                    const int x = kb + 32 * w - own0;
-                                    sees = x <= -32 ? ~0u
-                                         : x < 0    ? ((1u << -x) - 1u) | (uint32_t)(above << -x)
-                                         : x < 64   ? (uint32_t)(above >> x)
-                                                    : 0u;
-                                }
-                            }
+                            const uint32_t sees = below & ~under;
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
                                 if (!((sees >> i) & 1u)) sv[32 * w + i] = kNegInf;
@@ -719,13 +859,14 @@ __global__ void __launch_bounds__(kThreadsOf<kQuant>, 1)
             const bool pair = !two && it.n > 1;  // one Q tile, shared: its first stream finishes it
             if (!two && a == 1) {
                 if (steps > 0) {
-                    sh->xml[s][r] = make_float2(m, l);
+                    if constexpr (kQuant) reinterpret_cast<float4 *>(sh->xml)[r] = make_float4(m, l, z, 0.f);
+                    else sh->xml[s][r] = make_float2(m, l);
                     tc::fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh->x_full[s]);
                 }
             } else {
-                float m2 = kNegInf, l2 = 0.f;
+                float m2 = kNegInf, l2 = 0.f, z2 = 0.f;
                 if (pair) {
                     if (!(ok = warp_wait_bounded(&sh->x_full[s ^ 1], x_ph))) {
                         fail();
@@ -733,8 +874,15 @@ __global__ void __launch_bounds__(kThreadsOf<kQuant>, 1)
                     }
                     x_ph ^= 1;
                     tc::fence_after();
-                    m2 = sh->xml[s ^ 1][r].x;
-                    l2 = sh->xml[s ^ 1][r].y;
+                    if constexpr (kQuant) {  // (one place: a thread reads the one posted last before it posts again)
+                        const float4 x = reinterpret_cast<const float4 *>(sh->xml)[r];
+                        m2 = x.x;
+                        l2 = x.y;
+                        z2 = x.z;
+                    } else {
+                        m2 = sh->xml[s ^ 1][r].x;
+                        l2 = sh->xml[s ^ 1][r].y;
+                    }
                 }
                 const bool valid = r < rows;
                 const long long row = (long long)it.row0 + qt * p.shape.tpt + t;
@@ -747,6 +895,7 @@ __global__ void __launch_bounds__(kThreadsOf<kQuant>, 1)
                 const bool whole = it.nc == 1;
                 const float inv = whole ? 1.f / lt : 1.f;  // (lt: 0 or NaN only where the row's scores are not finite)
                 const float f1 = w1 * inv, f2 = w2 * inv;
+                const float zt = kQuant ? z * f1 + z2 * f2 : 0.f;
                 const int pslot = it.ci == 0 ? 1 : 0;
                 if (active) {
                     if (valid && whole && p.lse) p.lse[lse_off] = M * kLn2 + logf(lt);
@@ -761,7 +910,7 @@ __global__ void __launch_bounds__(kThreadsOf<kQuant>, 1)
                         float acc[32];
                         // (a share that no row of its tiles sees has O = 0 and f = 0)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) acc[i] = __uint_as_float(ov[i]) * f1;
+                        for (int i = 0; i < 32; ++i) acc[i] = kQuant ? __fmaf_rn(__uint_as_float(ov[i]), f1, zt) : __uint_as_float(ov[i]) * f1;
                         if (pair) {
                             tc::tmem_ld32(tl + kColO + (s ^ 1) * 128 + 32 * h, ov);
                             tc::wait_ld();

@@ -348,7 +348,7 @@ sv_status launch_release_shared(const ReleaseSharedArgs &args, cudaStream_t stre
 
 struct ChunkPlan {
     int grid;
-    size_t off_counters, off_part_ml, off_part_o, bytes;
+    size_t off_counters, off_rows, off_part_ml, off_part_o, bytes;
 };
 
 struct ChunkArgs {

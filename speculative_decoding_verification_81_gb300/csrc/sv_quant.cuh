@@ -23,19 +23,24 @@ __device__ __forceinline__ uint32_t pack(const uint32_t (&c)[8]) {
     return c[0] | c[2] << 4 | c[4] << 8 | c[6] << 12 | c[1] << 16 | c[3] << 20 | c[5] << 24 | c[7] << 28;
 }
 
-// A word's eight values in bf16, dims 0 .. 7 in order: each (minimum + step * code) rounded once.
-// step and base: the two parameters twice each.  Below 16 a code in the last bits of 128 is 128 +
-// code in bf16; what is taken off is exact.
-__device__ __forceinline__ uint4 expand(uint32_t w, uint32_t step, uint32_t base) {
-    uint32_t v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t x = (w >> (4 * i) & 0x000f000fu) | 0x43004300u;
-        uint32_t c;
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(x), "r"(0x43004300u));
-        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(v[i]) : "r"(c), "r"(step), "r"(base));
-    }
-    return make_uint4(v[0], v[1], v[2], v[3]);
+// A pair of codes in the last four bits of each half, less 8, as a pair of bf16: in the last bits of
+// 128 a code is 128 + code, and what is taken off is exact.
+__device__ __forceinline__ uint32_t centred(uint32_t pair) {
+    const uint32_t x = (pair & 0x000f000fu) | 0x43004300u;
+    uint32_t c;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(x), "r"(0x43084308u));
+    return c;
+}
+// The same as a pair of f16 (in the last bits of 1024).
+__device__ __forceinline__ uint32_t centred_f16(uint32_t pair) {
+    const uint32_t x = (pair & 0x000f000fu) | 0x64006400u;
+    uint32_t c;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(c) : "r"(x), "r"(0x64086408u));
+    return c;
+}
+// A word's eight codes less 8 in bf16, dims 0 .. 7 in order.
+__device__ __forceinline__ uint4 expand(uint32_t w) {
+    return make_uint4(centred(w), centred(w >> 4), centred(w >> 8), centred(w >> 12));
 }
 
 }  // namespace quant

@@ -1,0 +1,818 @@
+// sv_quant_rows.cu -- attention over pages held in 4 bits, form for few rows a
+// sequence: single tokens, chains, draft trees.
+//
+// An item is the rows of some tokens of one sequence and the heads of them that
+// share K/V: up to 8 NT columns.  Each of the CTA's eight warps takes 16 slots of
+// every 128-slot tile and goes on by itself to the item's end:
+//     S = codes Q^T             (16 slots x 8 NT columns; codes less 8, exact in bf16)
+//     s = step_k S + middle_k sum(q), scaled to log2 units
+//     P = 2^(s - u) step_v, rounded to f16; l += 2^(s - u); z += 2^(s - u) middle_v
+//     O^T += codes^T P          (D dims x 8 NT columns; codes less 8, exact in f16)
+// and out = (O + z) / l, where the warps, then the CTAs that share an item, are
+// brought to one u.  A column's u moves only when some P would pass 2^12: f16 then
+// holds P to 2^-12 of itself, or of 2^-14 of the largest where it is smaller, and
+// the steps and middles never meet a matrix product, so that nothing of the cache
+// is rounded.
+//
+// Why the warp's own products of 16 x 8 (mma.sync; 1024 multiply-adds a clock and SM
+// measured, a quarter of tcgen05's): the codes become operands in the registers that
+// they are loaded to, eleven instructions for eight of them, where tensor memory's
+// products want them written to shared memory as 16-bit tiles first, four times the
+// pages' bytes, and read from there for a column count that is mostly padding; and a
+// slot's step and middle are a lane's own, where a thread a row needs each of them
+// from shared memory.
+#include <mutex>
+
+#include "sv_attn_common.cuh"
+#include "sv_chunk.cuh"
+#include "sv_quant.cuh"
+#include "sv_quant_rows.h"
+
+namespace sv {
+namespace chunk {
+
+namespace {
+
+constexpr int kRW = 8, kRT = 32 * kRW;  // warps, threads
+constexpr int kU = 16;                  // slots of a unit
+constexpr float kUnset = -1e38f;        // u of a column that has seen no slot
+constexpr float kRoom = 12.f;           // log2 of the largest P
+constexpr float kLeast = -60.f;         // log2 of a step below which it counts as this much for u
+
+// K codes, V codes, K's and V's parameters of a unit.
+template <int D>
+constexpr int kUnitRaw = kU * (D + 8);
+template <int NT>
+constexpr int kCtasAnSm = NT <= 2 ? 2 : 1;
+template <int D, int NT>
+constexpr int kRowsDepth = D == 128 ? (NT <= 2 ? 4 : 6) : 8;  // units of a warp on their way
+template <int NT>
+constexpr int kMeet = NT <= 2 ? 1 : 2;  // blocks of 8 columns that the warps bring together at once
+template <int D>
+constexpr int kMeetBytes = kRW * 8 * D * 4;
+
+template <int D, int NT>
+struct RowsShared {
+    uint8_t ring[kRW][kRowsDepth<D, NT>][kUnitRaw<D>];
+    float4 meet[kMeet<NT> * kMeetBytes<D> / 16];
+    uint8_t q[2][8 * NT * D * 2];
+    float qs[8 * NT];
+    float u[kRW][8 * NT];
+    float2 ml[kRW][8 * NT];
+    unsigned long long above[2][kTreeNodes];
+    long long warp_units[kRW];
+    long long before[kRT];
+    uint64_t full[kRW][kRowsDepth<D, NT>];
+    uint8_t tok[2][8 * NT];
+    int lost, last;
+};
+
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 x;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(a) : "memory");
+    return x;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+    uint2 x;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(a) : "memory");
+    return x;
+}
+__device__ __forceinline__ uint32_t lds4(uint32_t a) {
+    uint32_t x;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(a) : "memory");
+    return x;
+}
+
+// 16 bytes to shared memory without a register, zeros where `on` is false.
+__device__ __forceinline__ void copy16(uint32_t to, const void *from, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// D (16 x 8, f32) += A (16 x 16) B (16 x 8): with g = lane / 4 and t = lane % 4, a0..a3 hold A at
+// rows g, g + 8, g, g + 8 and columns 2t, 2t + 1 (the last two 8 further), b0, b1 B at rows 2t,
+// 2t + 1 and 8 further, column g, d[0..3] D at (g, 2t), (g, 2t + 1), (g + 8, 2t), (g + 8, 2t + 1).
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The transpose of an 8 x 8 matrix of 16 bits, lane (g, t) with row g, columns 2t and 2t + 1.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// Two floats to f16 (nearest even), lo in the low half.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float lg2_approx(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Place of 16-byte piece `piece` of column c's row of Q, of D / 8: lane t reads pieces
+// (D / 32) t .. of it, and eight lanes (two columns, t = 0 .. 3) then meet eight bank groups.
+template <int D>
+__device__ __forceinline__ uint32_t q_piece(int c, int piece) {
+    const int x = D == 128 ? (piece >> 3 & 1) ^ (c & 1) << 1 : c & 1;
+    return (uint32_t)(c * (D * 2) + ((piece ^ x) << 4));
+}
+
+// Row r of a unit's S is slot r ^ (r >> 1 & 1): the slots of rows 2t and 2t + 1, whose V codes lane
+// t reads, then start in the other 64 bytes for every other t.
+__device__ __forceinline__ int slot_of(int r) { return r ^ (r >> 1 & 1); }
+
+struct RowsItem {
+    int b, h;          // sequence (-1: no more), group of heads
+    int row0, ntok;    // first row, tokens
+    int pos0;          // position of the first token
+    int seq_row0;      // the sequence's first row
+    int kt0, n;        // first K/V tile and number of tiles of this run
+    int c_first, nc, ci;  // CTAs that share the item's tiles, this one's number among them
+};
+
+// The items of this CTA's units, one after another; the same in every lane.
+struct RowsWalk {
+    long long U, u0, u1, ui;  // ui: first unit of item (b, h, i)
+    int nctas, b, h, i;
+    RowsSeq seq;
+    bool loaded;
+};
+
+__device__ __forceinline__ RowsSeq load_seq(const RowsParams &p, int b) {
+    return rows_seq(p.rows, p.prefix_lens[b], p.row_starts[b], p.row_starts[b + 1]);
+}
+
+__device__ __noinline__ void next_item(const RowsParams &p, RowsWalk &w, RowsItem &it) {
+    it.b = -1;
+    while (w.b < p.B && w.ui < w.u1) {
+        if (!w.loaded) {
+            w.seq = load_seq(p, w.b);
+            w.loaded = true;
+            w.h = w.i = 0;
+        }
+        if (w.seq.items == 0 || w.h == p.groups) {
+            ++w.b;
+            w.loaded = false;
+            continue;
+        }
+        const RowsSeq s = w.seq;
+        const int i = w.i, h = w.h, n = rows_tiles(p.rows, s, i);
+        const long long first = w.ui + kRowsItemCost;  // unit of the first tile
+        w.ui = first + n;
+        if (++w.i == s.items) w.i = 0, ++w.h;
+        const int a = w.u0 > first ? (int)min(w.u0 - first, (long long)n) : 0;
+        const int z = w.u1 > first ? (int)min(w.u1 - first, (long long)n) : 0;
+        if (a >= z) continue;
+        it.b = w.b;
+        it.h = h;
+        it.row0 = s.row0 + i * p.rows.tok;
+        it.ntok = min(p.rows.tok, s.n - i * p.rows.tok);
+        it.pos0 = s.L + i * p.rows.tok;
+        it.seq_row0 = s.row0;
+        it.kt0 = rows_first_tile(p.rows, it.pos0) + a;
+        it.n = z - a;
+        it.c_first = blockIdx.x;
+        it.nc = 1;
+        if (it.n < n) {
+            it.c_first = cta_of(w.U, w.nctas, first);
+            it.nc = cta_of(w.U, w.nctas, first + n - 1) - it.c_first + 1;
+        }
+        it.ci = (int)blockIdx.x - it.c_first;
+        return;
+    }
+}
+
+}  // namespace
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const RowsParams p) {
+    constexpr int kDepth = kRowsDepth<D, NT>;
+    constexpr int kRow = D / 2;   // bytes of a row's codes
+    constexpr int kW = D / 32;    // words of a K row a lane: words kW t + j
+    constexpr int kX = D / 16;    // blocks of 16 dims of O^T
+    extern __shared__ __align__(16) uint8_t dynamic[];
+    using Sh = RowsShared<D, NT>;
+    Sh &sh = *reinterpret_cast<Sh *>(dynamic);
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, t = lane & 3;
+    if (lane < kDepth) mbar_init(&sh.full[warp][lane], 1);
+    fence_mbar_init();
+    if (tid == 0) sh.lost = 0;
+    griddep_wait();
+    griddep_launch_dependents();
+    unsigned long long call = 0;
+    if (tid == 0) call = begin_call(p.call);
+
+    // ---- the work list: units before each thread's sequences, and this CTA's share
+    RowsWalk walk;
+    {
+        const int per = (p.B + kRT - 1) / kRT, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+        long long mine = 0;
+#pragma unroll 1
+        for (int b = b0; b < b1; ++b) {
+            const RowsSeq s = load_seq(p, b);
+            mine += rows_units_before(p.rows, s, s.items) * p.groups;
+        }
+        long long x = mine;
+#pragma unroll 1
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, off);
+            if (lane >= off) x += y;
+        }
+        if (lane == 31) sh.warp_units[warp] = x;
+        __syncthreads();
+        long long base = 0;
+        walk.U = 0;
+#pragma unroll 1
+        for (int w = 0; w < kRW; ++w) {
+            if (w < warp) base += sh.warp_units[w];
+            walk.U += sh.warp_units[w];
+        }
+        sh.before[tid] = base + x - mine;
+        __syncthreads();
+        walk.nctas = rows_ctas(walk.U, gridDim.x);
+        const bool has = walk.U > 0 && (int)blockIdx.x < walk.nctas;
+        walk.u0 = has ? cta_begin(walk.U, walk.nctas, blockIdx.x) : 0;
+        walk.u1 = has ? cta_begin(walk.U, walk.nctas, blockIdx.x + 1) : 0;
+        walk.b = p.B;
+        walk.ui = 0;
+        walk.h = walk.i = 0;
+        walk.loaded = false;
+        if (has) {  // the last thread with at most u0 units before its sequences, then the sequence
+            int at = 0;
+#pragma unroll 1
+            for (int i = lane; i < kRT; i += 32) at += sh.before[i] <= walk.u0;
+            at = __reduce_add_sync(0xffffffffu, at) - 1;
+            walk.b = at * per;
+            walk.ui = sh.before[at];
+#pragma unroll 1
+            while (walk.b < p.B) {
+                walk.seq = load_seq(p, walk.b);
+                const long long head = rows_units_before(p.rows, walk.seq, walk.seq.items);
+                if (walk.seq.items > 0 && walk.ui + head * p.groups > walk.u0) {
+                    walk.loaded = true;
+                    walk.h = (int)quot(walk.u0 - walk.ui, head);
+                    const long long v = walk.u0 - walk.ui - walk.h * head;
+                    walk.i = rows_item_at(p.rows, walk.seq, v);
+                    walk.ui += walk.h * head + rows_units_before(p.rows, walk.seq, walk.i);
+                    break;
+                }
+                walk.ui += head * p.groups;
+                ++walk.b;
+            }
+        }
+    }
+
+    uint8_t *const ring = sh.ring[warp][0];
+    const uint32_t ring_at = smem_u32(ring);
+    uint32_t put = 0, got = 0;  // units asked for and used
+    bool lost = false;
+    RowsItem it;
+
+    // of the item at hand, or of the one whose copies are begun: this warp's tiles i0 .. i1 - 1, the
+    // next to ask for, and, a lane a tile from `base` on, the cache rows of the unit's halves
+    int i0 = 0, i1 = 0, ask = 0, base = 0, y0 = -1, y1 = -1;
+    auto load_rows = [&](const RowsItem &x) {
+        const int slot = (x.kt0 + base + lane) * kTileSlots + warp * kU;
+        const int lo = p.rows.window > 0 ? max(0, x.pos0 - p.rows.window + 1) : 0, hi = x.pos0 + x.ntok;
+        const int32_t *trow = p.block_table + (size_t)x.b * p.max_pages;
+        auto row = [&](int s) -> int {  // (a page id out of range is reported; page 0 is read in its place)
+            int pg = trow[s / p.page_size];
+            if (pg < 0 || pg >= p.num_pages) pg = 0;
+            return (pg * p.Hkv + x.h / p.parts) * p.page_size + s % p.page_size;
+        };
+        y0 = y1 = -1;
+        if (base + lane < i1) {
+            if (p.page_size > 8) {
+                y0 = row(slot);
+                y1 = y0 + 8;
+            } else {
+                if (slot + 8 > lo && slot < hi) y0 = row(slot);
+                if (slot + 16 > lo && slot + 8 < hi) y1 = row(slot + 8);
+            }
+        }
+    };
+    auto fetch = [&](const RowsItem &x) {  // the unit of tile `ask`
+        if (ask - base == 32) {
+            base = ask;
+            load_rows(x);
+        }
+        const int a0 = __shfl_sync(0xffffffffu, y0, ask - base), a1 = __shfl_sync(0xffffffffu, y1, ask - base);
+        if (lane == 0) {
+            const uint32_t st = put % kDepth;
+            uint64_t *bar = &sh.full[warp][st];
+            uint8_t *to = ring + st * kUnitRaw<D>;
+            mbar_arrive_expect_tx(bar, (uint32_t)(((a0 >= 0) + (a1 >= 0)) * (kUnitRaw<D> / 2)));
+            const bool whole = p.page_size > 8;
+            const int rows = whole ? 16 : 8;
+#pragma unroll 1
+            for (int half = 0; half < (whole ? 1 : 2); ++half) {
+                const int y = half ? a1 : a0;
+                if (y < 0) continue;
+                bulk_load(to + half * 8 * kRow, p.k_codes + (size_t)y * kRow, rows * kRow, bar);
+                bulk_load(to + kU * kRow + half * 8 * kRow, p.v_codes + (size_t)y * kRow, rows * kRow, bar);
+                bulk_load(to + 2 * kU * kRow + half * 32, p.k_params + y, rows * 4, bar);
+                bulk_load(to + 2 * kU * kRow + kU * 4 + half * 32, p.v_params + y, rows * 4, bar);
+            }
+        }
+        ++put;
+        ++ask;
+    };
+    int qb = 0;
+    auto begin = [&](const RowsItem &x, int buf) {  // its first copies, and its queries
+        const int lo = p.rows.window > 0 ? max(0, x.pos0 - p.rows.window + 1) : 0, hi = x.pos0 + x.ntok;
+        const int s0 = x.kt0 * kTileSlots + warp * kU;  // (the slots seen end, or begin, within a tile)
+        i0 = s0 + kU <= lo ? 1 : 0;
+        i1 = s0 < hi ? min(x.n, (hi - s0 - 1) / kTileSlots + 1) : 0;
+        if (lost) i1 = 0;
+        ask = base = i0;
+        load_rows(x);
+#pragma unroll 1
+        for (int i = 0; i < kDepth; ++i)
+            if (ask < i1) fetch(x);
+        const int heads = min(p.Gs, p.G - x.h % p.parts * p.Gs), cols = x.ntok * p.Gs;
+        const int head0 = x.h / p.parts * p.G + x.h % p.parts * p.Gs;
+        const uint32_t q_at = smem_u32(sh.q[buf]);
+        for (int i = tid; i < 8 * NT * (D / 8); i += kRT) {
+            const int c = i / (D / 8), piece = i % (D / 8), tk = c / p.Gs, hd = c - tk * p.Gs;
+            const bool on = c < cols && hd < heads;
+            const uint16_t *from = p.q + (size_t)(x.row0 + (on ? tk : 0)) * p.q_stride + (size_t)(head0 + (on ? hd : 0)) * D + piece * 8;
+            copy16(q_at + q_piece<D>(c, piece), from, on);
+            if (piece == 0) sh.tok[buf][c] = (uint8_t)min(tk, x.ntok - 1);
+        }
+        if (p.parents && warp < 2) {  // a token's set of nodes above it, of those up to the item's last
+            const int node0 = x.row0 - x.seq_row0, nodes = min(node0 + x.ntok, kTreeNodes);
+            const int32_t *par = p.parents + x.seq_row0;
+            const int a = lane < nodes ? par[lane] : -1, b = lane + 32 < nodes ? par[lane + 32] : -1;
+            const int tk = tid, node = node0 + tk;
+            const unsigned long long set = ancestors_warp(false, a, b, node, tk < x.ntok && node < nodes);
+            sh.above[buf][tk] = set;
+        }
+    };
+    next_item(p, walk, it);
+    if (it.b >= 0) begin(it, 0);
+
+    // ---- seq_status, while the first copies are on their way
+    const int own = p.seq_status ? (int)blockIdx.x * kRW + warp : p.B;
+#pragma unroll 1
+    for (int sb = own; sb < p.B; sb += (int)gridDim.x * kRW) {
+        const int L = p.prefix_lens[sb], first = p.row_starts[sb], end = p.row_starts[sb + 1];
+        const RowsSeq s = rows_seq(p.rows, L, first, end);
+        bool bad = !lengths_ok(Shape{1, p.rows.window, p.rows.num_rows, p.rows.S_max}, L, first, end);
+        if (s.n > 0) {
+            const int lo = p.rows.window > 0 ? max(0, L - p.rows.window + 1) : 0;
+            const int32_t *trow = p.block_table + (size_t)sb * p.max_pages;
+#pragma unroll 1
+            for (int j = lo / p.page_size + lane; j <= (L + s.n - 1) / p.page_size; j += 32) {
+                const int pg = trow[j];
+                if (pg < 0 || pg >= p.num_pages) bad = true;
+            }
+            if (p.parents) {
+                bad = bad || s.n > kTreeNodes;
+#pragma unroll 1
+                for (int i = lane; i < min(s.n, kTreeNodes); i += 32) {
+                    const int par = p.parents[first + i];
+                    if (i == 0 ? par != -1 : par < 0 || par >= i) bad = true;
+                }
+            }
+        }
+        bad = __any_sync(0xffffffffu, bad);
+        if (lane == 0) p.seq_status[sb] = bad ? SV_ERR_BAD_INPUT : SV_OK;
+    }
+
+#pragma unroll 1
+    while (it.b >= 0) {
+        const int cols = it.ntok * p.Gs, nt = (cols + 7) / 8;
+        const int lo = p.rows.window > 0 ? max(0, it.pos0 - p.rows.window + 1) : 0, hi = it.pos0 + it.ntok;
+        const int own0 = it.pos0 - (it.row0 - it.seq_row0);  // slot of the sequence's first new row
+        // below: every row sees the slots; from all_lo on too
+        const int all_hi = p.parents ? own0 : it.pos0 + 1;
+        const int all_lo = p.rows.window > 0 ? it.pos0 + it.ntok - p.rows.window : 0;
+        copies_done();
+        for (int i = lane; i < 8 * NT; i += 32) sh.u[warp][i] = kUnset;
+        __syncthreads();
+        const uint32_t q_at = smem_u32(sh.q[qb]), u_at = smem_u32(sh.u[warp]), qs_at = smem_u32(sh.qs);
+        float o[kX][NT][4], l[NT][2], z[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            l[n][0] = l[n][1] = z[n][0] = z[n][1] = 0.f;
+#pragma unroll
+            for (int x = 0; x < kX; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[x][n][e] = 0.f;
+        }
+        // the columns' sums of Q, by products with ones; each warp a block of columns
+        if (warp < NT) {
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint32_t one = 0x3f803f80u;
+#pragma unroll
+            for (int j = 0; j < kW; ++j) {
+                const uint4 b = lds16(q_at + q_piece<D>(8 * warp + g, kW * t + j));
+                mma_bf16(s, one, one, one, one, b.x, b.y);
+                mma_bf16(s, one, one, one, one, b.z, b.w);
+            }
+            if (g == 0) {
+                sh.qs[8 * warp + 2 * t] = s[0];
+                sh.qs[8 * warp + 2 * t + 1] = s[1];
+            }
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int i = i0; i < i1; ++i) {
+            const uint32_t st = got % kDepth;
+            if (!warp_wait_bounded(&sh.full[warp][st], got / kDepth & 1)) {
+                lost = true;
+                break;
+            }
+            const uint32_t at = ring_at + st * kUnitRaw<D>;
+            const int slot0 = (it.kt0 + i) * kTileSlots + warp * kU;
+            // ---- S
+            float s[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+            {
+                uint32_t k0[kW], k1[kW];
+                const uint32_t ka = at + slot_of(g) * kRow + t * (4 * kW);
+                if constexpr (kW == 4) {
+                    const uint4 a = lds16(ka), b = lds16(ka + 8 * kRow);
+                    k0[0] = a.x, k0[1] = a.y, k0[2] = a.z, k0[3] = a.w;
+                    k1[0] = b.x, k1[1] = b.y, k1[2] = b.z, k1[3] = b.w;
+                } else {
+                    const uint2 a = lds8(ka), b = lds8(ka + 8 * kRow);
+                    k0[0] = a.x, k0[1] = a.y;
+                    k1[0] = b.x, k1[1] = b.y;
+                }
+#pragma unroll
+                for (int j = 0; j < kW; ++j) {
+                    const uint4 a = quant::expand(k0[j]), b = quant::expand(k1[j]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const uint4 q = lds16(q_at + q_piece<D>(8 * n + g, kW * t + j));
+                        mma_bf16(s[n], a.x, b.x, a.y, b.y, q.x, q.y);
+                        mma_bf16(s[n], a.z, b.z, a.w, b.w, q.z, q.w);
+                    }
+                }
+            }
+            // ---- steps and middles of the lane's two slots (rows g and g + 8 of S)
+            const int slot = slot0 + slot_of(g);
+            float ks[2], km[2], vs[2], vm[2], bound[2];
+            const bool inside = slot0 >= lo && slot0 + kU <= hi;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint32_t pa = at + 2 * kU * kRow + (slot_of(g) + 8 * r) * 4;
+                const uint32_t kp = lds4(pa);
+                uint32_t vp = lds4(pa + kU * 4);
+                if (!inside && (slot + 8 * r < lo || slot + 8 * r >= hi)) vp = 0;  // (it may hold anything; K's is hidden)
+                ks[r] = bf16_lo(kp) * p.scale_log2;
+                km[r] = __fmaf_rn(8.f, bf16_lo(kp), bf16_hi(kp)) * p.scale_log2;
+                vs[r] = bf16_lo(vp);
+                vm[r] = __fmaf_rn(8.f, vs[r], bf16_hi(vp));
+                bound[r] = kRoom - fmaxf(lg2_approx(fabsf(vs[r])), kLeast);
+            }
+            const bool masked = slot0 + kU > all_hi || slot0 < all_lo;
+            bool over = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const uint2 q2 = lds8(qs_at + (8 * n + 2 * t) * 4), u2 = lds8(u_at + (8 * n + 2 * t) * 4);
+                const float qs[2] = {__uint_as_float(q2.x), __uint_as_float(q2.y)};
+                const float u[2] = {__uint_as_float(u2.x), __uint_as_float(u2.y)};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[n][e] = __fmaf_rn(s[n][e], ks[e >> 1], km[e >> 1] * qs[e & 1]);
+                if (masked) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int tk = sh.tok[qb][8 * n + 2 * t + c], pos = it.pos0 + tk;
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const int x = slot + 8 * r;
+                            bool sees = x <= pos && (p.rows.window == 0 || x > pos - p.rows.window);
+                            if (p.parents) sees = x < own0 || (x - own0 < kTreeNodes && (sh.above[qb][tk] >> (x - own0) & 1));
+                            if (!sees) s[n][2 * r + c] = kNegInf;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) over = over || s[n][e] - u[e & 1] > bound[e >> 1];
+            }
+            if (__any_sync(0xffffffffu, over)) {  // some column's u moves up to its largest P
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const uint2 u2 = lds8(u_at + (8 * n + 2 * t) * 4);
+                    float u[2] = {__uint_as_float(u2.x), __uint_as_float(u2.y)}, f[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float a = fmaxf(s[n][c] + (kRoom - bound[0]), s[n][2 + c] + (kRoom - bound[1]));
+#pragma unroll
+                        for (int off = 4; off < 32; off <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+                        const bool up = a > u[c] + kRoom;
+                        f[c] = up ? ex2_approx(u[c] - a) : 1.f;
+                        if (up) u[c] = a;
+                        l[n][c] *= f[c];
+                        z[n][c] *= f[c];
+                    }
+#pragma unroll
+                    for (int x = 0; x < kX; ++x)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[x][n][e] *= f[e & 1];
+                    if (g == 0) *reinterpret_cast<float2 *>(&sh.u[warp][8 * n + 2 * t]) = make_float2(u[0], u[1]);
+                }
+                __syncwarp();
+            }
+            // ---- P
+            uint32_t p0[NT], p1[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                p0[n] = p1[n] = 0;
+                const uint2 u2 = lds8(u_at + (8 * n + 2 * t) * 4);
+                const float u[2] = {__uint_as_float(u2.x), __uint_as_float(u2.y)};
+                float e[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) e[k] = ex2_approx(s[n][k] - u[k & 1]);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    l[n][c] += e[c] + e[2 + c];
+                    z[n][c] = __fmaf_rn(e[c], vm[0], __fmaf_rn(e[2 + c], vm[1], z[n][c]));
+                }
+                p0[n] = transposed(pack_f16x2(e[0] * vs[0], e[1] * vs[0]));
+                p1[n] = transposed(pack_f16x2(e[2] * vs[1], e[3] * vs[1]));
+            }
+            // ---- O^T: a byte of each of four slots' words is two dims' operand
+            {
+                const uint32_t va = at + kU * kRow + g * (kX), s0 = slot_of(2 * t), s1 = slot_of(2 * t + 1);
+                uint32_t w[4][kX / 4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const uint32_t from = va + ((y & 1 ? s1 : s0) + (y >> 1) * 8) * kRow;
+                    if constexpr (kX == 8) {
+                        const uint2 a = lds8(from);
+                        w[y][0] = a.x, w[y][1] = a.y;
+                    } else {
+                        w[y][0] = lds4(from);
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < kX; ++x) {
+                    const int b = x & 3;
+                    const uint32_t sel = b | b << 4 | (4 + b) << 8 | (4 + b) << 12;
+                    const uint32_t c0 = __byte_perm(w[0][x >> 2], w[1][x >> 2], sel), c1 = __byte_perm(w[2][x >> 2], w[3][x >> 2], sel);
+                    const uint32_t a0 = quant::centred_f16(c0), a1 = quant::centred_f16(c0 >> 4);
+                    const uint32_t a2 = quant::centred_f16(c1), a3 = quant::centred_f16(c1 >> 4);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma_f16(o[x][n], a0, a1, a2, a3, p0[n], p1[n]);
+                    }
+                }
+            }
+            __syncwarp();
+            ++got;
+            if (ask < i1) fetch(it);
+        }
+        if (lost) {  // its own copies still on their way, this one too
+#pragma unroll 1
+            for (; got < put; ++got) warp_wait_bounded(&sh.full[warp][got % kDepth], got / kDepth & 1);
+            sh.lost = 1;
+        }
+        // ---- the warps' sums
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            if (n >= nt) break;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) {
+                    l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], off);
+                    z[n][c] += __shfl_xor_sync(0xffffffffu, z[n][c], off);
+                }
+                if (g == 0) sh.ml[warp][8 * n + 2 * t + c] = make_float2(sh.u[warp][8 * n + 2 * t + c], l[n][c]);
+            }
+        }
+        const RowsItem cur = it;
+        next_item(p, walk, it);
+        qb ^= 1;
+        if (it.b >= 0) begin(it, qb);  // (the next item's copies run while this one's sums meet)
+        const bool whole = cur.nc == 1;
+        const int heads = min(p.Gs, p.G - cur.h % p.parts * p.Gs);
+        const int head0 = cur.h / p.parts * p.G + cur.h % p.parts * p.Gs;
+        const int part = (int)blockIdx.x * 2 + (cur.ci == 0 ? 1 : 0);
+        // where column c's row goes; -1: it is padding
+        auto out_row = [&](int c) -> long long {
+            const int tk = c / p.Gs, hd = c - tk * p.Gs;
+            return c < cols && hd < heads ? (long long)(cur.row0 + tk) * p.Hq + head0 + hd : -1;
+        };
+#pragma unroll
+        for (int n0 = 0; n0 < NT; n0 += kMeet<NT>) {
+            if (n0 >= nt) break;
+#pragma unroll
+            for (int dn = 0; dn < kMeet<NT>; ++dn) {
+                const int n = n0 + dn;
+                if (n >= NT || n >= nt) break;
+#pragma unroll
+                for (int x = 0; x < kX; ++x)
+                    sh.meet[((warp * kMeet<NT> + dn) * kX + x) * 32 + lane] =
+                        make_float4(o[x][n][0] + z[n][0], o[x][n][1] + z[n][1], o[x][n][2] + z[n][0], o[x][n][3] + z[n][1]);
+            }
+            __syncthreads();
+            // a task: eight dims of two columns
+            for (int i = tid; i < kMeet<NT> * (kX / 4) * 32; i += kRT) {
+                const int ln = i & 31, w4 = (i >> 5) % (kX / 4), dn = (i >> 5) / (kX / 4), n = n0 + dn;
+                if (n >= nt) break;
+                const int c0 = 8 * n + 2 * (ln & 3);
+                float M[2] = {kUnset, kUnset}, sum[2] = {0.f, 0.f}, f[2][kRW], acc[2][8] = {};
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                    for (int w = 0; w < kRW; ++w) M[c] = fmaxf(M[c], sh.ml[w][c0 + c].x);
+#pragma unroll
+                    for (int w = 0; w < kRW; ++w) {
+                        const float2 y = sh.ml[w][c0 + c];
+                        f[c][w] = ex2_approx(y.x - M[c]);
+                        sum[c] = __fmaf_rn(y.y, f[c][w], sum[c]);
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < kRW; ++w)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        constexpr int kDim[4][2] = {{0, 2}, {4, 6}, {1, 3}, {5, 7}};
+                        const float4 v = sh.meet[((w * kMeet<NT> + dn) * kX + 4 * w4 + b) * 32 + ln];
+                        acc[0][kDim[b][0]] = __fmaf_rn(v.x, f[0][w], acc[0][kDim[b][0]]);
+                        acc[1][kDim[b][0]] = __fmaf_rn(v.y, f[1][w], acc[1][kDim[b][0]]);
+                        acc[0][kDim[b][1]] = __fmaf_rn(v.z, f[0][w], acc[0][kDim[b][1]]);
+                        acc[1][kDim[b][1]] = __fmaf_rn(v.w, f[1][w], acc[1][kDim[b][1]]);
+                    }
+                const int dim = (ln >> 2) * (D / 8) + 8 * w4;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    if (whole) {
+                        const long long row = out_row(c0 + c);
+                        if (row < 0) continue;
+                        const float inv = 1.f / sum[c];
+                        *reinterpret_cast<uint4 *>(p.out + row * D + dim) =
+                            make_uint4(pack_bf16x2(acc[c][0] * inv, acc[c][1] * inv), pack_bf16x2(acc[c][2] * inv, acc[c][3] * inv),
+                                       pack_bf16x2(acc[c][4] * inv, acc[c][5] * inv), pack_bf16x2(acc[c][6] * inv, acc[c][7] * inv));
+                        if (p.lse && dim == 0) p.lse[row] = M[c] * kLn2 + logf(sum[c]);
+                    } else {
+                        float4 *to = reinterpret_cast<float4 *>(p.part_o + ((size_t)part * kRowsCols + c0 + c) * D + dim);
+                        __stcg(to, make_float4(acc[c][0], acc[c][1], acc[c][2], acc[c][3]));
+                        __stcg(to + 1, make_float4(acc[c][4], acc[c][5], acc[c][6], acc[c][7]));
+                        if (dim == 0) __stcg(reinterpret_cast<float2 *>(p.part_ml) + (size_t)part * kRowsCols + c0 + c, make_float2(M[c], sum[c]));
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        if (whole) continue;
+        // ---- an item shared by CTAs: the one that arrives last adds the shares up, in their order
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+            int *ctr = p.counters + rows_counter(call, cur.c_first);
+            int before_me;
+            asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before_me) : "l"(ctr) : "memory");
+            sh.last = before_me == cur.nc - 1;
+        }
+        __syncthreads();
+        if (!sh.last) continue;
+        __threadfence();
+        for (int i = tid; i < cols * (D / 8); i += kRT) {
+            const int c = i / (D / 8), dim = i % (D / 8) * 8;
+            const long long row = out_row(c);
+            if (row < 0) continue;
+            float acc[8] = {}, M = kUnset, sum = 0.f;
+            constexpr int kAhead = 4;
+#pragma unroll 1
+            for (int k0 = 0; k0 < cur.nc; k0 += kAhead) {
+                float2 ml[kAhead];
+                float4 a[kAhead], b[kAhead];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const int j = min(k0 + k, cur.nc - 1);
+                    const size_t from = (size_t)(2 * (cur.c_first + j) + (j == 0 ? 1 : 0)) * kRowsCols + c;
+                    ml[k] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml) + from);
+                    a[k] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + from * D + dim));
+                    b[k] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + from * D + dim) + 1);
+                }
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    if (k0 + k >= cur.nc) continue;
+                    const float Mn = fmaxf(M, ml[k].x), f = ex2_approx(M - Mn), w = ex2_approx(ml[k].x - Mn);
+                    M = Mn;
+                    sum = sum * f + ml[k].y * w;
+                    const float v[8] = {a[k].x, a[k].y, a[k].z, a[k].w, b[k].x, b[k].y, b[k].z, b[k].w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) acc[e] = __fmaf_rn(v[e], w, acc[e] * f);
+                }
+            }
+            const float inv = 1.f / sum;
+            *reinterpret_cast<uint4 *>(p.out + row * D + dim) =
+                make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                           pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
+            if (p.lse && dim == 0) p.lse[row] = M * kLn2 + logf(sum);
+        }
+    }
+    copies_done();
+    __syncthreads();
+    if (tid == 0) {
+        if (sh.lost) give_up(p.call, p.seq_status, p.B);
+        // the next call's, whose grid may be another
+        for (int c = blockIdx.x; c < kRowsMaxGrid; c += gridDim.x) p.counters[rows_counter(call + 1, c)] = 0;
+    }
+    if (lane == 0 && own < p.B && gave_up(p.call))
+        for (int sb = own; sb < p.B; sb += (int)gridDim.x * kRW) p.seq_status[sb] = SV_ERR_TIMEOUT;
+}
+
+namespace {
+
+struct Form {
+    const void *fn;
+    int cols, smem, ctas;
+};
+
+template <int D, int NT>
+Form form() {
+    return Form{reinterpret_cast<const void *>(&quant_rows_kernel<D, NT>), 8 * NT, (int)sizeof(RowsShared<D, NT>), kCtasAnSm<NT>};
+}
+
+constexpr int kForms = 4;
+// By columns, the fewest first.
+const Form &form_at(int D, int i) {
+    static const Form f128[kForms] = {form<128, 1>(), form<128, 2>(), form<128, 3>(), form<128, 5>()};
+    static const Form f64[kForms] = {form<64, 1>(), form<64, 2>(), form<64, 4>(), form<64, 8>()};
+    return D == 128 ? f128[i] : f64[i];
+}
+
+// CTAs of a form that the current device holds at once, asked for once a device; 0 where it does not run.
+int form_grid(int D, int i) {
+    struct Entry {
+        int dev, D, i, grid;
+    };
+    static std::mutex mu;
+    static Entry cache[64];
+    static int ncache = 0;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    for (int k = 0; k < ncache; ++k)
+        if (cache[k].dev == dev && cache[k].D == D && cache[k].i == i) return cache[k].grid;
+    const Form &f = form_at(D, i);
+    int occ = 0;
+    if (cudaFuncSetAttribute(f.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, f.smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, f.fn, kRT, f.smem) != cudaSuccess || occ < 1)
+        return 0;
+    const int grid = device_sm_count() * (occ < f.ctas ? occ : f.ctas);
+    if (ncache < 64) cache[ncache++] = Entry{dev, D, i, grid};
+    return grid;
+}
+
+}  // namespace
+
+// Rows a sequence go by the call's mean: the lengths are on the device, and any form
+// takes any rows.
+int rows_form(const ChunkArgs &a) {
+    const int G = a.Hq / a.Hkv;
+    const long long mean = ((long long)a.num_rows + a.B - 1) / a.B * G;
+    if (mean > kRowsMost) return -1;
+    int i = 0;
+    while (i + 1 < kForms && form_at(a.D, i).cols < mean) ++i;
+    return i;
+}
+
+sv_status launch_rows(const ChunkArgs &a, const QuantParams &c, int form, int *counters, cudaStream_t st) {
+    const Form &f = form_at(a.D, form);
+    const int grid = form_grid(a.D, form);
+    if (grid <= 0 || grid > kRowsMaxGrid) return SV_ERR_CUDA;
+    RowsParams p{};
+    static_cast<QuantParams &>(p) = c;
+    p.counters = counters;
+    p.q = static_cast<const uint16_t *>(a.q);
+    p.q_stride = a.q_stride;
+    p.parts = (p.G + f.cols - 1) / f.cols;
+    p.Gs = (p.G + p.parts - 1) / p.parts;
+    p.groups = p.Hkv * p.parts;
+    p.rows = RowsShape{f.cols / p.Gs, c.shape.window, c.shape.num_rows, c.shape.S_max};
+    if (a.parents && p.rows.tok > kTreeNodes) p.rows.tok = kTreeNodes;
+    void *args[] = {&p};
+    return launch_pdl(f.fn, dim3((unsigned)grid), dim3(kRT), (size_t)f.smem, st, args) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+}  // namespace chunk
+}  // namespace sv

@@ -1,0 +1,31 @@
+// sv_quant_rows.h -- parameters and entry of the form for few rows a sequence of
+// the attention over pages held in 4 bits (sv_quant_rows.cu).
+#pragma once
+
+#include "sv_chunk.cuh"
+#include "sv_quant_list.h"
+
+namespace sv {
+namespace chunk {
+
+constexpr int kRowsCols = 64;      // columns (rows times heads) of an item at most
+constexpr int kRowsMaxGrid = 512;  // CTAs of a call at most: the workspace's shares and counters
+constexpr int kRowsMost = 64;      // columns of a mean sequence up to which a call takes this form
+
+struct RowsParams : QuantParams {
+    const uint16_t *q;
+    long long q_stride;  // elements between rows of q
+    RowsShape rows;
+    int parts, Gs;       // a KV head's query heads go in `parts` groups of Gs (the last may have fewer)
+    int groups;          // Hkv * parts
+};
+
+// The counter of an item shared from CTA `cta` on, in the set of the given call.
+SV_CALL_HD int rows_counter(unsigned long long call, int cta) { return (int)(call & 1) * kRowsMaxGrid + cta; }
+
+// The form for the call's rows; -1 where it has too many.
+int rows_form(const ChunkArgs &args);
+sv_status launch_rows(const ChunkArgs &args, const QuantParams &params, int form, int *counters, cudaStream_t stream);
+
+}  // namespace chunk
+}  // namespace sv
