@@ -43,5 +43,18 @@ __device__ __forceinline__ uint4 expand(uint32_t w) {
     return make_uint4(centred(w), centred(w >> 4), centred(w >> 8), centred(w >> 12));
 }
 
+// The same in f16: of a byte's two codes the second is 1024 + 16 code where it lies, so that the pairs
+// of a word's bytes need no shifts but one.
+__device__ __forceinline__ uint32_t centred_f16_high(uint32_t pair) {
+    const uint32_t x = (pair & 0x00f000f0u) | 0x64006400u;
+    uint32_t c;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(c) : "r"(x), "r"(0x2c002c00u), "r"(0xd480d480u));  // x / 16 - 72
+    return c;
+}
+__device__ __forceinline__ uint4 expand_f16(uint32_t w) {
+    const uint32_t v = w >> 8;
+    return make_uint4(centred_f16(w), centred_f16_high(w), centred_f16(v), centred_f16_high(v));
+}
+
 }  // namespace quant
 }  // namespace sv

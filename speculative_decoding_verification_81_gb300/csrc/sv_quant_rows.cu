@@ -26,7 +26,7 @@
 #include "sv_attn_common.cuh"
 #include "sv_chunk.cuh"
 #include "sv_quant.cuh"
-#include "sv_quant_rows.h"
+#include "sv_quant_walk.cuh"
 
 namespace sv {
 namespace chunk {
@@ -35,9 +35,6 @@ namespace {
 
 constexpr int kRW = 8, kRT = 32 * kRW;  // warps, threads
 constexpr int kU = 16;                  // slots of a unit
-constexpr float kUnset = -1e38f;        // u of a column that has seen no slot
-constexpr float kRoom = 12.f;           // log2 of the largest P
-constexpr float kLeast = -60.f;         // log2 of a step below which it counts as this much for u
 
 // K codes, V codes, K's and V's parameters of a unit.
 template <int D>
@@ -123,12 +120,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return r;
 }
 
-__device__ __forceinline__ float lg2_approx(float x) {
-    float y;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // Place of 16-byte piece `piece` of column c's row of Q, of D / 8: lane t reads pieces
 // (D / 32) t .. of it, and eight lanes (two columns, t = 0 .. 3) then meet eight bank groups.
 template <int D>
@@ -140,67 +131,6 @@ __device__ __forceinline__ uint32_t q_piece(int c, int piece) {
 // Row r of a unit's S is slot r ^ (r >> 1 & 1): the slots of rows 2t and 2t + 1, whose V codes lane
 // t reads, then start in the other 64 bytes for every other t.
 __device__ __forceinline__ int slot_of(int r) { return r ^ (r >> 1 & 1); }
-
-struct RowsItem {
-    int b, h;          // sequence (-1: no more), group of heads
-    int row0, ntok;    // first row, tokens
-    int pos0;          // position of the first token
-    int seq_row0;      // the sequence's first row
-    int kt0, n;        // first K/V tile and number of tiles of this run
-    int c_first, nc, ci;  // CTAs that share the item's tiles, this one's number among them
-};
-
-// The items of this CTA's units, one after another; the same in every lane.
-struct RowsWalk {
-    long long U, u0, u1, ui;  // ui: first unit of item (b, h, i)
-    int nctas, b, h, i;
-    RowsSeq seq;
-    bool loaded;
-};
-
-__device__ __forceinline__ RowsSeq load_seq(const RowsParams &p, int b) {
-    return rows_seq(p.rows, p.prefix_lens[b], p.row_starts[b], p.row_starts[b + 1]);
-}
-
-__device__ __noinline__ void next_item(const RowsParams &p, RowsWalk &w, RowsItem &it) {
-    it.b = -1;
-    while (w.b < p.B && w.ui < w.u1) {
-        if (!w.loaded) {
-            w.seq = load_seq(p, w.b);
-            w.loaded = true;
-            w.h = w.i = 0;
-        }
-        if (w.seq.items == 0 || w.h == p.groups) {
-            ++w.b;
-            w.loaded = false;
-            continue;
-        }
-        const RowsSeq s = w.seq;
-        const int i = w.i, h = w.h, n = rows_tiles(p.rows, s, i);
-        const long long first = w.ui + kRowsItemCost;  // unit of the first tile
-        w.ui = first + n;
-        if (++w.i == s.items) w.i = 0, ++w.h;
-        const int a = w.u0 > first ? (int)min(w.u0 - first, (long long)n) : 0;
-        const int z = w.u1 > first ? (int)min(w.u1 - first, (long long)n) : 0;
-        if (a >= z) continue;
-        it.b = w.b;
-        it.h = h;
-        it.row0 = s.row0 + i * p.rows.tok;
-        it.ntok = min(p.rows.tok, s.n - i * p.rows.tok);
-        it.pos0 = s.L + i * p.rows.tok;
-        it.seq_row0 = s.row0;
-        it.kt0 = rows_first_tile(p.rows, it.pos0) + a;
-        it.n = z - a;
-        it.c_first = blockIdx.x;
-        it.nc = 1;
-        if (it.n < n) {
-            it.c_first = cta_of(w.U, w.nctas, first);
-            it.nc = cta_of(w.U, w.nctas, first + n - 1) - it.c_first + 1;
-        }
-        it.ci = (int)blockIdx.x - it.c_first;
-        return;
-    }
-}
 
 }  // namespace
 
@@ -222,65 +152,8 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const Ro
     unsigned long long call = 0;
     if (tid == 0) call = begin_call(p.call);
 
-    // ---- the work list: units before each thread's sequences, and this CTA's share
     RowsWalk walk;
-    {
-        const int per = (p.B + kRT - 1) / kRT, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-        long long mine = 0;
-#pragma unroll 1
-        for (int b = b0; b < b1; ++b) {
-            const RowsSeq s = load_seq(p, b);
-            mine += rows_units_before(p.rows, s, s.items) * p.groups;
-        }
-        long long x = mine;
-#pragma unroll 1
-        for (int off = 1; off < 32; off <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, x, off);
-            if (lane >= off) x += y;
-        }
-        if (lane == 31) sh.warp_units[warp] = x;
-        __syncthreads();
-        long long base = 0;
-        walk.U = 0;
-#pragma unroll 1
-        for (int w = 0; w < kRW; ++w) {
-            if (w < warp) base += sh.warp_units[w];
-            walk.U += sh.warp_units[w];
-        }
-        sh.before[tid] = base + x - mine;
-        __syncthreads();
-        walk.nctas = rows_ctas(walk.U, gridDim.x);
-        const bool has = walk.U > 0 && (int)blockIdx.x < walk.nctas;
-        walk.u0 = has ? cta_begin(walk.U, walk.nctas, blockIdx.x) : 0;
-        walk.u1 = has ? cta_begin(walk.U, walk.nctas, blockIdx.x + 1) : 0;
-        walk.b = p.B;
-        walk.ui = 0;
-        walk.h = walk.i = 0;
-        walk.loaded = false;
-        if (has) {  // the last thread with at most u0 units before its sequences, then the sequence
-            int at = 0;
-#pragma unroll 1
-            for (int i = lane; i < kRT; i += 32) at += sh.before[i] <= walk.u0;
-            at = __reduce_add_sync(0xffffffffu, at) - 1;
-            walk.b = at * per;
-            walk.ui = sh.before[at];
-#pragma unroll 1
-            while (walk.b < p.B) {
-                walk.seq = load_seq(p, walk.b);
-                const long long head = rows_units_before(p.rows, walk.seq, walk.seq.items);
-                if (walk.seq.items > 0 && walk.ui + head * p.groups > walk.u0) {
-                    walk.loaded = true;
-                    walk.h = (int)quot(walk.u0 - walk.ui, head);
-                    const long long v = walk.u0 - walk.ui - walk.h * head;
-                    walk.i = rows_item_at(p.rows, walk.seq, v);
-                    walk.ui += walk.h * head + rows_units_before(p.rows, walk.seq, walk.i);
-                    break;
-                }
-                walk.ui += head * p.groups;
-                ++walk.b;
-            }
-        }
-    }
+    plan_walk<kRT>(p, sh.warp_units, sh.before, tid, walk);
 
     uint8_t *const ring = sh.ring[warp][0];
     const uint32_t ring_at = smem_u32(ring);
@@ -375,27 +248,7 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const Ro
     const int own = p.seq_status ? (int)blockIdx.x * kRW + warp : p.B;
 #pragma unroll 1
     for (int sb = own; sb < p.B; sb += (int)gridDim.x * kRW) {
-        const int L = p.prefix_lens[sb], first = p.row_starts[sb], end = p.row_starts[sb + 1];
-        const RowsSeq s = rows_seq(p.rows, L, first, end);
-        bool bad = !lengths_ok(Shape{1, p.rows.window, p.rows.num_rows, p.rows.S_max}, L, first, end);
-        if (s.n > 0) {
-            const int lo = p.rows.window > 0 ? max(0, L - p.rows.window + 1) : 0;
-            const int32_t *trow = p.block_table + (size_t)sb * p.max_pages;
-#pragma unroll 1
-            for (int j = lo / p.page_size + lane; j <= (L + s.n - 1) / p.page_size; j += 32) {
-                const int pg = trow[j];
-                if (pg < 0 || pg >= p.num_pages) bad = true;
-            }
-            if (p.parents) {
-                bad = bad || s.n > kTreeNodes;
-#pragma unroll 1
-                for (int i = lane; i < min(s.n, kTreeNodes); i += 32) {
-                    const int par = p.parents[first + i];
-                    if (i == 0 ? par != -1 : par < 0 || par >= i) bad = true;
-                }
-            }
-        }
-        bad = __any_sync(0xffffffffu, bad);
+        const bool bad = bad_sequence(p, sb, lane);
         if (lane == 0) p.seq_status[sb] = bad ? SV_ERR_BAD_INPUT : SV_OK;
     }
 
@@ -734,7 +587,10 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const Ro
     if (tid == 0) {
         if (sh.lost) give_up(p.call, p.seq_status, p.B);
         // the next call's, whose grid may be another
-        for (int c = blockIdx.x; c < kRowsMaxGrid; c += gridDim.x) p.counters[rows_counter(call + 1, c)] = 0;
+        for (int c = blockIdx.x; c < kRowsMaxGrid; c += gridDim.x) {
+            p.counters[rows_counter(call + 1, c)] = 0;
+            p.counters[rows_counter(call + 1, c) + 1] = 0;
+        }
     }
     if (lane == 0 && own < p.B && gave_up(p.call))
         for (int sb = own; sb < p.B; sb += (int)gridDim.x * kRW) p.seq_status[sb] = SV_ERR_TIMEOUT;
@@ -752,11 +608,11 @@ Form form() {
     return Form{reinterpret_cast<const void *>(&quant_rows_kernel<D, NT>), 8 * NT, (int)sizeof(RowsShared<D, NT>), kCtasAnSm<NT>};
 }
 
-constexpr int kForms = 4;
+constexpr int kForms = 2;
 // By columns, the fewest first.
 const Form &form_at(int D, int i) {
-    static const Form f128[kForms] = {form<128, 1>(), form<128, 2>(), form<128, 3>(), form<128, 5>()};
-    static const Form f64[kForms] = {form<64, 1>(), form<64, 2>(), form<64, 4>(), form<64, 8>()};
+    static const Form f128[kForms] = {form<128, 1>(), form<128, 2>()};
+    static const Form f64[kForms] = {form<64, 1>(), form<64, 2>()};
     return D == 128 ? f128[i] : f64[i];
 }
 
@@ -796,20 +652,24 @@ int rows_form(const ChunkArgs &a) {
     return i;
 }
 
-sv_status launch_rows(const ChunkArgs &a, const QuantParams &c, int form, int *counters, cudaStream_t st) {
+RowsParams rows_params(const ChunkArgs &a, const QuantParams &c, int cols) {
+    RowsParams p{};
+    static_cast<QuantParams &>(p) = c;
+    p.q = static_cast<const uint16_t *>(a.q);
+    p.q_stride = a.q_stride;
+    p.parts = (p.G + cols - 1) / cols;
+    p.Gs = (p.G + p.parts - 1) / p.parts;
+    p.groups = p.Hkv * p.parts;
+    p.rows = RowsShape{cols / p.Gs, c.shape.window, c.shape.num_rows, c.shape.S_max};
+    if (a.parents && p.rows.tok > kTreeNodes) p.rows.tok = kTreeNodes;
+    return p;
+}
+
+sv_status launch_rows(const ChunkArgs &a, const QuantParams &c, int form, cudaStream_t st) {
     const Form &f = form_at(a.D, form);
     const int grid = form_grid(a.D, form);
     if (grid <= 0 || grid > kRowsMaxGrid) return SV_ERR_CUDA;
-    RowsParams p{};
-    static_cast<QuantParams &>(p) = c;
-    p.counters = counters;
-    p.q = static_cast<const uint16_t *>(a.q);
-    p.q_stride = a.q_stride;
-    p.parts = (p.G + f.cols - 1) / f.cols;
-    p.Gs = (p.G + p.parts - 1) / p.parts;
-    p.groups = p.Hkv * p.parts;
-    p.rows = RowsShape{f.cols / p.Gs, c.shape.window, c.shape.num_rows, c.shape.S_max};
-    if (a.parents && p.rows.tok > kTreeNodes) p.rows.tok = kTreeNodes;
+    RowsParams p = rows_params(a, c, f.cols);
     void *args[] = {&p};
     return launch_pdl(f.fn, dim3((unsigned)grid), dim3(kRT), (size_t)f.smem, st, args) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }

@@ -10,7 +10,10 @@ namespace chunk {
 
 constexpr int kRowsCols = 64;      // columns (rows times heads) of an item at most
 constexpr int kRowsMaxGrid = 512;  // CTAs of a call at most: the workspace's shares and counters
-constexpr int kRowsMost = 64;      // columns of a mean sequence up to which a call takes this form
+constexpr int kRowsMost = 16;      // columns of a mean sequence up to which a call takes this form
+constexpr float kUnset = -1e38f;   // u of a column that has seen no slot
+constexpr float kRoom = 12.f;      // log2 of the largest P
+constexpr float kLeast = -60.f;    // log2 of a step below which it counts as this much for u
 
 struct RowsParams : QuantParams {
     const uint16_t *q;
@@ -20,12 +23,14 @@ struct RowsParams : QuantParams {
     int groups;          // Hkv * parts
 };
 
-// The counter of an item shared from CTA `cta` on, in the set of the given call.
-SV_CALL_HD int rows_counter(unsigned long long call, int cta) { return (int)(call & 1) * kRowsMaxGrid + cta; }
+// The counters (two) of an item shared from CTA `cta` on, in the set of the given call.
+SV_CALL_HD int rows_counter(unsigned long long call, int cta) { return ((int)(call & 1) * kRowsMaxGrid + cta) * 2; }
 
 // The form for the call's rows; -1 where it has too many.
 int rows_form(const ChunkArgs &args);
-sv_status launch_rows(const ChunkArgs &args, const QuantParams &params, int form, int *counters, cudaStream_t stream);
+sv_status launch_rows(const ChunkArgs &args, const QuantParams &params, int form, cudaStream_t stream);
+// What a form of `cols` columns an item takes.
+RowsParams rows_params(const ChunkArgs &args, const QuantParams &params, int cols);
 
 }  // namespace chunk
 }  // namespace sv

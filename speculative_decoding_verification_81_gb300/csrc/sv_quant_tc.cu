@@ -1,30 +1,820 @@
-// sv_quant_tc.cu -- the chunk attention over pages held in 4 bits: the kernel of
-// sv_chunk_tc.cuh with sixteen warps.
+// sv_quant_tc.cu -- attention over pages held in 4 bits on the 5th-generation
+// tensor cores: chains, draft trees and parts of prompts.
 //
-// Source: as sv_chunk_tc.cu, which says how the steps, items and warps go
-// together.  What differs: warps 8 and 11 copy the codes and parameters of K and
-// V tiles to a ring of their own (8.5 KB a tile at D = 128 for 32), and warps
-// 12-15, a thread a slot, turn each into bf16 values in the swizzled tiles that
-// the products read.  A value is minimum + step * code rounded once to bf16, what
-// a cache in bf16 would hold of it; a slot that no row of the item sees is zeros.
-// A row may be a node of a draft tree: it then sees the slots before its sequence's
-// rows and its own path's, a 64-bit set that each softmax thread makes of the
-// parents.
-#include "sv_chunk_tc.cuh"
+// An item is the rows of some tokens of one sequence and the heads of them that
+// share K/V, N <= 64 columns (a multiple of 16); for each 128-slot tile of K/V
+//     S = codes_k Q^T           (128 slots x N, f32 in tensor memory; codes less 8, exact in bf16)
+//     s = step_k S + middle_k sum(q) - u, in log2 units
+//     P = 2^s step_v, rounded to f16; l += 2^s; z += 2^s middle_v
+//     O^T += codes_v^T P        (D dims x N, f32 in tensor memory; codes less 8, exact in f16)
+// and out = (O + z) / l.  A column's u moves only when some P would pass 2^12, so
+// that f16 holds P to 2^-12 of itself, or of 2^-14 of the largest where it is
+// smaller; nothing of the cache is rounded.
+//
+// Why slots are the rows of S: a slot's steps and middles are then numbers of the
+// thread that has the slot.  With queries as rows every thread would need all of a
+// tile's, four floats a score from shared memory, which set the pace (a chunk of 2048
+// rows after 14336 slots 640 us).  What a column needs, its u and the sum of its q,
+// is two floats, for few columns.
+//
+// Warps: 0-3 and 4-7 softmax, half of the columns each, a thread a slot; at an
+// item's end a thread a dim.  8-11 turn a tile's codes into operands, a thread a
+// slot: K's to tensor memory, V's to shared memory.  12 loads codes, parameters and
+// queries, 13 issues the products, 14 walks the work list (sv_quant_list.h).
+// An item cut by a CTA's range leaves its share in the workspace; the softmax
+// group that arrives last adds the shares of its columns in their order.  Every wait
+// is bounded; the warps of a softmax group agree on a wait that gave up before any
+// of them leaves the group's barriers.
+#include "sv_attn_common.cuh"
+#include "sv_chunk.cuh"
+#include "sv_quant.cuh"
+#include "sv_quant_walk.cuh"
 
 namespace sv {
 namespace chunk {
 
-const void *quant_kernel_fn(int D) {
-    return D == 128 ? reinterpret_cast<const void *>(&chunk_attention_kernel<128, true>)
-                    : reinterpret_cast<const void *>(&chunk_attention_kernel<64, true>);
-}
+namespace {
+
+constexpr int kTT = 512;                       // threads
+constexpr int kN = 64;                         // columns of an item at most
+constexpr uint32_t kTCols = 512, kTColS = 0, kTColO = 128, kTColK = 256;  // two of each, 64 columns apart
 
 template <int D>
-constexpr int kQuantSmem = (kStagesOf<D, true> + 2) * kTileBytes<D> + kRawBytes<D, true> + (int)sizeof(QuantShared);
-static_assert(kQuantSmem<128> <= 227 * 1024 && kQuantSmem<64> <= 227 * 1024, "shared memory");
+constexpr int kVTile = kBK * D * 2;            // V's operand
+constexpr int kPTile = kBK * kN * 2;
+constexpr int kQBox = kN * 128;                // 64 columns of 64 dims
+template <int D>
+constexpr int kQTile = kQBox * (D / 64);
+template <int D>
+constexpr int kTRaw = kBK * (D + 8);           // a tile's codes and parameters
+template <int D>
+constexpr int kTRawStages = D == 128 ? 5 : 8;
 
-int quant_smem_bytes(int D) { return D == 128 ? kQuantSmem<128> : kQuantSmem<64>; }
+struct TShared {
+    uint64_t raw_full[8], raw_empty[8];
+    uint64_t k_full[2], k_empty[2], v_full[2], pv_done[2];
+    uint64_t s_full[2], s_empty[2], p_full[2];
+    uint64_t q_full[2], q_empty[2], o_full[2], o_empty[2];
+    uint64_t item_full[kItems], item_empty[kItems];
+    uint64_t fin;
+    RowsItem items[kItems];
+    uint2 slots[4][kBK];               // a tile's slots: K's parameters, V's
+    float4 col[kN / 2];                // of two columns: the sums of q, the u negated
+    float most[2][4][32];
+    float2 sums[2][4][32];             // (l, z)
+    float2 f[2][16];                   // what a column's sums are to be multiplied by
+    unsigned long long above[2][kTreeNodes];
+    long long warp_units[kTT / 32];
+    long long before[kTT];
+    unsigned long long call;
+    uint8_t tok[kN];
+    uint32_t tmem;
+    int abort_flag, last[2];
+};
+
+template <int D>
+constexpr int kTSmem = 2 * (kVTile<D> + kPTile + kQTile<D>) + kTRawStages<D> * kTRaw<D> + (int)sizeof(TShared);
+static_assert(kTSmem<128> <= 227 * 1024 && kTSmem<64> <= 227 * 1024, "shared memory");
+
+__device__ __noinline__ bool twait_long(uint32_t bar, uint32_t parity) {
+    const long long t0 = clock64();
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (__all_sync(0xffffffffu, ok != 0)) return true;
+        if (__any_sync(0xffffffffu, clock64() - t0 > kWaitCycles)) return false;
+    }
+}
+// Wait for the phase of `bar` with the given parity, by a whole warp with one verdict.
+__device__ __forceinline__ bool twait(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || twait_long(smem_u32(bar), parity);
+}
+
+__device__ __forceinline__ uint32_t telect() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+
+// Barrier of a softmax group's 128 threads; whether any of them says so.
+__device__ __forceinline__ bool group_any(int group, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x), "r"(1 + group)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void group_sync(int group) { named_bar_sync(1 + group, 128); }
+
+__device__ __forceinline__ void tmem_ld8(uint32_t at, float2 (&x)[4]) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(at));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t at, const float2 (&x)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at),
+                 "r"(__float_as_uint(x[0].x)), "r"(__float_as_uint(x[0].y)), "r"(__float_as_uint(x[1].x)),
+                 "r"(__float_as_uint(x[1].y)), "r"(__float_as_uint(x[2].x)), "r"(__float_as_uint(x[2].y)),
+                 "r"(__float_as_uint(x[3].x)), "r"(__float_as_uint(x[3].y))
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t t_sw128(int row, int c) { return (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4)); }
+
+__device__ __forceinline__ uint32_t t_pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// The sums (or maxima) over the warp of 32 values a lane: lane c's is that of v[c].
+template <bool kMax>
+__device__ __forceinline__ float across(float (&v)[32], int lane) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const bool up = lane & off;
+#pragma unroll
+        for (int i = 0; i < off; ++i) {
+            const float keep = up ? v[i + off] : v[i], send = up ? v[i] : v[i + off];
+            const float got = __shfl_xor_sync(0xffffffffu, send, off);
+            v[i] = kMax ? fmaxf(keep, got) : keep + got;
+        }
+    }
+    return v[0];
+}
+
+}  // namespace
+
+template <int D>
+__global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant__ CUtensorMap tmq, const RowsParams p) {
+    constexpr int kRow = D / 2, kRaw = kTRawStages<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];  // (the swizzle's atoms are 1024 bytes)
+    uint8_t *const vbuf = smem, *const pbuf = vbuf + 2 * kVTile<D>, *const qbuf = pbuf + 2 * kPTile;
+    uint8_t *const raw = qbuf + 2 * kQTile<D>;
+    TShared *sh = reinterpret_cast<TShared *>(raw + kRaw * kTRaw<D>);
+    const uint32_t base_u32 = smem_u32(smem);
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    if (tid == 0) {
+#pragma unroll 1
+        for (int i = 0; i < kRaw; ++i) {
+            mbar_init(&sh->raw_full[i], 1);
+            mbar_init(&sh->raw_empty[i], 4);
+        }
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh->k_full[i], 4);
+            mbar_init(&sh->k_empty[i], 1);
+            mbar_init(&sh->v_full[i], 4);
+            mbar_init(&sh->pv_done[i], 1);
+            mbar_init(&sh->s_full[i], 1);
+            mbar_init(&sh->s_empty[i], 8);
+            mbar_init(&sh->p_full[i], 8);
+            mbar_init(&sh->q_full[i], 1);
+            mbar_init(&sh->q_empty[i], 1 + 2);  // the products, the softmax groups
+            mbar_init(&sh->o_full[i], 1);
+            mbar_init(&sh->o_empty[i], 8);
+        }
+#pragma unroll 1
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&sh->item_full[i], 1);
+            mbar_init(&sh->item_empty[i], 8 + 4 + 2);
+        }
+        mbar_init(&sh->fin, 1);
+        sh->abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (tid < kN) sh->tok[tid] = (uint8_t)(tid / p.Gs);
+    if (tid == 32 * 12) prefetch_tensormap(&tmq);
+    if (warp == 13) tc::tmem_alloc(&sh->tmem, kTCols);
+    griddep_wait();
+    griddep_launch_dependents();
+    if (tid == 0) sh->call = begin_call(p.call);
+    RowsWalk walk;
+    tc::fence_before();
+    plan_walk<kTT>(p, sh->warp_units, sh->before, tid, walk);  // (two barriers of the CTA)
+    tc::fence_after();
+    const uint32_t tbase = sh->tmem;
+    volatile int *abort_flag = &sh->abort_flag;
+    auto fail = [&] { *abort_flag = 1; };
+    const bool aligned = (base_u32 & 1023u) == 0;  // (always: nothing else takes shared memory here)
+
+    if (warp < 8) {
+        // ===================== softmax: a thread a slot, the columns of its group
+        const int group = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+        const uint32_t tl = tbase + ((uint32_t)(quarter * 32) << 16);
+        uint32_t tile = 0;  // tiles of the CTA before this item
+        bool bad = !aligned;
+#pragma unroll 1
+        for (uint32_t k = 0;; ++k) {
+            const int slot_i = k % kItems;
+            bad = bad || !warp_wait_bounded(&sh->item_full[slot_i], (k / kItems) & 1);
+            if (group_any(group, bad)) {
+                bad = true;
+                break;
+            }
+            const RowsItem it = sh->items[slot_i];
+            if (it.b < 0) break;
+            const int cols = it.ntok * p.Gs, N = (cols + 15) & ~15, nch = N / 16;  // chunks of 8 columns a group
+            const int c0 = group * (N / 2);                                        // the group's first column
+            const int own0 = it.pos0 - (it.row0 - it.seq_row0);                    // slot of the sequence's first new row
+            const int all_hi = p.parents ? own0 : it.pos0 + 1;                     // below, and from all_lo on, every row sees a slot
+            const int all_lo = p.rows.window > 0 ? it.pos0 + it.ntok - p.rows.window : 0;
+            bad = !warp_wait_bounded(&sh->q_full[k & 1], (k >> 1) & 1);
+            if (!bad && r < N / 2) {  // the sums of this group's columns of Q
+                const uint8_t *q = qbuf + (k & 1) * kQTile<D>;
+                float2 s = make_float2(0.f, 0.f);
+#pragma unroll 4
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(q + (c >> 3) * kQBox + t_sw128(c0 + r, c & 7));
+                    s = __fadd2_rn(s, __fadd2_rn(__fadd2_rn(make_float2(bf16_lo(x.x), bf16_hi(x.x)), make_float2(bf16_lo(x.y), bf16_hi(x.y))),
+                                                 __fadd2_rn(make_float2(bf16_lo(x.z), bf16_hi(x.z)), make_float2(bf16_lo(x.w), bf16_hi(x.w)))));
+                }
+                float *to = reinterpret_cast<float *>(&sh->col[(c0 + r) >> 1]) + (r & 1);
+                to[0] = s.x + s.y;
+                to[2] = -kUnset;
+            }
+            if (p.parents && quarter < 2) {  // a token's set of nodes above it, of those up to the item's last
+                const int node0 = it.row0 - it.seq_row0, nodes = min(node0 + it.ntok, kTreeNodes);
+                const int32_t *par = p.parents + it.seq_row0;
+                const int a = lane < nodes ? par[lane] : -1, b = lane + 32 < nodes ? par[lane + 32] : -1;
+                sh->above[group][r] = ancestors_warp(false, a, b, node0 + r, r < it.ntok && node0 + r < nodes);
+            }
+            if (group_any(group, bad)) {
+                bad = true;
+                break;
+            }
+            if (r == 0) mbar_arrive(&sh->q_empty[k & 1]);
+            float2 l[16], z[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) l[i] = z[i] = make_float2(0.f, 0.f);
+            const uint32_t o_at = tl + kTColO + (k & 1) * kN + c0;
+#pragma unroll 1
+            for (int j = 0; j < it.n; ++j) {
+                const uint32_t g = tile + j, buf = g & 1, ph = (g >> 1) & 1;
+                const int slot0 = (it.kt0 + j) * kBK, slot = slot0 + r;
+                bad = !warp_wait_bounded(&sh->s_full[buf], ph) || !warp_wait_bounded(&sh->pv_done[buf], ph ^ 1);
+                tc::fence_after();
+                const uint2 par = sh->slots[g & 3][r];
+                const float ks = bf16_lo(par.x) * p.scale_log2;
+                const float km = __fmaf_rn(8.f, bf16_lo(par.x), bf16_hi(par.x)) * p.scale_log2;
+                const float vs = bf16_lo(par.y), vm = __fmaf_rn(8.f, vs, bf16_hi(par.y));
+                const float lv = fmaxf(lg2_approx(fabsf(vs)), kLeast);  // log2 of what P gets from the step
+                const float2 ks2 = make_float2(ks, ks), km2 = make_float2(km, km);
+                uint32_t sees = ~0u;  // a bit a column of the group
+                if (slot0 + kBK > all_hi || slot0 < all_lo) {
+                    if (p.parents) {
+                        const int node = slot - own0;
+                        if (node >= 0) {
+                            sees = 0;
+#pragma unroll 1
+                            for (int c = 0; c < N / 2; ++c) {
+                                const int tk = min((int)sh->tok[c0 + c], it.ntok - 1);
+                                if (node < kTreeNodes && (sh->above[group][tk] >> node & 1)) sees |= 1u << c;
+                            }
+                        }
+                    } else {  // tokens slot - pos0 .. slot - pos0 + window - 1
+                        const long long from = (long long)(slot - it.pos0) * p.Gs - c0;
+                        const long long to = p.rows.window > 0 ? from + (long long)p.rows.window * p.Gs : 32;
+                        const uint32_t under = from >= 32 ? ~0u : from <= 0 ? 0u : (1u << from) - 1u;
+                        const uint32_t below = to >= 32 ? ~0u : to <= 0 ? 0u : (1u << to) - 1u;
+                        sees = below & ~under;
+                    }
+                }
+                float2 x[16];
+                const uint32_t s_at = tl + kTColS + buf * kN + c0;
+                auto scores = [&](bool less) __attribute__((always_inline)) {  // less: less u
+#pragma unroll
+                    for (int ch = 0; ch < 4; ++ch) {
+                        float2(&y)[4] = *reinterpret_cast<float2(*)[4]>(&x[4 * ch]);
+                        if (ch < nch) tmem_ld8(s_at + 8 * ch, y);
+                    }
+                    tc::wait_ld();
+#pragma unroll
+                    for (int ch = 0; ch < 4; ++ch) {
+                        if (ch >= nch) break;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 c4 = sh->col[(c0 >> 1) + 4 * ch + i];
+                            float2 t = less ? make_float2(c4.z, c4.w) : make_float2(0.f, 0.f);
+                            t = __ffma2_rn(km2, make_float2(c4.x, c4.y), t);
+                            x[4 * ch + i] = __ffma2_rn(x[4 * ch + i], ks2, t);
+                        }
+                    }
+                    if (sees != ~0u) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            if (!(sees >> (2 * i) & 1)) x[i].x = kNegInf;
+                            if (!(sees >> (2 * i + 1) & 1)) x[i].y = kNegInf;
+                        }
+                    }
+                };
+                scores(true);
+                float top = kNegInf;
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) {
+                    if (ch >= nch) break;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top = fmaxf(fmaxf(top, x[4 * ch + i].x), x[4 * ch + i].y);
+                }
+                if (group_any(group, bad || top + lv > kRoom)) {
+                    if (group_any(group, bad)) {
+                        bad = true;
+                        break;
+                    }
+                    // some column's u moves up to its largest P (the first tile's do)
+                    scores(false);
+                    {
+                        float v[32];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const bool on = i < 4 * nch;
+                            v[2 * i] = on ? x[i].x + lv : kNegInf;
+                            v[2 * i + 1] = on ? x[i].y + lv : kNegInf;
+                        }
+                        sh->most[group][quarter][lane] = across<true>(v, lane);
+                    }
+                    group_sync(group);
+                    if (quarter == 0 && lane < N / 2) {
+                        const float a = fmaxf(fmaxf(sh->most[group][0][lane], sh->most[group][1][lane]),
+                                              fmaxf(sh->most[group][2][lane], sh->most[group][3][lane]));
+                        float *nu = reinterpret_cast<float *>(&sh->col[(c0 + lane) >> 1]) + 2 + (lane & 1);
+                        const float u = -*nu;
+                        const bool up = a > u + kRoom;
+                        reinterpret_cast<float *>(sh->f[group])[lane] = up ? ex2_approx(u - a) : 1.f;
+                        if (up) *nu = -a;
+                    }
+                    const uint32_t before = g - 1;  // the products that added to O last
+                    if (j > 0) bad = !warp_wait_bounded(&sh->pv_done[before & 1], (before >> 1) & 1);
+                    if (group_any(group, bad)) {
+                        bad = true;
+                        break;
+                    }
+                    tc::fence_after();
+#pragma unroll
+                    for (int ch = 0; ch < 4; ++ch) {
+                        if (ch >= nch) break;
+                        float2 f[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            f[i] = sh->f[group][4 * ch + i];
+                            l[4 * ch + i] = __fmul2_rn(l[4 * ch + i], f[i]);
+                            z[4 * ch + i] = __fmul2_rn(z[4 * ch + i], f[i]);
+                        }
+                        if (j > 0) {
+                            float2 o[4];
+                            tmem_ld8(o_at + 8 * ch, o);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) o[i] = __fmul2_rn(o[i], f[i]);
+                            tmem_st8(o_at + 8 * ch, o);
+                        }
+                    }
+                    tc::wait_st();
+                    scores(true);
+                }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->s_empty[buf]);
+                const float2 vs2 = make_float2(vs, vs), vm2 = make_float2(vm, vm);
+                uint8_t *const to = pbuf + buf * kPTile + r * 128;
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) {
+                    if (ch >= nch) break;
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int n = 4 * ch + i;
+                        const float2 e = make_float2(ex2_approx(x[n].x), ex2_approx(x[n].y));
+                        l[n] = __fadd2_rn(l[n], e);
+                        z[n] = __ffma2_rn(e, vm2, z[n]);
+                        const float2 y = __fmul2_rn(e, vs2);
+                        w[i] = t_pack_f16x2(y.x, y.y);
+                    }
+                    *reinterpret_cast<uint4 *>(to + ((((c0 >> 3) + ch) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->p_full[buf]);
+            }
+            if (bad) break;
+            tile += it.n;
+            // ---- the columns' sums over the slots, then a thread a dim
+            bad = !warp_wait_bounded(&sh->o_full[k & 1], (k >> 1) & 1);
+            {
+                float v[32];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[2 * i] = l[i].x, v[2 * i + 1] = l[i].y;
+                const float ls = across<false>(v, lane);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[2 * i] = z[i].x, v[2 * i + 1] = z[i].y;
+                sh->sums[group][quarter][lane] = make_float2(ls, across<false>(v, lane));
+            }
+            if (group_any(group, bad)) {
+                bad = true;
+                break;
+            }
+            tc::fence_after();
+            const bool whole = it.nc == 1;
+            const int part = (int)blockIdx.x * 2 + (it.ci == 0 ? 1 : 0);
+            const int hpart = it.h % p.parts * p.Gs, heads = min(p.Gs, p.G - hpart);
+            const int head0 = it.h / p.parts * p.G + hpart;
+            // where a column's row goes; -1: it is padding
+            auto out_row = [&](int c) -> long long {
+                const int tk = sh->tok[c], hd = c - tk * p.Gs;
+                return c < cols && hd < heads ? (long long)(it.row0 + tk) * p.Hq + head0 + hd : -1;
+            };
+            float lsum = 0.f, zsum = 0.f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                lsum += sh->sums[group][w][lane].x;
+                zsum += sh->sums[group][w][lane].y;
+            }
+            const float inv = whole ? 1.f / lsum : 1.f;
+            if (quarter == 0 && lane < N / 2) {
+                const float u = -(reinterpret_cast<const float *>(&sh->col[(c0 + lane) >> 1])[2 + (lane & 1)]);
+                const long long row = out_row(c0 + lane);
+                if (whole) {
+                    if (p.lse && row >= 0) p.lse[row] = u * kLn2 + logf(lsum);
+                } else {
+                    __stcg(reinterpret_cast<float2 *>(p.part_ml) + (size_t)part * kRowsCols + c0 + lane, make_float2(u, lsum));
+                }
+            }
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) {
+                if (ch >= nch) break;
+                float2 o[4];
+                __syncwarp();
+                tmem_ld8(o_at + 8 * ch, o);
+                tc::wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int c = 8 * ch + i;
+                    const float a = i & 1 ? o[i >> 1].y : o[i >> 1].x;
+                    const float y = (a + __shfl_sync(0xffffffffu, zsum, c)) * __shfl_sync(0xffffffffu, inv, c);
+                    const long long row = out_row(c0 + c);
+                    if (row < 0 || r >= D) continue;
+                    if (whole) p.out[row * D + r] = (uint16_t)pack_bf16x2(y, 0.f);
+                    else __stcg(p.part_o + ((size_t)part * kRowsCols + c0 + c) * D + r, y);
+                }
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sh->o_empty[k & 1]);
+                mbar_arrive(&sh->item_empty[slot_i]);
+            }
+            if (whole) {
+                group_sync(group);  // (the columns' numbers are read until here)
+                continue;
+            }
+            // ---- an item shared by CTAs: the group that arrives last adds the shares of its columns up, in their order
+            __threadfence();
+            group_sync(group);
+            if (r == 0) {
+                int *ctr = p.counters + rows_counter(sh->call, it.c_first) + group;
+                int before_me;
+                asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before_me) : "l"(ctr) : "memory");
+                sh->last[group] = before_me == it.nc - 1;
+            }
+            group_sync(group);
+            if (!sh->last[group]) continue;
+            __threadfence();
+#pragma unroll 1
+            for (int i = r; i < N / 2 * (D / 4); i += 128) {
+                const int c = c0 + i / (D / 4), dim = i % (D / 4) * 4;
+                const long long row = out_row(c);
+                if (row < 0) continue;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                float M = kUnset, sum = 0.f;
+                constexpr int kAhead = 4;
+#pragma unroll 1
+                for (int k0 = 0; k0 < it.nc; k0 += kAhead) {
+                    float2 ml[kAhead];
+                    float4 a[kAhead];
+#pragma unroll
+                    for (int q = 0; q < kAhead; ++q) {
+                        const int m = min(k0 + q, it.nc - 1);
+                        const size_t from = (size_t)(2 * (it.c_first + m) + (m == 0 ? 1 : 0)) * kRowsCols + c;
+                        ml[q] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml) + from);
+                        a[q] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + from * D + dim));
+                    }
+#pragma unroll
+                    for (int q = 0; q < kAhead; ++q) {
+                        if (k0 + q >= it.nc) continue;
+                        const float Mn = fmaxf(M, ml[q].x), f = ex2_approx(M - Mn), w = ex2_approx(ml[q].x - Mn);
+                        M = Mn;
+                        sum = sum * f + ml[q].y * w;
+                        acc.x = __fmaf_rn(a[q].x, w, acc.x * f);
+                        acc.y = __fmaf_rn(a[q].y, w, acc.y * f);
+                        acc.z = __fmaf_rn(a[q].z, w, acc.z * f);
+                        acc.w = __fmaf_rn(a[q].w, w, acc.w * f);
+                    }
+                }
+                const float in = 1.f / sum;
+                *reinterpret_cast<uint2 *>(p.out + row * D + dim) = make_uint2(pack_bf16x2(acc.x * in, acc.y * in), pack_bf16x2(acc.z * in, acc.w * in));
+                if (p.lse && dim == 0) p.lse[row] = M * kLn2 + logf(sum);
+            }
+        }
+        if (bad) fail();
+    } else {
+        if (warp < 12) {
+            // ===================== codes to operands: a thread a slot
+            const int quarter = warp & 3, r = quarter * 32 + lane;
+            const uint32_t k_at = tbase + ((uint32_t)(quarter * 32) << 16) + kTColK;
+            uint32_t g = 0;
+            bool ok = aligned;
+#pragma unroll 1
+            for (uint32_t k = 0; ok; ++k) {
+                const int slot_i = k % kItems;
+                if (!(ok = twait(&sh->item_full[slot_i], (k / kItems) & 1))) break;
+                const int b = sh->items[slot_i].b, n = sh->items[slot_i].n, pos0 = sh->items[slot_i].pos0;
+                const int ntok = sh->items[slot_i].ntok, kt0 = sh->items[slot_i].kt0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->item_empty[slot_i]);
+                if (b < 0) break;
+                const int lo = p.rows.window > 0 ? max(0, pos0 - p.rows.window + 1) : 0, hi = pos0 + ntok;
+#pragma unroll 1
+                for (int j = 0; j < n; ++j, ++g) {
+                    const uint32_t rs = g % kRaw, buf = g & 1, ph = (g >> 1) & 1;
+                    if (!(ok = twait(&sh->raw_full[rs], (g / kRaw) & 1))) break;
+                    const uint8_t *from = raw + rs * kTRaw<D>;
+                    const int at = (kt0 + j) * kBK + r;
+                    const bool seen = at >= lo && at < hi;  // (another slot may hold anything)
+                    const uint32_t *par = reinterpret_cast<const uint32_t *>(from + 2 * kBK * kRow);
+                    // pieces of 32 dims, in turn from another one on for rows two and two (four and four), so
+                    // that eight lanes of an access meet eight bank groups
+                    constexpr int kPieces = D / 32;
+                    const int turn = r >> (D == 128 ? 1 : 2);
+                    uint4 c[kPieces];
+#pragma unroll
+                    for (int i = 0; i < kPieces; ++i)
+                        c[i] = *reinterpret_cast<const uint4 *>(from + r * kRow + ((i + turn) & (kPieces - 1)) * 16);
+                    if (!(ok = twait(&sh->k_empty[buf], ph ^ 1))) break;
+                    tc::fence_after();
+                    sh->slots[g & 3][r] = make_uint2(seen ? par[r] : 0u, seen ? par[kBK + r] : 0u);
+                    // (a thread's row in order: the pieces put back by selects, a bit of the turn at a time)
+                    if constexpr (kPieces == 4) {
+                        const bool one = turn & 1, two = turn & 2;
+                        uint4 y[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) y[i] = one ? c[(i + 3) & 3] : c[i];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) c[i] = two ? y[(i + 2) & 3] : y[i];
+                    } else {
+                        const uint4 y = c[0];
+                        c[0] = turn & 1 ? c[1] : y;
+                        c[1] = turn & 1 ? y : c[1];
+                    }
+#pragma unroll
+                    for (int i = 0; i < kPieces; i += 2) {  // 64 dims, 32 columns of tensor memory at a time
+                        uint32_t v[32];
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const uint4 &y = c[i + (q >> 2)];
+                            const uint32_t w = (q & 3) == 0 ? y.x : (q & 3) == 1 ? y.y : (q & 3) == 2 ? y.z : y.w;
+                            const uint4 e = quant::expand(w);
+                            v[4 * q] = e.x, v[4 * q + 1] = e.y, v[4 * q + 2] = e.z, v[4 * q + 3] = e.w;
+                        }
+                        tc::tmem_st32(k_at + buf * kN + i * 16, v);
+                    }
+                    // V's codes, on their way while K's are written
+#pragma unroll
+                    for (int i = 0; i < kPieces; ++i)
+                        c[i] = *reinterpret_cast<const uint4 *>(from + kBK * kRow + r * kRow + ((i + turn) & (kPieces - 1)) * 16);
+                    tc::wait_st();
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&sh->k_full[buf]);
+                        mbar_arrive(&sh->raw_empty[rs]);
+                    }
+                    if (!(ok = twait(&sh->pv_done[buf], ph ^ 1))) break;
+                    if (__shfl_sync(0xffffffffu, *abort_flag, 0)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *const to = vbuf + buf * kVTile<D> + r * 128;
+#pragma unroll
+                    for (int i = 0; i < kPieces; ++i) {
+                        const int piece = (i + turn) & (kPieces - 1);
+                        const uint32_t words[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            *reinterpret_cast<uint4 *>(to + (piece >> 1) * kBox + ((((piece & 1) * 4 + q) ^ (r & 7)) << 4)) =
+                                quant::expand_f16(words[q]);
+                    }
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh->v_full[buf]);
+                }
+            }
+            if (!ok) fail();
+        } else if (warp == 12) {
+            // ===================== codes and parameters of the tiles, a lane a page; the queries
+            const int ps = p.page_size;
+            const int sub = ps < kBK ? ps : kBK;      // slots of a copy
+            const int npg = kBK / sub;                // copies a tile
+            const int tpp = ps < kBK ? 1 : ps / kBK;  // tiles a page (of 128 slots or more)
+            uint32_t g = 0, nq = 0;
+            bool ok = aligned;
+#pragma unroll 1
+            for (uint32_t k = 0; ok; ++k) {
+                const int slot_i = k % kItems;
+                if (!(ok = twait(&sh->item_full[slot_i], (k / kItems) & 1))) break;
+                const RowsItem it = sh->items[slot_i];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->item_empty[slot_i]);
+                if (it.b < 0) break;
+                const int lo = p.rows.window > 0 ? max(0, it.pos0 - p.rows.window + 1) : 0, hi = it.pos0 + it.ntok;
+                const int32_t *trow = p.block_table + (size_t)it.b * p.max_pages;
+                // cache row of the first slot of this lane's copy of tile j; -1: no slot of it is seen.  In the place
+                // of a page id out of range (reported by the check, its rows unspecified) page 0 is read.
+                auto first_row = [&](int j) -> int {
+                    const int t = it.kt0 + j, s0 = t * kBK + lane * sub;
+                    if (lane >= npg || s0 >= hi || s0 + sub <= lo) return -1;
+                    const int page = tpp == 1 ? t * npg + lane : t / tpp;
+                    int pg = trow[page];
+                    if (pg < 0 || pg >= p.num_pages) pg = 0;
+                    return (pg * p.Hkv + it.h / p.parts) * ps + (tpp == 1 ? 0 : (t - page * tpp) * kBK);
+                };
+                int y = first_row(0);
+                if (!(ok = twait(&sh->q_empty[k & 1], ((k >> 1) & 1) ^ 1))) break;
+                if (lane == 0) {
+                    uint8_t *qd = qbuf + (k & 1) * kQTile<D>;
+                    mbar_arrive_expect_tx(&sh->q_full[k & 1], (uint32_t)(D * 2 * p.Gs * p.rows.tok));
+#pragma unroll 1
+                    for (int hf = 0; hf < D / 64; ++hf)
+                        tma_load_3d(qd + hf * kQBox, &tmq, hf * 64, it.h / p.parts * p.G + it.h % p.parts * p.Gs, it.row0, &sh->q_full[k & 1]);
+                }
+                __syncwarp();
+                ++nq;
+#pragma unroll 1
+                for (int j = 0; j < it.n; ++j, ++g) {
+                    const int y_next = j + 1 < it.n ? first_row(j + 1) : -1;
+                    const int copies = __popc(__ballot_sync(0xffffffffu, y >= 0));
+                    const uint32_t rs = g % kRaw;
+                    if (!(ok = twait(&sh->raw_empty[rs], ((g / kRaw) & 1) ^ 1))) break;
+                    if (__shfl_sync(0xffffffffu, *abort_flag, 0)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(&sh->raw_full[rs], (uint32_t)(copies * sub * (D + 8)));
+                    __syncwarp();  // the expected bytes are set before any copy lands
+                    if (y >= 0) {
+                        uint8_t *to = raw + rs * kTRaw<D>;
+                        uint64_t *bar = &sh->raw_full[rs];
+                        bulk_load(to + lane * sub * kRow, p.k_codes + (size_t)y * kRow, (uint32_t)(sub * kRow), bar);
+                        bulk_load(to + kBK * kRow + lane * sub * kRow, p.v_codes + (size_t)y * kRow, (uint32_t)(sub * kRow), bar);
+                        bulk_load(to + 2 * kBK * kRow + lane * sub * 4, p.k_params + y, (uint32_t)(sub * 4), bar);
+                        bulk_load(to + 2 * kBK * kRow + kBK * 4 + lane * sub * 4, p.v_params + y, (uint32_t)(sub * 4), bar);
+                    }
+                    y = y_next;
+                }
+            }
+            if (!ok) fail();
+            // every copy issued must land before the CTA may exit
+#pragma unroll 1
+            for (uint32_t q = nq > 2 ? nq - 2 : 0; q < nq; ++q) twait(&sh->q_full[q & 1], (q >> 1) & 1);
+            if (__shfl_sync(0xffffffffu, *abort_flag, 0))
+#pragma unroll 1
+                for (uint32_t q = g > kRaw ? g - kRaw : 0; q < g; ++q) twait(&sh->raw_full[q % kRaw], (q / kRaw) & 1);
+        } else if (warp == 13) {
+            // ===================== the products: S of a tile, then O of the tile before
+            const uint32_t leader = telect();
+            const uint64_t desc_v = tc::smem_desc(base_u32, kBox, 1024);
+            const uint64_t desc_p = tc::smem_desc(base_u32 + 2 * kVTile<D>, kPTile, 1024);
+            const uint64_t desc_q = tc::smem_desc(base_u32 + 2 * (kVTile<D> + kPTile), 16, 1024);
+            uint32_t g = 0;
+            bool ok = aligned;
+            // the tile whose O is still to be added to: flags, columns, item
+            bool live = false, first = false, end = false;
+            uint32_t ln = 0, lk = 0;
+            auto add_o = [&]() -> bool {
+                const uint32_t t = g - 1, buf = t & 1, ph = (t >> 1) & 1;
+                if (!twait(&sh->v_full[buf], ph) || !twait(&sh->p_full[buf], ph)) return false;
+                if (first && !twait(&sh->o_empty[lk & 1], ((lk >> 1) & 1) ^ 1)) return false;
+                tc::fence_after();
+                // f16 both, V's dims and P's columns contiguous
+                const uint32_t idesc = (1u << 4) | (1u << 15) | (1u << 16) | ((ln >> 3) << 17) | (8u << 24);
+                if (leader) {
+#pragma unroll
+                    for (int kk = 0; kk < kBK / 16; ++kk)
+                        tc::mma_bf16(tbase + kTColO + (lk & 1) * kN, desc_v + (uint64_t)(buf * (kVTile<D> >> 4) + kk * (2048 >> 4)),
+                                     desc_p + (uint64_t)(buf * (kPTile >> 4) + kk * (2048 >> 4)), idesc, kk > 0 || !first ? 1u : 0u);
+                    tc::commit(&sh->pv_done[buf]);
+                    if (end) tc::commit(&sh->o_full[lk & 1]);
+                }
+                __syncwarp();
+                return true;
+            };
+#pragma unroll 1
+            for (uint32_t k = 0; ok; ++k) {
+                const int slot_i = k % kItems;
+                if (!(ok = twait(&sh->item_full[slot_i], (k / kItems) & 1))) break;
+                const int b = __reduce_max_sync(0xffffffffu, sh->items[slot_i].b), n = __reduce_max_sync(0xffffffffu, sh->items[slot_i].n);
+                const uint32_t N = (uint32_t)(__reduce_max_sync(0xffffffffu, sh->items[slot_i].ntok) * p.Gs + 15) & ~15u;
+                if (b < 0) {
+                    if (live) ok = add_o();
+                    break;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->item_empty[slot_i]);
+                if (!(ok = twait(&sh->q_full[k & 1], (k >> 1) & 1))) break;
+                const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | (8u << 24);
+#pragma unroll 1
+                for (int j = 0; j < n; ++j) {
+                    const uint32_t buf = g & 1, ph = (g >> 1) & 1;
+                    if (!(ok = twait(&sh->k_full[buf], ph) && twait(&sh->s_empty[buf], ph ^ 1))) break;
+                    tc::fence_after();
+                    if (leader) {
+                        const uint64_t dq = desc_q + (uint64_t)((k & 1) * (kQTile<D> >> 4));
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            tc::mma_bf16_ts(tbase + kTColS + buf * kN, tbase + kTColK + buf * kN + kk * 8,
+                                            dq + (uint64_t)((kk >> 2) * (kQBox >> 4) + (kk & 3) * 2), idesc, kk > 0 ? 1u : 0u);
+                        tc::commit(&sh->s_full[buf]);
+                        tc::commit(&sh->k_empty[buf]);
+                        if (j == n - 1) tc::commit(&sh->q_empty[k & 1]);
+                    }
+                    __syncwarp();
+                    if (live && !(ok = add_o())) break;
+                    live = true;
+                    first = j == 0;
+                    end = j == n - 1;
+                    ln = N;
+                    lk = k;
+                    ++g;
+                }
+            }
+            if (!ok) fail();
+            // every product issued is complete before the tensor memory is given back
+            if (leader) tc::commit(&sh->fin);
+            __syncwarp();
+            twait(&sh->fin, 0);
+        } else {
+            // ===================== the work list (warp 14), then seq_status (both)
+            if (warp == 14) {
+                uint32_t k = 0;
+                RowsItem it;
+                bool ok = aligned;
+                do {
+                    next_item(p, walk, it);
+                    const int slot_i = k % kItems;
+                    if (!(ok = twait(&sh->item_empty[slot_i], ((k / kItems) & 1) ^ 1) && !__shfl_sync(0xffffffffu, *abort_flag, 0))) break;
+                    if (lane == 0) {
+                        sh->items[slot_i] = it;
+                        mbar_arrive(&sh->item_full[slot_i]);
+                    }
+                    __syncwarp();
+                    ++k;
+                } while (it.b >= 0);
+                if (!ok) fail();
+            }
+            const int own = p.seq_status ? (int)blockIdx.x * 2 + warp - 14 : p.B;
+#pragma unroll 1
+            for (int sb = own; sb < p.B; sb += (int)gridDim.x * 2) {
+                const bool bad = bad_sequence(p, sb, lane);
+                if (lane == 0) p.seq_status[sb] = bad ? SV_ERR_BAD_INPUT : SV_OK;
+            }
+            if (lane == 0 && own < p.B && gave_up(p.call))
+#pragma unroll 1
+                for (int sb = own; sb < p.B; sb += (int)gridDim.x * 2) p.seq_status[sb] = SV_ERR_TIMEOUT;
+            // the next call's counters, whose grid may be another
+            if (warp == 15)
+                for (int c = blockIdx.x * 32 + lane; c < kRowsMaxGrid; c += gridDim.x * 32) {
+                    p.counters[rows_counter(sh->call + 1, c)] = 0;
+                    p.counters[rows_counter(sh->call + 1, c) + 1] = 0;
+                }
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 13) {
+        tc::fence_after();
+        tc::tmem_dealloc(tbase, kTCols);
+    }
+    if (tid == 0 && *abort_flag) give_up(p.call, p.seq_status, p.B);
+}
+
+const void *quant_kernel_fn(int D) {
+    return D == 128 ? reinterpret_cast<const void *>(&quant_tc_kernel<128>) : reinterpret_cast<const void *>(&quant_tc_kernel<64>);
+}
+
+int quant_smem_bytes(int D) { return D == 128 ? kTSmem<128> : kTSmem<64>; }
 
 }  // namespace chunk
 }  // namespace sv

@@ -1,0 +1,168 @@
+// sv_quant_walk.cuh -- the items that a CTA takes of the work list of the
+// attention over pages held in 4 bits (sv_quant_list.h).
+#pragma once
+
+#include "sv_device.cuh"
+#include "sv_quant_rows.h"
+
+namespace sv {
+namespace chunk {
+
+__device__ __forceinline__ float lg2_approx(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+
+struct RowsItem {
+    int b, h;          // sequence (-1: no more), group of heads
+    int row0, ntok;    // first row, tokens
+    int pos0;          // position of the first token
+    int seq_row0;      // the sequence's first row
+    int kt0, n;        // first K/V tile and number of tiles of this run
+    int c_first, nc, ci;  // CTAs that share the item's tiles, this one's number among them
+};
+
+// The items of this CTA's units, one after another; the same in every lane.
+struct RowsWalk {
+    long long U, u0, u1, ui;  // ui: first unit of item (b, h, i)
+    int nctas, b, h, i;
+    RowsSeq seq;
+    bool loaded;
+};
+
+__device__ __forceinline__ RowsSeq load_seq(const RowsParams &p, int b) {
+    return rows_seq(p.rows, p.prefix_lens[b], p.row_starts[b], p.row_starts[b + 1]);
+}
+
+static __device__ __noinline__ void next_item(const RowsParams &p, RowsWalk &w, RowsItem &it) {
+    it.b = -1;
+    while (w.b < p.B && w.ui < w.u1) {
+        if (!w.loaded) {
+            w.seq = load_seq(p, w.b);
+            w.loaded = true;
+            w.h = w.i = 0;
+        }
+        if (w.seq.items == 0 || w.h == p.groups) {
+            ++w.b;
+            w.loaded = false;
+            continue;
+        }
+        const RowsSeq s = w.seq;
+        const int i = w.i, h = w.h, n = rows_tiles(p.rows, s, i);
+        const long long first = w.ui + kRowsItemCost;  // unit of the first tile
+        w.ui = first + n;
+        if (++w.i == s.items) w.i = 0, ++w.h;
+        const int a = w.u0 > first ? (int)min(w.u0 - first, (long long)n) : 0;
+        const int z = w.u1 > first ? (int)min(w.u1 - first, (long long)n) : 0;
+        if (a >= z) continue;
+        it.b = w.b;
+        it.h = h;
+        it.row0 = s.row0 + i * p.rows.tok;
+        it.ntok = min(p.rows.tok, s.n - i * p.rows.tok);
+        it.pos0 = s.L + i * p.rows.tok;
+        it.seq_row0 = s.row0;
+        it.kt0 = rows_first_tile(p.rows, it.pos0) + a;
+        it.n = z - a;
+        it.c_first = blockIdx.x;
+        it.nc = 1;
+        if (it.n < n) {
+            it.c_first = cta_of(w.U, w.nctas, first);
+            it.nc = cta_of(w.U, w.nctas, first + n - 1) - it.c_first + 1;
+        }
+        it.ci = (int)blockIdx.x - it.c_first;
+        return;
+    }
+}
+
+// Whether sequence sb has lengths that are none, a page id out of range among those its rows see, or
+// parents that are no tree; by a whole warp.
+static __device__ __noinline__ bool bad_sequence(const RowsParams &p, int sb, int lane) {
+    const int L = p.prefix_lens[sb], first = p.row_starts[sb], end = p.row_starts[sb + 1];
+    const RowsSeq s = rows_seq(p.rows, L, first, end);
+    bool bad = !lengths_ok(Shape{1, p.rows.window, p.rows.num_rows, p.rows.S_max}, L, first, end);
+    if (s.n > 0) {
+        const int lo = p.rows.window > 0 ? max(0, L - p.rows.window + 1) : 0;
+        const int32_t *trow = p.block_table + (size_t)sb * p.max_pages;
+#pragma unroll 1
+        for (int j = lo / p.page_size + lane; j <= (L + s.n - 1) / p.page_size; j += 32) {
+            const int pg = trow[j];
+            if (pg < 0 || pg >= p.num_pages) bad = true;
+        }
+        if (p.parents) {
+            bad = bad || s.n > kTreeNodes;
+#pragma unroll 1
+            for (int i = lane; i < min(s.n, kTreeNodes); i += 32) {
+                const int par = p.parents[first + i];
+                if (i == 0 ? par != -1 : par < 0 || par >= i) bad = true;
+            }
+        }
+    }
+    return __any_sync(0xffffffffu, bad);
+}
+
+// This CTA's share of the list, by its kT threads together: units before each thread's sequences
+// (`before`, kT of them; warp_units, kT / 32), then the place where the share begins.
+template <int kT>
+__device__ __forceinline__ void plan_walk(const RowsParams &p, long long *warp_units, long long *before, int tid, RowsWalk &w) {
+    const int lane = tid & 31, warp = tid >> 5;
+    const int per = (p.B + kT - 1) / kT, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+    long long mine = 0;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+        const RowsSeq s = load_seq(p, b);
+        mine += rows_units_before(p.rows, s, s.items) * p.groups;
+    }
+    long long x = mine;
+#pragma unroll 1
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+    }
+    if (lane == 31) warp_units[warp] = x;
+    __syncthreads();
+    long long base = 0;
+    w.U = 0;
+#pragma unroll 1
+    for (int i = 0; i < kT / 32; ++i) {
+        if (i < warp) base += warp_units[i];
+        w.U += warp_units[i];
+    }
+    before[tid] = base + x - mine;
+    __syncthreads();
+    w.nctas = rows_ctas(w.U, gridDim.x);
+    const bool has = w.U > 0 && (int)blockIdx.x < w.nctas;
+    w.u0 = has ? cta_begin(w.U, w.nctas, blockIdx.x) : 0;
+    w.u1 = has ? cta_begin(w.U, w.nctas, blockIdx.x + 1) : 0;
+    w.b = p.B;
+    w.ui = 0;
+    w.h = w.i = 0;
+    w.loaded = false;
+    if (has) {  // the last thread with at most u0 units before its sequences, then the sequence
+        int at = 0;
+#pragma unroll 1
+        for (int i = lane; i < kT; i += 32) at += before[i] <= w.u0;
+        at = __reduce_add_sync(0xffffffffu, at) - 1;
+        w.b = at * per;
+        w.ui = before[at];
+#pragma unroll 1
+        while (w.b < p.B) {
+            w.seq = load_seq(p, w.b);
+            const long long head = rows_units_before(p.rows, w.seq, w.seq.items);
+            if (w.seq.items > 0 && w.ui + head * p.groups > w.u0) {
+                w.loaded = true;
+                w.h = (int)quot(w.u0 - w.ui, head);
+                const long long v = w.u0 - w.ui - w.h * head;
+                w.i = rows_item_at(p.rows, w.seq, v);
+                w.ui += w.h * head + rows_units_before(p.rows, w.seq, w.i);
+                break;
+            }
+            w.ui += head * p.groups;
+            ++w.b;
+        }
+    }
+}
+
+}  // namespace chunk
+}  // namespace sv
