@@ -54,10 +54,9 @@ bool q_map(CUtensorMap *map, const void *q, int num_rows, int Hq, int D, long lo
 // SMs of the current device once the kernel is known to run on it as
 // planned, asked for once a device: the attribute calls cost more than a
 // launch.  0 when it cannot run.
-int ready_sms(int D, bool quant) {
+int ready_sms(int D, int quant) {
     struct Entry {
-        int dev, D, sms;
-        bool quant;
+        int dev, D, sms, quant;
     };
     static std::mutex mu;
     static Entry cache[64];
@@ -67,10 +66,10 @@ int ready_sms(int D, bool quant) {
     std::lock_guard<std::mutex> lock(mu);
     for (int i = 0; i < ncache; ++i)
         if (cache[i].dev == dev && cache[i].D == D && cache[i].quant == quant) return cache[i].sms;
-    const void *fn = quant ? chunk::quant_kernel_fn(D) : chunk::kernel_fn(D);
+    const void *fn = quant ? chunk::quant_kernel_fn(D, quant) : chunk::kernel_fn(D);
     const int smem = quant ? chunk::quant_smem_bytes(D) : chunk::smem_bytes(D);
     const int threads = quant ? 512 : chunk::kThreads;
-    const int regs = quant ? 0 : chunk::kLaunchRegs;
+    const int regs = quant ? 128 : chunk::kLaunchRegs;
     int max_optin = 0, sms = device_sm_count(), occ = 0;
     cudaFuncAttributes at;
     // the kernel hands its launch registers out again (setmaxnreg): it must
@@ -89,7 +88,7 @@ int ready_sms(int D, bool quant) {
 sv_status plan_chunk(int Hq, int Hkv, int D, bool quant, ChunkPlan *plan) {
     if ((D != 64 && D != 128) || Hq / Hkv > chunk::kRows) return SV_ERR_UNSUPPORTED;
     ChunkPlan pl{};
-    pl.grid = ready_sms(D, quant);
+    pl.grid = ready_sms(D, quant ? 4 : 0);
     if (pl.grid <= 0) return SV_ERR_CUDA;
     const size_t tiles = (size_t)pl.grid * 2 * 2;
     static_assert(3 * sizeof(chunk::CallWords) <= chunk::kCallBytes, "the forms' words");
@@ -143,11 +142,13 @@ sv_status launch_chunk_attention(const ChunkArgs &a, const ChunkPlan &pl, void *
         p.call += 2;
         p.counters = reinterpret_cast<int *>(base + pl.off_rows);
         if (const int form = chunk::rows_form(a); form >= 0) return chunk::launch_rows(a, p, form, st);
-        const chunk::RowsParams rp = chunk::rows_params(a, p, chunk::kRowsCols);
+        const int chunks = chunk::quant_chunks(a);
+        if (ready_sms(a.D, chunks) != pl.grid) return SV_ERR_CUDA;
+        const chunk::RowsParams rp = chunk::rows_params(a, p, 16 * chunks);
         CUtensorMap tmq;
         if (!q_map(&tmq, a.q, a.num_rows, a.Hq, a.D, a.q_stride, rp.Gs, rp.rows.tok)) return SV_ERR_CUDA;
         void *args[] = {&tmq, const_cast<chunk::RowsParams *>(&rp)};
-        return launch_pdl(chunk::quant_kernel_fn(a.D), dim3(pl.grid), dim3(512), chunk::quant_smem_bytes(a.D), st, args) == cudaSuccess
+        return launch_pdl(chunk::quant_kernel_fn(a.D, chunks), dim3(pl.grid), dim3(512), chunk::quant_smem_bytes(a.D), st, args) == cudaSuccess
                    ? SV_OK
                    : SV_ERR_CUDA;
     } else if (const int cluster = chunk::few_cluster(a)) {

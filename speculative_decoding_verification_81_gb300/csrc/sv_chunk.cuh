@@ -125,7 +125,7 @@ sv_status launch_few(const ChunkArgs &args, const Params &params, int cluster, c
 
 const void *kernel_fn(int D);
 int smem_bytes(int D);
-const void *quant_kernel_fn(int D);
+const void *quant_kernel_fn(int D, int chunks);  // of 16 columns: 2 .. 4
 int quant_smem_bytes(int D);
 
 }  // namespace chunk

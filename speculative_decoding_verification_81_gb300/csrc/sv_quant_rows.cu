@@ -57,6 +57,8 @@ struct RowsShared {
     float u[kRW][8 * NT];
     float2 ml[kRW][8 * NT];
     unsigned long long above[2][kTreeNodes];
+    RowsWalk walk;       // warp 0's
+    RowsItem items[2];   // the item at hand and the next
     long long warp_units[kRW];
     long long before[kRT];
     uint64_t full[kRW][kRowsDepth<D, NT>];
@@ -152,14 +154,31 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const Ro
     unsigned long long call = 0;
     if (tid == 0) call = begin_call(p.call);
 
-    RowsWalk walk;
-    plan_walk<kRT>(p, sh.warp_units, sh.before, tid, walk);
+    auto look_ahead = [&](int to) {  // the next item (by one warp)
+        RowsWalk walk = sh.walk;
+        RowsItem x;
+        next_item(p, walk, x);
+        __syncwarp();
+        if (lane == 0) {
+            sh.walk = walk;
+            sh.items[to] = x;
+        }
+        __syncwarp();
+    };
+    {
+        RowsWalk walk;
+        plan_walk<kRT>(p, sh.warp_units, sh.before, tid, walk);
+        if (tid == 0) {
+            sh.walk = walk;
+            sh.items[1].b = 0;
+        }
+        __syncwarp();
+    }
 
     uint8_t *const ring = sh.ring[warp][0];
     const uint32_t ring_at = smem_u32(ring);
     uint32_t put = 0, got = 0;  // units asked for and used
     bool lost = false;
-    RowsItem it;
 
     // of the item at hand, or of the one whose copies are begun: this warp's tiles i0 .. i1 - 1, the
     // next to ask for, and, a lane a tile from `base` on, the cache rows of the unit's halves
@@ -210,7 +229,6 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const Ro
         ++put;
         ++ask;
     };
-    int qb = 0;
     auto begin = [&](const RowsItem &x, int buf) {  // its first copies, and its queries
         const int lo = p.rows.window > 0 ? max(0, x.pos0 - p.rows.window + 1) : 0, hi = x.pos0 + x.ntok;
         const int s0 = x.kt0 * kTileSlots + warp * kU;  // (the slots seen end, or begin, within a tile)
@@ -241,8 +259,10 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const Ro
             sh.above[buf][tk] = set;
         }
     };
-    next_item(p, walk, it);
-    if (it.b >= 0) begin(it, 0);
+    // (item k is items[k & 1]; the first look ahead is of item 0, the loop's of the one after)
+    if (warp == 0) look_ahead(0);
+    __syncthreads();
+    if (sh.items[0].b >= 0) begin(sh.items[0], 0);
 
     // ---- seq_status, while the first copies are on their way
     const int own = p.seq_status ? (int)blockIdx.x * kRW + warp : p.B;
@@ -253,7 +273,9 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const Ro
     }
 
 #pragma unroll 1
-    while (it.b >= 0) {
+    for (int qb = 0;; qb ^= 1) {
+        const RowsItem it = sh.items[qb];
+        if (it.b < 0) break;
         const int cols = it.ntok * p.Gs, nt = (cols + 7) / 8;
         const int lo = p.rows.window > 0 ? max(0, it.pos0 - p.rows.window + 1) : 0, hi = it.pos0 + it.ntok;
         const int own0 = it.pos0 - (it.row0 - it.seq_row0);  // slot of the sequence's first new row
@@ -289,6 +311,7 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const Ro
             }
         }
         __syncthreads();
+        if (warp == 0) look_ahead(qb ^ 1);
 #pragma unroll 1
         for (int i = i0; i < i1; ++i) {
             const uint32_t st = got % kDepth;
@@ -437,7 +460,7 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const Ro
             }
             __syncwarp();
             ++got;
-            if (ask < i1) fetch(it);
+            if (ask < i1) fetch(sh.items[qb]);
         }
         if (lost) {  // its own copies still on their way, this one too
 #pragma unroll 1
@@ -458,10 +481,7 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const Ro
                 if (g == 0) sh.ml[warp][8 * n + 2 * t + c] = make_float2(sh.u[warp][8 * n + 2 * t + c], l[n][c]);
             }
         }
-        const RowsItem cur = it;
-        next_item(p, walk, it);
-        qb ^= 1;
-        if (it.b >= 0) begin(it, qb);  // (the next item's copies run while this one's sums meet)
+        const RowsItem cur = sh.items[qb];
         const bool whole = cur.nc == 1;
         const int heads = min(p.Gs, p.G - cur.h % p.parts * p.Gs);
         const int head0 = cur.h / p.parts * p.G + cur.h % p.parts * p.Gs;
@@ -484,6 +504,7 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const Ro
                         make_float4(o[x][n][0] + z[n][0], o[x][n][1] + z[n][1], o[x][n][2] + z[n][0], o[x][n][3] + z[n][1]);
             }
             __syncthreads();
+            if (n0 == 0 && sh.items[qb ^ 1].b >= 0) begin(sh.items[qb ^ 1], qb ^ 1);  // (its copies run while the sums meet)
             // a task: eight dims of two columns
             for (int i = tid; i < kMeet<NT> * (kX / 4) * 32; i += kRT) {
                 const int ln = i & 31, w4 = (i >> 5) % (kX / 4), dn = (i >> 5) / (kX / 4), n = n0 + dn;
@@ -643,9 +664,15 @@ int form_grid(int D, int i) {
 
 // Rows a sequence go by the call's mean: the lengths are on the device, and any form
 // takes any rows.
+static long long mean_columns(const ChunkArgs &a) { return ((long long)a.num_rows + a.B - 1) / a.B * (a.Hq / a.Hkv); }
+
+int quant_chunks(const ChunkArgs &a) {
+    const long long mean = mean_columns(a);
+    return mean <= 32 ? 2 : mean <= 48 ? 3 : 4;
+}
+
 int rows_form(const ChunkArgs &a) {
-    const int G = a.Hq / a.Hkv;
-    const long long mean = ((long long)a.num_rows + a.B - 1) / a.B * G;
+    const long long mean = mean_columns(a);
     if (mean > kRowsMost) return -1;
     int i = 0;
     while (i + 1 < kForms && form_at(a.D, i).cols < mean) ++i;

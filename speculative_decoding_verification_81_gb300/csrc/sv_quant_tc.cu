@@ -39,6 +39,8 @@ constexpr int kTT = 512;                       // threads
 constexpr int kN = 64;                         // columns of an item at most
 constexpr uint32_t kTCols = 512, kTColS = 0, kTColO = 128, kTColK = 256;  // two of each, 64 columns apart
 
+constexpr int kTRegsSoftmax = 152, kTRegsOther = 104;  // 256 x 152 + 256 x 104 = 512 x 128
+
 template <int D>
 constexpr int kVTile = kBK * D * 2;            // V's operand
 constexpr int kPTile = kBK * kN * 2;
@@ -76,24 +78,40 @@ template <int D>
 constexpr int kTSmem = 2 * (kVTile<D> + kPTile + kQTile<D>) + kTRawStages<D> * kTRaw<D> + (int)sizeof(TShared);
 static_assert(kTSmem<128> <= 227 * 1024 && kTSmem<64> <= 227 * 1024, "shared memory");
 
+// A probe of `bar` that may suspend for some microseconds, so that a warp that waits takes no issue slots
+// from the others.
+__device__ __forceinline__ bool tprobe(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+}
 __device__ __noinline__ bool twait_long(uint32_t bar, uint32_t parity) {
     const long long t0 = clock64();
     while (true) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
-        if (__all_sync(0xffffffffu, ok != 0)) return true;
+        if (__all_sync(0xffffffffu, tprobe(bar, parity))) return true;
         if (__any_sync(0xffffffffu, clock64() - t0 > kWaitCycles)) return false;
     }
 }
 // Wait for the phase of `bar` with the given parity, by a whole warp with one verdict.
 __device__ __forceinline__ bool twait(uint64_t *bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || twait_long(smem_u32(bar), parity);
+    return __all_sync(0xffffffffu, tprobe(smem_u32(bar), parity)) || twait_long(smem_u32(bar), parity);
+}
+// The same without a call, for the softmax warps (a function that both parts call costs the kernel its
+// register split).
+__device__ __forceinline__ bool twait_here(uint64_t *bar, uint32_t parity) {
+    const uint32_t at = smem_u32(bar);
+    if (__all_sync(0xffffffffu, tprobe(at, parity))) return true;
+    const long long t0 = clock64();
+    while (true) {
+        if (__all_sync(0xffffffffu, tprobe(at, parity))) return true;
+        if (__any_sync(0xffffffffu, clock64() - t0 > kWaitCycles)) return false;
+    }
 }
 
 __device__ __forceinline__ uint32_t telect() {
@@ -159,9 +177,9 @@ __device__ __forceinline__ float across(float (&v)[32], int lane) {
 
 }  // namespace
 
-template <int D>
+template <int D, int kCh>  // kCh chunks of 8 columns a softmax group
 __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant__ CUtensorMap tmq, const RowsParams p) {
-    constexpr int kRow = D / 2, kRaw = kTRawStages<D>;
+    constexpr int kRow = D / 2, kRaw = kTRawStages<D>, N = 16 * kCh;
     extern __shared__ __align__(1024) uint8_t smem[];  // (the swizzle's atoms are 1024 bytes)
     uint8_t *const vbuf = smem, *const pbuf = vbuf + 2 * kVTile<D>, *const qbuf = pbuf + 2 * kPTile;
     uint8_t *const raw = qbuf + 2 * kQTile<D>;
@@ -197,6 +215,8 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
         sh->abort_flag = 0;
         fence_mbar_init();
     }
+    for (int i = tid; i < 2 * kQTile<D> / 16; i += kTT) reinterpret_cast<uint4 *>(qbuf)[i] = make_uint4(0, 0, 0, 0);  // (columns past the items' stay zeros)
+    tc::fence_proxy_async_smem();
     if (tid < kN) sh->tok[tid] = (uint8_t)(tid / p.Gs);
     if (tid == 32 * 12) prefetch_tensormap(&tmq);
     if (warp == 13) tc::tmem_alloc(&sh->tmem, kTCols);
@@ -214,6 +234,7 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
 
     if (warp < 8) {
         // ===================== softmax: a thread a slot, the columns of its group
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTRegsSoftmax));
         const int group = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t tl = tbase + ((uint32_t)(quarter * 32) << 16);
         uint32_t tile = 0;  // tiles of the CTA before this item
@@ -221,19 +242,19 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
 #pragma unroll 1
         for (uint32_t k = 0;; ++k) {
             const int slot_i = k % kItems;
-            bad = bad || !warp_wait_bounded(&sh->item_full[slot_i], (k / kItems) & 1);
+            bad = bad || !twait_here(&sh->item_full[slot_i], (k / kItems) & 1);
             if (group_any(group, bad)) {
                 bad = true;
                 break;
             }
             const RowsItem it = sh->items[slot_i];
             if (it.b < 0) break;
-            const int cols = it.ntok * p.Gs, N = (cols + 15) & ~15, nch = N / 16;  // chunks of 8 columns a group
-            const int c0 = group * (N / 2);                                        // the group's first column
+            const int cols = it.ntok * p.Gs;
+            const int c0 = group * (N / 2);                      // the group's first column
             const int own0 = it.pos0 - (it.row0 - it.seq_row0);                    // slot of the sequence's first new row
             const int all_hi = p.parents ? own0 : it.pos0 + 1;                     // below, and from all_lo on, every row sees a slot
             const int all_lo = p.rows.window > 0 ? it.pos0 + it.ntok - p.rows.window : 0;
-            bad = !warp_wait_bounded(&sh->q_full[k & 1], (k >> 1) & 1);
+            bad = !twait_here(&sh->q_full[k & 1], (k >> 1) & 1);
             if (!bad && r < N / 2) {  // the sums of this group's columns of Q
                 const uint8_t *q = qbuf + (k & 1) * kQTile<D>;
                 float2 s = make_float2(0.f, 0.f);
@@ -258,15 +279,15 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
                 break;
             }
             if (r == 0) mbar_arrive(&sh->q_empty[k & 1]);
-            float2 l[16], z[16];
+            float2 l[4 * kCh], z[4 * kCh];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) l[i] = z[i] = make_float2(0.f, 0.f);
+            for (int i = 0; i < 4 * kCh; ++i) l[i] = z[i] = make_float2(0.f, 0.f);
             const uint32_t o_at = tl + kTColO + (k & 1) * kN + c0;
 #pragma unroll 1
             for (int j = 0; j < it.n; ++j) {
                 const uint32_t g = tile + j, buf = g & 1, ph = (g >> 1) & 1;
                 const int slot0 = (it.kt0 + j) * kBK, slot = slot0 + r;
-                bad = !warp_wait_bounded(&sh->s_full[buf], ph) || !warp_wait_bounded(&sh->pv_done[buf], ph ^ 1);
+                bad = !twait_here(&sh->s_full[buf], ph) || !twait_here(&sh->pv_done[buf], ph ^ 1);
                 tc::fence_after();
                 const uint2 par = sh->slots[g & 3][r];
                 const float ks = bf16_lo(par.x) * p.scale_log2;
@@ -294,41 +315,38 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
                         sees = below & ~under;
                     }
                 }
-                float2 x[16];
+                float2 x[kCh][4];
                 const uint32_t s_at = tl + kTColS + buf * kN + c0;
                 auto scores = [&](bool less) __attribute__((always_inline)) {  // less: less u
 #pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) {
-                        float2(&y)[4] = *reinterpret_cast<float2(*)[4]>(&x[4 * ch]);
-                        if (ch < nch) tmem_ld8(s_at + 8 * ch, y);
+                    for (int ch = 0; ch < kCh; ++ch) {
+                        tmem_ld8(s_at + 8 * ch, x[ch]);
                     }
                     tc::wait_ld();
 #pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) {
-                        if (ch >= nch) break;
+                    for (int ch = 0; ch < kCh; ++ch) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const float4 c4 = sh->col[(c0 >> 1) + 4 * ch + i];
                             float2 t = less ? make_float2(c4.z, c4.w) : make_float2(0.f, 0.f);
                             t = __ffma2_rn(km2, make_float2(c4.x, c4.y), t);
-                            x[4 * ch + i] = __ffma2_rn(x[4 * ch + i], ks2, t);
+                            x[ch][i] = __ffma2_rn(x[ch][i], ks2, t);
                         }
                     }
                     if (sees != ~0u) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            if (!(sees >> (2 * i) & 1)) x[i].x = kNegInf;
-                            if (!(sees >> (2 * i + 1) & 1)) x[i].y = kNegInf;
+                        for (int i = 0; i < 4 * kCh; ++i) {
+                            if (!(sees >> (2 * i) & 1)) x[i >> 2][i & 3].x = kNegInf;
+                            if (!(sees >> (2 * i + 1) & 1)) x[i >> 2][i & 3].y = kNegInf;
                         }
                     }
                 };
                 scores(true);
                 float top = kNegInf;
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
-                    if (ch >= nch) break;
+                for (int ch = 0; ch < kCh; ++ch) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) top = fmaxf(fmaxf(top, x[4 * ch + i].x), x[4 * ch + i].y);
+                    for (int i = 0; i < 4; ++i) top = fmaxf(fmaxf(top, x[ch][i].x), x[ch][i].y);
                 }
                 if (group_any(group, bad || top + lv > kRoom)) {
                     if (group_any(group, bad)) {
@@ -341,9 +359,8 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
                         float v[32];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const bool on = i < 4 * nch;
-                            v[2 * i] = on ? x[i].x + lv : kNegInf;
-                            v[2 * i + 1] = on ? x[i].y + lv : kNegInf;
+                            v[2 * i] = i < 4 * kCh ? x[i / 4 % kCh][i & 3].x + lv : kNegInf;
+                            v[2 * i + 1] = i < 4 * kCh ? x[i / 4 % kCh][i & 3].y + lv : kNegInf;
                         }
                         sh->most[group][quarter][lane] = across<true>(v, lane);
                     }
@@ -358,15 +375,14 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
                         if (up) *nu = -a;
                     }
                     const uint32_t before = g - 1;  // the products that added to O last
-                    if (j > 0) bad = !warp_wait_bounded(&sh->pv_done[before & 1], (before >> 1) & 1);
+                    if (j > 0) bad = !twait_here(&sh->pv_done[before & 1], (before >> 1) & 1);
                     if (group_any(group, bad)) {
                         bad = true;
                         break;
                     }
                     tc::fence_after();
 #pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) {
-                        if (ch >= nch) break;
+                    for (int ch = 0; ch < kCh; ++ch) {
                         float2 f[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -392,13 +408,12 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
                 const float2 vs2 = make_float2(vs, vs), vm2 = make_float2(vm, vm);
                 uint8_t *const to = pbuf + buf * kPTile + r * 128;
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
-                    if (ch >= nch) break;
+                for (int ch = 0; ch < kCh; ++ch) {
                     uint32_t w[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int n = 4 * ch + i;
-                        const float2 e = make_float2(ex2_approx(x[n].x), ex2_approx(x[n].y));
+                        const float2 e = make_float2(ex2_approx(x[ch][i].x), ex2_approx(x[ch][i].y));
                         l[n] = __fadd2_rn(l[n], e);
                         z[n] = __ffma2_rn(e, vm2, z[n]);
                         const float2 y = __fmul2_rn(e, vs2);
@@ -413,14 +428,14 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
             if (bad) break;
             tile += it.n;
             // ---- the columns' sums over the slots, then a thread a dim
-            bad = !warp_wait_bounded(&sh->o_full[k & 1], (k >> 1) & 1);
+            bad = !twait_here(&sh->o_full[k & 1], (k >> 1) & 1);
             {
                 float v[32];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[2 * i] = l[i].x, v[2 * i + 1] = l[i].y;
+                for (int i = 0; i < 16; ++i) v[2 * i] = i < 4 * kCh ? l[i % (4 * kCh)].x : 0.f, v[2 * i + 1] = i < 4 * kCh ? l[i % (4 * kCh)].y : 0.f;
                 const float ls = across<false>(v, lane);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[2 * i] = z[i].x, v[2 * i + 1] = z[i].y;
+                for (int i = 0; i < 16; ++i) v[2 * i] = i < 4 * kCh ? z[i % (4 * kCh)].x : 0.f, v[2 * i + 1] = i < 4 * kCh ? z[i % (4 * kCh)].y : 0.f;
                 sh->sums[group][quarter][lane] = make_float2(ls, across<false>(v, lane));
             }
             if (group_any(group, bad)) {
@@ -454,8 +469,7 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
                 }
             }
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
-                if (ch >= nch) break;
+            for (int ch = 0; ch < kCh; ++ch) {
                 float2 o[4];
                 __syncwarp();
                 tmem_ld8(o_at + 8 * ch, o);
@@ -531,6 +545,7 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
         }
         if (bad) fail();
     } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTRegsOther));
         if (warp < 12) {
             // ===================== codes to operands: a thread a slot
             const int quarter = warp & 3, r = quarter * 32 + lane;
@@ -700,16 +715,16 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
             const uint64_t desc_q = tc::smem_desc(base_u32 + 2 * (kVTile<D> + kPTile), 16, 1024);
             uint32_t g = 0;
             bool ok = aligned;
-            // the tile whose O is still to be added to: flags, columns, item
+            // the tile whose O is still to be added to: flags, item
             bool live = false, first = false, end = false;
-            uint32_t ln = 0, lk = 0;
+            uint32_t lk = 0;
             auto add_o = [&]() -> bool {
                 const uint32_t t = g - 1, buf = t & 1, ph = (t >> 1) & 1;
                 if (!twait(&sh->v_full[buf], ph) || !twait(&sh->p_full[buf], ph)) return false;
                 if (first && !twait(&sh->o_empty[lk & 1], ((lk >> 1) & 1) ^ 1)) return false;
                 tc::fence_after();
                 // f16 both, V's dims and P's columns contiguous
-                const uint32_t idesc = (1u << 4) | (1u << 15) | (1u << 16) | ((ln >> 3) << 17) | (8u << 24);
+                constexpr uint32_t idesc = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < kBK / 16; ++kk)
@@ -726,7 +741,6 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
                 const int slot_i = k % kItems;
                 if (!(ok = twait(&sh->item_full[slot_i], (k / kItems) & 1))) break;
                 const int b = __reduce_max_sync(0xffffffffu, sh->items[slot_i].b), n = __reduce_max_sync(0xffffffffu, sh->items[slot_i].n);
-                const uint32_t N = (uint32_t)(__reduce_max_sync(0xffffffffu, sh->items[slot_i].ntok) * p.Gs + 15) & ~15u;
                 if (b < 0) {
                     if (live) ok = add_o();
                     break;
@@ -734,7 +748,7 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh->item_empty[slot_i]);
                 if (!(ok = twait(&sh->q_full[k & 1], (k >> 1) & 1))) break;
-                const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | (8u << 24);
+                constexpr uint32_t idesc = tc::idesc_bf16(kBK, N, false);
 #pragma unroll 1
                 for (int j = 0; j < n; ++j) {
                     const uint32_t buf = g & 1, ph = (g >> 1) & 1;
@@ -755,7 +769,6 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
                     live = true;
                     first = j == 0;
                     end = j == n - 1;
-                    ln = N;
                     lk = k;
                     ++g;
                 }
@@ -810,8 +823,12 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
     if (tid == 0 && *abort_flag) give_up(p.call, p.seq_status, p.B);
 }
 
-const void *quant_kernel_fn(int D) {
-    return D == 128 ? reinterpret_cast<const void *>(&quant_tc_kernel<128>) : reinterpret_cast<const void *>(&quant_tc_kernel<64>);
+const void *quant_kernel_fn(int D, int chunks) {
+    switch (chunks) {
+        case 2: return D == 128 ? reinterpret_cast<const void *>(&quant_tc_kernel<128, 2>) : reinterpret_cast<const void *>(&quant_tc_kernel<64, 2>);
+        case 3: return D == 128 ? reinterpret_cast<const void *>(&quant_tc_kernel<128, 3>) : reinterpret_cast<const void *>(&quant_tc_kernel<64, 3>);
+        default: return D == 128 ? reinterpret_cast<const void *>(&quant_tc_kernel<128, 4>) : reinterpret_cast<const void *>(&quant_tc_kernel<64, 4>);
+    }
 }
 
 int quant_smem_bytes(int D) { return D == 128 ? kTSmem<128> : kTSmem<64>; }

@@ -36,7 +36,7 @@ __device__ __forceinline__ RowsSeq load_seq(const RowsParams &p, int b) {
     return rows_seq(p.rows, p.prefix_lens[b], p.row_starts[b], p.row_starts[b + 1]);
 }
 
-static __device__ __noinline__ void next_item(const RowsParams &p, RowsWalk &w, RowsItem &it) {
+__device__ __forceinline__ void next_item(const RowsParams &p, RowsWalk &w, RowsItem &it) {
     it.b = -1;
     while (w.b < p.B && w.ui < w.u1) {
         if (!w.loaded) {
