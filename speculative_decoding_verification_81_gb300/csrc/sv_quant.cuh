@@ -51,9 +51,13 @@ __device__ __forceinline__ uint32_t centred_f16_high(uint32_t pair) {
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(c) : "r"(x), "r"(0x2c002c00u), "r"(0xd480d480u));  // x / 16 - 72
     return c;
 }
-__device__ __forceinline__ uint4 expand_f16(uint32_t w) {
+// A word's eight values in f16, each step * (code - 8) + middle rounded once (step and middle twice each).
+__device__ __forceinline__ uint4 scaled_f16(uint32_t w, uint32_t step, uint32_t mid) {
     const uint32_t v = w >> 8;
-    return make_uint4(centred_f16(w), centred_f16_high(w), centred_f16(v), centred_f16_high(v));
+    uint32_t x[4] = {centred_f16(w), centred_f16_high(w), centred_f16(v), centred_f16_high(v)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(x[i]) : "r"(x[i]), "r"(step), "r"(mid));
+    return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
 }  // namespace quant

@@ -68,17 +68,6 @@ SV_HD_CALL long long rows_units_before(const RowsShape &p, const RowsSeq &s, int
     return u;
 }
 
-// The last item whose first unit is at most v (units of one group of heads).
-SV_HD int rows_item_at(const RowsShape &p, const RowsSeq &s, long long v) {
-    int lo = 0, hi = s.items - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (rows_units_before(p, s, mid) <= v) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
-}
-
 // CTAs that take part, of `grid`.
 SV_HD int rows_ctas(long long U, int grid) {
     const long long want = U / kRowsMinUnits > 0 ? U / kRowsMinUnits : 1;

@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const Ro
     };
     {
         RowsWalk walk;
-        plan_walk<kRT>(p, sh.warp_units, sh.before, tid, walk);
+        plan_walk<kRT>(p, sh.warp_units, sh.before, tid, 0, walk);
         if (tid == 0) {
             sh.walk = walk;
             sh.items[1].b = 0;

@@ -2,29 +2,31 @@
 // tensor cores: chains, draft trees and parts of prompts.
 //
 // An item is the rows of some tokens of one sequence and the heads of them that
-// share K/V, N <= 64 columns (a multiple of 16); for each 128-slot tile of K/V
+// share K/V, N = 32, 48 or 64 columns; for each 128-slot tile of K/V
 //     S = codes_k Q^T           (128 slots x N, f32 in tensor memory; codes less 8, exact in bf16)
 //     s = step_k S + middle_k sum(q) - u, in log2 units
-//     P = 2^s step_v, rounded to f16; l += 2^s; z += 2^s middle_v
-//     O^T += codes_v^T P        (D dims x N, f32 in tensor memory; codes less 8, exact in f16)
-// and out = (O + z) / l.  A column's u moves only when some P would pass 2^12, so
-// that f16 holds P to 2^-12 of itself, or of 2^-14 of the largest where it is
-// smaller; nothing of the cache is rounded.
+//     P = 2^s 2^e, rounded to f16; l += 2^s
+//     O^T += (v 2^-e)^T P       (D dims x N, f32 in tensor memory; v 2^-e in f16)
+// and out = O / l.  e is the exponent of a slot's largest value of V, so that f16
+// holds its values to 2^-12 of themselves (below 2^-14 of the largest, to 2^-26 of
+// that); a column's u moves only when some P would pass 2^12.  K is not rounded.
 //
-// Why slots are the rows of S: a slot's steps and middles are then numbers of the
-// thread that has the slot.  With queries as rows every thread would need all of a
-// tile's, four floats a score from shared memory, which set the pace (a chunk of 2048
-// rows after 14336 slots 640 us).  What a column needs, its u and the sum of its q,
-// is two floats, for few columns.
+// Why slots are the rows of S: a slot's step, middle and exponent are then numbers
+// of the thread that has the slot.  With queries as rows every thread would need
+// all of a tile's from shared memory, which set the pace (a chunk of 2048 rows
+// after 14336 slots 640 us).  What a column needs, its u and the sum of its q, is
+// two floats, for few columns.
 //
-// Warps: 0-3 and 4-7 softmax, half of the columns each, a thread a slot; at an
-// item's end a thread a dim.  8-11 turn a tile's codes into operands, a thread a
-// slot: K's to tensor memory, V's to shared memory.  12 loads codes, parameters and
-// queries, 13 issues the products, 14 walks the work list (sv_quant_list.h).
-// An item cut by a CTA's range leaves its share in the workspace; the softmax
-// group that arrives last adds the shares of its columns in their order.  Every wait
-// is bounded; the warps of a softmax group agree on a wait that gave up before any
-// of them leaves the group's barriers.
+// The softmax groups, warps 0-3 and 4-7, take the tiles in turn, a thread a slot,
+// each with its own u, l and O, so that one's exponentials run beside the other's
+// loads; at an item's end the group of its first tile brings the two together, a
+// thread a dim.  Warps 8-11 turn a tile's codes into operands, a thread a slot:
+// K's to tensor memory, V's to shared memory.  12 loads codes, parameters and
+// queries, 13 issues the products, 14 walks the work list (sv_quant_list.h).  An
+// item cut by a CTA's range leaves its share in the workspace; the CTA that arrives
+// last adds the shares up in their order.  Every wait is bounded; the warps of a
+// softmax group agree on a wait that gave up before any of them leaves the group's
+// barriers.
 #include "sv_attn_common.cuh"
 #include "sv_chunk.cuh"
 #include "sv_quant.cuh"
@@ -37,9 +39,9 @@ namespace {
 
 constexpr int kTT = 512;                       // threads
 constexpr int kN = 64;                         // columns of an item at most
-constexpr uint32_t kTCols = 512, kTColS = 0, kTColO = 128, kTColK = 256;  // two of each, 64 columns apart
+constexpr uint32_t kTCols = 512, kTColS = 0, kTColO = 128, kTColK = 256;  // one a group each, 64 columns apart
 
-constexpr int kTRegsSoftmax = 152, kTRegsOther = 104;  // 256 x 152 + 256 x 104 = 512 x 128
+constexpr int kTRegsSoftmax = 168, kTRegsOther = 88;  // 256 x 168 + 256 x 88 = 512 x 128
 
 template <int D>
 constexpr int kVTile = kBK * D * 2;            // V's operand
@@ -50,21 +52,22 @@ constexpr int kQTile = kQBox * (D / 64);
 template <int D>
 constexpr int kTRaw = kBK * (D + 8);           // a tile's codes and parameters
 template <int D>
-constexpr int kTRawStages = D == 128 ? 5 : 8;
+constexpr int kTRawStages = D == 128 ? 4 : 7;
 
 struct TShared {
     uint64_t raw_full[8], raw_empty[8];
     uint64_t k_full[2], k_empty[2], v_full[2], pv_done[2];
     uint64_t s_full[2], s_empty[2], p_full[2];
-    uint64_t q_full[2], q_empty[2], o_full[2], o_empty[2];
+    uint64_t q_full[2], q_empty[2], o_full[2], o_empty[2], x_full;
     uint64_t item_full[kItems], item_empty[kItems];
     uint64_t fin;
     RowsItem items[kItems];
-    uint2 slots[4][kBK];               // a tile's slots: K's parameters, V's
-    float4 col[kN / 2];                // of two columns: the sums of q, the u negated
-    float most[2][4][32];
-    float2 sums[2][4][32];             // (l, z)
-    float2 f[2][16];                   // what a column's sums are to be multiplied by
+    uint2 slots[4][kBK];               // a tile's slots: K's parameters, 2^e
+    float4 col[2][kN / 2];             // a group's, of two columns: the sums of q, the u negated
+    float part[2][4][kN];              // a warp's maxima or sums
+    float2 f[2][kN / 2];               // what the columns are to be multiplied by
+    float2 other[kN];                  // the (u, l) of the group that does not finish the item
+    float2 w[2][kN];                   // what the two groups' O are to be multiplied by
     unsigned long long above[2][kTreeNodes];
     long long warp_units[kTT / 32];
     long long before[kTT];
@@ -135,19 +138,23 @@ __device__ __forceinline__ bool group_any(int group, bool x) {
 }
 __device__ __forceinline__ void group_sync(int group) { named_bar_sync(1 + group, 128); }
 
-__device__ __forceinline__ void tmem_ld8(uint32_t at, float2 (&x)[4]) {
-    uint32_t r[8];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+// 16 columns of tensor memory as eight pairs.
+__device__ __forceinline__ void tmem_ld16(uint32_t at, float2 *x) {
+    uint32_t r[16];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
                  : "r"(at));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+    for (int i = 0; i < 8; ++i) x[i] = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
 }
-__device__ __forceinline__ void tmem_st8(uint32_t at, const float2 (&x)[4]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at),
-                 "r"(__float_as_uint(x[0].x)), "r"(__float_as_uint(x[0].y)), "r"(__float_as_uint(x[1].x)),
-                 "r"(__float_as_uint(x[1].y)), "r"(__float_as_uint(x[2].x)), "r"(__float_as_uint(x[2].y)),
-                 "r"(__float_as_uint(x[3].x)), "r"(__float_as_uint(x[3].y))
+__device__ __forceinline__ void tmem_st16(uint32_t at, const float2 *x) {
+    uint32_t r[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[2 * i] = __float_as_uint(x[i].x), r[2 * i + 1] = __float_as_uint(x[i].y);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+                 "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
                  : "memory");
 }
 
@@ -199,18 +206,19 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
             mbar_init(&sh->v_full[i], 4);
             mbar_init(&sh->pv_done[i], 1);
             mbar_init(&sh->s_full[i], 1);
-            mbar_init(&sh->s_empty[i], 8);
-            mbar_init(&sh->p_full[i], 8);
+            mbar_init(&sh->s_empty[i], 4);
+            mbar_init(&sh->p_full[i], 4);
             mbar_init(&sh->q_full[i], 1);
             mbar_init(&sh->q_empty[i], 1 + 2);  // the products, the softmax groups
             mbar_init(&sh->o_full[i], 1);
-            mbar_init(&sh->o_empty[i], 8);
+            mbar_init(&sh->o_empty[i], 4);
         }
 #pragma unroll 1
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&sh->item_full[i], 1);
             mbar_init(&sh->item_empty[i], 8 + 4 + 2);
         }
+        mbar_init(&sh->x_full, 1);
         mbar_init(&sh->fin, 1);
         sh->abort_flag = 0;
         fence_mbar_init();
@@ -225,7 +233,7 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
     if (tid == 0) sh->call = begin_call(p.call);
     RowsWalk walk;
     tc::fence_before();
-    plan_walk<kTT>(p, sh->warp_units, sh->before, tid, walk);  // (two barriers of the CTA)
+    plan_walk<kTT>(p, sh->warp_units, sh->before, tid, 14, walk);  // (two barriers of the CTA)
     tc::fence_after();
     const uint32_t tbase = sh->tmem;
     volatile int *abort_flag = &sh->abort_flag;
@@ -233,11 +241,14 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
     const bool aligned = (base_u32 & 1023u) == 0;  // (always: nothing else takes shared memory here)
 
     if (warp < 8) {
-        // ===================== softmax: a thread a slot, the columns of its group
+        // ===================== softmax: a thread a slot, every second tile
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTRegsSoftmax));
         const int group = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t tl = tbase + ((uint32_t)(quarter * 32) << 16);
-        uint32_t tile = 0;  // tiles of the CTA before this item
+        const uint32_t s_at = tl + kTColS + group * kN, o_at = tl + kTColO + group * kN;
+        float4 *const col = sh->col[group];
+        uint8_t *const pto = pbuf + group * kPTile;
+        uint32_t tile = 0, o_ph = 0, x_ph = 0;  // tiles of the CTA before this item
         bool bad = !aligned;
 #pragma unroll 1
         for (uint32_t k = 0;; ++k) {
@@ -249,22 +260,20 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
             }
             const RowsItem it = sh->items[slot_i];
             if (it.b < 0) break;
-            const int cols = it.ntok * p.Gs;
-            const int c0 = group * (N / 2);                      // the group's first column
-            const int own0 = it.pos0 - (it.row0 - it.seq_row0);                    // slot of the sequence's first new row
-            const int all_hi = p.parents ? own0 : it.pos0 + 1;                     // below, and from all_lo on, every row sees a slot
+            const int own0 = it.pos0 - (it.row0 - it.seq_row0);  // slot of the sequence's first new row
+            const int all_hi = p.parents ? own0 : it.pos0 + 1;   // below, and from all_lo on, every row sees a slot
             const int all_lo = p.rows.window > 0 ? it.pos0 + it.ntok - p.rows.window : 0;
             bad = !twait_here(&sh->q_full[k & 1], (k >> 1) & 1);
-            if (!bad && r < N / 2) {  // the sums of this group's columns of Q
+            if (!bad && r < N) {  // the columns' sums of Q
                 const uint8_t *q = qbuf + (k & 1) * kQTile<D>;
                 float2 s = make_float2(0.f, 0.f);
 #pragma unroll 4
                 for (int c = 0; c < D / 8; ++c) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(q + (c >> 3) * kQBox + t_sw128(c0 + r, c & 7));
+                    const uint4 x = *reinterpret_cast<const uint4 *>(q + (c >> 3) * kQBox + t_sw128(r, c & 7));
                     s = __fadd2_rn(s, __fadd2_rn(__fadd2_rn(make_float2(bf16_lo(x.x), bf16_hi(x.x)), make_float2(bf16_lo(x.y), bf16_hi(x.y))),
                                                  __fadd2_rn(make_float2(bf16_lo(x.z), bf16_hi(x.z)), make_float2(bf16_lo(x.w), bf16_hi(x.w)))));
                 }
-                float *to = reinterpret_cast<float *>(&sh->col[(c0 + r) >> 1]) + (r & 1);
+                float *to = reinterpret_cast<float *>(&col[r >> 1]) + (r & 1);
                 to[0] = s.x + s.y;
                 to[2] = -kUnset;
             }
@@ -279,172 +288,179 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
                 break;
             }
             if (r == 0) mbar_arrive(&sh->q_empty[k & 1]);
-            float2 l[4 * kCh], z[4 * kCh];
+            float2 l[N / 2];
 #pragma unroll
-            for (int i = 0; i < 4 * kCh; ++i) l[i] = z[i] = make_float2(0.f, 0.f);
-            const uint32_t o_at = tl + kTColO + (k & 1) * kN + c0;
+            for (int i = 0; i < N / 2; ++i) l[i] = make_float2(0.f, 0.f);
+            const int j0 = (group ^ (int)tile) & 1;  // this group's first tile of the item
 #pragma unroll 1
-            for (int j = 0; j < it.n; ++j) {
-                const uint32_t g = tile + j, buf = g & 1, ph = (g >> 1) & 1;
+            for (int j = j0; j < it.n; j += 2) {
+                const uint32_t g = tile + j, ph = (g >> 1) & 1;
                 const int slot0 = (it.kt0 + j) * kBK, slot = slot0 + r;
-                bad = !twait_here(&sh->s_full[buf], ph) || !twait_here(&sh->pv_done[buf], ph ^ 1);
+                bad = bad || !twait_here(&sh->s_full[group], ph);
                 tc::fence_after();
                 const uint2 par = sh->slots[g & 3][r];
                 const float ks = bf16_lo(par.x) * p.scale_log2;
                 const float km = __fmaf_rn(8.f, bf16_lo(par.x), bf16_hi(par.x)) * p.scale_log2;
-                const float vs = bf16_lo(par.y), vm = __fmaf_rn(8.f, vs, bf16_hi(par.y));
-                const float lv = fmaxf(lg2_approx(fabsf(vs)), kLeast);  // log2 of what P gets from the step
-                const float2 ks2 = make_float2(ks, ks), km2 = make_float2(km, km);
-                uint32_t sees = ~0u;  // a bit a column of the group
-                if (slot0 + kBK > all_hi || slot0 < all_lo) {
-                    if (p.parents) {
-                        const int node = slot - own0;
-                        if (node >= 0) {
-                            sees = 0;
-#pragma unroll 1
-                            for (int c = 0; c < N / 2; ++c) {
-                                const int tk = min((int)sh->tok[c0 + c], it.ntok - 1);
-                                if (node < kTreeNodes && (sh->above[group][tk] >> node & 1)) sees |= 1u << c;
-                            }
-                        }
-                    } else {  // tokens slot - pos0 .. slot - pos0 + window - 1
-                        const long long from = (long long)(slot - it.pos0) * p.Gs - c0;
-                        const long long to = p.rows.window > 0 ? from + (long long)p.rows.window * p.Gs : 32;
-                        const uint32_t under = from >= 32 ? ~0u : from <= 0 ? 0u : (1u << from) - 1u;
-                        const uint32_t below = to >= 32 ? ~0u : to <= 0 ? 0u : (1u << to) - 1u;
-                        sees = below & ~under;
-                    }
-                }
-                float2 x[kCh][4];
-                const uint32_t s_at = tl + kTColS + buf * kN + c0;
+                const float w = __uint_as_float(par.y), e = (float)((int)(par.y >> 23) - 127);  // 2^e, e
+                const float2 ks2 = make_float2(ks, ks), km2 = make_float2(km, km), w2 = make_float2(w, w);
+                const bool masked = slot0 + kBK > all_hi || slot0 < all_lo;
+                float2 x[N / 2];
                 auto scores = [&](bool less) __attribute__((always_inline)) {  // less: less u
 #pragma unroll
-                    for (int ch = 0; ch < kCh; ++ch) {
-                        tmem_ld8(s_at + 8 * ch, x[ch]);
-                    }
+                    for (int ch = 0; ch < N / 16; ++ch) tmem_ld16(s_at + 16 * ch, x + 8 * ch);
                     tc::wait_ld();
 #pragma unroll
-                    for (int ch = 0; ch < kCh; ++ch) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float4 c4 = sh->col[(c0 >> 1) + 4 * ch + i];
-                            float2 t = less ? make_float2(c4.z, c4.w) : make_float2(0.f, 0.f);
-                            t = __ffma2_rn(km2, make_float2(c4.x, c4.y), t);
-                            x[ch][i] = __ffma2_rn(x[ch][i], ks2, t);
-                        }
+                    for (int i = 0; i < N / 2; ++i) {
+                        const float4 c4 = col[i];
+                        const float2 t = less ? make_float2(c4.z, c4.w) : make_float2(0.f, 0.f);
+                        x[i] = __ffma2_rn(x[i], ks2, __ffma2_rn(km2, make_float2(c4.x, c4.y), t));
                     }
-                    if (sees != ~0u) {
+                    if (masked) {
+                        unsigned long long sees = ~0ull;  // a bit a column
+                        if (p.parents) {
+                            const int node = slot - own0;
+                            if (node >= 0) {
+                                sees = 0;
+#pragma unroll 1
+                                for (int c = 0; c < N; ++c) {
+                                    const int tk = min((int)sh->tok[c], it.ntok - 1);
+                                    if (node < kTreeNodes && (sh->above[group][tk] >> node & 1)) sees |= 1ull << c;
+                                }
+                            }
+                        } else {  // tokens slot - pos0 .. slot - pos0 + window - 1
+                            const long long from = (long long)(slot - it.pos0) * p.Gs;
+                            const long long to = p.rows.window > 0 ? from + (long long)p.rows.window * p.Gs : 64;
+                            const unsigned long long under = from >= 64 ? ~0ull : from <= 0 ? 0ull : (1ull << from) - 1ull;
+                            const unsigned long long below = to >= 64 ? ~0ull : to <= 0 ? 0ull : (1ull << to) - 1ull;
+                            sees = below & ~under;
+                        }
+                        const uint32_t half[2] = {(uint32_t)sees, (uint32_t)(sees >> 32)};
 #pragma unroll
-                        for (int i = 0; i < 4 * kCh; ++i) {
-                            if (!(sees >> (2 * i) & 1)) x[i >> 2][i & 3].x = kNegInf;
-                            if (!(sees >> (2 * i + 1) & 1)) x[i >> 2][i & 3].y = kNegInf;
+                        for (int i = 0; i < N / 2; ++i) {
+                            if (!(half[i >> 4] >> (2 * i & 31) & 1)) x[i].x = kNegInf;
+                            if (!(half[i >> 4] >> ((2 * i & 31) + 1) & 1)) x[i].y = kNegInf;
                         }
                     }
                 };
                 scores(true);
-                float top = kNegInf;
+                float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
-                for (int ch = 0; ch < kCh; ++ch) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) top = fmaxf(fmaxf(top, x[ch][i].x), x[ch][i].y);
-                }
-                if (group_any(group, bad || top + lv > kRoom)) {
+                for (int i = 0; i < N / 2; ++i) top[i & 3] = fmaxf(fmaxf(top[i & 3], x[i].x), x[i].y);
+                if (group_any(group, bad || fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) + e > kRoom)) {
                     if (group_any(group, bad)) {
                         bad = true;
                         break;
                     }
                     // some column's u moves up to its largest P (the first tile's do)
                     scores(false);
-                    {
+#pragma unroll
+                    for (int h = 0; h < (N + 31) / 32; ++h) {
                         float v[32];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            v[2 * i] = i < 4 * kCh ? x[i / 4 % kCh][i & 3].x + lv : kNegInf;
-                            v[2 * i + 1] = i < 4 * kCh ? x[i / 4 % kCh][i & 3].y + lv : kNegInf;
+                            const float2 y = 16 * h + i < N / 2 ? x[(16 * h + i) % (N / 2)] : make_float2(kNegInf, kNegInf);
+                            v[2 * i] = y.x + e;
+                            v[2 * i + 1] = y.y + e;
                         }
-                        sh->most[group][quarter][lane] = across<true>(v, lane);
+                        sh->part[group][quarter][32 * h + lane] = across<true>(v, lane);
                     }
                     group_sync(group);
-                    if (quarter == 0 && lane < N / 2) {
-                        const float a = fmaxf(fmaxf(sh->most[group][0][lane], sh->most[group][1][lane]),
-                                              fmaxf(sh->most[group][2][lane], sh->most[group][3][lane]));
-                        float *nu = reinterpret_cast<float *>(&sh->col[(c0 + lane) >> 1]) + 2 + (lane & 1);
+                    if (r < N) {
+                        const float a = fmaxf(fmaxf(sh->part[group][0][r], sh->part[group][1][r]),
+                                              fmaxf(sh->part[group][2][r], sh->part[group][3][r]));
+                        float *nu = reinterpret_cast<float *>(&col[r >> 1]) + 2 + (r & 1);
                         const float u = -*nu;
                         const bool up = a > u + kRoom;
-                        reinterpret_cast<float *>(sh->f[group])[lane] = up ? ex2_approx(u - a) : 1.f;
+                        reinterpret_cast<float *>(sh->f[group])[r] = up ? ex2_approx(u - a) : 1.f;
                         if (up) *nu = -a;
                     }
-                    const uint32_t before = g - 1;  // the products that added to O last
-                    if (j > 0) bad = !twait_here(&sh->pv_done[before & 1], (before >> 1) & 1);
+                    // (the products that added to O last)
+                    if (j > j0) bad = !twait_here(&sh->pv_done[group], ph ^ 1);
                     if (group_any(group, bad)) {
                         bad = true;
                         break;
                     }
                     tc::fence_after();
 #pragma unroll
-                    for (int ch = 0; ch < kCh; ++ch) {
-                        float2 f[4];
+                    for (int i = 0; i < N / 2; ++i) l[i] = __fmul2_rn(l[i], sh->f[group][i]);
+                    if (j > j0) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            f[i] = sh->f[group][4 * ch + i];
-                            l[4 * ch + i] = __fmul2_rn(l[4 * ch + i], f[i]);
-                            z[4 * ch + i] = __fmul2_rn(z[4 * ch + i], f[i]);
-                        }
-                        if (j > 0) {
-                            float2 o[4];
-                            tmem_ld8(o_at + 8 * ch, o);
+                        for (int ch = 0; ch < N / 16; ++ch) {
+                            tmem_ld16(o_at + 16 * ch, x);
                             tc::wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) o[i] = __fmul2_rn(o[i], f[i]);
-                            tmem_st8(o_at + 8 * ch, o);
+                            for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(x[i], sh->f[group][8 * ch + i]);
+                            tmem_st16(o_at + 16 * ch, x);
                         }
+                        tc::wait_st();
                     }
-                    tc::wait_st();
                     scores(true);
                 }
                 tc::fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh->s_empty[buf]);
-                const float2 vs2 = make_float2(vs, vs), vm2 = make_float2(vm, vm);
-                uint8_t *const to = pbuf + buf * kPTile + r * 128;
+                if (lane == 0) mbar_arrive(&sh->s_empty[group]);
+                bad = !twait_here(&sh->pv_done[group], ph ^ 1);  // (P's place; told at the next vote)
 #pragma unroll
-                for (int ch = 0; ch < kCh; ++ch) {
-                    uint32_t w[4];
+                for (int ch = 0; ch < N / 8; ++ch) {
+                    uint32_t y[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int n = 4 * ch + i;
-                        const float2 e = make_float2(ex2_approx(x[ch][i].x), ex2_approx(x[ch][i].y));
-                        l[n] = __fadd2_rn(l[n], e);
-                        z[n] = __ffma2_rn(e, vm2, z[n]);
-                        const float2 y = __fmul2_rn(e, vs2);
-                        w[i] = t_pack_f16x2(y.x, y.y);
+                        const float2 z = make_float2(ex2_approx(x[n].x), ex2_approx(x[n].y));
+                        l[n] = __fadd2_rn(l[n], z);
+                        const float2 q = __fmul2_rn(z, w2);
+                        y[i] = t_pack_f16x2(q.x, q.y);
                     }
-                    *reinterpret_cast<uint4 *>(to + ((((c0 >> 3) + ch) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4 *>(pto + r * 128 + ((ch ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
                 }
                 tc::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh->p_full[buf]);
+                if (lane == 0) mbar_arrive(&sh->p_full[group]);
             }
-            if (bad) break;
-            tile += it.n;
-            // ---- the columns' sums over the slots, then a thread a dim
-            bad = !twait_here(&sh->o_full[k & 1], (k >> 1) & 1);
-            {
+            // ---- the columns' sums over the slots
+            const bool mine = j0 == 0, both = it.n > 1;  // whether this group finishes the item; whether the other has a share
+            if (j0 < it.n) {
+                bad = bad || !twait_here(&sh->o_full[group], o_ph);
+                o_ph ^= 1;
+            }
+#pragma unroll
+            for (int h = 0; h < (N + 31) / 32; ++h) {
                 float v[32];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[2 * i] = i < 4 * kCh ? l[i % (4 * kCh)].x : 0.f, v[2 * i + 1] = i < 4 * kCh ? l[i % (4 * kCh)].y : 0.f;
-                const float ls = across<false>(v, lane);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v[2 * i] = i < 4 * kCh ? z[i % (4 * kCh)].x : 0.f, v[2 * i + 1] = i < 4 * kCh ? z[i % (4 * kCh)].y : 0.f;
-                sh->sums[group][quarter][lane] = make_float2(ls, across<false>(v, lane));
+                for (int i = 0; i < 16; ++i) {
+                    const float2 y = 16 * h + i < N / 2 ? l[(16 * h + i) % (N / 2)] : make_float2(0.f, 0.f);
+                    v[2 * i] = y.x;
+                    v[2 * i + 1] = y.y;
+                }
+                sh->part[group][quarter][32 * h + lane] = across<false>(v, lane);
             }
+            tile += it.n;
             if (group_any(group, bad)) {
                 bad = true;
                 break;
             }
             tc::fence_after();
+            float lsum = 0.f, u = 0.f;
+            if (r < N) {
+                lsum = (sh->part[group][0][r] + sh->part[group][1][r]) + (sh->part[group][2][r] + sh->part[group][3][r]);
+                u = -(reinterpret_cast<const float *>(&col[r >> 1])[2 + (r & 1)]);
+            }
+            if (!mine) {
+                x_ph ^= both ? 1 : 0;
+                if (both && r < N) sh->other[r] = make_float2(u, lsum);
+                tc::fence_before();
+                group_sync(group);
+                if (both && r == 0) mbar_arrive(&sh->x_full);
+                if (lane == 0) mbar_arrive(&sh->item_empty[slot_i]);
+                continue;
+            }
+            if (both) {
+                bad = !twait_here(&sh->x_full, x_ph);
+                x_ph ^= 1;
+                tc::fence_after();
+            }
             const bool whole = it.nc == 1;
-            const int part = (int)blockIdx.x * 2 + (it.ci == 0 ? 1 : 0);
+            const int part = (int)blockIdx.x * 2 + (it.ci == 0 ? 1 : 0), cols = it.ntok * p.Gs;
             const int hpart = it.h % p.parts * p.Gs, heads = min(p.Gs, p.G - hpart);
             const int head0 = it.h / p.parts * p.G + hpart;
             // where a column's row goes; -1: it is padding
@@ -452,54 +468,59 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
                 const int tk = sh->tok[c], hd = c - tk * p.Gs;
                 return c < cols && hd < heads ? (long long)(it.row0 + tk) * p.Hq + head0 + hd : -1;
             };
-            float lsum = 0.f, zsum = 0.f;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                lsum += sh->sums[group][w][lane].x;
-                zsum += sh->sums[group][w][lane].y;
+            if (r < N) {
+                const float2 y = both ? sh->other[r] : make_float2(kUnset, 0.f);
+                const float M = fmaxf(u, y.x), f0 = ex2_approx(u - M), f1 = ex2_approx(y.x - M);
+                const float sum = lsum * f0 + y.y * f1, inv = whole ? 1.f / sum : 1.f;
+                sh->w[group][r] = make_float2(f0 * inv, f1 * inv);
+                const long long row = out_row(r);
+                if (!whole) __stcg(reinterpret_cast<float2 *>(p.part_ml) + (size_t)part * kRowsCols + r, make_float2(M, sum));
+                else if (p.lse && row >= 0) p.lse[row] = M * kLn2 + logf(sum);
             }
-            const float inv = whole ? 1.f / lsum : 1.f;
-            if (quarter == 0 && lane < N / 2) {
-                const float u = -(reinterpret_cast<const float *>(&sh->col[(c0 + lane) >> 1])[2 + (lane & 1)]);
-                const long long row = out_row(c0 + lane);
-                if (whole) {
-                    if (p.lse && row >= 0) p.lse[row] = u * kLn2 + logf(lsum);
-                } else {
-                    __stcg(reinterpret_cast<float2 *>(p.part_ml) + (size_t)part * kRowsCols + c0 + lane, make_float2(u, lsum));
-                }
+            if (group_any(group, bad)) {
+                bad = true;
+                break;
             }
-#pragma unroll
-            for (int ch = 0; ch < kCh; ++ch) {
-                float2 o[4];
+            const uint32_t o2_at = tl + kTColO + (group ^ 1) * kN;
+#pragma unroll 1
+            for (int ch = 0; ch < N / 16; ++ch) {  // 16 columns of a dim
+                float2 a[8], b[8];
                 __syncwarp();
-                tmem_ld8(o_at + 8 * ch, o);
+                tmem_ld16(o_at + 16 * ch, a);
+                if (both) tmem_ld16(o2_at + 16 * ch, b);
                 tc::wait_ld();
+                if (r < D) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int c = 8 * ch + i;
-                    const float a = i & 1 ? o[i >> 1].y : o[i >> 1].x;
-                    const float y = (a + __shfl_sync(0xffffffffu, zsum, c)) * __shfl_sync(0xffffffffu, inv, c);
-                    const long long row = out_row(c0 + c);
-                    if (row < 0 || r >= D) continue;
-                    if (whole) p.out[row * D + r] = (uint16_t)pack_bf16x2(y, 0.f);
-                    else __stcg(p.part_o + ((size_t)part * kRowsCols + c0 + c) * D + r, y);
+                    for (int i = 0; i < 16; ++i) {
+                        const int c = 16 * ch + i;
+                        const float2 f = sh->w[group][c];
+                        float y = (i & 1 ? a[i >> 1].y : a[i >> 1].x) * f.x;
+                        if (both) y = __fmaf_rn(i & 1 ? b[i >> 1].y : b[i >> 1].x, f.y, y);
+                        if (whole) *reinterpret_cast<uint16_t *>(pto + (c * D + r) * 2) = (uint16_t)pack_bf16x2(y, 0.f);
+                        else __stcg(p.part_o + ((size_t)part * kRowsCols + c) * D + r, y);
+                    }
                 }
             }
             tc::fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&sh->o_empty[k & 1]);
+            if (!whole) __threadfence();
+            group_sync(group);
+            if (lane == 0) {  // O may start over
+                mbar_arrive(&sh->o_empty[group]);
+                if (both) mbar_arrive(&sh->o_empty[group ^ 1]);
                 mbar_arrive(&sh->item_empty[slot_i]);
             }
-            if (whole) {
-                group_sync(group);  // (the columns' numbers are read until here)
-                continue;
+            if (whole) {  // rows by 16 bytes, through the place of P
+#pragma unroll 1
+                for (int i = r; i < N * (D / 8); i += 128) {
+                    const int c = i / (D / 8), piece = i % (D / 8);
+                    const long long row = out_row(c);
+                    if (row >= 0) *reinterpret_cast<uint4 *>(p.out + row * D + piece * 8) = *reinterpret_cast<const uint4 *>(pto + (c * D + piece * 8) * 2);
+                }
+                continue;  // (the next item's first vote comes before the next P)
             }
-            // ---- an item shared by CTAs: the group that arrives last adds the shares of its columns up, in their order
-            __threadfence();
-            group_sync(group);
+            // ---- an item shared by CTAs: the one that arrives last adds the shares up, in their order
             if (r == 0) {
-                int *ctr = p.counters + rows_counter(sh->call, it.c_first) + group;
+                int *ctr = p.counters + rows_counter(sh->call, it.c_first);
                 int before_me;
                 asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before_me) : "l"(ctr) : "memory");
                 sh->last[group] = before_me == it.nc - 1;
@@ -508,23 +529,23 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
             if (!sh->last[group]) continue;
             __threadfence();
 #pragma unroll 1
-            for (int i = r; i < N / 2 * (D / 4); i += 128) {
-                const int c = c0 + i / (D / 4), dim = i % (D / 4) * 4;
+            for (int i = r; i < N * (D / 8); i += 128) {
+                const int c = i / (D / 8), dim = i % (D / 8) * 8;
                 const long long row = out_row(c);
                 if (row < 0) continue;
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                float M = kUnset, sum = 0.f;
+                float acc[8] = {}, M = kUnset, sum = 0.f;
                 constexpr int kAhead = 4;
 #pragma unroll 1
                 for (int k0 = 0; k0 < it.nc; k0 += kAhead) {
                     float2 ml[kAhead];
-                    float4 a[kAhead];
+                    float4 a[kAhead], b[kAhead];
 #pragma unroll
                     for (int q = 0; q < kAhead; ++q) {
                         const int m = min(k0 + q, it.nc - 1);
                         const size_t from = (size_t)(2 * (it.c_first + m) + (m == 0 ? 1 : 0)) * kRowsCols + c;
                         ml[q] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml) + from);
                         a[q] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + from * D + dim));
+                        b[q] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + from * D + dim) + 1);
                     }
 #pragma unroll
                     for (int q = 0; q < kAhead; ++q) {
@@ -532,14 +553,15 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
                         const float Mn = fmaxf(M, ml[q].x), f = ex2_approx(M - Mn), w = ex2_approx(ml[q].x - Mn);
                         M = Mn;
                         sum = sum * f + ml[q].y * w;
-                        acc.x = __fmaf_rn(a[q].x, w, acc.x * f);
-                        acc.y = __fmaf_rn(a[q].y, w, acc.y * f);
-                        acc.z = __fmaf_rn(a[q].z, w, acc.z * f);
-                        acc.w = __fmaf_rn(a[q].w, w, acc.w * f);
+                        const float y[8] = {a[q].x, a[q].y, a[q].z, a[q].w, b[q].x, b[q].y, b[q].z, b[q].w};
+#pragma unroll
+                        for (int z = 0; z < 8; ++z) acc[z] = __fmaf_rn(y[z], w, acc[z] * f);
                     }
                 }
                 const float in = 1.f / sum;
-                *reinterpret_cast<uint2 *>(p.out + row * D + dim) = make_uint2(pack_bf16x2(acc.x * in, acc.y * in), pack_bf16x2(acc.z * in, acc.w * in));
+                *reinterpret_cast<uint4 *>(p.out + row * D + dim) =
+                    make_uint4(pack_bf16x2(acc[0] * in, acc[1] * in), pack_bf16x2(acc[2] * in, acc[3] * in),
+                               pack_bf16x2(acc[4] * in, acc[5] * in), pack_bf16x2(acc[6] * in, acc[7] * in));
                 if (p.lse && dim == 0) p.lse[row] = M * kLn2 + logf(sum);
             }
         }
@@ -580,7 +602,14 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
                         c[i] = *reinterpret_cast<const uint4 *>(from + r * kRow + ((i + turn) & (kPieces - 1)) * 16);
                     if (!(ok = twait(&sh->k_empty[buf], ph ^ 1))) break;
                     tc::fence_after();
-                    sh->slots[g & 3][r] = make_uint2(seen ? par[r] : 0u, seen ? par[kBK + r] : 0u);
+                    // V's values times 2^-e, below 2
+                    const uint32_t vpar = seen ? par[kBK + r] : 0u;
+                    const float vstep = bf16_lo(vpar), vmid = __fmaf_rn(8.f, vstep, bf16_hi(vpar));
+                    const uint32_t most = __float_as_uint(__fmaf_rn(8.f, fabsf(vstep), fabsf(vmid))) >> 23;
+                    const uint32_t e = min(max(most, (uint32_t)(127 + (int)kLeast)), 253u);  // the exponent, and 127
+                    const float down = __uint_as_float((254u - e) << 23);
+                    const uint32_t step2 = t_pack_f16x2(vstep * down, vstep * down), mid2 = t_pack_f16x2(vmid * down, vmid * down);
+                    sh->slots[g & 3][r] = make_uint2(seen ? par[r] : 0u, e << 23);
                     // (a thread's row in order: the pieces put back by selects, a bit of the turn at a time)
                     if constexpr (kPieces == 4) {
                         const bool one = turn & 1, two = turn & 2;
@@ -630,7 +659,7 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
                             *reinterpret_cast<uint4 *>(to + (piece >> 1) * kBox + ((((piece & 1) * 4 + q) ^ (r & 7)) << 4)) =
-                                quant::expand_f16(words[q]);
+                                quant::scaled_f16(words[q], step2, mid2);
                     }
                     tc::fence_proxy_async_smem();
                     __syncwarp();
@@ -715,23 +744,26 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
             const uint64_t desc_q = tc::smem_desc(base_u32 + 2 * (kVTile<D> + kPTile), 16, 1024);
             uint32_t g = 0;
             bool ok = aligned;
-            // the tile whose O is still to be added to: flags, item
+            // the tile whose O is still to be added to: a group's first or last of its item
             bool live = false, first = false, end = false;
-            uint32_t lk = 0;
+            uint32_t o_ph = 3;  // a bit a group
             auto add_o = [&]() -> bool {
                 const uint32_t t = g - 1, buf = t & 1, ph = (t >> 1) & 1;
                 if (!twait(&sh->v_full[buf], ph) || !twait(&sh->p_full[buf], ph)) return false;
-                if (first && !twait(&sh->o_empty[lk & 1], ((lk >> 1) & 1) ^ 1)) return false;
+                if (first) {
+                    if (!twait(&sh->o_empty[buf], (o_ph >> buf) & 1)) return false;
+                    o_ph ^= 1u << buf;
+                }
                 tc::fence_after();
                 // f16 both, V's dims and P's columns contiguous
                 constexpr uint32_t idesc = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < kBK / 16; ++kk)
-                        tc::mma_bf16(tbase + kTColO + (lk & 1) * kN, desc_v + (uint64_t)(buf * (kVTile<D> >> 4) + kk * (2048 >> 4)),
+                        tc::mma_bf16(tbase + kTColO + buf * kN, desc_v + (uint64_t)(buf * (kVTile<D> >> 4) + kk * (2048 >> 4)),
                                      desc_p + (uint64_t)(buf * (kPTile >> 4) + kk * (2048 >> 4)), idesc, kk > 0 || !first ? 1u : 0u);
                     tc::commit(&sh->pv_done[buf]);
-                    if (end) tc::commit(&sh->o_full[lk & 1]);
+                    if (end) tc::commit(&sh->o_full[buf]);
                 }
                 __syncwarp();
                 return true;
@@ -767,9 +799,8 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
                     __syncwarp();
                     if (live && !(ok = add_o())) break;
                     live = true;
-                    first = j == 0;
-                    end = j == n - 1;
-                    lk = k;
+                    first = j < 2;
+                    end = j >= n - 2;
                     ++g;
                 }
             }

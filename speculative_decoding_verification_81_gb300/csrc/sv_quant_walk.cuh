@@ -103,9 +103,9 @@ static __device__ __noinline__ bool bad_sequence(const RowsParams &p, int sb, in
 }
 
 // This CTA's share of the list, by its kT threads together: units before each thread's sequences
-// (`before`, kT of them; warp_units, kT / 32), then the place where the share begins.
+// (`before`, kT of them; warp_units, kT / 32), then, for warp `who`, the place where the share begins.
 template <int kT>
-__device__ __forceinline__ void plan_walk(const RowsParams &p, long long *warp_units, long long *before, int tid, RowsWalk &w) {
+__device__ __forceinline__ void plan_walk(const RowsParams &p, long long *warp_units, long long *before, int tid, int who, RowsWalk &w) {
     const int lane = tid & 31, warp = tid >> 5;
     const int per = (p.B + kT - 1) / kT, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
     long long mine = 0;
@@ -139,7 +139,7 @@ __device__ __forceinline__ void plan_walk(const RowsParams &p, long long *warp_u
     w.ui = 0;
     w.h = w.i = 0;
     w.loaded = false;
-    if (has) {  // the last thread with at most u0 units before its sequences, then the sequence
+    if (has && warp == who) {  // the last thread with at most u0 units before its sequences, then the sequence
         int at = 0;
 #pragma unroll 1
         for (int i = lane; i < kT; i += 32) at += before[i] <= w.u0;
@@ -154,8 +154,21 @@ __device__ __forceinline__ void plan_walk(const RowsParams &p, long long *warp_u
                 w.loaded = true;
                 w.h = (int)quot(w.u0 - w.ui, head);
                 const long long v = w.u0 - w.ui - w.h * head;
-                w.i = rows_item_at(p.rows, w.seq, v);
-                w.ui += w.h * head + rows_units_before(p.rows, w.seq, w.i);
+                // the last item whose first unit is at most v: 32 candidates at a time
+                int span = w.seq.items, first = 0;
+                long long at_item = 0;
+#pragma unroll 1
+                while (span > 1) {
+                    const int step = (span + 31) / 32, c = first + lane * step;
+                    const bool in = lane * step < span;
+                    const long long u = in ? rows_units_before(p.rows, w.seq, c) : 0;
+                    const int hit = 31 - __clz(__ballot_sync(0xffffffffu, in && u <= v));  // (lane 0 always)
+                    at_item = __shfl_sync(0xffffffffu, u, hit);
+                    first += hit * step;
+                    span = min(step, span - hit * step);
+                }
+                w.i = first;
+                w.ui += w.h * head + at_item;
                 break;
             }
             w.ui += head * p.groups;
