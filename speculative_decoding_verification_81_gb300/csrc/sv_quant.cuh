@@ -31,6 +31,13 @@ __device__ __forceinline__ uint32_t centred(uint32_t pair) {
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(x), "r"(0x43084308u));
     return c;
 }
+// A word's eight codes as 1 + code / 16 in bf16, dims 0 .. 7 in order: a code in the first bits behind
+// the point, no subtraction.
+__device__ __forceinline__ uint4 sixteenths(uint32_t w) {
+    constexpr uint32_t kMask = 0x00780078u, kOne = 0x3f803f80u;
+    return make_uint4((w << 3 & kMask) | kOne, (w >> 1 & kMask) | kOne, (w >> 5 & kMask) | kOne, (w >> 9 & kMask) | kOne);
+}
+
 // The same as a pair of f16 (in the last bits of 1024).
 __device__ __forceinline__ uint32_t centred_f16(uint32_t pair) {
     const uint32_t x = (pair & 0x000f000fu) | 0x64006400u;

@@ -3,26 +3,30 @@
 //
 // An item is the rows of some tokens of one sequence and the heads of them that
 // share K/V, N = 32, 48 or 64 columns; for each 128-slot tile of K/V
-//     S = codes_k Q^T           (128 slots x N, f32 in tensor memory; codes less 8, exact in bf16)
-//     s = step_k S + middle_k sum(q) - u, in log2 units
-//     P = 2^s 2^e, rounded to f16; l += 2^s
-//     O^T += (v 2^-e)^T P       (D dims x N, f32 in tensor memory; v 2^-e in f16)
-// and out = O / l.  e is the exponent of a slot's largest value of V, so that f16
-// holds its values to 2^-12 of themselves (below 2^-14 of the largest, to 2^-26 of
-// that); a column's u moves only when some P would pass 2^12.  K is not rounded.
+//     S = (1 + codes_k / 16) Q^T + r sum(q) - i u   (128 slots x N, f32 in tensor memory)
+//     P = 2^(step S) 2^e, rounded to f16; l += 2^(step S)
+//     O^T += (v 2^-e)^T P                           (D dims x N, f32 in tensor memory)
+// and out = O / l.  step is 16 steps of the slot's K, scaled to log2 units, r what
+// its minimum adds in such steps and i the step's inverse: a column's sum of q and
+// its u enter the product as sixteen more dims, each number in three bf16 parts of
+// which the six largest products are taken (2^-24 of the whole is left out), so that
+// a score comes out of it but for one factor.  The codes are exact in bf16.  e is
+// the exponent of a slot's largest value of V, so that f16 holds its values to 2^-12
+// of themselves (below 2^-14 of the largest, to 2^-26 of that).  A column's u moves
+// only when some P would pass 2^12.
 //
-// Why slots are the rows of S: a slot's step, middle and exponent are then numbers
-// of the thread that has the slot.  With queries as rows every thread would need
-// all of a tile's from shared memory, which set the pace (a chunk of 2048 rows
-// after 14336 slots 640 us).  What a column needs, its u and the sum of its q, is
-// two floats, for few columns.
+// Why slots are the rows of S: a slot's step and exponent are then numbers of the
+// thread that has the slot.  With queries as rows every thread would need all of a
+// tile's from shared memory, which set the pace (a chunk of 2048 rows after 14336
+// slots 640 us).
 //
 // The softmax groups, warps 0-3 and 4-7, take the tiles in turn, a thread a slot,
 // each with its own u, l and O, so that one's exponentials run beside the other's
 // loads; at an item's end the group of its first tile brings the two together, a
 // thread a dim.  Warps 8-11 turn a tile's codes into operands, a thread a slot:
 // K's to tensor memory, V's to shared memory.  12 loads codes, parameters and
-// queries, 13 issues the products, 14 walks the work list (sv_quant_list.h).  An
+// queries, 13 issues the products, 14 walks the work list (sv_quant_list.h), 15
+// adds the sums of an item's queries to them.  An
 // item cut by a CTA's range leaves its share in the workspace; the CTA that arrives
 // last adds the shares up in their order.  Every wait is bounded; the warps of a
 // softmax group agree on a wait that gave up before any of them leaves the group's
@@ -40,13 +44,19 @@ namespace {
 constexpr int kTT = 512;                       // threads
 constexpr int kN = 64;                         // columns of an item at most
 constexpr uint32_t kTCols = 512, kTColS = 0, kTColO = 128, kTColK = 256;  // one a group each, 64 columns apart
+constexpr uint32_t kTColsK = 80;               // of K's operand: D / 2, and eight for the sixteen dims more
 
-constexpr int kTRegsSoftmax = 168, kTRegsOther = 88;  // 256 x 168 + 256 x 88 = 512 x 128
+// 256 x 184 + 256 x 72 = 256 x 168 + 256 x 88 = 512 x 128
+template <int kCh>
+constexpr int kTRegsSoftmax = kCh == 4 ? 184 : 168;
+template <int kCh>
+constexpr int kTRegsOther = 256 - kTRegsSoftmax<kCh>;
 
 template <int D>
 constexpr int kVTile = kBK * D * 2;            // V's operand
 constexpr int kPTile = kBK * kN * 2;
 constexpr int kQBox = kN * 128;                // 64 columns of 64 dims
+constexpr int kExt = kQBox;                    // the sixteen dims more, of two items' and two groups' columns
 template <int D>
 constexpr int kQTile = kQBox * (D / 64);
 template <int D>
@@ -58,14 +68,14 @@ struct TShared {
     uint64_t raw_full[8], raw_empty[8];
     uint64_t k_full[2], k_empty[2], v_full[2], pv_done[2];
     uint64_t s_full[2], s_empty[2], p_full[2];
-    uint64_t q_full[2], q_empty[2], o_full[2], o_empty[2], x_full;
+    uint64_t q_full[2], q_empty[2], ext_full[2], o_full[2], o_empty[2], x_full;
     uint64_t item_full[kItems], item_empty[kItems];
     uint64_t fin;
     RowsItem items[kItems];
-    uint2 slots[4][kBK];               // a tile's slots: K's parameters, 2^e
-    float4 col[2][kN / 2];             // a group's, of two columns: the sums of q, the u negated
+    float2 slots[4][kBK];              // a tile's slots: K's step, 2^e
+    float u[2][kN];                    // a group's columns'
     float part[2][4][kN];              // a warp's maxima or sums
-    float2 f[2][kN / 2];               // what the columns are to be multiplied by
+    float2 f[2][kN / 2], d[2][kN / 2]; // what a column's sums are to be multiplied by, what is to be added to its scores
     float2 other[kN];                  // the (u, l) of the group that does not finish the item
     float2 w[2][kN];                   // what the two groups' O are to be multiplied by
     unsigned long long above[2][kTreeNodes];
@@ -78,43 +88,28 @@ struct TShared {
 };
 
 template <int D>
-constexpr int kTSmem = 2 * (kVTile<D> + kPTile + kQTile<D>) + kTRawStages<D> * kTRaw<D> + (int)sizeof(TShared);
+constexpr int kTSmem = 2 * (kVTile<D> + kPTile + kQTile<D>) + kExt + kTRawStages<D> * kTRaw<D> + (int)sizeof(TShared);
 static_assert(kTSmem<128> <= 227 * 1024 && kTSmem<64> <= 227 * 1024, "shared memory");
 
-// A probe of `bar` that may suspend for some microseconds, so that a warp that waits takes no issue slots
-// from the others.
-__device__ __forceinline__ bool tprobe(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(20000u)
-        : "memory");
-    return ok != 0;
+// Wait for the phase of `bar` with the given parity, by a whole warp with one verdict; a probe suspends
+// the warp for some 150 cycles, so that this many take about a second.
+constexpr int kProbes = 1 << 23;
+__device__ __noinline__ bool twait_long(uint64_t *bar, uint32_t parity) {
+    bool ok = false;
+#pragma unroll 1
+    for (int i = 0; i < kProbes && !ok; ++i) ok = mbar_try_wait(bar, parity);
+    return __all_sync(0xffffffffu, ok);
 }
-__device__ __noinline__ bool twait_long(uint32_t bar, uint32_t parity) {
-    const long long t0 = clock64();
-    while (true) {
-        if (__all_sync(0xffffffffu, tprobe(bar, parity))) return true;
-        if (__any_sync(0xffffffffu, clock64() - t0 > kWaitCycles)) return false;
-    }
-}
-// Wait for the phase of `bar` with the given parity, by a whole warp with one verdict.
 __device__ __forceinline__ bool twait(uint64_t *bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, tprobe(smem_u32(bar), parity)) || twait_long(smem_u32(bar), parity);
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || twait_long(bar, parity);
 }
 // The same without a call, for the softmax warps (a function that both parts call costs the kernel its
 // register split).
 __device__ __forceinline__ bool twait_here(uint64_t *bar, uint32_t parity) {
-    const uint32_t at = smem_u32(bar);
-    if (__all_sync(0xffffffffu, tprobe(at, parity))) return true;
-    const long long t0 = clock64();
-    while (true) {
-        if (__all_sync(0xffffffffu, tprobe(at, parity))) return true;
-        if (__any_sync(0xffffffffu, clock64() - t0 > kWaitCycles)) return false;
-    }
+    bool ok = mbar_try_wait(bar, parity);
+#pragma unroll 1
+    for (int i = 0; i < kProbes && !ok; ++i) ok = mbar_try_wait(bar, parity);
+    return __all_sync(0xffffffffu, ok);
 }
 
 __device__ __forceinline__ uint32_t telect() {
@@ -158,6 +153,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const float2 *x) {
                  : "memory");
 }
 
+__device__ __forceinline__ void tmem_st8(uint32_t at, const float2 (&x)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at),
+                 "r"(__float_as_uint(x[0].x)), "r"(__float_as_uint(x[0].y)), "r"(__float_as_uint(x[1].x)),
+                 "r"(__float_as_uint(x[1].y)), "r"(__float_as_uint(x[2].x)), "r"(__float_as_uint(x[2].y)),
+                 "r"(__float_as_uint(x[3].x)), "r"(__float_as_uint(x[3].y))
+                 : "memory");
+}
+
 __device__ __forceinline__ uint32_t t_sw128(int row, int c) { return (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4)); }
 
 __device__ __forceinline__ uint32_t t_pack_f16x2(float lo, float hi) {
@@ -166,11 +169,22 @@ __device__ __forceinline__ uint32_t t_pack_f16x2(float lo, float hi) {
     return r;
 }
 
-// The sums (or maxima) over the warp of 32 values a lane: lane c's is that of v[c].
+// x as three bf16 parts, the halves of the words a sum of products needs: side A's (x1, x1, x2, x1, x3, x2)
+// or side B's (x1, x2, x1, x3, x1, x2), two zeros behind them.
+template <bool kA>
+__device__ __forceinline__ uint4 parts3(float x) {
+    const uint32_t a = pack_bf16x2(x, 0.f) & 0xffffu;
+    const float y = x - __uint_as_float(a << 16);
+    const uint32_t b = pack_bf16x2(y, 0.f) & 0xffffu;
+    const uint32_t c = pack_bf16x2(y - __uint_as_float(b << 16), 0.f) & 0xffffu;
+    return kA ? make_uint4(a | a << 16, b | a << 16, c | b << 16, 0u) : make_uint4(a | b << 16, a | c << 16, a | b << 16, 0u);
+}
+
+// The sums (or maxima) over the warp of 16 values a lane: lane c's and c + 16's is that of v[c].
 template <bool kMax>
-__device__ __forceinline__ float across(float (&v)[32], int lane) {
+__device__ __forceinline__ float across(float (&v)[16], int lane) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
+    for (int off = 8; off > 0; off >>= 1) {
         const bool up = lane & off;
 #pragma unroll
         for (int i = 0; i < off; ++i) {
@@ -179,7 +193,8 @@ __device__ __forceinline__ float across(float (&v)[32], int lane) {
             v[i] = kMax ? fmaxf(keep, got) : keep + got;
         }
     }
-    return v[0];
+    const float got = __shfl_xor_sync(0xffffffffu, v[0], 16);
+    return kMax ? fmaxf(v[0], got) : v[0] + got;
 }
 
 }  // namespace
@@ -189,7 +204,7 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
     constexpr int kRow = D / 2, kRaw = kTRawStages<D>, N = 16 * kCh;
     extern __shared__ __align__(1024) uint8_t smem[];  // (the swizzle's atoms are 1024 bytes)
     uint8_t *const vbuf = smem, *const pbuf = vbuf + 2 * kVTile<D>, *const qbuf = pbuf + 2 * kPTile;
-    uint8_t *const raw = qbuf + 2 * kQTile<D>;
+    uint8_t *const ext = qbuf + 2 * kQTile<D>, *const raw = ext + kExt;
     TShared *sh = reinterpret_cast<TShared *>(raw + kRaw * kTRaw<D>);
     const uint32_t base_u32 = smem_u32(smem);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -209,21 +224,22 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
             mbar_init(&sh->s_empty[i], 4);
             mbar_init(&sh->p_full[i], 4);
             mbar_init(&sh->q_full[i], 1);
-            mbar_init(&sh->q_empty[i], 1 + 2);  // the products, the softmax groups
+            mbar_init(&sh->q_empty[i], 1 + 1);  // the products, the sums
+            mbar_init(&sh->ext_full[i], 1);
             mbar_init(&sh->o_full[i], 1);
             mbar_init(&sh->o_empty[i], 4);
         }
 #pragma unroll 1
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&sh->item_full[i], 1);
-            mbar_init(&sh->item_empty[i], 8 + 4 + 2);
+            mbar_init(&sh->item_empty[i], 8 + 4 + 2 + 1);
         }
         mbar_init(&sh->x_full, 1);
         mbar_init(&sh->fin, 1);
         sh->abort_flag = 0;
         fence_mbar_init();
     }
-    for (int i = tid; i < 2 * kQTile<D> / 16; i += kTT) reinterpret_cast<uint4 *>(qbuf)[i] = make_uint4(0, 0, 0, 0);  // (columns past the items' stay zeros)
+    for (int i = tid; i < (2 * kQTile<D> + kExt) / 16; i += kTT) reinterpret_cast<uint4 *>(qbuf)[i] = make_uint4(0, 0, 0, 0);  // (columns past the items' stay zeros)
     tc::fence_proxy_async_smem();
     if (tid < kN) sh->tok[tid] = (uint8_t)(tid / p.Gs);
     if (tid == 32 * 12) prefetch_tensormap(&tmq);
@@ -242,11 +258,10 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
 
     if (warp < 8) {
         // ===================== softmax: a thread a slot, every second tile
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTRegsSoftmax));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTRegsSoftmax<kCh>));
         const int group = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t tl = tbase + ((uint32_t)(quarter * 32) << 16);
         const uint32_t s_at = tl + kTColS + group * kN, o_at = tl + kTColO + group * kN;
-        float4 *const col = sh->col[group];
         uint8_t *const pto = pbuf + group * kPTile;
         uint32_t tile = 0, o_ph = 0, x_ph = 0;  // tiles of the CTA before this item
         bool bad = !aligned;
@@ -263,31 +278,15 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
             const int own0 = it.pos0 - (it.row0 - it.seq_row0);  // slot of the sequence's first new row
             const int all_hi = p.parents ? own0 : it.pos0 + 1;   // below, and from all_lo on, every row sees a slot
             const int all_lo = p.rows.window > 0 ? it.pos0 + it.ntok - p.rows.window : 0;
-            bad = !twait_here(&sh->q_full[k & 1], (k >> 1) & 1);
-            if (!bad && r < N) {  // the columns' sums of Q
-                const uint8_t *q = qbuf + (k & 1) * kQTile<D>;
-                float2 s = make_float2(0.f, 0.f);
-#pragma unroll 4
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(q + (c >> 3) * kQBox + t_sw128(r, c & 7));
-                    s = __fadd2_rn(s, __fadd2_rn(__fadd2_rn(make_float2(bf16_lo(x.x), bf16_hi(x.x)), make_float2(bf16_lo(x.y), bf16_hi(x.y))),
-                                                 __fadd2_rn(make_float2(bf16_lo(x.z), bf16_hi(x.z)), make_float2(bf16_lo(x.w), bf16_hi(x.w)))));
-                }
-                float *to = reinterpret_cast<float *>(&col[r >> 1]) + (r & 1);
-                to[0] = s.x + s.y;
-                to[2] = -kUnset;
-            }
+            if (r < N) sh->u[group][r] = kUnset;
             if (p.parents && quarter < 2) {  // a token's set of nodes above it, of those up to the item's last
                 const int node0 = it.row0 - it.seq_row0, nodes = min(node0 + it.ntok, kTreeNodes);
                 const int32_t *par = p.parents + it.seq_row0;
                 const int a = lane < nodes ? par[lane] : -1, b = lane + 32 < nodes ? par[lane + 32] : -1;
                 sh->above[group][r] = ancestors_warp(false, a, b, node0 + r, r < it.ntok && node0 + r < nodes);
             }
-            if (group_any(group, bad)) {
-                bad = true;
-                break;
-            }
-            if (r == 0) mbar_arrive(&sh->q_empty[k & 1]);
+            group_sync(group);
+            bool unset = true;  // some column has no u yet
             float2 l[N / 2];
 #pragma unroll
             for (int i = 0; i < N / 2; ++i) l[i] = make_float2(0.f, 0.f);
@@ -298,103 +297,107 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
                 const int slot0 = (it.kt0 + j) * kBK, slot = slot0 + r;
                 bad = bad || !twait_here(&sh->s_full[group], ph);
                 tc::fence_after();
-                const uint2 par = sh->slots[g & 3][r];
-                const float ks = bf16_lo(par.x) * p.scale_log2;
-                const float km = __fmaf_rn(8.f, bf16_lo(par.x), bf16_hi(par.x)) * p.scale_log2;
-                const float w = __uint_as_float(par.y), e = (float)((int)(par.y >> 23) - 127);  // 2^e, e
-                const float2 ks2 = make_float2(ks, ks), km2 = make_float2(km, km), w2 = make_float2(w, w);
+                const float2 par = sh->slots[g & 3][r];
+                const float ks = par.x, w = par.y, e = (float)((int)(__float_as_uint(w) >> 23) - 127);  // w: 2^e
+                const float2 ks2 = make_float2(ks, ks), w2 = make_float2(w, w);
                 const bool masked = slot0 + kBK > all_hi || slot0 < all_lo;
                 float2 x[N / 2];
-                auto scores = [&](bool less) __attribute__((always_inline)) {  // less: less u
 #pragma unroll
-                    for (int ch = 0; ch < N / 16; ++ch) tmem_ld16(s_at + 16 * ch, x + 8 * ch);
-                    tc::wait_ld();
+                for (int ch = 0; ch < N / 16; ++ch) tmem_ld16(s_at + 16 * ch, x + 8 * ch);
+                tc::wait_ld();
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) x[i] = __fmul2_rn(x[i], ks2);
+                if (masked) {
+                    unsigned long long sees = ~0ull;  // a bit a column
+                    if (p.parents) {
+                        const int node = slot - own0;
+                        if (node >= 0) {
+                            sees = 0;
+#pragma unroll 1
+                            for (int c = 0; c < N; ++c) {
+                                const int tk = min((int)sh->tok[c], it.ntok - 1);
+                                if (node < kTreeNodes && (sh->above[group][tk] >> node & 1)) sees |= 1ull << c;
+                            }
+                        }
+                    } else {  // tokens slot - pos0 .. slot - pos0 + window - 1
+                        const long long from = (long long)(slot - it.pos0) * p.Gs;
+                        const long long to = p.rows.window > 0 ? from + (long long)p.rows.window * p.Gs : 64;
+                        const unsigned long long under = from >= 64 ? ~0ull : from <= 0 ? 0ull : (1ull << from) - 1ull;
+                        const unsigned long long below = to >= 64 ? ~0ull : to <= 0 ? 0ull : (1ull << to) - 1ull;
+                        sees = below & ~under;
+                    }
+                    const uint32_t half[2] = {(uint32_t)sees, (uint32_t)(sees >> 32)};
 #pragma unroll
                     for (int i = 0; i < N / 2; ++i) {
-                        const float4 c4 = col[i];
-                        const float2 t = less ? make_float2(c4.z, c4.w) : make_float2(0.f, 0.f);
-                        x[i] = __ffma2_rn(x[i], ks2, __ffma2_rn(km2, make_float2(c4.x, c4.y), t));
+                        if (!(half[i >> 4] >> (2 * i & 31) & 1)) x[i].x = kNegInf;
+                        if (!(half[i >> 4] >> ((2 * i & 31) + 1) & 1)) x[i].y = kNegInf;
                     }
-                    if (masked) {
-                        unsigned long long sees = ~0ull;  // a bit a column
-                        if (p.parents) {
-                            const int node = slot - own0;
-                            if (node >= 0) {
-                                sees = 0;
-#pragma unroll 1
-                                for (int c = 0; c < N; ++c) {
-                                    const int tk = min((int)sh->tok[c], it.ntok - 1);
-                                    if (node < kTreeNodes && (sh->above[group][tk] >> node & 1)) sees |= 1ull << c;
-                                }
-                            }
-                        } else {  // tokens slot - pos0 .. slot - pos0 + window - 1
-                            const long long from = (long long)(slot - it.pos0) * p.Gs;
-                            const long long to = p.rows.window > 0 ? from + (long long)p.rows.window * p.Gs : 64;
-                            const unsigned long long under = from >= 64 ? ~0ull : from <= 0 ? 0ull : (1ull << from) - 1ull;
-                            const unsigned long long below = to >= 64 ? ~0ull : to <= 0 ? 0ull : (1ull << to) - 1ull;
-                            sees = below & ~under;
-                        }
-                        const uint32_t half[2] = {(uint32_t)sees, (uint32_t)(sees >> 32)};
-#pragma unroll
-                        for (int i = 0; i < N / 2; ++i) {
-                            if (!(half[i >> 4] >> (2 * i & 31) & 1)) x[i].x = kNegInf;
-                            if (!(half[i >> 4] >> ((2 * i & 31) + 1) & 1)) x[i].y = kNegInf;
-                        }
-                    }
-                };
-                scores(true);
+                }
                 float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
                 for (int i = 0; i < N / 2; ++i) top[i & 3] = fmaxf(fmaxf(top[i & 3], x[i].x), x[i].y);
-                if (group_any(group, bad || fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) + e > kRoom)) {
+                if (group_any(group, bad || unset || fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) + e > kRoom)) {
                     if (group_any(group, bad)) {
                         bad = true;
                         break;
                     }
                     // some column's u moves up to its largest P (the first tile's do)
-                    scores(false);
+                    const float2 *const us = reinterpret_cast<const float2 *>(sh->u[group]);
 #pragma unroll
-                    for (int h = 0; h < (N + 31) / 32; ++h) {
-                        float v[32];
+                    for (int h = 0; h < N / 16; ++h) {
+                        float v[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float2 y = 16 * h + i < N / 2 ? x[(16 * h + i) % (N / 2)] : make_float2(kNegInf, kNegInf);
-                            v[2 * i] = y.x + e;
-                            v[2 * i + 1] = y.y + e;
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 y = x[8 * h + i], u = us[8 * h + i];
+                            v[2 * i] = y.x + (e + (u.x == kUnset ? 0.f : u.x));
+                            v[2 * i + 1] = y.y + (e + (u.y == kUnset ? 0.f : u.y));
                         }
-                        sh->part[group][quarter][32 * h + lane] = across<true>(v, lane);
+                        const float a = across<true>(v, lane);
+                        if (lane < 16) sh->part[group][quarter][16 * h + lane] = a;
                     }
                     group_sync(group);
+                    bool still = false;
                     if (r < N) {
                         const float a = fmaxf(fmaxf(sh->part[group][0][r], sh->part[group][1][r]),
                                               fmaxf(sh->part[group][2][r], sh->part[group][3][r]));
-                        float *nu = reinterpret_cast<float *>(&col[r >> 1]) + 2 + (r & 1);
-                        const float u = -*nu;
-                        const bool up = a > u + kRoom;
+                        const float u = sh->u[group][r];
+                        const bool none = u == kUnset, up = a > u + kRoom;
+                        const float was = none ? 0.f : u, now = up ? a : was;
                         reinterpret_cast<float *>(sh->f[group])[r] = up ? ex2_approx(u - a) : 1.f;
-                        if (up) *nu = -a;
+                        reinterpret_cast<float *>(sh->d[group])[r] = was - now;
+                        if (up) {
+                            sh->u[group][r] = a;
+                            // (behind the group's last S of the item the place may be the next item's but one)
+                            if (j + 2 < it.n) *reinterpret_cast<uint4 *>(ext + t_sw128(r, ((k & 1) * 2 + group) * 2 + 1)) = parts3<false>(-a);
+                        }
+                        still = none && !up;
                     }
+                    tc::fence_proxy_async_smem();  // (the next S reads u)
                     // (the products that added to O last)
                     if (j > j0) bad = !twait_here(&sh->pv_done[group], ph ^ 1);
                     if (group_any(group, bad)) {
                         bad = true;
                         break;
                     }
+                    unset = group_any(group, still);
                     tc::fence_after();
 #pragma unroll
-                    for (int i = 0; i < N / 2; ++i) l[i] = __fmul2_rn(l[i], sh->f[group][i]);
+                    for (int i = 0; i < N / 2; ++i) {
+                        l[i] = __fmul2_rn(l[i], sh->f[group][i]);
+                        x[i] = __fadd2_rn(x[i], sh->d[group][i]);
+                    }
                     if (j > j0) {
-#pragma unroll
+#pragma unroll 1
                         for (int ch = 0; ch < N / 16; ++ch) {
-                            tmem_ld16(o_at + 16 * ch, x);
+                            float2 o[8];
+                            tmem_ld16(o_at + 16 * ch, o);
                             tc::wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(x[i], sh->f[group][8 * ch + i]);
-                            tmem_st16(o_at + 16 * ch, x);
+                            for (int i = 0; i < 8; ++i) o[i] = __fmul2_rn(o[i], sh->f[group][8 * ch + i]);
+                            tmem_st16(o_at + 16 * ch, o);
                         }
                         tc::wait_st();
                     }
-                    scores(true);
                 }
                 tc::fence_before();
                 __syncwarp();
@@ -424,15 +427,15 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
                 o_ph ^= 1;
             }
 #pragma unroll
-            for (int h = 0; h < (N + 31) / 32; ++h) {
-                float v[32];
+            for (int h = 0; h < N / 16; ++h) {
+                float v[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float2 y = 16 * h + i < N / 2 ? l[(16 * h + i) % (N / 2)] : make_float2(0.f, 0.f);
-                    v[2 * i] = y.x;
-                    v[2 * i + 1] = y.y;
+                for (int i = 0; i < 8; ++i) {
+                    v[2 * i] = l[8 * h + i].x;
+                    v[2 * i + 1] = l[8 * h + i].y;
                 }
-                sh->part[group][quarter][32 * h + lane] = across<false>(v, lane);
+                const float a = across<false>(v, lane);
+                if (lane < 16) sh->part[group][quarter][16 * h + lane] = a;
             }
             tile += it.n;
             if (group_any(group, bad)) {
@@ -443,7 +446,7 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
             float lsum = 0.f, u = 0.f;
             if (r < N) {
                 lsum = (sh->part[group][0][r] + sh->part[group][1][r]) + (sh->part[group][2][r] + sh->part[group][3][r]);
-                u = -(reinterpret_cast<const float *>(&col[r >> 1])[2 + (r & 1)]);
+                u = sh->u[group][r];
             }
             if (!mine) {
                 x_ph ^= both ? 1 : 0;
@@ -567,7 +570,7 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
         }
         if (bad) fail();
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTRegsOther));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTRegsOther<kCh>));
         if (warp < 12) {
             // ===================== codes to operands: a thread a slot
             const int quarter = warp & 3, r = quarter * 32 + lane;
@@ -603,13 +606,21 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
                     if (!(ok = twait(&sh->k_empty[buf], ph ^ 1))) break;
                     tc::fence_after();
                     // V's values times 2^-e, below 2
-                    const uint32_t vpar = seen ? par[kBK + r] : 0u;
+                    const uint32_t vpar = seen ? par[kBK + r] : 0u, kpar = seen ? par[r] : 0u;
                     const float vstep = bf16_lo(vpar), vmid = __fmaf_rn(8.f, vstep, bf16_hi(vpar));
                     const uint32_t most = __float_as_uint(__fmaf_rn(8.f, fabsf(vstep), fabsf(vmid))) >> 23;
                     const uint32_t e = min(max(most, (uint32_t)(127 + (int)kLeast)), 253u);  // the exponent, and 127
                     const float down = __uint_as_float((254u - e) << 23);
                     const uint32_t step2 = t_pack_f16x2(vstep * down, vstep * down), mid2 = t_pack_f16x2(vmid * down, vmid * down);
-                    sh->slots[g & 3][r] = make_uint2(seen ? par[r] : 0u, e << 23);
+                    // K's score in units of 16 steps: 1 + code / 16, and a multiple of the sum of q.  Codes that say less
+                    // than 2^-60 of the middle, or than 2^-100, are left out
+                    const float k16 = 16.f * bf16_lo(kpar) * p.scale_log2;
+                    const float kmid = __fmaf_rn(8.f, bf16_lo(kpar), bf16_hi(kpar)) * p.scale_log2;
+                    const float least = fmaxf(0x1p-100f, fabsf(kmid) * 0x1p-60f);
+                    const bool coded = fabsf(k16) >= least;
+                    const float ks = coded ? k16 : fmaxf(0x1p-100f, fabsf(kmid)), inv = 1.f / ks;
+                    const float rest = coded ? __fmaf_rn(kmid, inv, -1.5f) : kmid * inv;
+                    sh->slots[g & 3][r] = make_float2(ks, __uint_as_float(e << 23));
                     // (a thread's row in order: the pieces put back by selects, a bit of the turn at a time)
                     if constexpr (kPieces == 4) {
                         const bool one = turn & 1, two = turn & 2;
@@ -624,16 +635,23 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
                         c[1] = turn & 1 ? y : c[1];
                     }
 #pragma unroll
-                    for (int i = 0; i < kPieces; i += 2) {  // 64 dims, 32 columns of tensor memory at a time
-                        uint32_t v[32];
+                    for (int i = 0; i < kPieces; ++i) {  // 32 dims, 16 columns of tensor memory at a time
+                        const uint32_t words[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+                        float2 x[8];
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const uint4 &y = c[i + (q >> 2)];
-                            const uint32_t w = (q & 3) == 0 ? y.x : (q & 3) == 1 ? y.y : (q & 3) == 2 ? y.z : y.w;
-                            const uint4 e = quant::expand(w);
-                            v[4 * q] = e.x, v[4 * q + 1] = e.y, v[4 * q + 2] = e.z, v[4 * q + 3] = e.w;
+                        for (int q = 0; q < 4; ++q) {
+                            uint4 y = quant::sixteenths(words[q]);
+                            if (!coded) y = make_uint4(0, 0, 0, 0);
+                            x[2 * q] = make_float2(__uint_as_float(y.x), __uint_as_float(y.y));
+                            x[2 * q + 1] = make_float2(__uint_as_float(y.z), __uint_as_float(y.w));
                         }
-                        tc::tmem_st32(k_at + buf * kN + i * 16, v);
+                        tmem_st16(k_at + buf * kTColsK + i * 16, x);
+                    }
+                    {
+                        const uint4 a = parts3<true>(rest), b = parts3<true>(inv);
+                        const float2 x[4] = {make_float2(__uint_as_float(a.x), __uint_as_float(a.y)), make_float2(__uint_as_float(a.z), 0.f),
+                                             make_float2(__uint_as_float(b.x), __uint_as_float(b.y)), make_float2(__uint_as_float(b.z), 0.f)};
+                        tmem_st8(k_at + buf * kTColsK + D / 2, x);
                     }
                     // V's codes, on their way while K's are written
 #pragma unroll
@@ -742,6 +760,7 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
             const uint64_t desc_v = tc::smem_desc(base_u32, kBox, 1024);
             const uint64_t desc_p = tc::smem_desc(base_u32 + 2 * kVTile<D>, kPTile, 1024);
             const uint64_t desc_q = tc::smem_desc(base_u32 + 2 * (kVTile<D> + kPTile), 16, 1024);
+            const uint64_t desc_x = tc::smem_desc(base_u32 + 2 * (kVTile<D> + kPTile + kQTile<D>), 16, 1024);
             uint32_t g = 0;
             bool ok = aligned;
             // the tile whose O is still to be added to: a group's first or last of its item
@@ -779,7 +798,7 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh->item_empty[slot_i]);
-                if (!(ok = twait(&sh->q_full[k & 1], (k >> 1) & 1))) break;
+                if (!(ok = twait(&sh->q_full[k & 1], (k >> 1) & 1) && twait(&sh->ext_full[k & 1], (k >> 1) & 1))) break;
                 constexpr uint32_t idesc = tc::idesc_bf16(kBK, N, false);
 #pragma unroll 1
                 for (int j = 0; j < n; ++j) {
@@ -790,8 +809,10 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
                         const uint64_t dq = desc_q + (uint64_t)((k & 1) * (kQTile<D> >> 4));
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk)
-                            tc::mma_bf16_ts(tbase + kTColS + buf * kN, tbase + kTColK + buf * kN + kk * 8,
+                            tc::mma_bf16_ts(tbase + kTColS + buf * kN, tbase + kTColK + buf * kTColsK + kk * 8,
                                             dq + (uint64_t)((kk >> 2) * (kQBox >> 4) + (kk & 3) * 2), idesc, kk > 0 ? 1u : 0u);
+                        tc::mma_bf16_ts(tbase + kTColS + buf * kN, tbase + kTColK + buf * kTColsK + D / 2,
+                                        desc_x + (uint64_t)(((k & 1) * 2 + buf) * 2), idesc, 1u);
                         tc::commit(&sh->s_full[buf]);
                         tc::commit(&sh->k_empty[buf]);
                         if (j == n - 1) tc::commit(&sh->q_empty[k & 1]);
@@ -826,6 +847,44 @@ __global__ void __launch_bounds__(kTT, 1) quant_tc_kernel(const __grid_constant_
                     __syncwarp();
                     ++k;
                 } while (it.b >= 0);
+                if (!ok) fail();
+            }
+            if (warp == 15) {  // the columns' sums of Q, two columns a lane; a group's u is 0 to begin with
+                bool ok = aligned;
+#pragma unroll 1
+                for (uint32_t k = 0; ok; ++k) {
+                    const int slot_i = k % kItems;
+                    if (!(ok = twait(&sh->item_full[slot_i], (k / kItems) & 1))) break;
+                    const int b = sh->items[slot_i].b;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh->item_empty[slot_i]);
+                    if (b < 0) break;
+                    if (!(ok = twait(&sh->q_full[k & 1], (k >> 1) & 1))) break;
+                    const uint8_t *q = qbuf + (k & 1) * kQTile<D>;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int c = lane + 32 * h;
+                        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 4
+                        for (int i = 0; i < D / 8; ++i) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(q + (i >> 3) * kQBox + t_sw128(c, i & 7));
+                            sum = __fadd2_rn(sum, __fadd2_rn(__fadd2_rn(make_float2(bf16_lo(x.x), bf16_hi(x.x)), make_float2(bf16_lo(x.y), bf16_hi(x.y))),
+                                                             __fadd2_rn(make_float2(bf16_lo(x.z), bf16_hi(x.z)), make_float2(bf16_lo(x.w), bf16_hi(x.w)))));
+                        }
+                        const uint4 y = parts3<false>(sum.x + sum.y);
+#pragma unroll
+                        for (int group = 0; group < 2; ++group) {
+                            *reinterpret_cast<uint4 *>(ext + t_sw128(c, ((k & 1) * 2 + group) * 2)) = y;
+                            *reinterpret_cast<uint4 *>(ext + t_sw128(c, ((k & 1) * 2 + group) * 2 + 1)) = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&sh->ext_full[k & 1]);
+                        mbar_arrive(&sh->q_empty[k & 1]);
+                    }
+                }
                 if (!ok) fail();
             }
             const int own = p.seq_status ? (int)blockIdx.x * 2 + warp - 14 : p.B;
