@@ -54,9 +54,10 @@ bool q_map(CUtensorMap *map, const void *q, int num_rows, int Hq, int D, long lo
 // SMs of the current device once the kernel is known to run on it as
 // planned, asked for once a device: the attribute calls cost more than a
 // launch.  0 when it cannot run.
-int ready_sms(int D, int quant) {
+int ready_sms(int D, bool quant) {
     struct Entry {
-        int dev, D, sms, quant;
+        int dev, D, sms;
+        bool quant;
     };
     static std::mutex mu;
     static Entry cache[64];
@@ -66,10 +67,10 @@ int ready_sms(int D, int quant) {
     std::lock_guard<std::mutex> lock(mu);
     for (int i = 0; i < ncache; ++i)
         if (cache[i].dev == dev && cache[i].D == D && cache[i].quant == quant) return cache[i].sms;
-    const void *fn = quant ? chunk::quant_kernel_fn(D, quant) : chunk::kernel_fn(D);
+    const void *fn = quant ? chunk::quant_kernel_fn(D) : chunk::kernel_fn(D);
     const int smem = quant ? chunk::quant_smem_bytes(D) : chunk::smem_bytes(D);
-    const int threads = quant ? 512 : chunk::kThreads;
-    const int regs = quant ? 128 : chunk::kLaunchRegs;
+    const int threads = quant ? chunk::kThreadsOf<true> : chunk::kThreadsOf<false>;
+    const int regs = quant ? chunk::kLaunchRegsOf<true> : chunk::kLaunchRegsOf<false>;
     int max_optin = 0, sms = device_sm_count(), occ = 0;
     cudaFuncAttributes at;
     // the kernel hands its launch registers out again (setmaxnreg): it must
@@ -88,7 +89,7 @@ int ready_sms(int D, int quant) {
 sv_status plan_chunk(int Hq, int Hkv, int D, bool quant, ChunkPlan *plan) {
     if ((D != 64 && D != 128) || Hq / Hkv > chunk::kRows) return SV_ERR_UNSUPPORTED;
     ChunkPlan pl{};
-    pl.grid = ready_sms(D, quant ? 4 : 0);
+    pl.grid = ready_sms(D, quant);
     if (pl.grid <= 0) return SV_ERR_CUDA;
     const size_t tiles = (size_t)pl.grid * 2 * 2;
     static_assert(3 * sizeof(chunk::CallWords) <= chunk::kCallBytes, "the forms' words");
@@ -96,7 +97,7 @@ sv_status plan_chunk(int Hq, int Hkv, int D, bool quant, ChunkPlan *plan) {
     pl.off_counters = off;
     off = align_up(off + sizeof(int) * (size_t)pl.grid * 2 * chunk::kCtaCounters, 256);
     pl.off_rows = off;
-    off = align_up(off + sizeof(int) * 2 * 2 * chunk::kRowsMaxGrid, 256);
+    off = align_up(off + sizeof(int) * 2 * chunk::kRowsMaxGrid, 256);
     static_assert(chunk::kRowsCols * 2 <= chunk::kRows, "twice the CTAs of half the rows find room in the shares' places");
     if (off > 64 * 1024 || pl.grid > chunk::kCallShares) return SV_ERR_UNSUPPORTED;  // (what starts as zeros; 1020 SMs)
     pl.off_part_ml = off;
@@ -139,33 +140,28 @@ sv_status launch_chunk_attention(const ChunkArgs &a, const ChunkPlan &pl, void *
         p.k_params = static_cast<const uint32_t *>(a.k_params);
         p.v_params = static_cast<const uint32_t *>(a.v_params);
         p.parents = a.parents;
-        p.call += 2;
-        p.counters = reinterpret_cast<int *>(base + pl.off_rows);
-        if (const int form = chunk::rows_form(a); form >= 0) return chunk::launch_rows(a, p, form, st);
-        const int chunks = chunk::quant_chunks(a);
-        if (ready_sms(a.D, chunks) != pl.grid) return SV_ERR_CUDA;
-        const chunk::RowsParams rp = chunk::rows_params(a, p, 16 * chunks);
-        CUtensorMap tmq;
-        if (!q_map(&tmq, a.q, a.num_rows, a.Hq, a.D, a.q_stride, rp.Gs, rp.rows.tok)) return SV_ERR_CUDA;
-        void *args[] = {&tmq, const_cast<chunk::RowsParams *>(&rp)};
-        return launch_pdl(chunk::quant_kernel_fn(a.D, chunks), dim3(pl.grid), dim3(512), chunk::quant_smem_bytes(a.D), st, args) == cudaSuccess
-                   ? SV_OK
-                   : SV_ERR_CUDA;
+        if (const int form = chunk::rows_form(a); form >= 0) {
+            p.call += 2;
+            p.counters = reinterpret_cast<int *>(base + pl.off_rows);
+            return chunk::launch_rows(a, p, form, st);
+        }
     } else if (const int cluster = chunk::few_cluster(a)) {
         ++p.call;
         return chunk::launch_few(a, p, cluster, st);
     }
     const long long rows = (long long)a.num_pages * a.Hkv * a.page_size;
     const int box_rows = a.page_size < chunk::kBK ? a.page_size : chunk::kBK;
-    CUtensorMap tmk, tmv, tmq, tmq1;
-    if (!cache_map(&tmk, a.k_pages, rows, a.D, box_rows) || !cache_map(&tmv, a.v_pages, rows, a.D, box_rows) ||
-        !q_map(&tmq, a.q, a.num_rows, a.Hq, a.D, a.q_stride, G, tpt) ||
+    CUtensorMap tmk{}, tmv{}, tmq, tmq1;
+    const bool paged = a.k_params || (cache_map(&tmk, a.k_pages, rows, a.D, box_rows) && cache_map(&tmv, a.v_pages, rows, a.D, box_rows));
+    if (!paged || !q_map(&tmq, a.q, a.num_rows, a.Hq, a.D, a.q_stride, G, tpt) ||
         !q_map(&tmq1, a.q, a.num_rows, a.Hq, a.D, a.q_stride, G, 1))
         return SV_ERR_CUDA;
     chunk::Params plain = p;
-    void *args[] = {&tmk, &tmv, &tmq, &tmq1, &plain};
-    return launch_pdl(chunk::kernel_fn(a.D), dim3(pl.grid), dim3(chunk::kThreads), chunk::smem_bytes(a.D), st,
-                      args) == cudaSuccess
+    void *args[] = {&tmk, &tmv, &tmq, &tmq1, a.k_params ? static_cast<void *>(&p) : &plain};
+    const cudaError_t rc =
+        a.k_params ? launch_pdl(chunk::quant_kernel_fn(a.D), dim3(pl.grid), dim3(chunk::kThreadsOf<true>), chunk::quant_smem_bytes(a.D), st, args)
+                   : launch_pdl(chunk::kernel_fn(a.D), dim3(pl.grid), dim3(chunk::kThreadsOf<false>), chunk::smem_bytes(a.D), st, args);
+    return rc == cudaSuccess
                ? SV_OK
                : SV_ERR_CUDA;
 }

@@ -13,9 +13,17 @@ namespace chunk {
 constexpr int kBK = kTileSlots;          // slots of a K/V tile
 constexpr int kRows = 128;               // rows of a Q tile (the MMA's M)
 constexpr int kBox = kBK * 64 * 2;       // 128 rows of 64 dims: 16 KB
-constexpr int kThreads = 32 * 12;
-constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;  // 256 x 200 + 128 x 104 = 384 x 168
-constexpr int kLaunchRegs = 168;
+constexpr int kExpandWarps = 4;          // that turn tiles held in 4 bits into bf16
+template <bool kQuant>
+constexpr int kThreadsOf = 32 * (kQuant ? 12 + kExpandWarps : 12);
+// bf16 pages: 256 x 200 + 128 x 104 = 384 x 168; in 4 bits: 256 x 176 + 256 x 80 = 512 x 128
+template <bool kQuant>
+constexpr int kSoftmaxRegsOf = kQuant ? 160 : 200;
+template <bool kQuant>
+constexpr int kOtherRegsOf = kQuant ? 96 : 104;
+template <bool kQuant>
+constexpr int kLaunchRegsOf = kQuant ? 128 : 168;
+constexpr int kTreeNodes = 64;           // rows of a sequence that is a tree, at most
 constexpr int kItems = 4;                // items published ahead
 constexpr int kWarpPlanB = 128;          // sequences up to which one warp plans alone
 constexpr int kNone = INT32_MIN;
@@ -27,8 +35,23 @@ constexpr uint32_t kCols = 512, kColS = 0, kColO = 256;
 
 template <int D>
 constexpr int kTileBytes = kBK * D * 2;
+// K and V tiles as the products read them; in 4 bits, those as they lie in the pages besides (codes and parameters)
+template <int D, bool kQuant>
+constexpr int kStagesOf = kQuant ? (D == 128 ? 4 : 8) : D == 128 ? 5 : 12;
 template <int D>
-constexpr int kStagesOf = D == 128 ? 5 : 12;  // K and V tiles in flight
+constexpr int kRawStages = D == 128 ? 3 : 10;
+template <int D>
+constexpr int kRawTile = kBK * (D / 2 + 4);
+// Steps and middles of K's slots in f32, read until their tile's softmax is done, two tiles after the
+// tile's place may be taken; exponents of V's, four a tile, read until its product is issued.
+template <int D>
+constexpr int kKSlots = kStagesOf<D, true> / 2 + 2;
+template <int D>
+constexpr int kVSlots = kStagesOf<D, true> / 2;
+constexpr int kSlotBytes = kBK * 8;
+template <int D, bool kQuant>
+constexpr int kRawBytes = kQuant ? kRawStages<D> * kRawTile<D> + kKSlots<D> * kSlotBytes + kVSlots<D> * 32 : 0;
+constexpr int kLeastV = -30;             // the least exponent of V's
 
 struct Params {
     uint16_t *out;
@@ -53,8 +76,16 @@ struct QuantParams : Params {
     const uint32_t *k_params, *v_params;  // a row's step and minimum, a word
     const int32_t *parents;               // or null: every row sees the rows before it
 };
-
-constexpr int kTreeNodes = 64;  // rows of a sequence that is a tree, at most
+template <bool kQuant>
+struct ParamsType {
+    using type = Params;
+};
+template <>
+struct ParamsType<true> {
+    using type = QuantParams;
+};
+template <bool kQuant>
+using ParamsOf = typename ParamsType<kQuant>::type;
 
 // This CTA's share added to the workspace's word, by one thread: the call's number.
 __device__ __forceinline__ unsigned long long begin_call(CallWords *words) {
@@ -93,6 +124,7 @@ struct Item {
     int c_first, nc;   // CTAs that share the item's tiles: c_first .. c_first + nc - 1
     int ci;            // this CTA's index among them
     int counters;      // a cut item's arrival counters, from p.counters on
+    int seq_row0;      // the sequence's first row
 };
 
 struct Shared {
@@ -105,11 +137,25 @@ struct Shared {
     uint64_t fin;
     float2 xml[2][kRows];              // a stream's (m, sum) of a one-tile item
     Item items[kItems];
-    long long warp_units[kThreads / 32];
-    int warp_items[kThreads / 32], warp_most[kThreads / 32];
+    long long warp_units[16];          // (12 or 16 warps)
+    int warp_items[16], warp_most[16];
     uint32_t tmem;
     int abort_flag;
 };
+
+struct QuantShared : Shared {
+    uint64_t raw_full[12], raw_empty[12];
+};
+template <bool kQuant>
+struct SharedType {
+    using type = Shared;
+};
+template <>
+struct SharedType<true> {
+    using type = QuantShared;
+};
+template <bool kQuant>
+using SharedOf = typename SharedType<kQuant>::type;
 
 // The form for a few rows over short tables (sv_chunk_few.cu).
 struct FewParams {
@@ -125,7 +171,7 @@ sv_status launch_few(const ChunkArgs &args, const Params &params, int cluster, c
 
 const void *kernel_fn(int D);
 int smem_bytes(int D);
-const void *quant_kernel_fn(int D, int chunks);  // of 16 columns: 2 .. 4
+const void *quant_kernel_fn(int D);
 int quant_smem_bytes(int D);
 
 }  // namespace chunk

@@ -61,9 +61,8 @@ struct RowsShared {
     RowsItem items[2];   // the item at hand and the next
     long long warp_units[kRW];
     long long before[kRT];
-    uint64_t full[kRW][kRowsDepth<D, NT>];
     uint8_t tok[2][8 * NT];
-    int lost, last;
+    int last;
 };
 
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
@@ -86,7 +85,11 @@ __device__ __forceinline__ uint32_t lds4(uint32_t a) {
 __device__ __forceinline__ void copy16(uint32_t to, const void *from, bool on) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>  // of a thread's groups of copies, the last kLeft may still be on their way
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
 
 // D (16 x 8, f32) += A (16 x 16) B (16 x 8): with g = lane / 4 and t = lane % 4, a0..a3 hold A at
 // rows g, g + 8, g, g + 8 and columns 2t, 2t + 1 (the last two 8 further), b0, b1 B at rows 2t,
@@ -146,9 +149,6 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const Ro
     using Sh = RowsShared<D, NT>;
     Sh &sh = *reinterpret_cast<Sh *>(dynamic);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, t = lane & 3;
-    if (lane < kDepth) mbar_init(&sh.full[warp][lane], 1);
-    fence_mbar_init();
-    if (tid == 0) sh.lost = 0;
     griddep_wait();
     griddep_launch_dependents();
     unsigned long long call = 0;
@@ -175,10 +175,8 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const Ro
         __syncwarp();
     }
 
-    uint8_t *const ring = sh.ring[warp][0];
-    const uint32_t ring_at = smem_u32(ring);
-    uint32_t put = 0, got = 0;  // units asked for and used
-    bool lost = false;
+    const uint32_t ring_at = smem_u32(sh.ring[warp][0]);
+    uint32_t got = 0;  // units used
 
     // of the item at hand, or of the one whose copies are begun: this warp's tiles i0 .. i1 - 1, the
     // next to ask for, and, a lane a tile from `base` on, the cache rows of the unit's halves
@@ -203,43 +201,39 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const Ro
             }
         }
     };
-    auto fetch = [&](const RowsItem &x) {  // the unit of tile `ask`
-        if (ask - base == 32) {
-            base = ask;
-            load_rows(x);
-        }
-        const int a0 = __shfl_sync(0xffffffffu, y0, ask - base), a1 = __shfl_sync(0xffffffffu, y1, ask - base);
-        if (lane == 0) {
-            const uint32_t st = put % kDepth;
-            uint64_t *bar = &sh.full[warp][st];
-            uint8_t *to = ring + st * kUnitRaw<D>;
-            mbar_arrive_expect_tx(bar, (uint32_t)(((a0 >= 0) + (a1 >= 0)) * (kUnitRaw<D> / 2)));
-            const bool whole = p.page_size > 8;
-            const int rows = whole ? 16 : 8;
-#pragma unroll 1
-            for (int half = 0; half < (whole ? 1 : 2); ++half) {
-                const int y = half ? a1 : a0;
-                if (y < 0) continue;
-                bulk_load(to + half * 8 * kRow, p.k_codes + (size_t)y * kRow, rows * kRow, bar);
-                bulk_load(to + kU * kRow + half * 8 * kRow, p.v_codes + (size_t)y * kRow, rows * kRow, bar);
-                bulk_load(to + 2 * kU * kRow + half * 32, p.k_params + y, rows * 4, bar);
-                bulk_load(to + 2 * kU * kRow + kU * 4 + half * 32, p.v_params + y, rows * 4, bar);
+    auto fetch = [&](const RowsItem &x, uint32_t unit) {  // the unit of tile `ask`: one group of copies, empty past the end
+        if (ask < i1) {
+            if (ask - base == 32) {
+                base = ask;
+                load_rows(x);
             }
+            const int a0 = __shfl_sync(0xffffffffu, y0, ask - base), a1 = __shfl_sync(0xffffffffu, y1, ask - base);
+            const uint32_t to = ring_at + unit % kDepth * kUnitRaw<D> + lane * 16;
+            if constexpr (D == 128) {
+                copy16(to, p.k_codes + (size_t)max(a0, 0) * kRow + lane * 16, a0 >= 0);
+                copy16(to + 512, p.k_codes + (size_t)max(a1, 0) * kRow + lane * 16, a1 >= 0);
+                copy16(to + 1024, p.v_codes + (size_t)max(a0, 0) * kRow + lane * 16, a0 >= 0);
+                copy16(to + 1536, p.v_codes + (size_t)max(a1, 0) * kRow + lane * 16, a1 >= 0);
+            } else {
+                const int a = lane < 16 ? a0 : a1;
+                copy16(to, p.k_codes + (size_t)max(a, 0) * kRow + (lane & 15) * 16, a >= 0);
+                copy16(to + 512, p.v_codes + (size_t)max(a, 0) * kRow + (lane & 15) * 16, a >= 0);
+            }
+            if (lane < 8) {
+                const int a = lane & 2 ? a1 : a0;
+                copy16(to + 2 * kU * kRow, (lane < 4 ? p.k_params : p.v_params) + max(a, 0) + (lane & 1) * 4, a >= 0);
+            }
+            ++ask;
         }
-        ++put;
-        ++ask;
+        copies_end();
     };
     auto begin = [&](const RowsItem &x, int buf) {  // its first copies, and its queries
         const int lo = p.rows.window > 0 ? max(0, x.pos0 - p.rows.window + 1) : 0, hi = x.pos0 + x.ntok;
         const int s0 = x.kt0 * kTileSlots + warp * kU;  // (the slots seen end, or begin, within a tile)
         i0 = s0 + kU <= lo ? 1 : 0;
         i1 = s0 < hi ? min(x.n, (hi - s0 - 1) / kTileSlots + 1) : 0;
-        if (lost) i1 = 0;
         ask = base = i0;
         load_rows(x);
-#pragma unroll 1
-        for (int i = 0; i < kDepth; ++i)
-            if (ask < i1) fetch(x);
         const int heads = min(p.Gs, p.G - x.h % p.parts * p.Gs), cols = x.ntok * p.Gs;
         const int head0 = x.h / p.parts * p.G + x.h % p.parts * p.Gs;
         const uint32_t q_at = smem_u32(sh.q[buf]);
@@ -250,6 +244,9 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const Ro
             copy16(q_at + q_piece<D>(c, piece), from, on);
             if (piece == 0) sh.tok[buf][c] = (uint8_t)min(tk, x.ntok - 1);
         }
+        copies_end();
+#pragma unroll 1
+        for (int i = 0; i < kDepth; ++i) fetch(x, got + i);
         if (p.parents && warp < 2) {  // a token's set of nodes above it, of those up to the item's last
             const int node0 = x.row0 - x.seq_row0, nodes = min(node0 + x.ntok, kTreeNodes);
             const int32_t *par = p.parents + x.seq_row0;
@@ -282,7 +279,7 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const Ro
         // below: every row sees the slots; from all_lo on too
         const int all_hi = p.parents ? own0 : it.pos0 + 1;
         const int all_lo = p.rows.window > 0 ? it.pos0 + it.ntok - p.rows.window : 0;
-        copies_done();
+        copies_wait<kDepth>();
         for (int i = lane; i < 8 * NT; i += 32) sh.u[warp][i] = kUnset;
         __syncthreads();
         const uint32_t q_at = smem_u32(sh.q[qb]), u_at = smem_u32(sh.u[warp]), qs_at = smem_u32(sh.qs);
@@ -315,10 +312,8 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const Ro
 #pragma unroll 1
         for (int i = i0; i < i1; ++i) {
             const uint32_t st = got % kDepth;
-            if (!warp_wait_bounded(&sh.full[warp][st], got / kDepth & 1)) {
-                lost = true;
-                break;
-            }
+            copies_wait<kDepth - 1>();
+            __syncwarp();
             const uint32_t at = ring_at + st * kUnitRaw<D>;
             const int slot0 = (it.kt0 + i) * kTileSlots + warp * kU;
             // ---- S
@@ -459,13 +454,8 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const Ro
                 }
             }
             __syncwarp();
+            fetch(sh.items[qb], got + kDepth);
             ++got;
-            if (ask < i1) fetch(sh.items[qb]);
-        }
-        if (lost) {  // its own copies still on their way, this one too
-#pragma unroll 1
-            for (; got < put; ++got) warp_wait_bounded(&sh.full[warp][got % kDepth], got / kDepth & 1);
-            sh.lost = 1;
         }
         // ---- the warps' sums
 #pragma unroll
@@ -603,18 +593,10 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const Ro
             if (p.lse && dim == 0) p.lse[row] = M * kLn2 + logf(sum);
         }
     }
-    copies_done();
-    __syncthreads();
-    if (tid == 0) {
-        if (sh.lost) give_up(p.call, p.seq_status, p.B);
-        // the next call's, whose grid may be another
-        for (int c = blockIdx.x; c < kRowsMaxGrid; c += gridDim.x) {
-            p.counters[rows_counter(call + 1, c)] = 0;
-            p.counters[rows_counter(call + 1, c) + 1] = 0;
-        }
+    copies_wait<0>();
+    if (tid == 0) {  // the next call's, whose grid may be another
+        for (int c = blockIdx.x; c < kRowsMaxGrid; c += gridDim.x) p.counters[rows_counter(call + 1, c)] = 0;
     }
-    if (lane == 0 && own < p.B && gave_up(p.call))
-        for (int sb = own; sb < p.B; sb += (int)gridDim.x * kRW) p.seq_status[sb] = SV_ERR_TIMEOUT;
 }
 
 namespace {
@@ -629,11 +611,11 @@ Form form() {
     return Form{reinterpret_cast<const void *>(&quant_rows_kernel<D, NT>), 8 * NT, (int)sizeof(RowsShared<D, NT>), kCtasAnSm<NT>};
 }
 
-constexpr int kForms = 2;
+constexpr int kForms = 4;
 // By columns, the fewest first.
 const Form &form_at(int D, int i) {
-    static const Form f128[kForms] = {form<128, 1>(), form<128, 2>()};
-    static const Form f64[kForms] = {form<64, 1>(), form<64, 2>()};
+    static const Form f128[kForms] = {form<128, 1>(), form<128, 2>(), form<128, 3>(), form<128, 5>()};
+    static const Form f64[kForms] = {form<64, 1>(), form<64, 2>(), form<64, 4>(), form<64, 8>()};
     return D == 128 ? f128[i] : f64[i];
 }
 
@@ -666,11 +648,6 @@ int form_grid(int D, int i) {
 // takes any rows.
 static long long mean_columns(const ChunkArgs &a) { return ((long long)a.num_rows + a.B - 1) / a.B * (a.Hq / a.Hkv); }
 
-int quant_chunks(const ChunkArgs &a) {
-    const long long mean = mean_columns(a);
-    return mean <= 32 ? 2 : mean <= 48 ? 3 : 4;
-}
-
 int rows_form(const ChunkArgs &a) {
     const long long mean = mean_columns(a);
     if (mean > kRowsMost) return -1;
@@ -679,7 +656,7 @@ int rows_form(const ChunkArgs &a) {
     return i;
 }
 
-RowsParams rows_params(const ChunkArgs &a, const QuantParams &c, int cols) {
+static RowsParams rows_params(const ChunkArgs &a, const QuantParams &c, int cols) {
     RowsParams p{};
     static_cast<QuantParams &>(p) = c;
     p.q = static_cast<const uint16_t *>(a.q);

@@ -23,16 +23,12 @@ struct RowsParams : QuantParams {
     int groups;          // Hkv * parts
 };
 
-// The counters (two) of an item shared from CTA `cta` on, in the set of the given call.
-SV_CALL_HD int rows_counter(unsigned long long call, int cta) { return ((int)(call & 1) * kRowsMaxGrid + cta) * 2; }
+// The counter of an item shared from CTA `cta` on, in the set of the given call.
+SV_CALL_HD int rows_counter(unsigned long long call, int cta) { return (int)(call & 1) * kRowsMaxGrid + cta; }
 
 // The form for the call's rows; -1 where it has too many.
 int rows_form(const ChunkArgs &args);
 sv_status launch_rows(const ChunkArgs &args, const QuantParams &params, int form, cudaStream_t stream);
-// Chunks of 16 columns an item, 2 .. 4, of the form on the tensor cores.
-int quant_chunks(const ChunkArgs &args);
-// What a form of `cols` columns an item takes.
-RowsParams rows_params(const ChunkArgs &args, const QuantParams &params, int cols);
 
 }  // namespace chunk
 }  // namespace sv
