@@ -18,9 +18,9 @@ template <bool kQuant>
 constexpr int kThreadsOf = 32 * (kQuant ? 12 + kExpandWarps : 12);
 // bf16 pages: 256 x 200 + 128 x 104 = 384 x 168; in 4 bits: 256 x 176 + 256 x 80 = 512 x 128
 template <bool kQuant>
-constexpr int kSoftmaxRegsOf = kQuant ? 160 : 200;
+constexpr int kSoftmaxRegsOf = kQuant ? 176 : 200;
 template <bool kQuant>
-constexpr int kOtherRegsOf = kQuant ? 96 : 104;
+constexpr int kOtherRegsOf = kQuant ? 80 : 104;
 template <bool kQuant>
 constexpr int kLaunchRegsOf = kQuant ? 128 : 168;
 constexpr int kTreeNodes = 64;           // rows of a sequence that is a tree, at most

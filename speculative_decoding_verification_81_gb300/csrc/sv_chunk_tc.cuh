@@ -159,18 +159,40 @@ __device__ __forceinline__ float2 unpack_f16x2(uint32_t x) {
     return y;
 }
 
-// This warp's P of the first 64 columns (packed at TMEM address s) times a.
-__device__ __noinline__ inline void rescale_p(uint32_t s, float a) {
-    uint32_t pv[32];
+// 16 columns of tensor memory a warp.
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+                 "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+// Waits for the loads of r; what uses it stays behind.
+__device__ __forceinline__ void ld_done(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                   "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+
+// This warp's P in the first n columns from TMEM address s on (n a multiple of 16) times a.
+__device__ __noinline__ inline void rescale_p(uint32_t s, int n, float a) {
     tc::wait_st();
-    tc::tmem_ld32(s, pv);
-    tc::wait_ld();
+#pragma unroll 1
+    for (int i = 0; i < n; i += 16) {
+        uint32_t pv[32];
+        tc::tmem_ld32(s + i, pv);  // (of which half is used; a row has room behind it)
+        tc::wait_ld();
+        uint32_t y[16];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        const float2 x = unpack_f16x2(pv[j]);
-        pv[j] = pack_f16x2(x.x * a, x.y * a);
+        for (int j = 0; j < 16; ++j) {
+            const float2 x = unpack_f16x2(pv[j]);
+            y[j] = pack_f16x2(x.x * a, x.y * a);
+        }
+        tmem_st16(s + i, y);
     }
-    tc::tmem_st32(s, pv);
 }
 
 // Of the slots at .. at + 31 a bit for each from lo on and below hi.
@@ -411,8 +433,7 @@ __device__ __forceinline__ void expand_quant(const P &p, S *sh, uint8_t *smem, u
     volatile int *abort_flag = &sh->abort_flag;
     auto fail = [&] { *abort_flag = 1; };
     const int r = 32 * w + lane;  // the slot in its tile
-    const uint32_t raw_at = smem_u32(raw) + r * kRow, par_at = smem_u32(raw) + kBK * kRow + r * 4;
-    const uint32_t out_at = smem_u32(smem) + r * 128;
+    const uint8_t *const raw_at = raw + r * kRow, *const par_at = raw + kBK * kRow + r * 4;
     float *slots = reinterpret_cast<float *>(raw_slots<D>(raw));
     uint32_t pos = 0;
     bool ok = true;
@@ -442,14 +463,11 @@ __device__ __forceinline__ void expand_quant(const P &p, S *sh, uint8_t *smem, u
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) c[i] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
             if (seen) {
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(par) : "r"(par_at + rs * kRawTile<D>) : "memory");
+                par = *reinterpret_cast<const uint32_t *>(par_at + rs * kRawTile<D>);
 #pragma unroll
                 for (int i = 0; i < kPieces; ++i) {
                     const int piece = (i + (r >> (D == 128 ? 1 : 2))) & (kPieces - 1);
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(c[i].x), "=r"(c[i].y), "=r"(c[i].z), "=r"(c[i].w)
-                                 : "r"(raw_at + rs * kRawTile<D> + piece * 16)
-                                 : "memory");
+                    c[i] = *reinterpret_cast<const uint4 *>(raw_at + rs * kRawTile<D> + piece * 16);
                 }
             }
             __syncwarp();
@@ -461,20 +479,18 @@ __device__ __forceinline__ void expand_quant(const P &p, S *sh, uint8_t *smem, u
             }
             const uint32_t tile = pos >> 1;
             const float step = bf16_lo(par), mid = __fmaf_rn(8.f, step, bf16_hi(par));
-            const uint32_t to = out_at + st * kTileBytes<D>;
+            uint8_t *const to = smem + r * 128 + st * kTileBytes<D>;
             auto store = [&](auto &&values) {
 #pragma unroll
                 for (int i = 0; i < kPieces; ++i) {
                     const int piece = (i + (r >> (D == 128 ? 1 : 2))) & (kPieces - 1);
                     const uint32_t words[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
-                    const uint32_t at = to + (piece >> 1) * kBox;
+                    uint8_t *const at = to + (piece >> 1) * kBox;
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const uint4 v = values(words[q]);
                         const uint32_t chunk = (uint32_t)((piece & 1) * 4 + q) ^ (uint32_t)(r & 7);
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + chunk * 16), "r"(v.x), "r"(v.y),
-                                     "r"(v.z), "r"(v.w)
-                                     : "memory");
+                        *reinterpret_cast<uint4 *>(at + chunk * 16) = v;
                     }
                 }
             };
@@ -483,11 +499,10 @@ __device__ __forceinline__ void expand_quant(const P &p, S *sh, uint8_t *smem, u
                 const uint32_t most = max(__reduce_max_sync(0xffffffffu, mine == 255u ? 0u : mine), (uint32_t)(126 + 15 + kLeastV));
                 const float down = __uint_as_float((127u + 15u + 126u - most) << 23);
                 const uint32_t step2 = pack_f16x2(step * down, step * down), mid2 = pack_f16x2(mid * down, mid * down);
-                if (lane == 0) {  // of two warps the exponents, then 2^-e
+                if (lane == 0) {  // e and 2^-e
                     const int e = (int)most - 126 - 15;
-                    float *to = slots + kKSlots<D> * (kSlotBytes / 4) + tile % kVSlots<D> * 8 + (w >> 1) * 4 + (w & 1);
-                    to[0] = (float)e;
-                    to[2] = __uint_as_float((uint32_t)(127 - e) << 23);
+                    reinterpret_cast<float2 *>(slots + kKSlots<D> * (kSlotBytes / 4))[tile % kVSlots<D> * 4 + w] =
+                        make_float2((float)e, __uint_as_float((uint32_t)(127 - e) << 23));
                 }
                 store([&](uint32_t x) { return quant::scaled_f16(x, step2, mid2); });  // (not seen: 0 of both)
             } else {
@@ -716,61 +731,70 @@ __global__ void __launch_bounds__(kThreadsOf<kQuant>, 1)
                 s_ph ^= 1;
                 tc::fence_after();
                 if (kQuant && active) {
-                    // in two halves of the columns (all of a row's scores beside what the codes need do
-                    // not fit a thread's registers)
+                    // a warp of V's slots at a time (all of a row's scores beside what the codes need do not
+                    // fit a thread's registers), the next ones' S on its way
                     const uint32_t pv = ring + 2 * j + 1;
                     ok = warp_wait_bounded(&sh->full[pv % kStages], (pv / kStages) & 1);  // (V's exponents)
                     if (!ok) break;
                     const uint8_t *slots = raw_slots<D>(raw);
                     const float4 *ks = reinterpret_cast<const float4 *>(slots + (pv >> 1) % kKS * kSlotBytes);
-                    const float4 *es = reinterpret_cast<const float4 *>(slots + kKS * kSlotBytes) + (pv >> 1) % kVS * 2;
+                    const float2 *es = reinterpret_cast<const float2 *>(slots + kKS * kSlotBytes) + (pv >> 1) % kVS * 4;
                     const float2 qs2 = make_float2(qs, qs);
                     const bool masked = kb + kBK > w_hi || kb < w_lo;
-#pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        float2 sv[32];
-                        {
-                            uint32_t ra[32], rb[32];
-                            tc::tmem_ld32(sbuf + 64 * h, ra);
-                            tc::tmem_ld32(sbuf + 64 * h + 32, rb);
-                            tc::wait_ld();
-                            // step * (q . (codes - 8)) + middle * sum(q), scaled
+                    // (weights of one part beside the next one's scores: neither alone fills the warp's time)
+                    uint32_t ra[2][32];
+                    float2 sv[2][16];
+                    tc::tmem_ld32(sbuf, ra[0]);
+                    float2 nb2 = make_float2(0.f, 0.f);
+                    float down = 0.f;
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const uint32_t *r2 = i < 16 ? ra + 2 * i : rb + 2 * (i - 16);
-                                const float4 k4 = ks[32 * h + i];
-                                sv[i] = __ffma2_rn(make_float2(__uint_as_float(r2[0]), __uint_as_float(r2[1])),
-                                                   make_float2(k4.x, k4.y), __fmul2_rn(make_float2(k4.z, k4.w), qs2));
+                    for (int h = 0; h <= 4; ++h) {
+                        if (h < 4) {  // step * (q . (codes - 8)) + middle * sum(q), scaled
+                            ld_done(ra[h & 1]);
+                            if (h < 3) tc::tmem_ld32(sbuf + 32 * (h + 1), ra[(h + 1) & 1]);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float4 k4 = ks[16 * h + i];
+                                sv[h & 1][i] = __ffma2_rn(make_float2(__uint_as_float(ra[h & 1][2 * i]), __uint_as_float(ra[h & 1][2 * i + 1])),
+                                                          make_float2(k4.x, k4.y), __fmul2_rn(make_float2(k4.z, k4.w), qs2));
                             }
                         }
+                        if (h > 0) {
+                            float2 ls = make_float2(0.f, 0.f);
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float2 x = __fadd2_rn(sv[(h - 1) & 1][i], nb2);
+                                const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                                ls = __fadd2_rn(ls, e);
+                                pk[i] = pack_f16x2(e.x, e.y);
+                            }
+                            l = __fmaf_rn(ls.x + ls.y, down, l);
+                            tmem_st16(sbuf + 16 * (h - 1), pk);
+                        }
+                        if (h == 4) break;
                         if (masked) {
+                            const int at = kb + 32 * h;
+                            uint32_t sees = visible(at, see_lo, see_hi);
+                            if (tree) {  // all of the slots before own0, and of those from it on the path's
+                                const int x = at - own0;
+                                sees = x <= -32 ? ~0u
+                                     : x < 0    ? ((1u << -x) - 1u) | (uint32_t)(above << -x)
+                                     : x < 64   ? (uint32_t)(above >> x)
+                                                : 0u;
+                            }
 #pragma unroll
-                            for (int w = 0; w < 2; ++w) {
-                                const int at = kb + 64 * h + 32 * w;
-                                uint32_t sees = visible(at, see_lo, see_hi);
-                                if (tree) {  // all of the slots before own0, and of those from it on the path's
-                                    const int x = at - own0;
-                                    sees = x <= -32 ? ~0u
-                                         : x < 0    ? ((1u << -x) - 1u) | (uint32_t)(above << -x)
-                                         : x < 64   ? (uint32_t)(above >> x)
-                                                    : 0u;
-                                }
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    if (!((sees >> (2 * i)) & 1u)) sv[16 * w + i].x = kNegInf;
-                                    if (!((sees >> (2 * i + 1)) & 1u)) sv[16 * w + i].y = kNegInf;
-                                }
+                            for (int i = 0; i < 16; ++i) {
+                                if (!((sees >> (2 * i)) & 1u)) sv[h & 1][i].x = kNegInf;
+                                if (!((sees >> (2 * i + 1)) & 1u)) sv[h & 1][i].y = kNegInf;
                             }
                         }
-                        // of the slots of each V warp the exponent joins the score
+                        // the exponent of these slots' V joins the score
+                        const float2 e2 = es[h];
                         float mq[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            float &to = mq[(i >> 4) * 2 + (i & 1)];
-                            to = fmaxf(fmaxf(to, sv[i].x), sv[i].y);
-                        }
-                        const float4 e4 = es[h];
-                        const float c = fmaxf(fmaxf(mq[0], mq[1]) + e4.x, fmaxf(mq[2], mq[3]) + e4.y);
+                        for (int i = 0; i < 16; ++i) mq[i & 3] = fmaxf(fmaxf(mq[i & 3], sv[h & 1][i].x), sv[h & 1][i].y);
+                        const float c = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) + e2.x;
                         const bool up = c > m + kRescaleThreshold;
                         if (__any_sync(0xffffffffu, up)) {
                             const float f = up ? ex2_approx(m - c) : 1.f;
@@ -778,23 +802,14 @@ __global__ void __launch_bounds__(kThreadsOf<kQuant>, 1)
                                 m = c;
                                 l *= f;
                             }
+                            if (h < 3) ld_done(ra[(h + 1) & 1]);
                             // (the wait for S covers this stream's earlier PV products: issued before it)
                             if (j != first) rescale_o<D>(o_cols, f);
-                            if (h == 1) rescale_p(sbuf, f);
+                            if (h > 0) rescale_p(sbuf, 16 * h, f);
                         }
-                        const float nb = m == kNegInf ? 0.f : -m;
-                        const float2 nb2[2] = {make_float2(nb + e4.x, nb + e4.x), make_float2(nb + e4.y, nb + e4.y)};
-                        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                        uint32_t pk[32];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float2 x = __fadd2_rn(sv[i], nb2[i >> 4]);
-                            const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-                            ls[i >> 4] = __fadd2_rn(ls[i >> 4], e);
-                            pk[i] = pack_f16x2(e.x, e.y);
-                        }
-                        l = __fmaf_rn(ls[0].x + ls[0].y, e4.z, __fmaf_rn(ls[1].x + ls[1].y, e4.w, l));
-                        tc::tmem_st32(sbuf + 32 * h, pk);
+                        const float nb = (m == kNegInf ? 0.f : -m) + e2.x;
+                        nb2 = make_float2(nb, nb);
+                        down = e2.y;
                     }
                     tc::wait_st();
                 } else if (active) {
