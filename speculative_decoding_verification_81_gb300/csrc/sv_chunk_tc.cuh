@@ -741,38 +741,22 @@ __global__ void __launch_bounds__(kThreadsOf<kQuant>, 1)
                     const float2 *es = reinterpret_cast<const float2 *>(slots + kKS * kSlotBytes) + (pv >> 1) % kVS * 4;
                     const float2 qs2 = make_float2(qs, qs);
                     const bool masked = kb + kBK > w_hi || kb < w_lo;
-                    // (weights of one part beside the next one's scores: neither alone fills the warp's time)
-                    uint32_t ra[2][32];
-                    float2 sv[2][16];
-                    tc::tmem_ld32(sbuf, ra[0]);
-                    float2 nb2 = make_float2(0.f, 0.f);
-                    float down = 0.f;
+                    uint32_t ra[32];
+                    float2 sv[16];
+                    tc::tmem_ld32(sbuf, ra);
+                    // (two of the four in line: with all of them and the next part's scores beside a part's weights a
+                    // prompt's 539 us become 534, but the chains' 87 become 110)
+#pragma unroll 2
+                    for (int h = 0; h < 4; ++h) {
+                        // step * (q . (codes - 8)) + middle * sum(q), scaled
+                        ld_done(ra);
 #pragma unroll
-                    for (int h = 0; h <= 4; ++h) {
-                        if (h < 4) {  // step * (q . (codes - 8)) + middle * sum(q), scaled
-                            ld_done(ra[h & 1]);
-                            if (h < 3) tc::tmem_ld32(sbuf + 32 * (h + 1), ra[(h + 1) & 1]);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const float4 k4 = ks[16 * h + i];
-                                sv[h & 1][i] = __ffma2_rn(make_float2(__uint_as_float(ra[h & 1][2 * i]), __uint_as_float(ra[h & 1][2 * i + 1])),
-                                                          make_float2(k4.x, k4.y), __fmul2_rn(make_float2(k4.z, k4.w), qs2));
-                            }
+                        for (int i = 0; i < 16; ++i) {
+                            const float4 k4 = ks[16 * h + i];
+                            sv[i] = __ffma2_rn(make_float2(__uint_as_float(ra[2 * i]), __uint_as_float(ra[2 * i + 1])),
+                                               make_float2(k4.x, k4.y), __fmul2_rn(make_float2(k4.z, k4.w), qs2));
                         }
-                        if (h > 0) {
-                            float2 ls = make_float2(0.f, 0.f);
-                            uint32_t pk[16];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const float2 x = __fadd2_rn(sv[(h - 1) & 1][i], nb2);
-                                const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-                                ls = __fadd2_rn(ls, e);
-                                pk[i] = pack_f16x2(e.x, e.y);
-                            }
-                            l = __fmaf_rn(ls.x + ls.y, down, l);
-                            tmem_st16(sbuf + 16 * (h - 1), pk);
-                        }
-                        if (h == 4) break;
+                        if (h < 3) tc::tmem_ld32(sbuf + 32 * (h + 1), ra);
                         if (masked) {
                             const int at = kb + 32 * h;
                             uint32_t sees = visible(at, see_lo, see_hi);
@@ -785,15 +769,15 @@ __global__ void __launch_bounds__(kThreadsOf<kQuant>, 1)
                             }
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
-                                if (!((sees >> (2 * i)) & 1u)) sv[h & 1][i].x = kNegInf;
-                                if (!((sees >> (2 * i + 1)) & 1u)) sv[h & 1][i].y = kNegInf;
+                                if (!((sees >> (2 * i)) & 1u)) sv[i].x = kNegInf;
+                                if (!((sees >> (2 * i + 1)) & 1u)) sv[i].y = kNegInf;
                             }
                         }
                         // the exponent of these slots' V joins the score
                         const float2 e2 = es[h];
                         float mq[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) mq[i & 3] = fmaxf(fmaxf(mq[i & 3], sv[h & 1][i].x), sv[h & 1][i].y);
+                        for (int i = 0; i < 16; ++i) mq[i & 3] = fmaxf(fmaxf(mq[i & 3], sv[i].x), sv[i].y);
                         const float c = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) + e2.x;
                         const bool up = c > m + kRescaleThreshold;
                         if (__any_sync(0xffffffffu, up)) {
@@ -802,14 +786,24 @@ __global__ void __launch_bounds__(kThreadsOf<kQuant>, 1)
                                 m = c;
                                 l *= f;
                             }
-                            if (h < 3) ld_done(ra[(h + 1) & 1]);
+                            if (h < 3) ld_done(ra);
                             // (the wait for S covers this stream's earlier PV products: issued before it)
                             if (j != first) rescale_o<D>(o_cols, f);
                             if (h > 0) rescale_p(sbuf, 16 * h, f);
                         }
                         const float nb = (m == kNegInf ? 0.f : -m) + e2.x;
-                        nb2 = make_float2(nb, nb);
-                        down = e2.y;
+                        const float2 nb2 = make_float2(nb, nb);
+                        float2 ls = make_float2(0.f, 0.f);
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 x = __fadd2_rn(sv[i], nb2);
+                            const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                            ls = __fadd2_rn(ls, e);
+                            pk[i] = pack_f16x2(e.x, e.y);
+                        }
+                        l = __fmaf_rn(ls.x + ls.y, e2.y, l);
+                        tmem_st16(sbuf + 16 * h, pk);
                     }
                     tc::wait_st();
                 } else if (active) {

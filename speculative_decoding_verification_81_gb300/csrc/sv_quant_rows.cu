@@ -611,11 +611,11 @@ Form form() {
     return Form{reinterpret_cast<const void *>(&quant_rows_kernel<D, NT>), 8 * NT, (int)sizeof(RowsShared<D, NT>), kCtasAnSm<NT>};
 }
 
-constexpr int kForms = 4;
+constexpr int kForms = 2;
 // By columns, the fewest first.
 const Form &form_at(int D, int i) {
-    static const Form f128[kForms] = {form<128, 1>(), form<128, 2>(), form<128, 3>(), form<128, 5>()};
-    static const Form f64[kForms] = {form<64, 1>(), form<64, 2>(), form<64, 4>(), form<64, 8>()};
+    static const Form f128[kForms] = {form<128, 1>(), form<128, 2>()};
+    static const Form f64[kForms] = {form<64, 1>(), form<64, 2>()};
     return D == 128 ? f128[i] : f64[i];
 }
 
