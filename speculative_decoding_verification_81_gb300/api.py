@@ -106,8 +106,11 @@ def _bind_to(L):
     if _bind is None and os.path.exists(path):
         _bind = _load_bind(path)
     if _bind is not None:
-        names = ("sv_build_block_tables", "sv_release_pages", "sv_append_kv_paged", "sv_chunk_attention_paged")
-        _bind.use(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names))
+        def addresses(*names):
+            return (ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names)
+        _bind.use(*addresses("sv_build_block_tables", "sv_release_pages", "sv_append_kv_paged", "sv_chunk_attention_paged"))
+        _bind.use_quant(*addresses("sv_append_kv_quant", "sv_chunk_attention_quant", "sv_compact_kv_quant",
+                                   "sv_fork_tables", "sv_copy_pages", "sv_release_shared_pages"))
         _bound = L
 
 
@@ -897,6 +900,9 @@ def sv_append_kv_quant(k_new, v_new, slot_map, k_codes, k_params, v_codes, v_par
     fused projection); slot_map [num_rows] int32 (-1: padding).  Writes the
     rows in 4 bits into k_codes/v_codes [num_pages,Hkv,page_size,D/2] uint8 and
     k_params/v_params [num_pages,Hkv,page_size,2] bf16 (step, minimum), in place."""
+    if stream is None and (native := _native()) is not None:
+        if native.append_kv_quant(k_new, v_new, slot_map, k_codes, k_params, v_codes, v_params, row_status) is not None:
+            return
     p_k, p_kp, p_v, p_vp, dev, num_pages, Hkv, page_size, D = _quant_pages(k_codes, k_params, v_codes, v_params)
     p_kn, k_stride = _rows(k_new, "k_new", Hkv, dev)
     p_vn, v_stride = _rows(v_new, "v_new", Hkv, dev)
@@ -924,6 +930,13 @@ def sv_chunk_attention_quant(q, k_codes, k_params, v_codes, v_params, block_tabl
     sv_append_kv_quant's).  parents [num_rows] int32: each sequence's rows (64 at
     most) are the nodes of a tree, a row's parent by its number in the sequence, -1
     for the first; None: every row sees the rows before it."""
+    if scale is None and isinstance(q, torch.Tensor) and q.dim() == 3:
+        scale = 1.0 / math.sqrt(q.shape[2] or 1)
+    if out is lse is ws is stream is None and (native := _native()) is not None:
+        r = native.chunk_attention_quant(q, k_codes, k_params, v_codes, v_params, block_table, prefix_lens, row_starts,
+                                         parents, scale, window, return_lse, seq_status, _chunk_ws)
+        if r is not None:
+            return r
     bf16, i32 = torch.bfloat16, torch.int32
     p_k, p_kp, p_v, p_vp, dev, num_pages, Hkv, page_size, D = _quant_pages(k_codes, k_params, v_codes, v_params)
     p_q, q_stride = _rows(q, "q", None, dev)
@@ -942,8 +955,6 @@ def sv_chunk_attention_quant(q, k_codes, k_params, v_codes, v_params, block_tabl
     p_par = _opt_arr(parents, "parents", i32, (num_rows,), dev)
     p_st = _opt_arr(seq_status, "seq_status", i32, (B,), dev)
     _need_int(window, "window")
-    if scale is None:
-        scale = 1.0 / math.sqrt(D or 1)
     with _Launch(dev, stream) as s:
         if out is None:
             out = torch.empty((num_rows, Hq, D), dtype=bf16, device=dev)
@@ -964,6 +975,11 @@ def sv_compact_kv_quant(k_codes, k_params, v_codes, v_params, block_table, prefi
                         path_nodes=None, new_kv_lens=None, seq_status=None, stream=None):
     """sv_compact_kv_paged in a cache held in 4 bits.  path_nodes [B,P] int32 or
     None (chain).  Returns new_kv_lens [B] int32 (may be prefix_lens itself)."""
+    if new_kv_lens is stream is None and (native := _native()) is not None:
+        r = native.compact_kv_quant(k_codes, k_params, v_codes, v_params, block_table, prefix_lens, accepted_len,
+                                    path_nodes, seq_status)
+        if r is not None:
+            return r
     i32 = torch.int32
     p_k, p_kp, p_v, p_vp, dev, num_pages, Hkv, page_size, D = _quant_pages(k_codes, k_params, v_codes, v_params)
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
@@ -1023,6 +1039,11 @@ def sv_fork_tables(sources, targets, fork_lens, page_counts, block_table, free_p
     [B,max_pages] (the targets' entries written in place), free_pages, shares
     [num_pages], free_count [1] int32.  Returns (copies [F,3] for sv_copy_pages,
     new_page_counts [B], new_free_count [1], new_shares [num_pages]), int32."""
+    if copies is new_page_counts is new_free_count is new_shares is stream is None and (native := _native()) is not None:
+        r = native.fork_tables(sources, targets, fork_lens, page_counts, block_table, free_pages, free_count, shares,
+                               page_size, fork_status)
+        if r is not None:
+            return r
     i32 = torch.int32
     p_tab, p_stk, p_fc, p_sh, dev, B, max_pages, num_pages = _pool(block_table, free_pages, free_count, shares, page_size)
     if not isinstance(sources, torch.Tensor) or sources.dim() != 1:
@@ -1050,6 +1071,9 @@ def sv_copy_pages(copies, planes, copy_status=None, stream=None):
     """copies [F,3] int32, rows (from, to, slots); planes: up to 64 tensors
     [num_pages,Hkv,page_size,X] of any type (pages of K, V, codes, parameters, of
     any number of layers).  The first slots of page `from` are written to page `to`."""
+    if stream is None and (native := _native()) is not None:
+        if native.copy_pages(copies, planes, copy_status) is not None:
+            return
     if not isinstance(planes, (list, tuple)) or not planes or not all(isinstance(t, torch.Tensor) for t in planes):
         raise TypeError("planes must be a list of tensors")
     if planes[0].dim() != 4:
@@ -1079,6 +1103,11 @@ def sv_release_shared_pages(keep_lens, page_counts, block_table, free_pages, fre
     """sv_release_pages where pages may be shared: a page goes to the stack (in
     place) with its last holder.  Returns (new_page_counts [B], new_free_count
     [1], new_shares [num_pages]), int32."""
+    if new_page_counts is new_free_count is new_shares is ws is stream is None and (native := _native()) is not None:
+        r = native.release_shared_pages(keep_lens, page_counts, block_table, free_pages, free_count, shares, page_size,
+                                        seq_status)
+        if r is not None:
+            return r
     i32 = torch.int32
     p_tab, p_stk, p_fc, p_sh, dev, B, max_pages, num_pages = _pool(block_table, free_pages, free_count, shares, page_size)
     p_keep = _arr(keep_lens, "keep_lens", i32, (B,), dev)

@@ -24,6 +24,12 @@ decltype(&sv_build_block_tables) f_build;
 decltype(&sv_release_pages) f_release;
 decltype(&sv_append_kv_paged) f_append;
 decltype(&sv_chunk_attention_paged) f_chunk;
+decltype(&sv_append_kv_quant) f_append_quant;
+decltype(&sv_chunk_attention_quant) f_chunk_quant;
+decltype(&sv_compact_kv_quant) f_compact_quant;
+decltype(&sv_fork_tables) f_fork;
+decltype(&sv_copy_pages) f_copy;
+decltype(&sv_release_shared_pages) f_release_shared;
 
 PyObject *none() { Py_RETURN_NONE; }
 
@@ -227,6 +233,200 @@ PyObject *chunk(PyObject *, PyObject *const *a, Py_ssize_t na) {
     return Py_BuildValue("(NN)", THPVariable_Wrap(std::move(out)), THPVariable_Wrap(std::move(lse)));
 }
 
+// ---- a cache held in 4 bits: codes [num_pages, Hkv, page_size, D/2] of bytes and parameters [..., 2] of bf16
+
+struct Quant {
+    const at::Tensor *k, *kp, *v, *vp;
+    int dev;
+    int num_pages, Hkv, page_size, D;
+};
+
+// The four arrays from a[0] on, on the current device; false where they are otherwise.
+bool quant_caches(PyObject *const *a, Quant &c) {
+    c.k = tensor(a[0]);
+    c.kp = tensor(a[1]);
+    c.v = tensor(a[2]);
+    c.vp = tensor(a[3]);
+    c.dev = device_of(c.k);
+    if (c.dev < 0 || c.k->dim() != 4) return false;
+    for (int i = 0; i < 4; ++i)
+        if (c.k->size(i) >= (1LL << 30)) return false;
+    const auto s = c.k->sizes();
+    c.num_pages = (int)s[0];
+    c.Hkv = (int)s[1];
+    c.page_size = (int)s[2];
+    c.D = 2 * (int)s[3];
+    return array(c.k, at::kByte, c.dev, {s[0], s[1], s[2], s[3]}) && array(c.v, at::kByte, c.dev, {s[0], s[1], s[2], s[3]}) &&
+           array(c.kp, at::kBFloat16, c.dev, {s[0], s[1], s[2], 2}) && array(c.vp, at::kBFloat16, c.dev, {s[0], s[1], s[2], 2});
+}
+
+// (k_new, v_new, slot_map, k_codes, k_params, v_codes, v_params, row_status); True when done
+PyObject *append_quant(PyObject *, PyObject *const *a, Py_ssize_t na) {
+    if (na != 8 || !f_append_quant) return none();
+    const at::Tensor *kn = tensor(a[0]), *vn = tensor(a[1]), *slots = tensor(a[2]);
+    Quant c;
+    if (!quant_caches(a + 3, c) || !kn || !vn || kn->dim() != 3 || !kn->is_cuda() || kn->get_device() != c.dev ||
+        !vn->is_cuda() || vn->get_device() != c.dev || vn->scalar_type() != kn->scalar_type() ||
+        !vn->sizes().equals(kn->sizes()))
+        return none();
+    const int64_t rows = kn->size(0);
+    const bool f32 = kn->scalar_type() == at::kFloat;
+    if ((!f32 && kn->scalar_type() != at::kBFloat16) || kn->size(1) != c.Hkv || kn->size(2) != c.D || rows >= (1LL << 31) ||
+        !i32(slots, c.dev, rows))
+        return none();
+    bool bad = false;
+    int32_t *st = status(a[7], c.dev, rows, bad);
+    const int64_t ks = row_stride(*kn), vs = row_stride(*vn);
+    if (bad || !ks || !vs) return none();
+    if (f_append_quant(kn->data_ptr(), vn->data_ptr(), f32 ? SV_F32 : SV_BF16, ks, vs, ip(*slots), (int)rows, c.Hkv, c.D,
+                       c.page_size, c.num_pages, c.k->data_ptr(), c.kp->data_ptr(), c.v->data_ptr(), c.vp->data_ptr(), st,
+                       stream_of(c.dev)) != SV_OK)
+        return none();
+    Py_RETURN_TRUE;
+}
+
+// (q, k_codes, k_params, v_codes, v_params, block_table, prefix_lens, row_starts, parents, scale, window, return_lse,
+// seq_status, workspaces): workspaces as chunk's.
+PyObject *chunk_quant(PyObject *, PyObject *const *a, Py_ssize_t na) {
+    if (na != 14 || !f_chunk_quant) return none();
+    const at::Tensor *q = tensor(a[0]), *tab = tensor(a[5]), *pre = tensor(a[6]), *starts = tensor(a[7]);
+    Quant c;
+    const int64_t window = small_int(a[10]);
+    if (!quant_caches(a + 1, c) || !q || q->dim() != 3 || !q->is_cuda() || q->get_device() != c.dev ||
+        q->scalar_type() != at::kBFloat16 || q->size(2) != c.D || !tab || tab->dim() != 2 || window < 0 ||
+        !PyFloat_CheckExact(a[9]) || !PyBool_Check(a[11]) || !PyDict_Check(a[13]))
+        return none();
+    const int64_t rows = q->size(0), hq = q->size(1), B = tab->size(0), mp = tab->size(1), d = c.D;
+    bool bad = rows >= (1LL << 31) || hq >= (1LL << 31) || B >= (1 << 30) || mp >= (1 << 30);
+    int32_t *par = bad ? nullptr : status(a[8], c.dev, rows, bad);
+    int32_t *st = status(a[12], c.dev, B, bad);
+    const int64_t qs = row_stride(*q);
+    if (bad || !qs || !array(tab, at::kInt, c.dev, {B, mp}) || !i32(pre, c.dev, B) || !i32(starts, c.dev, B + 1)) return none();
+    const cudaStream_t s = c10::cuda::getCurrentCUDAStream(c.dev).stream();
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &cap) != cudaSuccess || cap != cudaStreamCaptureStatusNone) return none();
+    PyObject *key = Py_BuildValue("(LiK)", (long long)d, c.dev, (unsigned long long)(uintptr_t)s);
+    PyObject *held = key ? PyDict_GetItemWithError(a[13], key) : nullptr;  // (borrowed)
+    Py_XDECREF(key);
+    if (PyErr_Occurred()) PyErr_Clear();
+    const at::Tensor *ws = held ? tensor(held) : nullptr;
+    if (!ws) return none();
+    at::Tensor out = empty({rows, hq, d}, at::kBFloat16), lse;
+    const bool want_lse = a[11] == Py_True;
+    if (want_lse) lse = empty({rows, hq}, at::kFloat);
+    if (f_chunk_quant(q->data_ptr(), qs, c.k->data_ptr(), c.kp->data_ptr(), c.v->data_ptr(), c.vp->data_ptr(), ip(*tab), (int)mp,
+                      c.num_pages, c.page_size, ip(*pre), ip(*starts), par, (int)B, (int)rows, (int)hq, c.Hkv, c.D,
+                      (float)PyFloat_AS_DOUBLE(a[9]), (int)window, out.data_ptr(),
+                      want_lse ? static_cast<float *>(lse.data_ptr()) : nullptr, st, ws->data_ptr(), (size_t)ws->numel(),
+                      reinterpret_cast<sv_stream_t>(s)) != SV_OK)
+        return none();
+    if (!want_lse) return THPVariable_Wrap(std::move(out));
+    return Py_BuildValue("(NN)", THPVariable_Wrap(std::move(out)), THPVariable_Wrap(std::move(lse)));
+}
+
+// (k_codes, k_params, v_codes, v_params, block_table, prefix_lens, accepted_len, path_nodes, seq_status)
+PyObject *compact_quant(PyObject *, PyObject *const *a, Py_ssize_t na) {
+    if (na != 9 || !f_compact_quant) return none();
+    const at::Tensor *tab = tensor(a[4]), *pre = tensor(a[5]), *acc = tensor(a[6]);
+    const at::Tensor *path = a[7] == Py_None ? nullptr : tensor(a[7]);
+    Quant c;
+    if (!quant_caches(a, c) || !tab || tab->dim() != 2 || (a[7] != Py_None && (!path || path->dim() != 2))) return none();
+    const int64_t B = tab->size(0), mp = tab->size(1), stride = path ? path->size(1) : 0;
+    bool bad = B >= (1 << 30) || mp >= (1 << 30) || stride >= (1 << 30);
+    int32_t *st = status(a[8], c.dev, B, bad);
+    if (bad || !array(tab, at::kInt, c.dev, {B, mp}) || !i32(pre, c.dev, B) || !i32(acc, c.dev, B) ||
+        (path && !array(path, at::kInt, c.dev, {B, stride})))
+        return none();
+    at::Tensor lens = empty({B}, at::kInt);
+    if (f_compact_quant(c.k->data_ptr(), c.kp->data_ptr(), c.v->data_ptr(), c.vp->data_ptr(), ip(*tab), (int)mp, c.num_pages,
+                        c.page_size, ip(*pre), ip(lens), path ? ip(*path) : nullptr, (int)stride, ip(*acc), (int)B, c.Hkv, c.D,
+                        st, stream_of(c.dev)) != SV_OK)
+        return none();
+    return THPVariable_Wrap(std::move(lens));
+}
+
+// ---- requests that share pages
+
+// (sources, targets, fork_lens, page_counts, block_table, free_pages, free_count, shares, page_size, fork_status)
+PyObject *fork(PyObject *, PyObject *const *a, Py_ssize_t na) {
+    if (na != 10 || !f_fork) return none();
+    const at::Tensor *src = tensor(a[0]), *tgt = tensor(a[1]), *len = tensor(a[2]), *cnt = tensor(a[3]), *tab = tensor(a[4]),
+                     *stk = tensor(a[5]), *fc = tensor(a[6]), *sh = tensor(a[7]);
+    const int64_t ps = small_int(a[8]);
+    const int dev = device_of(tab);
+    if (dev < 0 || ps <= 0 || tab->dim() != 2 || !stk || stk->dim() != 1 || !src || src->dim() != 1) return none();
+    const int64_t B = tab->size(0), mp = tab->size(1), np = stk->size(0), F = src->size(0);
+    bool bad = B >= (1 << 30) || mp >= (1 << 30) || np >= (1 << 30) || F >= (1 << 28);
+    int32_t *st = status(a[9], dev, F, bad);
+    if (bad || !array(tab, at::kInt, dev, {B, mp}) || !i32(stk, dev, np) || !i32(sh, dev, np) || !i32(src, dev, F) ||
+        !i32(tgt, dev, F) || !i32(len, dev, F) || !i32(cnt, dev, B) || !i32(fc, dev, 1))
+        return none();
+    const c10::Storage all = memory((3 * F + B + 1) * 4);
+    at::Tensor copies = part(all, at::kInt, 0, {F, 3}), counts = ints(all, 3 * F, B), left = ints(all, 3 * F + B, 1);
+    at::Tensor shares = empty({np}, at::kInt);
+    if (f_fork(ip(*src), ip(*tgt), ip(*len), ip(*cnt), ip(*stk), ip(*fc), ip(*sh), (int)F, (int)B, (int)ps, (int)mp, (int)np,
+               ip(*tab), ip(copies), ip(counts), ip(left), ip(shares), st, stream_of(dev)) != SV_OK)
+        return none();
+    return Py_BuildValue("(NNNN)", THPVariable_Wrap(std::move(copies)), THPVariable_Wrap(std::move(counts)),
+                         THPVariable_Wrap(std::move(left)), THPVariable_Wrap(std::move(shares)));
+}
+
+// (copies, planes, copy_status); True when done
+PyObject *copy(PyObject *, PyObject *const *a, Py_ssize_t na) {
+    constexpr int kMost = 64;
+    if (na != 3 || !f_copy || !PyList_CheckExact(a[1])) return none();
+    const at::Tensor *copies = tensor(a[0]);
+    const int dev = device_of(copies);
+    const Py_ssize_t n = PyList_GET_SIZE(a[1]);
+    if (dev < 0 || copies->dim() != 2 || n < 1 || n > kMost) return none();
+    void *planes[kMost];
+    int bytes[kMost];
+    const at::Tensor *first = nullptr;
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        const at::Tensor *t = tensor(PyList_GET_ITEM(a[1], i));
+        if (!t || t->dim() != 4 || !t->is_cuda() || t->get_device() != dev || !t->is_contiguous()) return none();
+        if (!first) first = t;
+        for (int d = 0; d < 3; ++d)
+            if (t->size(d) != first->size(d) || t->size(d) >= (1LL << 31)) return none();
+        const int64_t row = t->size(3) * (int64_t)t->element_size();
+        if (row >= (1LL << 31)) return none();
+        planes[i] = t->data_ptr();
+        bytes[i] = (int)row;
+    }
+    const int64_t F = copies->size(0);
+    bool bad = F >= (1LL << 31);
+    int32_t *st = status(a[2], dev, F, bad);
+    if (bad || !array(copies, at::kInt, dev, {F, 3})) return none();
+    if (f_copy(ip(*copies), (int)F, planes, bytes, (int)n, (int)first->size(1), (int)first->size(2), (int)first->size(0), st,
+               stream_of(dev)) != SV_OK)
+        return none();
+    Py_RETURN_TRUE;
+}
+
+// (keep_lens, page_counts, block_table, free_pages, free_count, shares, page_size, seq_status)
+PyObject *release_shared(PyObject *, PyObject *const *a, Py_ssize_t na) {
+    if (na != 8 || !f_release_shared) return none();
+    const at::Tensor *keep = tensor(a[0]), *cnt = tensor(a[1]), *tab = tensor(a[2]), *stk = tensor(a[3]), *fc = tensor(a[4]),
+                     *sh = tensor(a[5]);
+    const int64_t ps = small_int(a[6]);
+    const int dev = device_of(tab);
+    if (dev < 0 || ps <= 0 || tab->dim() != 2 || !stk || stk->dim() != 1) return none();
+    const int64_t B = tab->size(0), mp = tab->size(1), np = stk->size(0);
+    bool bad = B >= (1 << 30) || mp >= (1 << 30) || np >= (1 << 30);
+    int32_t *st = status(a[7], dev, B, bad);
+    if (bad || !array(tab, at::kInt, dev, {B, mp}) || !i32(stk, dev, np) || !i32(sh, dev, np) || !i32(keep, dev, B) ||
+        !i32(cnt, dev, B) || !i32(fc, dev, 1))
+        return none();
+    const c10::Storage all = memory((B + 1) * 4);
+    at::Tensor counts = ints(all, 0, B), left = ints(all, B, 1), shares = empty({np}, at::kInt);
+    const c10::Storage ws = memory(4 * np);  // (the stream's later work alone may take it over)
+    if (f_release_shared(ip(*keep), ip(*cnt), ip(*tab), ip(*stk), ip(*fc), ip(*sh), (int)B, (int)ps, (int)mp, (int)np, ip(counts),
+                         ip(left), ip(shares), st, ws.mutable_data(), (size_t)(4 * np), stream_of(dev)) != SV_OK)
+        return none();
+    return Py_BuildValue("(NNN)", THPVariable_Wrap(std::move(counts)), THPVariable_Wrap(std::move(left)),
+                         THPVariable_Wrap(std::move(shares)));
+}
+
 // No C++ exception (an allocation that fails, say) leaves these functions: the
 // interpreted form of the call meets and reports it.
 template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)>
@@ -250,6 +450,19 @@ PyObject *use(PyObject *, PyObject *args) {
     Py_RETURN_NONE;
 }
 
+// The same of (append_quant, chunk_quant, compact_quant, fork_tables, copy_pages, release_shared).
+PyObject *use_quant(PyObject *, PyObject *args) {
+    unsigned long long x[6];
+    if (!PyArg_ParseTuple(args, "KKKKKK", x, x + 1, x + 2, x + 3, x + 4, x + 5)) return nullptr;
+    f_append_quant = reinterpret_cast<decltype(f_append_quant)>((uintptr_t)x[0]);
+    f_chunk_quant = reinterpret_cast<decltype(f_chunk_quant)>((uintptr_t)x[1]);
+    f_compact_quant = reinterpret_cast<decltype(f_compact_quant)>((uintptr_t)x[2]);
+    f_fork = reinterpret_cast<decltype(f_fork)>((uintptr_t)x[3]);
+    f_copy = reinterpret_cast<decltype(f_copy)>((uintptr_t)x[4]);
+    f_release_shared = reinterpret_cast<decltype(f_release_shared)>((uintptr_t)x[5]);
+    Py_RETURN_NONE;
+}
+
 PyCFunction fast(PyObject *(*f)(PyObject *, PyObject *const *, Py_ssize_t)) {
     return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
 }
@@ -259,6 +472,13 @@ PyMethodDef methods[] = {{"use", use, METH_VARARGS, nullptr},
                          {"release_pages", fast(guarded<release>), METH_FASTCALL, nullptr},
                          {"append_kv_paged", fast(guarded<append>), METH_FASTCALL, nullptr},
                          {"chunk_attention_paged", fast(guarded<chunk>), METH_FASTCALL, nullptr},
+                         {"use_quant", use_quant, METH_VARARGS, nullptr},
+                         {"append_kv_quant", fast(guarded<append_quant>), METH_FASTCALL, nullptr},
+                         {"chunk_attention_quant", fast(guarded<chunk_quant>), METH_FASTCALL, nullptr},
+                         {"compact_kv_quant", fast(guarded<compact_quant>), METH_FASTCALL, nullptr},
+                         {"fork_tables", fast(guarded<fork>), METH_FASTCALL, nullptr},
+                         {"copy_pages", fast(guarded<copy>), METH_FASTCALL, nullptr},
+                         {"release_shared_pages", fast(guarded<release_shared>), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_sv_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
