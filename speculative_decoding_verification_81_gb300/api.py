@@ -110,7 +110,7 @@ def _bind_to(L):
             return (ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names)
         _bind.use(*addresses("sv_build_block_tables", "sv_release_pages", "sv_append_kv_paged", "sv_chunk_attention_paged"))
         _bind.use_quant(*addresses("sv_append_kv_quant", "sv_chunk_attention_quant", "sv_compact_kv_quant",
-                                   "sv_fork_tables", "sv_copy_pages", "sv_release_shared_pages"))
+                                   "sv_fork_tables", "sv_copy_pages", "sv_release_shared_pages", "sv_workspace_size"))
         _bound = L
 
 
@@ -1118,7 +1118,7 @@ def sv_release_shared_pages(keep_lens, page_counts, block_table, free_pages, fre
         new_free_count = _given(new_free_count, "new_free_count", (1,), dev)
         new_shares = _given(new_shares, "new_shares", (num_pages,), dev)
         if ws is None:  # (any contents: no call needs another's)
-            ws = torch.empty(4 * num_pages, dtype=torch.uint8, device=dev)
+            ws = torch.empty(sv_workspace_size(SV_OP_RELEASE_SHARED_PAGES, 0, num_pages), dtype=torch.uint8, device=dev)
         rc = lib().sv_release_shared_pages(p_keep, p_cnt, p_tab, p_stk, p_fc, p_sh, B, page_size, max_pages, num_pages,
                                            new_page_counts.data_ptr(), new_free_count.data_ptr(), new_shares.data_ptr(),
                                            p_st, _arr(ws, "ws", torch.uint8, ws.shape, dev), ws.numel(), s)

@@ -39,7 +39,7 @@ size_t sv_workspace_size(sv_op op, int B, int T_or_N, int V, sv_dtype dtype, int
         sv::ChunkPlan pl;
         return sv::plan_chunk(Hq, Hkv, D, false, &pl) == SV_OK ? pl.bytes : 0;
     }
-    if (op == SV_OP_RELEASE_SHARED_PAGES) return T_or_N > 0 ? (size_t)T_or_N * sizeof(int) : 0;
+    if (op == SV_OP_RELEASE_SHARED_PAGES) return T_or_N > 0 ? ((size_t)T_or_N + sv::kReleaseMaxWarps) * sizeof(int) : 0;
     if (B <= 0 || T_or_N <= 0) return 0;
     switch (op) {
         case SV_OP_CHUNK_ATTENTION:
@@ -464,7 +464,7 @@ sv_status sv_release_shared_pages(const int32_t *keep_lens, const int32_t *page_
     if (B <= 0 || page_size <= 0 || max_pages <= 0 || num_pages <= 0) return SV_ERR_INVALID_ARG;
     if (new_page_counts == page_counts || new_free_count == free_count || new_shares == shares) return SV_ERR_INVALID_ARG;
     if (!page_tables_ok(B, page_size, max_pages, num_pages)) return SV_ERR_UNSUPPORTED;
-    if (!workspace || workspace_bytes < (size_t)num_pages * sizeof(int) || reinterpret_cast<uintptr_t>(workspace) % sizeof(int) != 0)
+    if (!workspace || workspace_bytes < ((size_t)num_pages + sv::kReleaseMaxWarps) * sizeof(int) || reinterpret_cast<uintptr_t>(workspace) % sizeof(int) != 0)
         return SV_ERR_WORKSPACE;
     sv::ReleaseSharedArgs a{keep_lens, page_counts, block_table,     free_pages,     free_count, shares,     B,
                             page_size, max_pages,   num_pages,       new_page_counts, new_free_count, new_shares, seq_status,

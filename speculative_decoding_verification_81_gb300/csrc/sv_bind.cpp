@@ -30,6 +30,7 @@ decltype(&sv_compact_kv_quant) f_compact_quant;
 decltype(&sv_fork_tables) f_fork;
 decltype(&sv_copy_pages) f_copy;
 decltype(&sv_release_shared_pages) f_release_shared;
+decltype(&sv_workspace_size) f_size;
 
 PyObject *none() { Py_RETURN_NONE; }
 
@@ -419,9 +420,11 @@ PyObject *release_shared(PyObject *, PyObject *const *a, Py_ssize_t na) {
         return none();
     const c10::Storage all = memory((B + 1) * 4);
     at::Tensor counts = ints(all, 0, B), left = ints(all, B, 1), shares = empty({np}, at::kInt);
-    const c10::Storage ws = memory(4 * np);  // (the stream's later work alone may take it over)
+    const size_t need = f_size(SV_OP_RELEASE_SHARED_PAGES, 0, (int)np, 0, SV_BF16, 0, 0, 0);
+    if (need == 0) return none();
+    const c10::Storage ws = memory((int64_t)need);  // (the stream's later work alone may take it over)
     if (f_release_shared(ip(*keep), ip(*cnt), ip(*tab), ip(*stk), ip(*fc), ip(*sh), (int)B, (int)ps, (int)mp, (int)np, ip(counts),
-                         ip(left), ip(shares), st, ws.mutable_data(), (size_t)(4 * np), stream_of(dev)) != SV_OK)
+                         ip(left), ip(shares), st, ws.mutable_data(), need, stream_of(dev)) != SV_OK)
         return none();
     return Py_BuildValue("(NNN)", THPVariable_Wrap(std::move(counts)), THPVariable_Wrap(std::move(left)),
                          THPVariable_Wrap(std::move(shares)));
@@ -450,16 +453,17 @@ PyObject *use(PyObject *, PyObject *args) {
     Py_RETURN_NONE;
 }
 
-// The same of (append_quant, chunk_quant, compact_quant, fork_tables, copy_pages, release_shared).
+// The same of (append_quant, chunk_quant, compact_quant, fork_tables, copy_pages, release_shared, workspace_size).
 PyObject *use_quant(PyObject *, PyObject *args) {
-    unsigned long long x[6];
-    if (!PyArg_ParseTuple(args, "KKKKKK", x, x + 1, x + 2, x + 3, x + 4, x + 5)) return nullptr;
+    unsigned long long x[7];
+    if (!PyArg_ParseTuple(args, "KKKKKKK", x, x + 1, x + 2, x + 3, x + 4, x + 5, x + 6)) return nullptr;
     f_append_quant = reinterpret_cast<decltype(f_append_quant)>((uintptr_t)x[0]);
     f_chunk_quant = reinterpret_cast<decltype(f_chunk_quant)>((uintptr_t)x[1]);
     f_compact_quant = reinterpret_cast<decltype(f_compact_quant)>((uintptr_t)x[2]);
     f_fork = reinterpret_cast<decltype(f_fork)>((uintptr_t)x[3]);
     f_copy = reinterpret_cast<decltype(f_copy)>((uintptr_t)x[4]);
     f_release_shared = reinterpret_cast<decltype(f_release_shared)>((uintptr_t)x[5]);
+    f_size = reinterpret_cast<decltype(f_size)>((uintptr_t)x[6]);
     Py_RETURN_NONE;
 }
 

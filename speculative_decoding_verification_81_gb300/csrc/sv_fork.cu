@@ -241,21 +241,28 @@ __global__ void __launch_bounds__(kPT) copy_pages_kernel(const __grid_constant__
 constexpr int kRT = 1024;
 constexpr int kRPer = kMaxSeqs / kRT;
 constexpr int kReleaseCluster = 8;
+constexpr long long kClusterEntries = 16384;  // entries of the table up to which one cluster gives pages back
+static_assert(kRT / 32 == 32, "a lane a warp of the CTA");
 
 // Entries that the sequences give up, in sequence order; a page whose count of
 // other holders is s keeps max(0, s - k) of them after k of its entries, and goes
-// to the stack in the place of the last one where k > s.  One cluster: its CTAs
-// count the shared pages' entries (atomic sums and a maximum), meet, take
-// consecutive ranges of the entries, meet over their numbers of pages pushed, and
-// push.
-__global__ void __launch_bounds__(kRT, 1) release_shared_kernel(const ReleaseSharedArgs a) {
-    extern __shared__ int sm[];
-    __shared__ int warp_sums[kRT / 32], pushed_by, before[kReleaseCluster];
-    int *upto = sm;              // [B + 1] entries before each sequence
-    int *kept = upto + a.B + 1;  // [B]
-    const int nct = gridDim.x, rank = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    griddep_wait();
-    griddep_launch_dependents();
+// to the stack in the place of the last one where k > s.  Four parts, each of which
+// needs the ones before it everywhere: the counts, marks and statuses are set; the
+// shared pages' entries are counted (atomic sums and a maximum); a warp counts the
+// pages of its run of consecutive entries that go to the stack; it pushes them.
+//
+// Up to kClusterEntries entries one cluster does all four and meets between them;
+// above, four launches over the whole GPU do (2048 branches of 2048 tokens: 57 us
+// in one cluster, whose eight SMs are then what bounds it).
+struct Shares {
+    const int *upto, *kept;  // entries before each sequence, pages that it keeps
+    int total, nfree;
+    bool pool_ok;
+};
+
+// The sequences' entries, by a whole CTA; `write`: the counts and statuses too.
+__device__ __forceinline__ Shares plan_shares(const ReleaseSharedArgs &a, int *sm, int *warp_sums, bool write) {
+    int *upto = sm, *kept = upto + a.B + 1;  // [B + 1], [B]
     const int per = (a.B + kRT - 1) / kRT;
     const int b0 = min((int)threadIdx.x * per, a.B), b1 = min(b0 + per, a.B);
     const int nfree = *a.free_count;
@@ -267,10 +274,6 @@ __global__ void __launch_bounds__(kRT, 1) release_shared_kernel(const ReleaseSha
         keep[i] = in ? a.keep_lens[b0 + i] : 0;
         held[i] = in ? a.page_counts[b0 + i] : 0;
     }
-    for (int i = rank * kRT + threadIdx.x; i < a.num_pages; i += nct * kRT) {
-        a.new_shares[i] = max(a.shares[i], 0);
-        a.last[i] = -1;
-    }
     int sum = 0;
 #pragma unroll
     for (int i = 0; i < kRPer; ++i) {
@@ -279,7 +282,7 @@ __global__ void __launch_bounds__(kRT, 1) release_shared_kernel(const ReleaseSha
         const int k = keep[i] >= 0 ? pages_of(keep[i], a.page_size) : 0;
         const bool valid = keep[i] >= 0 && held[i] >= k && held[i] <= a.max_pages && (pool_ok || held[i] == k);
         kept[b] = k;
-        if (rank == 0) {
+        if (write) {
             a.new_page_counts[b] = valid ? k : held[i];
             if (a.seq_status) a.seq_status[b] = valid ? SV_OK : SV_ERR_BAD_INPUT;
         }
@@ -294,17 +297,27 @@ __global__ void __launch_bounds__(kRT, 1) release_shared_kernel(const ReleaseSha
         r += held[i];
     }
     if (threadIdx.x == 0) upto[a.B] = total;
-    __threadfence();
     __syncthreads();
-    cluster_sync();  // (counts, marks and statuses are set before any entry changes them)
+    return Shares{upto, kept, total, nfree, pool_ok};
+}
 
-    auto page = [&](int e, int &b) {
-        b = last_at_most(upto, a.B, e);
-        return a.block_table[(size_t)b * a.max_pages + kept[b] + e - upto[b]];
-    };
-    for (int e = rank * kRT + threadIdx.x; e < total; e += nct * kRT) {
+__device__ __forceinline__ void mark_pages(const ReleaseSharedArgs &a, int rank, int nct) {
+    for (int i = rank * kRT + threadIdx.x; i < a.num_pages; i += nct * kRT) {
+        a.new_shares[i] = max(a.shares[i], 0);
+        a.last[i] = -1;
+    }
+}
+
+__device__ __forceinline__ int entry_page(const ReleaseSharedArgs &a, const Shares &s, int e, int &b) {
+    b = last_at_most(s.upto, a.B, e);
+    return a.block_table[(size_t)b * a.max_pages + s.kept[b] + e - s.upto[b]];
+}
+
+__device__ __forceinline__ void count_entries(const ReleaseSharedArgs &a, const Shares &s, int rank, int nct) {
+    for (long long x = rank * kRT + threadIdx.x; x < s.total; x += nct * kRT) {
+        const int e = (int)x;
         int b;
-        const int pg = page(e, b);
+        const int pg = entry_page(a, s, e, b);
         if (pg < 0 || pg >= a.num_pages) {
             if (a.seq_status) a.seq_status[b] = SV_ERR_BAD_INPUT;
         } else if (a.shares[pg] > 0) {
@@ -312,27 +325,73 @@ __global__ void __launch_bounds__(kRT, 1) release_shared_kernel(const ReleaseSha
             atomicMax(&a.last[pg], e);
         }
     }
+}
+
+// A warp's run of entries: warp w of n takes [first, end).
+struct Run {
+    int first, end;
+};
+__device__ __forceinline__ Run run_of(int total, int w, int n) {
+    const int run = (total + n - 1) / n;
+    const int first = (int)min((long long)w * run, (long long)total);
+    return Run{first, min(first + run, total)};
+}
+
+// Whether the page of entry e, below end, goes to the stack.
+__device__ __forceinline__ bool goes(const ReleaseSharedArgs &a, const Shares &s, int e, int end, int &pg, int &b) {
+    if (e >= end) return false;
+    pg = entry_page(a, s, e, b);
+    if (pg < 0 || pg >= a.num_pages) return false;
+    if (a.shares[pg] <= 0) return true;
+    return __ldcg(&a.last[pg]) == e && __ldcg(&a.new_shares[pg]) < 0;
+}
+
+__device__ __forceinline__ int count_pushes(const ReleaseSharedArgs &a, const Shares &s, const Run &run, int lane) {
+    int mine = 0;
+    for (int e = run.first; e < run.end; e += 32) {
+        int pg, b;
+        mine += __popc(__ballot_sync(0xffffffffu, goes(a, s, e + lane, run.end, pg, b)));
+    }
+    return mine;
+}
+
+// The run's pages, to the stack's places from nfree + at on.
+__device__ __forceinline__ void push_pages(const ReleaseSharedArgs &a, const Shares &s, const Run &run, int at, int lane) {
+    for (int e = run.first; e < run.end; e += 32) {
+        int pg, b;
+        const bool push = goes(a, s, e + lane, run.end, pg, b);
+        const uint32_t votes = __ballot_sync(0xffffffffu, push);
+        if (push) {
+            const long long to = (long long)s.nfree + at + __popc(votes & ((1u << lane) - 1u));
+            if (to < a.num_pages) a.free_pages[to] = pg;
+            else if (a.seq_status) a.seq_status[b] = SV_ERR_BAD_INPUT;  // (some page was free already)
+            if (a.shares[pg] > 0) a.new_shares[pg] = 0;  // (only this entry looks at it again)
+        }
+        at += __popc(votes);
+    }
+}
+
+__device__ __forceinline__ int new_free(const ReleaseSharedArgs &a, const Shares &s, long long pushed) {
+    return s.pool_ok ? (int)min((long long)s.nfree + pushed, (long long)a.num_pages) : s.nfree;
+}
+
+__global__ void __launch_bounds__(kRT, 1) release_shared_kernel(const ReleaseSharedArgs a) {
+    extern __shared__ int sm[];
+    __shared__ int warp_sums[kRT / 32], pushed_by, before[kReleaseCluster];
+    const int nct = gridDim.x, rank = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    griddep_wait();
+    griddep_launch_dependents();
+    mark_pages(a, rank, nct);
+    const Shares s = plan_shares(a, sm, warp_sums, rank == 0);
+    __threadfence();
+    __syncthreads();
+    cluster_sync();  // (counts, marks and statuses are set before any entry changes them)
+    count_entries(a, s, rank, nct);
     __threadfence();
     __syncthreads();
     cluster_sync();
-
-    // a warp a run of consecutive entries
-    const int runs = nct * (kRT / 32), run = (total + runs - 1) / runs;
-    const long long begin = (long long)(rank * (kRT / 32) + warp) * run;
-    const int e0 = (int)min(begin, (long long)total), e1 = min(e0 + run, total);
-    // whether entry e's page goes to the stack
-    auto goes = [&](int e, int &pg, int &b) {
-        if (e >= e1) return false;
-        pg = page(e, b);
-        if (pg < 0 || pg >= a.num_pages) return false;
-        if (a.shares[pg] <= 0) return true;
-        return __ldcg(&a.last[pg]) == e && __ldcg(&a.new_shares[pg]) < 0;
-    };
-    int mine = 0;
-    for (int e = e0; e < e1; e += 32) {
-        int pg, b;
-        mine += __popc(__ballot_sync(0xffffffffu, goes(e + lane, pg, b)));
-    }
+    const Run run = run_of(s.total, rank * (kRT / 32) + warp, nct * (kRT / 32));
+    const int mine = count_pushes(a, s, run, lane);
     int pushed;
     const int ahead = __shfl_sync(0xffffffffu, block_scan<kRT>(lane == 0 ? mine : 0, warp_sums, &pushed), 0);
     if (threadIdx.x == 0) pushed_by = pushed;
@@ -346,20 +405,40 @@ __global__ void __launch_bounds__(kRT, 1) release_shared_kernel(const ReleaseSha
         if (c < rank) at += before[c];
         all += before[c];
     }
-    if (rank == 0 && threadIdx.x == 0) *a.new_free_count = pool_ok ? (int)min((long long)nfree + all, (long long)a.num_pages) : nfree;
-    for (int e = e0; e < e1; e += 32) {
-        int pg, b;
-        const bool push = goes(e + lane, pg, b);
-        const uint32_t votes = __ballot_sync(0xffffffffu, push);
-        if (push) {
-            const long long to = (long long)nfree + at + __popc(votes & ((1u << lane) - 1u));
-            if (to < a.num_pages) a.free_pages[to] = pg;
-            else if (a.seq_status) a.seq_status[b] = SV_ERR_BAD_INPUT;  // (some page was free already)
-            if (a.shares[pg] > 0) a.new_shares[pg] = 0;  // (only this entry looks at it again)
-        }
-        at += __popc(votes);
-    }
+    if (rank == 0 && threadIdx.x == 0) *a.new_free_count = new_free(a, s, all);
+    push_pages(a, s, run, at, lane);
     cluster_sync();  // (a CTA's shared memory is read by the others until here)
+}
+
+template <int kPart>
+__global__ void __launch_bounds__(kRT, 1) release_part_kernel(const ReleaseSharedArgs a) {
+    extern __shared__ int sm[];
+    __shared__ int warp_sums[kRT / 32];
+    const int nct = gridDim.x, rank = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int *const pushes = a.last + a.num_pages;  // [kReleaseMaxWarps], a warp's
+    griddep_wait();
+    griddep_launch_dependents();
+    if (kPart == 0) mark_pages(a, rank, nct);
+    if (kPart == 0 && rank > 0) return;
+    const Shares s = plan_shares(a, sm, warp_sums, kPart == 0);
+    const int w = rank * (kRT / 32) + warp, n = nct * (kRT / 32);
+    const Run run = run_of(s.total, w, n);
+    if (kPart == 1) count_entries(a, s, rank, nct);
+    if (kPart == 2) {
+        const int mine = count_pushes(a, s, run, lane);
+        if (lane == 0) pushes[w] = mine;
+    }
+    if (kPart == 3) {
+        const int first = rank * (kRT / 32);
+        int before = 0, behind = 0, all, ahead;
+        for (int i = threadIdx.x; i < n; i += kRT) (i < first ? before : behind) += pushes[i];
+        block_scan<kRT>(before, warp_sums, &ahead);
+        block_scan<kRT>(behind, warp_sums, &all);
+        const int own = warp_scan(pushes[first + lane], lane);  // (all of the CTA's, in every warp)
+        const int at = ahead + (warp > 0 ? __shfl_sync(0xffffffffu, own, (warp - 1) & 31) : 0);
+        if (rank == 0 && threadIdx.x == 0) *a.new_free_count = new_free(a, s, (long long)ahead + all);
+        push_pages(a, s, run, at, lane);
+    }
 }
 
 // Room in shared memory for any call, asked for once a device and kernel.
@@ -424,6 +503,19 @@ sv_status launch_release_shared(const ReleaseSharedArgs &a, cudaStream_t st) {
     void *args[] = {&ka};
     const size_t smem = (size_t)(2 * a.B + 1) * sizeof(int);
     if (smem > 40 * 1024) return SV_ERR_UNSUPPORTED;  // (never: B <= 4096)
+    const long long entries = (long long)a.B * a.max_pages;
+    if (entries > kClusterEntries) {
+        const int sms = device_sm_count();
+        if (sms <= 0) return SV_ERR_CUDA;
+        long long grid = (entries + 2 * kRT - 1) / (2 * kRT);
+        if (grid > sms) grid = sms;
+        if (grid > kReleaseMaxWarps / (kRT / 32)) grid = kReleaseMaxWarps / (kRT / 32);
+        const void *parts[] = {(const void *)release_part_kernel<0>, (const void *)release_part_kernel<1>,
+                               (const void *)release_part_kernel<2>, (const void *)release_part_kernel<3>};
+        for (const void *part : parts)
+            if (launch_pdl(part, dim3((unsigned)grid), dim3(kRT), smem, st, args) != cudaSuccess) return SV_ERR_CUDA;
+        return SV_OK;
+    }
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = kReleaseCluster;

@@ -337,8 +337,9 @@ struct ReleaseSharedArgs {
     int32_t *new_free_count;
     int32_t *new_shares;
     int32_t *seq_status;
-    int *last;  // [num_pages], the workspace: a shared page's last entry
+    int *last;  // the workspace: [num_pages] a shared page's last entry, [kReleaseMaxWarps] pages that a warp pushes
 };
+constexpr int kReleaseMaxWarps = 8192;
 
 sv_status launch_fork_tables(const ForkArgs &args, cudaStream_t stream);
 sv_status launch_copy_pages(const CopyPagesArgs &args, cudaStream_t stream);
