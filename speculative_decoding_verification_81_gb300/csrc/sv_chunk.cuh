@@ -51,7 +51,7 @@ constexpr int kVSlots = kStagesOf<D, true> / 2;
 constexpr int kSlotBytes = kBK * 8;
 template <int D, bool kQuant>
 constexpr int kRawBytes = kQuant ? kRawStages<D> * kRawTile<D> + kKSlots<D> * kSlotBytes + kVSlots<D> * 32 : 0;
-constexpr int kLeastV = -30;             // the least exponent of V's
+constexpr int kLeastV = -90;             // the least exponent of V's (a row's l stays below 2^(8 + 90) a slot)
 
 struct Params {
     uint16_t *out;

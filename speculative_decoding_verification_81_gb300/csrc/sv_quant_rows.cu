@@ -357,7 +357,8 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const Ro
                 km[r] = __fmaf_rn(8.f, bf16_lo(kp), bf16_hi(kp)) * p.scale_log2;
                 vs[r] = bf16_lo(vp);
                 vm[r] = __fmaf_rn(8.f, vs[r], bf16_hi(vp));
-                bound[r] = kRoom - fmaxf(lg2_approx(fabsf(vs[r])), kLeast);
+                // (a step that is nothing beside the middle counts as 2^-24 of it: what the weight meets is no larger)
+                bound[r] = kRoom - fmaxf(lg2_approx(fmaxf(fabsf(vs[r]), fabsf(vm[r]) * 0x1p-24f)), kLeast);
             }
             const bool masked = slot0 + kU > all_hi || slot0 < all_lo;
             bool over = false;

@@ -13,7 +13,7 @@ constexpr int kRowsMaxGrid = 512;  // CTAs of a call at most: the workspace's sh
 constexpr int kRowsMost = 16;      // columns of a mean sequence up to which a call takes this form
 constexpr float kUnset = -1e38f;   // u of a column that has seen no slot
 constexpr float kRoom = 12.f;      // log2 of the largest P
-constexpr float kLeast = -60.f;    // log2 of a step below which it counts as this much for u
+constexpr float kLeast = -90.f;    // log2 of a step below which it counts as this much for u (l stays below 2^(12 + 90) a slot)
 
 struct RowsParams : QuantParams {
     const uint16_t *q;
