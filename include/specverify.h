@@ -516,10 +516,10 @@ sv_status sv_append_kv_quant(const void *k_new, const void *v_new, sv_dtype dtyp
  *            prefix_lens[b] and those of the nodes on its path, its own too.  A
  *            sequence whose parents are none such, or whose rows are more, is
  *            reported as SV_ERR_BAD_INPUT, its rows unspecified.  Not with a window
- * For few rows the codes themselves are multiplied and steps and minima applied
- * to the f32 scores and to the weights before these are rounded to bf16;
- * otherwise a value is rounded to bf16 before the products, to what a bf16 cache
- * would hold of it.  The rest is as in that call.
+ * A score is the f32 of the cache's values, which are not rounded; weights and,
+ * for more than 16 rows times heads of a KV head in the mean sequence, the values
+ * of V are rounded to f16 under a common exponent.  V's steps below 2^-90 count as
+ * that much.  The rest is as in that call.
  * Supported: as sv_chunk_attention_paged.
  */
 sv_status sv_chunk_attention_quant(const void *q, long long q_stride, const void *k_codes,

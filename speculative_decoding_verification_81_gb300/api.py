@@ -881,6 +881,12 @@ def sv_chunk_attention_paged(q, k_pages, v_pages, block_table, prefix_lens, row_
     return out if lse is None else (out, lse)
 
 
+def _given_ws(ws, dev):
+    if not isinstance(ws, torch.Tensor):
+        raise TypeError("ws must be a tensor")
+    return _arr(ws, "ws", torch.uint8, ws.shape, dev)
+
+
 def _quant_pages(k_codes, k_params, v_codes, v_params):
     """The four arrays of a cache held in 4 bits: their pointers, the device and
     the sizes (num_pages, Hkv, page_size, D)."""
@@ -966,7 +972,7 @@ def sv_chunk_attention_quant(q, k_codes, k_params, v_codes, v_params, block_tabl
             p_q, q_stride, p_k, p_kp, p_v, p_vp, p_tab, max_pages, num_pages, page_size, p_pre, p_row, p_par, B,
             num_rows, Hq, Hkv, D, float(scale), window, _arr(out, "out", bf16, (num_rows, Hq, D), dev),
             _opt_arr(lse, "lse", torch.float32, (num_rows, Hq), dev), p_st,
-            _arr(ws, "ws", torch.uint8, ws.shape, dev), ws.numel(), s)
+            _given_ws(ws, dev), ws.numel(), s)
     _check("sv_chunk_attention_quant", rc)
     return out if lse is None else (out, lse)
 
@@ -1121,7 +1127,7 @@ def sv_release_shared_pages(keep_lens, page_counts, block_table, free_pages, fre
             ws = torch.empty(sv_workspace_size(SV_OP_RELEASE_SHARED_PAGES, 0, num_pages), dtype=torch.uint8, device=dev)
         rc = lib().sv_release_shared_pages(p_keep, p_cnt, p_tab, p_stk, p_fc, p_sh, B, page_size, max_pages, num_pages,
                                            new_page_counts.data_ptr(), new_free_count.data_ptr(), new_shares.data_ptr(),
-                                           p_st, _arr(ws, "ws", torch.uint8, ws.shape, dev), ws.numel(), s)
+                                           p_st, _given_ws(ws, dev), ws.numel(), s)
     _check("sv_release_shared_pages", rc)
     return new_page_counts, new_free_count, new_shares
 

@@ -13,7 +13,7 @@ namespace chunk {
 constexpr int kBK = kTileSlots;          // slots of a K/V tile
 constexpr int kRows = 128;               // rows of a Q tile (the MMA's M)
 constexpr int kBox = kBK * 64 * 2;       // 128 rows of 64 dims: 16 KB
-constexpr int kExpandWarps = 4;          // that turn tiles held in 4 bits into bf16
+constexpr int kExpandWarps = 4;          // that turn tiles held in 4 bits into operands
 template <bool kQuant>
 constexpr int kThreadsOf = 32 * (kQuant ? 12 + kExpandWarps : 12);
 // bf16 pages: 256 x 200 + 128 x 104 = 384 x 168; in 4 bits: 256 x 176 + 256 x 80 = 512 x 128

@@ -1,9 +1,9 @@
 // sv_quant.cuh -- the 4-bit form of a K or V row.
 //
 // Codes c_d (0 .. 15) and two bf16 numbers: x_d ~ minimum + step * c_d.  One
-// step and minimum a row and head: K's fold into the scores (step * (q . c) +
-// minimum * sum(q)) and V's into the weights, so that a product with the codes
-// themselves, exact in bf16, is all that a matrix instruction has to do.
+// step and minimum a row and head: K's are applied to the f32 scores (step * (q .
+// (c - 8)) + (minimum + 8 step) * sum(q)), so that the products have to do with codes
+// alone, which are exact in bf16 and f16.
 //
 // Eight codes are a word, dims 0, 2, 4, 6, 1, 3, 5, 7 from its lowest four bits
 // up: the word shifted right by 4 i and masked has dims 2i and 2i + 1 in its two
@@ -31,13 +31,6 @@ __device__ __forceinline__ uint32_t centred(uint32_t pair) {
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(x), "r"(0x43084308u));
     return c;
 }
-// A word's eight codes as 1 + code / 16 in bf16, dims 0 .. 7 in order: a code in the first bits behind
-// the point, no subtraction.
-__device__ __forceinline__ uint4 sixteenths(uint32_t w) {
-    constexpr uint32_t kMask = 0x00780078u, kOne = 0x3f803f80u;
-    return make_uint4((w << 3 & kMask) | kOne, (w >> 1 & kMask) | kOne, (w >> 5 & kMask) | kOne, (w >> 9 & kMask) | kOne);
-}
-
 // The same as a pair of f16 (in the last bits of 1024).
 __device__ __forceinline__ uint32_t centred_f16(uint32_t pair) {
     const uint32_t x = (pair & 0x000f000fu) | 0x64006400u;

@@ -1,9 +1,9 @@
 // sv_quant_rows.cu -- attention over pages held in 4 bits, form for few rows a
-// sequence: single tokens, chains, draft trees.
+// sequence: single tokens and short chains.
 //
 // An item is the rows of some tokens of one sequence and the heads of them that
-// share K/V: up to 8 NT columns.  Each of the CTA's eight warps takes 16 slots of
-// every 128-slot tile and goes on by itself to the item's end:
+// share K/V: up to 8 NT columns, NT = 1 or 2.  Each of the CTA's eight warps takes 16
+// slots of every 128-slot tile and goes on by itself to the item's end:
 //     S = codes Q^T             (16 slots x 8 NT columns; codes less 8, exact in bf16)
 //     s = step_k S + middle_k sum(q), scaled to log2 units
 //     P = 2^(s - u) step_v, rounded to f16; l += 2^(s - u); z += 2^(s - u) middle_v
@@ -21,6 +21,17 @@
 // pages' bytes, and read from there for a column count that is mostly padding; and a
 // slot's step and middle are a lane's own, where a thread a row needs each of them
 // from shared memory.
+//
+// Every lane copies its 16 bytes of a unit four units ahead (cp.async): with a bulk
+// copy for each of a page's four parts 32 single tokens took 51 us instead of 44.
+//
+// What bounds it (32 query over 8 KV heads of 128): the instructions, some 320 a unit
+// of which the integer pipe has half (52% busy, 2.1 of 4 issue slots taken), and the
+// barriers where an item's warps meet -- 32 single tokens after 2048-4096 slots 44 us,
+// 0.36 of the measured bandwidth, 64 after 4096 97 us, 0.44.  One token after 2047
+// slots is 12.6 us: the launch, the list, the page table, the pages and the joining of
+// some 70 CTAs' shares one after another.  S in sums of their own, so that no product
+// waits for another: no gain.
 #include <mutex>
 
 #include "sv_attn_common.cuh"
@@ -39,19 +50,16 @@ constexpr int kU = 16;                  // slots of a unit
 // K codes, V codes, K's and V's parameters of a unit.
 template <int D>
 constexpr int kUnitRaw = kU * (D + 8);
-template <int NT>
-constexpr int kCtasAnSm = NT <= 2 ? 2 : 1;
-template <int D, int NT>
-constexpr int kRowsDepth = D == 128 ? (NT <= 2 ? 4 : 6) : 8;  // units of a warp on their way
-template <int NT>
-constexpr int kMeet = NT <= 2 ? 1 : 2;  // blocks of 8 columns that the warps bring together at once
+constexpr int kCtasAnSm = 2;
+template <int D>
+constexpr int kRowsDepth = D == 128 ? 4 : 8;  // units of a warp on their way
 template <int D>
 constexpr int kMeetBytes = kRW * 8 * D * 4;
 
 template <int D, int NT>
 struct RowsShared {
-    uint8_t ring[kRW][kRowsDepth<D, NT>][kUnitRaw<D>];
-    float4 meet[kMeet<NT> * kMeetBytes<D> / 16];
+    uint8_t ring[kRW][kRowsDepth<D>][kUnitRaw<D>];
+    float4 meet[kMeetBytes<D> / 16];
     uint8_t q[2][8 * NT * D * 2];
     float qs[8 * NT];
     float u[kRW][8 * NT];
@@ -140,8 +148,8 @@ __device__ __forceinline__ int slot_of(int r) { return r ^ (r >> 1 & 1); }
 }  // namespace
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const RowsParams p) {
-    constexpr int kDepth = kRowsDepth<D, NT>;
+__global__ void __launch_bounds__(kRT, kCtasAnSm) quant_rows_kernel(const RowsParams p) {
+    constexpr int kDepth = kRowsDepth<D>;
     constexpr int kRow = D / 2;   // bytes of a row's codes
     constexpr int kW = D / 32;    // words of a K row a lane: words kW t + j
     constexpr int kX = D / 16;    // blocks of 16 dims of O^T
@@ -167,7 +175,7 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const Ro
     };
     {
         RowsWalk walk;
-        plan_walk<kRT>(p, sh.warp_units, sh.before, tid, 0, walk);
+        plan_walk<kRT>(p, sh.warp_units, sh.before, tid, walk);
         if (tid == 0) {
             sh.walk = walk;
             sh.items[1].b = 0;
@@ -483,23 +491,17 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const Ro
             return c < cols && hd < heads ? (long long)(cur.row0 + tk) * p.Hq + head0 + hd : -1;
         };
 #pragma unroll
-        for (int n0 = 0; n0 < NT; n0 += kMeet<NT>) {
-            if (n0 >= nt) break;
+        for (int n = 0; n < NT; ++n) {  // a block of 8 columns
+            if (n >= nt) break;
 #pragma unroll
-            for (int dn = 0; dn < kMeet<NT>; ++dn) {
-                const int n = n0 + dn;
-                if (n >= NT || n >= nt) break;
-#pragma unroll
-                for (int x = 0; x < kX; ++x)
-                    sh.meet[((warp * kMeet<NT> + dn) * kX + x) * 32 + lane] =
-                        make_float4(o[x][n][0] + z[n][0], o[x][n][1] + z[n][1], o[x][n][2] + z[n][0], o[x][n][3] + z[n][1]);
-            }
+            for (int x = 0; x < kX; ++x)
+                sh.meet[(warp * kX + x) * 32 + lane] =
+                    make_float4(o[x][n][0] + z[n][0], o[x][n][1] + z[n][1], o[x][n][2] + z[n][0], o[x][n][3] + z[n][1]);
             __syncthreads();
-            if (n0 == 0 && sh.items[qb ^ 1].b >= 0) begin(sh.items[qb ^ 1], qb ^ 1);  // (its copies run while the sums meet)
+            if (n == 0 && sh.items[qb ^ 1].b >= 0) begin(sh.items[qb ^ 1], qb ^ 1);  // (its copies run while the sums meet)
             // a task: eight dims of two columns
-            for (int i = tid; i < kMeet<NT> * (kX / 4) * 32; i += kRT) {
-                const int ln = i & 31, w4 = (i >> 5) % (kX / 4), dn = (i >> 5) / (kX / 4), n = n0 + dn;
-                if (n >= nt) break;
+            for (int i = tid; i < kX / 4 * 32; i += kRT) {
+                const int ln = i & 31, w4 = i >> 5;
                 const int c0 = 8 * n + 2 * (ln & 3);
                 float M[2] = {kUnset, kUnset}, sum[2] = {0.f, 0.f}, f[2][kRW], acc[2][8] = {};
 #pragma unroll
@@ -518,7 +520,7 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm<NT>) quant_rows_kernel(const Ro
 #pragma unroll
                     for (int b = 0; b < 4; ++b) {
                         constexpr int kDim[4][2] = {{0, 2}, {4, 6}, {1, 3}, {5, 7}};
-                        const float4 v = sh.meet[((w * kMeet<NT> + dn) * kX + 4 * w4 + b) * 32 + ln];
+                        const float4 v = sh.meet[(w * kX + 4 * w4 + b) * 32 + ln];
                         acc[0][kDim[b][0]] = __fmaf_rn(v.x, f[0][w], acc[0][kDim[b][0]]);
                         acc[1][kDim[b][0]] = __fmaf_rn(v.y, f[1][w], acc[1][kDim[b][0]]);
                         acc[0][kDim[b][1]] = __fmaf_rn(v.z, f[0][w], acc[0][kDim[b][1]]);
@@ -609,7 +611,7 @@ struct Form {
 
 template <int D, int NT>
 Form form() {
-    return Form{reinterpret_cast<const void *>(&quant_rows_kernel<D, NT>), 8 * NT, (int)sizeof(RowsShared<D, NT>), kCtasAnSm<NT>};
+    return Form{reinterpret_cast<const void *>(&quant_rows_kernel<D, NT>), 8 * NT, (int)sizeof(RowsShared<D, NT>), kCtasAnSm};
 }
 
 constexpr int kForms = 2;

@@ -4,12 +4,41 @@
 // Source: as sv_chunk_tc.cu, which says how the steps, items and warps go
 // together.  What differs: warps 8 and 11 copy the codes and parameters of K and
 // V tiles to a ring of their own (8.5 KB a tile at D = 128 for 32), and warps
-// 12-15, a thread a slot, turn each into bf16 values in the swizzled tiles that
-// the products read.  A value is minimum + step * code rounded once to bf16, what
-// a cache in bf16 would hold of it; a slot that no row of the item sees is zeros.
-// A row may be a node of a draft tree: it then sees the slots before its sequence's
-// rows and its own path's, a 64-bit set that each softmax thread makes of the
-// parents.
+// 12-15, a thread a slot, turn each into 16-bit operands in the swizzled tiles that
+// the products read:
+//     S = Q (codes_k - 8)^T               (bf16 products; the codes are exact)
+//     x = step_k S + middle_k sum(q)      (f32, log2 units; middle = minimum + 8 steps)
+//     P = 2^(x + e - m), rounded to f16;  l += 2^(x - m)
+//     O += P V 2^-e                       (f16 products)
+// where e is the exponent of the largest value of V in a warp's 32 slots, fourteen
+// less: V 2^-e stays below 2^15 and keeps 2^-12 of itself down to 2^-28 of that
+// largest value.  K is not rounded at all -- a score's error would be in the
+// log-sum-exp, which is f32 -- and P and V lose 2^-11 together, a quarter of what the
+// output's own rounding to bf16 takes (error against 64 bits 1.7e-3 of the output's
+// size, which is that rounding; with P and V in bf16 it was 3.4e-3).  A slot that no
+// row of the item sees is zeros.  A row may be a node of a draft tree: it then sees
+// the slots before its sequence's rows and its own path's, a 64-bit set that each
+// softmax thread makes of the parents.
+//
+// Why not the values of K in 16 bits: two parts of them are needed for the scores'
+// last bits, which makes three products of two.  Why queries as the rows of S although
+// every thread then reads every slot's step and middle (64 reads of 16 bytes a tile):
+// with slots as the rows a thread has its own, but a tile does 48 columns' work
+// instead of 128 or 256 and its barriers cost what they cost here (2048 rows after
+// 14336 slots 1390 us against 538, trees of 26 80 against 34; chains of 9 97 and 85).
+//
+// What bounds it (32 query over 8 KV heads of 128): the chain of a step's parts and
+// the one instruction cache that all roles are fetched through, not the tensor core
+// (2048 rows after 14336 slots 538 us, 0.51 of the measured rate; a prompt of 4096
+// 181 us, 0.40) nor memory (chains of 9 after 2048-4096 slots for 32 requests 85 us,
+// 0.19 of the measured bandwidth, and the same for 8 to 40 columns a sequence).  A
+// step's softmax takes 2600 cycles, a tile's expansion 900 for K and 900 for V.
+// Ablations of the latter: without the scores' constants 490 us, without exponentials
+// 485, without the operands' stores 470, without the three 340.
+// Tried without gain: the expansion by eight warps, four for K and four for V (fewer
+// registers for the softmax); tiles copied by each expanding warp in 16-byte pieces
+// (chains 133 us) or loaded to registers a tile ahead (121); three places for tiles
+// and six for codes; 152 or 144 registers for the softmax.
 #include "sv_chunk_tc.cuh"
 
 namespace sv {

@@ -14,7 +14,6 @@ __device__ __forceinline__ float lg2_approx(float x) {
     return y;
 }
 
-
 struct RowsItem {
     int b, h;          // sequence (-1: no more), group of heads
     int row0, ntok;    // first row, tokens
@@ -103,9 +102,9 @@ static __device__ __noinline__ bool bad_sequence(const RowsParams &p, int sb, in
 }
 
 // This CTA's share of the list, by its kT threads together: units before each thread's sequences
-// (`before`, kT of them; warp_units, kT / 32), then, for warp `who`, the place where the share begins.
+// (`before`, kT of them; warp_units, kT / 32), then, for warp 0, the place where the share begins.
 template <int kT>
-__device__ __forceinline__ void plan_walk(const RowsParams &p, long long *warp_units, long long *before, int tid, int who, RowsWalk &w) {
+__device__ __forceinline__ void plan_walk(const RowsParams &p, long long *warp_units, long long *before, int tid, RowsWalk &w) {
     const int lane = tid & 31, warp = tid >> 5;
     const int per = (p.B + kT - 1) / kT, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
     long long mine = 0;
@@ -139,7 +138,7 @@ __device__ __forceinline__ void plan_walk(const RowsParams &p, long long *warp_u
     w.ui = 0;
     w.h = w.i = 0;
     w.loaded = false;
-    if (has && warp == who) {  // the last thread with at most u0 units before its sequences, then the sequence
+    if (has && warp == 0) {  // the last thread with at most u0 units before its sequences, then the sequence
         int at = 0;
 #pragma unroll 1
         for (int i = lane; i < kT; i += 32) at += before[i] <= w.u0;

@@ -1,16 +1,15 @@
 """The cache held in 4 bits and the attention over it from their definitions,
 in 64 bits, with the bounds that the kernels' roundings allow.
 
-Bounds, beside those of chunk_ref.py (P in bf16 among them), for one output
+Bounds, beside those of chunk_ref.py (P in 16 bits among them), for one output
 element with weights w_j, A = sum_j w_j |v_j|, S = sum_j w_j 8 step_j and
-Q = max_j scale * sum_d |q_d k_jd|.  The form for many rows rounds the values of K
-and V to bf16, each off by at most 2^-8 of itself: scores by at most 2^-8 Q, the
-weights by as much relative, in the numerator and in the sum, 2 Q 2^-8 A (and its
-square, for exp), and V 2^-8 A.  The form for few rows multiplies the codes
-themselves: w_j step_j is rounded to bf16 before it meets codes - 8, of 8 at most,
-2^-8 S; its scores are sums of products with 128 + code, the part of 128 taken off
-again, whose f32 sums are off by at most Q' 2^-16, Q' = scale * sum_d |q_d| (143 step +
-|minimum|).
+Q = max_j scale * sum_d |q_d k_jd|: values of K and V rounded to bf16 would each be
+off by at most 2^-8 of themselves, scores by at most 2^-8 Q, the weights by as much
+relative, in the numerator and in the sum, 2 Q 2^-8 A (and its square, for exp), and V
+2^-8 A; w_j step_j in 16 bits before it meets codes - 8, of 8 at most, 2^-8 S; scores
+from sums of codes that a larger part is taken off again, whose f32 sums are off by at
+most Q' 2^-16, Q' = scale * sum_d |q_d| (143 step + |minimum|).  The kernels stay
+below: K's codes are exact, P and V (or P and its step) in f16, off by 2^-11.
 """
 import numpy as np
 import torch
