@@ -1,10 +1,10 @@
 """libspecverify: the target model's verification step of speculative
 decoding on one GB300 (sm_103a) -- tree/chain verification attention,
 full-vocabulary stochastic (chain and tree) and greedy (tree) acceptance, KV
-compaction, the fused step that runs them side by side, and the paged cache
-around it (page tables, new rows, attention of prompt chunks) -- as hand-written
-CUDA kernels behind a C ABI (include/specverify.h), with this thin Python
-binding on top.
+compaction, the fused step that runs them side by side, the paged cache around
+it (page tables, new rows, attention of prompt chunks), the same cache held in 4
+bits and requests that share its pages -- as hand-written CUDA kernels behind a
+C ABI (include/specverify.h), with this thin Python binding on top.
 """
 from .api import (SV_BF16, SV_ERR_BAD_INPUT, SV_ERR_CUDA, SV_ERR_INVALID_ARG, SV_ERR_NO_PAGES,
                   SV_ERR_TIMEOUT, SV_ERR_UNSUPPORTED, SV_ERR_WORKSPACE, SV_F32, SV_OK, SV_OP_CHUNK_ATTENTION,
