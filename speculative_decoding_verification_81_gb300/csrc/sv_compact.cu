@@ -51,7 +51,8 @@ __global__ void __launch_bounds__(kCT) compact_kv_kernel(CompactArgs a) {
         const int32_t *path = a.path_nodes + (size_t)b * a.path_stride;
         for (int d = threadIdx.x; d <= acc; d += kCT) {
             const int src = path[d];
-            if (d == 0 ? src != 0 : src <= path[d - 1]) bad = 1;
+            // (an increasing path from 0 has path[d] >= d: nothing below is looked up)
+            if (d == 0 ? src != 0 : src <= path[d - 1] || src < d) bad = 1;
             if ((long long)L + src >= a.S_max) bad = 1;
             if (!bad && a.block_table && (!page_ok(L + src) || !page_ok(L + d))) bad = 1;
         }
