@@ -68,10 +68,10 @@ __global__ void __launch_bounds__(kFT) copy_shares_kernel(const int32_t *shares,
                                                           int32_t *status, int n) {
     griddep_wait();
     griddep_launch_dependents();
-    const int first = blockIdx.x * kFT + threadIdx.x, step = gridDim.x * kFT;
-    for (int i = first; i < num_pages; i += step) new_shares[i] = max(shares[i], 0);
+    const long long first = (long long)blockIdx.x * kFT + threadIdx.x, step = (long long)gridDim.x * kFT;
+    for (long long i = first; i < num_pages; i += step) new_shares[i] = max(shares[i], 0);
     if (status)
-        for (int i = first; i < n; i += step) status[i] = SV_OK;
+        for (long long i = first; i < n; i += step) status[i] = SV_OK;
 }
 
 // Fork f: the first fork_lens[f] slots of sequence sources[f] for targets[f], which
@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(kFT) fork_tables_kernel(const ForkArgs a) {
         if (code != SV_OK && a.fork_status) atomicMax(&a.fork_status[f], code);
     }
     // the shared entries
-    for (int i = first; i < total; i += step) {
-        const int f = last_at_most(starts, a.F, i), j = i - starts[f];
+    for (long long i = first; i < total; i += step) {
+        const int f = last_at_most(starts, a.F, (int)i), j = (int)i - starts[f];
         const int pg = a.block_table[(size_t)src[f] * a.max_pages + j];
         a.block_table[(size_t)tgt[f] * a.max_pages + j] = pg;
         if (pg >= 0 && pg < a.num_pages) atomicAdd(&a.new_shares[pg], 1);
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kPT) copy_pages_kernel(const __grid_constant__
 constexpr int kRT = 1024;
 constexpr int kRPer = kMaxSeqs / kRT;
 constexpr int kReleaseCluster = 8;
-constexpr long long kClusterEntries = 16384;  // entries of the table up to which one cluster gives pages back
+constexpr long long kClusterEntries = 49152;  // entries of the table up to which one cluster gives pages back
 static_assert(kRT / 32 == 32, "a lane a warp of the CTA");
 
 // Entries that the sequences give up, in sequence order; a page whose count of
@@ -252,8 +252,11 @@ static_assert(kRT / 32 == 32, "a lane a warp of the CTA");
 // pages of its run of consecutive entries that go to the stack; it pushes them.
 //
 // Up to kClusterEntries entries one cluster does all four and meets between them;
-// above, four launches over the whole GPU do (2048 branches of 2048 tokens: 57 us
-// in one cluster, whose eight SMs are then what bounds it).
+// above, four launches over the whole GPU do.  Both measured, us, the cluster first:
+// tables of 2 thousand entries 8.9 and 11.8, of 31 thousand 11.9 and 14.7, of 300
+// thousand (2048 branches of 2048 tokens) 57 and 22.6, where the cluster's eight SMs
+// are what bounds it.  One CTA alone is 0.3 us quicker for 2 thousand and 5 us slower
+// for 8 thousand.
 struct Shares {
     const int *upto, *kept;  // entries before each sequence, pages that it keeps
     int total, nfree;
@@ -302,7 +305,7 @@ __device__ __forceinline__ Shares plan_shares(const ReleaseSharedArgs &a, int *s
 }
 
 __device__ __forceinline__ void mark_pages(const ReleaseSharedArgs &a, int rank, int nct) {
-    for (int i = rank * kRT + threadIdx.x; i < a.num_pages; i += nct * kRT) {
+    for (long long i = rank * kRT + threadIdx.x; i < a.num_pages; i += nct * kRT) {
         a.new_shares[i] = max(a.shares[i], 0);
         a.last[i] = -1;
     }
@@ -332,14 +335,15 @@ struct Run {
     int first, end;
 };
 __device__ __forceinline__ Run run_of(int total, int w, int n) {
-    const int run = (total + n - 1) / n;
-    const int first = (int)min((long long)w * run, (long long)total);
-    return Run{first, min(first + run, total)};
+    const long long run = ((long long)total + n - 1) / n;
+    const int first = (int)min(w * run, (long long)total);
+    return Run{first, (int)min((long long)first + run, (long long)total)};
 }
 
 // Whether the page of entry e, below end, goes to the stack.
-__device__ __forceinline__ bool goes(const ReleaseSharedArgs &a, const Shares &s, int e, int end, int &pg, int &b) {
-    if (e >= end) return false;
+__device__ __forceinline__ bool goes(const ReleaseSharedArgs &a, const Shares &s, long long x, int end, int &pg, int &b) {
+    if (x >= end) return false;
+    const int e = (int)x;
     pg = entry_page(a, s, e, b);
     if (pg < 0 || pg >= a.num_pages) return false;
     if (a.shares[pg] <= 0) return true;
@@ -348,18 +352,20 @@ __device__ __forceinline__ bool goes(const ReleaseSharedArgs &a, const Shares &s
 
 __device__ __forceinline__ int count_pushes(const ReleaseSharedArgs &a, const Shares &s, const Run &run, int lane) {
     int mine = 0;
-    for (int e = run.first; e < run.end; e += 32) {
+    for (long long x = run.first; x < run.end; x += 32) {
+        const int e = (int)x;
         int pg, b;
-        mine += __popc(__ballot_sync(0xffffffffu, goes(a, s, e + lane, run.end, pg, b)));
+        mine += __popc(__ballot_sync(0xffffffffu, goes(a, s, (long long)e + lane, run.end, pg, b)));
     }
     return mine;
 }
 
 // The run's pages, to the stack's places from nfree + at on.
 __device__ __forceinline__ void push_pages(const ReleaseSharedArgs &a, const Shares &s, const Run &run, int at, int lane) {
-    for (int e = run.first; e < run.end; e += 32) {
+    for (long long x = run.first; x < run.end; x += 32) {
+        const int e = (int)x;
         int pg, b;
-        const bool push = goes(a, s, e + lane, run.end, pg, b);
+        const bool push = goes(a, s, (long long)e + lane, run.end, pg, b);
         const uint32_t votes = __ballot_sync(0xffffffffu, push);
         if (push) {
             const long long to = (long long)s.nfree + at + __popc(votes & ((1u << lane) - 1u));

@@ -177,6 +177,8 @@ def test_bad_forks():
     (4096, 8, 100, 64, 16, 5),
     (3, 3, 200000, 1, 16, 6),
     (513, 2, 50, 50, 1, 7),
+    (3000, 4, 300, 40, 8, 8),   # a table of more entries than one cluster takes
+    (4096, 2, 40, 100, 8, 9),
 ])
 def test_release_shared(B, g, past_hi, new_hi, ps, seed):
     rng = np.random.default_rng(seed)

@@ -8,6 +8,7 @@ import torch
 
 import quant_ref
 import speculative_decoding_verification_81_gb300 as sv
+from test_gpu_chunk import Case as Bf16Case
 from test_gpu_quant import Case, i32, near
 
 pytestmark = pytest.mark.gpu
@@ -102,9 +103,13 @@ def fixed(c):
 
 
 def test_forms_take_turns_in_one_workspace():
-    """Every call of a kind has one answer, bit for bit, whatever ran before it in the workspace."""
+    """Every call of a kind has one answer, bit for bit, whatever ran before it in the workspace, which
+    the calls over the bf16 cache share."""
     cases = {name: Case(lens, seed=3, **kw) for name, (lens, kw) in CASES.items()}
-    first = {name: c.check() for name, c in cases.items()}
+    for name in ("single tokens", "a prompt", "many single tokens"):
+        lens, kw = CASES[name]
+        cases[f"{name}, bf16"] = Bf16Case(lens, seed=3, **kw)
+    first = {name: [t.clone() for t in c.run()] for name, c in cases.items()}
     rng = np.random.default_rng(4)
     for name in rng.choice(list(cases), 60):
         assert same(cases[name].run(), first[name]), name
@@ -134,7 +139,7 @@ def test_captured_and_replayed(name):
 
 def test_tables_and_rows_captured():
     rng = np.random.default_rng(6)
-    B, ps, mp = 2100, 16, 9
+    B, ps, mp = 2100, 16, 30
     held = rng.integers(1, mp + 1, B)
     ids = rng.permutation(int(held.sum()) + 7)
     table = np.full((B, mp), -1)
