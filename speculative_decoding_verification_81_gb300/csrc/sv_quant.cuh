@@ -19,10 +19,6 @@ constexpr float kFifteenth = 0.06666667014360428f;  // 1 / 15 in f32
 constexpr float kSmallestStep = 1.1754943508222875e-38f;  // 2^-126: below it 1 / step may not be finite
 constexpr uint32_t kNotFinite = 0x7fc00000u;        // step 0, minimum NaN: a row that has no encoding
 
-__device__ __forceinline__ uint32_t pack(const uint32_t (&c)[8]) {
-    return c[0] | c[2] << 4 | c[4] << 8 | c[6] << 12 | c[1] << 16 | c[3] << 20 | c[5] << 24 | c[7] << 28;
-}
-
 // A pair of codes in the last four bits of each half, less 8, as a pair of bf16: in the last bits of
 // 128 a code is 128 + code, and what is taken off is exact.
 __device__ __forceinline__ uint32_t centred(uint32_t pair) {
