@@ -98,7 +98,7 @@ sv_status plan_chunk(int Hq, int Hkv, int D, bool quant, ChunkPlan *plan) {
     off = align_up(off + sizeof(int) * (size_t)pl.grid * 2 * chunk::kCtaCounters, 256);
     pl.off_rows = off;
     off = align_up(off + sizeof(int) * 2 * chunk::kRowsMaxGrid, 256);
-    static_assert(chunk::kRowsCols * 2 <= chunk::kRows, "twice the CTAs of half the rows find room in the shares' places");
+    static_assert(chunk::kRowsCols * 2 <= chunk::kRows, "twice the CTAs find room for their shares' rows");
     if (off > 64 * 1024 || pl.grid > chunk::kCallShares) return SV_ERR_UNSUPPORTED;  // (what starts as zeros; 1020 SMs)
     pl.off_part_ml = off;
     off = align_up(off + tiles * chunk::kRows * 2 * sizeof(float), 256);

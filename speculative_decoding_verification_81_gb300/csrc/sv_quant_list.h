@@ -1,10 +1,10 @@
 // sv_quant_list.h -- the work list of the attention over pages held in 4 bits,
 // form for few rows, as arithmetic on host or device.
 //
-// An item is up to `tok` consecutive rows of one sequence and one group of heads
-// that share K/V; its units are kRowsItemCost and one for each 128-slot tile that
+// An item is up to `tok` consecutive rows of one sequence and one KV head (all the
+// heads that share it); its units are kRowsItemCost and one for each 128-slot tile that
 // its rows see (a tile is a unit of 16 slots for each of a CTA's eight warps).  The
-// list runs over sequences, then groups of heads, then items, and is cut as the
+// list runs over sequences, then KV heads, then items, and is cut as the
 // other form's is (sv_chunk_list.h): CTA c of nctas takes units floor(U c / nctas)
 // .. floor(U (c + 1) / nctas) - 1 of the U.
 #pragma once
@@ -26,7 +26,7 @@ struct RowsShape {
 struct RowsSeq {
     int L, n;   // filled slots, new rows (0: none, or refused)
     int row0;   // its first row
-    int items;  // of one group of heads
+    int items;  // of one KV head
 };
 
 SV_HD RowsSeq rows_seq(const RowsShape &p, int L, int r0, int r1) {
@@ -50,7 +50,7 @@ SV_HD int rows_tiles(const RowsShape &p, const RowsSeq &s, int i) {
     return (s.L + t1 + kTileSlots - 1) / kTileSlots - rows_first_tile(p, s.L + t0);
 }
 
-// Units of items 0 .. i - 1 of one group of heads.
+// Units of items 0 .. i - 1 of one KV head.
 SV_HD_CALL long long rows_units_before(const RowsShape &p, const RowsSeq &s, int i) {
     if (i <= 0) return 0;
     long long u = (long long)i * kRowsItemCost;

@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm) quant_rows_kernel(const RowsPa
         auto row = [&](int s) -> int {  // (a page id out of range is reported; page 0 is read in its place)
             int pg = trow[s / p.page_size];
             if (pg < 0 || pg >= p.num_pages) pg = 0;
-            return (pg * p.Hkv + x.h / p.parts) * p.page_size + s % p.page_size;
+            return (pg * p.Hkv + x.h) * p.page_size + s % p.page_size;
         };
         y0 = y1 = -1;
         if (base + lane < i1) {
@@ -242,12 +242,11 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm) quant_rows_kernel(const RowsPa
         i1 = s0 < hi ? min(x.n, (hi - s0 - 1) / kTileSlots + 1) : 0;
         ask = base = i0;
         load_rows(x);
-        const int heads = min(p.Gs, p.G - x.h % p.parts * p.Gs), cols = x.ntok * p.Gs;
-        const int head0 = x.h / p.parts * p.G + x.h % p.parts * p.Gs;
+        const int cols = x.ntok * p.G, head0 = x.h * p.G;
         const uint32_t q_at = smem_u32(sh.q[buf]);
         for (int i = tid; i < 8 * NT * (D / 8); i += kRT) {
-            const int c = i / (D / 8), piece = i % (D / 8), tk = c / p.Gs, hd = c - tk * p.Gs;
-            const bool on = c < cols && hd < heads;
+            const int c = i / (D / 8), piece = i % (D / 8), tk = c / p.G, hd = c - tk * p.G;
+            const bool on = c < cols;
             const uint16_t *from = p.q + (size_t)(x.row0 + (on ? tk : 0)) * p.q_stride + (size_t)(head0 + (on ? hd : 0)) * D + piece * 8;
             copy16(q_at + q_piece<D>(c, piece), from, on);
             if (piece == 0) sh.tok[buf][c] = (uint8_t)min(tk, x.ntok - 1);
@@ -281,7 +280,7 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm) quant_rows_kernel(const RowsPa
     for (int qb = 0;; qb ^= 1) {
         const RowsItem it = sh.items[qb];
         if (it.b < 0) break;
-        const int cols = it.ntok * p.Gs, nt = (cols + 7) / 8;
+        const int cols = it.ntok * p.G, nt = (cols + 7) / 8;
         const int lo = p.rows.window > 0 ? max(0, it.pos0 - p.rows.window + 1) : 0, hi = it.pos0 + it.ntok;
         const int own0 = it.pos0 - (it.row0 - it.seq_row0);  // slot of the sequence's first new row
         // below: every row sees the slots; from all_lo on too
@@ -482,13 +481,11 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm) quant_rows_kernel(const RowsPa
         }
         const RowsItem cur = sh.items[qb];
         const bool whole = cur.nc == 1;
-        const int heads = min(p.Gs, p.G - cur.h % p.parts * p.Gs);
-        const int head0 = cur.h / p.parts * p.G + cur.h % p.parts * p.Gs;
         const int part = (int)blockIdx.x * 2 + (cur.ci == 0 ? 1 : 0);
         // where column c's row goes; -1: it is padding
         auto out_row = [&](int c) -> long long {
-            const int tk = c / p.Gs, hd = c - tk * p.Gs;
-            return c < cols && hd < heads ? (long long)(cur.row0 + tk) * p.Hq + head0 + hd : -1;
+            const int tk = c / p.G;
+            return c < cols ? (long long)(cur.row0 + tk) * p.Hq + cur.h * p.G + c - tk * p.G : -1;
         };
 #pragma unroll
         for (int n = 0; n < NT; ++n) {  // a block of 8 columns
@@ -659,24 +656,15 @@ int rows_form(const ChunkArgs &a) {
     return i;
 }
 
-static RowsParams rows_params(const ChunkArgs &a, const QuantParams &c, int cols) {
-    RowsParams p{};
-    static_cast<QuantParams &>(p) = c;
-    p.q = static_cast<const uint16_t *>(a.q);
-    p.q_stride = a.q_stride;
-    p.parts = (p.G + cols - 1) / cols;
-    p.Gs = (p.G + p.parts - 1) / p.parts;
-    p.groups = p.Hkv * p.parts;
-    p.rows = RowsShape{cols / p.Gs, c.shape.window, c.shape.num_rows, c.shape.S_max};
-    if (a.parents && p.rows.tok > kTreeNodes) p.rows.tok = kTreeNodes;
-    return p;
-}
-
 sv_status launch_rows(const ChunkArgs &a, const QuantParams &c, int form, cudaStream_t st) {
     const Form &f = form_at(a.D, form);
     const int grid = form_grid(a.D, form);
     if (grid <= 0 || grid > kRowsMaxGrid) return SV_ERR_CUDA;
-    RowsParams p = rows_params(a, c, f.cols);
+    RowsParams p{};
+    static_cast<QuantParams &>(p) = c;
+    p.q = static_cast<const uint16_t *>(a.q);
+    p.q_stride = a.q_stride;
+    p.rows = RowsShape{f.cols / p.G, c.shape.window, c.shape.num_rows, c.shape.S_max};  // (G is at most the mean's columns)
     void *args[] = {&p};
     return launch_pdl(f.fn, dim3((unsigned)grid), dim3(kRT), (size_t)f.smem, st, args) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }

@@ -8,7 +8,7 @@
 namespace sv {
 namespace chunk {
 
-constexpr int kRowsCols = 64;      // columns (rows times heads) of an item at most
+constexpr int kRowsCols = 16;      // columns (rows times heads) of an item at most
 constexpr int kRowsMaxGrid = 512;  // CTAs of a call at most: the workspace's shares and counters
 // Columns of a mean sequence up to which a call takes this form.  Both measured, us, this one first, for 32
 // requests after 2048-4096 slots: 4 columns 44 and 117, 8 columns 45 and 85, 16 columns 58 and 84; 24 columns
@@ -22,8 +22,6 @@ struct RowsParams : QuantParams {
     const uint16_t *q;
     long long q_stride;  // elements between rows of q
     RowsShape rows;
-    int parts, Gs;       // a KV head's query heads go in `parts` groups of Gs (the last may have fewer)
-    int groups;          // Hkv * parts
 };
 
 // The counter of an item shared from CTA `cta` on, in the set of the given call.

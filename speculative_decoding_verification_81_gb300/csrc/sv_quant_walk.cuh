@@ -15,7 +15,7 @@ __device__ __forceinline__ float lg2_approx(float x) {
 }
 
 struct RowsItem {
-    int b, h;          // sequence (-1: no more), group of heads
+    int b, h;          // sequence (-1: no more), KV head
     int row0, ntok;    // first row, tokens
     int pos0;          // position of the first token
     int seq_row0;      // the sequence's first row
@@ -43,7 +43,7 @@ __device__ __forceinline__ void next_item(const RowsParams &p, RowsWalk &w, Rows
             w.loaded = true;
             w.h = w.i = 0;
         }
-        if (w.seq.items == 0 || w.h == p.groups) {
+        if (w.seq.items == 0 || w.h == p.Hkv) {
             ++w.b;
             w.loaded = false;
             continue;
@@ -111,7 +111,7 @@ __device__ __forceinline__ void plan_walk(const RowsParams &p, long long *warp_u
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
         const RowsSeq s = load_seq(p, b);
-        mine += rows_units_before(p.rows, s, s.items) * p.groups;
+        mine += rows_units_before(p.rows, s, s.items) * p.Hkv;
     }
     long long x = mine;
 #pragma unroll 1
@@ -149,7 +149,7 @@ __device__ __forceinline__ void plan_walk(const RowsParams &p, long long *warp_u
         while (w.b < p.B) {
             w.seq = load_seq(p, w.b);
             const long long head = rows_units_before(p.rows, w.seq, w.seq.items);
-            if (w.seq.items > 0 && w.ui + head * p.groups > w.u0) {
+            if (w.seq.items > 0 && w.ui + head * p.Hkv > w.u0) {
                 w.loaded = true;
                 w.h = (int)quot(w.u0 - w.ui, head);
                 const long long v = w.u0 - w.ui - w.h * head;
@@ -170,7 +170,7 @@ __device__ __forceinline__ void plan_walk(const RowsParams &p, long long *warp_u
                 w.ui += w.h * head + at_item;
                 break;
             }
-            w.ui += head * p.groups;
+            w.ui += head * p.Hkv;
             ++w.b;
         }
     }
