@@ -15,7 +15,7 @@ namespace sv {
 namespace chunk {
 
 constexpr int kRowsItemCost = 2;  // an item's start, its warps' meeting and its stores, in tiles
-constexpr int kRowsMinUnits = 2;  // of a CTA at least (2047 slots before one token: 12.6 us, with 3 13.9, with 8 21)
+constexpr int kRowsMinUnits = 2;  // of a CTA at least (2047 slots before one token: 12.6 us then, with 3 13.9, with 8 21)
 
 struct RowsShape {
     int tok;     // rows of an item

@@ -27,10 +27,11 @@
 //
 // What bounds it (32 query over 8 KV heads of 128): the instructions, some 320 a unit
 // of which the integer pipe has half (52% busy, 2.1 of 4 issue slots taken), and the
-// barriers where an item's warps meet -- 32 single tokens after 2048-4096 slots 44 us,
-// 0.36 of the measured bandwidth, 64 after 4096 97 us, 0.44.  One token after 2047
-// slots is 12.6 us: the launch, the list, the page table, the pages and the joining of
-// some 70 CTAs' shares one after another.  S in sums of their own, so that no product
+// barriers where an item's warps meet -- 32 single tokens after 2048-4096 slots 43 us,
+// 0.36 of the measured bandwidth, 64 after 4096 96 us, 0.44.  One token after 2047
+// slots is 11.6 us: in cycles, the list 4000, the page table 1800, the pages and two
+// tiles 3800, the warps' meeting 1600, the joining of 72 CTAs' shares 2300, and the
+// launch, one after another.  S in sums of their own, so that no product
 // waits for another: no gain.
 #include <mutex>
 
@@ -163,25 +164,11 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm) quant_rows_kernel(const RowsPa
     if (tid == 0) call = begin_call(p.call);
 
     auto look_ahead = [&](int to) {  // the next item (by one warp)
-        RowsWalk walk = sh.walk;
-        RowsItem x;
-        next_item(p, walk, x);
-        __syncwarp();
-        if (lane == 0) {
-            sh.walk = walk;
-            sh.items[to] = x;
-        }
+        if (lane == 0) next_item(p, sh.walk, sh.items[to]);
         __syncwarp();
     };
-    {
-        RowsWalk walk;
-        plan_walk<kRT>(p, sh.warp_units, sh.before, tid, walk);
-        if (tid == 0) {
-            sh.walk = walk;
-            sh.items[1].b = 0;
-        }
-        __syncwarp();
-    }
+    plan_walk<kRT>(p, sh.warp_units, sh.before, tid, sh.walk);
+    if (tid == 0) sh.items[1].b = 0;
 
     const uint32_t ring_at = smem_u32(sh.ring[warp][0]);
     uint32_t got = 0;  // units used

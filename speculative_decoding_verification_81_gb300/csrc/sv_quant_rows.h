@@ -11,7 +11,7 @@ namespace chunk {
 constexpr int kRowsCols = 16;      // columns (rows times heads) of an item at most
 constexpr int kRowsMaxGrid = 512;  // CTAs of a call at most: the workspace's shares and counters
 // Columns of a mean sequence up to which a call takes this form.  Both measured, us, this one first, for 32
-// requests after 2048-4096 slots: 4 columns 44 and 117, 8 columns 45 and 85, 16 columns 58 and 84; 24 columns
+// requests after 2048-4096 slots: 4 columns 43 and 117, 8 columns 44 and 85, 16 columns 57 and 84; 24 columns
 // (two items of this form a head) 99 and 84.  A form of 40 columns took 106 for 36, where the other takes 85.
 constexpr int kRowsMost = 16;
 constexpr float kUnset = -1e38f;   // u of a column that has seen no slot

@@ -23,7 +23,8 @@ struct RowsItem {
     int c_first, nc, ci;  // CTAs that share the item's tiles, this one's number among them
 };
 
-// The items of this CTA's units, one after another; the same in every lane.
+// The items of this CTA's units, one after another: in shared memory, where one thread goes on from item to item
+// (a copy a lane does not fit the registers and went to the stack).
 struct RowsWalk {
     long long U, u0, u1, ui;  // ui: first unit of item (b, h, i)
     int nctas, b, h, i;
@@ -101,79 +102,112 @@ static __device__ __noinline__ bool bad_sequence(const RowsParams &p, int sb, in
     return __any_sync(0xffffffffu, bad);
 }
 
-// This CTA's share of the list, by its kT threads together: units before each thread's sequences
-// (`before`, kT of them; warp_units, kT / 32), then, for warp 0, the place where the share begins.
-template <int kT>
-__device__ __forceinline__ void plan_walk(const RowsParams &p, long long *warp_units, long long *before, int tid, RowsWalk &w) {
-    const int lane = tid & 31, warp = tid >> 5;
-    const int per = (p.B + kT - 1) / kT, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-    long long mine = 0;
-#pragma unroll 1
-    for (int b = b0; b < b1; ++b) {
-        const RowsSeq s = load_seq(p, b);
-        mine += rows_units_before(p.rows, s, s.items) * p.Hkv;
-    }
-    long long x = mine;
+// Inclusive prefix sum over the warp.
+__device__ __forceinline__ long long scan_units(long long x, int lane) {
 #pragma unroll 1
     for (int off = 1; off < 32; off <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, x, off);
         if (lane >= off) x += y;
     }
-    if (lane == 31) warp_units[warp] = x;
-    __syncthreads();
-    long long base = 0;
-    w.U = 0;
+    return x;
+}
+
+// This CTA's share of the list and the place where it begins, to `w`, by its kT threads together; warp 0 may
+// use it at once.  Up to 32 sequences warp 0 sums alone, a lane a sequence (one token: 4200 cycles, so 2800);
+// above, each thread sums a few (`before`, kT of them: the units before each thread's; warp_units, kT / 32).
+template <int kT>
+__device__ __forceinline__ void plan_walk(const RowsParams &p, long long *warp_units, long long *before, int tid, RowsWalk &w) {
+    const int lane = tid & 31, warp = tid >> 5;
+    const bool one = p.B <= 32;
+    long long U = 0, ui = 0;
+    int b = p.B, per = 1;
+    RowsSeq s{};
+    long long head = 0, x = 0;  // of a lane's sequence: units of a KV head; units up to and with it
+    if (one) {
+        if (warp > 0) return;
+        if (lane < p.B) s = load_seq(p, lane);
+        head = rows_units_before(p.rows, s, s.items);
+        x = scan_units(head * p.Hkv, lane);
+        U = __shfl_sync(0xffffffffu, x, 31);
+    } else {
+        per = (p.B + kT - 1) / kT;
+        const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+        long long mine = 0;
 #pragma unroll 1
-    for (int i = 0; i < kT / 32; ++i) {
-        if (i < warp) base += warp_units[i];
-        w.U += warp_units[i];
-    }
-    before[tid] = base + x - mine;
-    __syncthreads();
-    w.nctas = rows_ctas(w.U, gridDim.x);
-    const bool has = w.U > 0 && (int)blockIdx.x < w.nctas;
-    w.u0 = has ? cta_begin(w.U, w.nctas, blockIdx.x) : 0;
-    w.u1 = has ? cta_begin(w.U, w.nctas, blockIdx.x + 1) : 0;
-    w.b = p.B;
-    w.ui = 0;
-    w.h = w.i = 0;
-    w.loaded = false;
-    if (has && warp == 0) {  // the last thread with at most u0 units before its sequences, then the sequence
-        int at = 0;
-#pragma unroll 1
-        for (int i = lane; i < kT; i += 32) at += before[i] <= w.u0;
-        at = __reduce_add_sync(0xffffffffu, at) - 1;
-        w.b = at * per;
-        w.ui = before[at];
-#pragma unroll 1
-        while (w.b < p.B) {
-            w.seq = load_seq(p, w.b);
-            const long long head = rows_units_before(p.rows, w.seq, w.seq.items);
-            if (w.seq.items > 0 && w.ui + head * p.Hkv > w.u0) {
-                w.loaded = true;
-                w.h = (int)quot(w.u0 - w.ui, head);
-                const long long v = w.u0 - w.ui - w.h * head;
-                // the last item whose first unit is at most v: 32 candidates at a time
-                int span = w.seq.items, first = 0;
-                long long at_item = 0;
-#pragma unroll 1
-                while (span > 1) {
-                    const int step = (span + 31) / 32, c = first + lane * step;
-                    const bool in = lane * step < span;
-                    const long long u = in ? rows_units_before(p.rows, w.seq, c) : 0;
-                    const int hit = 31 - __clz(__ballot_sync(0xffffffffu, in && u <= v));  // (lane 0 always)
-                    at_item = __shfl_sync(0xffffffffu, u, hit);
-                    first += hit * step;
-                    span = min(step, span - hit * step);
-                }
-                w.i = first;
-                w.ui += w.h * head + at_item;
-                break;
-            }
-            w.ui += head * p.Hkv;
-            ++w.b;
+        for (int k = b0; k < b1; ++k) {
+            const RowsSeq q = load_seq(p, k);
+            mine += rows_units_before(p.rows, q, q.items) * p.Hkv;
         }
+        const long long sum = scan_units(mine, lane);
+        if (lane == 31) warp_units[warp] = sum;
+        __syncthreads();
+        long long base = 0;
+#pragma unroll 1
+        for (int i = 0; i < kT / 32; ++i) {
+            if (i < warp) base += warp_units[i];
+            U += warp_units[i];
+        }
+        before[tid] = base + sum - mine;
+        __syncthreads();
+        if (warp > 0) return;
     }
+    const int nctas = rows_ctas(U, gridDim.x);
+    const bool has = U > 0 && (int)blockIdx.x < nctas;
+    const long long u0 = has ? cta_begin(U, nctas, blockIdx.x) : 0, u1 = has ? cta_begin(U, nctas, blockIdx.x + 1) : 0;
+    int h = 0, first = 0;
+    if (has) {
+        if (one) {  // the sequence that holds unit u0
+            b = __ffs(__ballot_sync(0xffffffffu, u0 < x)) - 1;
+            ui = __shfl_sync(0xffffffffu, x - head * p.Hkv, b);
+            head = __shfl_sync(0xffffffffu, head, b);
+            s.L = __shfl_sync(0xffffffffu, s.L, b);
+            s.n = __shfl_sync(0xffffffffu, s.n, b);
+            s.row0 = __shfl_sync(0xffffffffu, s.row0, b);
+            s.items = __shfl_sync(0xffffffffu, s.items, b);
+        } else {  // the last thread with at most u0 units before its sequences, then the sequence
+            int at = 0;
+#pragma unroll 1
+            for (int i = lane; i < kT; i += 32) at += before[i] <= u0;
+            at = __reduce_add_sync(0xffffffffu, at) - 1;
+            ui = before[at];
+#pragma unroll 1
+            for (b = at * per; b < p.B; ++b) {
+                s = load_seq(p, b);
+                head = rows_units_before(p.rows, s, s.items);
+                if (ui + head * p.Hkv > u0) break;
+                ui += head * p.Hkv;
+            }
+        }
+        h = (int)quot(u0 - ui, head);
+        const long long v = u0 - ui - h * head;
+        // the last item whose first unit is at most v: 32 candidates at a time
+        int span = s.items;
+        long long at_item = 0;
+#pragma unroll 1
+        while (span > 1) {
+            const int step = (span + 31) / 32, c = first + lane * step;
+            const bool in = lane * step < span;
+            const long long u = in ? rows_units_before(p.rows, s, c) : 0;
+            const int hit = 31 - __clz(__ballot_sync(0xffffffffu, in && u <= v));  // (lane 0 always)
+            at_item = __shfl_sync(0xffffffffu, u, hit);
+            first += hit * step;
+            span = min(step, span - hit * step);
+        }
+        ui += h * head + at_item;
+    }
+    if (lane == 0) {
+        w.U = U;
+        w.u0 = u0;
+        w.u1 = u1;
+        w.ui = ui;
+        w.nctas = nctas;
+        w.b = b;
+        w.h = h;
+        w.i = first;
+        w.seq = s;
+        w.loaded = true;
+    }
+    __syncwarp();
 }
 
 }  // namespace chunk
