@@ -712,9 +712,11 @@ __global__ void __launch_bounds__(kThreadsOf<kQuant>, 1)
                 }
                 if (active) qs = row_sum<D>(qbuf + (qp & 1) * kTile, r);
                 __syncwarp();
+                // (eight arrivals a tile, of the warps that waited for it alone: where two tiles are on the streams each
+                // warp's is two.  One for a tile that the warp has not waited for could complete the phase before)
                 if (lane == 0) {
-                    mbar_arrive(&sh->q_empty[qpos & 1]);
-                    if (two) mbar_arrive(&sh->q_empty[(qpos & 1) ^ 1]);
+                    mbar_arrive(&sh->q_empty[qp & 1]);
+                    if (two) mbar_arrive(&sh->q_empty[qp & 1]);
                 }
                 qpos += two ? 2 : 1;
             }

@@ -115,6 +115,26 @@ def test_forms_take_turns_in_one_workspace():
         assert same(cases[name].run(), first[name]), name
 
 
+@pytest.mark.parametrize("seed", range(8))
+def test_items_of_one_and_of_two_tiles_in_turn(seed):
+    """Chunks whose rows fill one or two of the kernel's tiles of queries, beside single tokens, each call
+    on pages that no cache holds: within the bounds, and the same bits every time."""
+    rng = np.random.default_rng(100 + seed)
+    page_size, d = int(rng.choice([16, 32, 64])), 128 if seed % 4 else 64
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for i in range(4):
+        lens = [(int(rng.integers(0, 2000)), int(rng.integers(30, 400))) for _ in range(rng.integers(3, 7))]
+        lens += [(int(rng.integers(1, 40)), 1) for _ in range(rng.integers(0, 30))]
+        c = Case([lens[j] for j in rng.permutation(len(lens))], hq=32, hkv=8, d=d, page_size=page_size, seed=int(rng.integers(1000)))
+        run = fixed(c)
+        flush.fill_(i)
+        first = run()
+        near(*first, c.want())
+        for _ in range(6):
+            flush.fill_(i + 1)
+            assert same(run(), first)
+
+
 @pytest.mark.parametrize("name", CASES)
 def test_captured_and_replayed(name):
     lens, kw = CASES[name]
