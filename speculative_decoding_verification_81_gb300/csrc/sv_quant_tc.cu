@@ -29,7 +29,7 @@
 //
 // What bounds it (32 query over 8 KV heads of 128): the chain of a step's parts and
 // the one instruction cache that all roles are fetched through, not the tensor core
-// (2048 rows after 14336 slots 538 us, 0.51 of the measured rate; a prompt of 4096
+// (2048 rows after 14336 slots 538-544 us, 0.5 of the measured rate; a prompt of 4096
 // 181 us, 0.40) nor memory (chains of 9 after 2048-4096 slots for 32 requests 85 us,
 // 0.19 of the measured bandwidth, and the same for 8 to 40 columns a sequence).  A
 // step's softmax takes 2600 cycles, a tile's expansion 900 for K and 900 for V.
