@@ -518,8 +518,8 @@ sv_status sv_append_kv_quant(const void *k_new, const void *v_new, sv_dtype dtyp
  *            reported as SV_ERR_BAD_INPUT, its rows unspecified.  Not with a window
  * A score is the f32 of the cache's values, which are not rounded; weights and,
  * for more than 16 rows times heads of a KV head in the mean sequence, the values
- * of V are rounded to f16 under a common exponent.  V's steps below 2^-90 count as
- * that much.  The rest is as in that call.
+ * of V are rounded to f16 under a common exponent (an exponent or step of V's below
+ * 2^-80 counts as that much).  The rest is as in that call.
  * Supported: as sv_chunk_attention_paged.
  */
 sv_status sv_chunk_attention_quant(const void *q, long long q_stride, const void *k_codes,

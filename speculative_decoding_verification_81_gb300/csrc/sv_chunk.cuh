@@ -29,6 +29,7 @@ constexpr int kWarpPlanB = 128;          // sequences up to which one warp plans
 constexpr int kNone = INT32_MIN;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units the maximum grows before O is rescaled
+constexpr float kTop = 7.f;  // in 4 bits: log2 of P at the maximum, of which f16 then keeps what is 2^-21 of it in full
 
 // Tensor-memory columns: S (then P) of streams 0 and 1, O of streams 0 and 1.
 constexpr uint32_t kCols = 512, kColS = 0, kColO = 256;
@@ -51,7 +52,7 @@ constexpr int kVSlots = kStagesOf<D, true> / 2;
 constexpr int kSlotBytes = kBK * 8;
 template <int D, bool kQuant>
 constexpr int kRawBytes = kQuant ? kRawStages<D> * kRawTile<D> + kKSlots<D> * kSlotBytes + kVSlots<D> * 32 : 0;
-constexpr int kLeastV = -90;             // the least exponent of V's (a row's l stays below 2^(8 + 90) a slot)
+constexpr int kLeastV = -80;             // the least exponent of V's (a row's l stays below 2^(15 + 80) a slot)
 
 struct Params {
     uint16_t *out;

@@ -780,7 +780,8 @@ __global__ void __launch_bounds__(kThreadsOf<kQuant>, 1)
                         float mq[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
                         for (int i = 0; i < 16; ++i) mq[i & 3] = fmaxf(fmaxf(mq[i & 3], sv[i].x), sv[i].y);
-                        const float c = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) + e2.x;
+                        // (m: kTop below the maximum that it was set to)
+                        const float c = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) + (e2.x - kTop);
                         const bool up = c > m + kRescaleThreshold;
                         if (__any_sync(0xffffffffu, up)) {
                             const float f = up ? ex2_approx(m - c) : 1.f;

@@ -10,7 +10,10 @@
 //     x = step_k S + middle_k sum(q)      (f32, log2 units; middle = minimum + 8 steps)
 //     P = 2^(x + e - m), rounded to f16;  l += 2^(x - m)
 //     O += P V 2^-e                       (f16 products)
-// where e is the exponent of the largest value of V in a warp's 32 slots, fourteen
+// where m is 7 below the largest x + e (up to 15 while it lags), so that P stays below 2^15
+// and is rounded by at most 2^-11 of itself down to 2^-21 of the largest -- beside one slot
+// with most of a row's weight the others' P are small, and l, which is f32, has them
+// all -- and e is the exponent of the largest value of V in a warp's 32 slots, fourteen
 // less: V 2^-e stays below 2^15 and keeps 2^-12 of itself down to 2^-28 of that
 // largest value.  K is not rounded at all -- a score's error would be in the
 // log-sum-exp, which is f32 -- and P and V lose 2^-11 together, a quarter of what the

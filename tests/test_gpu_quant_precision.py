@@ -1,0 +1,89 @@
+"""The attention over pages held in 4 bits at the precision that it states, against
+64 bits.
+
+What an output may be off by, as shares of its norm (rows of D independent values):
+    its own rounding to bf16   2^-7 / sqrt(12) at most in the mean square (2.26e-3; a step is
+                               2^-7 of the lowest value that has it)
+    P, V and V's middle in f16 2^-11 / sqrt(3) each at most, 2.8e-4
+so 2.31e-3 together, and LIMIT = 2.5e-3 with 2^-24 to spare for the sums.  P is a whole
+2^-24 below 2^-14, where the largest P is 2^7 or more: a slot of weight w beside one of
+weight 1 has P = 2^7 w or more, off by 2^-25 / (2^7 w) of itself, below 2^-11 down to
+w = 2^-21.  The norm of one row and head has fewer values, D = 64 at the least: the mean of
+64 squares of a uniform error is off by 0.11 of itself, five times which is 1.25 in the norm.
+
+A log-sum-exp of size x is off by some ten roundings of f32 of sizes up to x and the
+scores', independent of one another: 2^-24 sqrt(10 / 3) (x + 6) in the mean square at most,
+below 2^-23 (x + 6)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import quant_ref
+import speculative_decoding_verification_81_gb300 as sv  # noqa: F401
+from test_gpu_quant import Case
+
+pytestmark = pytest.mark.gpu
+LIMIT = 2.5e-3
+
+
+def shares(out, want):
+    """Errors' norms over the rows' norms: of all rows, and the largest of a row and head."""
+    have = ~torch.isnan(want[..., 0])
+    o, d = want[have], out[have].double() - want[have]
+    assert torch.isfinite(d).all()
+    return (d.norm() / o.norm()).item(), (d.norm(dim=-1) / o.norm(dim=-1)).max().item()
+
+
+def stated(c):
+    (out, lse), (o, e, _, _) = c.run(), c.want()
+    of_all, of_one = shares(out, o)
+    assert of_all < LIMIT and of_one < 1.25 * LIMIT, (of_all, of_one)
+    have = ~torch.isnan(e)
+    d, size = (lse.double() - e)[have], e[have].square().mean().sqrt().item()
+    rms = d.square().mean().sqrt().item()
+    assert rms < 2.0 ** -23 * (size + 6), (rms, size)
+
+
+# ---------------------------------------------------------------- a slot that has most of the weight
+
+def dominated(lens, at, weight, zero, seed=0, **kw):
+    """In each sequence slot `at` has about this weight, and values of 0 under a step of 0 or of its
+    own (codes of 8 each): the outputs are the other slots'."""
+    c = Case(lens, seed=seed, **kw)
+    ps, hkv, d = c.page_size, c.k[0].shape[1], c.q.shape[2]
+    rows, hq, _ = c.q.shape
+    c.q.mul_(0.25).add_(1.0)
+    for params in (c.k[1], c.v[1]):
+        step = params[..., 0].float()
+        params[..., 1] = (-7.5 * step).to(torch.bfloat16)
+    where = [(c.table[b, at // ps].item(), at % ps) for b in range(len(lens))]
+    for pg, s in where:
+        for codes, params in (c.k, c.v):
+            codes[pg, :, s] = 0x88 if codes is c.v[0] else 0
+            params[pg, :, s] = 0
+        if zero == "codes":
+            c.v[1][pg, :, s, 0], c.v[1][pg, :, s, 1] = 0.25, -2.0
+        c.k[1][pg, :, s, 1] = -50.0  # (no weight, for the moment)
+    lse = c.want()[1]
+    for b, (pg, s) in enumerate(where):
+        r = slice(int(c.starts[b]), int(c.starts[b + 1]))
+        size = (c.scale * c.q[r].double().sum(-1)).reshape(-1, hkv, hq // hkv)
+        level = lse[r].reshape(-1, hkv, hq // hkv) + math.log(weight / (1 - weight))
+        c.k[1][pg, :, s, 1] = (level / size).mean((0, 2)).to(torch.bfloat16)
+    return c
+
+
+# (as many heads as keep an item on one CTA, or the most of it: a cut item's parts have a maximum each)
+@pytest.mark.parametrize("zero", ["step", "codes"])
+@pytest.mark.parametrize("lens,at,kw", [
+    ([(16384, 40)], 0, dict(hq=64, hkv=64)),
+    ([(16384, 130)], 0, dict(hq=64, hkv=64)),
+    ([(16384, 130)], 9000, dict(hq=64, hkv=64, page_size=128)),
+    ([(12000, 70), (9000, 33)], 3, dict(hq=160, hkv=40, d=64, page_size=64)),
+])
+def test_one_slot_has_most_of_the_weight(lens, at, kw, zero):
+    c = dominated(lens, at, 0.99, zero, seed=len(lens) + at, **kw)
+    of_all, _ = shares(c.run()[0], c.want()[0])
+    assert of_all < LIMIT, of_all
