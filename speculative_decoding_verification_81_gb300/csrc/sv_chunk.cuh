@@ -29,7 +29,7 @@ constexpr int kWarpPlanB = 128;          // sequences up to which one warp plans
 constexpr int kNone = INT32_MIN;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units the maximum grows before O is rescaled
-constexpr float kTop = 7.f;  // in 4 bits: log2 of P at the maximum, of which f16 then keeps what is 2^-21 of it in full
+constexpr float kTop = 7.f;  // in 4 bits: log2 of P at the maximum as it is set, of which f16 then keeps what is 2^-21 of it in full
 
 // Tensor-memory columns: S (then P) of streams 0 and 1, O of streams 0 and 1.
 constexpr uint32_t kCols = 512, kColS = 0, kColO = 256;

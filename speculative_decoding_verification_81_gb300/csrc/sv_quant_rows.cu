@@ -9,10 +9,10 @@
 //     P = 2^(s - u) step_v, rounded to f16; l += 2^(s - u); z += 2^(s - u) middle_v
 //     O^T += codes^T P          (D dims x 8 NT columns; codes less 8, exact in f16)
 // and out = (O + z) / l, where the warps, then the CTAs that share an item, are
-// brought to one u.  A column's u moves only when some P would pass 2^12: f16 then
-// holds P to 2^-12 of itself, or of 2^-14 of the largest where it is smaller, and
-// the steps and middles never meet a matrix product, so that nothing of the cache
-// is rounded.
+// brought to one u.  A column's u moves only when some P would pass 2^15, to where the
+// largest is 2^7: f16 then rounds P by at most 2^-11 of itself down to 2^-21 of the
+// largest, and the steps and middles never meet a matrix product, so that nothing
+// of the cache is rounded.
 //
 // Why the warp's own products of 16 x 8 (mma.sync; 1024 multiply-adds a clock and SM
 // measured, a quarter of tcgen05's): the codes become operands in the registers that
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm) quant_rows_kernel(const RowsPa
 #pragma unroll
                 for (int e = 0; e < 4; ++e) over = over || s[n][e] - u[e & 1] > bound[e >> 1];
             }
-            if (__any_sync(0xffffffffu, over)) {  // some column's u moves up to its largest P
+            if (__any_sync(0xffffffffu, over)) {  // some column's u moves up, so that its largest P is 2^kTop
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const uint2 u2 = lds8(u_at + (8 * n + 2 * t) * 4);
@@ -390,6 +390,7 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm) quant_rows_kernel(const RowsPa
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
                         const bool up = a > u[c] + kRoom;
+                        a -= kTop;
                         f[c] = up ? ex2_approx(u[c] - a) : 1.f;
                         if (up) u[c] = a;
                         l[n][c] *= f[c];

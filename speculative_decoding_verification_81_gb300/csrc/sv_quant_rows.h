@@ -15,8 +15,8 @@ constexpr int kRowsMaxGrid = 512;  // CTAs of a call at most: the workspace's sh
 // (two items of this form a head) 99 and 84.  A form of 40 columns took 106 for 36, where the other takes 85.
 constexpr int kRowsMost = 16;
 constexpr float kUnset = -1e38f;   // u of a column that has seen no slot
-constexpr float kRoom = 12.f;      // log2 of the largest P
-constexpr float kLeast = -90.f;    // log2 of a step below which it counts as this much for u (l stays below 2^(12 + 90) a slot)
+constexpr float kRoom = 15.f;      // log2 of the largest P; kTop as u moves
+constexpr float kLeast = -80.f;    // log2 of a step below which it counts as this much for u (l stays below 2^(15 + 80) a slot)
 
 struct RowsParams : QuantParams {
     const uint16_t *q;

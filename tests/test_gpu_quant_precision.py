@@ -82,6 +82,10 @@ def dominated(lens, at, weight, zero, seed=0, **kw):
     ([(16384, 130)], 0, dict(hq=64, hkv=64)),
     ([(16384, 130)], 9000, dict(hq=64, hkv=64, page_size=128)),
     ([(12000, 70), (9000, 33)], 3, dict(hq=160, hkv=40, d=64, page_size=64)),
+    ([(16384, 1)], 0, dict(hq=32, hkv=8)),
+    ([(16384, 1)] * 4, 0, dict(hq=128, hkv=128)),
+    ([(16384, 1)] * 4, 9000, dict(hq=128, hkv=128, d=64)),
+    ([(12000, 4), (16000, 3)], 1, dict(hq=240, hkv=60, page_size=128)),
 ])
 def test_one_slot_has_most_of_the_weight(lens, at, kw, zero):
     c = dominated(lens, at, 0.99, zero, seed=len(lens) + at, **kw)
