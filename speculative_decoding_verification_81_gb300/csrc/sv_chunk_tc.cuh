@@ -426,7 +426,9 @@ __device__ __forceinline__ void load_quant(const P &p, S *sh, uint8_t *raw, int 
 // bf16; their step and middle (minimum + 8 steps), times the scale, lie beside the tile
 // in f32.  V's values go to f16 times 2^-e, where a warp's 32 slots share e: their
 // largest is below 2^15, and what is above 2^-28 of it keeps 2^-12 of itself.  A slot
-// that no row of the item sees has zeros.
+// that no row of the item sees has zeros, and so has one whose row of V is not finite: a
+// weight of 0 would bring it to every row of the tile.  Its NaN goes into the score instead,
+// which is masked where the slot is hidden.
 template <int D, class P, class S>
 __device__ __forceinline__ void expand_quant(const P &p, S *sh, uint8_t *smem, uint8_t *raw, int w, int lane) {
     constexpr int kRow = D / 2, kPieces = D / 32, kStages = kStagesOf<D, true>, kRaw = kRawStages<D>;
@@ -478,7 +480,7 @@ __device__ __forceinline__ void expand_quant(const P &p, S *sh, uint8_t *smem, u
                 break;
             }
             const uint32_t tile = pos >> 1;
-            const float step = bf16_lo(par), mid = __fmaf_rn(8.f, step, bf16_hi(par));
+            float step = bf16_lo(par), mid = __fmaf_rn(8.f, step, bf16_hi(par));
             uint8_t *const to = smem + r * 128 + st * kTileBytes<D>;
             auto store = [&](auto &&values) {
 #pragma unroll
@@ -495,8 +497,13 @@ __device__ __forceinline__ void expand_quant(const P &p, S *sh, uint8_t *smem, u
                 }
             };
             if (pos & 1) {
-                const uint32_t mine = __float_as_uint(__fmaf_rn(8.f, fabsf(step), fabsf(mid))) >> 23;  // (255: not finite)
-                const uint32_t most = max(__reduce_max_sync(0xffffffffu, mine == 255u ? 0u : mine), (uint32_t)(126 + 15 + kLeastV));
+                uint32_t mine = __float_as_uint(__fmaf_rn(8.f, fabsf(step), fabsf(mid))) >> 23;
+                if (mine == 255u) {  // (the softmax reads K's middle once V's tile is there too)
+                    slots[tile % kKSlots<D> * (kSlotBytes / 4) + (r >> 1) * 4 + (r & 1) + 2] = __uint_as_float(0x7fc00000u);
+                    step = mid = 0.f;
+                    mine = 0;
+                }
+                const uint32_t most = max(__reduce_max_sync(0xffffffffu, mine), (uint32_t)(126 + 15 + kLeastV));
                 const float down = __uint_as_float((127u + 15u + 126u - most) << 23);
                 const uint32_t step2 = pack_f16x2(step * down, step * down), mid2 = pack_f16x2(mid * down, mid * down);
                 if (lane == 0) {  // e and 2^-e
@@ -736,7 +743,7 @@ __global__ void __launch_bounds__(kThreadsOf<kQuant>, 1)
                     // a warp of V's slots at a time (all of a row's scores beside what the codes need do not
                     // fit a thread's registers), the next ones' S on its way
                     const uint32_t pv = ring + 2 * j + 1;
-                    ok = warp_wait_bounded(&sh->full[pv % kStages], (pv / kStages) & 1);  // (V's exponents)
+                    ok = warp_wait_bounded(&sh->full[pv % kStages], (pv / kStages) & 1);  // (V's exponents, and its NaN)
                     if (!ok) break;
                     const uint8_t *slots = raw_slots<D>(raw);
                     const float4 *ks = reinterpret_cast<const float4 *>(slots + (pv >> 1) % kKS * kSlotBytes);

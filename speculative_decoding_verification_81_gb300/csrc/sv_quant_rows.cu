@@ -341,6 +341,7 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm) quant_rows_kernel(const RowsPa
             const int slot = slot0 + slot_of(g);
             float ks[2], km[2], vs[2], vm[2], bound[2];
             const bool inside = slot0 >= lo && slot0 + kU <= hi;
+            const bool masked = slot0 + kU > all_hi || slot0 < all_lo;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const uint32_t pa = at + 2 * kU * kRow + (slot_of(g) + 8 * r) * 4;
@@ -351,10 +352,15 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm) quant_rows_kernel(const RowsPa
                 km[r] = __fmaf_rn(8.f, bf16_lo(kp), bf16_hi(kp)) * p.scale_log2;
                 vs[r] = bf16_lo(vp);
                 vm[r] = __fmaf_rn(8.f, vs[r], bf16_hi(vp));
+                // (a row of V that is not finite goes into the score, which is masked where the slot is hidden: a weight
+                // of 0 would bring it to every column)
+                if (masked && !(fabsf(vm[r]) < __builtin_huge_valf())) {
+                    km[r] = __uint_as_float(0x7fc00000u);
+                    vs[r] = vm[r] = 0.f;
+                }
                 // (a step that is nothing beside the middle counts as 2^-24 of it: what the weight meets is no larger)
                 bound[r] = kRoom - fmaxf(lg2_approx(fmaxf(fabsf(vs[r]), fabsf(vm[r]) * 0x1p-24f)), kLeast);
             }
-            const bool masked = slot0 + kU > all_hi || slot0 < all_lo;
             bool over = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
