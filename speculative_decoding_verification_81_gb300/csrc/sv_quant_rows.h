@@ -14,7 +14,7 @@ constexpr int kRowsMaxGrid = 512;  // CTAs of a call at most: the workspace's sh
 // requests after 2048-4096 slots: 4 columns 43 and 117, 8 columns 44 and 85, 16 columns 57 and 84; 24 columns
 // (two items of this form a head) 99 and 84.  A form of 40 columns took 106 for 36, where the other takes 85.
 constexpr int kRowsMost = 16;
-constexpr float kUnset = -1e38f;   // u of a column that has seen no slot
+constexpr float kUnset = -3.4028234663852886e38f;  // u of a column that has seen no slot: no finite score is less
 constexpr float kRoom = 15.f;      // log2 of the largest P; kTop as u moves
 constexpr float kLeast = -80.f;    // log2 of a step below which it counts as this much for u (l stays below 2^(15 + 80) a slot)
 

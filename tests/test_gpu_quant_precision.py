@@ -91,3 +91,28 @@ def test_one_slot_has_most_of_the_weight(lens, at, kw, zero):
     c = dominated(lens, at, 0.99, zero, seed=len(lens) + at, **kw)
     of_all, _ = shares(c.run()[0], c.want()[0])
     assert of_all < LIMIT, of_all
+
+
+# ---------------------------------------------------------------- scores at the ends of f32
+
+@pytest.mark.parametrize("lens,kw", [([(0, 1)], {}), ([(40, 1)], dict(d=64)), ([(300, 2)], dict(hq=8, hkv=4)),
+                                     ([(100, 30)], {})])
+@pytest.mark.parametrize("size", [-1.5, -0.875, 0.875, 1.5])
+def test_scores_near_the_ends_of_the_range(lens, kw, size):
+    """Scores past 2^126 in log2 units: in f32 they are whole multiples of 2^103, and the weights have no
+    bound, since exp of an error of that size has none.  What holds for any weights: an output is among
+    the values that its row sees, but for the roundings to f16 and bf16 (2^-11 twice and 2^-8 of the
+    largest of them), and the log-sum-exp is the score."""
+    c = Case(lens, seed=31, scale=1.0, **kw)
+    (_, hq, d), ps, hkv, n = c.q.shape, c.page_size, c.k[0].shape[1], sum(lens[0])
+    c.q.fill_(size * 2.0 ** 60)
+    c.k[0].zero_()
+    c.k[1][..., 0], c.k[1][..., 1] = 0.0, 2.0 ** 66 / d
+    out, lse = c.run()
+    s = torch.arange(n, device="cuda")
+    pg = c.table[0, s // ps].long()
+    v = quant_ref.values(c.v[0][pg, :, s % ps], c.v[1][pg, :, s % ps]).repeat_interleave(hq // hkv, 1)
+    room = v.abs().amax(0) * 2.0 ** -7
+    assert (out.double() >= v.amin(0) - room).all() and (out.double() <= v.amax(0) + room).all()
+    score = size * 2.0 ** 126
+    assert ((lse.double() - score).abs() < abs(score) * 2.0 ** -21).all()
