@@ -600,10 +600,11 @@ sv_status sv_fork_tables(const int32_t *sources, const int32_t *targets, const i
  *
  *   copies     int32 [F, 3]; copy_status int32 [F] or NULL
  *   planes     HOST array of num_planes device pointers to arrays [num_pages, Hkv,
- *              page_size, row_bytes[i]] of bytes: K and V pages of any number of
+ *              page_size, row_bytes[i]] of bytes: K and V pages of one or more
  *              layers, codes and parameters of pages held in 4 bits
  *   row_bytes  HOST array
- * Supported: num_planes <= 64, row_bytes a multiple of 4 up to 4096, F <= 2^20,
+ * Supported: num_planes <= 64 (more take several calls, which the Python binding
+ * makes of a longer list), row_bytes a multiple of 4 up to 4096, F <= 2^20,
  * num_pages * Hkv * page_size < 2^31.
  */
 sv_status sv_copy_pages(const int32_t *copies, int F, void *const *planes, const int *row_bytes,

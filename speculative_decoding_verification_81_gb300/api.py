@@ -1073,10 +1073,14 @@ def sv_fork_tables(sources, targets, fork_lens, page_counts, block_table, free_p
     return copies, new_page_counts, new_free_count, new_shares
 
 
+_MAX_PLANES = 64  # of a launch of sv_copy_pages
+
+
 def sv_copy_pages(copies, planes, copy_status=None, stream=None):
-    """copies [F,3] int32, rows (from, to, slots); planes: up to 64 tensors
+    """copies [F,3] int32, rows (from, to, slots); planes: a list of tensors
     [num_pages,Hkv,page_size,X] of any type (pages of K, V, codes, parameters, of
-    any number of layers).  The first slots of page `from` are written to page `to`."""
+    any number of layers; 64 a launch).  The first slots of page `from` are written
+    to page `to`."""
     if stream is None and (native := _native()) is not None:
         if native.copy_pages(copies, planes, copy_status) is not None:
             return
@@ -1097,10 +1101,19 @@ def sv_copy_pages(copies, planes, copy_status=None, stream=None):
     _fits32(F=F, num_pages=num_pages, Hkv=Hkv, page_size=page_size, row_bytes=max(row_bytes))
     p_c = _arr(copies, "copies", torch.int32, (F, 3), dev)
     p_st = _opt_arr(copy_status, "copy_status", torch.int32, (F,), dev)
+    if n > _MAX_PLANES:  # (several launches, and none before every plane is known to be taken)
+        for t, b in zip(planes, row_bytes):
+            if b <= 0 or b % 4 or t.data_ptr() % 16:
+                _check("sv_copy_pages", SV_ERR_INVALID_ARG)
+            if b > 4096:
+                _check("sv_copy_pages", SV_ERR_UNSUPPORTED)
     with _Launch(dev, stream) as s:
-        rc = lib().sv_copy_pages(p_c, F, (ctypes.c_void_p * n)(*(t.data_ptr() for t in planes)),
-                                 (ctypes.c_int * n)(*row_bytes), n, Hkv, page_size, num_pages, p_st, s)
-    _check("sv_copy_pages", rc)
+        for i in range(0, n, _MAX_PLANES):
+            part, sizes = planes[i:i + _MAX_PLANES], row_bytes[i:i + _MAX_PLANES]
+            m = len(part)
+            rc = lib().sv_copy_pages(p_c, F, (ctypes.c_void_p * m)(*(t.data_ptr() for t in part)),
+                                     (ctypes.c_int * m)(*sizes), m, Hkv, page_size, num_pages, p_st, s)
+            _check("sv_copy_pages", rc)
 
 
 def sv_release_shared_pages(keep_lens, page_counts, block_table, free_pages, free_count, shares, page_size,

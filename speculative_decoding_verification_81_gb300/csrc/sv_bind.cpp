@@ -372,9 +372,9 @@ PyObject *fork(PyObject *, PyObject *const *a, Py_ssize_t na) {
                          THPVariable_Wrap(std::move(left)), THPVariable_Wrap(std::move(shares)));
 }
 
-// (copies, planes, copy_status); True when done
+// (copies, planes, copy_status); True when done.  64 planes a launch, and none launched before all are looked at.
 PyObject *copy(PyObject *, PyObject *const *a, Py_ssize_t na) {
-    constexpr int kMost = 64;
+    constexpr int kPart = 64, kMost = 1024;
     if (na != 3 || !f_copy || !PyList_CheckExact(a[1])) return none();
     const at::Tensor *copies = tensor(a[0]);
     const int dev = device_of(copies);
@@ -390,17 +390,18 @@ PyObject *copy(PyObject *, PyObject *const *a, Py_ssize_t na) {
         for (int d = 0; d < 3; ++d)
             if (t->size(d) != first->size(d) || t->size(d) >= (1LL << 31)) return none();
         const int64_t row = t->size(3) * (int64_t)t->element_size();
-        if (row >= (1LL << 31)) return none();
         planes[i] = t->data_ptr();
+        if (row <= 0 || row > 4096 || row % 4 != 0 || reinterpret_cast<uintptr_t>(planes[i]) % 16 != 0) return none();
         bytes[i] = (int)row;
     }
     const int64_t F = copies->size(0);
     bool bad = F >= (1LL << 31);
     int32_t *st = status(a[2], dev, F, bad);
     if (bad || !array(copies, at::kInt, dev, {F, 3})) return none();
-    if (f_copy(ip(*copies), (int)F, planes, bytes, (int)n, (int)first->size(1), (int)first->size(2), (int)first->size(0), st,
-               stream_of(dev)) != SV_OK)
-        return none();
+    for (Py_ssize_t i = 0; i < n; i += kPart)
+        if (f_copy(ip(*copies), (int)F, planes + i, bytes + i, (int)(n - i < kPart ? n - i : kPart), (int)first->size(1),
+                   (int)first->size(2), (int)first->size(0), st, stream_of(dev)) != SV_OK)
+            return none();
     Py_RETURN_TRUE;
 }
 
