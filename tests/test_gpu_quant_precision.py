@@ -46,6 +46,62 @@ def stated(c):
     assert rms < 2.0 ** -23 * (size + 6), (rms, size)
 
 
+EVEN = [
+    ([(0, 1)], dict(hq=32, hkv=8)),
+    ([(2047, 1), (4095, 1)], dict(hq=32, hkv=8)),
+    ([(20000, 1)], dict(hq=32, hkv=8, page_size=64)),
+    ([(900, 2)] * 9, dict(hq=32, hkv=8, d=64)),
+    ([(300, 3), (41, 1), (1999, 4)], dict(hq=16, hkv=4, page_size=128)),
+    ([(2500, 9)] * 7 + [(33, 9)], dict(hq=32, hkv=8)),
+    ([(1500, 26), (127, 26), (0, 26)], dict(hq=8, hkv=2, d=64, tree=3)),
+    ([(700, 64), (2000, 60)], dict(hq=32, hkv=8, tree=5)),
+    ([(0, 700)], dict(hq=8, hkv=2)),
+    ([(6000, 200)], dict(hq=8, hkv=8, page_size=384)),
+    ([(3000, 300), (100, 1)], dict(hq=14, hkv=2, d=64, window=640)),
+]
+# The form for few rows goes by the rows of the mean sequence: it meets long ones among single tokens, cut into
+# many items, and the other form single tokens beside long prompts.
+UNEVEN = [
+    ([(300, 1)] * 60 + [(1000, 130)], dict(hq=32, hkv=8)),
+    ([(50, 1)] * 90 + [(700, 200), (0, 100)], dict(hq=8, hkv=8)),
+    ([(90, 1)] * 40 + [(300, 40)], dict(hq=14, hkv=2, d=64)),
+    ([(200, 1)] * 30 + [(500, 40), (90, 26)], dict(hq=8, hkv=2, tree=3)),
+    ([(100, 1)] * 50 + [(500, 64), (0, 64), (77, 50)], dict(hq=4, hkv=2, tree=64, d=64)),
+    ([(300, 1)] * 60 + [(1000, 130)], dict(hq=32, hkv=8, window=37)),
+    ([(50, 1)] * 90 + [(700, 200), (0, 100)], dict(hq=8, hkv=8, window=129, page_size=128)),
+    ([(90, 1)] * 40 + [(300, 40)], dict(hq=14, hkv=2, d=64, window=1)),
+    ([(700, 1)] * 20 + [(100, 400)], dict(hq=32, hkv=8)),
+    ([(700, 1)] * 20 + [(100, 400)], dict(hq=32, hkv=8, window=200)),
+]
+
+
+@pytest.mark.parametrize("i", range(len(EVEN) + len(UNEVEN)))
+def test_as_near_as_stated(i):
+    lens, kw = (EVEN + UNEVEN)[i]
+    stated(Case(lens, seed=200 + i, spare_rows=i % 3, strided=i % 2 == 0, **kw))
+
+
+@pytest.mark.parametrize("i", range(len(EVEN) + len(UNEVEN)))
+def test_every_row_sees_its_slots_and_no_other(i):
+    """With q = 0 the weights are even, and with values of 15/16 at dim s mod D of slot s, 0 elsewhere, an
+    output counts the seen slots of its residue: one slot more or less is 1 / 157 of it or more here, and
+    nothing is rounded but the output, to bf16 (1 / 256 at most), and the division."""
+    lens, kw = (EVEN + UNEVEN)[i]
+    c = Case(lens, seed=300 + i, **kw)
+    c.q.zero_()
+    (codes, params), ps, d = c.v, c.page_size, c.q.shape[2]
+    one_hot = quant_ref.packed(15 * torch.eye(d, dtype=torch.uint8, device="cuda"))
+    for b, (L, n) in enumerate(lens):
+        s = torch.arange(max(0, L - c.window + 1) if c.window else 0, L + n, device="cuda")
+        pg = c.table[b, s // ps].long()
+        codes[pg, :, s % ps] = one_hot[s % d][:, None]
+        params[pg, :, s % ps] = torch.tensor([1 / 16, 0], dtype=torch.bfloat16, device="cuda")
+    (out, lse), (o, e, _, _) = c.run(), c.want()
+    have = ~torch.isnan(e)
+    assert ((out.double() - o).abs() <= o.abs() * 2.0 ** -8 + o.abs() * 2.0 ** -20)[have].all()
+    assert ((lse.double() - e).abs() <= 2.0 ** -20 * (1 + e))[have].all()
+
+
 # ---------------------------------------------------------------- a slot that has most of the weight
 
 def dominated(lens, at, weight, zero, seed=0, **kw):
