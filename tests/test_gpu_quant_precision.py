@@ -102,6 +102,27 @@ def test_every_row_sees_its_slots_and_no_other(i):
     assert ((lse.double() - e).abs() <= 2.0 ** -20 * (1 + e))[have].all()
 
 
+@pytest.mark.parametrize("seed", range(24))
+def test_drawn_shapes(seed):
+    """Lengths, head layouts, pages, windows and trees drawn over their ranges; the same bits twice."""
+    rng = np.random.default_rng(4000 + seed)
+    kind = ("single", "short", "chunks", "mixed", "tree")[seed % 5]
+    hkv, d = int(rng.choice([1, 2, 3, 8])), int(rng.choice([64, 128]))
+    g = int(rng.choice([1, 2, 3, 4, 7, 8, 12, 16, 17, 32, 100, 128]))
+    B = int(rng.integers(1, 40)) if hkv * g < 200 else 3
+    past = rng.integers(0, int(rng.choice([3, 40, 300, 1500])) + 1, B)
+    new = {"single": np.ones(B, int), "short": rng.integers(0, 9, B), "chunks": rng.integers(1, 200, B),
+           "tree": rng.integers(0, 65, B), "mixed": np.where(rng.random(B) < 0.7, 1, rng.integers(0, 300, B))}[kind]
+    new[0] = max(new[0], 1)
+    c = Case(list(zip(past.tolist(), new.tolist())), hq=hkv * g, hkv=hkv, d=d, page_size=int(rng.choice([8, 16, 32, 64, 128, 256, 384])),
+             window=0 if kind == "tree" else int(rng.choice([0, 0, 1, 7, 100, 128, 500])), seed=seed, strided=seed % 3 == 0,
+             spare_rows=seed % 4, tree=int(rng.integers(1, 8)) if kind == "tree" else 0)
+    stated(c)
+    n = int(c.starts[-1])  # (rows behind it are no sequence's)
+    a, b = c.run(), c.run()
+    assert all(torch.equal(x[:n].view(t), y[:n].view(t)) for x, y, t in zip(a, b, (torch.int16, torch.int32)))
+
+
 # ---------------------------------------------------------------- a slot that has most of the weight
 
 def dominated(lens, at, weight, zero, seed=0, **kw):
