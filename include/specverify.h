@@ -520,9 +520,9 @@ sv_status sv_append_kv_quant(const void *k_new, const void *v_new, sv_dtype dtyp
  * for more than 16 rows times heads of a KV head in the mean sequence, the values
  * of V are rounded to f16 under a common exponent (an exponent or step of V's below
  * 2^-80 counts as that much; beside values of V past 2^44 the weights of slots whose
- * values are less than 2^-100 of them may be lost).  A row of the cache whose parameters are not finite
- * (as sv_append_kv_quant makes them) may be seen: every row of q that sees it, and no
- * other, is NaN in out, and in lse where it is K's (where it is V's, lse may be NaN).
+ * values are less than 2^-100 of them may be lost).  A row of the cache whose minimum
+ * is NaN (sv_append_kv_quant makes them) may be seen: every row of q that sees it, and
+ * no other, is NaN in out, and in lse where it is K's (where it is V's, lse may be).
  * The rest is as in that call.
  * Supported: as sv_chunk_attention_paged.
  */

@@ -13,8 +13,11 @@
 // of a call, of any grid, add kCallShares to the workspace's word together,
 // each its share as it begins: what a CTA reads as it adds lacks its own share
 // at least, so that the quotient is the number of calls before, the same for
-// every CTA.  The form for few rows, which has no counters to zero, counts its
-// calls in words of its own.
+// every CTA.  Three words, since calls of the others come between: the forms on
+// the tensor cores (sv_chunk_tc.cuh), over bf16 pages and over pages held in 4 bits,
+// share the first and the counters below; the form for few rows over bf16 pages
+// (sv_chunk_few.cu) has no counters to zero; the one over pages held in 4 bits
+// (sv_quant_rows.cu) has two sets of its own (rows_counter) for any grid.
 //
 // A wait that gave up concerns the whole call: its CTA may have left any item
 // undone, and items shared with others unmerged.  The CTA sets gave_up to the
@@ -35,7 +38,7 @@ namespace sv {
 namespace chunk {
 
 constexpr int kCallShares = 4096;     // CTAs of a call at most
-constexpr int kCallBytes = 256;       // the workspace's first bytes: CallWords of the two forms
+constexpr int kCallBytes = 256;       // the workspace's first bytes: CallWords of the three
 constexpr int kCtaCounters = 2 * 4;   // of a CTA in a set: [Q tile][quarter]
 
 struct CallWords {

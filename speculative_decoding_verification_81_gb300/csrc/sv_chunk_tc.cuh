@@ -425,7 +425,8 @@ __device__ __forceinline__ void load_quant(const P &p, S *sh, uint8_t *raw, int 
 // The tiles as the products read them: a thread a slot.  K's codes less 8 are exact in
 // bf16; their step and middle (minimum + 8 steps), times the scale, lie beside the tile
 // in f32.  V's values go to f16 times 2^-e, where a warp's 32 slots share e: their
-// largest is below 2^15, and what is above 2^-28 of it keeps 2^-12 of itself.  A slot
+// largest is below 2^15, and above 2^-28 of it steps are exact, middles and values rounded
+// by at most 2^-11 of themselves each.  A slot
 // that no row of the item sees has zeros, and so has one whose row of V is not finite: a
 // weight of 0 would bring it to every row of the tile.  Its NaN goes into the score instead,
 // which is masked where the slot is hidden.

@@ -15,7 +15,10 @@ namespace sv {
 namespace chunk {
 
 constexpr int kRowsItemCost = 2;  // an item's start, its warps' meeting and its stores, in tiles
-constexpr int kRowsMinUnits = 2;  // of a CTA at least (2047 slots before one token: 12.6 us then, with 3 13.9, with 8 21)
+// Units of a CTA at least.  Measured, us, with 1, 2, 3 and 8 (32 query over 8 KV heads of 128): one token after 511
+// slots 10.1, 10.8, 12.1, 16.1, after 2047 11.8, 11.6, 13.0, 20.4, after 8191 16.4, 15.4, 15.4, 21.6; 8 single tokens
+// after 511 11.4, 11.5, 12.9, 19.2; chains of 4 for 4 requests after 2047 17.4, 17.4, 18.3, 28.1.
+constexpr int kRowsMinUnits = 2;
 
 struct RowsShape {
     int tok;     // rows of an item

@@ -29,7 +29,7 @@
 // of which the integer pipe has half (52% busy, 2.1 of 4 issue slots taken), and the
 // barriers where an item's warps meet -- 32 single tokens after 2048-4096 slots 43 us,
 // 0.36 of the measured bandwidth, 64 after 4096 96 us, 0.44.  One token after 2047
-// slots is 11.6 us: in cycles, the list 4000, the page table 1800, the pages and two
+// slots is 11.6 us: in cycles, the list 2800, the page table 1800, the pages and two
 // tiles 3800, the warps' meeting 1600, the joining of 72 CTAs' shares 2300, and the
 // launch, one after another.  S in sums of their own, so that no product
 // waits for another: no gain.

@@ -14,12 +14,14 @@
 // and is rounded by at most 2^-11 of itself down to 2^-21 of the largest -- beside one slot
 // with most of a row's weight the others' P are small, and l, which is f32, has them
 // all -- and e is the exponent of the largest value of V in a warp's 32 slots, fourteen
-// less: V 2^-e stays below 2^15 and keeps 2^-12 of itself down to 2^-28 of that
-// largest value.  K is not rounded at all -- a score's error would be in the
-// log-sum-exp, which is f32 -- and P and V lose 2^-11 together, a quarter of what the
-// output's own rounding to bf16 takes (error against 64 bits 1.7e-3 of the output's
-// size, which is that rounding; with P and V in bf16 it was 3.4e-3).  A slot that no
-// row of the item sees is zeros.  A row may be a node of a draft tree: it then sees
+// less: V 2^-e stays below 2^15, and its middle and then its values are rounded by at
+// most 2^-11 of themselves each, down to 2^-28 of that largest value (its steps not at
+// all).  K is not rounded -- a score's error would be in the log-sum-exp, which is
+// f32 -- and what P and V lose is a third of what the output's own rounding to bf16
+// takes (error against 64 bits 1.7e-3 of the output's size, which is that rounding,
+// with a slot of weight 0.99 or 0.999 among 16384 too; with P and V in bf16 it was
+// 3.4e-3; with the largest P at 2^0 those two 5.7e-3 and 5.7e-2).  A slot that no row
+// of the item sees is zeros.  A row may be a node of a draft tree: it then sees
 // the slots before its sequence's rows and its own path's, a 64-bit set that each
 // softmax thread makes of the parents.
 //
