@@ -28,7 +28,7 @@
 // What bounds it (32 query over 8 KV heads of 128): the instructions, some 320 a unit
 // of which the integer pipe has half (52% busy, 2.1 of 4 issue slots taken), and the
 // barriers where an item's warps meet -- 32 single tokens after 2048-4096 slots 43 us,
-// 0.36 of the measured bandwidth, 64 after 4096 96 us, 0.44.  One token after 2047
+// 0.36 of the measured bandwidth, 64 after 4096 94 us, 0.45.  One token after 2047
 // slots is 11.6 us: in cycles, the list 2800, the page table 1800, the pages and two
 // tiles 3800, the warps' meeting 1600, the joining of 72 CTAs' shares 2300, and the
 // launch, one after another.  S in sums of their own, so that no product
@@ -341,7 +341,6 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm) quant_rows_kernel(const RowsPa
             const int slot = slot0 + slot_of(g);
             float ks[2], km[2], vs[2], vm[2], bound[2];
             const bool inside = slot0 >= lo && slot0 + kU <= hi;
-            const bool masked = slot0 + kU > all_hi || slot0 < all_lo;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const uint32_t pa = at + 2 * kU * kRow + (slot_of(g) + 8 * r) * 4;
@@ -352,15 +351,10 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm) quant_rows_kernel(const RowsPa
                 km[r] = __fmaf_rn(8.f, bf16_lo(kp), bf16_hi(kp)) * p.scale_log2;
                 vs[r] = bf16_lo(vp);
                 vm[r] = __fmaf_rn(8.f, vs[r], bf16_hi(vp));
-                // (a row of V that is not finite goes into the score, which is masked where the slot is hidden: a weight
-                // of 0 would bring it to every column)
-                if (masked && !(fabsf(vm[r]) < __builtin_huge_valf())) {
-                    km[r] = __uint_as_float(0x7fc00000u);
-                    vs[r] = vm[r] = 0.f;
-                }
                 // (a step that is nothing beside the middle counts as 2^-24 of it: what the weight meets is no larger)
                 bound[r] = kRoom - fmaxf(lg2_approx(fmaxf(fabsf(vs[r]), fabsf(vm[r]) * 0x1p-24f)), kLeast);
             }
+            const bool masked = slot0 + kU > all_hi || slot0 < all_lo;
             bool over = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -379,7 +373,15 @@ __global__ void __launch_bounds__(kRT, kCtasAnSm) quant_rows_kernel(const RowsPa
                             bool sees = x <= pos && (p.rows.window == 0 || x > pos - p.rows.window);
                             if (p.parents) sees = x < own0 || (x - own0 < kTreeNodes && (sh.above[qb][tk] >> (x - own0) & 1));
                             if (!sees) s[n][2 * r + c] = kNegInf;
+                            else if (!(fabsf(vm[r]) < __builtin_huge_valf())) s[n][2 * r + c] = __uint_as_float(0x7fc00000u);
                         }
+                    }
+                    // (a row of V that is not finite is in the scores of the columns that see it now: a weight of 0 would
+                    // bring it to the others)
+                    if (n == NT - 1) {
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)
+                            if (!(fabsf(vm[r]) < __builtin_huge_valf())) vs[r] = vm[r] = 0.f;
                     }
                 }
 #pragma unroll
